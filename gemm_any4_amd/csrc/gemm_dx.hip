@@ -1,0 +1,389 @@
+// dx = dy * W, the gradient of a quantised layer's input (W [N][K] in any4,
+// plain int4, any2 or any3).  The C ABI is declared in include/any4.h.
+//
+//     dx[m][k] = sum_n dy[m][n] w[n][k],   w the any4_dequant values (bf16)
+//
+// The sum runs over the rows of W, while a packed tile holds 16 rows x 128 k
+// with each row's k together.  So the layer is first dequantised and turned,
+// W^T [K][N] (k_dequant_t), which makes the product one of two matrices whose
+// summed dimension is contiguous (k_dx).
+#include "frag.h"
+
+namespace {
+
+enum { FMT_ANY4, FMT_INT4, FMT_ANY2, FMT_ANY3 };
+
+constexpr int STEP = 64;             // n of one step of the product; W^T rows are padded to it
+
+// ---------------------------------------------------------------------------
+// W^T
+// ---------------------------------------------------------------------------
+constexpr int DT_THREADS = 256;
+constexpr int DT_STRIDE = 36;        // dwords of a staged row of 64 n
+
+template <int FMT>
+__device__ __forceinline__ uint32_t code_pair(const uint32_t (&p)[4], int i)
+{
+    // codes 2i (low half) and 2i + 1 (high half) of a lane's 32
+    if constexpr (FMT == FMT_ANY2) {
+        const uint32_t b = p[i / 8] >> (4 * (i % 8));
+        return (b & 3u) | (b & 12u) << 14;
+    } else if constexpr (FMT == FMT_ANY3) {
+        uint32_t b;
+        if (i < 12) {
+            b = p[i / 4] >> (8 * (i % 4));
+        } else {
+            const int s = 8 * (i - 12) + 6;      // two bits of each dword's byte i - 12
+            b = (p[0] >> s & 3u) | (p[1] >> s & 3u) << 2 | (p[2] >> s & 3u) << 4;
+        }
+        return (b & 7u) | (b & 56u) << 13;
+    } else {
+        const uint32_t b = p[i / 4] >> (8 * (i % 4));
+        return (b & 15u) | (b & 240u) << 12;
+    }
+}
+
+// A workgroup turns 64 rows x 128 k: each wave decodes one packed tile (a lane
+// the 32 k of one row), neighbouring lanes pair up their rows' values, and
+// the block leaves through LDS as 128-byte pieces of W^T's rows.
+template <int FMT>
+__global__ __launch_bounds__(DT_THREADS) void k_dequant_t(const uint8_t* __restrict__ packed,
+                                                          const uint16_t* __restrict__ lut,
+                                                          const uint16_t* __restrict__ alpha,
+                                                          const uint16_t* __restrict__ beta,
+                                                          uint16_t* __restrict__ wt, int N, int K, int g, int Np)
+{
+    constexpr int BYTES = FMT == FMT_ANY2 ? 8 : FMT == FMT_ANY3 ? 12 : 16;
+    __shared__ float table[4][16][17];
+    __shared__ __attribute__((aligned(16))) uint32_t turned[128 * DT_STRIDE];
+    const int Kc = K / 128, c = blockIdx.x % Kc, n0 = blockIdx.x / Kc * 64;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, j = lane & 15, kq = lane >> 4;
+    if constexpr (FMT != FMT_INT4) {
+        for (int i = tid; i < 1024; i += DT_THREADS) {
+            const int n = n0 + i / 16;
+            table[i / 256][i / 16 % 16][i % 16] = n < N ? bf16_to_f32(lut[static_cast<size_t>(n) * 16 + i % 16]) : 0.0f;
+        }
+        __syncthreads();
+    }
+    const int n = n0 + 16 * w + j;
+    uint32_t out[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        out[i] = 0u;
+    if (n < N) {
+        const int G = K / g, grp = (c * 128 + kq * 32) / g;
+        const float a = bf16_to_f32(alpha[static_cast<size_t>(n) * G + grp]);
+        const float b = bf16_to_f32(beta[static_cast<size_t>(n) * G + grp]);
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+            packed + ((static_cast<size_t>(n / 16) * Kc + c) * 64 + lane) * BYTES);
+        uint32_t p[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < BYTES / 4; ++i)
+            p[i] = src[i];
+        const float* T = table[w][j];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t q = code_pair<FMT>(p, i);
+            const float lo = FMT == FMT_INT4 ? static_cast<float>(q & 0xffffu) : T[q & 0xffffu];
+            const float hi = FMT == FMT_INT4 ? static_cast<float>(q >> 16) : T[q >> 16];
+            out[i] = f32_to_bf16(fmaf(a, lo, b)) | f32_to_bf16(fmaf(a, hi, b)) << 16;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        // rows j and j ^ 1: the even lane takes both values of k 2i, the odd of 2i + 1
+        const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(out[i]), 0xB1, 0xf, 0xf, true));
+        const uint32_t pair = j & 1 ? __builtin_amdgcn_perm(out[i], other, 0x07060302u)
+                                    : __builtin_amdgcn_perm(other, out[i], 0x05040100u);
+        turned[(32 * kq + 2 * i + (j & 1)) * DT_STRIDE + 8 * w + j / 2] = pair;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int q = tid + DT_THREADS * i, k = q / 8, e = q % 8;
+        *reinterpret_cast<u32x4_t*>(wt + static_cast<size_t>(c * 128 + k) * Np + n0 + 8 * e) =
+            *reinterpret_cast<const u32x4_t*>(&turned[k * DT_STRIDE + 4 * e]);
+    }
+}
+
+// dy with rows padded to Np by zeros, where its own rows are not whole steps
+// of aligned 16-byte pieces.
+__global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ dy, uint16_t* __restrict__ out, int N, int Np,
+                                                  size_t pieces)
+{
+    const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;
+    if (i >= pieces)
+        return;
+    const int per = Np / 8;
+    const size_t m = i / per;
+    const int n = static_cast<int>(i % per) * 8;
+    reinterpret_cast<u32x4_t*>(out)[i] = load8(dy + m * N + n, N - n);
+}
+
+// ---------------------------------------------------------------------------
+// the product
+// ---------------------------------------------------------------------------
+// 128 rows of dy x 128 rows of W^T a workgroup, 64 n a step: both tiles go to
+// LDS by direct loads, the next step's while this one is multiplied.  A row of
+// a tile is eight 16-byte pieces; piece q stands at q ^ key(row), keys chosen
+// so that the 16 lanes of an operand read touch all 64 banks once.
+constexpr int BM = 128, BN = 128, DX_THREADS = 256;
+
+struct DxArgs {
+    const uint16_t* dy;     // [M][Np]
+    const uint16_t* wt;     // [K][Np]
+    uint16_t* dx;           // [M][K]
+    float* part;            // [S][M][K] or null (S = 1)
+    int M, K, Np, S;
+};
+
+// rows of dy are read as operands 16 in a row; rows of W^T by row_of()
+__device__ __forceinline__ int key_dy(int r) { return r >> 1 & 7; }
+__device__ __forceinline__ int key_wt(int r) { return (r >> 1 & 1) | (r >> 4 & 3) << 1; }
+// row of W^T (of 64) that operand t's lane row rho holds: a lane's outputs are
+// then 16 adjacent k
+__device__ __forceinline__ int row_of(int t, int rho) { return 16 * (rho >> 2) + 4 * t + (rho & 3); }
+
+typedef const __attribute__((address_space(1))) uint32_t* gptr_t;
+typedef __attribute__((address_space(3))) uint32_t* lptr_t;
+
+__global__ __launch_bounds__(DX_THREADS) void k_dx(const DxArgs p)
+{
+    __shared__ __attribute__((aligned(16))) uint16_t sa[2][BM * STEP], sb[2][BN * STEP];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, g = lane >> 4;
+    const int tiles_k = p.K / BN, tiles_m = (p.M + BM - 1) / BM, tiles = tiles_k * tiles_m;
+    // workgroups go to the eight XCDs in turn: each gets a run of tiles that
+    // share rows, which its L2 then holds
+    int id = blockIdx.x;
+    if (tiles % 8 == 0)
+        id = id % 8 * (tiles / 8) + id / 8;
+    const int m0 = id / tiles_k * BM, k0 = id % tiles_k * BN;
+    const int steps = p.Np / STEP;
+    const int s0 = static_cast<int>(static_cast<int64_t>(steps) * blockIdx.y / p.S);
+    const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (blockIdx.y + 1) / p.S);
+
+    // a wave's load instruction fills 8 rows of a tile; lane: row lane / 8, place lane % 8
+    const uint16_t* ga[4];
+    const uint16_t* gb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (w * 4 + i) * 8 + lane / 8;
+        const int m = m0 + r < p.M ? m0 + r : p.M - 1;
+        ga[i] = p.dy + static_cast<size_t>(m) * p.Np + ((lane & 7) ^ key_dy(r)) * 8;
+        gb[i] = p.wt + static_cast<size_t>(k0 + r) * p.Np + ((lane & 7) ^ key_wt(r)) * 8;
+    }
+    auto fetch = [&](int st, int buf) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __builtin_amdgcn_global_load_lds((gptr_t)(ga[i] + static_cast<size_t>(st) * STEP),
+                                             (lptr_t)(&sa[buf][(w * 4 + i) * 8 * STEP]), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((gptr_t)(gb[i] + static_cast<size_t>(st) * STEP),
+                                             (lptr_t)(&sb[buf][(w * 4 + i) * 8 * STEP]), 16, 0, 0);
+        }
+    };
+    f32x4_t acc[4][4];     // [rows of dy][rows of W^T]
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            acc[i][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const int wm = (w >> 1) * 64, wk = (w & 1) * 64;
+    if (s0 < s1)
+        fetch(s0, 0);
+    for (int st = s0; st < s1; ++st) {
+        const int buf = (st - s0) & 1;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();      // this step's tiles are in, and the other buffer has been read
+        if (st + 1 < s1)
+            fetch(st + 1, buf ^ 1);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            bf16x8_t a[4], b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int ra = wm + 16 * i + c, rb = wk + row_of(i, c);
+                a[i] = *reinterpret_cast<const bf16x8_t*>(&sa[buf][ra * STEP + ((4 * kk + g) ^ key_dy(ra)) * 8]);
+                b[i] = *reinterpret_cast<const bf16x8_t*>(&sb[buf][rb * STEP + ((4 * kk + g) ^ key_wt(rb)) * 8]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    acc[i][t] = mfma(b[t], a[i], acc[i][t]);
+        }
+    }
+    // lane: row c of dy, k 16g .. 16g + 15 of the wave's 64
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = m0 + wm + 16 * i + c;
+        if (m >= p.M)
+            continue;
+        const size_t at = static_cast<size_t>(m) * p.K + k0 + wk + 16 * g;
+        if (p.part) {
+            f32x4_t* o = reinterpret_cast<f32x4_t*>(p.part + static_cast<size_t>(blockIdx.y) * p.M * p.K + at);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                o[t] = acc[i][t];
+        } else {
+            u32x4_t o[2];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    o[t / 2][2 * (t % 2) + e] = f32_to_bf16(acc[i][t][2 * e]) | f32_to_bf16(acc[i][t][2 * e + 1]) << 16;
+            u32x4_t* d = reinterpret_cast<u32x4_t*>(p.dx + at);
+            d[0] = o[0];
+            d[1] = o[1];
+        }
+    }
+}
+
+// The splits' sums in order, 4 values a thread.
+__global__ __launch_bounds__(256) void k_dx_sum(const float* __restrict__ part, uint16_t* __restrict__ dx, int S, size_t quads)
+{
+    const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;
+    if (i >= quads)
+        return;
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < S; ++s)
+        v += reinterpret_cast<const f32x4_t*>(part)[s * quads + i];
+    u32x2_t o;
+    o[0] = f32_to_bf16(v[0]) | f32_to_bf16(v[1]) << 16;
+    o[1] = f32_to_bf16(v[2]) | f32_to_bf16(v[3]) << 16;
+    reinterpret_cast<u32x2_t*>(dx)[i] = o;
+}
+
+// dx = 0: a layer without outputs.
+__global__ __launch_bounds__(256) void k_dx_zero(uint16_t* dx, size_t octs)
+{
+    const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;
+    if (i < octs)
+        reinterpret_cast<u32x4_t*>(dx)[i] = u32x4_t{0u, 0u, 0u, 0u};
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+int64_t padded(int64_t N) { return (N + STEP - 1) / STEP * STEP; }
+
+// n is split where the tiles alone leave the 256 CUs idle, at least 4 steps to
+// a split; the partial sums are fp32.
+int dx_splits(int64_t M, int64_t N, int64_t K)
+{
+    const int64_t tiles = (M + BM - 1) / BM * (K / BN), steps = padded(N) / STEP;
+    int64_t S = (512 + tiles - 1) / tiles;
+    S = S < steps / 4 ? S : steps / 4;
+    return static_cast<int>(S < 1 ? 1 : S > 16 ? 16 : S);
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+size_t wt_bytes(int64_t N, int64_t K) { return up256(static_cast<size_t>(K) * padded(N) * 2); }
+
+size_t dx_part_bytes(int64_t M, int64_t N, int64_t K)
+{
+    const int S = dx_splits(M, N, K);
+    return S > 1 ? up256(static_cast<size_t>(S) * M * K * 4) : 0;
+}
+
+bool dx_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t g)
+{
+    const int64_t top = static_cast<int64_t>(1) << 31;
+    return M >= 0 && M <= 65535 * 64 && N >= 0 && N < top / 32 && K >= 0 && K < top && g > 0 && g % 128 == 0 &&
+           K % g == 0 && N * K < 2 * top && M * K * 2 < top && M * N * 2 < top;
+}
+
+any4_status gemm_dx(int fmt, const uint16_t* dy, const uint8_t* packed, const uint16_t* lut, const uint16_t* alpha,
+                    const uint16_t* beta, uint16_t* dx, int64_t M, int64_t N, int64_t K, int64_t g, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream)
+{
+    if (!dx_sizes_ok(M, N, K, g))
+        return ANY4_E_SHAPE;
+    if (M == 0 || K == 0)
+        return ANY4_OK;
+    if (!dx || (N > 0 && (!dy || !packed || (fmt != FMT_INT4 && !lut) || !alpha || !beta || !workspace)))
+        return ANY4_E_NULL;
+    if (!is_aligned(dx, 16) || (N > 0 && (!is_aligned(dy, 2) || !is_aligned(packed, 16) || !is_aligned(lut, 2) ||
+                                          !is_aligned(alpha, 2) || !is_aligned(beta, 2) || !is_aligned(workspace, 16))))
+        return ANY4_E_ALIGN;
+    if (N > 0 && workspace_bytes < any4_gemm_dx_workspace_size(M, N, K, g))
+        return ANY4_E_WORKSPACE;
+    (void)hipGetLastError();
+    if (N == 0) {
+        const size_t octs = static_cast<size_t>(M) * K / 8;
+        hipLaunchKernelGGL(k_dx_zero, dim3(static_cast<unsigned>((octs + 255) / 256)), dim3(256), 0, stream, dx, octs);
+        return launch_status();
+    }
+    const int Np = static_cast<int>(padded(N));
+    char* at = static_cast<char*>(workspace);
+    uint16_t* wt = reinterpret_cast<uint16_t*>(at);
+    at += wt_bytes(N, K);
+    const dim3 grid(static_cast<unsigned>(Np / 64 * (K / 128)));
+#define TURN(FMT_) hipLaunchKernelGGL(k_dequant_t<FMT_>, grid, dim3(DT_THREADS), 0, stream, packed, lut, alpha, beta, wt, \
+                                      static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), Np)
+    if (fmt == FMT_ANY4) TURN(FMT_ANY4);
+    else if (fmt == FMT_INT4) TURN(FMT_INT4);
+    else if (fmt == FMT_ANY2) TURN(FMT_ANY2);
+    else TURN(FMT_ANY3);
+#undef TURN
+    DxArgs a{dy, wt, dx, nullptr, static_cast<int>(M), static_cast<int>(K), Np, dx_splits(M, N, K)};
+    if (N != Np || !is_aligned(dy, 16)) {
+        uint16_t* copy = reinterpret_cast<uint16_t*>(at);
+        const size_t pieces = static_cast<size_t>(M) * (Np / 8);
+        hipLaunchKernelGGL(k_pad_rows, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, dy, copy,
+                           static_cast<int>(N), Np, pieces);
+        a.dy = copy;
+    }
+    at += up256(static_cast<size_t>(M) * Np * 2);
+    if (a.S > 1)
+        a.part = reinterpret_cast<float*>(at);
+    const unsigned tiles = static_cast<unsigned>((M + BM - 1) / BM * (K / BN));
+    hipLaunchKernelGGL(k_dx, dim3(tiles, static_cast<unsigned>(a.S)), dim3(DX_THREADS), 0, stream, a);
+    if (a.S > 1) {
+        const size_t quads = static_cast<size_t>(M) * K / 4;
+        hipLaunchKernelGGL(k_dx_sum, dim3(static_cast<unsigned>((quads + 255) / 256)), dim3(256), 0, stream, a.part, dx, a.S,
+                           quads);
+    }
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t any4_gemm_dx_workspace_size(int64_t M, int64_t N, int64_t K, int64_t g)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || !dx_sizes_ok(M, N, K, g))
+        return 0;
+    return wt_bytes(N, K) + up256(static_cast<size_t>(M) * padded(N) * 2) + dx_part_bytes(M, N, K);
+}
+
+any4_status any4_gemm_dx(const uint16_t* dy, const uint8_t* packed, const uint16_t* lut, const uint16_t* alpha,
+                         const uint16_t* beta, uint16_t* dx, int64_t M, int64_t N, int64_t K, int64_t g, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream)
+{
+    return gemm_dx(FMT_ANY4, dy, packed, lut, alpha, beta, dx, M, N, K, g, workspace, workspace_bytes, stream);
+}
+
+any4_status any4_gemm_int4_dx(const uint16_t* dy, const uint8_t* packed, const uint16_t* alpha, const uint16_t* beta,
+                              uint16_t* dx, int64_t M, int64_t N, int64_t K, int64_t g, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream)
+{
+    return gemm_dx(FMT_INT4, dy, packed, nullptr, alpha, beta, dx, M, N, K, g, workspace, workspace_bytes, stream);
+}
+
+any4_status any2_gemm_dx(const uint16_t* dy, const uint8_t* packed, const uint16_t* lut, const uint16_t* alpha,
+                         const uint16_t* beta, uint16_t* dx, int64_t M, int64_t N, int64_t K, int64_t g, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream)
+{
+    return gemm_dx(FMT_ANY2, dy, packed, lut, alpha, beta, dx, M, N, K, g, workspace, workspace_bytes, stream);
+}
+
+any4_status any3_gemm_dx(const uint16_t* dy, const uint8_t* packed, const uint16_t* lut, const uint16_t* alpha,
+                         const uint16_t* beta, uint16_t* dx, int64_t M, int64_t N, int64_t K, int64_t g, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream)
+{
+    return gemm_dx(FMT_ANY3, dy, packed, lut, alpha, beta, dx, M, N, K, g, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,1139 @@
+// Low-rank adapters beside a frozen any4 layer, served for many requests at
+// once and trained, and activations kept in 8 bits.  The C ABI is declared in
+// include/any4.h.
+//
+// The mathematics.  Row m of the batch uses adapter a = ids[m]:
+//     h[m]   = A_a x[m]                       y'[m]  = y[m]  + s_a sum_j h[m][j] B_a[j]
+//     dh[m]  = s_a B_a dy[m]                  dx'[m] = dx[m] + sum_j dh[m][j] A_a[j]
+//     dA_a   = sum_m dh[m]^T x[m]             dB_a   = s_a sum_m h[m]^T dy[m]
+// A is [L][r][K] and B [L][r][N] (rank-major), so a pass is made of three
+// products, each used twice:
+//     shrink   part[m][j] = sum_d in[m][d] W_a[j][d]       (x with A, dy with B)
+//     expand   out[m][d]  = base[m][d] + sum_j c[m][j] W_a[j][d]
+//     wgrad    G_a[j][d]  = sum_m c[m][j] in[m][d]
+// The fp32 factors (h, dh) enter the matrix cores as three bf16 parts
+// (split3), which together are the fp32 value: with r <= 128 the products are
+// never what bounds a kernel, so nothing is rounded that need not be.
+//
+// Rows of one adapter are worked on in tiles.  Up to SMALL_M rows a wave finds
+// its tile from the ids alone (ballots); beyond that the plan (rows sorted by
+// adapter, tables of tiles and chunks) is made by k_plan* once, in the
+// workspace or, for callers that keep it, in a buffer of theirs.
+#include "frag.h"
+
+namespace {
+
+constexpr int SMALL_M = 64;          // up to here tiles come from ballots over the ids
+constexpr int SMALL_T = 16;          // rows of a tile there
+constexpr int TILE_T = 64;           // rows of a tile of the plan
+constexpr int CHUNK = 512;           // rows of a chunk of the weight gradient
+constexpr int MAX_RANK = 128;
+constexpr int MAX_ADAPTERS = 4096;
+constexpr int64_t MAX_M = 65535 * 64;
+
+// ---------------------------------------------------------------------------
+// the plan: rows sorted by adapter (stable), tiles and chunks of equal adapter
+// ---------------------------------------------------------------------------
+// int32 words: [0] tiles, [1] chunks, [2] M, [3] L, then
+//   seg   [L+2]  first sorted position of each adapter, of the rows without
+//                one (entry L), and M
+//   slot  [L+1]  first partial-sum slot of each adapter (adapters of one chunk
+//                or none have no slot)
+//   tile  [TB][3]  adapter (-1: none), first sorted position, rows
+//   chunk [CB][4]  the same and the chunk's slot (-1: the only one)
+//   perm  [M]    row at each sorted position
+struct PlanLayout {
+    int64_t seg, slot, tile, chunk, perm, words;
+    int64_t TB, CB;
+
+    __host__ __device__ PlanLayout(int64_t M, int64_t L)
+    {
+        const int64_t segs = M < L + 1 ? M : L + 1;
+        TB = M / TILE_T + segs;
+        CB = M / CHUNK + segs;
+        seg = 4;
+        slot = seg + L + 2;
+        tile = slot + L + 1;
+        chunk = tile + 3 * TB;
+        perm = chunk + 4 * CB;
+        words = perm + M;
+    }
+};
+
+constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_WAVES = PLAN_THREADS / WAVE;
+constexpr int PLAN_ONE_M = 16384;    // up to here (and PLAN_ONE_L) one workgroup does it all
+constexpr int PLAN_ONE_L = 512;
+constexpr int PLAN_PARTS = 256;      // beyond: waves of their own, with counts in memory
+
+__device__ __forceinline__ int adapter_of(int id, int L) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(L) ? id : L; }
+
+// Lanes of the wave that hold the same value, by the values in turn.
+__device__ __forceinline__ uint64_t same_lanes(int v, bool live)
+{
+    uint64_t left = __ballot(live), mine = 0;
+    while (left) {
+        const int a = __builtin_amdgcn_readlane(v, __builtin_ctzll(left));
+        const uint64_t m = __ballot(live && v == a);
+        if (v == a)
+            mine = m;
+        left &= ~m;
+    }
+    return mine;
+}
+
+__device__ __forceinline__ void count_rows(const int* ids, int m0, int m1, int L, int* cnt)
+{
+    for (int m = m0 + (threadIdx.x & 63); m < m1; m += WAVE)
+        atomicAdd(&cnt[adapter_of(ids[m], L)], 1);
+}
+
+// Places the rows [m0, m1) at the positions that `next` counts up, in row order.
+__device__ __forceinline__ void place_rows(const int* ids, int m0, int m1, int L, int* next, int* perm)
+{
+    const int lane = threadIdx.x & 63;
+    for (int b = m0; b < m1; b += WAVE) {
+        const int m = b + lane;
+        const bool live = m < m1;
+        const int a = live ? adapter_of(ids[m], L) : -1;
+        const uint64_t mask = same_lanes(a, live);
+        const int lead = mask ? __builtin_ctzll(mask) : lane;
+        int at = 0;
+        if (live && lane == lead)
+            at = atomicAdd(&next[a], __builtin_popcountll(mask));
+        at = __shfl(at, lead);
+        if (live)
+            perm[at + __builtin_popcountll(mask & ((1ull << lane) - 1))] = m;
+    }
+}
+
+struct Four {
+    int v[4];
+};
+
+// Exclusive sums over the block's threads.
+__device__ __forceinline__ Four block_scan(Four x, int (*wave_sum)[4])
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    Four s = x;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        for (int d = 1; d < WAVE; d <<= 1) {
+            const int o = __shfl_up(s.v[q], d);
+            s.v[q] += lane >= d ? o : 0;
+        }
+        if (lane == 63)
+            wave_sum[w][q] = s.v[q];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        int before = 0;
+        for (int i = 0; i < w; ++i)
+            before += wave_sum[i][q];
+        s.v[q] += before - x.v[q];
+    }
+    return s;
+}
+
+__device__ __forceinline__ int chunks_of(int rows) { return (rows + CHUNK - 1) / CHUNK; }
+
+// From cnt[part][L+1] (rows of each adapter in each part of the batch): the
+// plan's tables, and cnt turned into the first position of each.
+__device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, int* plan, int* s_seg,
+                                            int* s_tile, int* s_chunk, int (*wave_sum)[4])
+{
+    const PlanLayout p(M, L);
+    const int tid = threadIdx.x, per = (L + 1 + PLAN_THREADS - 1) / PLAN_THREADS;
+    Four sum = {{0, 0, 0, 0}};
+    for (int e = 0; e < per; ++e) {
+        const int a = tid * per + e;
+        if (a > L)
+            break;
+        int n = 0;
+        for (int q = 0; q < parts; ++q) {
+            const int c = cnt[static_cast<size_t>(q) * (L + 1) + a];
+            cnt[static_cast<size_t>(q) * (L + 1) + a] = n;
+            n += c;
+        }
+        const int ch = a < L ? chunks_of(n) : 0;
+        s_seg[a] = n;
+        sum.v[0] += n;
+        sum.v[1] += (n + TILE_T - 1) / TILE_T;
+        sum.v[2] += ch;
+        sum.v[3] += ch > 1 ? ch : 0;
+    }
+    Four at = block_scan(sum, wave_sum);
+    for (int e = 0; e < per; ++e) {
+        const int a = tid * per + e;
+        if (a > L)
+            break;
+        const int n = s_seg[a], ch = a < L ? chunks_of(n) : 0;
+        for (int q = 0; q < parts; ++q)
+            cnt[static_cast<size_t>(q) * (L + 1) + a] += at.v[0];
+        s_seg[a] = at.v[0];
+        s_tile[a] = at.v[1];
+        s_chunk[a] = at.v[2];
+        plan[p.seg + a] = at.v[0];
+        plan[p.slot + a] = at.v[3];
+        at.v[0] += n;
+        at.v[1] += (n + TILE_T - 1) / TILE_T;
+        at.v[2] += ch;
+        at.v[3] += ch > 1 ? ch : 0;
+        if (a == L) {
+            s_seg[L + 1] = M;
+            s_tile[L + 1] = at.v[1];
+            s_chunk[L + 1] = at.v[2];
+            plan[p.seg + L + 1] = M;
+            plan[0] = at.v[1];
+            plan[1] = at.v[2];
+            plan[2] = M;
+            plan[3] = L;
+        }
+    }
+    __syncthreads();
+    for (int kind = 0; kind < 2; ++kind) {
+        const int* start = kind ? s_chunk : s_tile;
+        const int total = start[L + 1], size = kind ? CHUNK : TILE_T;
+        for (int t = tid; t < total; t += PLAN_THREADS) {
+            int lo = 0, hi = L + 1;      // the last adapter that starts at or before t
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (start[mid] <= t)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            const int first = s_seg[lo] + (t - start[lo]) * size;
+            const int left = s_seg[lo + 1] - first, rows = left < size ? left : size;
+            if (kind == 0) {
+                int* o = plan + p.tile + 3 * static_cast<int64_t>(t);
+                o[0] = lo < L ? lo : -1;
+                o[1] = first;
+                o[2] = rows;
+            } else {
+                int* o = plan + p.chunk + 4 * static_cast<int64_t>(t);
+                o[0] = lo;
+                o[1] = first;
+                o[2] = rows;
+                o[3] = start[lo + 1] - start[lo] > 1 ? plan[p.slot + lo] + t - start[lo] : -1;
+            }
+        }
+    }
+}
+
+__global__ __launch_bounds__(PLAN_THREADS) void k_plan(const int* __restrict__ ids, int* plan, int M, int L)
+{
+    __shared__ int cnt[PLAN_WAVES * (PLAN_ONE_L + 1)];
+    __shared__ int s_seg[PLAN_ONE_L + 2], s_tile[PLAN_ONE_L + 2], s_chunk[PLAN_ONE_L + 2];
+    __shared__ int wave_sum[PLAN_WAVES][4];
+    for (int i = threadIdx.x; i < PLAN_WAVES * (L + 1); i += PLAN_THREADS)
+        cnt[i] = 0;
+    __syncthreads();
+    const int w = threadIdx.x >> 6, per = (M + PLAN_WAVES * WAVE - 1) / (PLAN_WAVES * WAVE) * WAVE;
+    const int m0 = w * per < M ? w * per : M, m1 = m0 + per < M ? m0 + per : M;
+    count_rows(ids, m0, m1, L, cnt + w * (L + 1));
+    __syncthreads();
+    plan_tables(cnt, PLAN_WAVES, M, L, plan, s_seg, s_tile, s_chunk, wave_sum);
+    __syncthreads();
+    place_rows(ids, m0, m1, L, cnt + w * (L + 1), plan + PlanLayout(M, L).perm);
+}
+
+// Larger batches or many adapters: the same in three launches, one wave for
+// each part of the batch, the counts in memory (PLAN_PARTS x (L + 1) words).
+__global__ __launch_bounds__(WAVE) void k_plan_count(const int* __restrict__ ids, int* cnt, int M, int L, int per)
+{
+    int* mine = cnt + static_cast<size_t>(blockIdx.x) * (L + 1);
+    for (int i = threadIdx.x; i <= L; i += WAVE)
+        mine[i] = 0;
+    __threadfence();     // the zeros are in place before the atomics below
+    __syncthreads();
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * per;
+    if (m0 < M)
+        count_rows(ids, static_cast<int>(m0), static_cast<int>(m0 + per < M ? m0 + per : M), L, mine);
+}
+
+__global__ __launch_bounds__(PLAN_THREADS) void k_plan_tables(int* cnt, int* plan, int M, int L)
+{
+    __shared__ int s_seg[MAX_ADAPTERS + 2], s_tile[MAX_ADAPTERS + 2], s_chunk[MAX_ADAPTERS + 2];
+    __shared__ int wave_sum[PLAN_WAVES][4];
+    plan_tables(cnt, PLAN_PARTS, M, L, plan, s_seg, s_tile, s_chunk, wave_sum);
+}
+
+__global__ __launch_bounds__(WAVE) void k_plan_place(const int* __restrict__ ids, int* cnt, int* plan, int M, int L, int per)
+{
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * per;
+    if (m0 < M)
+        place_rows(ids, static_cast<int>(m0), static_cast<int>(m0 + per < M ? m0 + per : M), L,
+                   cnt + static_cast<size_t>(blockIdx.x) * (L + 1), plan + PlanLayout(M, L).perm);
+}
+
+bool plan_in_one(int64_t M, int64_t L) { return M <= PLAN_ONE_M && L <= PLAN_ONE_L; }
+
+// words of the plan, and of the counts behind it
+int64_t plan_words(int64_t M, int64_t L)
+{
+    return PlanLayout(M, L).words + (plan_in_one(M, L) ? 0 : PLAN_PARTS * (L + 1));
+}
+
+void launch_plan(const int32_t* ids, int32_t* plan, int64_t M, int64_t L, hipStream_t stream)
+{
+    const int m = static_cast<int>(M), l = static_cast<int>(L);
+    if (plan_in_one(M, L)) {
+        hipLaunchKernelGGL(k_plan, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
+        return;
+    }
+    int* cnt = plan + PlanLayout(M, L).words;
+    const int per = (m + PLAN_PARTS * WAVE - 1) / (PLAN_PARTS * WAVE) * WAVE;
+    hipLaunchKernelGGL(k_plan_count, dim3(PLAN_PARTS), dim3(WAVE), 0, stream, ids, cnt, m, l, per);
+    hipLaunchKernelGGL(k_plan_tables, dim3(1), dim3(PLAN_THREADS), 0, stream, cnt, plan, m, l);
+    hipLaunchKernelGGL(k_plan_place, dim3(PLAN_PARTS), dim3(WAVE), 0, stream, ids, cnt, plan, m, l, per);
+}
+
+// ---------------------------------------------------------------------------
+// the rows of a tile
+// ---------------------------------------------------------------------------
+struct Rows {
+    int a;        // adapter, -1: rows without one, -2: no such tile
+    int count;
+};
+
+struct Batch {
+    const int* ids;     // [M]
+    const int* plan;    // null for M <= SMALL_M
+    int M, L;
+};
+
+// Puts the rows of tile t into rows[] (wave 0 writes; the caller synchronises).
+template <int T>
+__device__ __forceinline__ Rows tile_rows(const Batch& b, int t, int* rows)
+{
+    const int tid = threadIdx.x;
+    if constexpr (T == SMALL_T) {
+        const int lane = tid & 63;
+        const bool live = lane < b.M;
+        const int id = live ? adapter_of(b.ids[lane], b.L) : -1;
+        uint64_t left = __ballot(live);
+        while (left) {
+            const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+            const uint64_t m = __ballot(live && id == a);
+            const int n = __builtin_popcountll(m), tiles = (n + T - 1) / T;
+            if (t < tiles) {
+                const int rank = __builtin_popcountll(m & ((1ull << lane) - 1)) - t * T;
+                if (tid < WAVE && (m >> lane & 1) && rank >= 0 && rank < T)
+                    rows[rank] = lane;
+                return {a < b.L ? a : -1, n - t * T < T ? n - t * T : T};
+            }
+            t -= tiles;
+            left &= ~m;
+        }
+        return {-2, 0};
+    } else {
+        if (t >= b.plan[0] || b.plan[2] != b.M || b.plan[3] != b.L)
+            return {-2, 0};
+        const PlanLayout p(b.M, b.L);
+        const int* e = b.plan + p.tile + 3 * static_cast<int64_t>(t);
+        const int first = e[1], n = e[2];
+        if (tid < n)
+            rows[tid] = b.plan[p.perm + first + tid];
+        return {e[0], n};
+    }
+}
+
+int64_t tile_bound(int64_t M, int64_t L)
+{
+    if (M <= SMALL_M)       // each adapter's rows in tiles of SMALL_T
+        return M / SMALL_T + (M < L + 1 ? M : L + 1);
+    return PlanLayout(M, L).TB;
+}
+
+// ---------------------------------------------------------------------------
+// activations in 8 bits: s = fp32(amax / 127) over GROUP8 channels,
+// q = rint(fp32(x * fp32(127 / amax)))
+// ---------------------------------------------------------------------------
+constexpr int GROUP8 = 128;
+
+__device__ __forceinline__ uint32_t abs_max(u32x4_t v)
+{
+    // magnitudes of bf16 values order as their bits, a NaN above an infinity
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = v[i] & 0x7fffu, hi = v[i] >> 16 & 0x7fffu;
+        m = max(m, max(lo, hi));
+    }
+    return m;
+}
+
+struct Scale8 {
+    float unit, inv;
+};
+
+__device__ __forceinline__ Scale8 scale8(uint32_t top)
+{
+    const float amax = bf16_to_f32(top);
+    // below 2^-100 the inverse would overflow: such a group is kept as zeros
+    const bool dead = amax < 0x1p-100f;
+    return {dead ? 0.0f : amax / 127.0f, dead ? 0.0f : 127.0f / amax};
+}
+
+__device__ __forceinline__ u32x2_t quantise8(u32x4_t v, float inv)
+{
+    u32x2_t q = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float f = __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+        const int k = __float2int_rn(f * inv);      // a NaN gives 0: its group's scale is NaN or inf
+        q[i / 4] |= static_cast<uint32_t>(k & 0xff) << (8 * (i & 3));
+    }
+    return q;
+}
+
+// Signed byte i of v as fp32.
+__device__ __forceinline__ float byte_to_f32(uint32_t v, int i)
+{
+    return static_cast<float>(static_cast<int>(v << (24 - 8 * i)) >> 24);
+}
+
+constexpr int ACT8_THREADS = 256;
+
+// One 16-lane group per GROUP8 channels, 16 bytes of x a lane.
+__global__ __launch_bounds__(ACT8_THREADS) void k_act8_save(const uint16_t* __restrict__ x, uint8_t* __restrict__ q,
+                                                            float* __restrict__ s, uint32_t slots)
+{
+    const uint32_t i = blockIdx.x * ACT8_THREADS + threadIdx.x;
+    if (i >= slots)      // slots is a multiple of 16: a group is live as a whole
+        return;
+    const u32x4_t v = reinterpret_cast<const u32x4_t*>(x)[i];
+    uint32_t top = abs_max(v);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1)
+        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
+    const Scale8 g = scale8(top);
+    reinterpret_cast<u32x2_t*>(q)[i] = quantise8(v, g.inv);
+    if ((i & 15) == 0)
+        s[i >> 4] = g.unit;
+}
+
+__global__ __launch_bounds__(ACT8_THREADS) void k_act8_load(const uint8_t* __restrict__ q, const float* __restrict__ s,
+                                                            uint16_t* __restrict__ x, uint32_t slots)
+{
+    const uint32_t i = blockIdx.x * ACT8_THREADS + threadIdx.x;
+    if (i >= slots)
+        return;
+    const u32x2_t v = reinterpret_cast<const u32x2_t*>(q)[i];
+    const float unit = s[i >> 4];
+    u32x4_t o;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        o[p] = f32_to_bf16(byte_to_f32(v[p / 2], (2 * p) & 3) * unit) |
+               f32_to_bf16(byte_to_f32(v[p / 2], (2 * p + 1) & 3) * unit) << 16;
+    reinterpret_cast<u32x4_t*>(x)[i] = o;
+}
+
+// ---------------------------------------------------------------------------
+// shrink: part[sk][m][j] = sum over this split's d of in[m][d] W_a[j][d]
+// ---------------------------------------------------------------------------
+// A workgroup takes a tile of rows, 16*RB ranks and one of SK ranges of d,
+// which its four waves share out again in steps of 128; the matrix cores sum
+// 16 rows x 16 ranks x 32 d at a time.  The four waves' sums meet in LDS, the
+// splits' in the expand kernel, both in a fixed order.
+struct ShrinkArgs {
+    Batch b;
+    const uint16_t* in;    // [M][D]
+    const uint16_t* w;     // [L][r][D]
+    float* part;           // [SK][M][r16]
+    uint8_t* q;            // [M][D] int8 and its scales, or null (D % 128 == 0)
+    float* qs;
+    int D, r, r16, SK;
+};
+
+constexpr int SHRINK_THREADS = 256;
+constexpr int SHRINK_WAVES = SHRINK_THREADS / WAVE;
+
+template <int T, int RB, bool Q8>
+__global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
+{
+    constexpr int MS = T / 16;
+    __shared__ int rows[T];
+    __shared__ f32x4_t red[SHRINK_WAVES - 1][MS * RB][WAVE];
+    const Rows tile = tile_rows<T>(p.b, blockIdx.x, rows);
+    if (tile.a == -2 || (tile.a < 0 && !Q8))
+        return;
+    __syncthreads();
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+    const int steps = (p.D + 127) / 128, parts = p.SK * SHRINK_WAVES;
+    const int at = blockIdx.y * SHRINK_WAVES + w, j0 = blockIdx.z * (16 * RB);
+    const int s0 = static_cast<int>(static_cast<int64_t>(steps) * at / parts);
+    const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (at + 1) / parts);
+
+    const uint16_t* in[MS];
+    const uint16_t* wt[RB];
+    size_t row[MS];
+#pragma unroll
+    for (int s = 0; s < MS; ++s) {     // rows behind the last read that one again
+        const int i = 16 * s + c;
+        row[s] = static_cast<size_t>(rows[i < tile.count ? i : tile.count - 1]);
+        in[s] = p.in + row[s] * p.D + 8 * g;
+    }
+#pragma unroll
+    for (int t = 0; t < RB; ++t) {     // and so do ranks behind the last
+        const int j = j0 + 16 * t + c;
+        wt[t] = p.w + (static_cast<size_t>(tile.a < 0 ? 0 : tile.a) * p.r + (j < p.r ? j : p.r - 1)) * p.D + 8 * g;
+    }
+    f32x4_t acc[MS][RB];
+#pragma unroll
+    for (int s = 0; s < MS; ++s)
+#pragma unroll
+        for (int t = 0; t < RB; ++t)
+            acc[s][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int st = s0; st < s1; ++st) {
+        const int d0 = st * 128;
+        u32x4_t wv[RB][4];
+#pragma unroll
+        for (int t = 0; t < RB; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                wv[t][i] = load8(wt[t] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g));
+#pragma unroll
+        for (int s = 0; s < MS; ++s) {
+            if (16 * s < tile.count) {
+                u32x4_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = load8(in[s] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g));
+                if constexpr (Q8) {
+                    if (blockIdx.z == 0 && 16 * s + c < tile.count) {
+                        // the four lanes of a row hold its 128 channels
+                        uint32_t top = max(max(abs_max(v[0]), abs_max(v[1])), max(abs_max(v[2]), abs_max(v[3])));
+                        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
+                        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+                        const Scale8 e = scale8(top);
+                        uint8_t* o = p.q + row[s] * p.D + d0 + 8 * g;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<u32x2_t*>(o + 32 * i) = quantise8(v[i], e.inv);
+                        if (g == 0)
+                            p.qs[row[s] * (p.D / GROUP8) + st] = e.unit;
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < RB; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[s][t] = mfma(__builtin_bit_cast(bf16x8_t, v[i]), __builtin_bit_cast(bf16x8_t, wv[t][i]), acc[s][t]);
+            }
+        }
+    }
+    if (tile.a < 0)
+        return;
+    if (w > 0) {
+#pragma unroll
+        for (int s = 0; s < MS; ++s)
+#pragma unroll
+            for (int t = 0; t < RB; ++t)
+                red[w - 1][s * RB + t][lane] = acc[s][t];
+    }
+    __syncthreads();
+    if (w > 0)
+        return;
+#pragma unroll
+    for (int s = 0; s < MS; ++s)
+#pragma unroll
+        for (int t = 0; t < RB; ++t) {
+            f32x4_t v = acc[s][t];
+#pragma unroll
+            for (int o = 0; o < SHRINK_WAVES - 1; ++o)
+                v += red[o][s * RB + t][lane];
+            const int j = j0 + 16 * t + c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = 16 * s + 4 * g + i;
+                if (m < tile.count && j < p.r16)
+                    p.part[(static_cast<size_t>(blockIdx.y) * p.b.M + rows[m]) * p.r16 + j] = j < p.r ? v[i] : 0.0f;
+            }
+        }
+}
+
+// ---------------------------------------------------------------------------
+// expand: out[m][d] = base[m][d] + f sum_j c[m][j] W_a[j][d]
+// ---------------------------------------------------------------------------
+// c is the sum of shrink's SK parts; with SCALED it takes the adapter's scale
+// here (dh), else the scale multiplies the sum over j (y).  A wave holds the
+// 128 columns of W it works on as matrix-core operands (8 x 8 blocks turned in
+// registers, all loads 16 bytes) and goes over the tile's rows, 16 at a time.
+struct ExpandArgs {
+    Batch b;
+    const float* part;        // [SK][M][r16]
+    const uint16_t* w;        // [L][r][D]
+    const float* scale;       // [L]
+    const uint16_t* base;     // [M][D] or null (0)
+    uint16_t* out;            // [M][D] or null (only c is wanted)
+    float* c;                 // [M][r] or null
+    int D, r, r16, SK;
+};
+
+constexpr int EXPAND_THREADS = 256;
+constexpr int EXPAND_COLS = 128 * EXPAND_THREADS / WAVE;
+
+template <int t>
+__device__ __forceinline__ void mul_column(f32x4_t (&acc)[8], const Split3& a, const u32x4_t (&R)[8])
+{
+    const bf16x8_t b = column<t>(R);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+        acc[t] = mfma(a.part[q], b, acc[t]);
+}
+
+__device__ __forceinline__ void mul_columns(f32x4_t (&acc)[8], const Split3& a, const u32x4_t (&R)[8])
+{
+    mul_column<0>(acc, a, R);
+    mul_column<1>(acc, a, R);
+    mul_column<2>(acc, a, R);
+    mul_column<3>(acc, a, R);
+    mul_column<4>(acc, a, R);
+    mul_column<5>(acc, a, R);
+    mul_column<6>(acc, a, R);
+    mul_column<7>(acc, a, R);
+}
+
+template <int T, int RK, bool SCALED>
+__global__ __launch_bounds__(EXPAND_THREADS) void k_expand(const ExpandArgs p)
+{
+    constexpr int MS = T / 16, STRIDE = 32 * RK + 4;   // 4: rows of a quarter wave in other banks
+    __shared__ int rows[T];
+    __shared__ __attribute__((aligned(16))) float cs[T * STRIDE];
+    const Rows tile = tile_rows<T>(p.b, blockIdx.x, rows);
+    if (tile.a == -2)
+        return;
+    __syncthreads();
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int d0 = blockIdx.y * EXPAND_COLS + (tid >> 6) * 128, d = d0 + 8 * c;     // this lane's 8 columns
+    if (tile.a < 0) {     // rows without an adapter: the base as it is
+        if (p.c && blockIdx.y == 0)
+            for (int i = tid; i < tile.count * p.r; i += EXPAND_THREADS)
+                p.c[static_cast<size_t>(rows[i / p.r]) * p.r + i % p.r] = 0.0f;
+        if (p.out && p.out != p.base && d < p.D)
+            for (int m = g; m < tile.count; m += 4) {
+                const size_t at = static_cast<size_t>(rows[m]) * p.D + d;
+                store8(p.out + at, p.base ? load8(p.base + at, p.D - d) : u32x4_t{0u, 0u, 0u, 0u}, p.D - d);
+            }
+        return;
+    }
+    u32x4_t W[RK][8];
+#pragma unroll
+    for (int k = 0; k < RK; ++k)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int j = 32 * k + 8 * g + u;
+            W[k][u] = u32x4_t{0u, 0u, 0u, 0u};
+            if (j < p.r && p.out)
+                W[k][u] = load8(p.w + (static_cast<size_t>(tile.a) * p.r + j) * p.D + d, p.D - d);
+        }
+    const float scale = p.scale[tile.a];
+    for (int i = tid; i < T * 32 * RK; i += EXPAND_THREADS) {
+        const int m = i / (32 * RK), j = i % (32 * RK);
+        float v = 0.0f;
+        if (m < tile.count && j < p.r16) {
+            const float* src = p.part + static_cast<size_t>(rows[m]) * p.r16 + j;
+            for (int s = 0; s < p.SK; ++s)
+                v += src[static_cast<size_t>(s) * p.b.M * p.r16];
+            if (SCALED)
+                v *= scale;
+            if (p.c && blockIdx.y == 0 && j < p.r)
+                p.c[static_cast<size_t>(rows[m]) * p.r + j] = v;
+        }
+        cs[m * STRIDE + j] = v;
+    }
+    __syncthreads();
+    if (!p.out || d0 >= p.D)     // waves leave whole: every lane holds matrix-core operands
+        return;
+    for (int s = 0; s < MS; ++s) {
+        if (16 * s >= tile.count)
+            break;
+        u32x4_t y[4];
+        size_t at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = 16 * s + 4 * g + i;
+            at[i] = static_cast<size_t>(rows[m < tile.count ? m : 0]) * p.D + d;
+            y[i] = u32x4_t{0u, 0u, 0u, 0u};
+            if (p.base && m < tile.count)
+                y[i] = load8(p.base + at[i], p.D - d);
+        }
+        f32x4_t acc[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < RK; ++k) {
+            float f[8];
+            const f32x4_t* src = reinterpret_cast<const f32x4_t*>(&cs[(16 * s + c) * STRIDE + 32 * k + 8 * g]);
+            const f32x4_t f0 = src[0], f1 = src[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f[e] = f0[e];
+                f[4 + e] = f1[e];
+            }
+            mul_columns(acc, split3(f), W[k]);
+        }
+        const float after = SCALED ? 1.0f : scale;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (16 * s + 4 * g + i >= tile.count)
+                continue;
+            u32x4_t o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = f32_to_bf16(fmaf(after, acc[2 * e][i], bf16_to_f32(y[i][e] & 0xffffu))) |
+                       f32_to_bf16(fmaf(after, acc[2 * e + 1][i], bf16_to_f32(y[i][e] >> 16))) << 16;
+            store8(p.out + at[i], o, p.D - d);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// wgrad: G_a[j][d] = f sum_m c[m][j] in[m][d]
+// ---------------------------------------------------------------------------
+// A workgroup takes 128 columns and the rows of one adapter (or one chunk of
+// them); its eight waves take 32 rows each in turn, and their sums meet in
+// LDS.  Chunks of one adapter leave partial sums, which k_wgrad_sum adds in
+// order.  In 8 bits, the row's scale of these 128 channels goes into c, whose
+// three bf16 parts hold it, and the whole numbers are exact bf16 values.
+struct WgradJob {
+    const uint16_t* in;      // [M][D] bf16, or null:
+    const uint8_t* q;        // [M][D] int8 and
+    const float* qs;         // [M][D/128] its scales
+    const float* c;          // [M][r]
+    float* out;              // [L][r][D] or null
+    float* part;             // [slots][r][cols * 128]
+    int D, cols;             // columns, and blocks of 128 of them
+    bool scaled;             // multiply by the adapter's scale
+};
+
+struct WgradArgs {
+    Batch b;
+    const float* scale;
+    WgradJob job[2];
+    int r;
+    bool chunked;            // blockIdx.y is a chunk of the plan; else an adapter
+};
+
+constexpr int WGRAD_THREADS = 512;
+constexpr int WGRAD_WAVES = WGRAD_THREADS / WAVE;
+
+template <int RT>
+__global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
+{
+    __shared__ int rows[CHUNK];
+    __shared__ float red[WGRAD_WAVES / 2][RT * 32][WAVE];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, g = lane >> 4;
+    const bool second = static_cast<int>(blockIdx.x) >= p.job[0].cols;
+    const WgradJob job = second ? p.job[1] : p.job[0];
+    const int cb = static_cast<int>(blockIdx.x) - (second ? p.job[0].cols : 0), j0 = blockIdx.z * (16 * RT);
+    int a = blockIdx.y, count = 0, slot = -1;
+    if (p.b.plan && (p.b.plan[2] != p.b.M || p.b.plan[3] != p.b.L))
+        return;
+    if (p.chunked) {
+        if (a >= p.b.plan[1])
+            return;
+        const PlanLayout l(p.b.M, p.b.L);
+        const int* e = p.b.plan + l.chunk + 4 * static_cast<int64_t>(a);
+        a = e[0];
+        const int first = e[1];
+        count = e[2];
+        slot = e[3];
+        if (tid < count)
+            rows[tid] = p.b.plan[l.perm + first + tid];
+    } else if (p.b.plan) {
+        const PlanLayout l(p.b.M, p.b.L);
+        const int first = p.b.plan[l.seg + a];
+        count = p.b.plan[l.seg + a + 1] - first;      // at most M <= CHUNK
+        if (tid < count)
+            rows[tid] = p.b.plan[l.perm + first + tid];
+    } else {
+        const bool mine = lane < p.b.M && p.b.ids[lane < p.b.M ? lane : 0] == a;
+        const uint64_t m = __ballot(mine);
+        count = __builtin_popcountll(m);
+        if (tid < WAVE && mine)
+            rows[__builtin_popcountll(m & ((1ull << lane) - 1))] = lane;
+    }
+    __syncthreads();
+    const int d = cb * 128 + 8 * c;
+    const bool q8 = !job.in;
+    f32x4_t acc[RT][8];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            acc[rt][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int m0 = 32 * w; m0 < count; m0 += 32 * WGRAD_WAVES) {
+        u32x4_t R[8];
+        float f[RT][8];
+        const int mine = m0 + 8 * g;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {     // rows behind the last read that one again, times zero
+            const int m = mine + u;
+            const size_t row = static_cast<size_t>(rows[m < count ? m : count - 1]);
+            float unit = 1.0f;
+            if (q8) {
+                u32x2_t v = *reinterpret_cast<const u32x2_t*>(job.q + row * job.D + d);
+                unit = job.qs[row * (job.D / GROUP8) + cb];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    R[u][e] = __builtin_amdgcn_perm(__float_as_uint(byte_to_f32(v[e / 2], (2 * e + 1) & 3)),
+                                                    __float_as_uint(byte_to_f32(v[e / 2], (2 * e) & 3)), 0x07060302u);
+            } else {
+                R[u] = load8(job.in + row * job.D + d, job.D - d);
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const int j = j0 + 16 * rt + c;
+                f[rt][u] = m < count && j < p.r ? job.c[row * p.r + j] * unit : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+            mul_columns(acc[rt], split3(f[rt]), R);
+    }
+#pragma unroll
+    for (int half = WGRAD_WAVES / 2; half > 0; half >>= 1) {
+        if (w >= half && w < 2 * half)
+#pragma unroll
+            for (int v = 0; v < RT * 32; ++v)
+                red[w - half][v][lane] = acc[v / 32][v / 4 % 8][v % 4];
+        __syncthreads();
+        if (w < half)
+#pragma unroll
+            for (int v = 0; v < RT * 32; ++v)
+                acc[v / 32][v / 4 % 8][v % 4] += red[w][v][lane];
+        __syncthreads();
+    }
+    if (w > 0 || d >= job.D)
+        return;
+    const float f = job.scaled && count ? p.scale[a] : 1.0f;
+    const size_t width = slot < 0 ? job.D : static_cast<size_t>(job.cols) * 128;
+    float* out = slot < 0 ? job.out + static_cast<size_t>(a) * p.r * width : job.part + static_cast<size_t>(slot) * p.r * width;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + 16 * rt + 4 * g + i;
+            if (j >= p.r)
+                continue;
+            float* o = out + j * width + d;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f32x4_t v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = slot < 0 ? f * acc[rt][4 * h + e][i] : acc[rt][4 * h + e][i];
+                if (slot >= 0 || d + 8 <= job.D) {
+                    reinterpret_cast<f32x4_a4_t*>(o)[h] = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (d + 4 * h + e < job.D)
+                            o[4 * h + e] = v[e];
+                }
+            }
+        }
+}
+
+// Adapters of several chunks: their partial sums in order.  Adapters without
+// rows: zeros.  (An adapter of one chunk is done.)
+__global__ __launch_bounds__(256) void k_wgrad_sum(const WgradArgs p)
+{
+    const int a = blockIdx.y, j = blockIdx.z;
+    if (p.b.plan[2] != p.b.M || p.b.plan[3] != p.b.L)
+        return;
+    const PlanLayout l(p.b.M, p.b.L);
+    const int n = chunks_of(p.b.plan[l.seg + a + 1] - p.b.plan[l.seg + a]);
+    if (n == 1)
+        return;
+    int d = blockIdx.x * 256 + threadIdx.x;
+    const int first = p.job[0].cols * 128;
+    const bool second = d >= first;
+    const WgradJob job = second ? p.job[1] : p.job[0];
+    d -= second ? first : 0;
+    if (d >= job.D || !job.out)
+        return;
+    const size_t width = static_cast<size_t>(job.cols) * 128;
+    const float* src = job.part + (static_cast<size_t>(p.b.plan[l.slot + a]) * p.r + j) * width + d;
+    float v = 0.0f;
+    for (int i = 0; i < n; ++i)
+        v += src[static_cast<size_t>(i) * p.r * width];
+    job.out[(static_cast<size_t>(a) * p.r + j) * job.D + d] = v * (job.scaled && n ? p.scale[a] : 1.0f);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+int round16(int64_t r) { return static_cast<int>((r + 15) / 16 * 16); }
+
+// Ranges that a shrink's D is split into: enough workgroups for the chip, at
+// least 128 d for each wave, and few enough that the parts stay small beside
+// the rows (the expand kernel reads them all).
+int split_of(int64_t M, int64_t L, int64_t D, int64_t r)
+{
+    const int64_t steps = (D + 127) / 128, most = (steps + SHRINK_WAVES - 1) / SHRINK_WAVES;
+    const int64_t groups = M <= SMALL_M ? 1 : (M + TILE_T - 1) / TILE_T * ((r + 63) / 64);
+    int64_t want = M <= SMALL_M ? 16 : (512 + groups - 1) / groups;
+    const int64_t cap = M <= SMALL_M ? 16 : 8;
+    want = want < cap ? want : cap;
+    (void)L;
+    return static_cast<int>(want < most ? want : most);
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+size_t part_bytes(int64_t M, int64_t L, int64_t D, int64_t r)
+{
+    return up256(static_cast<size_t>(split_of(M, L, D, r)) * M * round16(r) * 4);
+}
+
+size_t plan_bytes(int64_t M, int64_t L) { return up256(static_cast<size_t>(plan_words(M, L)) * 4); }
+
+// partial-sum slots: chunks of adapters with more than one
+int64_t slot_bound(int64_t M) { return M > CHUNK ? 2 * (M / CHUNK) : 0; }
+
+size_t wgrad_bytes(int64_t M, int64_t D, int64_t r)
+{
+    return up256(static_cast<size_t>(slot_bound(M)) * r * ((D + 127) / 128 * 128) * 4);
+}
+
+bool sizes_ok(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L)
+{
+    const int64_t top = static_cast<int64_t>(1) << 31, widest = static_cast<int64_t>(1) << 24;   // grids: 512 columns a workgroup
+    return M >= 0 && M <= MAX_M && N >= 0 && N <= widest && K >= 128 && K % 128 == 0 && K <= widest && r >= 1 &&
+           r <= MAX_RANK && L >= 1 && L <= MAX_ADAPTERS && M * K * 2 < top && M * N * 2 < top &&
+           L * r * K < top / 2 && L * r * N < top / 2;
+}
+
+template <bool Q8>
+void launch_shrink(const ShrinkArgs& s, int64_t tiles, hipStream_t stream)
+{
+    const int rb = s.r <= 16 ? 1 : s.r <= 32 ? 2 : 4;
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(s.SK), static_cast<unsigned>((s.r + 16 * rb - 1) / (16 * rb)));
+#define SHRINK(T_, RB_) hipLaunchKernelGGL((k_shrink<T_, RB_, Q8>), grid, dim3(SHRINK_THREADS), 0, stream, s)
+    if (s.b.M <= SMALL_M) {
+        if (rb == 1) SHRINK(SMALL_T, 1);
+        else if (rb == 2) SHRINK(SMALL_T, 2);
+        else SHRINK(SMALL_T, 4);
+    } else {
+        if (rb == 1) SHRINK(TILE_T, 1);
+        else if (rb == 2) SHRINK(TILE_T, 2);
+        else SHRINK(TILE_T, 4);
+    }
+#undef SHRINK
+}
+
+template <bool SCALED>
+void launch_expand(const ExpandArgs& e, int64_t tiles, hipStream_t stream)
+{
+    const unsigned cols = e.out ? static_cast<unsigned>((e.D + EXPAND_COLS - 1) / EXPAND_COLS) : 1;
+    const dim3 grid(static_cast<unsigned>(tiles), cols);
+#define EXPAND(T_, RK_) hipLaunchKernelGGL((k_expand<T_, RK_, SCALED>), grid, dim3(EXPAND_THREADS), 0, stream, e)
+    if (e.b.M <= SMALL_M) {
+        if (e.r <= 32) EXPAND(SMALL_T, 1);
+        else if (e.r <= 64) EXPAND(SMALL_T, 2);
+        else EXPAND(SMALL_T, 4);
+    } else {
+        if (e.r <= 32) EXPAND(TILE_T, 1);
+        else if (e.r <= 64) EXPAND(TILE_T, 2);
+        else EXPAND(TILE_T, 4);
+    }
+#undef EXPAND
+}
+
+void launch_wgrad(const WgradArgs& a, hipStream_t stream)
+{
+    const int rt = a.r <= 16 ? 1 : a.r <= 32 ? 2 : 4;
+    const int64_t ys = a.chunked ? PlanLayout(a.b.M, a.b.L).CB : a.b.L;
+    const unsigned cols = static_cast<unsigned>(a.job[0].cols + a.job[1].cols);
+    const dim3 grid(cols, static_cast<unsigned>(ys), static_cast<unsigned>((a.r + 16 * rt - 1) / (16 * rt)));
+    if (rt == 1)
+        hipLaunchKernelGGL(k_wgrad<1>, grid, dim3(WGRAD_THREADS), 0, stream, a);
+    else if (rt == 2)
+        hipLaunchKernelGGL(k_wgrad<2>, grid, dim3(WGRAD_THREADS), 0, stream, a);
+    else
+        hipLaunchKernelGGL(k_wgrad<4>, grid, dim3(WGRAD_THREADS), 0, stream, a);
+    if (a.chunked)
+        hipLaunchKernelGGL(k_wgrad_sum, dim3((cols * 128 + 255) / 256, static_cast<unsigned>(a.b.L), static_cast<unsigned>(a.r)),
+                           dim3(256), 0, stream, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t any4_lora_plan_bytes(int64_t M, int64_t L)
+{
+    if (M <= 0 || M > MAX_M || L < 1 || L > MAX_ADAPTERS)
+        return 0;
+    return plan_bytes(M, L);
+}
+
+any4_status any4_lora_plan(const int32_t* ids, void* plan, size_t bytes, int64_t M, int64_t L, hipStream_t stream)
+{
+    if (M < 0 || M > MAX_M || L < 1 || L > MAX_ADAPTERS)
+        return ANY4_E_SHAPE;
+    if (M == 0)
+        return ANY4_OK;
+    if (!ids || !plan)
+        return ANY4_E_NULL;
+    if (!is_aligned(ids, 4) || !is_aligned(plan, 16))
+        return ANY4_E_ALIGN;
+    if (bytes < plan_bytes(M, L))
+        return ANY4_E_WORKSPACE;
+    (void)hipGetLastError();
+    launch_plan(ids, static_cast<int32_t*>(plan), M, L, stream);
+    return launch_status();
+}
+
+size_t any4_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L)
+{
+    if (M <= 0 || !sizes_ok(M, N, K, r, L))
+        return 0;
+    return part_bytes(M, L, K, r) + (M <= SMALL_M ? 0 : plan_bytes(M, L));
+}
+
+any4_status any4_lora(const uint16_t* x, const uint16_t* A, const uint16_t* B, const float* scale, const int32_t* ids,
+                      const void* plan, const uint16_t* y, uint16_t* out, float* h, int8_t* q, float* qs, int64_t M,
+                      int64_t N, int64_t K, int64_t r, int64_t L, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream)
+{
+    if (!sizes_ok(M, N, K, r, L))
+        return ANY4_E_SHAPE;
+    if (M == 0)
+        return ANY4_OK;
+    if (!x || !A || !scale || !ids || (N > 0 && (!B || !y || !out)) || (!q != !qs) || !workspace)
+        return ANY4_E_NULL;
+    if (!is_aligned(x, 16) || !is_aligned(A, 16) || !is_aligned(B, 2) || !is_aligned(y, 2) || !is_aligned(out, 2) ||
+        !is_aligned(scale, 4) || !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(h, 4) ||
+        !is_aligned(q, 16) || !is_aligned(qs, 4) || !is_aligned(workspace, 16))
+        return ANY4_E_ALIGN;
+    if (workspace_bytes < any4_lora_workspace_size(M, N, K, r, L))
+        return ANY4_E_WORKSPACE;
+    (void)hipGetLastError();
+    float* part = static_cast<float*>(workspace);
+    Batch b{ids, nullptr, static_cast<int>(M), static_cast<int>(L)};
+    if (M > SMALL_M) {
+        b.plan = static_cast<const int*>(plan);
+        if (!plan) {
+            int32_t* made = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + part_bytes(M, L, K, r));
+            launch_plan(ids, made, M, L, stream);
+            b.plan = made;
+        }
+    }
+    const int r16 = round16(r), SK = split_of(M, L, K, r);
+    const int64_t tiles = tile_bound(M, L);
+    const ShrinkArgs s{b, x, A, part, reinterpret_cast<uint8_t*>(q), qs, static_cast<int>(K), static_cast<int>(r), r16, SK};
+    if (q)
+        launch_shrink<true>(s, tiles, stream);
+    else
+        launch_shrink<false>(s, tiles, stream);
+    const ExpandArgs e{b, part, B, scale, y, N > 0 ? out : nullptr, h, static_cast<int>(N), static_cast<int>(r), r16, SK};
+    if (e.out || h)
+        launch_expand<false>(e, tiles, stream);
+    return launch_status();
+}
+
+size_t any4_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L)
+{
+    if (M <= 0 || N <= 0 || !sizes_ok(M, N, K, r, L))
+        return 0;
+    return part_bytes(M, L, N, r) + up256(static_cast<size_t>(M) * r * 4) + (M <= SMALL_M ? 0 : plan_bytes(M, L)) +
+           wgrad_bytes(M, K, r) + wgrad_bytes(M, N, r);
+}
+
+any4_status any4_lora_backward(const uint16_t* dy, const uint16_t* x, const int8_t* q, const float* qs, const float* h,
+                               const uint16_t* A, const uint16_t* B, const float* scale, const int32_t* ids,
+                               const void* plan, const uint16_t* dx, uint16_t* dx_out, float* dA, float* dB, int64_t M,
+                               int64_t N, int64_t K, int64_t r, int64_t L, void* workspace, size_t workspace_bytes,
+                               hipStream_t stream)
+{
+    if (!sizes_ok(M, N, K, r, L) || M == 0 || N == 0)
+        return ANY4_E_SHAPE;
+    if (!dy || !A || !B || !scale || !ids || !workspace || (dA && !x && (!q || !qs)) || (dB && !h))
+        return ANY4_E_NULL;
+    if (!is_aligned(dy, 2) || !is_aligned(x, 16) || !is_aligned(q, 16) || !is_aligned(qs, 4) || !is_aligned(h, 4) ||
+        !is_aligned(A, 16) || !is_aligned(B, 2) || !is_aligned(scale, 4) || !is_aligned(ids, 4) ||
+        !is_aligned(plan, 16) || !is_aligned(dx, 16) || !is_aligned(dx_out, 16) || !is_aligned(dA, 4) ||
+        !is_aligned(dB, 4) || !is_aligned(workspace, 16))
+        return ANY4_E_ALIGN;
+    if (workspace_bytes < any4_lora_backward_workspace_size(M, N, K, r, L))
+        return ANY4_E_WORKSPACE;
+    (void)hipGetLastError();
+    char* at = static_cast<char*>(workspace);
+    float* part = reinterpret_cast<float*>(at);
+    at += part_bytes(M, L, N, r);
+    float* dh = reinterpret_cast<float*>(at);
+    at += up256(static_cast<size_t>(M) * r * 4);
+    Batch b{ids, nullptr, static_cast<int>(M), static_cast<int>(L)};
+    if (M > SMALL_M) {
+        b.plan = static_cast<const int*>(plan);
+        if (!plan) {
+            launch_plan(ids, reinterpret_cast<int32_t*>(at), M, L, stream);
+            b.plan = reinterpret_cast<const int*>(at);
+        }
+        at += plan_bytes(M, L);
+    }
+    const int r16 = round16(r), SK = split_of(M, L, N, r);
+    const int64_t tiles = tile_bound(M, L);
+    if (dx_out || dA) {
+        const ShrinkArgs s{b, dy, B, part, nullptr, nullptr, static_cast<int>(N), static_cast<int>(r), r16, SK};
+        launch_shrink<false>(s, tiles, stream);
+        const ExpandArgs e{b, part, A, scale, dx, dx_out, dh, static_cast<int>(K), static_cast<int>(r), r16, SK};
+        launch_expand<true>(e, tiles, stream);
+    }
+    if (dA || dB) {
+        const bool chunked = M > CHUNK;
+        WgradArgs g{b, scale, {}, static_cast<int>(r), chunked};
+        g.job[0] = WgradJob{x, reinterpret_cast<const uint8_t*>(q), qs, dh, dA, reinterpret_cast<float*>(at),
+                            static_cast<int>(K), dA ? static_cast<int>(K / 128) : 0, false};
+        at += wgrad_bytes(M, K, r);
+        g.job[1] = WgradJob{dy, nullptr, nullptr, h, dB, reinterpret_cast<float*>(at), static_cast<int>(N),
+                            dB ? static_cast<int>((N + 127) / 128) : 0, true};
+        launch_wgrad(g, stream);
+    }
+    return launch_status();
+}
+
+any4_status any4_act8_save(const uint16_t* x, int8_t* q, float* qs, int64_t M, int64_t K, hipStream_t stream)
+{
+    if (M < 0 || M > MAX_M || K < 0 || K % GROUP8 != 0 || K >= (static_cast<int64_t>(1) << 31) ||
+        M * K * 2 >= (static_cast<int64_t>(1) << 31))
+        return ANY4_E_SHAPE;
+    if (M == 0 || K == 0)
+        return ANY4_OK;
+    if (!x || !q || !qs)
+        return ANY4_E_NULL;
+    if (!is_aligned(x, 16) || !is_aligned(q, 16) || !is_aligned(qs, 4))
+        return ANY4_E_ALIGN;
+    (void)hipGetLastError();
+    const uint32_t slots = static_cast<uint32_t>(M * K / 8);
+    hipLaunchKernelGGL(k_act8_save, dim3((slots + ACT8_THREADS - 1) / ACT8_THREADS), dim3(ACT8_THREADS), 0, stream, x,
+                       reinterpret_cast<uint8_t*>(q), qs, slots);
+    return launch_status();
+}
+
+any4_status any4_act8_load(const int8_t* q, const float* qs, uint16_t* x, int64_t M, int64_t K, hipStream_t stream)
+{
+    if (M < 0 || M > MAX_M || K < 0 || K % GROUP8 != 0 || K >= (static_cast<int64_t>(1) << 31) ||
+        M * K * 2 >= (static_cast<int64_t>(1) << 31))
+        return ANY4_E_SHAPE;
+    if (M == 0 || K == 0)
+        return ANY4_OK;
+    if (!q || !qs || !x)
+        return ANY4_E_NULL;
+    if (!is_aligned(q, 16) || !is_aligned(qs, 4) || !is_aligned(x, 16))
+        return ANY4_E_ALIGN;
+    (void)hipGetLastError();
+    const uint32_t slots = static_cast<uint32_t>(M * K / 8);
+    hipLaunchKernelGGL(k_act8_load, dim3((slots + ACT8_THREADS - 1) / ACT8_THREADS), dim3(ACT8_THREADS), 0, stream,
+                       reinterpret_cast<const uint8_t*>(q), qs, x, slots);
+    return launch_status();
+}
+
+}  // extern "C"

@@ -1,6 +1,8 @@
 /*
  * any4.h -- C ABI of libany4.so, the MI355X (gfx950) any4 dequantize-GEMM
- * (with plain int4, the any2 and any3 variants and the any4 quantiser).
+ * (with plain int4, the any2 and any3 variants, the any4 quantiser, and what
+ * fine-tunes of such a layer need: low-rank adapters, activations in 8 bits
+ * and the input's gradient).
  *
  * any4 (the 10100.com any4 explainer, section 二) stores each weight of a
  * row as a 4-bit index into that row's 16-entry bf16 lookup table; each
@@ -349,6 +351,149 @@ any4_status any3_gemm(const uint16_t* x, const uint8_t* packed, const uint16_t* 
 any4_status any4_quantize(const float* W, const float* ex, uint8_t* idx, uint16_t* lut,
                           uint16_t* alpha, uint16_t* beta, int64_t N, int64_t K, int64_t g,
                           int iters, int bits, hipStream_t stream);
+
+/*
+ * Low-rank adapters beside a layer, for many requests at once: row m of the
+ * batch uses adapter a = ids[m] (a fine-tune of the frozen layer) on top of
+ * the shared projection, whichever format that has:
+ *     h[m]   = A_a x[m]                          (fp32, r values)
+ *     out[m] = bf16_rne( y[m] + scale[a] * sum_j h[m][j] B_a[j] )
+ *   x      [M][K] bf16            y, out  [M][N] bf16
+ *   A      [L][r][K] bf16, B [L][r][N] bf16 (B rank-major: the transpose of the
+ *          usual [N][r]); adapters of lower rank are padded with zero rows
+ *   scale  [L] fp32               ids     [M] int32
+ * A row whose id is not in 0..L-1 (-1, say) has no adapter: out[m] = y[m] bit
+ * for bit, h[m] = 0.  Products are exact and sums fp32; the fp32 h enters the
+ * second product unrounded, so out carries fp32 summation error and one
+ * rounding.  Results are deterministic and a row's result depends on no other
+ * row's values.  A non-finite weight of an adapter makes the outputs it
+ * reaches non-finite (which kind is not specified).
+ * Sizes of all any4_lora* calls: 0 <= M <= 65535*64, 0 <= N <= 2^24, K <= 2^24 a
+ * positive multiple of 128, 1 <= r <= 128, 1 <= L <= 4096; x, y, A and B below
+ * 2 GiB.
+ * N, r and M need not be multiples of anything.
+ */
+
+/*
+ * any4_lora_plan_bytes, any4_lora_plan -- the rows of a batch sorted by
+ * adapter (stable), with the tables the kernels go by: `bytes` of device
+ * memory at `plan`, 16-byte aligned.  The plan depends on ids alone, so a
+ * program makes it once per batch and hands it to the calls of every layer;
+ * calls without one make their own in the workspace (batches of at most 64
+ * rows need none and ignore it).  any4_lora_plan_bytes gives 0 for sizes out
+ * of range and M = 0.  M = 0 is a no-op.
+ * Errors: ANY4_E_SHAPE, ANY4_E_NULL, ANY4_E_ALIGN, ANY4_E_WORKSPACE (bytes too
+ * small), ANY4_E_HIP.
+ */
+size_t any4_lora_plan_bytes(int64_t M, int64_t L);
+any4_status any4_lora_plan(const int32_t* ids, void* plan, size_t bytes, int64_t M, int64_t L,
+                           hipStream_t stream);
+
+/*
+ * any4_lora -- out and, where asked for, what the backward pass needs.
+ *   plan   device, of these ids, M and L; or NULL.  (A plan of another M or L
+ *          leaves the outputs unwritten.)
+ *   out    device, written; may be y itself, else must not overlap an input.
+ *   h      device, [M][r] fp32, written; or NULL.
+ *   q, qs  device, x in 8 bits as any4_act8_save writes it, in the same pass
+ *          over x (rows without an adapter too); or both NULL.
+ *   workspace  device, 16-byte aligned, any4_lora_workspace_size(M, N, K, r, L)
+ *          bytes (0 for sizes out of range and M = 0), required; contents need
+ *          not be initialised; calls that share one must be ordered.
+ *   M = 0 is a no-op; N = 0 only writes h, q and qs (B, y, out may be NULL).
+ *   x, A, plan, q and workspace need 16-byte alignment, the others that of
+ *   their elements.
+ * Errors: ANY4_E_SHAPE, ANY4_E_NULL, ANY4_E_ALIGN, ANY4_E_WORKSPACE, ANY4_E_HIP.
+ */
+size_t any4_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L);
+any4_status any4_lora(const uint16_t* x, const uint16_t* A, const uint16_t* B, const float* scale,
+                      const int32_t* ids, const void* plan, const uint16_t* y, uint16_t* out,
+                      float* h, int8_t* q, float* qs, int64_t M, int64_t N, int64_t K, int64_t r,
+                      int64_t L, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * any4_lora_backward -- the gradients of any4_lora for dy = d loss / d out
+ * (bf16 [M][N]):
+ *     dh[m]     = scale[a] * B_a dy[m]                       (a = ids[m])
+ *     dx_out[m] = bf16_rne( dx[m] + sum_j dh[m][j] A_a[j] )
+ *     dA_a      = sum_{ids[m] = a} dh[m]^T x[m]              (fp32 [L][r][K])
+ *     dB_a      = scale[a] * sum_{ids[m] = a} h[m]^T dy[m]   (fp32 [L][r][N])
+ * with h as any4_lora wrote it.  The gradient of y is dy itself; dx is what
+ * the shared projection's backward pass gave (any4_gemm_dx), NULL for zero.
+ * dA and dB are written whole: an adapter without rows gets zeros.
+ *   x      device, [M][K] bf16, or NULL with q, qs: x in 8 bits (its values
+ *          q * qs enter dA unrounded).  x goes first where both are given.
+ *   dx_out may be dx itself.  dx_out, dA and dB may each be NULL: not wanted
+ *          (x, q, qs are then not read without dA, h not without dB).
+ *   plan, workspace  as for any4_lora, any4_lora_backward_workspace_size bytes.
+ *   M >= 1, N >= 1.  x, A, q, dx, dx_out, plan and workspace need 16-byte
+ *   alignment, the others that of their elements.
+ * Errors: as any4_lora.
+ */
+size_t any4_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L);
+any4_status any4_lora_backward(const uint16_t* dy, const uint16_t* x, const int8_t* q,
+                               const float* qs, const float* h, const uint16_t* A,
+                               const uint16_t* B, const float* scale, const int32_t* ids,
+                               const void* plan, const uint16_t* dx, uint16_t* dx_out, float* dA,
+                               float* dB, int64_t M, int64_t N, int64_t K, int64_t r, int64_t L,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * any4_act8_save, any4_act8_load -- an activation kept in 8 bits between the
+ * forward and the backward pass, and read back: one fp32 scale per 128
+ * channels of a row,
+ *     amax = max |x|,  qs = fp32(amax / 127),  q = rint( fp32( x * fp32(127 / amax) ) )
+ *     x'   = bf16_rne( fp32( q * qs ) )
+ * (rint: nearest, ties to even).  Bit-exact: there is one correct answer.  A
+ * group whose amax is below 2^-100 is kept as zeros (qs = 0); a group with an
+ * infinity or NaN has a non-finite qs and reads back as non-finite values.
+ *   x  device, [M][K] bf16    q  device, [M][K] int8    qs  device, [M][K/128] fp32
+ *   0 <= M <= 65535*64, K >= 0 a multiple of 128, x below 2 GiB.  M*K == 0 is a
+ *   no-op.  x and q need 16-byte alignment, qs 4.
+ * Errors: ANY4_E_SHAPE, ANY4_E_NULL, ANY4_E_ALIGN, ANY4_E_HIP.
+ */
+any4_status any4_act8_save(const uint16_t* x, int8_t* q, float* qs, int64_t M, int64_t K,
+                           hipStream_t stream);
+any4_status any4_act8_load(const int8_t* q, const float* qs, uint16_t* x, int64_t M, int64_t K,
+                           hipStream_t stream);
+
+/*
+ * any4_gemm_dx, any4_gemm_int4_dx, any2_gemm_dx, any3_gemm_dx -- the gradient
+ * of a quantised layer's input (the layer itself is frozen):
+ *     dx[m][k] = bf16_rne( sum_n dy[m][n] * w[n][k] )
+ * with w the values of any4_dequant (any2_dequant, any3_dequant; plain int4 as
+ * any4_gemm_int4 reads it), exact products and fp32 sums.  Deterministic: the
+ * order of a sum depends only on the shape.
+ *   dy     device, [M][N] bf16    dx  device, [M][K] bf16, written whole
+ *   packed, lut, alpha, beta  as for the format's dequantisation.
+ *   workspace  device, 16-byte aligned, any4_gemm_dx_workspace_size(M, N, K, g)
+ *          bytes (any format; 0 for sizes out of range and empty ones),
+ *          required; contents need not be initialised; calls that share one
+ *          must be ordered.
+ *   0 <= M <= 65535*64, 0 <= N < 2^26, K >= 0 and g as for any4_gemm (K/g is not
+ *   limited).  Every buffer but the workspace below 2 GiB.  M*K == 0 is a
+ *   no-op; N = 0 writes dx = 0 (the other pointers may be NULL).
+ *   dx, packed and workspace need 16-byte alignment, the others 2 (dy with 16
+ *   and N a multiple of 64 is read in place, else through a padded copy).
+ * Errors: ANY4_E_SHAPE, ANY4_E_NULL, ANY4_E_ALIGN, ANY4_E_WORKSPACE, ANY4_E_HIP.
+ */
+size_t any4_gemm_dx_workspace_size(int64_t M, int64_t N, int64_t K, int64_t g);
+any4_status any4_gemm_dx(const uint16_t* dy, const uint8_t* packed, const uint16_t* lut,
+                         const uint16_t* alpha, const uint16_t* beta, uint16_t* dx, int64_t M,
+                         int64_t N, int64_t K, int64_t g, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+any4_status any4_gemm_int4_dx(const uint16_t* dy, const uint8_t* packed, const uint16_t* alpha,
+                              const uint16_t* beta, uint16_t* dx, int64_t M, int64_t N, int64_t K,
+                              int64_t g, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+any4_status any2_gemm_dx(const uint16_t* dy, const uint8_t* packed, const uint16_t* lut,
+                         const uint16_t* alpha, const uint16_t* beta, uint16_t* dx, int64_t M,
+                         int64_t N, int64_t K, int64_t g, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+any4_status any3_gemm_dx(const uint16_t* dy, const uint8_t* packed, const uint16_t* lut,
+                         const uint16_t* alpha, const uint16_t* beta, uint16_t* dx, int64_t M,
+                         int64_t N, int64_t K, int64_t g, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
 
 /*
  * any4_read_probe -- a measurement aid, not part of the method: reads `bytes`
