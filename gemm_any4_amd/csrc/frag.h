@@ -28,12 +28,16 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float f)
 }
 
 // 8 bf16 at p, of which only the first `valid` (any integer) are in the row:
-// the others read as 0 and their memory is not touched.
+// the others read as 0 and their memory is not touched.  WHOLE: the row is a
+// multiple of 8 long, so that all 8 are in it or none.
+template <bool WHOLE = false>
 __device__ __forceinline__ u32x4_t load8(const uint16_t* p, int valid)
 {
-    if (valid >= 8)
-        return *reinterpret_cast<const u32x4_a2_t*>(p);
     u32x4_t v = {0u, 0u, 0u, 0u};
+    if (WHOLE ? valid > 0 : valid >= 8)
+        return *reinterpret_cast<const u32x4_a2_t*>(p);
+    if constexpr (WHOLE)
+        return v;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < valid)
@@ -41,12 +45,15 @@ __device__ __forceinline__ u32x4_t load8(const uint16_t* p, int valid)
     return v;
 }
 
+template <bool WHOLE = false>
 __device__ __forceinline__ void store8(uint16_t* p, u32x4_t v, int valid)
 {
-    if (valid >= 8) {
+    if (WHOLE ? valid > 0 : valid >= 8) {
         *reinterpret_cast<u32x4_a2_t*>(p) = v;
         return;
     }
+    if constexpr (WHOLE)
+        return;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < valid)

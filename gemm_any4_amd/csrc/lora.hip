@@ -29,7 +29,8 @@ constexpr int TILE_T = 64;           // rows of a tile of the plan
 constexpr int CHUNK = 512;           // rows of a chunk of the weight gradient
 constexpr int MAX_RANK = 128;
 constexpr int MAX_ADAPTERS = 4096;
-constexpr int64_t MAX_M = 65535 * 64;
+constexpr int64_t MAX_M = static_cast<int64_t>(1) << 21;   // tiles fit a grid's second dimension
+constexpr int64_t ACT8_MAX_M = 65535 * 64;
 
 // ---------------------------------------------------------------------------
 // the plan: rows sorted by adapter (stable), tiles and chunks of equal adapter
@@ -451,7 +452,7 @@ struct ShrinkArgs {
 constexpr int SHRINK_THREADS = 256;
 constexpr int SHRINK_WAVES = SHRINK_THREADS / WAVE;
 
-template <int T, int RB, bool Q8>
+template <int T, int RB, bool Q8, bool WHOLE>
 __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
 {
     constexpr int MS = T / 16;
@@ -494,14 +495,14 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
         for (int t = 0; t < RB; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                wv[t][i] = load8(wt[t] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g));
+                wv[t][i] = load8<WHOLE>(wt[t] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g));
 #pragma unroll
         for (int s = 0; s < MS; ++s) {
             if (16 * s < tile.count) {
                 u32x4_t v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    v[i] = load8(in[s] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g));
+                    v[i] = load8<WHOLE>(in[s] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g));
                 if constexpr (Q8) {
                     if (blockIdx.z == 0 && 16 * s + c < tile.count) {
                         // the four lanes of a row hold its 128 channels
@@ -597,30 +598,74 @@ __device__ __forceinline__ void mul_columns(f32x4_t (&acc)[8], const Split3& a, 
     mul_column<7>(acc, a, R);
 }
 
-template <int T, int RK, bool SCALED>
+template <int T, int RK, bool SCALED, bool WHOLE>
 __global__ __launch_bounds__(EXPAND_THREADS) void k_expand(const ExpandArgs p)
 {
     constexpr int MS = T / 16, STRIDE = 32 * RK + 4;   // 4: rows of a quarter wave in other banks
+    constexpr int PARTS = 8;                           // parts whose loads go out together
     __shared__ int rows[T];
     __shared__ __attribute__((aligned(16))) float cs[T * STRIDE];
-    const Rows tile = tile_rows<T>(p.b, blockIdx.x, rows);
+    const Rows tile = tile_rows<T>(p.b, blockIdx.y, rows);
     if (tile.a == -2)
         return;
     __syncthreads();
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
-    const int d0 = blockIdx.y * EXPAND_COLS + (tid >> 6) * 128, d = d0 + 8 * c;     // this lane's 8 columns
+    const int d0 = blockIdx.x * EXPAND_COLS + (tid >> 6) * 128, d = d0 + 8 * c;     // this lane's 8 columns
+    const bool first = blockIdx.x == 0;
     if (tile.a < 0) {     // rows without an adapter: the base as it is
-        if (p.c && blockIdx.y == 0)
+        if (p.c && first)
             for (int i = tid; i < tile.count * p.r; i += EXPAND_THREADS)
                 p.c[static_cast<size_t>(rows[i / p.r]) * p.r + i % p.r] = 0.0f;
         if (p.out && p.out != p.base && d < p.D)
             for (int m = g; m < tile.count; m += 4) {
                 const size_t at = static_cast<size_t>(rows[m]) * p.D + d;
-                store8(p.out + at, p.base ? load8(p.base + at, p.D - d) : u32x4_t{0u, 0u, 0u, 0u}, p.D - d);
+                store8<WHOLE>(p.out + at, p.base ? load8<WHOLE>(p.base + at, p.D - d) : u32x4_t{0u, 0u, 0u, 0u}, p.D - d);
             }
         return;
     }
-    u32x4_t W[RK][8];
+    // every load of the workgroup goes out before the first wait: the parts of
+    // c, W and the base rows
+    constexpr int QUADS = 8 * RK, PER = (T * QUADS + EXPAND_THREADS - 1) / EXPAND_THREADS;
+    const float scale = p.scale[tile.a];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        const int i = tid + e * EXPAND_THREADS, m = i / QUADS, j = i % QUADS * 4;
+        if (i < T * QUADS) {
+            f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (m < tile.count && j < p.r16) {
+                const float* src = p.part + static_cast<size_t>(rows[m]) * p.r16 + j;
+                const size_t next = static_cast<size_t>(p.b.M) * p.r16;
+                for (int s0 = 0; s0 < p.SK; s0 += PARTS) {
+                    f32x4_t x[PARTS];
+#pragma unroll
+                    for (int s = 0; s < PARTS; ++s)
+                        x[s] = s0 + s < p.SK ? *reinterpret_cast<const f32x4_t*>(src + (s0 + s) * next)
+                                             : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int s = 0; s < PARTS; ++s)
+                        v += x[s];
+                }
+                if (SCALED)
+                    v *= scale;
+                if (p.c && first)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (j + q < p.r)
+                            p.c[static_cast<size_t>(rows[m]) * p.r + j + q] = v[q];
+            }
+            *reinterpret_cast<f32x4_t*>(&cs[m * STRIDE + j]) = v;
+        }
+    }
+    u32x4_t W[RK][8], y[MS][4];
+#pragma unroll
+    for (int s = 0; s < MS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = 16 * s + 4 * g + i;
+            y[s][i] = u32x4_t{0u, 0u, 0u, 0u};
+            if (p.out && p.base && m < tile.count)
+                y[s][i] = load8<WHOLE>(p.base + static_cast<size_t>(rows[m]) * p.D + d, p.D - d);
+        }
 #pragma unroll
     for (int k = 0; k < RK; ++k)
 #pragma unroll
@@ -628,39 +673,15 @@ __global__ __launch_bounds__(EXPAND_THREADS) void k_expand(const ExpandArgs p)
             const int j = 32 * k + 8 * g + u;
             W[k][u] = u32x4_t{0u, 0u, 0u, 0u};
             if (j < p.r && p.out)
-                W[k][u] = load8(p.w + (static_cast<size_t>(tile.a) * p.r + j) * p.D + d, p.D - d);
+                W[k][u] = load8<WHOLE>(p.w + (static_cast<size_t>(tile.a) * p.r + j) * p.D + d, p.D - d);
         }
-    const float scale = p.scale[tile.a];
-    for (int i = tid; i < T * 32 * RK; i += EXPAND_THREADS) {
-        const int m = i / (32 * RK), j = i % (32 * RK);
-        float v = 0.0f;
-        if (m < tile.count && j < p.r16) {
-            const float* src = p.part + static_cast<size_t>(rows[m]) * p.r16 + j;
-            for (int s = 0; s < p.SK; ++s)
-                v += src[static_cast<size_t>(s) * p.b.M * p.r16];
-            if (SCALED)
-                v *= scale;
-            if (p.c && blockIdx.y == 0 && j < p.r)
-                p.c[static_cast<size_t>(rows[m]) * p.r + j] = v;
-        }
-        cs[m * STRIDE + j] = v;
-    }
     __syncthreads();
     if (!p.out || d0 >= p.D)     // waves leave whole: every lane holds matrix-core operands
         return;
+#pragma unroll
     for (int s = 0; s < MS; ++s) {
         if (16 * s >= tile.count)
             break;
-        u32x4_t y[4];
-        size_t at[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = 16 * s + 4 * g + i;
-            at[i] = static_cast<size_t>(rows[m < tile.count ? m : 0]) * p.D + d;
-            y[i] = u32x4_t{0u, 0u, 0u, 0u};
-            if (p.base && m < tile.count)
-                y[i] = load8(p.base + at[i], p.D - d);
-        }
         f32x4_t acc[8];
 #pragma unroll
         for (int t = 0; t < 8; ++t)
@@ -680,14 +701,15 @@ __global__ __launch_bounds__(EXPAND_THREADS) void k_expand(const ExpandArgs p)
         const float after = SCALED ? 1.0f : scale;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (16 * s + 4 * g + i >= tile.count)
+            const int m = 16 * s + 4 * g + i;
+            if (m >= tile.count)
                 continue;
             u32x4_t o;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                o[e] = f32_to_bf16(fmaf(after, acc[2 * e][i], bf16_to_f32(y[i][e] & 0xffffu))) |
-                       f32_to_bf16(fmaf(after, acc[2 * e + 1][i], bf16_to_f32(y[i][e] >> 16))) << 16;
-            store8(p.out + at[i], o, p.D - d);
+                o[e] = f32_to_bf16(fmaf(after, acc[2 * e][i], bf16_to_f32(y[s][i][e] & 0xffffu))) |
+                       f32_to_bf16(fmaf(after, acc[2 * e + 1][i], bf16_to_f32(y[s][i][e] >> 16))) << 16;
+            store8<WHOLE>(p.out + static_cast<size_t>(rows[m]) * p.D + d, o, p.D - d);
         }
     }
 }
@@ -722,7 +744,7 @@ struct WgradArgs {
 constexpr int WGRAD_THREADS = 512;
 constexpr int WGRAD_WAVES = WGRAD_THREADS / WAVE;
 
-template <int RT>
+template <int RT, bool WHOLE>
 __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
 {
     __shared__ int rows[CHUNK];
@@ -784,7 +806,7 @@ __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
                     R[u][e] = __builtin_amdgcn_perm(__float_as_uint(byte_to_f32(v[e / 2], (2 * e + 1) & 3)),
                                                     __float_as_uint(byte_to_f32(v[e / 2], (2 * e) & 3)), 0x07060302u);
             } else {
-                R[u] = load8(job.in + row * job.D + d, job.D - d);
+                R[u] = load8<WHOLE>(job.in + row * job.D + d, job.D - d);
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
@@ -910,12 +932,12 @@ bool sizes_ok(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L)
            L * r * K < top / 2 && L * r * N < top / 2;
 }
 
-template <bool Q8>
-void launch_shrink(const ShrinkArgs& s, int64_t tiles, hipStream_t stream)
+template <bool Q8, bool WHOLE>
+void launch_shrink_as(const ShrinkArgs& s, int64_t tiles, hipStream_t stream)
 {
     const int rb = s.r <= 16 ? 1 : s.r <= 32 ? 2 : 4;
     const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(s.SK), static_cast<unsigned>((s.r + 16 * rb - 1) / (16 * rb)));
-#define SHRINK(T_, RB_) hipLaunchKernelGGL((k_shrink<T_, RB_, Q8>), grid, dim3(SHRINK_THREADS), 0, stream, s)
+#define SHRINK(T_, RB_) hipLaunchKernelGGL((k_shrink<T_, RB_, Q8, WHOLE>), grid, dim3(SHRINK_THREADS), 0, stream, s)
     if (s.b.M <= SMALL_M) {
         if (rb == 1) SHRINK(SMALL_T, 1);
         else if (rb == 2) SHRINK(SMALL_T, 2);
@@ -928,12 +950,22 @@ void launch_shrink(const ShrinkArgs& s, int64_t tiles, hipStream_t stream)
 #undef SHRINK
 }
 
-template <bool SCALED>
-void launch_expand(const ExpandArgs& e, int64_t tiles, hipStream_t stream)
+void launch_shrink(const ShrinkArgs& s, int64_t tiles, hipStream_t stream)
+{
+    if (s.q)                      // D is a multiple of 128 then
+        launch_shrink_as<true, true>(s, tiles, stream);
+    else if (s.D % 8 == 0)
+        launch_shrink_as<false, true>(s, tiles, stream);
+    else
+        launch_shrink_as<false, false>(s, tiles, stream);
+}
+
+template <bool SCALED, bool WHOLE>
+void launch_expand_as(const ExpandArgs& e, int64_t tiles, hipStream_t stream)
 {
     const unsigned cols = e.out ? static_cast<unsigned>((e.D + EXPAND_COLS - 1) / EXPAND_COLS) : 1;
-    const dim3 grid(static_cast<unsigned>(tiles), cols);
-#define EXPAND(T_, RK_) hipLaunchKernelGGL((k_expand<T_, RK_, SCALED>), grid, dim3(EXPAND_THREADS), 0, stream, e)
+    const dim3 grid(cols, static_cast<unsigned>(tiles));     // neighbours write neighbouring columns
+#define EXPAND(T_, RK_) hipLaunchKernelGGL((k_expand<T_, RK_, SCALED, WHOLE>), grid, dim3(EXPAND_THREADS), 0, stream, e)
     if (e.b.M <= SMALL_M) {
         if (e.r <= 32) EXPAND(SMALL_T, 1);
         else if (e.r <= 64) EXPAND(SMALL_T, 2);
@@ -946,18 +978,28 @@ void launch_expand(const ExpandArgs& e, int64_t tiles, hipStream_t stream)
 #undef EXPAND
 }
 
+void launch_expand(const ExpandArgs& e, int64_t tiles, bool scaled, hipStream_t stream)
+{
+    if (scaled)                   // D is K, a multiple of 128
+        launch_expand_as<true, true>(e, tiles, stream);
+    else if (e.D % 8 == 0)
+        launch_expand_as<false, true>(e, tiles, stream);
+    else
+        launch_expand_as<false, false>(e, tiles, stream);
+}
+
+template <bool WHOLE>
 void launch_wgrad(const WgradArgs& a, hipStream_t stream)
 {
     const int rt = a.r <= 16 ? 1 : a.r <= 32 ? 2 : 4;
     const int64_t ys = a.chunked ? PlanLayout(a.b.M, a.b.L).CB : a.b.L;
     const unsigned cols = static_cast<unsigned>(a.job[0].cols + a.job[1].cols);
     const dim3 grid(cols, static_cast<unsigned>(ys), static_cast<unsigned>((a.r + 16 * rt - 1) / (16 * rt)));
-    if (rt == 1)
-        hipLaunchKernelGGL(k_wgrad<1>, grid, dim3(WGRAD_THREADS), 0, stream, a);
-    else if (rt == 2)
-        hipLaunchKernelGGL(k_wgrad<2>, grid, dim3(WGRAD_THREADS), 0, stream, a);
-    else
-        hipLaunchKernelGGL(k_wgrad<4>, grid, dim3(WGRAD_THREADS), 0, stream, a);
+#define WGRAD(RT_) hipLaunchKernelGGL((k_wgrad<RT_, WHOLE>), grid, dim3(WGRAD_THREADS), 0, stream, a)
+    if (rt == 1) WGRAD(1);
+    else if (rt == 2) WGRAD(2);
+    else WGRAD(4);
+#undef WGRAD
     if (a.chunked)
         hipLaunchKernelGGL(k_wgrad_sum, dim3((cols * 128 + 255) / 256, static_cast<unsigned>(a.b.L), static_cast<unsigned>(a.r)),
                            dim3(256), 0, stream, a);
@@ -1029,13 +1071,10 @@ any4_status any4_lora(const uint16_t* x, const uint16_t* A, const uint16_t* B, c
     const int r16 = round16(r), SK = split_of(M, L, K, r);
     const int64_t tiles = tile_bound(M, L);
     const ShrinkArgs s{b, x, A, part, reinterpret_cast<uint8_t*>(q), qs, static_cast<int>(K), static_cast<int>(r), r16, SK};
-    if (q)
-        launch_shrink<true>(s, tiles, stream);
-    else
-        launch_shrink<false>(s, tiles, stream);
+    launch_shrink(s, tiles, stream);
     const ExpandArgs e{b, part, B, scale, y, N > 0 ? out : nullptr, h, static_cast<int>(N), static_cast<int>(r), r16, SK};
     if (e.out || h)
-        launch_expand<false>(e, tiles, stream);
+        launch_expand(e, tiles, false, stream);
     return launch_status();
 }
 
@@ -1083,9 +1122,9 @@ any4_status any4_lora_backward(const uint16_t* dy, const uint16_t* x, const int8
     const int64_t tiles = tile_bound(M, L);
     if (dx_out || dA) {
         const ShrinkArgs s{b, dy, B, part, nullptr, nullptr, static_cast<int>(N), static_cast<int>(r), r16, SK};
-        launch_shrink<false>(s, tiles, stream);
+        launch_shrink(s, tiles, stream);
         const ExpandArgs e{b, part, A, scale, dx, dx_out, dh, static_cast<int>(K), static_cast<int>(r), r16, SK};
-        launch_expand<true>(e, tiles, stream);
+        launch_expand(e, tiles, true, stream);
     }
     if (dA || dB) {
         const bool chunked = M > CHUNK;
@@ -1095,14 +1134,17 @@ any4_status any4_lora_backward(const uint16_t* dy, const uint16_t* x, const int8
         at += wgrad_bytes(M, K, r);
         g.job[1] = WgradJob{dy, nullptr, nullptr, h, dB, reinterpret_cast<float*>(at), static_cast<int>(N),
                             dB ? static_cast<int>((N + 127) / 128) : 0, true};
-        launch_wgrad(g, stream);
+        if (N % 8 == 0)
+            launch_wgrad<true>(g, stream);
+        else
+            launch_wgrad<false>(g, stream);
     }
     return launch_status();
 }
 
 any4_status any4_act8_save(const uint16_t* x, int8_t* q, float* qs, int64_t M, int64_t K, hipStream_t stream)
 {
-    if (M < 0 || M > MAX_M || K < 0 || K % GROUP8 != 0 || K >= (static_cast<int64_t>(1) << 31) ||
+    if (M < 0 || M > ACT8_MAX_M || K < 0 || K % GROUP8 != 0 || K >= (static_cast<int64_t>(1) << 31) ||
         M * K * 2 >= (static_cast<int64_t>(1) << 31))
         return ANY4_E_SHAPE;
     if (M == 0 || K == 0)
@@ -1120,7 +1162,7 @@ any4_status any4_act8_save(const uint16_t* x, int8_t* q, float* qs, int64_t M, i
 
 any4_status any4_act8_load(const int8_t* q, const float* qs, uint16_t* x, int64_t M, int64_t K, hipStream_t stream)
 {
-    if (M < 0 || M > MAX_M || K < 0 || K % GROUP8 != 0 || K >= (static_cast<int64_t>(1) << 31) ||
+    if (M < 0 || M > ACT8_MAX_M || K < 0 || K % GROUP8 != 0 || K >= (static_cast<int64_t>(1) << 31) ||
         M * K * 2 >= (static_cast<int64_t>(1) << 31))
         return ANY4_E_SHAPE;
     if (M == 0 || K == 0)
