@@ -28,16 +28,12 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float f)
 }
 
 // 8 bf16 at p, of which only the first `valid` (any integer) are in the row:
-// the others read as 0 and their memory is not touched.  WHOLE: the row is a
-// multiple of 8 long, so that all 8 are in it or none.
-template <bool WHOLE = false>
+// the others read as 0 and their memory is not touched.
 __device__ __forceinline__ u32x4_t load8(const uint16_t* p, int valid)
 {
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if (WHOLE ? valid > 0 : valid >= 8)
+    if (valid >= 8)
         return *reinterpret_cast<const u32x4_a2_t*>(p);
-    if constexpr (WHOLE)
-        return v;
+    u32x4_t v = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < valid)
@@ -45,20 +41,99 @@ __device__ __forceinline__ u32x4_t load8(const uint16_t* p, int valid)
     return v;
 }
 
-template <bool WHOLE = false>
 __device__ __forceinline__ void store8(uint16_t* p, u32x4_t v, int valid)
 {
-    if (WHOLE ? valid > 0 : valid >= 8) {
+    if (valid >= 8) {
         *reinterpret_cast<u32x4_a2_t*>(p) = v;
         return;
     }
-    if constexpr (WHOLE)
-        return;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < valid)
             p[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
 }
+
+// A bf16 matrix below 2 GiB, read and written 8 elements at a time at 32-bit
+// element offsets through bounds-checked buffer accesses (an offset past the
+// end reads 0 and writes nothing), without branches between the loads: what a
+// lane does not need, it asks for past the end.
+//   WHOLE   16-byte aligned with rows a multiple of 8 long: all 8 elements are in
+//           a row or none.
+//   else    a lane may stand at an odd element; fetch() reads the aligned dwords
+//           that hold its elements, and finish() shifts them into place once
+//           they are there.  A wave that reaches a row's end (edge, uniform)
+//           reads only the dwords with elements of the row, one by one, and
+//           clears the rest.  (Single elements under branches made such a
+//           wave wait for each: 2048 x 4099, rank 64, 38 us for the expand
+//           kernel against 17 us at 4096 columns.)
+constexpr uint32_t OOR = 0x80000000u;
+
+template <bool WHOLE>
+struct Matrix {
+    struct Piece {
+        u32x4_t v;
+        uint32_t last;      // not WHOLE: the fifth dword
+    };
+    uint16_t* p;
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t skew;          // bytes from the first dword's start to the first element
+
+    __device__ __forceinline__ Matrix(const uint16_t* base, size_t elements) : p(const_cast<uint16_t*>(base))
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(base);
+        skew = WHOLE ? 0u : static_cast<uint32_t>(at) & 2u;
+        const size_t bytes = !base ? 0 : WHOLE ? elements * 2 : (skew + elements * 2 + 3) & ~static_cast<size_t>(3);
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at - skew), static_cast<short>(0),
+                                                 static_cast<int>(bytes), 0x00020000);
+    }
+    // the first `valid` (any integer) of the 8 elements from `at` on; zeros behind
+    __device__ __forceinline__ Piece fetch(uint32_t at, int valid, bool edge) const
+    {
+        Piece o;
+        o.last = 0u;
+        if constexpr (WHOLE) {
+            o.v = __builtin_amdgcn_raw_buffer_load_b128(rsrc, valid > 0 ? at * 2 : OOR, 0, 0);
+        } else {
+            const uint32_t from = at * 2 + skew, odd = from & 2u, low = from - odd;
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o.v[i] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, 2 * i - static_cast<int>(odd >> 1) < valid && valid > 0 ? low + 4 * i : OOR, 0, 0);
+            } else {
+                o.v = __builtin_amdgcn_raw_buffer_load_b128(rsrc, valid > 0 ? low : OOR, 0, 0);
+            }
+            o.last = __builtin_amdgcn_raw_buffer_load_b32(rsrc, odd && valid >= 8 ? low + 16 : OOR, 0, 0);
+        }
+        return o;
+    }
+    __device__ __forceinline__ u32x4_t finish(const Piece& x, uint32_t at, int valid, bool edge) const
+    {
+        if constexpr (WHOLE) {
+            return x.v;
+        } else {
+            const uint32_t by = ((at * 2 + skew) & 2u) * 8;
+            u32x4_t o = {__builtin_amdgcn_alignbit(x.v[1], x.v[0], by), __builtin_amdgcn_alignbit(x.v[2], x.v[1], by),
+                         __builtin_amdgcn_alignbit(x.v[3], x.v[2], by), __builtin_amdgcn_alignbit(x.last, x.v[3], by)};
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[i] &= valid >= 2 * i + 2 ? 0xffffffffu : valid == 2 * i + 1 ? 0xffffu : 0u;
+            }
+            return o;
+        }
+    }
+    __device__ __forceinline__ void store(uint32_t at, u32x4_t v, int valid, bool edge) const
+    {
+        if constexpr (WHOLE) {
+            __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, valid > 0 ? at * 2 : OOR, 0, 0);
+        } else {
+            if (edge)
+                store8(p + at, v, valid);
+            else if (valid > 0)
+                *reinterpret_cast<u32x4_a2_t*>(p + at) = v;
+        }
+    }
+};
 
 // Column t of the 8 x 8 block whose row u is R[u] (8 bf16): the 8 values a
 // lane gives the matrix cores along the summed dimension.

@@ -19,32 +19,36 @@
 // its tile from the ids alone (ballots); beyond that the plan (rows sorted by
 // adapter, tables of tiles and chunks) is made by k_plan* once, in the
 // workspace or, for callers that keep it, in a buffer of theirs.
+#include <type_traits>
+
 #include "frag.h"
 
 namespace {
 
 constexpr int SMALL_M = 64;          // up to here tiles come from ballots over the ids
 constexpr int SMALL_T = 16;          // rows of a tile there
-constexpr int TILE_T = 64;           // rows of a tile of the plan
+constexpr int TILE_T = 32;           // rows of a tile of the plan
 constexpr int CHUNK = 512;           // rows of a chunk of the weight gradient
 constexpr int MAX_RANK = 128;
 constexpr int MAX_ADAPTERS = 4096;
-constexpr int64_t MAX_M = static_cast<int64_t>(1) << 21;   // tiles fit a grid's second dimension
+constexpr int64_t MAX_M = static_cast<int64_t>(1) << 20;   // tiles fit a grid's second dimension
 constexpr int64_t ACT8_MAX_M = 65535 * 64;
 
 // ---------------------------------------------------------------------------
 // the plan: rows sorted by adapter (stable), tiles and chunks of equal adapter
 // ---------------------------------------------------------------------------
 // int32 words: [0] tiles, [1] chunks, [2] M, [3] L, then
-//   seg   [L+2]  first sorted position of each adapter, of the rows without
-//                one (entry L), and M
-//   slot  [L+1]  first partial-sum slot of each adapter (adapters of one chunk
-//                or none have no slot)
-//   tile  [TB][3]  adapter (-1: none), first sorted position, rows
-//   chunk [CB][4]  the same and the chunk's slot (-1: the only one)
-//   perm  [M]    row at each sorted position
+//   first [L+1]  first tile of each adapter (entry L: of the rows without one)
+//   count [L+1]  its rows
+//   slot  [L+1]  its first partial-sum slot (adapters of one chunk or none have
+//                no slot)
+//   chunk [CB][4]  adapter, first place, rows, slot (-1: the only chunk)
+//   tile  [TB][2]  adapter (-1: none), rows
+//   rows  [TB][TILE_T]  the rows of each tile; places behind the last repeat it
+// A place is TILE_T * tile + position: the rows of one adapter stand together, and
+// a kernel that knows its tile's number knows where they are.
 struct PlanLayout {
-    int64_t seg, slot, tile, chunk, perm, words;
+    int64_t first, count, slot, chunk, tile, rows, words;
     int64_t TB, CB;
 
     __host__ __device__ PlanLayout(int64_t M, int64_t L)
@@ -52,12 +56,13 @@ struct PlanLayout {
         const int64_t segs = M < L + 1 ? M : L + 1;
         TB = M / TILE_T + segs;
         CB = M / CHUNK + segs;
-        seg = 4;
-        slot = seg + L + 2;
-        tile = slot + L + 1;
-        chunk = tile + 3 * TB;
-        perm = chunk + 4 * CB;
-        words = perm + M;
+        first = 4;
+        count = first + L + 1;
+        slot = count + L + 1;
+        chunk = (slot + L + 1 + 3) / 4 * 4;
+        tile = chunk + 4 * CB;
+        rows = tile + (2 * TB + 3) / 4 * 4;
+        words = rows + TILE_T * TB;
     }
 };
 
@@ -69,43 +74,35 @@ constexpr int PLAN_PARTS = 256;      // beyond: waves of their own, with counts 
 
 __device__ __forceinline__ int adapter_of(int id, int L) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(L) ? id : L; }
 
-// Lanes of the wave that hold the same value, by the values in turn.
-__device__ __forceinline__ uint64_t same_lanes(int v, bool live)
+// This lane's place among the rows of its adapter that the wave has counted so
+// far in n[]; the wave's rows in order.  Lanes of equal adapter find each other
+// by ballots, and the first of them adds them all.
+__device__ __forceinline__ int count_rows(int a, bool live, int* n)
 {
+    const int lane = threadIdx.x & 63;
     uint64_t left = __ballot(live), mine = 0;
     while (left) {
-        const int a = __builtin_amdgcn_readlane(v, __builtin_ctzll(left));
-        const uint64_t m = __ballot(live && v == a);
-        if (v == a)
+        const int v = __builtin_amdgcn_readlane(a, __builtin_ctzll(left));
+        const uint64_t m = __ballot(live && a == v);
+        if (a == v)
             mine = m;
         left &= ~m;
     }
-    return mine;
+    const int lead = mine ? __builtin_ctzll(mine) : lane;
+    int at = 0;
+    if (live && lane == lead)
+        at = atomicAdd(&n[a], __builtin_popcountll(mine));
+    return __shfl(at, lead) + __builtin_popcountll(mine & ((1ull << lane) - 1));
 }
 
-__device__ __forceinline__ void count_rows(const int* ids, int m0, int m1, int L, int* cnt)
+// Row m is number `at` of the n rows of an adapter whose first place is given;
+// the last one also fills the tile's empty places.
+__device__ __forceinline__ void place_row(int m, int at, int n, int64_t first, int* rows)
 {
-    for (int m = m0 + (threadIdx.x & 63); m < m1; m += WAVE)
-        atomicAdd(&cnt[adapter_of(ids[m], L)], 1);
-}
-
-// Places the rows [m0, m1) at the positions that `next` counts up, in row order.
-__device__ __forceinline__ void place_rows(const int* ids, int m0, int m1, int L, int* next, int* perm)
-{
-    const int lane = threadIdx.x & 63;
-    for (int b = m0; b < m1; b += WAVE) {
-        const int m = b + lane;
-        const bool live = m < m1;
-        const int a = live ? adapter_of(ids[m], L) : -1;
-        const uint64_t mask = same_lanes(a, live);
-        const int lead = mask ? __builtin_ctzll(mask) : lane;
-        int at = 0;
-        if (live && lane == lead)
-            at = atomicAdd(&next[a], __builtin_popcountll(mask));
-        at = __shfl(at, lead);
-        if (live)
-            perm[at + __builtin_popcountll(mask & ((1ull << lane) - 1))] = m;
-    }
+    rows[first + at] = m;
+    if (at == n - 1)
+        for (int i = n; i % TILE_T; ++i)
+            rows[first + i] = m;
 }
 
 struct Four {
@@ -117,31 +114,37 @@ __device__ __forceinline__ Four block_scan(Four x, int (*wave_sum)[4])
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     Four s = x;
+    for (int d = 1; d < WAVE; d <<= 1) {
+        int o[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        for (int d = 1; d < WAVE; d <<= 1) {
-            const int o = __shfl_up(s.v[q], d);
-            s.v[q] += lane >= d ? o : 0;
-        }
+        for (int q = 0; q < 4; ++q)
+            o[q] = __shfl_up(s.v[q], d);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            s.v[q] += lane >= d ? o[q] : 0;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
         if (lane == 63)
             wave_sum[w][q] = s.v[q];
-    }
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         int before = 0;
-        for (int i = 0; i < w; ++i)
-            before += wave_sum[i][q];
+        for (int i = 0; i < PLAN_WAVES; ++i)
+            before += i < w ? wave_sum[i][q] : 0;
         s.v[q] += before - x.v[q];
     }
     return s;
 }
 
+__device__ __forceinline__ int tiles_of(int rows) { return (rows + TILE_T - 1) / TILE_T; }
 __device__ __forceinline__ int chunks_of(int rows) { return (rows + CHUNK - 1) / CHUNK; }
 
 // From cnt[part][L+1] (rows of each adapter in each part of the batch): the
-// plan's tables, and cnt turned into the first position of each.
-__device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, int* plan, int* s_seg,
+// plan's tables, s_rows and s_tile (rows and first tile of each adapter), and
+// cnt turned into the number of the adapter's rows in earlier parts.
+__device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, int* plan, int* s_rows,
                                             int* s_tile, int* s_chunk, int (*wave_sum)[4])
 {
     const PlanLayout p(M, L);
@@ -158,36 +161,30 @@ __device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, i
             n += c;
         }
         const int ch = a < L ? chunks_of(n) : 0;
-        s_seg[a] = n;
-        sum.v[0] += n;
-        sum.v[1] += (n + TILE_T - 1) / TILE_T;
-        sum.v[2] += ch;
-        sum.v[3] += ch > 1 ? ch : 0;
+        s_rows[a] = n;
+        sum.v[0] += tiles_of(n);
+        sum.v[1] += ch;
+        sum.v[2] += ch > 1 ? ch : 0;
     }
     Four at = block_scan(sum, wave_sum);
     for (int e = 0; e < per; ++e) {
         const int a = tid * per + e;
         if (a > L)
             break;
-        const int n = s_seg[a], ch = a < L ? chunks_of(n) : 0;
-        for (int q = 0; q < parts; ++q)
-            cnt[static_cast<size_t>(q) * (L + 1) + a] += at.v[0];
-        s_seg[a] = at.v[0];
-        s_tile[a] = at.v[1];
-        s_chunk[a] = at.v[2];
-        plan[p.seg + a] = at.v[0];
-        plan[p.slot + a] = at.v[3];
-        at.v[0] += n;
-        at.v[1] += (n + TILE_T - 1) / TILE_T;
-        at.v[2] += ch;
-        at.v[3] += ch > 1 ? ch : 0;
+        const int n = s_rows[a], ch = a < L ? chunks_of(n) : 0;
+        s_tile[a] = at.v[0];
+        s_chunk[a] = at.v[1];
+        plan[p.first + a] = at.v[0];
+        plan[p.count + a] = n;
+        plan[p.slot + a] = at.v[2];
+        at.v[0] += tiles_of(n);
+        at.v[1] += ch;
+        at.v[2] += ch > 1 ? ch : 0;
         if (a == L) {
-            s_seg[L + 1] = M;
-            s_tile[L + 1] = at.v[1];
-            s_chunk[L + 1] = at.v[2];
-            plan[p.seg + L + 1] = M;
-            plan[0] = at.v[1];
-            plan[1] = at.v[2];
+            s_tile[L + 1] = at.v[0];
+            s_chunk[L + 1] = at.v[1];
+            plan[0] = at.v[0];
+            plan[1] = at.v[1];
             plan[2] = M;
             plan[3] = L;
         }
@@ -205,17 +202,15 @@ __device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, i
                 else
                     hi = mid;
             }
-            const int first = s_seg[lo] + (t - start[lo]) * size;
-            const int left = s_seg[lo + 1] - first, rows = left < size ? left : size;
+            const int before = (t - start[lo]) * size, left = s_rows[lo] - before, rows = left < size ? left : size;
             if (kind == 0) {
-                int* o = plan + p.tile + 3 * static_cast<int64_t>(t);
+                int* o = plan + p.tile + 2 * static_cast<int64_t>(t);
                 o[0] = lo < L ? lo : -1;
-                o[1] = first;
-                o[2] = rows;
+                o[1] = rows;
             } else {
                 int* o = plan + p.chunk + 4 * static_cast<int64_t>(t);
                 o[0] = lo;
-                o[1] = first;
+                o[1] = s_tile[lo] * TILE_T + before;
                 o[2] = rows;
                 o[3] = start[lo + 1] - start[lo] > 1 ? plan[p.slot + lo] + t - start[lo] : -1;
             }
@@ -223,21 +218,34 @@ __device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, i
     }
 }
 
+// STEPS x 64 rows a wave, their ids in registers from the first load on.
+template <int STEPS>
 __global__ __launch_bounds__(PLAN_THREADS) void k_plan(const int* __restrict__ ids, int* plan, int M, int L)
 {
     __shared__ int cnt[PLAN_WAVES * (PLAN_ONE_L + 1)];
-    __shared__ int s_seg[PLAN_ONE_L + 2], s_tile[PLAN_ONE_L + 2], s_chunk[PLAN_ONE_L + 2];
+    __shared__ int s_rows[PLAN_ONE_L + 2], s_tile[PLAN_ONE_L + 2], s_chunk[PLAN_ONE_L + 2];
     __shared__ int wave_sum[PLAN_WAVES][4];
+    const int w = threadIdx.x >> 6, m0 = w * (STEPS * WAVE) + (threadIdx.x & 63);
+    int a[STEPS], at[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+        a[i] = m0 + i * WAVE < M ? ids[m0 + i * WAVE] : -1;
     for (int i = threadIdx.x; i < PLAN_WAVES * (L + 1); i += PLAN_THREADS)
         cnt[i] = 0;
     __syncthreads();
-    const int w = threadIdx.x >> 6, per = (M + PLAN_WAVES * WAVE - 1) / (PLAN_WAVES * WAVE) * WAVE;
-    const int m0 = w * per < M ? w * per : M, m1 = m0 + per < M ? m0 + per : M;
-    count_rows(ids, m0, m1, L, cnt + w * (L + 1));
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        a[i] = adapter_of(a[i], L);
+        at[i] = count_rows(a[i], m0 + i * WAVE < M, cnt + w * (L + 1));
+    }
     __syncthreads();
-    plan_tables(cnt, PLAN_WAVES, M, L, plan, s_seg, s_tile, s_chunk, wave_sum);
-    __syncthreads();
-    place_rows(ids, m0, m1, L, cnt + w * (L + 1), plan + PlanLayout(M, L).perm);
+    plan_tables(cnt, PLAN_WAVES, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
+    int* rows = plan + PlanLayout(M, L).rows;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+        if (m0 + i * WAVE < M)
+            place_row(m0 + i * WAVE, cnt[w * (L + 1) + a[i]] + at[i], s_rows[a[i]],
+                      static_cast<int64_t>(s_tile[a[i]]) * TILE_T, rows);
 }
 
 // Larger batches or many adapters: the same in three launches, one wave for
@@ -249,24 +257,30 @@ __global__ __launch_bounds__(WAVE) void k_plan_count(const int* __restrict__ ids
         mine[i] = 0;
     __threadfence();     // the zeros are in place before the atomics below
     __syncthreads();
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * per;
-    if (m0 < M)
-        count_rows(ids, static_cast<int>(m0), static_cast<int>(m0 + per < M ? m0 + per : M), L, mine);
+    const int m0 = blockIdx.x * per, m1 = m0 + per < M ? m0 + per : M;     // per * PLAN_PARTS < 2^22
+    for (int m = m0 + threadIdx.x; m < m1; m += WAVE)
+        atomicAdd(&mine[adapter_of(ids[m], L)], 1);
 }
 
 __global__ __launch_bounds__(PLAN_THREADS) void k_plan_tables(int* cnt, int* plan, int M, int L)
 {
-    __shared__ int s_seg[MAX_ADAPTERS + 2], s_tile[MAX_ADAPTERS + 2], s_chunk[MAX_ADAPTERS + 2];
+    __shared__ int s_rows[MAX_ADAPTERS + 2], s_tile[MAX_ADAPTERS + 2], s_chunk[MAX_ADAPTERS + 2];
     __shared__ int wave_sum[PLAN_WAVES][4];
-    plan_tables(cnt, PLAN_PARTS, M, L, plan, s_seg, s_tile, s_chunk, wave_sum);
+    plan_tables(cnt, PLAN_PARTS, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
 }
 
 __global__ __launch_bounds__(WAVE) void k_plan_place(const int* __restrict__ ids, int* cnt, int* plan, int M, int L, int per)
 {
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * per;
-    if (m0 < M)
-        place_rows(ids, static_cast<int>(m0), static_cast<int>(m0 + per < M ? m0 + per : M), L,
-                   cnt + static_cast<size_t>(blockIdx.x) * (L + 1), plan + PlanLayout(M, L).perm);
+    const PlanLayout p(M, L);
+    const int m0 = blockIdx.x * per, m1 = m0 + per < M ? m0 + per : M;
+    for (int b = m0; b < m1; b += WAVE) {
+        const int m = b + threadIdx.x;
+        const bool live = m < m1;
+        const int a = live ? adapter_of(ids[m], L) : -1;
+        const int at = count_rows(a, live, cnt + static_cast<size_t>(blockIdx.x) * (L + 1));
+        if (live)
+            place_row(m, at, plan[p.count + a], static_cast<int64_t>(plan[p.first + a]) * TILE_T, plan + p.rows);
+    }
 }
 
 bool plan_in_one(int64_t M, int64_t L) { return M <= PLAN_ONE_M && L <= PLAN_ONE_L; }
@@ -281,7 +295,10 @@ void launch_plan(const int32_t* ids, int32_t* plan, int64_t M, int64_t L, hipStr
 {
     const int m = static_cast<int>(M), l = static_cast<int>(L);
     if (plan_in_one(M, L)) {
-        hipLaunchKernelGGL(k_plan, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
+        if (M <= PLAN_ONE_M / 4)
+            hipLaunchKernelGGL(k_plan<PLAN_ONE_M / 4 / PLAN_THREADS>, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
+        else
+            hipLaunchKernelGGL(k_plan<PLAN_ONE_M / PLAN_THREADS>, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
         return;
     }
     int* cnt = plan + PlanLayout(M, L).words;
@@ -294,24 +311,25 @@ void launch_plan(const int32_t* ids, int32_t* plan, int64_t M, int64_t L, hipStr
 // ---------------------------------------------------------------------------
 // the rows of a tile
 // ---------------------------------------------------------------------------
-struct Rows {
-    int a;        // adapter, -1: rows without one, -2: no such tile
-    int count;
-};
-
 struct Batch {
     const int* ids;     // [M]
     const int* plan;    // null for M <= SMALL_M
     int M, L;
 };
 
-// Puts the rows of tile t into rows[] (wave 0 writes; the caller synchronises).
+struct Tile {
+    int a;              // adapter, -1: rows without one, -2: no such tile
+    int count;
+    const int* rows;    // its T rows; places behind the last repeat it
+};
+
+// Every wave finds tile t for itself.  own: SMALL_T ints of LDS of this wave
+// (the small form keeps the rows there).
 template <int T>
-__device__ __forceinline__ Rows tile_rows(const Batch& b, int t, int* rows)
+__device__ __forceinline__ Tile find_tile(const Batch& b, int t, int* own)
 {
-    const int tid = threadIdx.x;
     if constexpr (T == SMALL_T) {
-        const int lane = tid & 63;
+        const int lane = threadIdx.x & 63;
         const bool live = lane < b.M;
         const int id = live ? adapter_of(b.ids[lane], b.L) : -1;
         uint64_t left = __ballot(live);
@@ -320,24 +338,27 @@ __device__ __forceinline__ Rows tile_rows(const Batch& b, int t, int* rows)
             const uint64_t m = __ballot(live && id == a);
             const int n = __builtin_popcountll(m), tiles = (n + T - 1) / T;
             if (t < tiles) {
-                const int rank = __builtin_popcountll(m & ((1ull << lane) - 1)) - t * T;
-                if (tid < WAVE && (m >> lane & 1) && rank >= 0 && rank < T)
-                    rows[rank] = lane;
-                return {a < b.L ? a : -1, n - t * T < T ? n - t * T : T};
+                const int count = n - t * T < T ? n - t * T : T;
+                const int at = __builtin_popcountll(m & ((1ull << lane) - 1)) - t * T;
+                if ((m >> lane & 1) && at >= 0 && at < T) {
+                    own[at] = lane;
+                    if (at == count - 1)
+                        for (int i = count; i < T; ++i)
+                            own[i] = lane;
+                }
+                return {a < b.L ? a : -1, count, own};
             }
             t -= tiles;
             left &= ~m;
         }
-        return {-2, 0};
+        return {-2, 0, own};
     } else {
-        if (t >= b.plan[0] || b.plan[2] != b.M || b.plan[3] != b.L)
-            return {-2, 0};
         const PlanLayout p(b.M, b.L);
-        const int* e = b.plan + p.tile + 3 * static_cast<int64_t>(t);
-        const int first = e[1], n = e[2];
-        if (tid < n)
-            rows[tid] = b.plan[p.perm + first + tid];
-        return {e[0], n};
+        const int* e = b.plan + p.tile + 2 * static_cast<int64_t>(t);     // in the plan's bounds for every t of the grid
+        const int a = e[0], count = e[1];
+        if (t >= b.plan[0] || b.plan[2] != b.M || b.plan[3] != b.L)
+            return {-2, 0, nullptr};
+        return {a, count, b.plan + p.rows + TILE_T * static_cast<int64_t>(t)};
     }
 }
 
@@ -380,13 +401,21 @@ __device__ __forceinline__ Scale8 scale8(uint32_t top)
 
 __device__ __forceinline__ u32x2_t quantise8(u32x4_t v, float inv)
 {
-    u32x2_t q = {0u, 0u};
+    // the product is rounded to fp32 first (no fma), then adding 1.5 * 2^23 rounds
+    // it to a whole number, ties to even, and leaves that in the low byte (0 for
+    // a NaN: its group's scale is NaN or inf)
+#pragma clang fp contract(off)
+    uint32_t k[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float f = __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
-        const int k = __float2int_rn(f * inv);      // a NaN gives 0: its group's scale is NaN or inf
-        q[i / 4] |= static_cast<uint32_t>(k & 0xff) << (8 * (i & 3));
+        const float f = __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16) * inv;
+        k[i] = __float_as_uint(f + 0x1.8p23f);
     }
+    u32x2_t q;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        q[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(k[4 * i + 3], k[4 * i + 2], 0x0c0c0400u),
+                                     __builtin_amdgcn_perm(k[4 * i + 1], k[4 * i], 0x0c0c0400u), 0x05040100u);
     return q;
 }
 
@@ -436,51 +465,47 @@ __global__ __launch_bounds__(ACT8_THREADS) void k_act8_load(const uint8_t* __res
 // shrink: part[sk][m][j] = sum over this split's d of in[m][d] W_a[j][d]
 // ---------------------------------------------------------------------------
 // A workgroup takes a tile of rows, 16*RB ranks and one of SK ranges of d,
-// which its four waves share out again in steps of 128; the matrix cores sum
-// 16 rows x 16 ranks x 32 d at a time.  The four waves' sums meet in LDS, the
+// which its eight waves share out again in steps of 128; the matrix cores sum
+// 16 rows x 16 ranks x 32 d at a time.  The eight waves' sums meet in LDS, the
 // splits' in the expand kernel, both in a fixed order.
 struct ShrinkArgs {
     Batch b;
     const uint16_t* in;    // [M][D]
     const uint16_t* w;     // [L][r][D]
-    float* part;           // [SK][M][r16]
+    float* part;           // [SK][tiles * T][r16]: by place, not by row
     uint8_t* q;            // [M][D] int8 and its scales, or null (D % 128 == 0)
     float* qs;
     int D, r, r16, SK;
 };
 
-constexpr int SHRINK_THREADS = 256;
+constexpr int SHRINK_THREADS = 512;
 constexpr int SHRINK_WAVES = SHRINK_THREADS / WAVE;
 
 template <int T, int RB, bool Q8, bool WHOLE>
 __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
 {
     constexpr int MS = T / 16;
-    __shared__ int rows[T];
-    __shared__ f32x4_t red[SHRINK_WAVES - 1][MS * RB][WAVE];
-    const Rows tile = tile_rows<T>(p.b, blockIdx.x, rows);
+    __shared__ int own[SHRINK_WAVES][SMALL_T];
+    __shared__ f32x4_t red[SHRINK_WAVES][MS * RB][WAVE];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+    const Tile tile = find_tile<T>(p.b, blockIdx.x, own[w]);
     if (tile.a == -2 || (tile.a < 0 && !Q8))
         return;
-    __syncthreads();
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
     const int steps = (p.D + 127) / 128, parts = p.SK * SHRINK_WAVES;
     const int at = blockIdx.y * SHRINK_WAVES + w, j0 = blockIdx.z * (16 * RB);
     const int s0 = static_cast<int>(static_cast<int64_t>(steps) * at / parts);
     const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (at + 1) / parts);
 
-    const uint16_t* in[MS];
-    const uint16_t* wt[RB];
-    size_t row[MS];
+    const Matrix<WHOLE> in(p.in, static_cast<size_t>(p.b.M) * p.D);
+    const Matrix<WHOLE> wt(p.w, static_cast<size_t>(p.b.L) * p.r * p.D);
+    uint32_t row[MS], wrow[RB];        // where the lane's first 8 of a row start
 #pragma unroll
-    for (int s = 0; s < MS; ++s) {     // rows behind the last read that one again
-        const int i = 16 * s + c;
-        row[s] = static_cast<size_t>(rows[i < tile.count ? i : tile.count - 1]);
-        in[s] = p.in + row[s] * p.D + 8 * g;
-    }
+    for (int s = 0; s < MS; ++s)
+        row[s] = static_cast<uint32_t>(tile.rows[16 * s + c]) * p.D + 8 * g;
 #pragma unroll
-    for (int t = 0; t < RB; ++t) {     // and so do ranks behind the last
+    for (int t = 0; t < RB; ++t) {     // ranks behind the last read that one again
         const int j = j0 + 16 * t + c;
-        wt[t] = p.w + (static_cast<size_t>(tile.a < 0 ? 0 : tile.a) * p.r + (j < p.r ? j : p.r - 1)) * p.D + 8 * g;
+        wrow[t] = static_cast<uint32_t>((tile.a < 0 ? 0 : tile.a) * p.r + (j < p.r ? j : p.r - 1)) * p.D + 8 * g;
     }
     f32x4_t acc[MS][RB];
 #pragma unroll
@@ -488,72 +513,101 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
 #pragma unroll
         for (int t = 0; t < RB; ++t)
             acc[s][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int st = s0; st < s1; ++st) {
+    typedef typename Matrix<WHOLE>::Piece Piece;
+    auto fetch = [&](int st, Piece (&v)[MS][4], Piece (&wv)[RB][4]) {
         const int d0 = st * 128;
+#pragma unroll
+        for (int t = 0; t < RB; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                wv[t][i] = wt.fetch(wrow[t] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g), d0 + 128 > p.D);
+#pragma unroll
+        for (int s = 0; s < MS; ++s)
+            if (16 * s < tile.count)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[s][i] = in.fetch(row[s] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g), d0 + 128 > p.D);
+    };
+    auto use = [&](int st, const Piece (&vp)[MS][4], const Piece (&wp)[RB][4]) {
+        const int d0 = st * 128;
+        const bool edge = d0 + 128 > p.D;
         u32x4_t wv[RB][4];
 #pragma unroll
         for (int t = 0; t < RB; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                wv[t][i] = load8<WHOLE>(wt[t] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g));
+                wv[t][i] = wt.finish(wp[t][i], wrow[t], p.D - (d0 + 32 * i + 8 * g), edge);
 #pragma unroll
         for (int s = 0; s < MS; ++s) {
-            if (16 * s < tile.count) {
-                u32x4_t v[4];
+            if (16 * s >= tile.count)
+                break;
+            u32x4_t v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = load8<WHOLE>(in[s] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g));
-                if constexpr (Q8) {
-                    if (blockIdx.z == 0 && 16 * s + c < tile.count) {
-                        // the four lanes of a row hold its 128 channels
-                        uint32_t top = max(max(abs_max(v[0]), abs_max(v[1])), max(abs_max(v[2]), abs_max(v[3])));
-                        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
-                        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-                        const Scale8 e = scale8(top);
-                        uint8_t* o = p.q + row[s] * p.D + d0 + 8 * g;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<u32x2_t*>(o + 32 * i) = quantise8(v[i], e.inv);
-                        if (g == 0)
-                            p.qs[row[s] * (p.D / GROUP8) + st] = e.unit;
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < RB; ++t)
+            for (int i = 0; i < 4; ++i)      // steps of 32 leave an odd start odd
+                v[i] = in.finish(vp[s][i], row[s], p.D - (d0 + 32 * i + 8 * g), edge);
+            if constexpr (Q8) {
+                if (blockIdx.z == 0 && 16 * s + c < tile.count) {
+                    // the four lanes of a row hold its 128 channels
+                    uint32_t top = max(max(abs_max(v[0]), abs_max(v[1])), max(abs_max(v[2]), abs_max(v[3])));
+                    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
+                    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+                    const Scale8 e = scale8(top);
+                    uint8_t* o = p.q + row[s] + st * 128;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[s][t] = mfma(__builtin_bit_cast(bf16x8_t, v[i]), __builtin_bit_cast(bf16x8_t, wv[t][i]), acc[s][t]);
+                        *reinterpret_cast<u32x2_t*>(o + 32 * i) = quantise8(v[i], e.inv);
+                    if (g == 0)
+                        p.qs[row[s] / GROUP8 + st] = e.unit;
+                }
             }
+#pragma unroll
+            for (int t = 0; t < RB; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[s][t] = mfma(__builtin_bit_cast(bf16x8_t, v[i]), __builtin_bit_cast(bf16x8_t, wv[t][i]), acc[s][t]);
+        }
+    };
+    // two steps in registers where they fit: the next one's loads are on their
+    // way while this one is multiplied (4096 x 14336, rank 16: 42 -> 32 us)
+    Piece v0[MS][4], w0[RB][4];
+    if constexpr (MS * RB <= 4 || (WHOLE && !Q8)) {
+        Piece v1[MS][4], w1[RB][4];
+        if (s0 < s1)
+            fetch(s0, v0, w0);
+        for (int st = s0; st < s1; st += 2) {
+            if (st + 1 < s1)
+                fetch(st + 1, v1, w1);
+            use(st, v0, w0);
+            if (st + 1 >= s1)
+                break;
+            if (st + 2 < s1)
+                fetch(st + 2, v0, w0);
+            use(st + 1, v1, w1);
+        }
+    } else {
+        for (int st = s0; st < s1; ++st) {
+            fetch(st, v0, w0);
+            use(st, v0, w0);
         }
     }
     if (tile.a < 0)
         return;
-    if (w > 0) {
 #pragma unroll
-        for (int s = 0; s < MS; ++s)
-#pragma unroll
-            for (int t = 0; t < RB; ++t)
-                red[w - 1][s * RB + t][lane] = acc[s][t];
-    }
+    for (int e = 0; e < MS * RB; ++e)
+        red[w][e][lane] = acc[e / RB][e % RB];
     __syncthreads();
-    if (w > 0)
-        return;
+    const size_t places = static_cast<size_t>(gridDim.x) * T;
+    for (int e = w; e < MS * RB; e += SHRINK_WAVES) {     // a 16 x 16 block a wave
+        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int s = 0; s < MS; ++s)
+        for (int o = 0; o < SHRINK_WAVES; ++o)
+            v += red[o][e][lane];
+        const int s = e / RB, j = j0 + 16 * (e % RB) + c;
+        if (j < p.r16)
 #pragma unroll
-        for (int t = 0; t < RB; ++t) {
-            f32x4_t v = acc[s][t];
-#pragma unroll
-            for (int o = 0; o < SHRINK_WAVES - 1; ++o)
-                v += red[o][s * RB + t][lane];
-            const int j = j0 + 16 * t + c;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int m = 16 * s + 4 * g + i;
-                if (m < tile.count && j < p.r16)
-                    p.part[(static_cast<size_t>(blockIdx.y) * p.b.M + rows[m]) * p.r16 + j] = j < p.r ? v[i] : 0.0f;
-            }
-        }
+            for (int i = 0; i < 4; ++i)
+                p.part[(blockIdx.y * places + blockIdx.x * T + 16 * s + 4 * g + i) * p.r16 + j] = j < p.r ? v[i] : 0.0f;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -565,12 +619,14 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
 // registers, all loads 16 bytes) and goes over the tile's rows, 16 at a time.
 struct ExpandArgs {
     Batch b;
-    const float* part;        // [SK][M][r16]
+    const float* part;        // [SK][tiles * T][r16]
     const uint16_t* w;        // [L][r][D]
     const float* scale;       // [L]
     const uint16_t* base;     // [M][D] or null (0)
     uint16_t* out;            // [M][D] or null (only c is wanted)
     float* c;                 // [M][r] or null
+    const float* h;           // [M][r] and
+    float* turned;            // [2][r16][tiles * T]: c and h by place, for wgrad; or null
     int D, r, r16, SK;
 };
 
@@ -603,38 +659,50 @@ __global__ __launch_bounds__(EXPAND_THREADS) void k_expand(const ExpandArgs p)
 {
     constexpr int MS = T / 16, STRIDE = 32 * RK + 4;   // 4: rows of a quarter wave in other banks
     constexpr int PARTS = 8;                           // parts whose loads go out together
-    __shared__ int rows[T];
+    __shared__ int own[EXPAND_THREADS / WAVE][SMALL_T], rows[T];
     __shared__ __attribute__((aligned(16))) float cs[T * STRIDE];
-    const Rows tile = tile_rows<T>(p.b, blockIdx.y, rows);
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const Tile tile = find_tile<T>(p.b, blockIdx.y, own[tid >> 6]);
     if (tile.a == -2)
         return;
-    __syncthreads();
-    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int d0 = blockIdx.x * EXPAND_COLS + (tid >> 6) * 128, d = d0 + 8 * c;     // this lane's 8 columns
-    const bool first = blockIdx.x == 0;
+    const bool first = blockIdx.x == 0, edge = __builtin_amdgcn_readfirstlane(d0) + 128 > p.D;
+    const Matrix<WHOLE> base(p.base, static_cast<size_t>(p.b.M) * p.D), out(p.out, static_cast<size_t>(p.b.M) * p.D);
+    const Matrix<WHOLE> wt(p.w, static_cast<size_t>(p.b.L) * p.r * p.D);
     if (tile.a < 0) {     // rows without an adapter: the base as it is
         if (p.c && first)
             for (int i = tid; i < tile.count * p.r; i += EXPAND_THREADS)
-                p.c[static_cast<size_t>(rows[i / p.r]) * p.r + i % p.r] = 0.0f;
-        if (p.out && p.out != p.base && d < p.D)
+                p.c[static_cast<size_t>(tile.rows[i / p.r]) * p.r + i % p.r] = 0.0f;
+        if (p.out && p.out != p.base)
             for (int m = g; m < tile.count; m += 4) {
-                const size_t at = static_cast<size_t>(rows[m]) * p.D + d;
-                store8<WHOLE>(p.out + at, p.base ? load8<WHOLE>(p.base + at, p.D - d) : u32x4_t{0u, 0u, 0u, 0u}, p.D - d);
+                const uint32_t at = static_cast<uint32_t>(tile.rows[m]) * p.D + d;
+                out.store(at, base.finish(base.fetch(at, p.base ? p.D - d : 0, edge), at, p.D - d, edge), p.D - d, edge);
             }
         return;
     }
-    // every load of the workgroup goes out before the first wait: the parts of
-    // c, W and the base rows
+    // the parts of c (by place: they wait for no row), W and the rows' numbers
+    // come in together, then all the base rows
     constexpr int QUADS = 8 * RK, PER = (T * QUADS + EXPAND_THREADS - 1) / EXPAND_THREADS;
     const float scale = p.scale[tile.a];
+    const size_t next = static_cast<size_t>(gridDim.y) * T * p.r16;
+    typename Matrix<WHOLE>::Piece wp[RK][8], yp[MS][4];
+    const uint32_t w0 = static_cast<uint32_t>(tile.a * p.r) * p.D + d;
+#pragma unroll
+    for (int k = 0; k < RK; ++k)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int j = 32 * k + 8 * g + u;
+            wp[k][u] = wt.fetch(w0 + j * p.D, p.out && j < p.r ? p.D - d : 0, edge);
+        }
+    if (tid < T)
+        rows[tid] = tile.rows[tid];
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
         const int i = tid + e * EXPAND_THREADS, m = i / QUADS, j = i % QUADS * 4;
         if (i < T * QUADS) {
             f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
             if (m < tile.count && j < p.r16) {
-                const float* src = p.part + static_cast<size_t>(rows[m]) * p.r16 + j;
-                const size_t next = static_cast<size_t>(p.b.M) * p.r16;
+                const float* src = p.part + (static_cast<size_t>(blockIdx.y) * T + m) * p.r16 + j;
                 for (int s0 = 0; s0 < p.SK; s0 += PARTS) {
                     f32x4_t x[PARTS];
 #pragma unroll
@@ -647,37 +715,42 @@ __global__ __launch_bounds__(EXPAND_THREADS) void k_expand(const ExpandArgs p)
                 }
                 if (SCALED)
                     v *= scale;
-                if (p.c && first)
+                if (p.c && first) {
+                    float* o = p.c + static_cast<size_t>(tile.rows[m]) * p.r + j;
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         if (j + q < p.r)
-                            p.c[static_cast<size_t>(rows[m]) * p.r + j + q] = v[q];
+                            o[q] = v[q];
+                }
             }
             *reinterpret_cast<f32x4_t*>(&cs[m * STRIDE + j]) = v;
         }
     }
-    u32x4_t W[RK][8], y[MS][4];
+    __syncthreads();
+    if (p.turned && first) {     // places behind the last count for nothing
+        const size_t places = static_cast<size_t>(gridDim.y) * T;
+        float* o = p.turned + static_cast<size_t>(blockIdx.y) * T;
+        for (int i = tid; i < T * p.r16; i += EXPAND_THREADS) {
+            const int j = i / T, m = i % T;
+            o[j * places + m] = cs[m * STRIDE + j];
+            o[(p.r16 + j) * places + m] = p.h && m < tile.count && j < p.r ? p.h[static_cast<size_t>(rows[m]) * p.r + j] : 0.0f;
+        }
+    }
+    if (!p.out || d0 >= p.D)     // waves leave whole: every lane holds matrix-core operands
+        return;
 #pragma unroll
     for (int s = 0; s < MS; ++s)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int m = 16 * s + 4 * g + i;
-            y[s][i] = u32x4_t{0u, 0u, 0u, 0u};
-            if (p.out && p.base && m < tile.count)
-                y[s][i] = load8<WHOLE>(p.base + static_cast<size_t>(rows[m]) * p.D + d, p.D - d);
+            yp[s][i] = base.fetch(static_cast<uint32_t>(rows[m]) * p.D + d, p.base && m < tile.count ? p.D - d : 0, edge);
         }
+    u32x4_t W[RK][8];
 #pragma unroll
     for (int k = 0; k < RK; ++k)
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int j = 32 * k + 8 * g + u;
-            W[k][u] = u32x4_t{0u, 0u, 0u, 0u};
-            if (j < p.r && p.out)
-                W[k][u] = load8<WHOLE>(p.w + (static_cast<size_t>(tile.a) * p.r + j) * p.D + d, p.D - d);
-        }
-    __syncthreads();
-    if (!p.out || d0 >= p.D)     // waves leave whole: every lane holds matrix-core operands
-        return;
+        for (int u = 0; u < 8; ++u)
+            W[k][u] = wt.finish(wp[k][u], w0 + (32 * k + 8 * g + u) * p.D, p.D - d, edge);
 #pragma unroll
     for (int s = 0; s < MS; ++s) {
         if (16 * s >= tile.count)
@@ -702,14 +775,14 @@ __global__ __launch_bounds__(EXPAND_THREADS) void k_expand(const ExpandArgs p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int m = 16 * s + 4 * g + i;
-            if (m >= tile.count)
-                continue;
+            const uint32_t at = static_cast<uint32_t>(rows[m]) * p.D + d;
+            const u32x4_t y = base.finish(yp[s][i], at, p.D - d, edge);
             u32x4_t o;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                o[e] = f32_to_bf16(fmaf(after, acc[2 * e][i], bf16_to_f32(y[s][i][e] & 0xffffu))) |
-                       f32_to_bf16(fmaf(after, acc[2 * e + 1][i], bf16_to_f32(y[s][i][e] >> 16))) << 16;
-            store8<WHOLE>(p.out + static_cast<size_t>(rows[m]) * p.D + d, o, p.D - d);
+                o[e] = f32_to_bf16(fmaf(after, acc[2 * e][i], bf16_to_f32(y[e] & 0xffffu))) |
+                       f32_to_bf16(fmaf(after, acc[2 * e + 1][i], bf16_to_f32(y[e] >> 16))) << 16;
+            out.store(at, o, m < tile.count ? p.D - d : 0, edge);
         }
     }
 }
@@ -726,7 +799,7 @@ struct WgradJob {
     const uint16_t* in;      // [M][D] bf16, or null:
     const uint8_t* q;        // [M][D] int8 and
     const float* qs;         // [M][D/128] its scales
-    const float* c;          // [M][r]
+    const float* c;          // up to SMALL_M rows [M][r], else [r16][places]
     float* out;              // [L][r][D] or null
     float* part;             // [slots][r][cols * 128]
     int D, cols;             // columns, and blocks of 128 of them
@@ -737,6 +810,7 @@ struct WgradArgs {
     Batch b;
     const float* scale;
     WgradJob job[2];
+    int64_t places;
     int r;
     bool chunked;            // blockIdx.y is a chunk of the plan; else an adapter
 };
@@ -744,122 +818,149 @@ struct WgradArgs {
 constexpr int WGRAD_THREADS = 512;
 constexpr int WGRAD_WAVES = WGRAD_THREADS / WAVE;
 
-template <int RT, bool WHOLE>
+template <int RT, bool WHOLE, bool SMALL>
 __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
 {
-    __shared__ int rows[CHUNK];
-    __shared__ float red[WGRAD_WAVES / 2][RT * 32][WAVE];
+    constexpr int STRIDE = 128 + 4;      // 4: rows of a quarter wave in other banks
+    __shared__ __attribute__((aligned(16))) float red[WGRAD_WAVES][16 * STRIDE];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, g = lane >> 4;
     const bool second = static_cast<int>(blockIdx.x) >= p.job[0].cols;
     const WgradJob job = second ? p.job[1] : p.job[0];
     const int cb = static_cast<int>(blockIdx.x) - (second ? p.job[0].cols : 0), j0 = blockIdx.z * (16 * RT);
-    int a = blockIdx.y, count = 0, slot = -1;
-    if (p.b.plan && (p.b.plan[2] != p.b.M || p.b.plan[3] != p.b.L))
-        return;
-    if (p.chunked) {
-        if (a >= p.b.plan[1])
+    int a = blockIdx.y, count = 0, slot = -1, first = 0;
+    const int* rows;
+    if constexpr (!SMALL) {
+        const PlanLayout l(p.b.M, p.b.L);
+        if (p.chunked) {
+            const int* e = p.b.plan + l.chunk + 4 * static_cast<int64_t>(a);
+            if (a >= p.b.plan[1])
+                return;
+            a = e[0];
+            first = e[1];
+            count = e[2];
+            slot = e[3];
+        } else {
+            first = p.b.plan[l.first + a] * TILE_T;
+            count = p.b.plan[l.count + a];
+        }
+        if (p.b.plan[2] != p.b.M || p.b.plan[3] != p.b.L)
             return;
-        const PlanLayout l(p.b.M, p.b.L);
-        const int* e = p.b.plan + l.chunk + 4 * static_cast<int64_t>(a);
-        a = e[0];
-        const int first = e[1];
-        count = e[2];
-        slot = e[3];
-        if (tid < count)
-            rows[tid] = p.b.plan[l.perm + first + tid];
-    } else if (p.b.plan) {
-        const PlanLayout l(p.b.M, p.b.L);
-        const int first = p.b.plan[l.seg + a];
-        count = p.b.plan[l.seg + a + 1] - first;      // at most M <= CHUNK
-        if (tid < count)
-            rows[tid] = p.b.plan[l.perm + first + tid];
+        rows = p.b.plan + l.rows + first;
     } else {
+        // every wave lists the rows for itself, where its sums go afterwards
+        int* own = reinterpret_cast<int*>(red[w]);
         const bool mine = lane < p.b.M && p.b.ids[lane < p.b.M ? lane : 0] == a;
         const uint64_t m = __ballot(mine);
         count = __builtin_popcountll(m);
-        if (tid < WAVE && mine)
-            rows[__builtin_popcountll(m & ((1ull << lane) - 1))] = lane;
+        if (count && lane >= count)
+            own[lane] = 63 - __builtin_clzll(m);      // places behind the last repeat it
+        if (mine)
+            own[__builtin_popcountll(m & ((1ull << lane) - 1))] = lane;
+        rows = own;
     }
-    __syncthreads();
     const int d = cb * 128 + 8 * c;
-    const bool q8 = !job.in;
+    const bool edge = cb * 128 + 128 > job.D;
+    const Matrix<WHOLE> in(job.in, static_cast<size_t>(p.b.M) * job.D);
     f32x4_t acc[RT][8];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int t = 0; t < 8; ++t)
             acc[rt][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int m0 = 32 * w; m0 < count; m0 += 32 * WGRAD_WAVES) {
-        u32x4_t R[8];
-        float f[RT][8];
-        const int mine = m0 + 8 * g;
+    // 32 rows: their numbers, 8 x 8 blocks of their columns and their factors
+    auto step = [&](int m0, auto in8) {
+        constexpr bool Q8 = decltype(in8)::value;
+        uint32_t row[8];
+        typename Matrix<WHOLE>::Piece x[8];
+        u32x2_t q[8];
+        float unit[8], f[RT][8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {     // rows behind the last read that one again, times zero
-            const int m = mine + u;
-            const size_t row = static_cast<size_t>(rows[m < count ? m : count - 1]);
-            float unit = 1.0f;
-            if (q8) {
-                u32x2_t v = *reinterpret_cast<const u32x2_t*>(job.q + row * job.D + d);
-                unit = job.qs[row * (job.D / GROUP8) + cb];
+        for (int u = 0; u < 8; ++u)      // m0 + 31 lies in the last row's tile
+            row[u] = static_cast<uint32_t>(rows[m0 + 8 * g + u]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    R[u][e] = __builtin_amdgcn_perm(__float_as_uint(byte_to_f32(v[e / 2], (2 * e + 1) & 3)),
-                                                    __float_as_uint(byte_to_f32(v[e / 2], (2 * e) & 3)), 0x07060302u);
+        for (int u = 0; u < 8; ++u) {
+            if constexpr (Q8) {
+                q[u] = *reinterpret_cast<const u32x2_t*>(job.q + row[u] * job.D + d);
+                unit[u] = job.qs[row[u] * (job.D / GROUP8) + cb];
             } else {
-                R[u] = load8<WHOLE>(job.in + row * job.D + d, job.D - d);
-            }
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const int j = j0 + 16 * rt + c;
-                f[rt][u] = m < count && j < p.r ? job.c[row * p.r + j] * unit : 0.0f;
+                x[u] = in.fetch(row[u] * job.D + d, job.D - d, edge);
             }
         }
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < RT; ++rt) {
+            const int j = j0 + 16 * rt + c;
+            if constexpr (SMALL) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)     // places behind the last count for nothing
+                    f[rt][u] = m0 + 8 * g + u < count && j < p.r ? job.c[row[u] * p.r + j] : 0.0f;
+            } else {                            // ranks behind the last: never stored
+                const f32x4_t* src = reinterpret_cast<const f32x4_t*>(job.c + (j < p.r ? j : p.r - 1) * p.places + first + m0 + 8 * g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[rt][e] = src[e / 4][e % 4];
+            }
+        }
+        u32x4_t R[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if constexpr (Q8) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    R[u][e] = __builtin_amdgcn_perm(__float_as_uint(byte_to_f32(q[u][e / 2], (2 * e + 1) & 3)),
+                                                    __float_as_uint(byte_to_f32(q[u][e / 2], (2 * e) & 3)), 0x07060302u);
+            } else {
+                R[u] = in.finish(x[u], row[u] * job.D + d, job.D - d, edge);
+            }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            if constexpr (Q8)
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    f[rt][u] *= unit[u];
             mul_columns(acc[rt], split3(f[rt]), R);
-    }
-#pragma unroll
-    for (int half = WGRAD_WAVES / 2; half > 0; half >>= 1) {
-        if (w >= half && w < 2 * half)
-#pragma unroll
-            for (int v = 0; v < RT * 32; ++v)
-                red[w - half][v][lane] = acc[v / 32][v / 4 % 8][v % 4];
-        __syncthreads();
-        if (w < half)
-#pragma unroll
-            for (int v = 0; v < RT * 32; ++v)
-                acc[v / 32][v / 4 % 8][v % 4] += red[w][v][lane];
-        __syncthreads();
-    }
-    if (w > 0 || d >= job.D)
-        return;
-    const float f = job.scaled && count ? p.scale[a] : 1.0f;
+        }
+    };
+    if (job.in)
+        for (int m0 = 32 * w; m0 < count; m0 += 32 * WGRAD_WAVES)
+            step(m0, std::false_type{});
+    else
+        for (int m0 = 32 * w; m0 < count; m0 += 32 * WGRAD_WAVES)
+            step(m0, std::true_type{});
+    const float f = slot < 0 && job.scaled && count ? p.scale[a] : 1.0f;
     const size_t width = slot < 0 ? job.D : static_cast<size_t>(job.cols) * 128;
     float* out = slot < 0 ? job.out + static_cast<size_t>(a) * p.r * width : job.part + static_cast<size_t>(slot) * p.r * width;
+    // 16 ranks at a time, the eight waves' sums side by side, then added in
+    // order by all threads: 4 columns of one rank each
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int rt = 0; rt < RT; ++rt) {
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = j0 + 16 * rt + 4 * g + i;
-            if (j >= p.r)
-                continue;
-            float* o = out + j * width + d;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                f32x4_t v;
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<f32x4_t*>(&red[w][(4 * g + i) * STRIDE + 8 * c + 4 * h]) =
+                    f32x4_t{acc[rt][4 * h][i], acc[rt][4 * h + 1][i], acc[rt][4 * h + 2][i], acc[rt][4 * h + 3][i]};
+        __syncthreads();
+        const int q = tid >> 5, e = (tid & 31) * 4, j = j0 + 16 * rt + q, at = cb * 128 + e;
+        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = slot < 0 ? f * acc[rt][4 * h + e][i] : acc[rt][4 * h + e][i];
-                if (slot >= 0 || d + 8 <= job.D) {
-                    reinterpret_cast<f32x4_a4_t*>(o)[h] = v;
-                } else {
+        for (int o = 0; o < WGRAD_WAVES; ++o)
+            v += *reinterpret_cast<const f32x4_t*>(&red[o][q * STRIDE + e]);
+        if (j >= p.r)
+            continue;
+        v *= f;
+        float* o = out + j * width + at;
+        if (WHOLE || slot >= 0 || at + 4 <= job.D) {
+            if (slot >= 0 || at < job.D)
+                *reinterpret_cast<f32x4_a4_t*>(o) = v;
+        } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (d + 4 * h + e < job.D)
-                            o[4 * h + e] = v[e];
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                if (at + i < job.D)
+                    o[i] = v[i];
         }
+    }
 }
 
 // Adapters of several chunks: their partial sums in order.  Adapters without
@@ -870,7 +971,7 @@ __global__ __launch_bounds__(256) void k_wgrad_sum(const WgradArgs p)
     if (p.b.plan[2] != p.b.M || p.b.plan[3] != p.b.L)
         return;
     const PlanLayout l(p.b.M, p.b.L);
-    const int n = chunks_of(p.b.plan[l.seg + a + 1] - p.b.plan[l.seg + a]);
+    const int n = chunks_of(p.b.plan[l.count + a]);
     if (n == 1)
         return;
     int d = blockIdx.x * 256 + threadIdx.x;
@@ -899,11 +1000,10 @@ int round16(int64_t r) { return static_cast<int>((r + 15) / 16 * 16); }
 int split_of(int64_t M, int64_t L, int64_t D, int64_t r)
 {
     const int64_t steps = (D + 127) / 128, most = (steps + SHRINK_WAVES - 1) / SHRINK_WAVES;
-    const int64_t groups = M <= SMALL_M ? 1 : (M + TILE_T - 1) / TILE_T * ((r + 63) / 64);
+    const int64_t groups = tile_bound(M, L) * ((r + 63) / 64);
     int64_t want = M <= SMALL_M ? 16 : (512 + groups - 1) / groups;
-    const int64_t cap = M <= SMALL_M ? 16 : 8;
+    const int64_t cap = M <= SMALL_M ? 16 : 4;
     want = want < cap ? want : cap;
-    (void)L;
     return static_cast<int>(want < most ? want : most);
 }
 
@@ -911,7 +1011,8 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 size_t part_bytes(int64_t M, int64_t L, int64_t D, int64_t r)
 {
-    return up256(static_cast<size_t>(split_of(M, L, D, r)) * M * round16(r) * 4);
+    const int64_t places = tile_bound(M, L) * (M <= SMALL_M ? SMALL_T : TILE_T);
+    return up256(static_cast<size_t>(split_of(M, L, D, r)) * places * round16(r) * 4);
 }
 
 size_t plan_bytes(int64_t M, int64_t L) { return up256(static_cast<size_t>(plan_words(M, L)) * 4); }
@@ -922,6 +1023,12 @@ int64_t slot_bound(int64_t M) { return M > CHUNK ? 2 * (M / CHUNK) : 0; }
 size_t wgrad_bytes(int64_t M, int64_t D, int64_t r)
 {
     return up256(static_cast<size_t>(slot_bound(M)) * r * ((D + 127) / 128 * 128) * 4);
+}
+
+// what the weight gradients multiply with: dh by row, or dh and h by place
+size_t factor_bytes(int64_t M, int64_t L, int64_t r)
+{
+    return up256(static_cast<size_t>(M <= SMALL_M ? M * r : 2 * round16(r) * tile_bound(M, L) * TILE_T) * 4);
 }
 
 bool sizes_ok(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L)
@@ -954,7 +1061,7 @@ void launch_shrink(const ShrinkArgs& s, int64_t tiles, hipStream_t stream)
 {
     if (s.q)                      // D is a multiple of 128 then
         launch_shrink_as<true, true>(s, tiles, stream);
-    else if (s.D % 8 == 0)
+    else if (s.D % 8 == 0 && is_aligned(s.in, 16) && is_aligned(s.w, 16))
         launch_shrink_as<false, true>(s, tiles, stream);
     else
         launch_shrink_as<false, false>(s, tiles, stream);
@@ -982,7 +1089,7 @@ void launch_expand(const ExpandArgs& e, int64_t tiles, bool scaled, hipStream_t 
 {
     if (scaled)                   // D is K, a multiple of 128
         launch_expand_as<true, true>(e, tiles, stream);
-    else if (e.D % 8 == 0)
+    else if (e.D % 8 == 0 && is_aligned(e.base, 16) && is_aligned(e.out, 16) && is_aligned(e.w, 16))
         launch_expand_as<false, true>(e, tiles, stream);
     else
         launch_expand_as<false, false>(e, tiles, stream);
@@ -995,10 +1102,16 @@ void launch_wgrad(const WgradArgs& a, hipStream_t stream)
     const int64_t ys = a.chunked ? PlanLayout(a.b.M, a.b.L).CB : a.b.L;
     const unsigned cols = static_cast<unsigned>(a.job[0].cols + a.job[1].cols);
     const dim3 grid(cols, static_cast<unsigned>(ys), static_cast<unsigned>((a.r + 16 * rt - 1) / (16 * rt)));
-#define WGRAD(RT_) hipLaunchKernelGGL((k_wgrad<RT_, WHOLE>), grid, dim3(WGRAD_THREADS), 0, stream, a)
-    if (rt == 1) WGRAD(1);
-    else if (rt == 2) WGRAD(2);
-    else WGRAD(4);
+#define WGRAD(RT_, SMALL_) hipLaunchKernelGGL((k_wgrad<RT_, WHOLE, SMALL_>), grid, dim3(WGRAD_THREADS), 0, stream, a)
+    if (a.b.M <= SMALL_M) {
+        if (rt == 1) WGRAD(1, true);
+        else if (rt == 2) WGRAD(2, true);
+        else WGRAD(4, true);
+    } else {
+        if (rt == 1) WGRAD(1, false);
+        else if (rt == 2) WGRAD(2, false);
+        else WGRAD(4, false);
+    }
 #undef WGRAD
     if (a.chunked)
         hipLaunchKernelGGL(k_wgrad_sum, dim3((cols * 128 + 255) / 256, static_cast<unsigned>(a.b.L), static_cast<unsigned>(a.r)),
@@ -1072,7 +1185,7 @@ any4_status any4_lora(const uint16_t* x, const uint16_t* A, const uint16_t* B, c
     const int64_t tiles = tile_bound(M, L);
     const ShrinkArgs s{b, x, A, part, reinterpret_cast<uint8_t*>(q), qs, static_cast<int>(K), static_cast<int>(r), r16, SK};
     launch_shrink(s, tiles, stream);
-    const ExpandArgs e{b, part, B, scale, y, N > 0 ? out : nullptr, h, static_cast<int>(N), static_cast<int>(r), r16, SK};
+    const ExpandArgs e{b, part, B, scale, y, N > 0 ? out : nullptr, h, nullptr, nullptr, static_cast<int>(N), static_cast<int>(r), r16, SK};
     if (e.out || h)
         launch_expand(e, tiles, false, stream);
     return launch_status();
@@ -1082,7 +1195,7 @@ size_t any4_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int64_
 {
     if (M <= 0 || N <= 0 || !sizes_ok(M, N, K, r, L))
         return 0;
-    return part_bytes(M, L, N, r) + up256(static_cast<size_t>(M) * r * 4) + (M <= SMALL_M ? 0 : plan_bytes(M, L)) +
+    return part_bytes(M, L, N, r) + factor_bytes(M, L, r) + (M <= SMALL_M ? 0 : plan_bytes(M, L)) +
            wgrad_bytes(M, K, r) + wgrad_bytes(M, N, r);
 }
 
@@ -1107,8 +1220,8 @@ any4_status any4_lora_backward(const uint16_t* dy, const uint16_t* x, const int8
     char* at = static_cast<char*>(workspace);
     float* part = reinterpret_cast<float*>(at);
     at += part_bytes(M, L, N, r);
-    float* dh = reinterpret_cast<float*>(at);
-    at += up256(static_cast<size_t>(M) * r * 4);
+    float* factors = reinterpret_cast<float*>(at);
+    at += factor_bytes(M, L, r);
     Batch b{ids, nullptr, static_cast<int>(M), static_cast<int>(L)};
     if (M > SMALL_M) {
         b.plan = static_cast<const int*>(plan);
@@ -1120,21 +1233,26 @@ any4_status any4_lora_backward(const uint16_t* dy, const uint16_t* x, const int8
     }
     const int r16 = round16(r), SK = split_of(M, L, N, r);
     const int64_t tiles = tile_bound(M, L);
-    if (dx_out || dA) {
+    const bool small = M <= SMALL_M, need_dh = dx_out || dA;
+    const int64_t places = tiles * TILE_T;
+    if (need_dh) {
         const ShrinkArgs s{b, dy, B, part, nullptr, nullptr, static_cast<int>(N), static_cast<int>(r), r16, SK};
         launch_shrink(s, tiles, stream);
-        const ExpandArgs e{b, part, A, scale, dx, dx_out, dh, static_cast<int>(K), static_cast<int>(r), r16, SK};
+    }
+    if (need_dh || (dB && !small)) {      // without dh: only h is turned
+        const ExpandArgs e{b, part, A, scale, dx, dx_out, small ? factors : nullptr, dB ? h : nullptr,
+                           small || (!dA && !dB) ? nullptr : factors, static_cast<int>(K), static_cast<int>(r), r16, need_dh ? SK : 0};
         launch_expand(e, tiles, true, stream);
     }
     if (dA || dB) {
         const bool chunked = M > CHUNK;
-        WgradArgs g{b, scale, {}, static_cast<int>(r), chunked};
-        g.job[0] = WgradJob{x, reinterpret_cast<const uint8_t*>(q), qs, dh, dA, reinterpret_cast<float*>(at),
+        WgradArgs g{b, scale, {}, places, static_cast<int>(r), chunked};
+        g.job[0] = WgradJob{x, reinterpret_cast<const uint8_t*>(q), qs, factors, dA, reinterpret_cast<float*>(at),
                             static_cast<int>(K), dA ? static_cast<int>(K / 128) : 0, false};
         at += wgrad_bytes(M, K, r);
-        g.job[1] = WgradJob{dy, nullptr, nullptr, h, dB, reinterpret_cast<float*>(at), static_cast<int>(N),
+        g.job[1] = WgradJob{dy, nullptr, nullptr, small ? h : factors + static_cast<size_t>(r16) * places, dB, reinterpret_cast<float*>(at), static_cast<int>(N),
                             dB ? static_cast<int>((N + 127) / 128) : 0, true};
-        if (N % 8 == 0)
+        if (N % 8 == 0 && is_aligned(dy, 16) && is_aligned(dA, 16) && is_aligned(dB, 16))
             launch_wgrad<true>(g, stream);
         else
             launch_wgrad<false>(g, stream);

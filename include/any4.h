@@ -368,7 +368,7 @@ any4_status any4_quantize(const float* W, const float* ex, uint8_t* idx, uint16_
  * rounding.  Results are deterministic and a row's result depends on no other
  * row's values.  A non-finite weight of an adapter makes the outputs it
  * reaches non-finite (which kind is not specified).
- * Sizes of all any4_lora* calls: 0 <= M <= 2^21, 0 <= N <= 2^24, K <= 2^24 a
+ * Sizes of all any4_lora* calls: 0 <= M <= 2^20, 0 <= N <= 2^24, K <= 2^24 a
  * positive multiple of 128, 1 <= r <= 128, 1 <= L <= 4096; x, y, A and B below
  * 2 GiB.
  * N, r and M need not be multiples of anything.

@@ -20,7 +20,7 @@ def backward(dy=A, x=A, q=None, qs=None, h=A, a=A, b=A, scale=A, ids=A, plan=Non
                                   ws_bytes, stream=0)
 
 
-SHAPES = [dict(M=-1), dict(M=(1 << 21) + 1), dict(N=-1), dict(K=0), dict(K=64), dict(K=192), dict(K=-128), dict(M=1, N=(1 << 24) + 1), dict(M=1, K=(1 << 24) + 128), dict(r=0),
+SHAPES = [dict(M=-1), dict(M=(1 << 20) + 1), dict(N=-1), dict(K=0), dict(K=64), dict(K=192), dict(K=-128), dict(M=1, N=(1 << 24) + 1), dict(M=1, K=(1 << 24) + 128), dict(r=0),
           dict(r=129), dict(L=0), dict(L=4097), dict(M=1 << 20, K=1024), dict(M=1 << 20, N=1024),
           dict(L=4096, r=128, K=2048), dict(L=4096, r=128, N=2048)]
 
@@ -82,7 +82,7 @@ def test_empty_batch_is_a_no_op():
 
 def test_plan_errors_and_sizes():
     assert any4.lora_plan_bytes(0, 4) == 0 and any4.lora_plan_bytes(4, 0) == 0
-    assert any4.lora_plan_bytes(4, 4097) == 0 and any4.lora_plan_bytes((1 << 21) + 1, 1) == 0
+    assert any4.lora_plan_bytes(4, 4097) == 0 and any4.lora_plan_bytes((1 << 20) + 1, 1) == 0
     need = any4.lora_plan_bytes(1000, 4)
     assert need >= 4 * 1000
     assert any4.lora_plan_raw(A, A, need - 1, 1000, 4, stream=0) == 4
