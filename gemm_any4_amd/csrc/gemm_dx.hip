@@ -123,12 +123,14 @@ __global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ d
 // ---------------------------------------------------------------------------
 // the product
 // ---------------------------------------------------------------------------
-// 128 rows of dy x 128 rows of W^T a workgroup, 64 n a step: both tiles go to
-// LDS by direct loads, the next step's while this one is multiplied.  A row of
-// a tile is eight 16-byte pieces; piece q stands at q ^ key(row), keys chosen
-// so that the 16 lanes of an operand read touch all 64 banks once.
-constexpr int BM = 128, BN = 128, DX_THREADS = 256;
-
+// A workgroup takes BM rows of dy x BN rows of W^T, 64 n a step; each wave has
+// 16*RM x 16*RN of the outputs.  Both tiles go to LDS by direct loads, the next
+// step's while this one is multiplied: one barrier a step.  Bound by the matrix
+// cores and the LDS reads that feed them (a wave's 128 x 64 outputs: 12 reads of
+// 1 KB for 32 products); 4096 x 14336 x 4096 takes 371 us, 1297 TFLOP/s (128 x 128
+// tiles of four 64 x 64 waves: 645 us).  A row of a tile is
+// eight 16-byte pieces; piece q stands at q ^ key(row), keys chosen so that the
+// 16 lanes of an operand read touch all 64 banks once.
 struct DxArgs {
     const uint16_t* dy;     // [M][Np]
     const uint16_t* wt;     // [K][Np]
@@ -144,77 +146,122 @@ __device__ __forceinline__ int key_wt(int r) { return (r >> 1 & 1) | (r >> 4 & 3
 // then 16 adjacent k
 __device__ __forceinline__ int row_of(int t, int rho) { return 16 * (rho >> 2) + 4 * t + (rho & 3); }
 
-typedef const __attribute__((address_space(1))) uint32_t* gptr_t;
-typedef __attribute__((address_space(3))) uint32_t* lptr_t;
-
-__global__ __launch_bounds__(DX_THREADS) void k_dx(const DxArgs p)
+// 16 bytes a lane from the buffer to 1 KB of LDS, lane after lane.
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint16_t* to, int at, int step)
 {
-    __shared__ __attribute__((aligned(16))) uint16_t sa[2][BM * STEP], sb[2][BN * STEP];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, g = lane >> 4;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, at, step, 0, 0);
+}
+
+// WM x WN waves of RM x 4 blocks of 16 x 16.
+template <int WM, int WN, int RM>
+__global__ __launch_bounds__(64 * WM * WN) void k_dx(const DxArgs p)
+{
+    constexpr int BM = WM * RM * 16, BN = WN * 64, WAVES = WM * WN;
+    constexpr int LA = BM / 8 / WAVES, LB = BN / 8 / WAVES;      // load instructions of a wave a step
+    // two buffers of their own each, so that loads into one are known not to
+    // touch reads of the other
+    __shared__ __attribute__((aligned(16))) uint16_t sa0[BM * STEP], sb0[BN * STEP], sa1[BM * STEP], sb1[BN * STEP];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
     const int tiles_k = p.K / BN, tiles_m = (p.M + BM - 1) / BM, tiles = tiles_k * tiles_m;
-    // workgroups go to the eight XCDs in turn: each gets a run of tiles that
-    // share rows, which its L2 then holds
+    // workgroups go to the eight XCDs in turn: each XCD gets a run of tiles, four
+    // rows of tiles high, whose operands its L2 then shares
     int id = blockIdx.x;
     if (tiles % 8 == 0)
         id = id % 8 * (tiles / 8) + id / 8;
-    const int m0 = id / tiles_k * BM, k0 = id % tiles_k * BN;
+    constexpr int HIGH = 4;
+    const int band = id / (HIGH * tiles_k), high = tiles_m - band * HIGH < HIGH ? tiles_m - band * HIGH : HIGH;
+    const int in_band = id - band * HIGH * tiles_k;
+    const int m0 = (band * HIGH + in_band % high) * BM, k0 = in_band / high * BN;
     const int steps = p.Np / STEP;
     const int s0 = static_cast<int>(static_cast<int64_t>(steps) * blockIdx.y / p.S);
     const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (blockIdx.y + 1) / p.S);
 
-    // a wave's load instruction fills 8 rows of a tile; lane: row lane / 8, place lane % 8
-    const uint16_t* ga[4];
-    const uint16_t* gb[4];
+    // a wave's load instruction fills 8 rows of a tile; lane: row lane / 8, place
+    // lane % 8.  Rows behind the last read as 0.
+    const size_t pitch = static_cast<size_t>(p.Np) * 2;
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(p.dy) + m0 * static_cast<size_t>(p.Np), static_cast<short>(0),
+        static_cast<int>((p.M - m0 < BM ? p.M - m0 : BM) * pitch), 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(p.wt) + k0 * static_cast<size_t>(p.Np), static_cast<short>(0), static_cast<int>(BN * pitch), 0x00020000);
+    int ga[LA], gb[LB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (w * 4 + i) * 8 + lane / 8;
-        const int m = m0 + r < p.M ? m0 + r : p.M - 1;
-        ga[i] = p.dy + static_cast<size_t>(m) * p.Np + ((lane & 7) ^ key_dy(r)) * 8;
-        gb[i] = p.wt + static_cast<size_t>(k0 + r) * p.Np + ((lane & 7) ^ key_wt(r)) * 8;
+    for (int i = 0; i < LA; ++i) {
+        const int r = (w * LA + i) * 8 + lane / 8;
+        ga[i] = static_cast<int>(r * pitch) + ((lane & 7) ^ key_dy(r)) * 16;
     }
-    auto fetch = [&](int st, int buf) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __builtin_amdgcn_global_load_lds((gptr_t)(ga[i] + static_cast<size_t>(st) * STEP),
-                                             (lptr_t)(&sa[buf][(w * 4 + i) * 8 * STEP]), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((gptr_t)(gb[i] + static_cast<size_t>(st) * STEP),
-                                             (lptr_t)(&sb[buf][(w * 4 + i) * 8 * STEP]), 16, 0, 0);
-        }
+    for (int i = 0; i < LB; ++i) {
+        const int r = (w * LB + i) * 8 + lane / 8;
+        gb[i] = static_cast<int>(r * pitch) + ((lane & 7) ^ key_wt(r)) * 16;
+    }
+    auto fetch = [&](int st, uint16_t* sa, uint16_t* sb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < LA; ++i)
+            load_lds(ra, sa + (w * LA + i) * 8 * STEP, ga[i], st * STEP * 2);
+#pragma unroll
+        for (int i = 0; i < LB; ++i)
+            load_lds(rb, sb + (w * LB + i) * 8 * STEP, gb[i], st * STEP * 2);
     };
-    f32x4_t acc[4][4];     // [rows of dy][rows of W^T]
+    f32x4_t acc[RM][4];     // [rows of dy][rows of W^T]
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RM; ++i)
 #pragma unroll
         for (int t = 0; t < 4; ++t)
             acc[i][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const int wm = (w >> 1) * 64, wk = (w & 1) * 64;
-    if (s0 < s1)
-        fetch(s0, 0);
-    for (int st = s0; st < s1; ++st) {
-        const int buf = (st - s0) & 1;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();      // this step's tiles are in, and the other buffer has been read
-        if (st + 1 < s1)
-            fetch(st + 1, buf ^ 1);
+    const int wm = (w / WN) * (RM * 16), wk = (w % WN) * 64;
+    // operand reads: 16 rows of dy on, or 4 of W^T, the key is the same, so one
+    // address each and constant distances; the second half of a step is four
+    // pieces on, bit 2 of the piece
+    const int oa = (wm + c) * STEP, ob = (wk + row_of(0, c)) * STEP;
+    const int pa = g ^ key_dy(wm + c), pb = g ^ key_wt(wk + row_of(0, c));
+    auto multiply = [&](const uint16_t* sa, const uint16_t* sb) __attribute__((always_inline)) {
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            bf16x8_t a[4], b[4];
+            bf16x8_t a[RM], b[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int ra = wm + 16 * i + c, rb = wk + row_of(i, c);
-                a[i] = *reinterpret_cast<const bf16x8_t*>(&sa[buf][ra * STEP + ((4 * kk + g) ^ key_dy(ra)) * 8]);
-                b[i] = *reinterpret_cast<const bf16x8_t*>(&sb[buf][rb * STEP + ((4 * kk + g) ^ key_wt(rb)) * 8]);
-            }
+            for (int t = 0; t < 4; ++t)
+                b[t] = *reinterpret_cast<const bf16x8_t*>(sb + ob + (pb ^ 4 * kk) * 8 + 4 * t * STEP);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < RM; ++i)
+                a[i] = *reinterpret_cast<const bf16x8_t*>(sa + oa + (pa ^ 4 * kk) * 8 + 16 * i * STEP);
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     acc[i][t] = mfma(b[t], a[i], acc[i][t]);
         }
+    };
+    // this step's tiles are in, and every wave has read the other buffer
+    auto meet = [&]() __attribute__((always_inline)) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    };
+    if (s0 < s1)
+        fetch(s0, sa0, sb0);
+    // the loads stay where they stand (sched_barrier): sunk to the next barrier
+    // they cost a sixth of the time
+    int st = s0;
+    for (; st + 1 < s1; st += 2) {
+        meet();
+        fetch(st + 1, sa1, sb1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(sa0, sb0);
+        __builtin_amdgcn_sched_barrier(0);
+        meet();
+        if (st + 2 < s1)
+            fetch(st + 2, sa0, sb0);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(sa1, sb1);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    if (st < s1) {
+        meet();
+        multiply(sa0, sb0);
     }
     // lane: row c of dy, k 16g .. 16g + 15 of the wave's 64
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RM; ++i) {
         const int m = m0 + wm + 16 * i + c;
         if (m >= p.M)
             continue;
@@ -266,14 +313,25 @@ __global__ __launch_bounds__(256) void k_dx_zero(uint16_t* dx, size_t octs)
 // ---------------------------------------------------------------------------
 int64_t padded(int64_t N) { return (N + STEP - 1) / STEP * STEP; }
 
+// Tiles: 256 x 256 where they fill the chip (or nearly), else 128 x 128.
+struct Shape {
+    bool big;
+    int64_t tiles;
+    int S;
+};
+
 // n is split where the tiles alone leave the 256 CUs idle, at least 4 steps to
 // a split; the partial sums are fp32.
-int dx_splits(int64_t M, int64_t N, int64_t K)
+Shape dx_shape(int64_t M, int64_t N, int64_t K)
 {
-    const int64_t tiles = (M + BM - 1) / BM * (K / BN), steps = padded(N) / STEP;
-    int64_t S = (512 + tiles - 1) / tiles;
+    const int64_t big = (M + 255) / 256 * (K / 256), small = (M + 127) / 128 * (K / 128), steps = padded(N) / STEP;
+    Shape s;
+    s.big = K % 256 == 0 && big >= 192;
+    s.tiles = s.big ? big : small;
+    int64_t S = s.big ? 1 : (512 + s.tiles - 1) / s.tiles;
     S = S < steps / 4 ? S : steps / 4;
-    return static_cast<int>(S < 1 ? 1 : S > 16 ? 16 : S);
+    s.S = static_cast<int>(S < 1 ? 1 : S > 16 ? 16 : S);
+    return s;
 }
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
@@ -282,14 +340,14 @@ size_t wt_bytes(int64_t N, int64_t K) { return up256(static_cast<size_t>(K) * pa
 
 size_t dx_part_bytes(int64_t M, int64_t N, int64_t K)
 {
-    const int S = dx_splits(M, N, K);
+    const int S = dx_shape(M, N, K).S;
     return S > 1 ? up256(static_cast<size_t>(S) * M * K * 4) : 0;
 }
 
 bool dx_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t g)
 {
     const int64_t top = static_cast<int64_t>(1) << 31;
-    return M >= 0 && M <= 65535 * 64 && N >= 0 && N < top / 32 && K >= 0 && K < top && g > 0 && g % 128 == 0 &&
+    return M >= 0 && M <= 65535 * 64 && N >= 0 && N <= static_cast<int64_t>(1) << 21 && K >= 0 && K < top && g > 0 && g % 128 == 0 &&
            K % g == 0 && N * K < 2 * top && M * K * 2 < top && M * N * 2 < top;
 }
 
@@ -326,7 +384,8 @@ any4_status gemm_dx(int fmt, const uint16_t* dy, const uint8_t* packed, const ui
     else if (fmt == FMT_ANY2) TURN(FMT_ANY2);
     else TURN(FMT_ANY3);
 #undef TURN
-    DxArgs a{dy, wt, dx, nullptr, static_cast<int>(M), static_cast<int>(K), Np, dx_splits(M, N, K)};
+    const Shape shape = dx_shape(M, N, K);
+    DxArgs a{dy, wt, dx, nullptr, static_cast<int>(M), static_cast<int>(K), Np, shape.S};
     if (N != Np || !is_aligned(dy, 16)) {
         uint16_t* copy = reinterpret_cast<uint16_t*>(at);
         const size_t pieces = static_cast<size_t>(M) * (Np / 8);
@@ -337,8 +396,11 @@ any4_status gemm_dx(int fmt, const uint16_t* dy, const uint8_t* packed, const ui
     at += up256(static_cast<size_t>(M) * Np * 2);
     if (a.S > 1)
         a.part = reinterpret_cast<float*>(at);
-    const unsigned tiles = static_cast<unsigned>((M + BM - 1) / BM * (K / BN));
-    hipLaunchKernelGGL(k_dx, dim3(tiles, static_cast<unsigned>(a.S)), dim3(DX_THREADS), 0, stream, a);
+    const dim3 tiles(static_cast<unsigned>(shape.tiles), static_cast<unsigned>(a.S));
+    if (shape.big)
+        hipLaunchKernelGGL((k_dx<2, 4, 8>), tiles, dim3(512), 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_dx<2, 2, 4>), tiles, dim3(256), 0, stream, a);
     if (a.S > 1) {
         const size_t quads = static_cast<size_t>(M) * K / 4;
         hipLaunchKernelGGL(k_dx_sum, dim3(static_cast<unsigned>((quads + 255) / 256)), dim3(256), 0, stream, a.part, dx, a.S,

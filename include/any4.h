@@ -470,7 +470,7 @@ any4_status any4_act8_load(const int8_t* q, const float* qs, uint16_t* x, int64_
  *          bytes (any format; 0 for sizes out of range and empty ones),
  *          required; contents need not be initialised; calls that share one
  *          must be ordered.
- *   0 <= M <= 65535*64, 0 <= N < 2^26, K >= 0 and g as for any4_gemm (K/g is not
+ *   0 <= M <= 65535*64, 0 <= N <= 2^21, K >= 0 and g as for any4_gemm (K/g is not
  *   limited).  Every buffer but the workspace below 2 GiB.  M*K == 0 is a
  *   no-op; N = 0 writes dx = 0 (the other pointers may be NULL).
  *   dx, packed and workspace need 16-byte alignment, the others 2 (dy with 16

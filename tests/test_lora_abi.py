@@ -121,7 +121,7 @@ def dx(call, dy=A, packed=A, lut=A, alpha=A, beta=A, out=A, M=4, N=64, K=256, g=
 @pytest.mark.parametrize("call", CALLS)
 def test_gemm_dx_errors(call):
     for bad in (dict(M=-1), dict(N=-1), dict(K=-128), dict(g=0), dict(g=64), dict(K=384, g=256), dict(M=65535 * 64 + 1),
-                dict(M=1 << 20, K=1024), dict(M=1 << 20, N=1024), dict(N=1 << 26), dict(N=1 << 20, K=4096, g=128)):
+                dict(M=1 << 20, K=1024), dict(M=1 << 20, N=1024), dict(N=(1 << 21) + 1), dict(N=1 << 20, K=4096, g=128)):
         assert dx(call, **bad) == 2, bad
         assert any4.gemm_dx_workspace_size(**(dict(M=4, N=64, K=256, g=128) | bad)) == 0
     for name in ("dy", "packed", "alpha", "beta", "out", "ws"):
