@@ -285,15 +285,259 @@ __global__ __launch_bounds__(64 * WM * WN) void k_dx(const DxArgs p)
     }
 }
 
-// The splits' sums in order, 4 values a thread.
+// ---------------------------------------------------------------------------
+// few rows: the layer decoded on its way into the product
+// ---------------------------------------------------------------------------
+// Up to FEW_M rows the weights are the work, so they are read packed and once.
+// A wave takes 32 k (a quarter of a packed tile's columns, 16 bytes of a row)
+// and 64 rows of W a step, a row a lane.  The row's table lies in registers as
+// bytes, low and high halves apart, and v_perm looks four codes up at a time.
+// Neighbouring lanes pair their values, LDS of the wave's own turns the block
+// (no barrier), and the matrix cores multiply it with dy, whose operands come
+// straight from memory.  Eight waves: four quarters of the columns, two halves
+// of the rows, which meet in LDS at the end; further splits of the rows leave
+// fp32 partial sums.
+constexpr int FEW_M = 64;
+constexpr int FEW_THREADS = 512;
+constexpr int FEW_STRIDE = 36;       // dwords of a turned row of 64 n
+
+struct FewArgs {
+    const uint16_t* dy;     // [M][N]
+    const uint8_t* packed;
+    const uint16_t* lut;
+    const uint16_t* alpha;
+    const uint16_t* beta;
+    uint16_t* dx;
+    float* part;            // [S][M][K] or null (S = 1)
+    int M, N, K, g, S;
+};
+
+// What a lane holds of its row for one step.
+struct RowStep {
+    uint32_t code[4];
+    u32x4_t table[2];
+    uint32_t alpha, beta;
+};
+
+// The row's weights for each code, as bytes: lo[i / 4] holds the low bytes of
+// codes i .. i + 3, hi their high bytes.  (Scaling and rounding the table's 4 to
+// 16 entries costs less than doing so for each of the 32 weights.)
+template <int FMT>
+struct ByteTable {
+    static constexpr int ENTRIES = FMT == FMT_ANY2 ? 4 : FMT == FMT_ANY3 ? 8 : 16;
+    uint32_t lo[ENTRIES / 4], hi[ENTRIES / 4];
+
+    __device__ __forceinline__ explicit ByteTable(const RowStep& r)
+    {
+        const float a = bf16_to_f32(r.alpha), b = bf16_to_f32(r.beta);
+        uint32_t v[ENTRIES / 2];
+#pragma unroll
+        for (int i = 0; i < ENTRIES / 2; ++i) {
+            const uint32_t e = r.table[i / 4][i % 4];
+            const float x = FMT == FMT_INT4 ? static_cast<float>(2 * i) : __uint_as_float(e << 16);
+            const float y = FMT == FMT_INT4 ? static_cast<float>(2 * i + 1) : __uint_as_float(e & 0xffff0000u);
+            v[i] = f32_to_bf16(fmaf(a, x, b)) | f32_to_bf16(fmaf(a, y, b)) << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < ENTRIES / 4; ++i) {
+            lo[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x06040200u);
+            hi[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x07050301u);
+        }
+    }
+    // The weights of the four codes in the bytes of s: (s0, s1) and (s2, s3).
+    __device__ __forceinline__ void find(uint32_t s, uint32_t& v01, uint32_t& v23) const
+    {
+        uint32_t l, h;
+        if constexpr (FMT == FMT_ANY2) {
+            l = __builtin_amdgcn_perm(0u, lo[0], s);
+            h = __builtin_amdgcn_perm(0u, hi[0], s);
+        } else if constexpr (FMT == FMT_ANY3) {
+            l = __builtin_amdgcn_perm(lo[1], lo[0], s);
+            h = __builtin_amdgcn_perm(hi[1], hi[0], s);
+        } else {
+            const uint32_t low3 = s & 0x07070707u;
+            const uint32_t upper = __builtin_amdgcn_perm(0u, 0xff00u, s >> 3 & 0x01010101u);      // 0xff where the code is 8 .. 15
+            l = (__builtin_amdgcn_perm(lo[1], lo[0], low3) & ~upper) | (__builtin_amdgcn_perm(lo[3], lo[2], low3) & upper);
+            h = (__builtin_amdgcn_perm(hi[1], hi[0], low3) & ~upper) | (__builtin_amdgcn_perm(hi[3], hi[2], low3) & upper);
+        }
+        v01 = __builtin_amdgcn_perm(h, l, 0x05010400u);
+        v23 = __builtin_amdgcn_perm(h, l, 0x07030602u);
+    }
+};
+
+// The 32 weights of a row's slot, as bf16: of each eight k, out holds (0, 2),
+// (4, 6), (1, 3) and (5, 7).
+template <int FMT>
+__device__ __forceinline__ void decode_row(const RowStep& r, uint32_t (&out)[16])
+{
+    const ByteTable<FMT> t(r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t even, odd;      // the codes of the eight's even and odd k, one a byte
+        if constexpr (FMT == FMT_ANY2) {
+            const uint32_t w = r.code[i / 2] >> (16 * (i % 2));     // two bits each
+            even = (w & 3u) | (w & 0x30u) << 4 | (w & 0x300u) << 8 | (w & 0x3000u) << 12;
+            odd = (w >> 2 & 3u) | (w >> 2 & 0x30u) << 4 | (w >> 2 & 0x300u) << 8 | (w >> 2 & 0x3000u) << 12;
+        } else if constexpr (FMT == FMT_ANY3) {
+            // four pairs of six bits; the last four from the bytes' top bits
+            const uint32_t w = i < 3 ? r.code[i < 3 ? i : 0]
+                                     : (r.code[0] >> 6 & 0x03030303u) | (r.code[1] >> 4 & 0x0c0c0c0cu) | (r.code[2] >> 2 & 0x30303030u);
+            even = w & 0x07070707u;
+            odd = w >> 3 & 0x07070707u;
+        } else {
+            even = r.code[i] & 0x0f0f0f0fu;
+            odd = r.code[i] >> 4 & 0x0f0f0f0fu;
+        }
+        t.find(even, out[4 * i], out[4 * i + 1]);
+        t.find(odd, out[4 * i + 2], out[4 * i + 3]);
+    }
+}
+
+// 16 * MB rows of dy x 128 k a workgroup.
+template <int FMT, int MB, bool WHOLE>
+__global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
+{
+    constexpr int BYTES = FMT == FMT_ANY2 ? 8 : FMT == FMT_ANY3 ? 12 : 16;
+    __shared__ __attribute__((aligned(16))) uint32_t turned[FEW_THREADS / WAVE][32 * FEW_STRIDE];
+    __shared__ f32x4_t red[4][2 * MB][WAVE];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
+    const int quarter = w & 3, Kc = p.K / 128, chunk = blockIdx.x % Kc, m0 = blockIdx.x / Kc * (16 * MB);
+    const int steps = (p.N + 63) / 64, parts = p.S * 2, at = blockIdx.y * 2 + (w >> 2);
+    const int s0 = static_cast<int>(static_cast<int64_t>(steps) * at / parts);
+    const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (at + 1) / parts);
+    const int G = p.K / p.g, grp = (chunk * 128 + quarter * 32) / p.g;
+    const Matrix<WHOLE> dy(p.dy, static_cast<size_t>(p.M) * p.N);
+    typedef typename Matrix<WHOLE>::Piece Piece;
+
+    auto fetch = [&](int st, RowStep& r) {
+        const int n = st * 64 + lane;
+        r.alpha = r.beta = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.code[i] = 0u;
+        r.table[0] = r.table[1] = u32x4_t{0u, 0u, 0u, 0u};
+        if (n >= p.N)            // weights of 0
+            return;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+            p.packed + ((static_cast<size_t>(n / 16) * Kc + chunk) * 64 + quarter * 16 + n % 16) * BYTES);
+#pragma unroll
+        for (int i = 0; i < BYTES / 4; ++i)
+            r.code[i] = src[i];
+        r.alpha = p.alpha[static_cast<size_t>(n) * G + grp];
+        r.beta = p.beta[static_cast<size_t>(n) * G + grp];
+        if constexpr (FMT != FMT_INT4) {
+            typedef u32x4_t __attribute__((aligned(2))) table_t;
+            const table_t* l = reinterpret_cast<const table_t*>(p.lut + static_cast<size_t>(n) * 16);
+            r.table[0] = l[0];
+            if constexpr (FMT == FMT_ANY4)
+                r.table[1] = l[1];
+        }
+    };
+    f32x4_t acc[MB][2];      // [rows of dy][halves of the 32 k]
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+        acc[i][0] = acc[i][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t* own = turned[w];
+    RowStep now, next;
+    if (s0 < s1)
+        fetch(s0, now);
+    for (int st = s0; st < s1; ++st) {
+        Piece x[MB][2];
+        const bool edge = st * 64 + 64 > p.N;
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                const int m = m0 + 16 * i + c, n = st * 64 + 32 * kk + 8 * g;
+                x[i][kk] = dy.fetch(static_cast<uint32_t>(m) * p.N + n, m < p.M ? p.N - n : 0, edge);
+            }
+        if (st + 1 < s1)
+            fetch(st + 1, next);
+        uint32_t v[16];
+        decode_row<FMT>(now, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v[i]), 0xB1, 0xf, 0xf, true));
+            const int k = 8 * (i / 4) + 4 * (i & 1) + (i >> 1 & 1) + 2 * (lane & 1);
+            own[k * FEW_STRIDE + lane / 2] = lane & 1 ? __builtin_amdgcn_perm(v[i], other, 0x07060302u)
+                                                                        : __builtin_amdgcn_perm(other, v[i], 0x05040100u);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const bf16x8_t wv = *reinterpret_cast<const bf16x8_t*>(&own[(16 * b + c) * FEW_STRIDE + 16 * kk + 4 * g]);
+#pragma unroll
+                for (int i = 0; i < MB; ++i) {
+                    const int m = m0 + 16 * i + c, n = st * 64 + 32 * kk + 8 * g;
+                    const u32x4_t d = dy.finish(x[i][kk], static_cast<uint32_t>(m) * p.N + n, p.N - n, edge);
+                    acc[i][b] = mfma(wv, __builtin_bit_cast(bf16x8_t, d), acc[i][b]);
+                }
+            }
+        now = next;
+    }
+    if (w >= 4)
+#pragma unroll
+        for (int i = 0; i < 2 * MB; ++i)
+            red[quarter][i][lane] = acc[i / 2][i % 2];
+    __syncthreads();
+    if (w >= 4)
+        return;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const f32x4_t v = acc[i][b] + red[quarter][2 * i + b][lane];
+            const int m = m0 + 16 * i + c;
+            if (m >= p.M)
+                continue;
+            const size_t o = static_cast<size_t>(m) * p.K + chunk * 128 + quarter * 32 + 16 * b + 4 * g;
+            if (p.part) {
+                *reinterpret_cast<f32x4_t*>(p.part + static_cast<size_t>(blockIdx.y) * p.M * p.K + o) = v;
+            } else {
+                u32x2_t y;
+                y[0] = f32_to_bf16(v[0]) | f32_to_bf16(v[1]) << 16;
+                y[1] = f32_to_bf16(v[2]) | f32_to_bf16(v[3]) << 16;
+                *reinterpret_cast<u32x2_t*>(p.dx + o) = y;
+            }
+        }
+}
+
+template <int FMT, bool WHOLE>
+void launch_few(const FewArgs& a, int mb, hipStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>((a.M + 16 * mb - 1) / (16 * mb) * (a.K / 128)), static_cast<unsigned>(a.S));
+#define FEW(MB_) hipLaunchKernelGGL((k_dx_few<FMT, MB_, WHOLE>), grid, dim3(FEW_THREADS), 0, stream, a)
+    if (mb == 1) FEW(1);
+    else FEW(4);
+#undef FEW
+}
+
+template <int FMT>
+void launch_few(const FewArgs& a, int mb, hipStream_t stream)
+{
+    if (a.N % 8 == 0 && is_aligned(a.dy, 16))
+        launch_few<FMT, true>(a, mb, stream);
+    else
+        launch_few<FMT, false>(a, mb, stream);
+}
+
+// The splits' sums in order, 4 values a thread, eight splits' loads at a time.
 __global__ __launch_bounds__(256) void k_dx_sum(const float* __restrict__ part, uint16_t* __restrict__ dx, int S, size_t quads)
 {
     const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;
     if (i >= quads)
         return;
     f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < S; ++s)
-        v += reinterpret_cast<const f32x4_t*>(part)[s * quads + i];
+    for (int s0 = 0; s0 < S; s0 += 8) {
+        f32x4_t x[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            x[s] = s0 + s < S ? reinterpret_cast<const f32x4_t*>(part)[(s0 + s) * quads + i] : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            v += x[s];
+    }
     u32x2_t o;
     o[0] = f32_to_bf16(v[0]) | f32_to_bf16(v[1]) << 16;
     o[1] = f32_to_bf16(v[2]) | f32_to_bf16(v[3]) << 16;
@@ -313,23 +557,34 @@ __global__ __launch_bounds__(256) void k_dx_zero(uint16_t* dx, size_t octs)
 // ---------------------------------------------------------------------------
 int64_t padded(int64_t N) { return (N + STEP - 1) / STEP * STEP; }
 
-// Tiles: 256 x 256 where they fill the chip (or nearly), else 128 x 128.
+// How a product is run: decoded on the way (few rows), else 256 x 256 tiles
+// where they fill the chip (or nearly), else 128 x 128.  n is split where the
+// tiles alone leave the 256 CUs idle; the partial sums are fp32.
 struct Shape {
+    int few;                 // blocks of 16 rows of a workgroup, 0: turned first
     bool big;
     int64_t tiles;
     int S;
 };
 
-// n is split where the tiles alone leave the 256 CUs idle, at least 4 steps to
-// a split; the partial sums are fp32.
 Shape dx_shape(int64_t M, int64_t N, int64_t K)
 {
-    const int64_t big = (M + 255) / 256 * (K / 256), small = (M + 127) / 128 * (K / 128), steps = padded(N) / STEP;
-    Shape s;
-    s.big = K % 256 == 0 && big >= 192;
-    s.tiles = s.big ? big : small;
-    int64_t S = s.big ? 1 : (512 + s.tiles - 1) / s.tiles;
-    S = S < steps / 4 ? S : steps / 4;
+    const int64_t steps = padded(N) / STEP;
+    Shape s{0, false, 0, 1};
+    int64_t S;
+    if (M <= FEW_M) {
+        s.few = M <= 16 ? 1 : 4;
+        s.tiles = (M + 16 * s.few - 1) / (16 * s.few) * (K / 128);
+        // two workgroups a CU for 16 rows; one where the partial sums are larger
+        S = ((M <= 16 ? 512 : 256) + s.tiles - 1) / s.tiles;      // at least a step for both halves of its waves
+        S = S < steps / 2 ? S : steps / 2;
+    } else {
+        const int64_t big = (M + 255) / 256 * (K / 256), small = (M + 127) / 128 * (K / 128);
+        s.big = K % 256 == 0 && big >= 192;
+        s.tiles = s.big ? big : small;
+        S = s.big ? 1 : (512 + s.tiles - 1) / s.tiles;
+        S = S < steps / 4 ? S : steps / 4;      // each at least 4 steps
+    }
     s.S = static_cast<int>(S < 1 ? 1 : S > 16 ? 16 : S);
     return s;
 }
@@ -373,6 +628,21 @@ any4_status gemm_dx(int fmt, const uint16_t* dy, const uint8_t* packed, const ui
         return launch_status();
     }
     const int Np = static_cast<int>(padded(N));
+    const Shape shape = dx_shape(M, N, K);
+    const size_t quads = static_cast<size_t>(M) * K / 4;
+    const dim3 sum_grid(static_cast<unsigned>((quads + 255) / 256));
+    if (shape.few) {
+        float* part = shape.S > 1 ? static_cast<float*>(workspace) : nullptr;
+        const FewArgs f{dy, packed, lut, alpha, beta, dx, part, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K),
+                        static_cast<int>(g), shape.S};
+        if (fmt == FMT_ANY4) launch_few<FMT_ANY4>(f, shape.few, stream);
+        else if (fmt == FMT_INT4) launch_few<FMT_INT4>(f, shape.few, stream);
+        else if (fmt == FMT_ANY2) launch_few<FMT_ANY2>(f, shape.few, stream);
+        else launch_few<FMT_ANY3>(f, shape.few, stream);
+        if (part)
+            hipLaunchKernelGGL(k_dx_sum, sum_grid, dim3(256), 0, stream, part, dx, shape.S, quads);
+        return launch_status();
+    }
     char* at = static_cast<char*>(workspace);
     uint16_t* wt = reinterpret_cast<uint16_t*>(at);
     at += wt_bytes(N, K);
@@ -384,7 +654,6 @@ any4_status gemm_dx(int fmt, const uint16_t* dy, const uint8_t* packed, const ui
     else if (fmt == FMT_ANY2) TURN(FMT_ANY2);
     else TURN(FMT_ANY3);
 #undef TURN
-    const Shape shape = dx_shape(M, N, K);
     DxArgs a{dy, wt, dx, nullptr, static_cast<int>(M), static_cast<int>(K), Np, shape.S};
     if (N != Np || !is_aligned(dy, 16)) {
         uint16_t* copy = reinterpret_cast<uint16_t*>(at);
@@ -401,11 +670,8 @@ any4_status gemm_dx(int fmt, const uint16_t* dy, const uint8_t* packed, const ui
         hipLaunchKernelGGL((k_dx<2, 4, 8>), tiles, dim3(512), 0, stream, a);
     else
         hipLaunchKernelGGL((k_dx<2, 2, 4>), tiles, dim3(256), 0, stream, a);
-    if (a.S > 1) {
-        const size_t quads = static_cast<size_t>(M) * K / 4;
-        hipLaunchKernelGGL(k_dx_sum, dim3(static_cast<unsigned>((quads + 255) / 256)), dim3(256), 0, stream, a.part, dx, a.S,
-                           quads);
-    }
+    if (a.S > 1)
+        hipLaunchKernelGGL(k_dx_sum, sum_grid, dim3(256), 0, stream, a.part, dx, a.S, quads);
     return launch_status();
 }
 
@@ -417,6 +683,8 @@ size_t any4_gemm_dx_workspace_size(int64_t M, int64_t N, int64_t K, int64_t g)
 {
     if (M <= 0 || N <= 0 || K <= 0 || !dx_sizes_ok(M, N, K, g))
         return 0;
+    if (dx_shape(M, N, K).few)
+        return dx_part_bytes(M, N, K) + 256;      // never 0 where the call has work
     return wt_bytes(N, K) + up256(static_cast<size_t>(M) * padded(N) * 2) + dx_part_bytes(M, N, K);
 }
 

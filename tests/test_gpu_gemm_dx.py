@@ -61,7 +61,8 @@ def check(dx, dy, w):
 
 @pytest.mark.parametrize("fmt", ["any4", "int4", "any2", "any3"])
 @pytest.mark.parametrize("M,N,K,g", [(1, 1, 128, 128), (1, 64, 256, 256), (5, 37, 384, 128), (64, 128, 256, 128),
-                                     (129, 200, 512, 512), (300, 1000, 128, 128)])
+                                     (16, 1000, 256, 128), (100, 333, 384, 384), (129, 200, 512, 512),
+                                     (300, 1000, 128, 128)])
 def test_formats_and_odd_sizes(fmt, M, N, K, g):
     call, w = layer(fmt, N, K, g)
     dy = grad(M, N)
@@ -69,34 +70,69 @@ def test_formats_and_odd_sizes(fmt, M, N, K, g):
 
 
 @pytest.mark.parametrize("M,N,K,g", [(16, 4096, 4096, 128), (64, 4099, 1024, 1024), (1000, 2048, 1152, 128),
-                                     (513, 1024, 4096, 512), (1, 14336, 512, 128)])
+                                     (513, 1024, 4096, 512), (1, 14336, 512, 128), (3001, 200, 4096, 128),
+                                     (2999, 333, 4352, 256), (128, 4100, 2048, 256), (17, 1000, 14336, 1024)])
 def test_larger_sizes(M, N, K, g):
-    """Sums split over workgroups, ragged last tiles, padded copies of dy."""
+    """Sums split over workgroups, ragged last tiles, padded copies of dy, both
+    tile sizes and the form for few rows."""
     call, w = layer("any4", N, K, g)
     dy = grad(M, N)
     check(call(dy), dy, w)
 
 
-def test_one_hot_rows_give_the_weights():
+@pytest.mark.parametrize("fmt", ["any4", "int4", "any2", "any3"])
+@pytest.mark.parametrize("N", [100, 190])
+def test_one_hot_rows_give_the_weights(fmt, N):
     """dy = unit vectors: dx is W itself, bit for bit."""
-    call, w = layer("any4", 190, 256, 128)
-    dy = torch.eye(190, dtype=torch.bfloat16, device=gu.DEV)
+    call, w = layer(fmt, N, 256, 128)
+    dy = torch.eye(N, dtype=torch.bfloat16, device=gu.DEV)
     assert torch.equal(call(dy).double(), w)
 
 
+@pytest.mark.parametrize("M", [20, 140])
 @pytest.mark.parametrize("N", [64, 100])
-def test_rows_do_not_touch_each_other(N):
+def test_rows_do_not_touch_each_other(M, N):
     """NaN and infinities in one row of dy, also behind an odd row's end."""
     call, w = layer("any4", N, 256, 128)
-    dy = grad(140, N)
+    dy = grad(M, N)
     clean = call(dy)
     dy[7] = float("nan")
-    dy[139, 3] = float("inf")
+    dy[M - 1, 3] = float("inf")
     got = call(dy)
-    keep = torch.ones(140, dtype=torch.bool, device=gu.DEV)
-    keep[7] = keep[139] = False
+    keep = torch.ones(M, dtype=torch.bool, device=gu.DEV)
+    keep[7] = keep[M - 1] = False
     assert torch.equal(got[keep], clean[keep])
-    assert torch.isnan(got[7]).all() and not torch.isfinite(got[139]).any()
+    assert torch.isnan(got[7]).all() and not torch.isfinite(got[M - 1]).any()
+
+
+@pytest.mark.parametrize("fmt", ["any4", "any2", "any3"])
+@pytest.mark.parametrize("M", [3, 150])
+def test_table_values_of_every_kind(fmt, M):
+    """Negative zeros, subnormals, infinities and NaN in a row's table come out
+    as any4_dequant writes them."""
+    call, w = layer(fmt, 48, 256, 128)
+    inp = workloads.generic(5, 1, 48, 256, 128)
+    lut = gu.dev_b16(inp.lut)
+    lut[0, :4] = torch.tensor([-0.0, 1e-40, float("inf"), float("nan")], device=gu.DEV)
+    al, be = gu.dev_b16(inp.alpha), gu.dev_b16(inp.beta)
+    be[0] = 0
+    if fmt == "any4":
+        packed = gu.dev_u8(oracle.tile(oracle.pack(inp.idx)))
+        ref, got = any4.dequant(packed, lut, al, be, 128), None
+        run = lambda dy: any4.gemm_dx(dy, packed, lut, al, be, 128)  # noqa: E731
+    else:
+        codes = (inp.idx & (3 if fmt == "any2" else 7)).astype(np.uint8)
+        packed = gu.dev_u8(oracle.tile2(oracle.pack2(codes)) if fmt == "any2" else oracle.tile3(codes))
+        ref = (any4.any2_dequant if fmt == "any2" else any4.any3_dequant)(packed, lut, al, be, 128)
+        run = lambda dy: (any4.any2_gemm_dx if fmt == "any2" else any4.any3_gemm_dx)(dy, packed, lut, al, be, 128)  # noqa: E731
+    dy = torch.zeros((M, 48), dtype=torch.bfloat16, device=gu.DEV)
+    dy[0, 0] = 1.0
+    dy[1:, 1] = 1.0
+    got = run(dy)
+    want = ref[0].float() + 0.0             # a sum with zeros: -0 becomes 0
+    same = (got[0].float() == want) | (torch.isnan(got[0]) & torch.isnan(want))
+    # a zero times an infinity or NaN of row 0 reaches the other rows' sums
+    assert same.all() and torch.isfinite(got[1:, torch.isfinite(ref[0])]).all()
 
 
 def test_unaligned_rows_and_caller_buffers():
