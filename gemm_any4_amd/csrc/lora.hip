@@ -419,6 +419,21 @@ __device__ __forceinline__ u32x2_t quantise8(u32x4_t v, float inv)
     return q;
 }
 
+// The 128 channels of a row that four lanes (g = 0 .. 3, 16 apart) hold, 8 at
+// 32 i + 8 g each: q and scale are where the first of them go, q at this lane's 8 g.
+__device__ __forceinline__ void store_row8(const u32x4_t (&v)[4], uint8_t* q, float* scale, int g)
+{
+    uint32_t top = max(max(abs_max(v[0]), abs_max(v[1])), max(abs_max(v[2]), abs_max(v[3])));
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+    const Scale8 e = scale8(top);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x2_t*>(q + 32 * i) = quantise8(v[i], e.inv);
+    if (g == 0)
+        *scale = e.unit;
+}
+
 // Signed byte i of v as fp32.
 __device__ __forceinline__ float byte_to_f32(uint32_t v, int i)
 {
@@ -546,19 +561,8 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
             for (int i = 0; i < 4; ++i)      // steps of 32 leave an odd start odd
                 v[i] = in.finish(vp[s][i], row[s], p.D - (d0 + 32 * i + 8 * g), edge);
             if constexpr (Q8) {
-                if (blockIdx.z == 0 && 16 * s + c < tile.count) {
-                    // the four lanes of a row hold its 128 channels
-                    uint32_t top = max(max(abs_max(v[0]), abs_max(v[1])), max(abs_max(v[2]), abs_max(v[3])));
-                    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
-                    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-                    const Scale8 e = scale8(top);
-                    uint8_t* o = p.q + row[s] + st * 128;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<u32x2_t*>(o + 32 * i) = quantise8(v[i], e.inv);
-                    if (g == 0)
-                        p.qs[row[s] / GROUP8 + st] = e.unit;
-                }
+                if (blockIdx.z == 0 && 16 * s + c < tile.count)
+                    store_row8(v, p.q + row[s] + d0, p.qs + row[s] / GROUP8 + st, g);
             }
 #pragma unroll
             for (int t = 0; t < RB; ++t)
@@ -652,6 +656,45 @@ __device__ __forceinline__ void mul_columns(f32x4_t (&acc)[8], const Split3& a, 
     mul_column<5>(acc, a, R);
     mul_column<6>(acc, a, R);
     mul_column<7>(acc, a, R);
+}
+
+// 16 rows x the wave's 128 columns: c from LDS ([16][32 * RK + 4]), W and the
+// base rows in registers.
+template <int RK, bool WHOLE>
+__device__ __forceinline__ void expand16(const float* cs, const u32x4_t (&W)[RK][8],
+                                         const typename Matrix<WHOLE>::Piece (&yp)[4], const int* rows, int count, float after,
+                                         const Matrix<WHOLE>& base, const Matrix<WHOLE>& out, int D, int d, bool edge)
+{
+    constexpr int STRIDE = 32 * RK + 4;
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    f32x4_t acc[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+        acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < RK; ++k) {
+        float f[8];
+        const f32x4_t* src = reinterpret_cast<const f32x4_t*>(cs + c * STRIDE + 32 * k + 8 * g);
+        const f32x4_t f0 = src[0], f1 = src[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f[e] = f0[e];
+            f[4 + e] = f1[e];
+        }
+        mul_columns(acc, split3(f), W[k]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = 4 * g + i;
+        const uint32_t at = static_cast<uint32_t>(rows[m]) * D + d;
+        const u32x4_t y = base.finish(yp[i], at, D - d, edge);
+        u32x4_t o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[e] = f32_to_bf16(fmaf(after, acc[2 * e][i], bf16_to_f32(y[e] & 0xffffu))) |
+                   f32_to_bf16(fmaf(after, acc[2 * e + 1][i], bf16_to_f32(y[e] >> 16))) << 16;
+        out.store(at, o, m < count ? D - d : 0, edge);
+    }
 }
 
 template <int T, int RK, bool SCALED, bool WHOLE>
@@ -755,36 +798,171 @@ __global__ __launch_bounds__(EXPAND_THREADS) void k_expand(const ExpandArgs p)
     for (int s = 0; s < MS; ++s) {
         if (16 * s >= tile.count)
             break;
-        f32x4_t acc[8];
+        expand16<RK, WHOLE>(cs + 16 * s * STRIDE, W, yp[s], rows + 16 * s, tile.count - 16 * s, SCALED ? 1.0f : scale, base, out,
+                            p.D, d, edge);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// both at once, for batches of a few rows
+// ---------------------------------------------------------------------------
+// Each workgroup works out its tile's c for itself (its eight waves share the
+// first product's d out, their sums meet in LDS) and goes on to 1024 columns of
+// the second, whose W and base rows it asked for at the start.  The first
+// product is repeated for every 1024 columns, from the caches; that is cheaper
+// than a second launch while its W is small (one_launch() has the rule).
+struct SmallArgs {
+    Batch b;
+    const uint16_t* in;       // [M][D1]
+    const uint16_t* w1;       // [L][r][D1]
+    const uint16_t* w2;       // [L][r][D2]
+    const float* scale;
+    const uint16_t* base;     // [M][D2] or null (0)
+    uint16_t* out;            // [M][D2] or null (only c is wanted)
+    float* c;                 // [M][r] or null
+    uint8_t* q;               // as in ShrinkArgs (D1 % 128 == 0)
+    float* qs;
+    int D1, D2, r;
+    bool scaled;              // c takes the scale (dh), else the sum over j does (y)
+};
+
+constexpr int SMALL_THREADS = 512;
+constexpr int SMALL_WAVES = SMALL_THREADS / WAVE;
+constexpr int SMALL_COLS = 128 * SMALL_WAVES;
+
+template <int RB, bool WHOLE1, bool WHOLE2>
+__global__ __launch_bounds__(SMALL_THREADS) void k_small(const SmallArgs p)
+{
+    constexpr int RK = (RB + 1) / 2, STRIDE = 32 * RK + 4;
+    __shared__ int own[SMALL_WAVES][SMALL_T];
+    __shared__ f32x4_t red[SMALL_WAVES][RB][WAVE];
+    __shared__ __attribute__((aligned(16))) float cs[SMALL_T * STRIDE];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
+    const Tile tile = find_tile<SMALL_T>(p.b, blockIdx.y, own[w]);
+    const bool first = blockIdx.x == 0;
+    if (tile.a == -2)
+        return;
+    const int d0 = blockIdx.x * SMALL_COLS + w * 128, d = d0 + 8 * c;
+    const bool edge2 = d0 + 128 > p.D2;
+    const Matrix<WHOLE2> base(p.base, static_cast<size_t>(p.b.M) * p.D2), out(p.out, static_cast<size_t>(p.b.M) * p.D2);
+    const Matrix<WHOLE2> w2(p.w2, static_cast<size_t>(p.b.L) * p.r * p.D2);
+    typename Matrix<WHOLE2>::Piece wp[RK][8], yp[4];
+    const int a = tile.a < 0 ? 0 : tile.a;
+    const uint32_t at2 = static_cast<uint32_t>(a * p.r) * p.D2 + d;
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-            acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < 4; ++i) {
+        const int m = 4 * g + i;
+        yp[i] = base.fetch(static_cast<uint32_t>(tile.rows[m]) * p.D2 + d, p.base && m < tile.count ? p.D2 - d : 0, edge2);
+    }
 #pragma unroll
-        for (int k = 0; k < RK; ++k) {
-            float f[8];
-            const f32x4_t* src = reinterpret_cast<const f32x4_t*>(&cs[(16 * s + c) * STRIDE + 32 * k + 8 * g]);
-            const f32x4_t f0 = src[0], f1 = src[1];
+    for (int k = 0; k < RK; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                f[e] = f0[e];
-                f[4 + e] = f1[e];
-            }
-            mul_columns(acc, split3(f), W[k]);
+        for (int u = 0; u < 8; ++u) {
+            const int j = 32 * k + 8 * g + u;
+            wp[k][u] = w2.fetch(at2 + j * p.D2, p.out && tile.a >= 0 && j < p.r ? p.D2 - d : 0, edge2);
         }
-        const float after = SCALED ? 1.0f : scale;
+    const float scale = p.scale[a];
+
+    f32x4_t acc[RB];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = 16 * s + 4 * g + i;
-            const uint32_t at = static_cast<uint32_t>(rows[m]) * p.D + d;
-            const u32x4_t y = base.finish(yp[s][i], at, p.D - d, edge);
-            u32x4_t o;
+    for (int t = 0; t < RB; ++t)
+        acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const bool quant = p.q && first;
+    if (tile.a >= 0 || quant) {
+        const Matrix<WHOLE1> in(p.in, static_cast<size_t>(p.b.M) * p.D1);
+        const Matrix<WHOLE1> w1(p.w1, static_cast<size_t>(p.b.L) * p.r * p.D1);
+        typedef typename Matrix<WHOLE1>::Piece Piece;
+        const uint32_t row = static_cast<uint32_t>(tile.rows[c]) * p.D1 + 8 * g;
+        uint32_t wrow[RB];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[e] = f32_to_bf16(fmaf(after, acc[2 * e][i], bf16_to_f32(y[e] & 0xffffu))) |
-                       f32_to_bf16(fmaf(after, acc[2 * e + 1][i], bf16_to_f32(y[e] >> 16))) << 16;
-            out.store(at, o, m < tile.count ? p.D - d : 0, edge);
+        for (int t = 0; t < RB; ++t) {     // ranks behind the last read that one again
+            const int j = 16 * t + c;
+            wrow[t] = static_cast<uint32_t>(a * p.r + (j < p.r ? j : p.r - 1)) * p.D1 + 8 * g;
+        }
+        const int steps = (p.D1 + 127) / 128;
+        auto fetch = [&](int st, Piece (&x)[4], Piece (&v)[RB][4]) {
+            const int o = st * 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int valid = p.D1 - (o + 32 * i + 8 * g);
+                x[i] = in.fetch(row + o + 32 * i, valid, o + 128 > p.D1);
+#pragma unroll
+                for (int t = 0; t < RB; ++t)
+                    v[t][i] = w1.fetch(wrow[t] + o + 32 * i, valid, o + 128 > p.D1);
+            }
+        };
+        auto use = [&](int st, const Piece (&xp)[4], const Piece (&vp)[RB][4]) {
+            const int o = st * 128;
+            u32x4_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i] = in.finish(xp[i], row, p.D1 - (o + 32 * i + 8 * g), o + 128 > p.D1);
+            if (quant && c < tile.count)
+                store_row8(x, p.q + row + o, p.qs + row / GROUP8 + st, g);
+#pragma unroll
+            for (int t = 0; t < RB; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[t] = mfma(__builtin_bit_cast(bf16x8_t, x[i]),
+                                  __builtin_bit_cast(bf16x8_t, w1.finish(vp[t][i], wrow[t], p.D1 - (o + 32 * i + 8 * g), o + 128 > p.D1)),
+                                  acc[t]);
+        };
+        // as many steps' loads at once as fit the registers (K = 4096, rank 16: all)
+        constexpr int DEPTH = RB == 1 ? 4 : RB == 2 ? 2 : 1;
+        Piece x[DEPTH][4], v[DEPTH][RB][4];
+        for (int st = w; st < steps; st += DEPTH * SMALL_WAVES) {
+#pragma unroll
+            for (int e = 0; e < DEPTH; ++e)
+                if (st + e * SMALL_WAVES < steps)
+                    fetch(st + e * SMALL_WAVES, x[e], v[e]);
+#pragma unroll
+            for (int e = 0; e < DEPTH; ++e)
+                if (st + e * SMALL_WAVES < steps)
+                    use(st + e * SMALL_WAVES, x[e], v[e]);
         }
     }
+#pragma unroll
+    for (int t = 0; t < RB; ++t)
+        red[w][t][lane] = acc[t];
+    __syncthreads();
+    if (w < 2 * RK) {          // 16 ranks a wave; zeros where there are none
+        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (w < RB)
+#pragma unroll
+            for (int o = 0; o < SMALL_WAVES; ++o)
+                v += red[o][w < RB ? w : 0][lane];
+        const int j = 16 * w + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = 4 * g + i;
+            float f = j < p.r && m < tile.count && tile.a >= 0 ? v[i] : 0.0f;
+            if (p.scaled && tile.a >= 0)
+                f *= scale;
+            cs[m * STRIDE + j] = f;
+            if (p.c && first && j < p.r && m < tile.count)
+                p.c[static_cast<size_t>(tile.rows[m]) * p.r + j] = f;
+        }
+    }
+    __syncthreads();
+    if (!p.out || d0 >= p.D2)     // waves leave whole: every lane holds matrix-core operands
+        return;
+    if (tile.a < 0) {             // rows without an adapter: the base as it is
+        if (p.out != p.base)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = 4 * g + i;
+                const uint32_t at = static_cast<uint32_t>(tile.rows[m]) * p.D2 + d;
+                out.store(at, base.finish(yp[i], at, p.D2 - d, edge2), m < tile.count ? p.D2 - d : 0, edge2);
+            }
+        return;
+    }
+    u32x4_t W[RK][8];
+#pragma unroll
+    for (int k = 0; k < RK; ++k)
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            W[k][u] = w2.finish(wp[k][u], at2 + (32 * k + 8 * g + u) * p.D2, p.D2 - d, edge2);
+    expand16<RK, WHOLE2>(cs, W, yp, tile.rows, tile.count, p.scaled ? 1.0f : scale, base, out, p.D2, d, edge2);
 }
 
 // ---------------------------------------------------------------------------
@@ -1095,6 +1273,30 @@ void launch_expand(const ExpandArgs& e, int64_t tiles, bool scaled, hipStream_t 
         launch_expand_as<false, false>(e, tiles, stream);
 }
 
+// Whether a few rows' two products go in one launch: the first one's W, read by
+// every workgroup at 64 bytes a clock, takes at most about two microseconds.
+bool one_launch(int64_t M, int64_t D1, int64_t r) { return M <= SMALL_M && r <= 64 && D1 * r <= 64 * 1024; }
+
+void launch_small(const SmallArgs& a, int64_t tiles, hipStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>(a.out ? (a.D2 + SMALL_COLS - 1) / SMALL_COLS : 1), static_cast<unsigned>(tiles));
+    const bool whole1 = a.D1 % 8 == 0 && is_aligned(a.in, 16) && is_aligned(a.w1, 16);
+    const bool whole2 = a.D2 % 8 == 0 && is_aligned(a.base, 16) && is_aligned(a.out, 16) && is_aligned(a.w2, 16);
+#define SMALL_AS(RB_, W1_, W2_) hipLaunchKernelGGL((k_small<RB_, W1_, W2_>), grid, dim3(SMALL_THREADS), 0, stream, a)
+#define SMALL_RB(W1_, W2_)                      \
+    do {                                        \
+        if (a.r <= 16) SMALL_AS(1, W1_, W2_);   \
+        else if (a.r <= 32) SMALL_AS(2, W1_, W2_); \
+        else SMALL_AS(4, W1_, W2_);             \
+    } while (0)
+    if (whole1 && whole2) SMALL_RB(true, true);
+    else if (whole1) SMALL_RB(true, false);
+    else if (whole2) SMALL_RB(false, true);
+    else SMALL_RB(false, false);
+#undef SMALL_RB
+#undef SMALL_AS
+}
+
 template <bool WHOLE>
 void launch_wgrad(const WgradArgs& a, hipStream_t stream)
 {
@@ -1148,7 +1350,7 @@ any4_status any4_lora_plan(const int32_t* ids, void* plan, size_t bytes, int64_t
 
 size_t any4_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L)
 {
-    if (M <= 0 || !sizes_ok(M, N, K, r, L))
+    if (M <= 0 || !sizes_ok(M, N, K, r, L) || one_launch(M, K, r))
         return 0;
     return part_bytes(M, L, K, r) + (M <= SMALL_M ? 0 : plan_bytes(M, L));
 }
@@ -1162,13 +1364,14 @@ any4_status any4_lora(const uint16_t* x, const uint16_t* A, const uint16_t* B, c
         return ANY4_E_SHAPE;
     if (M == 0)
         return ANY4_OK;
-    if (!x || !A || !scale || !ids || (N > 0 && (!B || !y || !out)) || (!q != !qs) || !workspace)
+    const size_t need = any4_lora_workspace_size(M, N, K, r, L);
+    if (!x || !A || !scale || !ids || (N > 0 && (!B || !y || !out)) || (!q != !qs) || (need && !workspace))
         return ANY4_E_NULL;
     if (!is_aligned(x, 16) || !is_aligned(A, 16) || !is_aligned(B, 2) || !is_aligned(y, 2) || !is_aligned(out, 2) ||
         !is_aligned(scale, 4) || !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(h, 4) ||
         !is_aligned(q, 16) || !is_aligned(qs, 4) || !is_aligned(workspace, 16))
         return ANY4_E_ALIGN;
-    if (workspace_bytes < any4_lora_workspace_size(M, N, K, r, L))
+    if (workspace_bytes < need)
         return ANY4_E_WORKSPACE;
     (void)hipGetLastError();
     float* part = static_cast<float*>(workspace);
@@ -1183,6 +1386,11 @@ any4_status any4_lora(const uint16_t* x, const uint16_t* A, const uint16_t* B, c
     }
     const int r16 = round16(r), SK = split_of(M, L, K, r);
     const int64_t tiles = tile_bound(M, L);
+    if (one_launch(M, K, r)) {
+        launch_small(SmallArgs{b, x, A, B, scale, y, N > 0 ? out : nullptr, h, reinterpret_cast<uint8_t*>(q), qs,
+                               static_cast<int>(K), static_cast<int>(N), static_cast<int>(r), false}, tiles, stream);
+        return launch_status();
+    }
     const ShrinkArgs s{b, x, A, part, reinterpret_cast<uint8_t*>(q), qs, static_cast<int>(K), static_cast<int>(r), r16, SK};
     launch_shrink(s, tiles, stream);
     const ExpandArgs e{b, part, B, scale, y, N > 0 ? out : nullptr, h, nullptr, nullptr, static_cast<int>(N), static_cast<int>(r), r16, SK};
@@ -1235,11 +1443,14 @@ any4_status any4_lora_backward(const uint16_t* dy, const uint16_t* x, const int8
     const int64_t tiles = tile_bound(M, L);
     const bool small = M <= SMALL_M, need_dh = dx_out || dA;
     const int64_t places = tiles * TILE_T;
-    if (need_dh) {
+    if (need_dh && one_launch(M, N, r)) {
+        launch_small(SmallArgs{b, dy, B, A, scale, dx, dx_out, factors, nullptr, nullptr, static_cast<int>(N),
+                               static_cast<int>(K), static_cast<int>(r), true}, tiles, stream);
+    } else if (need_dh) {
         const ShrinkArgs s{b, dy, B, part, nullptr, nullptr, static_cast<int>(N), static_cast<int>(r), r16, SK};
         launch_shrink(s, tiles, stream);
     }
-    if (need_dh || (dB && !small)) {      // without dh: only h is turned
+    if ((need_dh && !one_launch(M, N, r)) || (dB && !small)) {      // without dh: only h is turned
         const ExpandArgs e{b, part, A, scale, dx, dx_out, small ? factors : nullptr, dB ? h : nullptr,
                            small || (!dA && !dB) ? nullptr : factors, static_cast<int>(K), static_cast<int>(r), r16, need_dh ? SK : 0};
         launch_expand(e, tiles, true, stream);

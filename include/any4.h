@@ -398,8 +398,9 @@ any4_status any4_lora_plan(const int32_t* ids, void* plan, size_t bytes, int64_t
  *   q, qs  device, x in 8 bits as any4_act8_save writes it, in the same pass
  *          over x (rows without an adapter too); or both NULL.
  *   workspace  device, 16-byte aligned, any4_lora_workspace_size(M, N, K, r, L)
- *          bytes (0 for sizes out of range and M = 0), required; contents need
- *          not be initialised; calls that share one must be ordered.
+ *          bytes, required where that is not 0 (it is 0 where the call needs
+ *          none, for M = 0 and for sizes out of range); contents need not be
+ *          initialised; calls that share one must be ordered.
  *   M = 0 is a no-op; N = 0 only writes h, q and qs (B, y, out may be NULL).
  *   x, A, plan, q and workspace need 16-byte alignment, the others that of
  *   their elements.

@@ -345,7 +345,8 @@ def test_refusals():
     refused(ValueError, ids=t["ids"][:7])
     refused(ValueError, h=torch.empty((8, 5), device=gu.DEV))
     refused(ValueError, workspace=torch.empty(64, dtype=torch.uint8))
-    refused(RuntimeError, workspace=torch.empty(64, dtype=torch.uint8, device=gu.DEV))
+    more = {k: v for k, v in make(80, 128, 16, 4, 2, "mixed").items() if k in a}
+    refused(RuntimeError, workspace=torch.empty(64, dtype=torch.uint8, device=gu.DEV), **more)
     refused(TypeError, plan=torch.empty(64, dtype=torch.int32, device=gu.DEV))
     refused(ValueError, plan=any4.lora_plan(t["ids"], 3))
     refused(RuntimeError, x=t["x"][:, :64].contiguous(), A=t["A"][:, :, :64].contiguous())   # K % 128
