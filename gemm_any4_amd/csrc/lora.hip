@@ -144,7 +144,8 @@ __device__ __forceinline__ int chunks_of(int rows) { return (rows + CHUNK - 1) /
 // From cnt[part][L+1] (rows of each adapter in each part of the batch): the
 // plan's tables, s_rows and s_tile (rows and first tile of each adapter), and
 // cnt turned into the number of the adapter's rows in earlier parts.
-__device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, int* plan, int* s_rows,
+template <int PARTS>
+__device__ __forceinline__ void plan_tables(int* cnt, int M, int L, int* plan, int* s_rows,
                                             int* s_tile, int* s_chunk, int (*wave_sum)[4])
 {
     const PlanLayout p(M, L);
@@ -155,10 +156,16 @@ __device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, i
         if (a > L)
             break;
         int n = 0;
-        for (int q = 0; q < parts; ++q) {
-            const int c = cnt[static_cast<size_t>(q) * (L + 1) + a];
-            cnt[static_cast<size_t>(q) * (L + 1) + a] = n;
-            n += c;
+        for (int q0 = 0; q0 < PARTS; q0 += 16) {     // sixteen reads, then the writes
+            int c[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                c[q] = cnt[static_cast<size_t>(q0 + q) * (L + 1) + a];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                cnt[static_cast<size_t>(q0 + q) * (L + 1) + a] = n;
+                n += c[q];
+            }
         }
         const int ch = a < L ? chunks_of(n) : 0;
         s_rows[a] = n;
@@ -239,7 +246,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan(const int* __restrict__ i
         at[i] = count_rows(a[i], m0 + i * WAVE < M, cnt + w * (L + 1));
     }
     __syncthreads();
-    plan_tables(cnt, PLAN_WAVES, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
+    plan_tables<PLAN_WAVES>(cnt, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
     int* rows = plan + PlanLayout(M, L).rows;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
@@ -266,7 +273,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan_tables(int* cnt, int* pla
 {
     __shared__ int s_rows[MAX_ADAPTERS + 2], s_tile[MAX_ADAPTERS + 2], s_chunk[MAX_ADAPTERS + 2];
     __shared__ int wave_sum[PLAN_WAVES][4];
-    plan_tables(cnt, PLAN_PARTS, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
+    plan_tables<PLAN_PARTS>(cnt, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
 }
 
 __global__ __launch_bounds__(WAVE) void k_plan_place(const int* __restrict__ ids, int* cnt, int* plan, int M, int L, int per)
@@ -295,8 +302,10 @@ void launch_plan(const int32_t* ids, int32_t* plan, int64_t M, int64_t L, hipStr
 {
     const int m = static_cast<int>(M), l = static_cast<int>(L);
     if (plan_in_one(M, L)) {
-        if (M <= PLAN_ONE_M / 4)
-            hipLaunchKernelGGL(k_plan<PLAN_ONE_M / 4 / PLAN_THREADS>, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
+        if (M <= 2 * PLAN_THREADS)
+            hipLaunchKernelGGL(k_plan<2>, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
+        else if (M <= 4 * PLAN_THREADS)
+            hipLaunchKernelGGL(k_plan<4>, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
         else
             hipLaunchKernelGGL(k_plan<PLAN_ONE_M / PLAN_THREADS>, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
         return;
@@ -420,16 +429,39 @@ __device__ __forceinline__ u32x2_t quantise8(u32x4_t v, float inv)
 }
 
 // The 128 channels of a row that four lanes (g = 0 .. 3, 16 apart) hold, 8 at
-// 32 i + 8 g each: q and scale are where the first of them go, q at this lane's 8 g.
-__device__ __forceinline__ void store_row8(const u32x4_t (&v)[4], uint8_t* q, float* scale, int g)
+// 32 i + 8 g each: q and scale are where the first of them go.  The lanes trade
+// their 8-byte pieces (a 4 x 4 transposition in two rounds of swaps between
+// rows of 16 lanes), so that each stores 32 bytes in one place.
+__device__ __forceinline__ void store_row8(const u32x4_t (&v)[4], uint8_t* q, float* scale, int g, bool live)
 {
     uint32_t top = max(max(abs_max(v[0]), abs_max(v[1])), max(abs_max(v[2]), abs_max(v[3])));
     top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
     top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
     const Scale8 e = scale8(top);
+    u32x2_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<u32x2_t*>(q + 32 * i) = quantise8(v[i], e.inv);
+        o[i] = quantise8(v[i], e.inv);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const auto s = __builtin_amdgcn_permlane32_swap(o[i][b], o[i + 2][b], false, false);
+            o[i][b] = s[0];
+            o[i + 2][b] = s[1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const auto s = __builtin_amdgcn_permlane16_swap(o[i][b], o[i + 1][b], false, false);
+            o[i][b] = s[0];
+            o[i + 1][b] = s[1];
+        }
+    }
+    if (!live)
+        return;
+    u32x4_t* to = reinterpret_cast<u32x4_t*>(q + 32 * g);
+    to[0] = u32x4_t{o[0][0], o[0][1], o[1][0], o[1][1]};
+    to[1] = u32x4_t{o[2][0], o[2][1], o[3][0], o[3][1]};
     if (g == 0)
         *scale = e.unit;
 }
@@ -561,8 +593,8 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
             for (int i = 0; i < 4; ++i)      // steps of 32 leave an odd start odd
                 v[i] = in.finish(vp[s][i], row[s], p.D - (d0 + 32 * i + 8 * g), edge);
             if constexpr (Q8) {
-                if (blockIdx.z == 0 && 16 * s + c < tile.count)
-                    store_row8(v, p.q + row[s] + d0, p.qs + row[s] / GROUP8 + st, g);
+                if (blockIdx.z == 0)
+                    store_row8(v, p.q + row[s] - 8 * g + d0, p.qs + row[s] / GROUP8 + st, g, 16 * s + c < tile.count);
             }
 #pragma unroll
             for (int t = 0; t < RB; ++t)
@@ -572,9 +604,10 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
         }
     };
     // two steps in registers where they fit: the next one's loads are on their
-    // way while this one is multiplied (4096 x 14336, rank 16: 42 -> 32 us)
+    // way while this one is multiplied (4096 x 14336, rank 16: 42 -> 32 us; with
+    // the 8-bit copy a second workgroup a CU is worth more: 53 -> 50 us)
     Piece v0[MS][4], w0[RB][4];
-    if constexpr (MS * RB <= 4 || (WHOLE && !Q8)) {
+    if constexpr (!Q8 && (WHOLE || MS * RB <= 4)) {
         Piece v1[MS][4], w1[RB][4];
         if (s0 < s1)
             fetch(s0, v0, w0);
@@ -897,8 +930,8 @@ __global__ __launch_bounds__(SMALL_THREADS) void k_small(const SmallArgs p)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 x[i] = in.finish(xp[i], row, p.D1 - (o + 32 * i + 8 * g), o + 128 > p.D1);
-            if (quant && c < tile.count)
-                store_row8(x, p.q + row + o, p.qs + row / GROUP8 + st, g);
+            if (quant)
+                store_row8(x, p.q + row - 8 * g + o, p.qs + row / GROUP8 + st, g, c < tile.count);
 #pragma unroll
             for (int t = 0; t < RB; ++t)
 #pragma unroll
