@@ -16,36 +16,143 @@ enum { FMT_ANY4, FMT_INT4, FMT_ANY2, FMT_ANY3 };
 constexpr int STEP = 64;             // n of one step of the product; W^T rows are padded to it
 
 // ---------------------------------------------------------------------------
-// W^T
+// a row's weights
 // ---------------------------------------------------------------------------
-constexpr int DT_THREADS = 256;
-constexpr int DT_STRIDE = 36;        // dwords of a staged row of 64 n
+// The row's table lies in registers as bytes, low and high halves apart, and
+// v_perm looks four codes up at a time.
+// What a lane holds of its row for 32 k.
+struct RowStep {
+    uint32_t code[4];
+    u32x4_t table[2];
+    uint32_t alpha, beta;
+};
+
+// The slot of row n, k 128 * chunk + 32 * quarter + 0 .. 31; a row n >= N has
+// weights of 0.
+template <int FMT>
+__device__ __forceinline__ RowStep fetch_row(const uint8_t* packed, const uint16_t* lut, const uint16_t* alpha,
+                                             const uint16_t* beta, int n, int N, int Kc, int chunk, int quarter, int g)
+{
+    constexpr int BYTES = FMT == FMT_ANY2 ? 8 : FMT == FMT_ANY3 ? 12 : 16;
+    RowStep r;
+    r.alpha = r.beta = 0u;
+    r.code[0] = r.code[1] = r.code[2] = r.code[3] = 0u;
+    r.table[0] = r.table[1] = u32x4_t{0u, 0u, 0u, 0u};
+    if (n >= N)
+        return r;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        packed + ((static_cast<size_t>(n / 16) * Kc + chunk) * 64 + quarter * 16 + n % 16) * BYTES);
+#pragma unroll
+    for (int i = 0; i < BYTES / 4; ++i)
+        r.code[i] = src[i];
+    const size_t grp = static_cast<size_t>(n) * (Kc * 128 / g) + (chunk * 128 + quarter * 32) / g;
+    r.alpha = alpha[grp];
+    r.beta = beta[grp];
+    if constexpr (FMT != FMT_INT4) {
+        typedef u32x4_t __attribute__((aligned(2))) table_t;
+        const table_t* l = reinterpret_cast<const table_t*>(lut + static_cast<size_t>(n) * 16);
+        r.table[0] = l[0];
+        if constexpr (FMT == FMT_ANY4)
+            r.table[1] = l[1];
+    }
+    return r;
+}
+
+// The row's weights for each code, as bytes: lo[i / 4] holds the low bytes of
+// codes i .. i + 3, hi their high bytes.  (Scaling and rounding the table's 4 to
+// 16 entries costs less than doing so for each of the 32 weights.)
+template <int FMT>
+struct ByteTable {
+    static constexpr int ENTRIES = FMT == FMT_ANY2 ? 4 : FMT == FMT_ANY3 ? 8 : 16;
+    uint32_t lo[ENTRIES / 4], hi[ENTRIES / 4];
+
+    __device__ __forceinline__ explicit ByteTable(const RowStep& r)
+    {
+        const float a = bf16_to_f32(r.alpha), b = bf16_to_f32(r.beta);
+        uint32_t v[ENTRIES / 2];
+#pragma unroll
+        for (int i = 0; i < ENTRIES / 2; ++i) {
+            const uint32_t e = r.table[i / 4][i % 4];
+            const float x = FMT == FMT_INT4 ? static_cast<float>(2 * i) : __uint_as_float(e << 16);
+            const float y = FMT == FMT_INT4 ? static_cast<float>(2 * i + 1) : __uint_as_float(e & 0xffff0000u);
+            v[i] = f32_to_bf16(fmaf(a, x, b)) | f32_to_bf16(fmaf(a, y, b)) << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < ENTRIES / 4; ++i) {
+            lo[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x06040200u);
+            hi[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x07050301u);
+        }
+    }
+    // The weights of the four codes in the bytes of s: (s0, s1) and (s2, s3).
+    __device__ __forceinline__ void find(uint32_t s, uint32_t& v01, uint32_t& v23) const
+    {
+        uint32_t l, h;
+        if constexpr (FMT == FMT_ANY2) {
+            l = __builtin_amdgcn_perm(0u, lo[0], s);
+            h = __builtin_amdgcn_perm(0u, hi[0], s);
+        } else if constexpr (FMT == FMT_ANY3) {
+            l = __builtin_amdgcn_perm(lo[1], lo[0], s);
+            h = __builtin_amdgcn_perm(hi[1], hi[0], s);
+        } else {
+            const uint32_t low3 = s & 0x07070707u;
+            const uint32_t upper = __builtin_amdgcn_perm(0u, 0xff00u, s >> 3 & 0x01010101u);      // 0xff where the code is 8 .. 15
+            l = (__builtin_amdgcn_perm(lo[1], lo[0], low3) & ~upper) | (__builtin_amdgcn_perm(lo[3], lo[2], low3) & upper);
+            h = (__builtin_amdgcn_perm(hi[1], hi[0], low3) & ~upper) | (__builtin_amdgcn_perm(hi[3], hi[2], low3) & upper);
+        }
+        v01 = __builtin_amdgcn_perm(h, l, 0x05010400u);
+        v23 = __builtin_amdgcn_perm(h, l, 0x07030602u);
+    }
+};
+
+// The 32 weights of a row's slot, as bf16: of each eight k, out holds (0, 2),
+// (4, 6), (1, 3) and (5, 7): first_k(i) and two on.
+__device__ __forceinline__ constexpr int first_k(int i) { return 8 * (i / 4) + 4 * (i & 1) + (i >> 1 & 1); }
 
 template <int FMT>
-__device__ __forceinline__ uint32_t code_pair(const uint32_t (&p)[4], int i)
+__device__ __forceinline__ void decode_row(const RowStep& r, uint32_t (&out)[16])
 {
-    // codes 2i (low half) and 2i + 1 (high half) of a lane's 32
-    if constexpr (FMT == FMT_ANY2) {
-        const uint32_t b = p[i / 8] >> (4 * (i % 8));
-        return (b & 3u) | (b & 12u) << 14;
-    } else if constexpr (FMT == FMT_ANY3) {
-        uint32_t b;
-        if (i < 12) {
-            b = p[i / 4] >> (8 * (i % 4));
+    const ByteTable<FMT> t(r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t even, odd;      // the codes of the eight's even and odd k, one a byte
+        if constexpr (FMT == FMT_ANY2) {
+            const uint32_t w = r.code[i / 2] >> (16 * (i % 2));     // two bits each
+            even = (w & 3u) | (w & 0x30u) << 4 | (w & 0x300u) << 8 | (w & 0x3000u) << 12;
+            odd = (w >> 2 & 3u) | (w >> 2 & 0x30u) << 4 | (w >> 2 & 0x300u) << 8 | (w >> 2 & 0x3000u) << 12;
+        } else if constexpr (FMT == FMT_ANY3) {
+            // four pairs of six bits; the last four from the bytes' top bits
+            const uint32_t w = i < 3 ? r.code[i < 3 ? i : 0]
+                                     : (r.code[0] >> 6 & 0x03030303u) | (r.code[1] >> 4 & 0x0c0c0c0cu) | (r.code[2] >> 2 & 0x30303030u);
+            even = w & 0x07070707u;
+            odd = w >> 3 & 0x07070707u;
         } else {
-            const int s = 8 * (i - 12) + 6;      // two bits of each dword's byte i - 12
-            b = (p[0] >> s & 3u) | (p[1] >> s & 3u) << 2 | (p[2] >> s & 3u) << 4;
+            even = r.code[i] & 0x0f0f0f0fu;
+            odd = r.code[i] >> 4 & 0x0f0f0f0fu;
         }
-        return (b & 7u) | (b & 56u) << 13;
-    } else {
-        const uint32_t b = p[i / 4] >> (8 * (i % 4));
-        return (b & 15u) | (b & 240u) << 12;
+        t.find(even, out[4 * i], out[4 * i + 1]);
+        t.find(odd, out[4 * i + 2], out[4 * i + 3]);
     }
 }
 
+// Neighbouring lanes hold rows n and n + 1 of the same k: the pair of rows for
+// first_k(i) (even lanes) or two k on (odd lanes).
+__device__ __forceinline__ uint32_t pair_rows(uint32_t v, bool odd)
+{
+    const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xf, 0xf, true));
+    return odd ? __builtin_amdgcn_perm(v, other, 0x07060302u) : __builtin_amdgcn_perm(other, v, 0x05040100u);
+}
+
+// ---------------------------------------------------------------------------
+// W^T
+// ---------------------------------------------------------------------------
+constexpr int DT_THREADS = 256;
+constexpr int DT_STRIDE = 36;                          // dwords of a staged row of 64 n
+constexpr int DT_QUARTER = 32 * DT_STRIDE + 16;        // of 32 such rows: the four quarters' writes in other banks
+
 // A workgroup turns 64 rows x 128 k: each wave decodes one packed tile (a lane
 // the 32 k of one row), neighbouring lanes pair up their rows' values, and
-// the block leaves through LDS as 128-byte pieces of W^T's rows.
+// the block leaves through LDS as 128-byte pieces of W^T's rows.  Bound by its
+// writes (14336 x 4096: 29 MB read, 117 MB written).
 template <int FMT>
 __global__ __launch_bounds__(DT_THREADS) void k_dequant_t(const uint8_t* __restrict__ packed,
                                                           const uint16_t* __restrict__ lut,
@@ -53,56 +160,20 @@ __global__ __launch_bounds__(DT_THREADS) void k_dequant_t(const uint8_t* __restr
                                                           const uint16_t* __restrict__ beta,
                                                           uint16_t* __restrict__ wt, int N, int K, int g, int Np)
 {
-    constexpr int BYTES = FMT == FMT_ANY2 ? 8 : FMT == FMT_ANY3 ? 12 : 16;
-    __shared__ float table[4][16][17];
-    __shared__ __attribute__((aligned(16))) uint32_t turned[128 * DT_STRIDE];
+    __shared__ __attribute__((aligned(16))) uint32_t turned[4 * DT_QUARTER];
     const int Kc = K / 128, c = blockIdx.x % Kc, n0 = blockIdx.x / Kc * 64;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, j = lane & 15, kq = lane >> 4;
-    if constexpr (FMT != FMT_INT4) {
-        for (int i = tid; i < 1024; i += DT_THREADS) {
-            const int n = n0 + i / 16;
-            table[i / 256][i / 16 % 16][i % 16] = n < N ? bf16_to_f32(lut[static_cast<size_t>(n) * 16 + i % 16]) : 0.0f;
-        }
-        __syncthreads();
-    }
-    const int n = n0 + 16 * w + j;
     uint32_t out[16];
+    decode_row<FMT>(fetch_row<FMT>(packed, lut, alpha, beta, n0 + 16 * w + j, N, Kc, c, kq, g), out);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-        out[i] = 0u;
-    if (n < N) {
-        const int G = K / g, grp = (c * 128 + kq * 32) / g;
-        const float a = bf16_to_f32(alpha[static_cast<size_t>(n) * G + grp]);
-        const float b = bf16_to_f32(beta[static_cast<size_t>(n) * G + grp]);
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(
-            packed + ((static_cast<size_t>(n / 16) * Kc + c) * 64 + lane) * BYTES);
-        uint32_t p[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int i = 0; i < BYTES / 4; ++i)
-            p[i] = src[i];
-        const float* T = table[w][j];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t q = code_pair<FMT>(p, i);
-            const float lo = FMT == FMT_INT4 ? static_cast<float>(q & 0xffffu) : T[q & 0xffffu];
-            const float hi = FMT == FMT_INT4 ? static_cast<float>(q >> 16) : T[q >> 16];
-            out[i] = f32_to_bf16(fmaf(a, lo, b)) | f32_to_bf16(fmaf(a, hi, b)) << 16;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        // rows j and j ^ 1: the even lane takes both values of k 2i, the odd of 2i + 1
-        const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(out[i]), 0xB1, 0xf, 0xf, true));
-        const uint32_t pair = j & 1 ? __builtin_amdgcn_perm(out[i], other, 0x07060302u)
-                                    : __builtin_amdgcn_perm(other, out[i], 0x05040100u);
-        turned[(32 * kq + 2 * i + (j & 1)) * DT_STRIDE + 8 * w + j / 2] = pair;
-    }
+        turned[kq * DT_QUARTER + (first_k(i) + 2 * (j & 1)) * DT_STRIDE + 8 * w + j / 2] = pair_rows(out[i], j & 1);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int q = tid + DT_THREADS * i, k = q / 8, e = q % 8;
         *reinterpret_cast<u32x4_t*>(wt + static_cast<size_t>(c * 128 + k) * Np + n0 + 8 * e) =
-            *reinterpret_cast<const u32x4_t*>(&turned[k * DT_STRIDE + 4 * e]);
+            *reinterpret_cast<const u32x4_t*>(&turned[k / 32 * DT_QUARTER + k % 32 * DT_STRIDE + 4 * e]);
     }
 }
 
@@ -290,8 +361,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_dx(const DxArgs p)
 // ---------------------------------------------------------------------------
 // Up to FEW_M rows the weights are the work, so they are read packed and once.
 // A wave takes 32 k (a quarter of a packed tile's columns, 16 bytes of a row)
-// and 64 rows of W a step, a row a lane.  The row's table lies in registers as
-// bytes, low and high halves apart, and v_perm looks four codes up at a time.
+// and 64 rows of W a step, a row a lane.
 // Neighbouring lanes pair their values, LDS of the wave's own turns the block
 // (no barrier), and the matrix cores multiply it with dy, whose operands come
 // straight from memory.  Eight waves: four quarters of the columns, two halves
@@ -312,92 +382,10 @@ struct FewArgs {
     int M, N, K, g, S;
 };
 
-// What a lane holds of its row for one step.
-struct RowStep {
-    uint32_t code[4];
-    u32x4_t table[2];
-    uint32_t alpha, beta;
-};
-
-// The row's weights for each code, as bytes: lo[i / 4] holds the low bytes of
-// codes i .. i + 3, hi their high bytes.  (Scaling and rounding the table's 4 to
-// 16 entries costs less than doing so for each of the 32 weights.)
-template <int FMT>
-struct ByteTable {
-    static constexpr int ENTRIES = FMT == FMT_ANY2 ? 4 : FMT == FMT_ANY3 ? 8 : 16;
-    uint32_t lo[ENTRIES / 4], hi[ENTRIES / 4];
-
-    __device__ __forceinline__ explicit ByteTable(const RowStep& r)
-    {
-        const float a = bf16_to_f32(r.alpha), b = bf16_to_f32(r.beta);
-        uint32_t v[ENTRIES / 2];
-#pragma unroll
-        for (int i = 0; i < ENTRIES / 2; ++i) {
-            const uint32_t e = r.table[i / 4][i % 4];
-            const float x = FMT == FMT_INT4 ? static_cast<float>(2 * i) : __uint_as_float(e << 16);
-            const float y = FMT == FMT_INT4 ? static_cast<float>(2 * i + 1) : __uint_as_float(e & 0xffff0000u);
-            v[i] = f32_to_bf16(fmaf(a, x, b)) | f32_to_bf16(fmaf(a, y, b)) << 16;
-        }
-#pragma unroll
-        for (int i = 0; i < ENTRIES / 4; ++i) {
-            lo[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x06040200u);
-            hi[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x07050301u);
-        }
-    }
-    // The weights of the four codes in the bytes of s: (s0, s1) and (s2, s3).
-    __device__ __forceinline__ void find(uint32_t s, uint32_t& v01, uint32_t& v23) const
-    {
-        uint32_t l, h;
-        if constexpr (FMT == FMT_ANY2) {
-            l = __builtin_amdgcn_perm(0u, lo[0], s);
-            h = __builtin_amdgcn_perm(0u, hi[0], s);
-        } else if constexpr (FMT == FMT_ANY3) {
-            l = __builtin_amdgcn_perm(lo[1], lo[0], s);
-            h = __builtin_amdgcn_perm(hi[1], hi[0], s);
-        } else {
-            const uint32_t low3 = s & 0x07070707u;
-            const uint32_t upper = __builtin_amdgcn_perm(0u, 0xff00u, s >> 3 & 0x01010101u);      // 0xff where the code is 8 .. 15
-            l = (__builtin_amdgcn_perm(lo[1], lo[0], low3) & ~upper) | (__builtin_amdgcn_perm(lo[3], lo[2], low3) & upper);
-            h = (__builtin_amdgcn_perm(hi[1], hi[0], low3) & ~upper) | (__builtin_amdgcn_perm(hi[3], hi[2], low3) & upper);
-        }
-        v01 = __builtin_amdgcn_perm(h, l, 0x05010400u);
-        v23 = __builtin_amdgcn_perm(h, l, 0x07030602u);
-    }
-};
-
-// The 32 weights of a row's slot, as bf16: of each eight k, out holds (0, 2),
-// (4, 6), (1, 3) and (5, 7).
-template <int FMT>
-__device__ __forceinline__ void decode_row(const RowStep& r, uint32_t (&out)[16])
-{
-    const ByteTable<FMT> t(r);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t even, odd;      // the codes of the eight's even and odd k, one a byte
-        if constexpr (FMT == FMT_ANY2) {
-            const uint32_t w = r.code[i / 2] >> (16 * (i % 2));     // two bits each
-            even = (w & 3u) | (w & 0x30u) << 4 | (w & 0x300u) << 8 | (w & 0x3000u) << 12;
-            odd = (w >> 2 & 3u) | (w >> 2 & 0x30u) << 4 | (w >> 2 & 0x300u) << 8 | (w >> 2 & 0x3000u) << 12;
-        } else if constexpr (FMT == FMT_ANY3) {
-            // four pairs of six bits; the last four from the bytes' top bits
-            const uint32_t w = i < 3 ? r.code[i < 3 ? i : 0]
-                                     : (r.code[0] >> 6 & 0x03030303u) | (r.code[1] >> 4 & 0x0c0c0c0cu) | (r.code[2] >> 2 & 0x30303030u);
-            even = w & 0x07070707u;
-            odd = w >> 3 & 0x07070707u;
-        } else {
-            even = r.code[i] & 0x0f0f0f0fu;
-            odd = r.code[i] >> 4 & 0x0f0f0f0fu;
-        }
-        t.find(even, out[4 * i], out[4 * i + 1]);
-        t.find(odd, out[4 * i + 2], out[4 * i + 3]);
-    }
-}
-
 // 16 * MB rows of dy x 128 k a workgroup.
 template <int FMT, int MB, bool WHOLE>
 __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
 {
-    constexpr int BYTES = FMT == FMT_ANY2 ? 8 : FMT == FMT_ANY3 ? 12 : 16;
     __shared__ __attribute__((aligned(16))) uint32_t turned[FEW_THREADS / WAVE][32 * FEW_STRIDE];
     __shared__ f32x4_t red[4][2 * MB][WAVE];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
@@ -405,33 +393,11 @@ __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
     const int steps = (p.N + 63) / 64, parts = p.S * 2, at = blockIdx.y * 2 + (w >> 2);
     const int s0 = static_cast<int>(static_cast<int64_t>(steps) * at / parts);
     const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (at + 1) / parts);
-    const int G = p.K / p.g, grp = (chunk * 128 + quarter * 32) / p.g;
     const Matrix<WHOLE> dy(p.dy, static_cast<size_t>(p.M) * p.N);
     typedef typename Matrix<WHOLE>::Piece Piece;
 
     auto fetch = [&](int st, RowStep& r) {
-        const int n = st * 64 + lane;
-        r.alpha = r.beta = 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            r.code[i] = 0u;
-        r.table[0] = r.table[1] = u32x4_t{0u, 0u, 0u, 0u};
-        if (n >= p.N)            // weights of 0
-            return;
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(
-            p.packed + ((static_cast<size_t>(n / 16) * Kc + chunk) * 64 + quarter * 16 + n % 16) * BYTES);
-#pragma unroll
-        for (int i = 0; i < BYTES / 4; ++i)
-            r.code[i] = src[i];
-        r.alpha = p.alpha[static_cast<size_t>(n) * G + grp];
-        r.beta = p.beta[static_cast<size_t>(n) * G + grp];
-        if constexpr (FMT != FMT_INT4) {
-            typedef u32x4_t __attribute__((aligned(2))) table_t;
-            const table_t* l = reinterpret_cast<const table_t*>(p.lut + static_cast<size_t>(n) * 16);
-            r.table[0] = l[0];
-            if constexpr (FMT == FMT_ANY4)
-                r.table[1] = l[1];
-        }
+        r = fetch_row<FMT>(p.packed, p.lut, p.alpha, p.beta, st * 64 + lane, p.N, Kc, chunk, quarter, p.g);
     };
     f32x4_t acc[MB][2];      // [rows of dy][halves of the 32 k]
 #pragma unroll
@@ -456,12 +422,8 @@ __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
         uint32_t v[16];
         decode_row<FMT>(now, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v[i]), 0xB1, 0xf, 0xf, true));
-            const int k = 8 * (i / 4) + 4 * (i & 1) + (i >> 1 & 1) + 2 * (lane & 1);
-            own[k * FEW_STRIDE + lane / 2] = lane & 1 ? __builtin_amdgcn_perm(v[i], other, 0x07060302u)
-                                                                        : __builtin_amdgcn_perm(other, v[i], 0x05040100u);
-        }
+        for (int i = 0; i < 16; ++i)
+            own[(first_k(i) + 2 * (lane & 1)) * FEW_STRIDE + lane / 2] = pair_rows(v[i], lane & 1);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
