@@ -754,7 +754,11 @@ def gemm_lora(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: t
     place on its output (so the projection is rounded to bf16 once more)."""
     dev = _gpu(x, "x", 2)
     with _on(dev, stream):
-        y = gemm(x, packed, lut, alpha, beta, g, out=out)
+        ws = None
+        if torch.cuda.is_current_stream_capturing():     # a graph keeps its workspace to itself
+            need = workspace_size(x.shape[0], lut.shape[0], x.shape[1], g)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        y = gemm(x, packed, lut, alpha, beta, g, out=out, workspace=ws)
         return lora(x, A, B, scale, ids, y, out=y, h=h, act=act, plan=plan)
 
 

@@ -1200,6 +1200,14 @@ __global__ __launch_bounds__(256) void k_wgrad_sum(const WgradArgs p)
     job.out[(static_cast<size_t>(a) * p.r + j) * job.D + d] = v * (job.scaled && n ? p.scale[a] : 1.0f);
 }
 
+// Gradients of an empty batch.
+__global__ __launch_bounds__(256) void k_lora_zero(float* __restrict__ p, size_t n)
+{
+    const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;
+    if (i < n)
+        p[i] = 0.0f;
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -1446,8 +1454,19 @@ any4_status any4_lora_backward(const uint16_t* dy, const uint16_t* x, const int8
                                int64_t N, int64_t K, int64_t r, int64_t L, void* workspace, size_t workspace_bytes,
                                hipStream_t stream)
 {
-    if (!sizes_ok(M, N, K, r, L) || M == 0 || N == 0)
+    if (!sizes_ok(M, N, K, r, L) || N == 0)
         return ANY4_E_SHAPE;
+    if (M == 0) {
+        if (!is_aligned(dA, 4) || !is_aligned(dB, 4))
+            return ANY4_E_ALIGN;
+        (void)hipGetLastError();
+        const size_t nA = dA ? static_cast<size_t>(L) * r * K : 0, nB = dB ? static_cast<size_t>(L) * r * N : 0;
+        if (nA)
+            hipLaunchKernelGGL(k_lora_zero, dim3(static_cast<unsigned>((nA + 255) / 256)), dim3(256), 0, stream, dA, nA);
+        if (nB)
+            hipLaunchKernelGGL(k_lora_zero, dim3(static_cast<unsigned>((nB + 255) / 256)), dim3(256), 0, stream, dB, nB);
+        return nA || nB ? launch_status() : ANY4_OK;
+    }
     if (!dy || !A || !B || !scale || !ids || !workspace || (dA && !x && (!q || !qs)) || (dB && !h))
         return ANY4_E_NULL;
     if (!is_aligned(dy, 2) || !is_aligned(x, 16) || !is_aligned(q, 16) || !is_aligned(qs, 4) || !is_aligned(h, 4) ||

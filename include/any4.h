@@ -367,7 +367,8 @@ any4_status any4_quantize(const float* W, const float* ex, uint8_t* idx, uint16_
  * second product unrounded, so out carries fp32 summation error and one
  * rounding.  Results are deterministic and a row's result depends on no other
  * row's values.  A non-finite weight of an adapter makes the outputs it
- * reaches non-finite (which kind is not specified).
+ * reaches non-finite, and a non-finite row the gradients of its adapter (which
+ * kind is not specified).
  * Sizes of all any4_lora* calls: 0 <= M <= 2^20, 0 <= N <= 2^24, K <= 2^24 a
  * positive multiple of 128, 1 <= r <= 128, 1 <= L <= 4096; x, y, A and B below
  * 2 GiB.
@@ -427,7 +428,7 @@ any4_status any4_lora(const uint16_t* x, const uint16_t* A, const uint16_t* B, c
  *   dx_out may be dx itself.  dx_out, dA and dB may each be NULL: not wanted
  *          (x, q, qs are then not read without dA, h not without dB).
  *   plan, workspace  as for any4_lora, any4_lora_backward_workspace_size bytes.
- *   M >= 1, N >= 1.  x, A, q, dx, dx_out, plan and workspace need 16-byte
+ *   N >= 1; M = 0 writes dA = dB = 0 (the other pointers may be NULL).  x, A, q, dx, dx_out, plan and workspace need 16-byte
  *   alignment, the others that of their elements.
  * Errors: as any4_lora.
  */

@@ -74,3 +74,34 @@ def test_step_through_two_layers(M, L, r):
         assert_near(dA, rA, eA, "dA")
         assert_near(dB, rB, eB, "dB")
         dy = dx
+
+
+@pytest.mark.parametrize("M", [3, 200])
+def test_layer_with_adapters_in_two_graphs(M):
+    """gemm_lora captured twice from one stream and replayed on two at once:
+    each graph has its own workspaces (M = 200: a whole dequantised layer)."""
+    L, r, K, N = 2, 8, 512, 264
+    layer = Layer(M, N, K, L, r, 4)
+    ids = torch.arange(M, device=gu.DEV, dtype=torch.int32) % L
+    xs = [torch.randn((M, K), generator=torch.Generator().manual_seed(s)).to(torch.bfloat16).to(gu.DEV) for s in (1, 2)]
+    refs = [any4.gemm_lora(x, *layer.frozen, *layer.adapters, ids).clone() for x in xs]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(any4.gemm_lora(x, *layer.frozen, *layer.adapters, ids))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for o in outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, t in zip(graphs, streams):
+            with torch.cuda.stream(t):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, refs))

@@ -158,12 +158,13 @@ def test_kept_plan_same_bits(M, L, kind):
     assert all(torch.equal(p, q) for p, q in zip(ga, gb))
 
 
+@pytest.mark.parametrize("N", [72, 37])
 @pytest.mark.parametrize("M", [5, 200])
-def test_masked_and_non_finite_values(M):
+def test_masked_and_non_finite_values(M, N):
     """A row's NaN or infinity stays in its row; rows without an adapter pass
     y through bit for bit whatever x holds; an unused adapter's weights are
     not read into anything; the gradients of other adapters stay clean."""
-    t = make(M, 256, 72, 8, 4, "mixed")
+    t = make(M, 256, N, 8, 4, "mixed")
     t["ids"] = torch.arange(M, device=gu.DEV, dtype=torch.int32) % 3      # adapter 3 unused
     t["ids"][2] = -1
     clean = any4.lora(t["x"], t["A"], t["B"], t["scale"], t["ids"], t["y"])
@@ -185,6 +186,13 @@ def test_masked_and_non_finite_values(M):
     assert torch.isnan(dA[0, :, 5]).all() and torch.isfinite(dA[0, :, 6:]).all()
     assert torch.isfinite(dA[2]).all() and torch.isfinite(dB[2]).all()
     assert torch.count_nonzero(dA[3]) == 0 and torch.count_nonzero(dB[3]) == 0
+    # a row of dy reaches its own dx and its adapter's gradients, no neighbour's
+    base = any4.lora_backward(t["dy"], t["x"], torch.zeros_like(h), t["A"], t["B"], t["scale"], t["ids"], dx=t["dx"])
+    t["dy"][3] = float("nan")            # adapter 0
+    got = any4.lora_backward(t["dy"], t["x"], torch.zeros_like(h), t["A"], t["B"], t["scale"], t["ids"], dx=t["dx"])
+    keep = torch.arange(M, device=gu.DEV) != 3
+    assert torch.isnan(got[0][3]).all() and torch.equal(got[0][keep], base[0][keep])
+    assert torch.equal(got[1][2], base[1][2]) and torch.equal(got[2][1:], base[2][1:])
 
 
 @pytest.mark.parametrize("M", [9, 150])
@@ -238,6 +246,9 @@ def test_empty_batch_and_no_outputs():
     e = torch.empty((0, 128), dtype=torch.bfloat16, device=gu.DEV)
     out = any4.lora(e, t["A"], t["B"], t["scale"], t["ids"][:0], torch.empty((0, 16), dtype=torch.bfloat16, device=gu.DEV))
     assert out.shape == (0, 16)
+    dx, dA, dB = any4.lora_backward(t["dy"][:0], e, torch.empty((0, 2), device=gu.DEV), t["A"], t["B"], t["scale"], t["ids"][:0],
+                                    dA=torch.full((1, 2, 128), 3.0, device=gu.DEV))
+    assert dx.shape == (0, 128) and not dA.any() and not dB.any()
     for M in (4, 80):
         t = make(M, 128, 16, 2, 1, "runs")
         h, act = torch.empty((M, 2), device=gu.DEV), any4.act8_empty(t["x"])
@@ -355,5 +366,5 @@ def test_refusals():
     h = torch.empty((8, 4), device=gu.DEV)
     with pytest.raises(TypeError):
         any4.lora_backward(t["dy"], t["x"], h, t["A"], t["B"], t["scale"], t["ids"], x_scale=torch.ones((8, 1), device=gu.DEV))
-    with pytest.raises(RuntimeError):
-        any4.lora_backward(t["dy"][:0], t["x"][:0], h[:0], t["A"], t["B"], t["scale"], t["ids"][:0])
+    with pytest.raises(ValueError):
+        any4.lora_backward(t["dy"], t["x"][:4], h, t["A"], t["B"], t["scale"], t["ids"])

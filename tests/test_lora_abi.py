@@ -34,8 +34,10 @@ def test_lora_shape_errors(bad):
     assert any4.lora_backward_workspace_size(**sizes) == 0
 
 
-def test_backward_needs_rows_and_outputs():
-    assert backward(M=0) == 2 and backward(N=0) == 2
+def test_backward_needs_outputs():
+    assert backward(N=0) == 2
+    assert backward(*[None] * 14, M=0, ws=None, ws_bytes=0) == 0       # nothing to write either
+    assert backward(M=0, dA=A + 2) == 3
     assert any4.lora_backward_workspace_size(0, 16, 128, 8, 2) == 0
 
 
