@@ -153,6 +153,26 @@ __device__ __forceinline__ f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// A wave's block of 16 rows x 128 bf16, loaded as it lies in memory (lane
+// 16 g + c has 16 bytes of row 4 i + g, columns 8 c on: a load covers whole 256-byte
+// pieces of rows), turned through LDS of the wave's own into matrix-core
+// operands (lane 16 g + c: row c, columns 32 i + 8 g on).  Loaded as operands, 64
+// lanes ask for 64 different places, and the vector cache answers one a clock:
+// 16 bytes a clock for a CU.
+constexpr int TURN_PITCH = 17;                  // 16-byte pieces of a staged row: 16 rows in 64 banks
+constexpr int TURN_PIECES = 16 * TURN_PITCH;
+
+__device__ __forceinline__ void turn16(u32x4_t* own, const u32x4_t (&in)[4], u32x4_t (&out)[4])
+{
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        own[(4 * i + g) * TURN_PITCH + c] = in[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        out[i] = own[c * TURN_PITCH + 4 * i + g];
+}
+
 // f = hi + mid + lo exactly, each part with the 8 significant bits of a bf16
 // (cut, not rounded, so hi cannot overflow; parts below 2^-126 are lost).
 // An fp32 factor enters the matrix cores as these three: the products with

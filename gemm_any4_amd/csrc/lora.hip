@@ -533,11 +533,14 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
 {
     constexpr int MS = T / 16;
     __shared__ int own[SHRINK_WAVES][SMALL_T];
-    __shared__ f32x4_t red[SHRINK_WAVES][MS * RB][WAVE];
+    // the waves' blocks on their way into operands, and afterwards their sums
+    constexpr int PIECES = TURN_PIECES > MS * RB * WAVE ? TURN_PIECES : MS * RB * WAVE;
+    __shared__ u32x4_t room[SHRINK_WAVES * PIECES];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
     const Tile tile = find_tile<T>(p.b, blockIdx.x, own[w]);
     if (tile.a == -2 || (tile.a < 0 && !Q8))
         return;
+    u32x4_t* turn = room + w * TURN_PIECES;
     const int steps = (p.D + 127) / 128, parts = p.SK * SHRINK_WAVES;
     const int at = blockIdx.y * SHRINK_WAVES + w, j0 = blockIdx.z * (16 * RB);
     const int s0 = static_cast<int>(static_cast<int64_t>(steps) * at / parts);
@@ -545,15 +548,13 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
 
     const Matrix<WHOLE> in(p.in, static_cast<size_t>(p.b.M) * p.D);
     const Matrix<WHOLE> wt(p.w, static_cast<size_t>(p.b.L) * p.r * p.D);
-    uint32_t row[MS], wrow[RB];        // where the lane's first 8 of a row start
+    uint32_t row[MS][4];               // where the lane's columns of row 16 s + 4 i + g start
 #pragma unroll
     for (int s = 0; s < MS; ++s)
-        row[s] = static_cast<uint32_t>(tile.rows[16 * s + c]) * p.D + 8 * g;
 #pragma unroll
-    for (int t = 0; t < RB; ++t) {     // ranks behind the last read that one again
-        const int j = j0 + 16 * t + c;
-        wrow[t] = static_cast<uint32_t>((tile.a < 0 ? 0 : tile.a) * p.r + (j < p.r ? j : p.r - 1)) * p.D + 8 * g;
-    }
+        for (int i = 0; i < 4; ++i)
+            row[s][i] = static_cast<uint32_t>(tile.rows[16 * s + 4 * i + g]) * p.D + 8 * c;
+    const uint32_t wrow = static_cast<uint32_t>((tile.a < 0 ? 0 : tile.a) * p.r + j0 + g) * p.D + 8 * c;
     f32x4_t acc[MS][RB];
 #pragma unroll
     for (int s = 0; s < MS; ++s)
@@ -562,39 +563,47 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
             acc[s][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     typedef typename Matrix<WHOLE>::Piece Piece;
     auto fetch = [&](int st, Piece (&v)[MS][4], Piece (&wv)[RB][4]) {
-        const int d0 = st * 128;
+        const int d0 = st * 128, valid = p.D - (d0 + 8 * c);
+        const bool edge = d0 + 128 > p.D;
 #pragma unroll
         for (int t = 0; t < RB; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                wv[t][i] = wt.fetch(wrow[t] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g), d0 + 128 > p.D);
+            for (int i = 0; i < 4; ++i)      // ranks behind the last are zeros
+                wv[t][i] = wt.fetch(wrow + (16 * t + 4 * i) * p.D + d0, j0 + 16 * t + 4 * i + g < p.r ? valid : 0, edge);
 #pragma unroll
         for (int s = 0; s < MS; ++s)
             if (16 * s < tile.count)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    v[s][i] = in.fetch(row[s] + d0 + 32 * i, p.D - (d0 + 32 * i + 8 * g), d0 + 128 > p.D);
+                    v[s][i] = in.fetch(row[s][i] + d0, 16 * s + 4 * i < tile.count ? valid : 0, edge);
     };
     auto use = [&](int st, const Piece (&vp)[MS][4], const Piece (&wp)[RB][4]) {
-        const int d0 = st * 128;
+        const int d0 = st * 128, valid = p.D - (d0 + 8 * c);
         const bool edge = d0 + 128 > p.D;
         u32x4_t wv[RB][4];
 #pragma unroll
-        for (int t = 0; t < RB; ++t)
+        for (int t = 0; t < RB; ++t) {
+            u32x4_t x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                wv[t][i] = wt.finish(wp[t][i], wrow[t], p.D - (d0 + 32 * i + 8 * g), edge);
+                x[i] = wt.finish(wp[t][i], wrow + (16 * t + 4 * i) * p.D + d0, valid, edge);
+            turn16(turn, x, wv[t]);
+        }
 #pragma unroll
         for (int s = 0; s < MS; ++s) {
             if (16 * s >= tile.count)
                 break;
-            u32x4_t v[4];
+            u32x4_t x[4], v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)      // steps of 32 leave an odd start odd
-                v[i] = in.finish(vp[s][i], row[s], p.D - (d0 + 32 * i + 8 * g), edge);
+            for (int i = 0; i < 4; ++i)
+                x[i] = in.finish(vp[s][i], row[s][i] + d0, valid, edge);
+            turn16(turn, x, v);
             if constexpr (Q8) {
-                if (blockIdx.z == 0)
-                    store_row8(v, p.q + row[s] - 8 * g + d0, p.qs + row[s] / GROUP8 + st, g, 16 * s + c < tile.count);
+                if (blockIdx.z == 0) {
+                    const bool live = 16 * s + c < tile.count;
+                    const size_t r = static_cast<size_t>(tile.rows[16 * s + c]);
+                    store_row8(v, p.q + r * p.D + d0, p.qs + r * (p.D / GROUP8) + st, g, live);
+                }
             }
 #pragma unroll
             for (int t = 0; t < RB; ++t)
@@ -607,7 +616,7 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
     // way while this one is multiplied (4096 x 14336, rank 16: 42 -> 32 us; with
     // the 8-bit copy a second workgroup a CU is worth more: 53 -> 50 us)
     Piece v0[MS][4], w0[RB][4];
-    if constexpr (!Q8 && (WHOLE || MS * RB <= 4)) {
+    if constexpr (!Q8 && (WHOLE ? RB <= 2 : MS * RB <= 2)) {
         Piece v1[MS][4], w1[RB][4];
         if (s0 < s1)
             fetch(s0, v0, w0);
@@ -629,21 +638,23 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
     }
     if (tile.a < 0)
         return;
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(room);        // [SHRINK_WAVES][MS * RB][WAVE]
+    __syncthreads();      // every wave has its operands
 #pragma unroll
     for (int e = 0; e < MS * RB; ++e)
-        red[w][e][lane] = acc[e / RB][e % RB];
+        red[(w * MS * RB + e) * WAVE + lane] = acc[e / RB][e % RB];
     __syncthreads();
     const size_t places = static_cast<size_t>(gridDim.x) * T;
     for (int e = w; e < MS * RB; e += SHRINK_WAVES) {     // a 16 x 16 block a wave
         f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int o = 0; o < SHRINK_WAVES; ++o)
-            v += red[o][e][lane];
+            v += red[(o * MS * RB + e) * WAVE + lane];
         const int s = e / RB, j = j0 + 16 * (e % RB) + c;
         if (j < p.r16)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                p.part[(blockIdx.y * places + blockIdx.x * T + 16 * s + 4 * g + i) * p.r16 + j] = j < p.r ? v[i] : 0.0f;
+                p.part[(blockIdx.y * places + blockIdx.x * T + 16 * s + 4 * g + i) * p.r16 + j] = v[i];
     }
 }
 
@@ -654,6 +665,11 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
 // here (dh), else the scale multiplies the sum over j (y).  A wave holds the
 // 128 columns of W it works on as matrix-core operands (8 x 8 blocks turned in
 // registers, all loads 16 bytes) and goes over the tile's rows, 16 at a time.
+// The factors of the weight gradients, in the order their operands take them:
+// of each tile (32 places) and 16 ranks, four places of a rank for each lane
+// (16 g + c: rank c, places 8 g + 0 .. 3), then the next four.
+__host__ __device__ constexpr size_t factor_at(size_t tile, int tiles16, int t) { return (tile * tiles16 + t) * (2 * WAVE); }
+
 struct ExpandArgs {
     Batch b;
     const float* part;        // [SK][tiles * T][r16]
@@ -663,7 +679,7 @@ struct ExpandArgs {
     uint16_t* out;            // [M][D] or null (only c is wanted)
     float* c;                 // [M][r] or null
     const float* h;           // [M][r] and
-    float* turned;            // [2][r16][tiles * T]: c and h by place, for wgrad; or null
+    float* turned;            // c and h as wgrad's operands (factor_at), or null
     int D, r, r16, SK;
 };
 
@@ -803,13 +819,22 @@ __global__ __launch_bounds__(EXPAND_THREADS) void k_expand(const ExpandArgs p)
         }
     }
     __syncthreads();
-    if (p.turned && first) {     // places behind the last count for nothing
-        const size_t places = static_cast<size_t>(gridDim.y) * T;
-        float* o = p.turned + static_cast<size_t>(blockIdx.y) * T;
-        for (int i = tid; i < T * p.r16; i += EXPAND_THREADS) {
-            const int j = i / T, m = i % T;
-            o[j * places + m] = cs[m * STRIDE + j];
-            o[(p.r16 + j) * places + m] = p.h && m < tile.count && j < p.r ? p.h[static_cast<size_t>(rows[m]) * p.r + j] : 0.0f;
+    if constexpr (T == TILE_T) {
+        if (p.turned && first) {     // places behind the last count for nothing
+            const int tiles16 = p.r16 / 16;
+            f32x4_t* o = reinterpret_cast<f32x4_t*>(p.turned) + factor_at(blockIdx.y, tiles16, 0);
+            f32x4_t* oh = o + factor_at(gridDim.y, tiles16, 0);
+            for (int i = tid; i < tiles16 * 2 * WAVE; i += EXPAND_THREADS) {
+                const int j = i / (2 * WAVE) * 16 + (i & 15), m = (i >> 4 & 3) * 8 + (i / WAVE & 1) * 4;
+                f32x4_t v, vh;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = cs[(m + e) * STRIDE + j];
+                    vh[e] = p.h && m + e < tile.count && j < p.r ? p.h[static_cast<size_t>(rows[m + e]) * p.r + j] : 0.0f;
+                }
+                o[i] = v;
+                oh[i] = vh;
+            }
         }
     }
     if (!p.out || d0 >= p.D)     // waves leave whole: every lane holds matrix-core operands
@@ -868,7 +893,8 @@ __global__ __launch_bounds__(SMALL_THREADS) void k_small(const SmallArgs p)
 {
     constexpr int RK = (RB + 1) / 2, STRIDE = 32 * RK + 4;
     __shared__ int own[SMALL_WAVES][SMALL_T];
-    __shared__ f32x4_t red[SMALL_WAVES][RB][WAVE];
+    constexpr int PIECES = TURN_PIECES > RB * WAVE ? TURN_PIECES : RB * WAVE;
+    __shared__ u32x4_t room[SMALL_WAVES * PIECES];       // as in k_shrink
     __shared__ __attribute__((aligned(16))) float cs[SMALL_T * STRIDE];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
     const Tile tile = find_tile<SMALL_T>(p.b, blockIdx.y, own[w]);
@@ -905,40 +931,47 @@ __global__ __launch_bounds__(SMALL_THREADS) void k_small(const SmallArgs p)
         const Matrix<WHOLE1> in(p.in, static_cast<size_t>(p.b.M) * p.D1);
         const Matrix<WHOLE1> w1(p.w1, static_cast<size_t>(p.b.L) * p.r * p.D1);
         typedef typename Matrix<WHOLE1>::Piece Piece;
-        const uint32_t row = static_cast<uint32_t>(tile.rows[c]) * p.D1 + 8 * g;
-        uint32_t wrow[RB];
+        u32x4_t* turn = room + w * TURN_PIECES;
+        uint32_t row[4];
 #pragma unroll
-        for (int t = 0; t < RB; ++t) {     // ranks behind the last read that one again
-            const int j = 16 * t + c;
-            wrow[t] = static_cast<uint32_t>(a * p.r + (j < p.r ? j : p.r - 1)) * p.D1 + 8 * g;
-        }
+        for (int i = 0; i < 4; ++i)
+            row[i] = static_cast<uint32_t>(tile.rows[4 * i + g]) * p.D1 + 8 * c;
+        const uint32_t wrow = static_cast<uint32_t>(a * p.r + g) * p.D1 + 8 * c;
         const int steps = (p.D1 + 127) / 128;
         auto fetch = [&](int st, Piece (&x)[4], Piece (&v)[RB][4]) {
-            const int o = st * 128;
+            const int o = st * 128, valid = p.D1 - (o + 8 * c);
+            const bool edge = o + 128 > p.D1;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int valid = p.D1 - (o + 32 * i + 8 * g);
-                x[i] = in.fetch(row + o + 32 * i, valid, o + 128 > p.D1);
+                x[i] = in.fetch(row[i] + o, 4 * i < tile.count ? valid : 0, edge);
 #pragma unroll
-                for (int t = 0; t < RB; ++t)
-                    v[t][i] = w1.fetch(wrow[t] + o + 32 * i, valid, o + 128 > p.D1);
+                for (int t = 0; t < RB; ++t)      // ranks behind the last are zeros
+                    v[t][i] = w1.fetch(wrow + (16 * t + 4 * i) * p.D1 + o, 16 * t + 4 * i + g < p.r ? valid : 0, edge);
             }
         };
         auto use = [&](int st, const Piece (&xp)[4], const Piece (&vp)[RB][4]) {
-            const int o = st * 128;
-            u32x4_t x[4];
+            const int o = st * 128, valid = p.D1 - (o + 8 * c);
+            const bool edge = o + 128 > p.D1;
+            u32x4_t y[4], x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                x[i] = in.finish(xp[i], row, p.D1 - (o + 32 * i + 8 * g), o + 128 > p.D1);
-            if (quant)
-                store_row8(x, p.q + row - 8 * g + o, p.qs + row / GROUP8 + st, g, c < tile.count);
+                y[i] = in.finish(xp[i], row[i] + o, valid, edge);
+            turn16(turn, y, x);
+            if (quant) {
+                const size_t r = static_cast<size_t>(tile.rows[c]);
+                store_row8(x, p.q + r * p.D1 + o, p.qs + r * (p.D1 / GROUP8) + st, g, c < tile.count);
+            }
 #pragma unroll
-            for (int t = 0; t < RB; ++t)
+            for (int t = 0; t < RB; ++t) {
+                u32x4_t v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[t] = mfma(__builtin_bit_cast(bf16x8_t, x[i]),
-                                  __builtin_bit_cast(bf16x8_t, w1.finish(vp[t][i], wrow[t], p.D1 - (o + 32 * i + 8 * g), o + 128 > p.D1)),
-                                  acc[t]);
+                    y[i] = w1.finish(vp[t][i], wrow + (16 * t + 4 * i) * p.D1 + o, valid, edge);
+                turn16(turn, y, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[t] = mfma(__builtin_bit_cast(bf16x8_t, x[i]), __builtin_bit_cast(bf16x8_t, v[i]), acc[t]);
+            }
         };
         // as many steps' loads at once as fit the registers (K = 4096, rank 16: all)
         constexpr int DEPTH = RB == 1 ? 4 : RB == 2 ? 2 : 1;
@@ -954,16 +987,18 @@ __global__ __launch_bounds__(SMALL_THREADS) void k_small(const SmallArgs p)
                     use(st + e * SMALL_WAVES, x[e], v[e]);
         }
     }
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(room);        // [SMALL_WAVES][RB][WAVE]
+    __syncthreads();      // every wave has its operands
 #pragma unroll
     for (int t = 0; t < RB; ++t)
-        red[w][t][lane] = acc[t];
+        red[(w * RB + t) * WAVE + lane] = acc[t];
     __syncthreads();
     if (w < 2 * RK) {          // 16 ranks a wave; zeros where there are none
         f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
         if (w < RB)
 #pragma unroll
             for (int o = 0; o < SMALL_WAVES; ++o)
-                v += red[o][w < RB ? w : 0][lane];
+                v += red[(o * RB + (w < RB ? w : 0)) * WAVE + lane];
         const int j = 16 * w + c;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1010,7 +1045,7 @@ struct WgradJob {
     const uint16_t* in;      // [M][D] bf16, or null:
     const uint8_t* q;        // [M][D] int8 and
     const float* qs;         // [M][D/128] its scales
-    const float* c;          // up to SMALL_M rows [M][r], else [r16][places]
+    const float* c;          // up to SMALL_M rows [M][r], else as factor_at() says
     float* out;              // [L][r][D] or null
     float* part;             // [slots][r][cols * 128]
     int D, cols;             // columns, and blocks of 128 of them
@@ -1021,8 +1056,7 @@ struct WgradArgs {
     Batch b;
     const float* scale;
     WgradJob job[2];
-    int64_t places;
-    int r;
+    int r, r16;
     bool chunked;            // blockIdx.y is a chunk of the plan; else an adapter
 };
 
@@ -1104,11 +1138,16 @@ __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
 #pragma unroll
                 for (int u = 0; u < 8; ++u)     // places behind the last count for nothing
                     f[rt][u] = m0 + 8 * g + u < count && j < p.r ? job.c[row[u] * p.r + j] : 0.0f;
-            } else {                            // ranks behind the last: never stored
-                const f32x4_t* src = reinterpret_cast<const f32x4_t*>(job.c + (j < p.r ? j : p.r - 1) * p.places + first + m0 + 8 * g);
+            } else if (j0 + 16 * rt < p.r16) {
+                const f32x4_t* src = reinterpret_cast<const f32x4_t*>(job.c) +
+                                     factor_at((first + m0) / TILE_T, p.r16 / 16, j0 / 16 + rt) + lane;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    f[rt][e] = src[e / 4][e % 4];
+                    f[rt][e] = src[e / 4 * WAVE][e % 4];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[rt][e] = 0.0f;
             }
         }
         u32x4_t R[8];
@@ -1494,7 +1533,6 @@ any4_status any4_lora_backward(const uint16_t* dy, const uint16_t* x, const int8
     const int r16 = round16(r), SK = split_of(M, L, N, r);
     const int64_t tiles = tile_bound(M, L);
     const bool small = M <= SMALL_M, need_dh = dx_out || dA;
-    const int64_t places = tiles * TILE_T;
     if (need_dh && one_launch(M, N, r)) {
         launch_small(SmallArgs{b, dy, B, A, scale, dx, dx_out, factors, nullptr, nullptr, static_cast<int>(N),
                                static_cast<int>(K), static_cast<int>(r), true}, tiles, stream);
@@ -1509,11 +1547,11 @@ any4_status any4_lora_backward(const uint16_t* dy, const uint16_t* x, const int8
     }
     if (dA || dB) {
         const bool chunked = M > CHUNK;
-        WgradArgs g{b, scale, {}, places, static_cast<int>(r), chunked};
+        WgradArgs g{b, scale, {}, static_cast<int>(r), r16, chunked};
         g.job[0] = WgradJob{x, reinterpret_cast<const uint8_t*>(q), qs, factors, dA, reinterpret_cast<float*>(at),
                             static_cast<int>(K), dA ? static_cast<int>(K / 128) : 0, false};
         at += wgrad_bytes(M, K, r);
-        g.job[1] = WgradJob{dy, nullptr, nullptr, small ? h : factors + static_cast<size_t>(r16) * places, dB, reinterpret_cast<float*>(at), static_cast<int>(N),
+        g.job[1] = WgradJob{dy, nullptr, nullptr, small ? h : factors + 4 * factor_at(tiles, r16 / 16, 0), dB, reinterpret_cast<float*>(at), static_cast<int>(N),
                             dB ? static_cast<int>((N + 127) / 128) : 0, true};
         if (N % 8 == 0 && is_aligned(dy, 16) && is_aligned(dA, 16) && is_aligned(dB, 16))
             launch_wgrad<true>(g, stream);
