@@ -363,13 +363,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_dx(const DxArgs p)
 // A wave takes 32 k (a quarter of a packed tile's columns, 16 bytes of a row)
 // and 64 rows of W a step, a row a lane.
 // Neighbouring lanes pair their values, LDS of the wave's own turns the block
-// (no barrier), and the matrix cores multiply it with dy, whose operands come
-// straight from memory.  Eight waves: four quarters of the columns, two halves
+// (no barrier), and the matrix cores multiply it with dy, whose rows come in
+// 128-byte pieces and are turned the same way (loaded as operands they cost the
+// vector cache a clock for every lane).  Eight waves: four quarters of the columns, two halves
 // of the rows, which meet in LDS at the end; further splits of the rows leave
 // fp32 partial sums.
 constexpr int FEW_M = 64;
 constexpr int FEW_THREADS = 512;
 constexpr int FEW_STRIDE = 36;       // dwords of a turned row of 64 n
+constexpr int FEW_PITCH = 9;         // 16-byte pieces of a staged row of dy
 
 struct FewArgs {
     const uint16_t* dy;     // [M][N]
@@ -387,6 +389,7 @@ template <int FMT, int MB, bool WHOLE>
 __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
 {
     __shared__ __attribute__((aligned(16))) uint32_t turned[FEW_THREADS / WAVE][32 * FEW_STRIDE];
+    __shared__ u32x4_t staged[FEW_THREADS / WAVE][16 * FEW_PITCH];
     __shared__ f32x4_t red[4][2 * MB][WAVE];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
     const int quarter = w & 3, Kc = p.K / 128, chunk = blockIdx.x % Kc, m0 = blockIdx.x / Kc * (16 * MB);
@@ -408,14 +411,16 @@ __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
     if (s0 < s1)
         fetch(s0, now);
     for (int st = s0; st < s1; ++st) {
+        // lane: piece lane % 8 of row 8 h + lane / 8
         Piece x[MB][2];
         const bool edge = st * 64 + 64 > p.N;
+        const int n = st * 64 + 8 * (lane & 7);
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const int m = m0 + 16 * i + c, n = st * 64 + 32 * kk + 8 * g;
-                x[i][kk] = dy.fetch(static_cast<uint32_t>(m) * p.N + n, m < p.M ? p.N - n : 0, edge);
+            for (int h = 0; h < 2; ++h) {
+                const int m = m0 + 16 * i + 8 * h + lane / 8;
+                x[i][h] = dy.fetch(static_cast<uint32_t>(m) * p.N + n, m < p.M ? p.N - n : 0, edge);
             }
         if (st + 1 < s1)
             fetch(st + 1, next);
@@ -424,18 +429,28 @@ __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             own[(first_k(i) + 2 * (lane & 1)) * FEW_STRIDE + lane / 2] = pair_rows(v[i], lane & 1);
+        bf16x8_t wv[2][2];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const bf16x8_t wv = *reinterpret_cast<const bf16x8_t*>(&own[(16 * b + c) * FEW_STRIDE + 16 * kk + 4 * g]);
+            for (int b = 0; b < 2; ++b)
+                wv[kk][b] = *reinterpret_cast<const bf16x8_t*>(&own[(16 * b + c) * FEW_STRIDE + 16 * kk + 4 * g]);
 #pragma unroll
-                for (int i = 0; i < MB; ++i) {
-                    const int m = m0 + 16 * i + c, n = st * 64 + 32 * kk + 8 * g;
-                    const u32x4_t d = dy.finish(x[i][kk], static_cast<uint32_t>(m) * p.N + n, p.N - n, edge);
-                    acc[i][b] = mfma(wv, __builtin_bit_cast(bf16x8_t, d), acc[i][b]);
-                }
+        for (int i = 0; i < MB; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int m = m0 + 16 * i + 8 * h + lane / 8;
+                staged[w][(8 * h + lane / 8) * FEW_PITCH + (lane & 7)] =
+                    dy.finish(x[i][h], static_cast<uint32_t>(m) * p.N + n, p.N - n, edge);
             }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                const bf16x8_t d = __builtin_bit_cast(bf16x8_t, staged[w][c * FEW_PITCH + 4 * kk + g]);
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    acc[i][b] = mfma(wv[kk][b], d, acc[i][b]);
+            }
+        }
         now = next;
     }
     if (w >= 4)
