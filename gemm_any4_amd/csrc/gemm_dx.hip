@@ -20,32 +20,31 @@ constexpr int STEP = 64;             // n of one step of the product; W^T rows a
 // ---------------------------------------------------------------------------
 // The row's table lies in registers as bytes, low and high halves apart, and
 // v_perm looks four codes up at a time.
-// What a lane holds of its row for 32 k.
-struct RowStep {
-    uint32_t code[4];
+// The slot of row n, k 128 * chunk + 32 * quarter + 0 .. 31.
+template <int FMT>
+__device__ __forceinline__ void fetch_codes(const uint8_t* packed, int n, int Kc, int chunk, int quarter, uint32_t (&code)[4])
+{
+    constexpr int BYTES = FMT == FMT_ANY2 ? 8 : FMT == FMT_ANY3 ? 12 : 16;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        packed + ((static_cast<size_t>(n / 16) * Kc + chunk) * 64 + quarter * 16 + n % 16) * BYTES);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        code[i] = i < BYTES / 4 ? src[i] : 0u;
+}
+
+// A row's table, and its scale and offset for 128 k.
+struct RowTable {
     u32x4_t table[2];
     uint32_t alpha, beta;
 };
 
-// The slot of row n, k 128 * chunk + 32 * quarter + 0 .. 31; a row n >= N has
-// weights of 0.
 template <int FMT>
-__device__ __forceinline__ RowStep fetch_row(const uint8_t* packed, const uint16_t* lut, const uint16_t* alpha,
-                                             const uint16_t* beta, int n, int N, int Kc, int chunk, int quarter, int g)
+__device__ __forceinline__ RowTable fetch_table(const uint16_t* lut, const uint16_t* alpha, const uint16_t* beta, int n, int Kc,
+                                                int chunk, int g)
 {
-    constexpr int BYTES = FMT == FMT_ANY2 ? 8 : FMT == FMT_ANY3 ? 12 : 16;
-    RowStep r;
-    r.alpha = r.beta = 0u;
-    r.code[0] = r.code[1] = r.code[2] = r.code[3] = 0u;
+    RowTable r;
     r.table[0] = r.table[1] = u32x4_t{0u, 0u, 0u, 0u};
-    if (n >= N)
-        return r;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(
-        packed + ((static_cast<size_t>(n / 16) * Kc + chunk) * 64 + quarter * 16 + n % 16) * BYTES);
-#pragma unroll
-    for (int i = 0; i < BYTES / 4; ++i)
-        r.code[i] = src[i];
-    const size_t grp = static_cast<size_t>(n) * (Kc * 128 / g) + (chunk * 128 + quarter * 32) / g;
+    const size_t grp = static_cast<size_t>(n) * (Kc * 128 / g) + chunk * 128 / g;
     r.alpha = alpha[grp];
     r.beta = beta[grp];
     if constexpr (FMT != FMT_INT4) {
@@ -66,7 +65,7 @@ struct ByteTable {
     static constexpr int ENTRIES = FMT == FMT_ANY2 ? 4 : FMT == FMT_ANY3 ? 8 : 16;
     uint32_t lo[ENTRIES / 4], hi[ENTRIES / 4];
 
-    __device__ __forceinline__ explicit ByteTable(const RowStep& r)
+    __device__ __forceinline__ explicit ByteTable(const RowTable& r)
     {
         const float a = bf16_to_f32(r.alpha), b = bf16_to_f32(r.beta);
         uint32_t v[ENTRIES / 2];
@@ -109,25 +108,24 @@ struct ByteTable {
 __device__ __forceinline__ constexpr int first_k(int i) { return 8 * (i / 4) + 4 * (i & 1) + (i >> 1 & 1); }
 
 template <int FMT>
-__device__ __forceinline__ void decode_row(const RowStep& r, uint32_t (&out)[16])
+__device__ __forceinline__ void decode(const ByteTable<FMT>& t, const uint32_t (&code)[4], uint32_t (&out)[16])
 {
-    const ByteTable<FMT> t(r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t even, odd;      // the codes of the eight's even and odd k, one a byte
         if constexpr (FMT == FMT_ANY2) {
-            const uint32_t w = r.code[i / 2] >> (16 * (i % 2));     // two bits each
+            const uint32_t w = code[i / 2] >> (16 * (i % 2));     // two bits each
             even = (w & 3u) | (w & 0x30u) << 4 | (w & 0x300u) << 8 | (w & 0x3000u) << 12;
             odd = (w >> 2 & 3u) | (w >> 2 & 0x30u) << 4 | (w >> 2 & 0x300u) << 8 | (w >> 2 & 0x3000u) << 12;
         } else if constexpr (FMT == FMT_ANY3) {
             // four pairs of six bits; the last four from the bytes' top bits
-            const uint32_t w = i < 3 ? r.code[i < 3 ? i : 0]
-                                     : (r.code[0] >> 6 & 0x03030303u) | (r.code[1] >> 4 & 0x0c0c0c0cu) | (r.code[2] >> 2 & 0x30303030u);
+            const uint32_t w = i < 3 ? code[i < 3 ? i : 0]
+                                     : (code[0] >> 6 & 0x03030303u) | (code[1] >> 4 & 0x0c0c0c0cu) | (code[2] >> 2 & 0x30303030u);
             even = w & 0x07070707u;
             odd = w >> 3 & 0x07070707u;
         } else {
-            even = r.code[i] & 0x0f0f0f0fu;
-            odd = r.code[i] >> 4 & 0x0f0f0f0fu;
+            even = code[i] & 0x0f0f0f0fu;
+            odd = code[i] >> 4 & 0x0f0f0f0fu;
         }
         t.find(even, out[4 * i], out[4 * i + 1]);
         t.find(odd, out[4 * i + 2], out[4 * i + 3]);
@@ -163,8 +161,13 @@ __global__ __launch_bounds__(DT_THREADS) void k_dequant_t(const uint8_t* __restr
     __shared__ __attribute__((aligned(16))) uint32_t turned[4 * DT_QUARTER];
     const int Kc = K / 128, c = blockIdx.x % Kc, n0 = blockIdx.x / Kc * 64;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, j = lane & 15, kq = lane >> 4;
-    uint32_t out[16];
-    decode_row<FMT>(fetch_row<FMT>(packed, lut, alpha, beta, n0 + 16 * w + j, N, Kc, c, kq, g), out);
+    const int n = n0 + 16 * w + j;
+    uint32_t out[16] = {};                  // rows behind the last: weights of 0
+    if (n < N) {
+        uint32_t code[4];
+        fetch_codes<FMT>(packed, n, Kc, c, kq, code);
+        decode(ByteTable<FMT>(fetch_table<FMT>(lut, alpha, beta, n, Kc, c, g)), code, out);
+    }
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         turned[kq * DT_QUARTER + (first_k(i) + 2 * (j & 1)) * DT_STRIDE + 8 * w + j / 2] = pair_rows(out[i], j & 1);
@@ -360,14 +363,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_dx(const DxArgs p)
 // few rows: the layer decoded on its way into the product
 // ---------------------------------------------------------------------------
 // Up to FEW_M rows the weights are the work, so they are read packed and once.
-// A wave takes 32 k (a quarter of a packed tile's columns, 16 bytes of a row)
-// and 64 rows of W a step, a row a lane.
-// Neighbouring lanes pair their values, LDS of the wave's own turns the block
-// (no barrier), and the matrix cores multiply it with dy, whose rows come in
-// 128-byte pieces and are turned the same way (loaded as operands they cost the
-// vector cache a clock for every lane).  Eight waves: four quarters of the columns, two halves
-// of the rows, which meet in LDS at the end; further splits of the rows leave
-// fp32 partial sums.
+// A wave takes a chunk of 128 k and 64 rows of W a step, a row a lane, whose
+// table and scales then serve 128 weights.  32 k at a time, neighbouring lanes
+// pair their values, LDS of the wave's own turns the block (no barrier), and
+// the matrix cores multiply it with dy, whose rows come in 128-byte pieces and
+// are turned the same way (loaded as operands they cost the vector cache a
+// clock for every lane).  Eight waves share the rows out, and their sums meet
+// in LDS at the end; further splits of the rows leave fp32 partial sums.  What
+// bounds it is the vector work of the lookups, five instructions a weight.
 constexpr int FEW_M = 64;
 constexpr int FEW_THREADS = 512;
 constexpr int FEW_STRIDE = 36;       // dwords of a turned row of 64 n
@@ -388,29 +391,35 @@ struct FewArgs {
 template <int FMT, int MB, bool WHOLE>
 __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
 {
-    __shared__ __attribute__((aligned(16))) uint32_t turned[FEW_THREADS / WAVE][32 * FEW_STRIDE];
-    __shared__ u32x4_t staged[FEW_THREADS / WAVE][16 * FEW_PITCH];
-    __shared__ f32x4_t red[4][2 * MB][WAVE];
+    constexpr int WAVES = FEW_THREADS / WAVE, TURNED = 32 * FEW_STRIDE / 4, STAGED = 16 * FEW_PITCH;     // 16-byte pieces a wave
+    constexpr int ROOM = TURNED + STAGED > 8 * WAVE ? TURNED + STAGED : 8 * WAVE;
+    __shared__ u32x4_t room[WAVES * ROOM];       // the waves' blocks, and afterwards their sums
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
-    const int quarter = w & 3, Kc = p.K / 128, chunk = blockIdx.x % Kc, m0 = blockIdx.x / Kc * (16 * MB);
-    const int steps = (p.N + 63) / 64, parts = p.S * 2, at = blockIdx.y * 2 + (w >> 2);
+    const int Kc = p.K / 128, chunk = blockIdx.x % Kc, m0 = blockIdx.x / Kc * (16 * MB);
+    const int steps = (p.N + 63) / 64, parts = p.S * WAVES, at = blockIdx.y * WAVES + w;
     const int s0 = static_cast<int>(static_cast<int64_t>(steps) * at / parts);
     const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (at + 1) / parts);
     const Matrix<WHOLE> dy(p.dy, static_cast<size_t>(p.M) * p.N);
     typedef typename Matrix<WHOLE>::Piece Piece;
+    uint32_t* turned = reinterpret_cast<uint32_t*>(room + w * (TURNED + STAGED));
+    u32x4_t* staged = room + w * (TURNED + STAGED) + TURNED;
 
-    auto fetch = [&](int st, RowStep& r) {
-        r = fetch_row<FMT>(p.packed, p.lut, p.alpha, p.beta, st * 64 + lane, p.N, Kc, chunk, quarter, p.g);
-    };
-    f32x4_t acc[MB][2];      // [rows of dy][halves of the 32 k]
+    f32x4_t acc[MB][8];      // [rows of dy][16 k each]
 #pragma unroll
     for (int i = 0; i < MB; ++i)
-        acc[i][0] = acc[i][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t* own = turned[w];
-    RowStep now, next;
-    if (s0 < s1)
-        fetch(s0, now);
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+            acc[i][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     for (int st = s0; st < s1; ++st) {
+        const int row = st * 64 + lane;
+        uint32_t code[4][4] = {};
+        RowTable r = {};                // rows behind the last: weights of 0
+        if (row < p.N) {
+            r = fetch_table<FMT>(p.lut, p.alpha, p.beta, row, Kc, chunk, p.g);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                fetch_codes<FMT>(p.packed, row, Kc, chunk, q, code[q]);
+        }
         // lane: piece lane % 8 of row 8 h + lane / 8
         Piece x[MB][2];
         const bool edge = st * 64 + 64 > p.N;
@@ -422,62 +431,63 @@ __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
                 const int m = m0 + 16 * i + 8 * h + lane / 8;
                 x[i][h] = dy.fetch(static_cast<uint32_t>(m) * p.N + n, m < p.M ? p.N - n : 0, edge);
             }
-        if (st + 1 < s1)
-            fetch(st + 1, next);
-        uint32_t v[16];
-        decode_row<FMT>(now, v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            own[(first_k(i) + 2 * (lane & 1)) * FEW_STRIDE + lane / 2] = pair_rows(v[i], lane & 1);
-        bf16x8_t wv[2][2];
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-                wv[kk][b] = *reinterpret_cast<const bf16x8_t*>(&own[(16 * b + c) * FEW_STRIDE + 16 * kk + 4 * g]);
+        bf16x8_t d[MB][2];
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int m = m0 + 16 * i + 8 * h + lane / 8;
-                staged[w][(8 * h + lane / 8) * FEW_PITCH + (lane & 7)] =
+                staged[(8 * h + lane / 8) * FEW_PITCH + (lane & 7)] =
                     dy.finish(x[i][h], static_cast<uint32_t>(m) * p.N + n, p.N - n, edge);
             }
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const bf16x8_t d = __builtin_bit_cast(bf16x8_t, staged[w][c * FEW_PITCH + 4 * kk + g]);
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    acc[i][b] = mfma(wv[kk][b], d, acc[i][b]);
-            }
+            for (int kk = 0; kk < 2; ++kk)
+                d[i][kk] = __builtin_bit_cast(bf16x8_t, staged[c * FEW_PITCH + 4 * kk + g]);
         }
-        now = next;
+        const ByteTable<FMT> t(r);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t v[16];
+            decode(t, code[q], v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                turned[(first_k(i) + 2 * (lane & 1)) * FEW_STRIDE + lane / 2] = pair_rows(v[i], lane & 1);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const bf16x8_t wv = *reinterpret_cast<const bf16x8_t*>(&turned[(16 * b + c) * FEW_STRIDE + 16 * kk + 4 * g]);
+#pragma unroll
+                    for (int i = 0; i < MB; ++i)
+                        acc[i][2 * q + b] = mfma(wv, d[i][kk], acc[i][2 * q + b]);
+                }
+        }
     }
-    if (w >= 4)
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(room);      // [WAVES][8][WAVE]
 #pragma unroll
-        for (int i = 0; i < 2 * MB; ++i)
-            red[quarter][i][lane] = acc[i / 2][i % 2];
-    __syncthreads();
-    if (w >= 4)
-        return;
+    for (int i = 0; i < MB; ++i) {
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
+        for (int b = 0; b < 8; ++b)
+            red[(w * 8 + b) * WAVE + lane] = acc[i][b];
+        __syncthreads();
+        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};             // wave w: the sums of its 16 k
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const f32x4_t v = acc[i][b] + red[quarter][2 * i + b][lane];
-            const int m = m0 + 16 * i + c;
-            if (m >= p.M)
-                continue;
-            const size_t o = static_cast<size_t>(m) * p.K + chunk * 128 + quarter * 32 + 16 * b + 4 * g;
-            if (p.part) {
-                *reinterpret_cast<f32x4_t*>(p.part + static_cast<size_t>(blockIdx.y) * p.M * p.K + o) = v;
-            } else {
-                u32x2_t y;
-                y[0] = f32_to_bf16(v[0]) | f32_to_bf16(v[1]) << 16;
-                y[1] = f32_to_bf16(v[2]) | f32_to_bf16(v[3]) << 16;
-                *reinterpret_cast<u32x2_t*>(p.dx + o) = y;
-            }
+        for (int o = 0; o < WAVES; ++o)
+            v += red[(o * 8 + w) * WAVE + lane];
+        const int m = m0 + 16 * i + c;
+        if (m >= p.M)
+            continue;
+        const size_t o = static_cast<size_t>(m) * p.K + chunk * 128 + 16 * w + 4 * g;
+        if (p.part) {
+            *reinterpret_cast<f32x4_t*>(p.part + static_cast<size_t>(blockIdx.y) * p.M * p.K + o) = v;
+        } else {
+            u32x2_t y;
+            y[0] = f32_to_bf16(v[0]) | f32_to_bf16(v[1]) << 16;
+            y[1] = f32_to_bf16(v[2]) | f32_to_bf16(v[3]) << 16;
+            *reinterpret_cast<u32x2_t*>(p.dx + o) = y;
         }
+    }
 }
 
 template <int FMT, bool WHOLE>
@@ -553,8 +563,8 @@ Shape dx_shape(int64_t M, int64_t N, int64_t K)
         s.few = M <= 16 ? 1 : 4;
         s.tiles = (M + 16 * s.few - 1) / (16 * s.few) * (K / 128);
         // two workgroups a CU for 16 rows; one where the partial sums are larger
-        S = ((M <= 16 ? 512 : 256) + s.tiles - 1) / s.tiles;      // at least a step for both halves of its waves
-        S = S < steps / 2 ? S : steps / 2;
+        S = ((M <= 16 ? 512 : 256) + s.tiles - 1) / s.tiles;
+        S = S < steps / 8 ? S : steps / 8;      // a step for each of its waves
     } else {
         const int64_t big = (M + 255) / 256 * (K / 256), small = (M + 127) / 128 * (K / 128);
         s.big = K % 256 == 0 && big >= 192;
