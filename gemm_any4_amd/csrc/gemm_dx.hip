@@ -371,7 +371,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_dx(const DxArgs p)
 // clock for every lane).  Eight waves share the rows out, and their sums meet
 // in LDS at the end; further splits of the rows leave fp32 partial sums.  What
 // bounds it is the vector work of the lookups, five instructions a weight.
-constexpr int FEW_M = 64;
+constexpr int FEW_M = 128;
 constexpr int FEW_THREADS = 512;
 constexpr int FEW_STRIDE = 36;       // dwords of a turned row of 64 n
 constexpr int FEW_PITCH = 9;         // 16-byte pieces of a staged row of dy
@@ -545,8 +545,10 @@ __global__ __launch_bounds__(256) void k_dx_zero(uint16_t* dx, size_t octs)
 int64_t padded(int64_t N) { return (N + STEP - 1) / STEP * STEP; }
 
 // How a product is run: decoded on the way (few rows), else 256 x 256 tiles
-// where they fill the chip (or nearly), else 128 x 128.  n is split where the
-// tiles alone leave the 256 CUs idle; the partial sums are fp32.
+// where they fill the chip (or nearly, or in long enough splits of n), else 128 x
+// 128.  n is split where the tiles alone leave the 256 CUs idle; the partial sums
+// are fp32.  128 rows decoded on the way take 25 us at 4096 x 4096 and 48 us at
+// 14336 x 4096, turned first 37 and 72; 192 rows 45 and 106 against 37 and 78.
 struct Shape {
     int few;                 // blocks of 16 rows of a workgroup, 0: turned first
     bool big;
@@ -567,10 +569,17 @@ Shape dx_shape(int64_t M, int64_t N, int64_t K)
         S = S < steps / 8 ? S : steps / 8;      // a step for each of its waves
     } else {
         const int64_t big = (M + 255) / 256 * (K / 256), small = (M + 127) / 128 * (K / 128);
-        s.big = K % 256 == 0 && big >= 192;
+        // the large tiles run a product half as fast again, but split they leave
+        // four times as many partial sums for the same workgroups: worth it from
+        // 32 steps a split (1024 x 14336 x 4096 in four: 168 -> 132 us with the sum;
+        // 1024 x 4096 x 4096, 16 steps: no gain)
+        S = big >= 192 ? 1 : (256 + big - 1) / (big > 0 ? big : 1);
+        s.big = K % 256 == 0 && (S == 1 || (S <= 16 && steps / S >= 32));
         s.tiles = s.big ? big : small;
-        S = s.big ? 1 : (512 + s.tiles - 1) / s.tiles;
-        S = S < steps / 4 ? S : steps / 4;      // each at least 4 steps
+        if (!s.big) {
+            S = (512 + s.tiles - 1) / s.tiles;
+            S = S < steps / 4 ? S : steps / 4;      // each at least 4 steps
+        }
     }
     s.S = static_cast<int>(S < 1 ? 1 : S > 16 ? 16 : S);
     return s;

@@ -71,7 +71,8 @@ def test_formats_and_odd_sizes(fmt, M, N, K, g):
 
 @pytest.mark.parametrize("M,N,K,g", [(16, 4096, 4096, 128), (64, 4099, 1024, 1024), (1000, 2048, 1152, 128),
                                      (513, 1024, 4096, 512), (1, 14336, 512, 128), (3001, 200, 4096, 128),
-                                     (2999, 333, 4352, 256), (128, 4100, 2048, 256), (17, 1000, 14336, 1024)])
+                                     (2999, 333, 4352, 256), (128, 4100, 2048, 256), (17, 1000, 14336, 1024),
+                                     (2000, 8200, 2048, 256), (129, 4096, 1024, 128)])
 def test_larger_sizes(M, N, K, g):
     """Sums split over workgroups, ragged last tiles, padded copies of dy, both
     tile sizes and the form for few rows."""
