@@ -225,7 +225,8 @@ __device__ __forceinline__ void plan_tables(int* cnt, int M, int L, int* plan, i
     }
 }
 
-// STEPS x 64 rows a wave, their ids in registers from the first load on.
+// STEPS x 64 rows a wave, their ids in registers from the first load on.  A chain
+// of waits, not of work: 5.8 us for 1031 rows, 7.6 us for 4096.
 template <int STEPS>
 __global__ __launch_bounds__(PLAN_THREADS) void k_plan(const int* __restrict__ ids, int* plan, int M, int L)
 {
@@ -474,7 +475,8 @@ __device__ __forceinline__ float byte_to_f32(uint32_t v, int i)
 
 constexpr int ACT8_THREADS = 256;
 
-// One 16-lane group per GROUP8 channels, 16 bytes of x a lane.
+// One 16-lane group per GROUP8 channels, 16 bytes of x a lane; one pass, bound by
+// its bytes: 8192 x 14336 72 us to keep and 58 us to read back (5.0 and 6.2 TB/s).
 __global__ __launch_bounds__(ACT8_THREADS) void k_act8_save(const uint16_t* __restrict__ x, uint8_t* __restrict__ q,
                                                             float* __restrict__ s, uint32_t slots)
 {
@@ -509,12 +511,18 @@ __global__ __launch_bounds__(ACT8_THREADS) void k_act8_load(const uint8_t* __res
 }
 
 // ---------------------------------------------------------------------------
-// shrink: part[sk][m][j] = sum over this split's d of in[m][d] W_a[j][d]
+// shrink: part[sk][place][j] = sum over this split's d of in[row][d] W_a[j][d]
 // ---------------------------------------------------------------------------
 // A workgroup takes a tile of rows, 16*RB ranks and one of SK ranges of d,
 // which its eight waves share out again in steps of 128; the matrix cores sum
 // 16 rows x 16 ranks x 32 d at a time.  The eight waves' sums meet in LDS, the
 // splits' in the expand kernel, both in a fixed order.
+// Bound by the bytes of `in`: 4096 x 14336, rank 16, 31 us (3.8 TB/s); 4096 x 4096
+// 12 us, of which six are the launch and its chain of waits (plan, rows, data),
+// and 17 us with the 8-bit copy; rank 64 adds W from the caches, 2048 x 4096 13
+// us.  A step ahead in registers gained a quarter while rows were loaded as
+// operands and nothing since they are turned (fewer workgroups fit a CU), so
+// there is none.  Tiles of 64 rows and four waves: 42 us at 4096 x 14336.
 struct ShrinkArgs {
     Batch b;
     const uint16_t* in;    // [M][D]
@@ -612,29 +620,10 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
                     acc[s][t] = mfma(__builtin_bit_cast(bf16x8_t, v[i]), __builtin_bit_cast(bf16x8_t, wv[t][i]), acc[s][t]);
         }
     };
-    // two steps in registers where they fit: the next one's loads are on their
-    // way while this one is multiplied (4096 x 14336, rank 16: 42 -> 32 us; with
-    // the 8-bit copy a second workgroup a CU is worth more: 53 -> 50 us)
-    Piece v0[MS][4], w0[RB][4];
-    if constexpr (!Q8 && (WHOLE ? RB <= 2 : MS * RB <= 2)) {
-        Piece v1[MS][4], w1[RB][4];
-        if (s0 < s1)
-            fetch(s0, v0, w0);
-        for (int st = s0; st < s1; st += 2) {
-            if (st + 1 < s1)
-                fetch(st + 1, v1, w1);
-            use(st, v0, w0);
-            if (st + 1 >= s1)
-                break;
-            if (st + 2 < s1)
-                fetch(st + 2, v0, w0);
-            use(st + 1, v1, w1);
-        }
-    } else {
-        for (int st = s0; st < s1; ++st) {
-            fetch(st, v0, w0);
-            use(st, v0, w0);
-        }
+    for (int st = s0; st < s1; ++st) {
+        Piece v[MS][4], wv[RB][4];
+        fetch(st, v, wv);
+        use(st, v, wv);
     }
     if (tile.a < 0)
         return;
@@ -665,6 +654,10 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
 // here (dh), else the scale multiplies the sum over j (y).  A wave holds the
 // 128 columns of W it works on as matrix-core operands (8 x 8 blocks turned in
 // registers, all loads 16 bytes) and goes over the tile's rows, 16 at a time.
+// Bound by the bytes of base and out: 4096 x 14336, rank 16, 43 us (5.5 TB/s);
+// 2048 x 4096, rank 64, 18 us, where W and the parts come to twice those bytes
+// from the caches.  Tiles of 64 rows: 52 us at the first (a third as many waves
+// fit a CU); the base rows loaded 16 at a time: 84 us.
 // The factors of the weight gradients, in the order their operands take them:
 // of each tile (32 places) and 16 ranks, four places of a rank for each lane
 // (16 g + c: rank c, places 8 g + 0 .. 3), then the next four.
@@ -1041,6 +1034,11 @@ __global__ __launch_bounds__(SMALL_THREADS) void k_small(const SmallArgs p)
 // LDS.  Chunks of one adapter leave partial sums, which k_wgrad_sum adds in
 // order.  In 8 bits, the row's scale of these 128 channels goes into c, whose
 // three bf16 parts hold it, and the whole numbers are exact bf16 values.
+// Bound by the bytes of `in`: 4096 rows of 4096 columns in 8 bits and 14336 in
+// bf16, rank 16, 26 us (5.1 TB/s); rank 64, 2048 x 8192, 22 us, where the factors
+// come to as many bytes again.  Factors by row instead of operand order: 46 and
+// 47 us.  Chunks of 1024 rows: 28 and 19 us there, but 17 against 12 us at 4096 x
+// 1024, rank 64, where they leave half the CUs idle; of 256: 27 and 27 us.
 struct WgradJob {
     const uint16_t* in;      // [M][D] bf16, or null:
     const uint8_t* q;        // [M][D] int8 and
@@ -1353,8 +1351,12 @@ void launch_expand(const ExpandArgs& e, int64_t tiles, bool scaled, hipStream_t 
         launch_expand_as<false, false>(e, tiles, stream);
 }
 
-// Whether a few rows' two products go in one launch: the first one's W, read by
-// every workgroup at 64 bytes a clock, takes at most about two microseconds.
+// Whether a few rows' two products go in one launch: while every workgroup can
+// read the first one's W for itself in about two microseconds.  One launch
+// against two, kernels alone: K 4096, rank 16, one row 7.7 us against 8.5, 16
+// adapters to 14336 columns 10.8 against 12.1; K 8192, rank 16, 10.9 against 8.5;
+// K 2048, rank 64, 11.7 against 10.5.  The second launch costs the caller another
+// 3 us.
 bool one_launch(int64_t M, int64_t D1, int64_t r) { return M <= SMALL_M && r <= 64 && D1 * r <= 64 * 1024; }
 
 void launch_small(const SmallArgs& a, int64_t tiles, hipStream_t stream)
