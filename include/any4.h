@@ -380,8 +380,8 @@ any4_status any4_quantize(const float* W, const float* ex, uint8_t* idx, uint16_
  * adapter (stable), with the tables the kernels go by: `bytes` of device
  * memory at `plan`, 16-byte aligned.  The plan depends on ids alone, so a
  * program makes it once per batch and hands it to the calls of every layer;
- * calls without one make their own in the workspace (batches of at most 64
- * rows need none and ignore it).  any4_lora_plan_bytes gives 0 for sizes out
+ * calls without one make their own in the workspace (small batches, of at
+ * most 64 rows, or 256 with few adapters in any4_lora, need none and ignore it).  any4_lora_plan_bytes gives 0 for sizes out
  * of range and M = 0.  M = 0 is a no-op.
  * Errors: ANY4_E_SHAPE, ANY4_E_NULL, ANY4_E_ALIGN, ANY4_E_WORKSPACE (bytes too
  * small), ANY4_E_HIP.

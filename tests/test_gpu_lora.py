@@ -112,7 +112,9 @@ SHAPES = [
     (64, 256, 64, 20, 64, "distinct"), (65, 384, 257, 17, 5, "mixed"), (130, 256, 1000, 33, 3, "runs"),
     (200, 128, 64, 128, 2, "mixed"), (513, 256, 129, 16, 1, "runs"), (1100, 128, 520, 64, 4, "mixed"),
     (1537, 384, 200, 65, 2, "runs"), (100, 256, 72, 5, 700, "mixed"), (90, 128, 16, 4, 4096, "distinct"),
-    (20000, 128, 24, 4, 3, "mixed"), (17000, 128, 8, 2, 600, "runs"),
+    (20000, 128, 24, 4, 3, "mixed"), (17000, 128, 8, 2, 600, "runs"), (256, 256, 40, 16, 1, "runs"),
+    (255, 128, 33, 8, 300, "mixed"), (257, 384, 72, 24, 4, "mixed"), (300, 128, 40, 8, 4096, "distinct"),
+    (400, 256, 136, 100, 2, "runs"),
 ]
 
 
@@ -145,7 +147,7 @@ def test_forward_and_gradients(M, K, N, r, L, kind):
     assert torch.equal(got8[2], got[2])
 
 
-@pytest.mark.parametrize("M,L,kind", [(70, 3, "mixed"), (1300, 4, "runs"), (600, 700, "mixed"), (17000, 5, "mixed")])
+@pytest.mark.parametrize("M,L,kind", [(70, 3, "mixed"), (270, 9, "mixed"), (1300, 4, "runs"), (600, 700, "mixed"), (17000, 5, "mixed")])
 def test_kept_plan_same_bits(M, L, kind):
     t = make(M, 128, 40, 8, L, kind)
     plan = any4.lora_plan(t["ids"], L)
@@ -159,7 +161,7 @@ def test_kept_plan_same_bits(M, L, kind):
 
 
 @pytest.mark.parametrize("N", [72, 37])
-@pytest.mark.parametrize("M", [5, 200])
+@pytest.mark.parametrize("M", [5, 200, 400])
 def test_masked_and_non_finite_values(M, N):
     """A row's NaN or infinity stays in its row; rows without an adapter pass
     y through bit for bit whatever x holds; an unused adapter's weights are
@@ -195,7 +197,7 @@ def test_masked_and_non_finite_values(M, N):
     assert torch.equal(got[1][2], base[1][2]) and torch.equal(got[2][1:], base[2][1:])
 
 
-@pytest.mark.parametrize("M", [9, 150])
+@pytest.mark.parametrize("M", [9, 150, 350])
 def test_no_row_has_an_adapter(M):
     t = make(M, 128, 50, 4, 2, "mixed")
     t["ids"].fill_(-1)
