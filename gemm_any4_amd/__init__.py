@@ -35,6 +35,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -590,18 +591,22 @@ def gemm_int4_dx_raw(dy_ptr, packed_ptr, alpha_ptr, beta_ptr, dx_ptr, M, N, K, g
                                    ws_ptr, ws_bytes, _stream(stream))
 
 
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
 def lora_plan_bytes(M: int, L: int) -> int:
     return int(lib().any4_lora_plan_bytes(M, L))
 
 
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
 def lora_workspace_size(M: int, N: int, K: int, r: int, L: int) -> int:
     return int(lib().any4_lora_workspace_size(M, N, K, r, L))
 
 
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
 def lora_backward_workspace_size(M: int, N: int, K: int, r: int, L: int) -> int:
     return int(lib().any4_lora_backward_workspace_size(M, N, K, r, L))
 
 
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
 def gemm_dx_workspace_size(M: int, N: int, K: int, g: int) -> int:
     return int(lib().any4_gemm_dx_workspace_size(M, N, K, g))
 
@@ -738,10 +743,12 @@ def lora(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
     with _on(dev, stream):
         if out is None:
             out = torch.empty_like(y)
-        p_out = _tensor(out, "out", bf16, (M, N), dev)
+            p_out = _ptr(out)
+        else:
+            p_out = _tensor(out, "out", bf16, (M, N), dev)
         ws, p_ws, nbytes = _scratch(workspace, lora_workspace_size(M, N, K, r, L), dev)
-        check(lora_raw(p_x, p_A, p_B, p_scale, p_ids, p_plan, p_y, p_out, p_h, p_q, p_qs, M, N, K,
-                       r, L, p_ws, nbytes, _current_handle(dev.index)))
+        check(lib().any4_lora(p_x, p_A, p_B, p_scale, p_ids, p_plan, p_y, p_out, p_h, p_q, p_qs, M, N,
+                              K, r, L, p_ws, nbytes, _current_handle(dev.index)))
     return out
 
 
@@ -804,9 +811,9 @@ def lora_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, A: torch.T
         p_out = None if out is None else _tensor(out, "out", bf16, (M, K), dev)
         p_dA, p_dB = _tensor(dA, "dA", f32, (L, r, K), dev), _tensor(dB, "dB", f32, (L, r, N), dev)
         ws, p_ws, nbytes = _scratch(workspace, lora_backward_workspace_size(M, N, K, r, L), dev)
-        check(lora_backward_raw(p_dy, p_x, p_q, p_qs, p_h, p_A, p_B, p_scale, p_ids, p_plan, p_dx,
-                                p_out, p_dA, p_dB, M, N, K, r, L, p_ws, nbytes,
-                                _current_handle(dev.index)))
+        check(lib().any4_lora_backward(p_dy, p_x, p_q, p_qs, p_h, p_A, p_B, p_scale, p_ids, p_plan,
+                                       p_dx, p_out, p_dA, p_dB, M, N, K, r, L, p_ws, nbytes,
+                                       _current_handle(dev.index)))
     return out, dA, dB
 
 
@@ -826,10 +833,14 @@ def act8_save(x: torch.Tensor, act: tuple | None = None, stream=None) -> tuple:
     M, K = x.shape
     p_x = _tensor(x, "x", torch.bfloat16, (M, K), dev)
     with _on(dev, stream):
-        q, qs = act8_empty(x) if act is None else act
-        p_q = _tensor(q, "q", torch.int8, (M, K), dev)
-        p_qs = _tensor(qs, "qs", torch.float32, (M, K // 128), dev)
-        check(act8_save_raw(p_x, p_q, p_qs, M, K, _current_handle(dev.index)))
+        if act is None:
+            q, qs = act8_empty(x)
+            p_q, p_qs = q.data_ptr() or None, qs.data_ptr() or None
+        else:
+            q, qs = act
+            p_q = _tensor(q, "q", torch.int8, (M, K), dev)
+            p_qs = _tensor(qs, "qs", torch.float32, (M, K // 128), dev)
+        check(lib().any4_act8_save(p_x, p_q, p_qs, M, K, _current_handle(dev.index)))
     return q, qs
 
 
@@ -845,8 +856,10 @@ def act8_load(q: torch.Tensor, qs: torch.Tensor, out: torch.Tensor | None = None
     with _on(dev, stream):
         if out is None:
             out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-        p_x = _tensor(out, "out", torch.bfloat16, (M, K), dev)
-        check(act8_load_raw(p_q, p_qs, p_x, M, K, _current_handle(dev.index)))
+            p_x = out.data_ptr() or None
+        else:
+            p_x = _tensor(out, "out", torch.bfloat16, (M, K), dev)
+        check(lib().any4_act8_load(p_q, p_qs, p_x, M, K, _current_handle(dev.index)))
     return out
 
 
