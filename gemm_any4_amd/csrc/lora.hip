@@ -143,22 +143,17 @@ __device__ __forceinline__ Four block_scan(Four x, int (*wave_sum)[4])
 __device__ __forceinline__ int tiles_of(int rows) { return (rows + TILE_T - 1) / TILE_T; }
 __device__ __forceinline__ int chunks_of(int rows) { return (rows + CHUNK - 1) / CHUNK; }
 
-// From cnt[part][L+1] (rows of each adapter in each part of the batch): the
+// From cnt[part][L+1] (rows of each adapter in each of the batch's 16 n parts): the
 // plan's tables, s_rows and s_tile (rows and first tile of each adapter), and
 // cnt turned into the number of the adapter's rows in earlier parts.
-template <int PARTS>
-__device__ __forceinline__ void plan_tables(int* cnt, int M, int L, int* plan, int* s_rows,
+__device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, int* plan, int* s_rows,
                                             int* s_tile, int* s_chunk, int (*wave_sum)[4])
 {
     const PlanLayout p(M, L);
     const int tid = threadIdx.x, per = (L + 1 + PLAN_THREADS - 1) / PLAN_THREADS;
-    Four sum = {{0, 0, 0, 0}};
-    for (int e = 0; e < per; ++e) {
-        const int a = tid * per + e;
-        if (a > L)
-            break;
+    for (int a = tid; a <= L; a += PLAN_THREADS) {
         int n = 0;
-        for (int q0 = 0; q0 < PARTS; q0 += 16) {     // sixteen reads, then the writes
+        for (int q0 = 0; q0 < parts; q0 += 16) {     // sixteen reads, then the writes
             int c[16];
 #pragma unroll
             for (int q = 0; q < 16; ++q)
@@ -169,8 +164,15 @@ __device__ __forceinline__ void plan_tables(int* cnt, int M, int L, int* plan, i
                 n += c[q];
             }
         }
-        const int ch = a < L ? chunks_of(n) : 0;
         s_rows[a] = n;
+    }
+    __syncthreads();
+    Four sum = {{0, 0, 0, 0}};
+    for (int e = 0; e < per; ++e) {
+        const int a = tid * per + e;
+        if (a > L)
+            break;
+        const int n = s_rows[a], ch = a < L ? chunks_of(n) : 0;
         sum.v[0] += tiles_of(n);
         sum.v[1] += ch;
         sum.v[2] += ch > 1 ? ch : 0;
@@ -227,33 +229,37 @@ __device__ __forceinline__ void plan_tables(int* cnt, int M, int L, int* plan, i
     }
 }
 
-// STEPS x 64 rows a wave, their ids in registers from the first load on.  A chain
-// of waits, not of work: 5.8 us for 1031 rows, 7.6 us for 4096.
+// Up to STEPS x 64 rows a wave, their ids in registers from the first load on.
+// A chain of waits, not of work: 5.3 us for 1031 rows, 6.2 us for 4096, 13 us for
+// 16384.
 template <int STEPS>
 __global__ __launch_bounds__(PLAN_THREADS) void k_plan(const int* __restrict__ ids, int* plan, int M, int L)
 {
     __shared__ int cnt[PLAN_WAVES * (PLAN_ONE_L + 1)];
     __shared__ int s_rows[PLAN_ONE_L + 2], s_tile[PLAN_ONE_L + 2], s_chunk[PLAN_ONE_L + 2];
     __shared__ int wave_sum[PLAN_WAVES][4];
-    const int w = threadIdx.x >> 6, m0 = w * (STEPS * WAVE) + (threadIdx.x & 63);
+    const int w = threadIdx.x >> 6, per = (M + PLAN_THREADS - 1) / PLAN_THREADS;      // at most STEPS
+    const int m0 = w * (per * WAVE) + (threadIdx.x & 63);
     int a[STEPS], at[STEPS];
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
-        a[i] = m0 + i * WAVE < M ? ids[m0 + i * WAVE] : -1;
+        a[i] = i < per && m0 + i * WAVE < M ? ids[m0 + i * WAVE] : -1;
     for (int i = threadIdx.x; i < PLAN_WAVES * (L + 1); i += PLAN_THREADS)
         cnt[i] = 0;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
+        if (i >= per)
+            break;
         a[i] = adapter_of(a[i], L);
         at[i] = count_rows(a[i], m0 + i * WAVE < M, cnt + w * (L + 1));
     }
     __syncthreads();
-    plan_tables<PLAN_WAVES>(cnt, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
+    plan_tables(cnt, PLAN_WAVES, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
     int* rows = plan + PlanLayout(M, L).rows;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
-        if (m0 + i * WAVE < M)
+        if (i < per && m0 + i * WAVE < M)
             place_row(m0 + i * WAVE, cnt[w * (L + 1) + a[i]] + at[i], s_rows[a[i]],
                       static_cast<int64_t>(s_tile[a[i]]) * TILE_T, rows);
 }
@@ -267,16 +273,18 @@ __global__ __launch_bounds__(WAVE) void k_plan_count(const int* __restrict__ ids
         mine[i] = 0;
     __threadfence();     // the zeros are in place before the atomics below
     __syncthreads();
-    const int m0 = blockIdx.x * per, m1 = m0 + per < M ? m0 + per : M;     // per * PLAN_PARTS < 2^22
-    for (int m = m0 + threadIdx.x; m < m1; m += WAVE)
-        atomicAdd(&mine[adapter_of(ids[m], L)], 1);
+    const int m0 = blockIdx.x * per, m1 = m0 + per < M ? m0 + per : M;     // parts * per < 2^21
+    for (int b = m0; b < m1; b += WAVE) {
+        const int m = b + threadIdx.x;
+        count_rows(m < m1 ? adapter_of(ids[m], L) : -1, m < m1, mine);
+    }
 }
 
-__global__ __launch_bounds__(PLAN_THREADS) void k_plan_tables(int* cnt, int* plan, int M, int L)
+__global__ __launch_bounds__(PLAN_THREADS) void k_plan_tables(int* cnt, int* plan, int M, int L, int parts)
 {
     __shared__ int s_rows[MAX_ADAPTERS + 2], s_tile[MAX_ADAPTERS + 2], s_chunk[MAX_ADAPTERS + 2];
     __shared__ int wave_sum[PLAN_WAVES][4];
-    plan_tables<PLAN_PARTS>(cnt, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
+    plan_tables(cnt, parts, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
 }
 
 __global__ __launch_bounds__(WAVE) void k_plan_place(const int* __restrict__ ids, int* cnt, int* plan, int M, int L, int per)
@@ -307,17 +315,18 @@ void launch_plan(const int32_t* ids, int32_t* plan, int64_t M, int64_t L, hipStr
     if (plan_in_one(M, L)) {
         if (M <= 2 * PLAN_THREADS)
             hipLaunchKernelGGL(k_plan<2>, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
-        else if (M <= 4 * PLAN_THREADS)
-            hipLaunchKernelGGL(k_plan<4>, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
+        else if (M <= 8 * PLAN_THREADS)
+            hipLaunchKernelGGL(k_plan<8>, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
         else
             hipLaunchKernelGGL(k_plan<PLAN_ONE_M / PLAN_THREADS>, dim3(1), dim3(PLAN_THREADS), 0, stream, ids, plan, m, l);
         return;
     }
     int* cnt = plan + PlanLayout(M, L).words;
-    const int per = (m + PLAN_PARTS * WAVE - 1) / (PLAN_PARTS * WAVE) * WAVE;
-    hipLaunchKernelGGL(k_plan_count, dim3(PLAN_PARTS), dim3(WAVE), 0, stream, ids, cnt, m, l, per);
-    hipLaunchKernelGGL(k_plan_tables, dim3(1), dim3(PLAN_THREADS), 0, stream, cnt, plan, m, l);
-    hipLaunchKernelGGL(k_plan_place, dim3(PLAN_PARTS), dim3(WAVE), 0, stream, ids, cnt, plan, m, l, per);
+    const int steps = (m + WAVE - 1) / WAVE, parts = steps < PLAN_PARTS ? (steps + 15) / 16 * 16 : PLAN_PARTS;
+    const int per = (steps + parts - 1) / parts * WAVE;
+    hipLaunchKernelGGL(k_plan_count, dim3(parts), dim3(WAVE), 0, stream, ids, cnt, m, l, per);
+    hipLaunchKernelGGL(k_plan_tables, dim3(1), dim3(PLAN_THREADS), 0, stream, cnt, plan, m, l, parts);
+    hipLaunchKernelGGL(k_plan_place, dim3(parts), dim3(WAVE), 0, stream, ids, cnt, plan, m, l, per);
 }
 
 // ---------------------------------------------------------------------------
