@@ -1231,6 +1231,34 @@ __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
     const float f = slot < 0 && job.scaled && count ? p.scale[a] : 1.0f;
     const size_t width = slot < 0 ? job.D : static_cast<size_t>(job.cols) * 128;
     float* out = slot < 0 ? job.out + static_cast<size_t>(a) * p.r * width : job.part + static_cast<size_t>(slot) * p.r * width;
+    auto store = [&](float* o, f32x4_t v, int at) {       // columns at .. at + 3 of this job
+        v *= f;
+        if (WHOLE || slot >= 0 || at + 4 <= job.D) {
+            if (slot >= 0 || at < job.D)
+                *reinterpret_cast<f32x4_a4_t*>(o) = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (at + i < job.D)
+                    o[i] = v[i];
+        }
+    };
+    if (count <= 32) {           // the first wave has it all
+        if (w > 0)
+            return;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = j0 + 16 * rt + 4 * g + i;
+                if (j < p.r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        store(out + j * width + d + 4 * h,
+                              f32x4_t{acc[rt][4 * h][i], acc[rt][4 * h + 1][i], acc[rt][4 * h + 2][i], acc[rt][4 * h + 3][i]}, d + 4 * h);
+            }
+        return;
+    }
     // 16 ranks at a time, the eight waves' sums side by side, then added in
     // order by all threads: 4 columns of one rank each
 #pragma unroll
@@ -1248,19 +1276,8 @@ __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
 #pragma unroll
         for (int o = 0; o < WGRAD_WAVES; ++o)
             v += *reinterpret_cast<const f32x4_t*>(&red[o][q * STRIDE + e]);
-        if (j >= p.r)
-            continue;
-        v *= f;
-        float* o = out + j * width + at;
-        if (WHOLE || slot >= 0 || at + 4 <= job.D) {
-            if (slot >= 0 || at < job.D)
-                *reinterpret_cast<f32x4_a4_t*>(o) = v;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (at + i < job.D)
-                    o[i] = v[i];
-        }
+        if (j < p.r)
+            store(out + j * width + at, v, at);
     }
 }
 
