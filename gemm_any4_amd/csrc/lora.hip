@@ -711,6 +711,7 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
 // 2048 x 4096, rank 64, 18 us, where W and the parts come to twice those bytes
 // from the caches.  Tiles of 64 rows: 52 us at the first (a third as many waves
 // fit a CU); the base rows loaded 16 at a time: 84 us.
+
 // The factors of the weight gradients, in the order their operands take them:
 // of each tile (32 places) and 16 ranks, four places of a rank for each lane
 // (16 g + c: rank c, places 8 g + 0 .. 3), then the next four.

@@ -381,8 +381,9 @@ any4_status any4_quantize(const float* W, const float* ex, uint8_t* idx, uint16_
  * memory at `plan`, 16-byte aligned.  The plan depends on ids alone, so a
  * program makes it once per batch and hands it to the calls of every layer;
  * calls without one make their own in the workspace (small batches, of at
- * most 64 rows, or 256 with few adapters in any4_lora, need none and ignore it).  any4_lora_plan_bytes gives 0 for sizes out
- * of range and M = 0.  M = 0 is a no-op.
+ * most 64 rows, or 256 with few adapters in any4_lora, need none and ignore
+ * it).  any4_lora_plan_bytes gives 0 for sizes out of range and M = 0.
+ * M = 0 is a no-op.
  * Errors: ANY4_E_SHAPE, ANY4_E_NULL, ANY4_E_ALIGN, ANY4_E_WORKSPACE (bytes too
  * small), ANY4_E_HIP.
  */
@@ -425,11 +426,13 @@ any4_status any4_lora(const uint16_t* x, const uint16_t* A, const uint16_t* B, c
  * dA and dB are written whole: an adapter without rows gets zeros.
  *   x      device, [M][K] bf16, or NULL with q, qs: x in 8 bits (its values
  *          q * qs enter dA unrounded).  x goes first where both are given.
- *   dx_out may be dx itself.  dx_out, dA and dB may each be NULL: not wanted
- *          (x, q, qs are then not read without dA, h not without dB).
+ *   dx_out may be dx itself, else must not overlap an input.  dx_out, dA and
+ *          dB may each be NULL: not wanted (x, q, qs are then not read without
+ *          dA, h not without dB).
  *   plan, workspace  as for any4_lora, any4_lora_backward_workspace_size bytes.
- *   N >= 1; M = 0 writes dA = dB = 0 (the other pointers may be NULL).  x, A, q, dx, dx_out, plan and workspace need 16-byte
- *   alignment, the others that of their elements.
+ *   N >= 1; M = 0 writes dA = dB = 0 (the other pointers may be NULL).
+ *   x, A, q, dx, dx_out, plan and workspace need 16-byte alignment, the others
+ *   that of their elements.
  * Errors: as any4_lora.
  */
 size_t any4_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L);
