@@ -137,7 +137,7 @@ __device__ __forceinline__ void decode(const ByteTable<FMT>& t, const uint32_t (
 __device__ __forceinline__ uint32_t pair_rows(uint32_t v, bool odd)
 {
     const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xf, 0xf, true));
-    return odd ? __builtin_amdgcn_perm(v, other, 0x07060302u) : __builtin_amdgcn_perm(other, v, 0x05040100u);
+    return __builtin_amdgcn_perm(other, v, odd ? 0x03020706u : 0x05040100u);     // one instruction, its selector kept
 }
 
 // ---------------------------------------------------------------------------
@@ -368,12 +368,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_dx(const DxArgs p)
 // pair their values, LDS of the wave's own turns the block (no barrier), and
 // the matrix cores multiply it with dy, whose rows come in 128-byte pieces and
 // are turned the same way (loaded as operands they cost the vector cache a
-// clock for every lane).  Eight waves share the rows out, and their sums meet
-// in LDS at the end; further splits of the rows leave fp32 partial sums.  What
-// bounds it is the vector work of the lookups, five instructions a weight.
-constexpr int FEW_M = 128;
+// clock for every lane).  The next step's weights are asked for once this one's
+// tables stand (14336 x 4096, 128 rows: 38 us, 39.5 without).  Eight waves share the
+// rows out, and their sums meet in LDS at the end; further splits of the rows
+// leave fp32 partial sums.  What bounds it is a step's chain of LDS and vector
+// work (lookups and pairing, four instructions a weight) with two waves a SIMD.
+// FEW_M, whole calls: 256 rows 4096 x 4096 26 us, turned first 35; 14336 x 4096 63
+// and 92; 4096 x 14336 72 and 86; 512 x 512 9 and 11; 320 rows 4096 x 4096 43 and 37.
+constexpr int FEW_M = 256;
 constexpr int FEW_THREADS = 512;
-constexpr int FEW_STRIDE = 36;       // dwords of a turned row of 64 n
+// Dwords of a turned row of 64 n: the 16 rows of an operand read lie in 64 banks.
+// Every other pair of rows has its halves exchanged, so that even and odd lanes
+// write to other banks too.
+constexpr int FEW_STRIDE = 36;
 constexpr int FEW_PITCH = 9;         // 16-byte pieces of a staged row of dy
 
 struct FewArgs {
@@ -392,7 +399,8 @@ template <int FMT, int MB, bool WHOLE>
 __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
 {
     constexpr int WAVES = FEW_THREADS / WAVE, TURNED = 32 * FEW_STRIDE / 4, STAGED = 16 * FEW_PITCH;     // 16-byte pieces a wave
-    constexpr int ROOM = TURNED + STAGED > 8 * WAVE ? TURNED + STAGED : 8 * WAVE;
+    constexpr int SUMS = MB > 1 ? 2 : 1;         // blocks of 16 rows whose sums meet at once
+    constexpr int ROOM = TURNED + STAGED > 8 * WAVE * SUMS ? TURNED + STAGED : 8 * WAVE * SUMS;
     __shared__ u32x4_t room[WAVES * ROOM];       // the waves' blocks, and afterwards their sums
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
     const int Kc = p.K / 128, chunk = blockIdx.x % Kc, m0 = blockIdx.x / Kc * (16 * MB);
@@ -410,16 +418,18 @@ __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
 #pragma unroll
         for (int b = 0; b < 8; ++b)
             acc[i][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int st = s0; st < s1; ++st) {
-        const int row = st * 64 + lane;
-        uint32_t code[4][4] = {};
-        RowTable r = {};                // rows behind the last: weights of 0
-        if (row < p.N) {
-            r = fetch_table<FMT>(p.lut, p.alpha, p.beta, row, Kc, chunk, p.g);
+    uint32_t next[4][4];
+    RowTable r;
+    auto fetch_weights = [&](int st) __attribute__((always_inline)) {
+        const int row = st * 64 + lane < p.N ? st * 64 + lane : 0;
+        r = fetch_table<FMT>(p.lut, p.alpha, p.beta, row, Kc, chunk, p.g);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                fetch_codes<FMT>(p.packed, row, Kc, chunk, q, code[q]);
-        }
+        for (int q = 0; q < 4; ++q)
+            fetch_codes<FMT>(p.packed, row, Kc, chunk, q, next[q]);
+    };
+    if (s0 < s1)
+        fetch_weights(s0);
+    for (int st = s0; st < s1; ++st) {
         // lane: piece lane % 8 of row 8 h + lane / 8
         Piece x[MB][2];
         const bool edge = st * 64 + 64 > p.N;
@@ -444,37 +454,55 @@ __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
             for (int kk = 0; kk < 2; ++kk)
                 d[i][kk] = __builtin_bit_cast(bf16x8_t, staged[c * FEW_PITCH + 4 * kk + g]);
         }
-        const ByteTable<FMT> t(r);
+        ByteTable<FMT> t(r);
+        if (st * 64 + lane >= p.N)      // rows behind the last: weights of 0
+#pragma unroll
+            for (int i = 0; i < ByteTable<FMT>::ENTRIES / 4; ++i)
+                t.lo[i] = t.hi[i] = 0u;
+        uint32_t code[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                code[q][i] = next[q][i];
+        if (st + 1 < s1)
+            fetch_weights(st + 1);
+        __builtin_amdgcn_sched_barrier(0);      // asked for here, not where they are used
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             uint32_t v[16];
             decode(t, code[q], v);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                turned[(first_k(i) + 2 * (lane & 1)) * FEW_STRIDE + lane / 2] = pair_rows(v[i], lane & 1);
+                turned[(first_k(i) + 2 * (lane & 1)) * FEW_STRIDE + (lane / 2 ^ 16 * ((first_k(i) >> 1 ^ lane) & 1))] =
+                    pair_rows(v[i], lane & 1);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const bf16x8_t wv = *reinterpret_cast<const bf16x8_t*>(&turned[(16 * b + c) * FEW_STRIDE + 16 * kk + 4 * g]);
+                    const bf16x8_t wv = *reinterpret_cast<const bf16x8_t*>(&turned[(16 * b + c) * FEW_STRIDE + (16 * kk ^ 8 * (c & 2)) + 4 * g]);
 #pragma unroll
                     for (int i = 0; i < MB; ++i)
                         acc[i][2 * q + b] = mfma(wv, d[i][kk], acc[i][2 * q + b]);
                 }
         }
     }
-    f32x4_t* red = reinterpret_cast<f32x4_t*>(room);      // [WAVES][8][WAVE]
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(room);      // [SUMS][WAVES][8][WAVE]
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-        __syncthreads();
+        if (i % SUMS == 0) {
+            __syncthreads();
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
-            red[(w * 8 + b) * WAVE + lane] = acc[i][b];
-        __syncthreads();
+            for (int e = 0; e < SUMS; ++e)
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    red[((e * WAVES + w) * 8 + b) * WAVE + lane] = acc[i + e][b];
+            __syncthreads();
+        }
         f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};             // wave w: the sums of its 16 k
 #pragma unroll
         for (int o = 0; o < WAVES; ++o)
-            v += red[(o * 8 + w) * WAVE + lane];
+            v += red[((i % SUMS * WAVES + o) * 8 + w) * WAVE + lane];
         const int m = m0 + 16 * i + c;
         if (m >= p.M)
             continue;
@@ -544,11 +572,9 @@ __global__ __launch_bounds__(256) void k_dx_zero(uint16_t* dx, size_t octs)
 // ---------------------------------------------------------------------------
 int64_t padded(int64_t N) { return (N + STEP - 1) / STEP * STEP; }
 
-// How a product is run: decoded on the way (few rows), else 256 x 256 tiles
-// where they fill the chip (or nearly, or in long enough splits of n), else 128 x
-// 128.  n is split where the tiles alone leave the 256 CUs idle; the partial sums
-// are fp32.  128 rows decoded on the way take 25 us at 4096 x 4096 and 48 us at
-// 14336 x 4096, turned first 37 and 72; 192 rows 45 and 106 against 37 and 78.
+// How a product is run: decoded on the way (few rows), else turned first, in
+// 256 x 256 or 128 x 128 tiles, n split where that leaves less to do for the
+// longest-working CU; the partial sums are fp32.
 struct Shape {
     int few;                 // blocks of 16 rows of a workgroup, 0: turned first
     bool big;
@@ -560,28 +586,45 @@ Shape dx_shape(int64_t M, int64_t N, int64_t K)
 {
     const int64_t steps = padded(N) / STEP;
     Shape s{0, false, 0, 1};
-    int64_t S;
+    int64_t least = INT64_MAX;
     if (M <= FEW_M) {
         s.few = M <= 16 ? 1 : 4;
         s.tiles = (M + 16 * s.few - 1) / (16 * s.few) * (K / 128);
-        // two workgroups a CU for 16 rows; one where the partial sums are larger
-        S = ((M <= 16 ? 512 : 256) + s.tiles - 1) / s.tiles;
-        S = S < steps / 8 ? S : steps / 8;      // a step for each of its waves
-    } else {
-        const int64_t big = (M + 255) / 256 * (K / 256), small = (M + 127) / 128 * (K / 128);
-        // the large tiles run a product half as fast again, but split they leave
-        // four times as many partial sums for the same workgroups: worth it from
-        // 32 steps a split (1024 x 14336 x 4096 in four: 168 -> 132 us with the sum;
-        // 1024 x 4096 x 4096, 16 steps: no gain)
-        S = big >= 192 ? 1 : (256 + big - 1) / (big > 0 ? big : 1);
-        s.big = K % 256 == 0 && (S == 1 || (S <= 16 && steps / S >= 32));
-        s.tiles = s.big ? big : small;
-        if (!s.big) {
-            S = (512 + s.tiles - 1) / s.tiles;
-            S = S < steps / 4 ? S : steps / 4;      // each at least 4 steps
+        // Of the splits that leave each wave a step, the one with the fewest steps
+        // over all rounds of the chip (its LDS holds two workgroups of 16 rows a CU,
+        // one of 64), two more a round to start and to add up.  As many workgroups as
+        // there are CUs, rounds or not: 64 rows, 4096 x 14336 (112 tiles) 36 us
+        // against 25; 16 rows 23 against 19.
+        const int64_t most = steps / 8 < 16 ? steps / 8 : 16, room = s.few == 1 ? 512 : 256;
+        for (int64_t n = 1; n == 1 || n <= most; ++n) {
+            const int64_t time = (s.tiles * n + room - 1) / room * ((steps + 8 * n - 1) / (8 * n) + 2);
+            if (time <= least) {
+                least = time;
+                s.S = static_cast<int>(n);
+            }
         }
+        return s;
     }
-    s.S = static_cast<int>(S < 1 ? 1 : S > 16 ? 16 : S);
+    // Turned first: the time of each choice in units of 10 ns, from what steps were
+    // measured to take (a large tile 1.6 us; a small one 0.7, two on a CU 0.95 together;
+    // splits 7 us and 0.3 us a MB of partial sums to write, read and add) on the CU with
+    // the most tiles.  Splits go up to two workgroups a CU, each at least four steps.
+    // A fixed number of workgroups instead (256 large or 512 small, rounded up),
+    // whole calls in us: M 2048, 4096 x 4096 91 against 75 here; 1500 83 against 69;
+    // 320 44 against 39; 600, 14336 x 4096 152 against 121; 2500 378 against 316; 600,
+    // 4096 x 14336 164 against 126; 3000, 2048 x 2048 57 against 40.
+    const int64_t tiles[2] = {(M + 127) / 128 * (K / 128), K % 256 ? 0 : (M + 255) / 256 * (K / 256)};
+    for (int big = 0; big < 2; ++big)
+        for (int64_t n = 1; tiles[big] && n <= 16 && (n == 1 || (tiles[big] * n <= 512 && steps / n >= 4)); ++n) {
+            const int64_t on_cu = (tiles[big] * n + 255) / 256, step = big ? 160 * on_cu : on_cu / 2 * 95 + on_cu % 2 * 70;
+            const int64_t time = step * ((steps + n - 1) / n) + (n > 1 ? 700 + n * M * K / 8333 : 300);
+            if (time < least) {
+                least = time;
+                s.big = big;
+                s.tiles = tiles[big];
+                s.S = static_cast<int>(n);
+            }
+        }
     return s;
 }
 
@@ -589,10 +632,12 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 size_t wt_bytes(int64_t N, int64_t K) { return up256(static_cast<size_t>(K) * padded(N) * 2); }
 
-size_t dx_part_bytes(int64_t M, int64_t N, int64_t K)
+size_t dx_bytes(const Shape& s, int64_t M, int64_t N, int64_t K)
 {
-    const int S = dx_shape(M, N, K).S;
-    return S > 1 ? up256(static_cast<size_t>(S) * M * K * 4) : 0;
+    const size_t part = s.S > 1 ? up256(static_cast<size_t>(s.S) * M * K * 4) : 0;
+    if (s.few)
+        return part + 256;       // never 0 where the call has work
+    return wt_bytes(N, K) + up256(static_cast<size_t>(M) * padded(N) * 2) + part;
 }
 
 bool dx_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t g)
@@ -615,7 +660,8 @@ any4_status gemm_dx(int fmt, const uint16_t* dy, const uint8_t* packed, const ui
     if (!is_aligned(dx, 16) || (N > 0 && (!is_aligned(dy, 2) || !is_aligned(packed, 16) || !is_aligned(lut, 2) ||
                                           !is_aligned(alpha, 2) || !is_aligned(beta, 2) || !is_aligned(workspace, 16))))
         return ANY4_E_ALIGN;
-    if (N > 0 && workspace_bytes < any4_gemm_dx_workspace_size(M, N, K, g))
+    const Shape shape = N > 0 ? dx_shape(M, N, K) : Shape{};
+    if (N > 0 && workspace_bytes < dx_bytes(shape, M, N, K))
         return ANY4_E_WORKSPACE;
     (void)hipGetLastError();
     if (N == 0) {
@@ -624,7 +670,6 @@ any4_status gemm_dx(int fmt, const uint16_t* dy, const uint8_t* packed, const ui
         return launch_status();
     }
     const int Np = static_cast<int>(padded(N));
-    const Shape shape = dx_shape(M, N, K);
     const size_t quads = static_cast<size_t>(M) * K / 4;
     const dim3 sum_grid(static_cast<unsigned>((quads + 255) / 256));
     if (shape.few) {
@@ -679,9 +724,7 @@ size_t any4_gemm_dx_workspace_size(int64_t M, int64_t N, int64_t K, int64_t g)
 {
     if (M <= 0 || N <= 0 || K <= 0 || !dx_sizes_ok(M, N, K, g))
         return 0;
-    if (dx_shape(M, N, K).few)
-        return dx_part_bytes(M, N, K) + 256;      // never 0 where the call has work
-    return wt_bytes(N, K) + up256(static_cast<size_t>(M) * padded(N) * 2) + dx_part_bytes(M, N, K);
+    return dx_bytes(dx_shape(M, N, K), M, N, K);
 }
 
 any4_status any4_gemm_dx(const uint16_t* dy, const uint8_t* packed, const uint16_t* lut, const uint16_t* alpha,

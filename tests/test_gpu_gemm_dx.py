@@ -62,7 +62,7 @@ def check(dx, dy, w):
 @pytest.mark.parametrize("fmt", ["any4", "int4", "any2", "any3"])
 @pytest.mark.parametrize("M,N,K,g", [(1, 1, 128, 128), (1, 64, 256, 256), (5, 37, 384, 128), (64, 128, 256, 128),
                                      (16, 1000, 256, 128), (100, 333, 384, 384), (129, 200, 512, 512),
-                                     (300, 1000, 128, 128)])
+                                     (300, 1000, 128, 128), (290, 200, 512, 512), (257, 1, 128, 128)])
 def test_formats_and_odd_sizes(fmt, M, N, K, g):
     call, w = layer(fmt, N, K, g)
     dy = grad(M, N)
@@ -72,7 +72,9 @@ def test_formats_and_odd_sizes(fmt, M, N, K, g):
 @pytest.mark.parametrize("M,N,K,g", [(16, 4096, 4096, 128), (64, 4099, 1024, 1024), (1000, 2048, 1152, 128),
                                      (513, 1024, 4096, 512), (1, 14336, 512, 128), (3001, 200, 4096, 128),
                                      (2999, 333, 4352, 256), (128, 4100, 2048, 256), (17, 1000, 14336, 1024),
-                                     (2000, 8200, 2048, 256), (129, 4096, 1024, 128)])
+                                     (2000, 8200, 2048, 256), (129, 4096, 1024, 128),
+                                     (193, 4099, 4096, 128), (256, 14336, 512, 128), (260, 4096, 1024, 128),
+                                     (600, 14336, 2048, 128), (1500, 4100, 4096, 4096), (2500, 8192, 2304, 256)])
 def test_larger_sizes(M, N, K, g):
     """Sums split over workgroups, ragged last tiles, padded copies of dy, both
     tile sizes and the form for few rows."""
@@ -82,7 +84,7 @@ def test_larger_sizes(M, N, K, g):
 
 
 @pytest.mark.parametrize("fmt", ["any4", "int4", "any2", "any3"])
-@pytest.mark.parametrize("N", [100, 190])
+@pytest.mark.parametrize("N", [100, 190, 300])
 def test_one_hot_rows_give_the_weights(fmt, N):
     """dy = unit vectors: dx is W itself, bit for bit."""
     call, w = layer(fmt, N, 256, 128)
@@ -90,7 +92,7 @@ def test_one_hot_rows_give_the_weights(fmt, N):
     assert torch.equal(call(dy).double(), w)
 
 
-@pytest.mark.parametrize("M", [20, 140])
+@pytest.mark.parametrize("M", [20, 140, 270])
 @pytest.mark.parametrize("N", [64, 100])
 def test_rows_do_not_touch_each_other(M, N):
     """NaN and infinities in one row of dy, also behind an odd row's end."""
@@ -107,7 +109,7 @@ def test_rows_do_not_touch_each_other(M, N):
 
 
 @pytest.mark.parametrize("fmt", ["any4", "any2", "any3"])
-@pytest.mark.parametrize("M", [3, 150])
+@pytest.mark.parametrize("M", [3, 150, 300])
 def test_table_values_of_every_kind(fmt, M):
     """Negative zeros, subnormals, infinities and NaN in a row's table come out
     as any4_dequant writes them."""
@@ -136,15 +138,16 @@ def test_table_values_of_every_kind(fmt, M):
     assert same.all() and torch.isfinite(got[1:, torch.isfinite(ref[0])]).all()
 
 
-def test_unaligned_rows_and_caller_buffers():
+@pytest.mark.parametrize("M", [70, 300])
+def test_unaligned_rows_and_caller_buffers(M):
     call, w = layer("any4", 128, 256, 128)
-    dy = grad(70, 128)
+    dy = grad(M, 128)
     ref = call(dy)
-    room = torch.zeros(70 * 128 + 8, dtype=torch.bfloat16, device=gu.DEV)
-    room[1:1 + 70 * 128] = dy.flatten()
+    room = torch.zeros(M * 128 + 8, dtype=torch.bfloat16, device=gu.DEV)
+    room[1:1 + M * 128] = dy.flatten()
     out = torch.empty_like(ref)
-    ws = torch.full((any4.gemm_dx_workspace_size(70, 128, 256, 128),), 255, dtype=torch.uint8, device=gu.DEV)
-    assert call(room[1:1 + 70 * 128].view(70, 128), out=out, workspace=ws) is out
+    ws = torch.full((any4.gemm_dx_workspace_size(M, 128, 256, 128),), 255, dtype=torch.uint8, device=gu.DEV)
+    assert call(room[1:1 + M * 128].view(M, 128), out=out, workspace=ws) is out
     assert torch.equal(out, ref)
 
 
@@ -158,7 +161,7 @@ def test_empty_sizes():
     assert dx.shape == (3, 256) and not dx.any()
 
 
-@pytest.mark.parametrize("M,N", [(40, 192), (40, 100)])
+@pytest.mark.parametrize("M,N", [(40, 192), (40, 100), (300, 192), (300, 100)])
 def test_captured_and_replayed(M, N):
     call, _ = layer("any4", N, 512, 128)
     dy = grad(M, N)
