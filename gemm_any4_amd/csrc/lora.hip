@@ -1323,13 +1323,27 @@ int round16(int64_t r) { return static_cast<int>((r + 15) / 16 * 16); }
 
 // Ranges that a shrink's D is split into: enough workgroups for the chip, at
 // least 128 d for each wave, and few enough that the parts stay small beside
-// the rows (the expand kernel reads them all).
+// the rows (the expand kernel reads them all).  Beyond rank 32 the registers
+// leave a CU one workgroup: the split with the fewest steps over all rounds of
+// the 256 CUs, two more a round to start and to add up.  (Two a CU and up to four
+// parts there too, whole calls in us: 1000 x 14336 to 4096, rank 128, 48 against 43;
+// 2048 x 4096, rank 128, 48 against 42; 8000 x 4096, rank 64, 77 against 71.)
 int split_of(int64_t M, int64_t L, int64_t D, int64_t r, bool ballots)
 {
     const int64_t steps = (D + 127) / 128, most = (steps + SHRINK_WAVES - 1) / SHRINK_WAVES;
     const int64_t groups = tile_bound(M, L, ballots) * ((r + 63) / 64);
-    const int64_t cap = M <= SMALL_M ? 16 : ballots ? 8 : 4;
+    const int64_t cap = M <= SMALL_M ? 16 : ballots || r > 32 ? 8 : 4;
     int64_t want = ballots ? cap : (512 + groups - 1) / groups;
+    if (!ballots && r > 32) {
+        int64_t least = INT64_MAX;
+        for (int64_t n = 1; n <= cap; ++n) {
+            const int64_t time = (groups * n + 255) / 256 * ((steps + SHRINK_WAVES * n - 1) / (SHRINK_WAVES * n) + 2);
+            if (time < least) {
+                least = time;
+                want = n;
+            }
+        }
+    }
     want = want < cap ? want : cap;
     return static_cast<int>(want < most ? want : most);
 }
