@@ -107,34 +107,39 @@ __device__ __forceinline__ void place_row(int m, int at, int n, int64_t first, i
             rows[first + i] = m;
 }
 
-struct Four {
-    int v[4];
+struct Three {
+    int v[3];
 };
 
-// Exclusive sums over the block's threads.
-__device__ __forceinline__ Four block_scan(Four x, int (*wave_sum)[4])
+// Exclusive sums over the block's threads (one_wave: only the first 64 threads'
+// values count, and only they ask).
+__device__ __forceinline__ Three block_scan(Three x, int (*wave_sum)[3], bool one_wave)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    Four s = x;
-    for (int d = 1; d < WAVE; d <<= 1) {
-        int o[4];
+    Three s = x;
+    if (!one_wave || w == 0)
+        for (int d = 1; d < WAVE; d <<= 1) {
+            int o[3];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            o[q] = __shfl_up(s.v[q], d);
+            for (int q = 0; q < 3; ++q)
+                o[q] = __shfl_up(s.v[q], d);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            s.v[q] += lane >= d ? o[q] : 0;
+            for (int q = 0; q < 3; ++q)
+                s.v[q] += lane >= d ? o[q] : 0;
+        }
+    if (!one_wave) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+            if (lane == 63)
+                wave_sum[w][q] = s.v[q];
+        __syncthreads();
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        if (lane == 63)
-            wave_sum[w][q] = s.v[q];
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 3; ++q) {
         int before = 0;
-        for (int i = 0; i < PLAN_WAVES; ++i)
-            before += i < w ? wave_sum[i][q] : 0;
+        if (!one_wave)
+            for (int i = 0; i < PLAN_WAVES; ++i)
+                before += i < w ? wave_sum[i][q] : 0;
         s.v[q] += before - x.v[q];
     }
     return s;
@@ -147,7 +152,7 @@ __device__ __forceinline__ int chunks_of(int rows) { return (rows + CHUNK - 1) /
 // plan's tables, s_rows and s_tile (rows and first tile of each adapter), and
 // cnt turned into the number of the adapter's rows in earlier parts.
 __device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, int* plan, int* s_rows,
-                                            int* s_tile, int* s_chunk, int (*wave_sum)[4])
+                                            int* s_tile, int* s_chunk, int* s_slot, int (*wave_sum)[3])
 {
     const PlanLayout p(M, L);
     const int tid = threadIdx.x, per = (L + 1 + PLAN_THREADS - 1) / PLAN_THREADS;
@@ -167,7 +172,7 @@ __device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, i
         s_rows[a] = n;
     }
     __syncthreads();
-    Four sum = {{0, 0, 0, 0}};
+    Three sum = {{0, 0, 0}};
     for (int e = 0; e < per; ++e) {
         const int a = tid * per + e;
         if (a > L)
@@ -177,7 +182,7 @@ __device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, i
         sum.v[1] += ch;
         sum.v[2] += ch > 1 ? ch : 0;
     }
-    Four at = block_scan(sum, wave_sum);
+    Three at = block_scan(sum, wave_sum, L < WAVE);
     for (int e = 0; e < per; ++e) {
         const int a = tid * per + e;
         if (a > L)
@@ -185,6 +190,7 @@ __device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, i
         const int n = s_rows[a], ch = a < L ? chunks_of(n) : 0;
         s_tile[a] = at.v[0];
         s_chunk[a] = at.v[1];
+        s_slot[a] = at.v[2];
         plan[p.first + a] = at.v[0];
         plan[p.count + a] = n;
         plan[p.slot + a] = at.v[2];
@@ -223,21 +229,22 @@ __device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, i
                 o[0] = lo;
                 o[1] = s_tile[lo] * TILE_T + before;
                 o[2] = rows;
-                o[3] = start[lo + 1] - start[lo] > 1 ? plan[p.slot + lo] + t - start[lo] : -1;
+                o[3] = start[lo + 1] - start[lo] > 1 ? s_slot[lo] + t - start[lo] : -1;
             }
         }
     }
 }
 
 // Up to STEPS x 64 rows a wave, their ids in registers from the first load on.
-// A chain of waits, not of work: 5.3 us for 1031 rows, 6.2 us for 4096, 13 us for
-// 16384.
+// A chain of waits, not of work: 3.9 us for 1031 rows, 4.9 us for 4096, 11.7 us for
+// 16384 (1.5 us more with the sums over all waves where the first holds all the
+// adapters).
 template <int STEPS>
 __global__ __launch_bounds__(PLAN_THREADS) void k_plan(const int* __restrict__ ids, int* plan, int M, int L)
 {
     __shared__ int cnt[PLAN_WAVES * (PLAN_ONE_L + 1)];
-    __shared__ int s_rows[PLAN_ONE_L + 2], s_tile[PLAN_ONE_L + 2], s_chunk[PLAN_ONE_L + 2];
-    __shared__ int wave_sum[PLAN_WAVES][4];
+    __shared__ int s_rows[PLAN_ONE_L + 2], s_tile[PLAN_ONE_L + 2], s_chunk[PLAN_ONE_L + 2], s_slot[PLAN_ONE_L + 2];
+    __shared__ int wave_sum[PLAN_WAVES][3];
     const int w = threadIdx.x >> 6, per = (M + PLAN_THREADS - 1) / PLAN_THREADS;      // at most STEPS
     const int m0 = w * (per * WAVE) + (threadIdx.x & 63);
     int a[STEPS], at[STEPS];
@@ -255,7 +262,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan(const int* __restrict__ i
         at[i] = count_rows(a[i], m0 + i * WAVE < M, cnt + w * (L + 1));
     }
     __syncthreads();
-    plan_tables(cnt, PLAN_WAVES, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
+    plan_tables(cnt, PLAN_WAVES, M, L, plan, s_rows, s_tile, s_chunk, s_slot, wave_sum);
     int* rows = plan + PlanLayout(M, L).rows;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
@@ -282,9 +289,10 @@ __global__ __launch_bounds__(WAVE) void k_plan_count(const int* __restrict__ ids
 
 __global__ __launch_bounds__(PLAN_THREADS) void k_plan_tables(int* cnt, int* plan, int M, int L, int parts)
 {
-    __shared__ int s_rows[MAX_ADAPTERS + 2], s_tile[MAX_ADAPTERS + 2], s_chunk[MAX_ADAPTERS + 2];
-    __shared__ int wave_sum[PLAN_WAVES][4];
-    plan_tables(cnt, parts, M, L, plan, s_rows, s_tile, s_chunk, wave_sum);
+    __shared__ int s_rows[MAX_ADAPTERS + 2], s_tile[MAX_ADAPTERS + 2], s_chunk[MAX_ADAPTERS + 2],
+        s_slot[MAX_ADAPTERS + 2];
+    __shared__ int wave_sum[PLAN_WAVES][3];
+    plan_tables(cnt, parts, M, L, plan, s_rows, s_tile, s_chunk, s_slot, wave_sum);
 }
 
 __global__ __launch_bounds__(WAVE) void k_plan_place(const int* __restrict__ ids, int* cnt, int* plan, int M, int L, int per)
