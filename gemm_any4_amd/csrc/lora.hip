@@ -1290,7 +1290,9 @@ __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
     }
 }
 
-// Adapters of several chunks: their partial sums in order.  Adapters without
+// Adapters of several chunks: their partial sums in order, 4 columns a thread and
+// four chunks' loads at a time (2048 rows of 4 adapters, rank 64, 4096 + 4099
+// columns 5.7 us; one column a thread 8.6).  Adapters without
 // rows: zeros.  (An adapter of one chunk is done.)
 __global__ __launch_bounds__(256) void k_wgrad_sum(const WgradArgs p)
 {
@@ -1301,7 +1303,7 @@ __global__ __launch_bounds__(256) void k_wgrad_sum(const WgradArgs p)
     const int n = chunks_of(p.b.plan[l.count + a]);
     if (n == 1)
         return;
-    int d = blockIdx.x * 256 + threadIdx.x;
+    int d = (blockIdx.x * 256 + threadIdx.x) * 4;
     const int first = p.job[0].cols * 128;
     const bool second = d >= first;
     const WgradJob job = second ? p.job[1] : p.job[0];
@@ -1310,10 +1312,27 @@ __global__ __launch_bounds__(256) void k_wgrad_sum(const WgradArgs p)
         return;
     const size_t width = static_cast<size_t>(job.cols) * 128;
     const float* src = job.part + (static_cast<size_t>(p.b.plan[l.slot + a]) * p.r + j) * width + d;
-    float v = 0.0f;
-    for (int i = 0; i < n; ++i)
-        v += src[static_cast<size_t>(i) * p.r * width];
-    job.out[(static_cast<size_t>(a) * p.r + j) * job.D + d] = v * (job.scaled && n ? p.scale[a] : 1.0f);
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i0 = 0; i0 < n; i0 += 4) {
+        f32x4_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = i0 + i < n ? *reinterpret_cast<const f32x4_t*>(src + static_cast<size_t>(i0 + i) * p.r * width)
+                              : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v += x[i];
+    }
+    v *= job.scaled && n ? p.scale[a] : 1.0f;
+    float* o = job.out + (static_cast<size_t>(a) * p.r + j) * job.D + d;
+    if (d + 4 <= job.D) {
+        *reinterpret_cast<f32x4_a4_t*>(o) = v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (d + e < job.D)
+                o[e] = v[e];
+    }
 }
 
 // Gradients of an empty batch.
@@ -1491,7 +1510,7 @@ void launch_wgrad(const WgradArgs& a, hipStream_t stream)
     }
 #undef WGRAD
     if (a.chunked)
-        hipLaunchKernelGGL(k_wgrad_sum, dim3((cols * 128 + 255) / 256, static_cast<unsigned>(a.b.L), static_cast<unsigned>(a.r)),
+        hipLaunchKernelGGL(k_wgrad_sum, dim3((cols * 32 + 255) / 256, static_cast<unsigned>(a.b.L), static_cast<unsigned>(a.r)),
                            dim3(256), 0, stream, a);
 }
 

@@ -114,7 +114,8 @@ SHAPES = [
     (1537, 384, 200, 65, 2, "runs"), (100, 256, 72, 5, 700, "mixed"), (90, 128, 16, 4, 4096, "distinct"),
     (20000, 128, 24, 4, 3, "mixed"), (17000, 128, 8, 2, 600, "runs"), (256, 256, 40, 16, 1, "runs"),
     (255, 128, 33, 8, 300, "mixed"), (257, 384, 72, 24, 4, "mixed"), (300, 128, 40, 8, 4096, "distinct"),
-    (400, 256, 136, 100, 2, "runs"),
+    (400, 256, 136, 100, 2, "runs"), (500, 128, 24, 4, 63, "mixed"), (500, 128, 24, 4, 64, "mixed"),
+    (1500, 128, 27, 4, 65, "runs"), (3300, 256, 30, 40, 2, "mixed"), (5000, 128, 129, 65, 1, "runs"),
 ]
 
 
