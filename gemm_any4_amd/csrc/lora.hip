@@ -580,7 +580,7 @@ __global__ __launch_bounds__(ACT8_THREADS) void k_act8_load(const uint8_t* __res
 // splits' in the expand kernel, both in a fixed order.
 // Bound by the bytes of `in`: 4096 x 14336, rank 16, 31 us (3.8 TB/s); 4096 x 4096
 // 12 us, of which six are the launch and its chain of waits (plan, rows, data),
-// and 17 us with the 8-bit copy; rank 64 adds W from the caches, 2048 x 4096 13
+// and 17 us with the 8-bit copy; rank 64 adds W from the caches, 2048 x 4096 12
 // us.  A step ahead in registers gained a quarter while rows were loaded as
 // operands and nothing since they are turned (fewer workgroups fit a CU), so
 // there is none.  Tiles of 64 rows and four waves: 42 us at 4096 x 14336.
