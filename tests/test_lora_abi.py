@@ -134,7 +134,7 @@ def test_gemm_dx_errors(call):
         assert dx(call, lut=None) == 1 and dx(call, lut=A + 1) == 3
     for name, off in (("dy", 1), ("packed", 8), ("alpha", 1), ("beta", 1), ("out", 8), ("ws", 8)):
         assert dx(call, **{name: A + off}) == 3
-    for M in (4, 200):
+    for M in (4, 300):
         need = any4.gemm_dx_workspace_size(M, 64, 256, 128)
         assert need > 0 and dx(call, M=M, ws_bytes=need - 1) == 4
     assert need >= 64 * 256 * 2          # beyond a few rows: the layer in bf16
