@@ -1093,7 +1093,7 @@ __global__ __launch_bounds__(SMALL_THREADS) void k_small(const SmallArgs p)
 // ---------------------------------------------------------------------------
 // A workgroup takes 128 columns and the rows of one adapter (or one chunk of
 // them); its eight waves take 32 rows each in turn, and their sums meet in
-// LDS.  Chunks of one adapter leave partial sums, which k_wgrad_sum adds in
+// LDS (WIDE: each wave 128 columns and all the rows).  Chunks of one adapter leave partial sums, which k_wgrad_sum adds in
 // order.  In 8 bits, the row's scale of these 128 channels goes into c, whose
 // three bf16 parts hold it, and the whole numbers are exact bf16 values.
 // Bound by the bytes of `in`: 4096 rows of 4096 columns in 8 bits and 14336 in
@@ -1123,15 +1123,20 @@ struct WgradArgs {
 constexpr int WGRAD_THREADS = 512;
 constexpr int WGRAD_WAVES = WGRAD_THREADS / WAVE;
 
-template <int RT, bool WHOLE, bool SMALL>
+template <int RT, bool WHOLE, bool SMALL, bool WIDE>
 __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
 {
     constexpr int STRIDE = 128 + 4;      // 4: rows of a quarter wave in other banks
     __shared__ __attribute__((aligned(16))) float red[WGRAD_WAVES][16 * STRIDE];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, g = lane >> 4;
-    const bool second = static_cast<int>(blockIdx.x) >= p.job[0].cols;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
+    constexpr int SHARE = WIDE ? 1 : WGRAD_WAVES;          // waves that share the rows out
+    const int block = WIDE ? static_cast<int>(blockIdx.x) * WGRAD_WAVES + w : static_cast<int>(blockIdx.x);
+    if (WIDE && block >= p.job[0].cols + p.job[1].cols)    // no barriers then
+        return;
+    const int at_row = WIDE ? 0 : 32 * w;
+    const bool second = block >= p.job[0].cols;
     const WgradJob job = second ? p.job[1] : p.job[0];
-    const int cb = static_cast<int>(blockIdx.x) - (second ? p.job[0].cols : 0), j0 = blockIdx.z * (16 * RT);
+    const int cb = block - (second ? p.job[0].cols : 0), j0 = blockIdx.z * (16 * RT);
     int a = blockIdx.y, count = 0, slot = -1, first = 0;
     const int* rows;
     if constexpr (!SMALL) {
@@ -1232,10 +1237,10 @@ __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
         }
     };
     if (job.in)
-        for (int m0 = 32 * w; m0 < count; m0 += 32 * WGRAD_WAVES)
+        for (int m0 = at_row; m0 < count; m0 += 32 * SHARE)
             step(m0, std::false_type{});
     else
-        for (int m0 = 32 * w; m0 < count; m0 += 32 * WGRAD_WAVES)
+        for (int m0 = at_row; m0 < count; m0 += 32 * SHARE)
             step(m0, std::true_type{});
     const float f = slot < 0 && job.scaled && count ? p.scale[a] : 1.0f;
     const size_t width = slot < 0 ? job.D : static_cast<size_t>(job.cols) * 128;
@@ -1252,8 +1257,8 @@ __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
                     o[i] = v[i];
         }
     };
-    if (count <= 32) {           // the first wave has it all
-        if (w > 0)
+    if (WIDE || count <= 32) {   // a wave, the first, has it all
+        if (!WIDE && w > 0)
             return;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
@@ -1491,14 +1496,15 @@ void launch_small(const SmallArgs& a, int64_t tiles, hipStream_t stream)
 #undef SMALL_AS
 }
 
-template <bool WHOLE>
-void launch_wgrad(const WgradArgs& a, hipStream_t stream)
+template <bool WHOLE, bool WIDE>
+void launch_wgrad_as(const WgradArgs& a, hipStream_t stream)
 {
     const int rt = a.r <= 16 ? 1 : a.r <= 32 ? 2 : 4;
     const int64_t ys = a.chunked ? PlanLayout(a.b.M, a.b.L).CB : a.b.L;
     const unsigned cols = static_cast<unsigned>(a.job[0].cols + a.job[1].cols);
-    const dim3 grid(cols, static_cast<unsigned>(ys), static_cast<unsigned>((a.r + 16 * rt - 1) / (16 * rt)));
-#define WGRAD(RT_, SMALL_) hipLaunchKernelGGL((k_wgrad<RT_, WHOLE, SMALL_>), grid, dim3(WGRAD_THREADS), 0, stream, a)
+    const dim3 grid(WIDE ? (cols + WGRAD_WAVES - 1) / WGRAD_WAVES : cols, static_cast<unsigned>(ys),
+                    static_cast<unsigned>((a.r + 16 * rt - 1) / (16 * rt)));
+#define WGRAD(RT_, SMALL_) hipLaunchKernelGGL((k_wgrad<RT_, WHOLE, SMALL_, WIDE>), grid, dim3(WGRAD_THREADS), 0, stream, a)
     if (!a.b.plan) {
         if (rt == 1) WGRAD(1, true);
         else if (rt == 2) WGRAD(2, true);
@@ -1512,6 +1518,25 @@ void launch_wgrad(const WgradArgs& a, hipStream_t stream)
     if (a.chunked)
         hipLaunchKernelGGL(k_wgrad_sum, dim3((cols * 32 + 255) / 256, static_cast<unsigned>(a.b.L), static_cast<unsigned>(a.r)),
                            dim3(256), 0, stream, a);
+}
+
+// Eight waves for one block of 128 columns, or one each: the latter leaves no wave
+// idle with adapters of few rows and needs no sums in LDS, but an eighth of the
+// workgroups, so from one a CU on.  Whole backward calls in us, shared against
+// one each: 635 rows of 52 adapters, 9600 to 11704, rank 39, 212 against 113; 64 of 64,
+// 4096 x 4096, rank 64, 88 and 54; 4096 of 64, rank 64, 196 and 132; 20000 of 8, rank
+// 64, 330 and 315; 4096 with nine tenths to one of 64, rank 16, 87 and 99.  Below:
+// 4096 of 8, rank 16, 60 and 80; 2048 of 4, rank 64, 58 and 81.  Low ranks with long
+// runs of rows gain nothing: 8000 of 16, 4096 to 14336, rank 16, 170 and 181.
+template <bool WHOLE>
+void launch_wgrad(const WgradArgs& a, hipStream_t stream)
+{
+    const int64_t ys = a.chunked ? PlanLayout(a.b.M, a.b.L).CB : a.b.L, cols = a.job[0].cols + a.job[1].cols;
+    const int64_t wide = (cols + WGRAD_WAVES - 1) / WGRAD_WAVES * ys * (a.r > 64 ? 2 : 1);
+    if (wide >= 256 && (a.r > 16 || a.b.M <= 256 * static_cast<int64_t>(a.b.L)))
+        launch_wgrad_as<WHOLE, true>(a, stream);
+    else
+        launch_wgrad_as<WHOLE, false>(a, stream);
 }
 
 }  // namespace

@@ -116,6 +116,9 @@ SHAPES = [
     (255, 128, 33, 8, 300, "mixed"), (257, 384, 72, 24, 4, "mixed"), (300, 128, 40, 8, 4096, "distinct"),
     (400, 256, 136, 100, 2, "runs"), (500, 128, 24, 4, 63, "mixed"), (500, 128, 24, 4, 64, "mixed"),
     (1500, 128, 27, 4, 65, "runs"), (3300, 256, 30, 40, 2, "mixed"), (5000, 128, 129, 65, 1, "runs"),
+    (2, 640, 1100, 113, 60, "distinct"), (64, 1024, 1025, 64, 64, "mixed"), (635, 1152, 1300, 39, 200, "mixed"),
+    (3000, 640, 2200, 17, 90, "runs"), (5000, 1024, 4099, 33, 20, "mixed"), (200, 512, 4099, 16, 200, "distinct"),
+    (20000, 2048, 2050, 65, 5, "runs"),
 ]
 
 
