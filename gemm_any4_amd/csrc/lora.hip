@@ -862,6 +862,9 @@ __global__ __launch_bounds__(EXPAND_THREADS) void k_expand(const ExpandArgs p)
                 }
                 if (SCALED)
                     v *= scale;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)      // ranks behind the last: zero weights times an infinity are NaN
+                    v[q] = j + q < p.r ? v[q] : 0.0f;
                 if (p.c && first) {
                     float* o = p.c + static_cast<size_t>(tile.rows[m]) * p.r + j;
 #pragma unroll
@@ -1058,9 +1061,8 @@ __global__ __launch_bounds__(SMALL_THREADS) void k_small(const SmallArgs p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int m = 4 * g + i;
-            float f = j < p.r && m < tile.count && tile.a >= 0 ? v[i] : 0.0f;
-            if (p.scaled && tile.a >= 0)
-                f *= scale;
+            float f = p.scaled ? v[i] * scale : v[i];
+            f = j < p.r && m < tile.count && tile.a >= 0 ? f : 0.0f;
             cs[m * STRIDE + j] = f;
             if (p.c && first && j < p.r && m < tile.count)
                 p.c[static_cast<size_t>(tile.rows[m]) * p.r + j] = f;

@@ -366,9 +366,10 @@ any4_status any4_quantize(const float* W, const float* ex, uint8_t* idx, uint16_
  * for bit, h[m] = 0.  Products are exact and sums fp32; the fp32 h enters the
  * second product unrounded, so out carries fp32 summation error and one
  * rounding.  Results are deterministic and a row's result depends on no other
- * row's values.  A non-finite weight of an adapter makes the outputs it
- * reaches non-finite, and a non-finite row the gradients of its adapter (which
- * kind is not specified).
+ * row's values.  Infinities and NaN of x, y, dy, dx and scale give the h, out
+ * and dx_out of the formulas, whatever r is.  A non-finite weight of an adapter
+ * makes the outputs it reaches non-finite, and a non-finite row the gradients
+ * of its adapter (which kind is not specified).
  * Sizes of all any4_lora* calls: 0 <= M <= 2^20, 0 <= N <= 2^24, K <= 2^24 a
  * positive multiple of 128, 1 <= r <= 128, 1 <= L <= 4096; x, y, A and B below
  * 2 GiB.
