@@ -394,8 +394,9 @@ any4_status any4_lora_plan(const int32_t* ids, void* plan, size_t bytes, int64_t
 
 /*
  * any4_lora -- out and, where asked for, what the backward pass needs.
- *   plan   device, of these ids, M and L; or NULL.  (A plan of another M or L
- *          leaves the outputs unwritten.)
+ *   plan   device, of these ids, M and L; or NULL.  (A plan that any4_lora_plan
+ *          made for another M > 0 or L leaves the outputs unwritten: its sizes
+ *          are looked at before anything else of it is read.)
  *   out    device, written; may be y itself, else must not overlap an input.
  *   h      device, [M][r] fp32, written; or NULL.
  *   q, qs  device, x in 8 bits as any4_act8_save writes it, in the same pass
