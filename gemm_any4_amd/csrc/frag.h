@@ -176,8 +176,9 @@ __device__ __forceinline__ void turn16(u32x4_t* own, const u32x4_t (&in)[4], u32
 // f = hi + mid + lo exactly, each part with the 8 significant bits of a bf16
 // (cut, not rounded, so hi cannot overflow; parts below 2^-126 are lost).
 // An fp32 factor enters the matrix cores as these three: the products with
-// bf16 values are then those of the fp32 factor itself.  An infinity or NaN
-// stays whole in hi.
+// bf16 values are then those of the fp32 factor itself.  An infinity stays whole
+// in hi.  A NaN may be cut to an infinity there (a payload in the low half alone),
+// but what is left of it is a quiet NaN, which mid holds.
 struct Split3 {
     bf16x8_t part[3];
 };
@@ -193,7 +194,7 @@ __device__ __forceinline__ Split3 split3(const float (&f)[8])
             const float v = f[2 * p + e];
             h[e] = __float_as_uint(v);
             float rest = v - __uint_as_float(h[e] & 0xffff0000u);
-            rest = (h[e] & 0x7f800000u) == 0x7f800000u ? 0.0f : rest;
+            rest = (h[e] & 0x7fffffffu) == 0x7f800000u ? 0.0f : rest;
             m[e] = __float_as_uint(rest);
             l[e] = __float_as_uint(rest - __uint_as_float(m[e] & 0xffff0000u));
         }
