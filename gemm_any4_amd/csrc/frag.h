@@ -153,6 +153,17 @@ __device__ __forceinline__ f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// Between writes and reads of LDS that belongs to one wave, by other lanes than
+// wrote: LDS serves a wave's instructions in the order in which they were
+// issued, so there is nothing to wait for, and no instruction here; the fences
+// keep the compiler from exchanging them.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // A wave's block of 16 rows x 128 bf16, loaded as it lies in memory (lane
 // 16 g + c has 16 bytes of row 4 i + g, columns 8 c on: a load covers whole 256-byte
 // pieces of rows), turned through LDS of the wave's own into matrix-core
@@ -168,9 +179,11 @@ __device__ __forceinline__ void turn16(u32x4_t* own, const u32x4_t (&in)[4], u32
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         own[(4 * i + g) * TURN_PITCH + c] = in[i];
+    wave_sync();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         out[i] = own[c * TURN_PITCH + 4 * i + g];
+    wave_sync();
 }
 
 // f = hi + mid + lo exactly, each part with the 8 significant bits of a bf16

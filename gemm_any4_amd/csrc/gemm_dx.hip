@@ -365,7 +365,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_dx(const DxArgs p)
 // Up to FEW_M rows the weights are the work, so they are read packed and once.
 // A wave takes a chunk of 128 k and 64 rows of W a step, a row a lane, whose
 // table and scales then serve 128 weights.  32 k at a time, neighbouring lanes
-// pair their values, LDS of the wave's own turns the block (no barrier), and
+// pair their values, LDS of the wave's own turns the block (wave_sync), and
 // the matrix cores multiply it with dy, whose rows come in 128-byte pieces and
 // are turned the same way (loaded as operands they cost the vector cache a
 // clock for every lane).  The next step's weights are asked for once this one's
@@ -450,9 +450,11 @@ __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
                 staged[(8 * h + lane / 8) * FEW_PITCH + (lane & 7)] =
                     dy.finish(x[i][h], static_cast<uint32_t>(m) * p.N + n, p.N - n, edge);
             }
+            wave_sync();
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
                 d[i][kk] = __builtin_bit_cast(bf16x8_t, staged[c * FEW_PITCH + 4 * kk + g]);
+            wave_sync();
         }
         ByteTable<FMT> t(r);
         if (st * 64 + lane >= p.N)      // rows behind the last: weights of 0
@@ -476,6 +478,7 @@ __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
             for (int i = 0; i < 16; ++i)
                 turned[(first_k(i) + 2 * (lane & 1)) * FEW_STRIDE + (lane / 2 ^ 16 * ((first_k(i) >> 1 ^ lane) & 1))] =
                     pair_rows(v[i], lane & 1);
+            wave_sync();
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
@@ -485,6 +488,7 @@ __global__ __launch_bounds__(FEW_THREADS) void k_dx_few(const FewArgs p)
                     for (int i = 0; i < MB; ++i)
                         acc[i][2 * q + b] = mfma(wv, d[i][kk], acc[i][2 * q + b]);
                 }
+            wave_sync();
         }
     }
     f32x4_t* red = reinterpret_cast<f32x4_t*>(room);      // [SUMS][WAVES][8][WAVE]

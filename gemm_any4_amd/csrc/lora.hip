@@ -409,6 +409,7 @@ __device__ __forceinline__ Tile search_tile(const Batch& b, int t, int* own)
                 }
                 before += __builtin_popcountll(mask[i]);
             }
+            wave_sync();
             return {a < b.L ? a : -1, count, own};
         }
         t -= tiles;
@@ -1183,6 +1184,7 @@ __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
             own[lane] = 63 - __builtin_clzll(m);      // places behind the last repeat it
         if (mine)
             own[__builtin_popcountll(m & ((1ull << lane) - 1))] = lane;
+        wave_sync();
         rows = own;
     }
     const int d = cb * 128 + 8 * c;
