@@ -201,10 +201,11 @@ __global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ d
 // 16*RM x 16*RN of the outputs.  Both tiles go to LDS by direct loads, the next
 // step's while this one is multiplied: one barrier a step.  Bound by the matrix
 // cores and the LDS reads that feed them (a wave's 128 x 64 outputs: 12 reads of
-// 1 KB for 32 products); 4096 x 14336 x 4096 takes 371 us, 1297 TFLOP/s (128 x 128
-// tiles of four 64 x 64 waves: 645 us).  A row of a tile is
-// eight 16-byte pieces; piece q stands at q ^ key(row), keys chosen so that the
-// 16 lanes of an operand read touch all 64 banks once.
+// 1 KB for 32 products); 4096 x 14336 x 4096 takes 368 us, 1307 TFLOP/s (the median
+// launch; the fastest 350, averages of whole runs 373 to 414; 128 x 128 tiles of
+// four 64 x 64 waves: 645 us).  A row of a tile is eight 16-byte pieces; piece q
+// stands at q ^ key(row), keys chosen so that the 16 lanes of an operand read
+// touch all 64 banks once.
 struct DxArgs {
     const uint16_t* dy;     // [M][Np]
     const uint16_t* wt;     // [K][Np]
@@ -365,14 +366,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_dx(const DxArgs p)
 // Up to FEW_M rows the weights are the work, so they are read packed and once.
 // A wave takes a chunk of 128 k and 64 rows of W a step, a row a lane, whose
 // table and scales then serve 128 weights.  32 k at a time, neighbouring lanes
-// pair their values, LDS of the wave's own turns the block (wave_sync), and
-// the matrix cores multiply it with dy, whose rows come in 128-byte pieces and
-// are turned the same way (loaded as operands they cost the vector cache a
-// clock for every lane).  The next step's weights are asked for once this one's
-// tables stand (14336 x 4096, 128 rows: 38 us, 39.5 without).  Eight waves share the
-// rows out, and their sums meet in LDS at the end; further splits of the rows
-// leave fp32 partial sums.  What bounds it is a step's chain of LDS and vector
-// work (lookups and pairing, four instructions a weight) with two waves a SIMD.
+// pair their values, LDS of the wave's own turns the block (wave_sync, no
+// barrier), and the matrix cores multiply it with dy, whose rows come in
+// 128-byte pieces and are turned the same way (loaded as operands they cost the
+// vector cache a clock for every lane).  The next step's weights are asked for
+// once this one's tables stand (14336 x 4096, 128 rows: 38 us, one more
+// without).  Eight waves share the rows out, and their sums meet in LDS at the
+// end; further splits of the rows leave fp32 partial sums.  What bounds it is a
+// step's chain of LDS and vector work (lookups and pairing, four instructions a
+// weight) with two waves a SIMD.
 // FEW_M, whole calls: 256 rows 4096 x 4096 26 us, turned first 35; 14336 x 4096 63
 // and 92; 4096 x 14336 72 and 86; 512 x 512 9 and 11; 320 rows 4096 x 4096 43 and 37.
 constexpr int FEW_M = 256;

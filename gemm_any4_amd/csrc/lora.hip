@@ -236,9 +236,9 @@ __device__ __forceinline__ void plan_tables(int* cnt, int parts, int M, int L, i
 }
 
 // Up to STEPS x 64 rows a wave, their ids in registers from the first load on.
-// A chain of waits, not of work: 3.9 us for 1031 rows, 4.9 us for 4096, 11.7 us for
+// A chain of waits, not of work: 4.0 us for 1031 rows, 4.9 us for 4096, 11.7 us for
 // 16384 (1.5 us more with the sums over all waves where the first holds all the
-// adapters).
+// adapters); half a microsecond more between a batch's other kernels.
 template <int STEPS>
 __global__ __launch_bounds__(PLAN_THREADS) void k_plan(const int* __restrict__ ids, int* plan, int M, int L)
 {
@@ -553,7 +553,7 @@ __device__ __forceinline__ float byte_to_f32(uint32_t v, int i)
 constexpr int ACT8_THREADS = 256;
 
 // One 16-lane group per GROUP8 channels, 16 bytes of x a lane; one pass, bound by
-// its bytes: 8192 x 14336 72 us to keep and 58 us to read back (5.0 and 6.2 TB/s).
+// its bytes: 8192 x 14336 71 us to keep and 58 us to read back (5.0 and 6.1 TB/s).
 __global__ __launch_bounds__(ACT8_THREADS) void k_act8_save(const uint16_t* __restrict__ x, uint8_t* __restrict__ q,
                                                             float* __restrict__ s, uint32_t slots)
 {
@@ -594,7 +594,7 @@ __global__ __launch_bounds__(ACT8_THREADS) void k_act8_load(const uint8_t* __res
 // which its eight waves share out again in steps of 128; the matrix cores sum
 // 16 rows x 16 ranks x 32 d at a time.  The eight waves' sums meet in LDS, the
 // splits' in the expand kernel, both in a fixed order.
-// Bound by the bytes of `in`: 4096 x 14336, rank 16, 31 us (3.8 TB/s); 4096 x 4096
+// Bound by the bytes of `in`: 4096 x 14336, rank 16, 30 us (3.9 TB/s); 4096 x 4096
 // 12 us, of which six are the launch and its chain of waits (plan, rows, data),
 // and 17 us with the 8-bit copy; rank 64 adds W from the caches, 2048 x 4096 12
 // us.  A step ahead in registers gained a quarter while rows were loaded as
@@ -731,7 +731,7 @@ __global__ __launch_bounds__(SHRINK_THREADS) void k_shrink(const ShrinkArgs p)
 // here (dh), else the scale multiplies the sum over j (y).  A wave holds the
 // 128 columns of W it works on as matrix-core operands (8 x 8 blocks turned in
 // registers, all loads 16 bytes) and goes over the tile's rows, 16 at a time.
-// Bound by the bytes of base and out: 4096 x 14336, rank 16, 43 us (5.5 TB/s);
+// Bound by the bytes of base and out: 4096 x 14336, rank 16, 45 us (5.2 TB/s);
 // 2048 x 4096, rank 64, 18 us, where W and the parts come to twice those bytes
 // from the caches.  Tiles of 64 rows: 52 us at the first (a third as many waves
 // fit a CU); the base rows loaded 16 at a time: 84 us.
@@ -1316,7 +1316,7 @@ __global__ __launch_bounds__(WGRAD_THREADS) void k_wgrad(const WgradArgs p)
 
 // Adapters of several chunks: their partial sums in order, 4 columns a thread and
 // four chunks' loads at a time (2048 rows of 4 adapters, rank 64, 4096 + 4099
-// columns 5.7 us; one column a thread 8.6).  Adapters without
+// columns 4.9 us; one column a thread 3 us more).  Adapters without
 // rows: zeros.  (An adapter of one chunk is done.)
 __global__ __launch_bounds__(256) void k_wgrad_sum(const WgradArgs p)
 {
@@ -1373,12 +1373,17 @@ __global__ __launch_bounds__(256) void k_lora_zero(float* __restrict__ p, size_t
 int round16(int64_t r) { return static_cast<int>((r + 15) / 16 * 16); }
 
 // Ranges that a shrink's D is split into: enough workgroups for the chip, at
-// least 128 d for each wave, and few enough that the parts stay small beside
-// the rows (the expand kernel reads them all).  Beyond rank 32 the registers
-// leave a CU one workgroup: the split with the fewest steps over all rounds of
-// the 256 CUs, two more a round to start and to add up.  (Two a CU and up to four
-// parts there too, whole calls in us: 1000 x 14336 to 4096, rank 128, 48 against 43;
-// 2048 x 4096, rank 128, 48 against 42; 8000 x 4096, rank 64, 77 against 71.)
+// most as many as leave a wave no more than one step of 128 d (some of the last
+// one's waves may have none), and few enough that the parts stay small beside
+// the rows (the expand kernel reads them all).  One split fewer where the steps
+// are no multiple of eight, so that each wave has a step, takes longer: whole
+// calls of 64 rows, rank 64, 1152 to 4096 11.2 us against 10.3 here; 1000 rows of
+// 2176, rank 8, 15.8 against 15.1; 1000 of 1152, rank 128, 28.2 and 28.4.
+// Beyond rank 32 the registers leave a CU one workgroup: the split with the
+// fewest steps over all rounds of the 256 CUs, two more a round to start and to
+// add up.  (Two a CU and up to four parts there too, whole calls in us: 1000 x
+// 14336 to 4096, rank 128, 48 against 43; 2048 x 4096, rank 128, 48 against 42;
+// 8000 x 4096, rank 64, 77 against 71.)
 int split_of(int64_t M, int64_t L, int64_t D, int64_t r, bool ballots)
 {
     const int64_t steps = (D + 127) / 128, most = (steps + SHRINK_WAVES - 1) / SHRINK_WAVES;
@@ -1544,9 +1549,12 @@ void launch_wgrad_as(const WgradArgs& a, hipStream_t stream)
 // workgroups, so from one a CU on.  Whole backward calls in us, shared against
 // one each: 635 rows of 52 adapters, 9600 to 11704, rank 39, 212 against 113; 64 of 64,
 // 4096 x 4096, rank 64, 88 and 54; 4096 of 64, rank 64, 196 and 132; 20000 of 8, rank
-// 64, 330 and 315; 4096 with nine tenths to one of 64, rank 16, 87 and 99.  Below:
-// 4096 of 8, rank 16, 60 and 80; 2048 of 4, rank 64, 58 and 81.  Low ranks with long
-// runs of rows gain nothing: 8000 of 16, 4096 to 14336, rank 16, 170 and 181.
+// 64, 330 and 315.  Below: 4096 of 8, rank 16, 60 and 80; 2048 of 4, rank 64, 58 and
+// 81.  Low ranks with long runs of rows gain nothing: 8000 of 16, 4096 to 14336, rank
+// 16, 170 and 181.  The rule counts adapters and knows nothing of how the rows are
+// spread over them; 4096 rows, 4096 x 4096, in a graph: nine tenths with one of 64,
+// rank 16, 77 and 73, rank 64, 188 and 162; but all with one of 64, 57 and 66, 102 and
+// 124.
 template <bool WHOLE>
 void launch_wgrad(const WgradArgs& a, hipStream_t stream)
 {
