@@ -27,7 +27,13 @@ For fine-tunes of such a layer: lora, gemm_lora, lora_backward and lora_plan
 (low-rank adapters of many requests at once, and their gradients); act8_save,
 act8_load and act8_empty (an activation kept in 8 bits); gemm_dx,
 gemm_int4_dx, any2_gemm_dx and any3_gemm_dx (the gradient of a layer's input).
-These take tensors of any GPU, run on that GPU's current stream (or `stream`,
+For a feed-forward block, dense or of experts: gemm_act, gemm_int4_act,
+any2_gemm_act and any3_gemm_act (the product with bias, activation, gate and
+residual), act_backward; route and route_backward (the experts of each token),
+experts_plan, experts_gemm and experts_gemm_dx (and their int4, any2 and any3
+forms: stacked layers, each row through its expert), combine and
+combine_backward (the weighted sum of the experts' outputs).
+These and the calls for fine-tunes take tensors of any GPU, run on that GPU's current stream (or `stream`,
 on which their outputs and workspaces are then allocated too) and can be
 captured into a graph.
 """
@@ -56,7 +62,10 @@ EXPORTS = ("any4_packed_bytes", "any4_pack", "any4_dequant", "any4_gemm_workspac
            "any4_lora_plan_bytes", "any4_lora_plan", "any4_lora_workspace_size", "any4_lora",
            "any4_lora_backward_workspace_size", "any4_lora_backward", "any4_act8_save",
            "any4_act8_load", "any4_gemm_dx_workspace_size", "any4_gemm_dx", "any4_gemm_int4_dx",
-           "any2_gemm_dx", "any3_gemm_dx")
+           "any2_gemm_dx", "any3_gemm_dx", "any4_gemm_act_workspace_size", "any4_gemm_act",
+           "any4_act_backward_workspace_size", "any4_act_backward", "any4_route", "any4_route_backward",
+           "any4_experts_workspace_size", "any4_experts_gemm", "any4_experts_dx_workspace_size",
+           "any4_experts_gemm_dx", "any4_combine", "any4_combine_backward")
 
 _lib = None
 
@@ -76,6 +85,7 @@ def lib() -> ctypes.CDLL:
                                "or python -m gemm_any4_amd.build")
         L = ctypes.CDLL(LIB_PATH)
         P, I64, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
+        INT, F32 = ctypes.c_int, ctypes.c_float
         L.any4_packed_bytes.restype = SZ
         L.any4_packed_bytes.argtypes = [I64, I64]
         L.any4_pack.restype = ctypes.c_int
@@ -116,7 +126,21 @@ def lib() -> ctypes.CDLL:
                 ("any4_gemm_dx", ctypes.c_int, [P] * 6 + [I64] * 4 + [P, SZ, P]),
                 ("any4_gemm_int4_dx", ctypes.c_int, [P] * 5 + [I64] * 4 + [P, SZ, P]),
                 ("any2_gemm_dx", ctypes.c_int, [P] * 6 + [I64] * 4 + [P, SZ, P]),
-                ("any3_gemm_dx", ctypes.c_int, [P] * 6 + [I64] * 4 + [P, SZ, P])):
+                ("any3_gemm_dx", ctypes.c_int, [P] * 6 + [I64] * 4 + [P, SZ, P]),
+                ("any4_gemm_act_workspace_size", SZ, [I64] * 4),
+                ("any4_gemm_act", ctypes.c_int, [INT] + [P] * 9 + [INT] * 2 + [I64] * 4 + [P, SZ, P]),
+                ("any4_act_backward_workspace_size", SZ, [I64] * 2 + [INT]),
+                ("any4_act_backward", ctypes.c_int, [P] * 4 + [INT] * 2 + [I64] * 2 + [P, SZ, P]),
+                ("any4_route", ctypes.c_int, [P, INT] + [P] * 3 + [INT] * 2 + [F32] + [I64] * 5 + [P]),
+                ("any4_route_backward", ctypes.c_int,
+                 [P, P, INT, P, P] + [INT] * 2 + [F32] + [I64] * 3 + [P]),
+                ("any4_experts_workspace_size", SZ, [I64] * 6),
+                ("any4_experts_gemm", ctypes.c_int,
+                 [INT, P, INT] + [P] * 9 + [INT] * 2 + [I64] * 6 + [P, SZ, P]),
+                ("any4_experts_dx_workspace_size", SZ, [I64] * 6),
+                ("any4_experts_gemm_dx", ctypes.c_int, [INT] + [P] * 8 + [I64] * 6 + [P, SZ, P]),
+                ("any4_combine", ctypes.c_int, [P] * 4 + [I64] * 3 + [P]),
+                ("any4_combine_backward", ctypes.c_int, [P] * 5 + [I64] * 3 + [P])):
             getattr(L, name).restype = restype
             getattr(L, name).argtypes = argtypes
         L.any4_read_probe.restype = ctypes.c_int
@@ -917,6 +941,431 @@ def any3_gemm_dx(dy: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alph
     """dx [M, K] = dy [M, N] * W, the gradient of any3_gemm()'s x."""
     return _gemm_dx("any3_gemm_dx", any3_packed_bytes, dy, packed, lut, alpha, beta, g, out,
                     workspace, stream)
+
+
+# --------------------------------------------------------------------------
+# the feed-forward block: epilogues, routing, experts
+# --------------------------------------------------------------------------
+_FORMATS = {"any4": 0, "int4": 1, "any2": 2, "any3": 3}
+_FORMAT_BYTES = (packed_bytes, packed_bytes, any2_packed_bytes, any3_packed_bytes)
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def gemm_act_raw(fmt, x_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, residual_ptr, z_ptr, out_ptr, act, gate,
+                 M, N, K, g, ws_ptr, ws_bytes, stream=None) -> int:
+    """fmt, act: the numbers of any4_format and any4_activation."""
+    return lib().any4_gemm_act(fmt, x_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, residual_ptr, z_ptr,
+                               out_ptr, act, gate, M, N, K, g, ws_ptr, ws_bytes, _stream(stream))
+
+
+def act_backward_raw(dy_ptr, z_ptr, dz_ptr, dbias_ptr, act, gate, M, N, ws_ptr, ws_bytes, stream=None) -> int:
+    return lib().any4_act_backward(dy_ptr, z_ptr, dz_ptr, dbias_ptr, act, gate, M, N, ws_ptr, ws_bytes, _stream(stream))
+
+
+def route_raw(logits_ptr, bf16, bias_ptr, w_ptr, ids_ptr, score, renorm, scale, T, E, k, groups, top_groups,
+              stream=None) -> int:
+    return lib().any4_route(logits_ptr, bf16, bias_ptr, w_ptr, ids_ptr, score, renorm, scale, T, E, k, groups,
+                            top_groups, _stream(stream))
+
+
+def route_backward_raw(dw_ptr, logits_ptr, bf16, ids_ptr, dlogits_ptr, score, renorm, scale, T, E, k,
+                       stream=None) -> int:
+    return lib().any4_route_backward(dw_ptr, logits_ptr, bf16, ids_ptr, dlogits_ptr, score, renorm, scale, T, E, k,
+                                     _stream(stream))
+
+
+def experts_gemm_raw(fmt, x_ptr, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, ids_ptr, plan_ptr, z_ptr,
+                     out_ptr, act, gate, T, k, E, N, K, g, ws_ptr, ws_bytes, stream=None) -> int:
+    return lib().any4_experts_gemm(fmt, x_ptr, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, ids_ptr,
+                                   plan_ptr, z_ptr, out_ptr, act, gate, T, k, E, N, K, g, ws_ptr, ws_bytes,
+                                   _stream(stream))
+
+
+def experts_gemm_dx_raw(fmt, dy_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, ids_ptr, plan_ptr, dx_ptr, T, k, E, N, K, g,
+                        ws_ptr, ws_bytes, stream=None) -> int:
+    return lib().any4_experts_gemm_dx(fmt, dy_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, ids_ptr, plan_ptr, dx_ptr,
+                                      T, k, E, N, K, g, ws_ptr, ws_bytes, _stream(stream))
+
+
+def combine_raw(y_ptr, w_ptr, residual_ptr, out_ptr, T, k, N, stream=None) -> int:
+    return lib().any4_combine(y_ptr, w_ptr, residual_ptr, out_ptr, T, k, N, _stream(stream))
+
+
+def combine_backward_raw(dout_ptr, y_ptr, w_ptr, dy_ptr, dw_ptr, T, k, N, stream=None) -> int:
+    return lib().any4_combine_backward(dout_ptr, y_ptr, w_ptr, dy_ptr, dw_ptr, T, k, N, _stream(stream))
+
+
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
+def gemm_act_workspace_size(M: int, N: int, K: int, g: int) -> int:
+    return int(lib().any4_gemm_act_workspace_size(M, N, K, g))
+
+
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
+def act_backward_workspace_size(M: int, N: int, gate: bool) -> int:
+    return int(lib().any4_act_backward_workspace_size(M, N, gate))
+
+
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
+def experts_workspace_size(T: int, k: int, E: int, N: int, K: int, g: int) -> int:
+    return int(lib().any4_experts_workspace_size(T, k, E, N, K, g))
+
+
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
+def experts_dx_workspace_size(T: int, k: int, E: int, N: int, K: int, g: int) -> int:
+    return int(lib().any4_experts_dx_workspace_size(T, k, E, N, K, g))
+
+
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
+def _layer_bytes(fmt: int, N: int, K: int) -> int:
+    return _FORMAT_BYTES[fmt](N, K)
+
+
+def _choice(name: str, value, table: dict) -> int:
+    number = table.get(value)
+    if number is None:
+        raise ValueError(f"{name} must be one of {', '.join(table)}, got {value!r}")
+    return number
+
+
+def _maybe(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple, device) -> int | None:
+    return None if t is None else _tensor(t, name, dtype, shape, device)
+
+
+def _layer(fmt: int, packed, lut, alpha, beta, g: int, dev, experts: bool) -> tuple:
+    """Checks a layer [N, K], or stacked ones [E, N, K]: (E, N, K, their addresses)."""
+    if g <= 0 or alpha.dim() != 2 + experts:
+        raise ValueError("alpha/beta must be [E, N, K/g]" if experts else "alpha/beta must be [N, K/g]")
+    lead = tuple(alpha.shape[:-1])
+    N, K = lead[-1], alpha.shape[-1] * g
+    E = lead[0] if experts else 1
+    bf16 = torch.bfloat16
+    if packed.dtype is not torch.uint8:
+        raise TypeError(f"packed must be {torch.uint8}, got {packed.dtype}")
+    if packed.numel() != E * _layer_bytes(fmt, N, K):
+        raise ValueError(f"packed must hold {E * _layer_bytes(fmt, N, K)} bytes")
+    return (E, N, K, _tensor(packed, "packed", torch.uint8, tuple(packed.shape), dev),
+            None if lut is None else _tensor(lut, "lut", bf16, lead + (16,), dev),
+            _tensor(alpha, "alpha", bf16, tuple(alpha.shape), dev),
+            _tensor(beta, "beta", bf16, tuple(alpha.shape), dev))
+
+
+def _gemm_act(fmt: int, x, packed, lut, alpha, beta, g, bias, act, gate, residual, z, out, workspace,
+              stream) -> torch.Tensor:
+    dev = _gpu(x, "x", 2)
+    _, N, K, p_packed, p_lut, p_alpha, p_beta = _layer(fmt, packed, lut, alpha, beta, g, dev, False)
+    M, bf16 = x.shape[0], torch.bfloat16
+    No = N // 2 if gate else N
+    if gate and N % 2:
+        raise ValueError("a gated layer must have an even number of rows")
+    p_x = _tensor(x, "x", bf16, (M, K), dev)
+    p_bias, p_residual = _maybe(bias, "bias", bf16, (N,), dev), _maybe(residual, "residual", bf16, (M, No), dev)
+    p_z, number = _maybe(z, "z", bf16, (M, N), dev), _choice("act", act, ACTIVATIONS)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((M, No), dtype=bf16, device=dev)
+            p_out = out.data_ptr() or None
+        else:
+            p_out = _tensor(out, "out", bf16, (M, No), dev)
+        ws, p_ws, nbytes = _scratch(workspace, gemm_act_workspace_size(M, N, K, g), dev)
+        check(lib().any4_gemm_act(fmt, p_x, p_packed, p_lut, p_alpha, p_beta, p_bias, p_residual, p_z, p_out, number,
+                                  1 if gate else 0, M, N, K, g, p_ws, nbytes, _current_handle(dev.index)))
+    return out
+
+
+def gemm_act(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor, g: int,
+             bias: torch.Tensor | None = None, act: str = "none", gate: bool = False,
+             residual: torch.Tensor | None = None, z: torch.Tensor | None = None, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out [M, No] = act(x W^T + bias) + residual with W an any4 layer [N, K]
+    (K = alpha.shape[1] * g), in one product: nothing is rounded in between.
+
+    act: one of ACTIVATIONS.  gate: the layer's rows are [gate; up], No = N / 2, and
+    out = act(gate) * up + residual.  bias bf16 [N]; residual bf16 [M, No] (may
+    be out itself).  For the backward pass z bf16 [M, N] gets x W^T + bias:
+    act_backward, then gemm_dx."""
+    return _gemm_act(0, x, packed, lut, alpha, beta, g, bias, act, gate, residual, z, out, workspace, stream)
+
+
+def gemm_int4_act(x: torch.Tensor, packed: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor, g: int,
+                  bias: torch.Tensor | None = None, act: str = "none", gate: bool = False,
+                  residual: torch.Tensor | None = None, z: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gemm_act of a plain int4 layer."""
+    return _gemm_act(1, x, packed, None, alpha, beta, g, bias, act, gate, residual, z, out, workspace, stream)
+
+
+def any2_gemm_act(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor,
+                  g: int, bias: torch.Tensor | None = None, act: str = "none", gate: bool = False,
+                  residual: torch.Tensor | None = None, z: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gemm_act of an any2 layer."""
+    return _gemm_act(2, x, packed, lut, alpha, beta, g, bias, act, gate, residual, z, out, workspace, stream)
+
+
+def any3_gemm_act(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor,
+                  g: int, bias: torch.Tensor | None = None, act: str = "none", gate: bool = False,
+                  residual: torch.Tensor | None = None, z: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gemm_act of an any3 layer."""
+    return _gemm_act(3, x, packed, lut, alpha, beta, g, bias, act, gate, residual, z, out, workspace, stream)
+
+
+def act_backward(dy: torch.Tensor, z: torch.Tensor, act: str, gate: bool = False, need_bias: bool = True,
+                 dz: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None) -> tuple:
+    """(dz, dbias) of an epilogue for dy bf16 [..., No], from z bf16 [..., N] as
+    gemm_act or experts_gemm kept it: dz bf16 like z (may be z), dbias fp32 [N], the
+    sum over all rows (need_bias = False: None).  The gradient of the product's
+    input is gemm_dx (experts_gemm_dx) of dz, that of the residual dy itself."""
+    if not z.is_cuda:
+        raise ValueError("z must be a GPU tensor")
+    if z.dim() < 2:
+        raise ValueError("z must be [..., N]")
+    dev, shape, bf16 = z.device, tuple(z.shape), torch.bfloat16
+    N = shape[-1]
+    M = z.numel() // N if N else 0
+    if gate and N % 2:
+        raise ValueError("a gated layer must have an even number of rows")
+    p_z = _tensor(z, "z", bf16, shape, dev)
+    p_dy = _tensor(dy, "dy", bf16, shape[:-1] + (N // 2 if gate else N,), dev)
+    number = _choice("act", act, ACTIVATIONS)
+    with _on(dev, stream):
+        if dz is None:
+            dz = torch.empty(shape, dtype=bf16, device=dev)
+            p_dz = dz.data_ptr() or None
+        else:
+            p_dz = _tensor(dz, "dz", bf16, shape, dev)
+        p_dbias, need = None, 0
+        if not need_bias:
+            dbias = None
+        else:
+            if dbias is None:
+                dbias = torch.empty(N, dtype=torch.float32, device=dev)
+            p_dbias = _tensor(dbias, "dbias", torch.float32, (N,), dev)
+            need = act_backward_workspace_size(M, N, bool(gate))
+        ws, p_ws, nbytes = _scratch(workspace, need, dev)
+        check(lib().any4_act_backward(p_dy, p_z, p_dz, p_dbias, number, 1 if gate else 0, M, N, p_ws, nbytes,
+                                      _current_handle(dev.index)))
+    return dz, dbias
+
+
+def _logits(logits: torch.Tensor) -> tuple:
+    dev = _gpu(logits, "logits", 2)
+    T, E = logits.shape
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    return dev, T, E, logits.dtype is torch.bfloat16, _tensor(logits, "logits", logits.dtype, (T, E), dev)
+
+
+def route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, score: str = "softmax", renorm: bool = True,
+          scale: float = 1.0, groups: int = 1, top_groups: int = 1, w: torch.Tensor | None = None,
+          ids: torch.Tensor | None = None, stream=None) -> tuple:
+    """(w fp32 [T, k], ids int32 [T, k]): the k experts of each token, best first, and
+    their weights, from the router's logits (fp32 or bf16 [T, E]).
+
+    score: "softmax" over the experts or "sigmoid".  bias fp32 [E] is added to the scores
+    for the choice alone.  groups, top_groups: of so many groups of experts only those
+    stay whose two best have the largest sum.  renorm: the weights are divided by their sum;
+    scale multiplies them.  Ties go to the lowest index; experts with a logit of -inf
+    or NaN are never chosen (ids of -1 with weights of 0 where fewer than k are left)."""
+    dev, T, E, half, p_logits = _logits(logits)
+    p_bias, number = _maybe(bias, "bias", torch.float32, (E,), dev), _choice("score", score, SCORES)
+    if not 1 <= k <= 64:
+        raise ValueError("k must be 1 .. 64")
+    with _on(dev, stream):
+        if w is None:
+            w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        if ids is None:
+            ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        p_w, p_ids = _tensor(w, "w", torch.float32, (T, k), dev), _tensor(ids, "ids", torch.int32, (T, k), dev)
+        check(lib().any4_route(p_logits, half, p_bias, p_w, p_ids, number, 1 if renorm else 0, scale, T, E, k, groups,
+                               top_groups, _current_handle(dev.index)))
+    return w, ids
+
+
+def route_backward(dw: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: str = "softmax",
+                   renorm: bool = True, scale: float = 1.0, out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """The gradient of route()'s logits (of their type) from that of its weights, dw
+    fp32 [T, k], for its ids: the choice is constant."""
+    dev, T, E, half, p_logits = _logits(logits)
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    k = ids.shape[1]
+    p_ids, p_dw = _tensor(ids, "ids", torch.int32, (T, k), dev), _tensor(dw, "dw", torch.float32, (T, k), dev)
+    number = _choice("score", score, SCORES)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty_like(logits)
+        p_out = _tensor(out, "out", logits.dtype, (T, E), dev)
+        check(lib().any4_route_backward(p_dw, p_logits, half, p_ids, p_out, number, 1 if renorm else 0, scale, T, E, k,
+                                        _current_handle(dev.index)))
+    return out
+
+
+def experts_plan(ids: torch.Tensor, E: int, stream=None) -> LoraPlan:
+    """The pairs of token and expert by expert, for the products of a block:
+    ids int32 [T, k] of E experts (outside 0..E-1: none)."""
+    _gpu(ids, "ids", 2)
+    return lora_plan(ids.reshape(-1), E, stream=stream)
+
+
+def _pairs(ids: torch.Tensor, E: int, plan, dev) -> tuple:
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    T, k = ids.shape
+    return T, k, _tensor(ids, "ids", torch.int32, (T, k), dev), _plan_ptr(plan, T * k, E, dev)
+
+
+def _experts_gemm(fmt: int, x, packed, lut, alpha, beta, g, ids, bias, act, gate, z, plan, out, workspace,
+                  stream) -> torch.Tensor:
+    if not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+    dev, bf16 = x.device, torch.bfloat16
+    E, N, K, p_packed, p_lut, p_alpha, p_beta = _layer(fmt, packed, lut, alpha, beta, g, dev, True)
+    T, k, p_ids, p_plan = _pairs(ids, E, plan, dev)
+    No, per_pair = N // 2 if gate else N, x.dim() == 3
+    if gate and N % 2:
+        raise ValueError("a gated layer must have an even number of rows")
+    p_x = _tensor(x, "x", bf16, (T, k, K) if per_pair else (T, K), dev)
+    p_bias, p_z = _maybe(bias, "bias", bf16, (E, N), dev), _maybe(z, "z", bf16, (T, k, N), dev)
+    number = _choice("act", act, ACTIVATIONS)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, k, No), dtype=bf16, device=dev)
+            p_out = out.data_ptr() or None
+        else:
+            p_out = _tensor(out, "out", bf16, (T, k, No), dev)
+        ws, p_ws, nbytes = _scratch(workspace, experts_workspace_size(T, k, E, N, K, g), dev)
+        check(lib().any4_experts_gemm(fmt, p_x, 1 if per_pair else 0, p_packed, p_lut, p_alpha, p_beta, p_bias, p_ids,
+                                      p_plan, p_z, p_out, number, 1 if gate else 0, T, k, E, N, K, g, p_ws, nbytes,
+                                      _current_handle(dev.index)))
+    return out
+
+
+def experts_gemm(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor,
+                 g: int, ids: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none", gate: bool = False,
+                 z: torch.Tensor | None = None, plan: LoraPlan | None = None, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out bf16 [T, k, No]: each token's row through its k experts (ids int32 [T, k]),
+    any4 layers [N, K] stacked: packed the E layers' bytes one after another, lut
+    [E, N, 16], alpha and beta [E, N, K/g], bias [E, N].
+
+    x bf16 [T, K], or [T, k, K]: a row for each pair (the block's second product).  act, gate
+    and z ([T, k, N]) as in gemm_act.  A pair whose id is not in 0..E-1 gives zeros.
+    plan: of experts_plan(ids, E), kept over the products of a block."""
+    return _experts_gemm(0, x, packed, lut, alpha, beta, g, ids, bias, act, gate, z, plan, out, workspace, stream)
+
+
+def experts_gemm_int4(x: torch.Tensor, packed: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor, g: int,
+                      ids: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none", gate: bool = False,
+                      z: torch.Tensor | None = None, plan: LoraPlan | None = None, out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """experts_gemm of plain int4 layers."""
+    return _experts_gemm(1, x, packed, None, alpha, beta, g, ids, bias, act, gate, z, plan, out, workspace, stream)
+
+
+def any2_experts_gemm(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor,
+                      g: int, ids: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+                      gate: bool = False, z: torch.Tensor | None = None, plan: LoraPlan | None = None,
+                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """experts_gemm of any2 layers."""
+    return _experts_gemm(2, x, packed, lut, alpha, beta, g, ids, bias, act, gate, z, plan, out, workspace, stream)
+
+
+def any3_experts_gemm(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor,
+                      g: int, ids: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+                      gate: bool = False, z: torch.Tensor | None = None, plan: LoraPlan | None = None,
+                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """experts_gemm of any3 layers."""
+    return _experts_gemm(3, x, packed, lut, alpha, beta, g, ids, bias, act, gate, z, plan, out, workspace, stream)
+
+
+def _experts_gemm_dx(fmt: int, dy, packed, lut, alpha, beta, g, ids, plan, out, workspace, stream) -> torch.Tensor:
+    dev, bf16 = _gpu(dy, "dy", 3), torch.bfloat16
+    E, N, K, p_packed, p_lut, p_alpha, p_beta = _layer(fmt, packed, lut, alpha, beta, g, dev, True)
+    T, k, p_ids, p_plan = _pairs(ids, E, plan, dev)
+    p_dy = _tensor(dy, "dy", bf16, (T, k, N), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, k, K), dtype=bf16, device=dev)
+            p_out = out.data_ptr() or None
+        else:
+            p_out = _tensor(out, "out", bf16, (T, k, K), dev)
+        ws, p_ws, nbytes = _scratch(workspace, experts_dx_workspace_size(T, k, E, N, K, g), dev)
+        check(lib().any4_experts_gemm_dx(fmt, p_dy, p_packed, p_lut, p_alpha, p_beta, p_ids, p_plan, p_out, T, k, E, N,
+                                         K, g, p_ws, nbytes, _current_handle(dev.index)))
+    return out
+
+
+def experts_gemm_dx(dy: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor,
+                    g: int, ids: torch.Tensor, plan: LoraPlan | None = None, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dx bf16 [T, k, K] = dy [T, k, N] W_e, the gradient of the rows that went through
+    experts_gemm.  Where the k pairs of a token shared a row, its gradient is their
+    sum: combine(dx)."""
+    return _experts_gemm_dx(0, dy, packed, lut, alpha, beta, g, ids, plan, out, workspace, stream)
+
+
+def experts_gemm_int4_dx(dy: torch.Tensor, packed: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor, g: int,
+                         ids: torch.Tensor, plan: LoraPlan | None = None, out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """experts_gemm_dx of plain int4 layers."""
+    return _experts_gemm_dx(1, dy, packed, None, alpha, beta, g, ids, plan, out, workspace, stream)
+
+
+def any2_experts_gemm_dx(dy: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: torch.Tensor,
+                         beta: torch.Tensor, g: int, ids: torch.Tensor, plan: LoraPlan | None = None,
+                         out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """experts_gemm_dx of any2 layers."""
+    return _experts_gemm_dx(2, dy, packed, lut, alpha, beta, g, ids, plan, out, workspace, stream)
+
+
+def any3_experts_gemm_dx(dy: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: torch.Tensor,
+                         beta: torch.Tensor, g: int, ids: torch.Tensor, plan: LoraPlan | None = None,
+                         out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """experts_gemm_dx of any3 layers."""
+    return _experts_gemm_dx(3, dy, packed, lut, alpha, beta, g, ids, plan, out, workspace, stream)
+
+
+def combine(y: torch.Tensor, w: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+            out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out bf16 [T, N] = residual + sum_j w[:, j] y[:, j]: the experts' outputs y bf16
+    [T, k, N] as the router weights them (w fp32 [T, k]; None: weights of 1, the sum of
+    the pairs' gradients).  residual bf16 [T, N] may be out itself."""
+    dev, bf16 = _gpu(y, "y", 3), torch.bfloat16
+    T, k, N = y.shape
+    p_y, p_w = _tensor(y, "y", bf16, (T, k, N), dev), _maybe(w, "w", torch.float32, (T, k), dev)
+    p_residual = _maybe(residual, "residual", bf16, (T, N), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, N), dtype=bf16, device=dev)
+        p_out = _tensor(out, "out", bf16, (T, N), dev)
+        check(lib().any4_combine(p_y, p_w, p_residual, p_out, T, k, N, _current_handle(dev.index)))
+    return out
+
+
+def combine_backward(dout: torch.Tensor, y: torch.Tensor, w: torch.Tensor, dy: torch.Tensor | None = None,
+                     dw: torch.Tensor | None = None, stream=None) -> tuple:
+    """(dy bf16 [T, k, N], dw fp32 [T, k]) of combine() for dout bf16 [T, N]; the
+    gradient of the residual is dout itself.  dy may be y itself."""
+    dev, bf16, f32 = _gpu(y, "y", 3), torch.bfloat16, torch.float32
+    T, k, N = y.shape
+    p_y, p_w = _tensor(y, "y", bf16, (T, k, N), dev), _tensor(w, "w", f32, (T, k), dev)
+    p_dout = _tensor(dout, "dout", bf16, (T, N), dev)
+    with _on(dev, stream):
+        if dy is None:
+            dy = torch.empty((T, k, N), dtype=bf16, device=dev)
+        if dw is None:
+            dw = torch.empty((T, k), dtype=f32, device=dev)
+        p_dy, p_dw = _tensor(dy, "dy", bf16, (T, k, N), dev), _tensor(dw, "dw", f32, (T, k), dev)
+        check(lib().any4_combine_backward(p_dout, p_y, p_w, p_dy, p_dw, T, k, N, _current_handle(dev.index)))
+    return dy, dw
 
 
 def read_probe_raw(buf_ptr, nbytes: int, out_ptr, stream=None) -> int:

@@ -5,7 +5,8 @@ import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", f) for f in ("any4.hip", "lora.hip", "gemm_dx.hip")]
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("any4.hip", "lora.hip", "gemm_dx.hip", "ffn.hip",
+                                               "route.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libany4.so")
 

@@ -1,0 +1,1100 @@
+// Products of quantised layers with what a feed-forward block puts around them:
+// bias, activation, gate and residual, for one layer (any4_gemm_act) or for the
+// stacked layers of many experts, each row through the expert that the router
+// chose (any4_experts_gemm), the experts' input gradient (any4_experts_gemm_dx)
+// and the activation's backward pass (any4_act_backward).  The C ABI is declared
+// in include/any4.h.
+//
+//     z[p] = W_e x[p / div] + bias_e      e = ids[p] (one layer: 0)
+//     out[p] = act(z) + residual[p], or with a gate, W_e = [gate; up],
+//     out[p] = act(z_gate) * z_up + residual[p]
+//
+// Rows of one expert are worked on in tiles, from the plan (plan.h) or, for few
+// pairs, from ballots over the ids.
+#include <type_traits>
+
+#include "codes.h"
+#include "plan.h"
+
+namespace {
+
+constexpr int MAX_EXPERTS = 1024;
+constexpr int STEP = 64;                                  // of the summed dimension, k_tile
+constexpr int64_t MAX_PAIRS = static_cast<int64_t>(1) << 20;
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------------------
+// the rows of a product
+// ---------------------------------------------------------------------------
+struct Rows {
+    const int* ids;      // few pairs: their experts; else null
+    const int* plan;     // or the pairs by expert; both null: one layer
+    int P, E, div;       // pairs, experts, pairs that share a row of x
+};
+
+struct Layer {           // of all experts, one after another
+    const uint8_t* packed;
+    const uint16_t *lut, *alpha, *beta;
+    int N, K, g;
+    size_t packed_bytes; // of one expert
+
+    __device__ __forceinline__ const uint8_t* codes(int e) const { return packed + e * packed_bytes; }
+    __device__ __forceinline__ const uint16_t* table(int e) const { return lut + static_cast<size_t>(e) * N * 16; }
+    __device__ __forceinline__ size_t scales(int e) const { return static_cast<size_t>(e) * N * (K / g); }
+};
+
+constexpr int FEW_T = 16;            // rows of a tile of k_few
+constexpr int FEW_P = WAVE;          // pairs up to which tiles come from ballots
+
+struct Tile {
+    int e;          // expert; E: rows without one; -1: no such tile
+    int count;
+};
+
+__device__ __forceinline__ int expert_of(int id, int E) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(E) ? id : E; }
+
+// Tile t of FEW_T rows, its pairs in own[0 .. count): every wave for itself.
+__device__ __forceinline__ Tile find_few(const Rows& r, int t, int* own)
+{
+    const int lane = threadIdx.x & 63;
+    if (r.plan) {
+        if (r.plan[2] != r.P || r.plan[3] != r.E)
+            return {-1, 0};
+        const PlanLayout p(r.P, r.E);
+        const int at = t / (TILE_T / FEW_T), from = t % (TILE_T / FEW_T) * FEW_T;
+        if (at >= r.plan[0])
+            return {-1, 0};
+        const int a = r.plan[p.tile + 2 * static_cast<int64_t>(at)], n = r.plan[p.tile + 2 * static_cast<int64_t>(at) + 1];
+        if (from >= n)
+            return {-1, 0};
+        if (lane < FEW_T)
+            own[lane] = r.plan[p.rows + TILE_T * static_cast<int64_t>(at) + from + lane];
+        wave_sync();
+        return {a < 0 ? r.E : a, n - from < FEW_T ? n - from : FEW_T};
+    }
+    if (!r.ids) {
+        const int left = r.P - t * FEW_T;
+        if (lane < FEW_T)
+            own[lane] = t * FEW_T + lane;
+        wave_sync();
+        return {left > 0 ? 0 : -1, left < FEW_T ? left : FEW_T};
+    }
+    const bool live = lane < r.P;
+    const int a = live ? expert_of(r.ids[lane], r.E) : -1;
+    uint64_t left = __ballot(live);
+    while (left) {
+        const int v = __builtin_amdgcn_readlane(a, __builtin_ctzll(left));
+        const uint64_t m = __ballot(live && a == v);
+        const int n = __builtin_popcountll(m), tiles = (n + FEW_T - 1) / FEW_T;
+        if (t < tiles) {
+            const int rank = __builtin_popcountll(m & ((1ull << lane) - 1));
+            if ((m >> lane & 1) && rank / FEW_T == t)
+                own[rank % FEW_T] = lane;
+            wave_sync();
+            return {v, n - t * FEW_T < FEW_T ? n - t * FEW_T : FEW_T};
+        }
+        t -= tiles;
+        left &= ~m;
+    }
+    return {-1, 0};
+}
+
+// ---------------------------------------------------------------------------
+// activations
+// ---------------------------------------------------------------------------
+enum { ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACTS };
+
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
+
+constexpr float GELU_C = 1.5957691216057308f;       // 2 sqrt(2 / pi)
+constexpr float GELU_D = 0.044715f;
+
+__device__ __forceinline__ float activate(float z, int act)
+{
+    switch (act) {
+    case ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
+    case ACT_SILU: return z * sigmoid(z);
+    case ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case ACT_GELU_TANH: return z * sigmoid(GELU_C * (z + GELU_D * z * z * z));
+    default: return z;
+    }
+}
+
+// act(z) and its slope
+__device__ __forceinline__ void activate_both(float z, int act, float& f, float& slope)
+{
+    switch (act) {
+    case ACT_RELU:
+        f = z > 0.0f || z != z ? z : 0.0f;
+        slope = z > 0.0f ? 1.0f : z != z ? z : 0.0f;
+        break;
+    case ACT_SILU: {
+        const float p = sigmoid(z);
+        f = z * p;
+        slope = p * (1.0f + z * (1.0f - p));
+        break;
+    }
+    case ACT_GELU: {
+        const float p = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+        f = z * p;
+        slope = p + z * 0.39894228040143268f * expf(-0.5f * z * z);
+        break;
+    }
+    case ACT_GELU_TANH: {
+        const float p = sigmoid(GELU_C * (z + GELU_D * z * z * z));
+        f = z * p;
+        slope = p + z * p * (1.0f - p) * GELU_C * (1.0f + 3.0f * GELU_D * z * z);
+        break;
+    }
+    default:
+        f = z;
+        slope = 1.0f;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the epilogue: everything in fp32, each result rounded once
+// ---------------------------------------------------------------------------
+struct Epilogue {
+    const uint16_t* bias;        // [E][N] or null
+    const uint16_t* residual;    // [P][No] or null
+    uint16_t* z;                 // [P][N] or null
+    uint16_t* out;               // [P][No]
+    float* part;                 // [S][P][N] or null (S = 1)
+    int N, No, act, S;           // No = N / 2: gated
+
+    __host__ __device__ __forceinline__ bool gated() const { return No != N; }
+};
+
+__device__ __forceinline__ float half_of(const u32x4_t& v, int i) { return bf16_to_f32(v[i / 2] >> (16 * (i & 1)) & 0xffffu); }
+
+__device__ __forceinline__ u32x4_t round8(const float (&v)[8])
+{
+    u32x4_t o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = f32_to_bf16(v[2 * i]) | f32_to_bf16(v[2 * i + 1]) << 16;
+    return o;
+}
+
+// Columns col .. col + 7 of pair p: v the (gate's) sums, u the up rows' where there
+// is a gate.
+__device__ __forceinline__ void finish8(const Epilogue& q, int e, int p, int col, float (&v)[8], float (&u)[8])
+{
+    const int valid = q.No - col;
+    if (valid <= 0)
+        return;
+    const bool gate = q.gated();
+    if (q.bias) {
+        const uint16_t* b = q.bias + static_cast<size_t>(e) * q.N + col;
+        const u32x4_t bv = load8(b, valid);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] += half_of(bv, i);
+        if (gate) {
+            const u32x4_t bu = load8(b + q.No, valid);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                u[i] += half_of(bu, i);
+        }
+    }
+    if (q.z) {
+        uint16_t* z = q.z + static_cast<size_t>(p) * q.N + col;
+        store8(z, round8(v), valid);
+        if (gate)
+            store8(z + q.No, round8(u), valid);
+    }
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        o[i] = activate(v[i], q.act);
+        if (gate)
+            o[i] *= u[i];
+    }
+    const size_t at = static_cast<size_t>(p) * q.No + col;
+    if (q.residual) {
+        const u32x4_t r = load8(q.residual + at, valid);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] += half_of(r, i);
+    }
+    store8(q.out + at, round8(o), valid);
+}
+
+// ---------------------------------------------------------------------------
+// few rows: packed weights read once, decoded in registers
+// ---------------------------------------------------------------------------
+constexpr int FEW_THREADS = 512;
+constexpr int FEW_WAVES = FEW_THREADS / WAVE;
+constexpr int FEW_ROWS = 64;         // rows of W of a workgroup
+
+struct FewArgs {
+    Rows r;
+    Layer w;
+    const uint16_t* x;
+    Epilogue q;
+};
+
+template <int I, int N, typename F>
+__device__ __forceinline__ void static_for(F&& f)
+{
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        static_for<I + 1, N>(f);
+    }
+}
+
+// D[i][lane] += sum over four k of A[i] B[lane]: A's block ABID for all lanes.
+template <int ABID>
+__device__ __forceinline__ f32x4_t mfma4(s16x4_t a, s16x4_t b, f32x4_t c)
+{
+    return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(a, b, c, 4, ABID, 0);
+}
+
+// The product of 4 * NB rows of x with the lane's row of W over chunks s0 .. s1.
+template <int FMT, int NB>
+__device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, const int* own, int count, int s0, int s1,
+                                            f32x4_t (&acc)[4])
+{
+    const int lane = threadIdx.x & 63, Kc = p.w.K / 128;
+    const uint8_t* packed = p.w.codes(e);
+    const uint16_t* lut = FMT == FMT_INT4 ? nullptr : p.w.table(e);
+    const uint16_t *alpha = p.w.alpha + p.w.scales(e), *beta = p.w.beta + p.w.scales(e);
+    const uint16_t* x[NB];           // 8 k of a row: the lane uses the even or the odd ones
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int i = 4 * b + (lane & 3);
+        x[b] = p.x + static_cast<size_t>(own[i < count ? i : count - 1] / p.r.div) * p.w.K + 8 * (lane >> 3);
+    }
+    const uint32_t pick = lane & 4 ? 0x07060302u : 0x05040100u;
+    for (int s = s0; s < s1; ++s) {
+        uint32_t code[4][4];
+        const RowTable row = fetch_table<FMT>(lut, alpha, beta, wr, Kc, s, p.w.g);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            fetch_codes<FMT>(packed, wr, Kc, s, q, code[q]);
+        s16x4_t a[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x[b] + s * 128 + 64 * j);
+                u32x2_t o;
+                o[0] = __builtin_amdgcn_perm(v[1], v[0], pick);
+                o[1] = __builtin_amdgcn_perm(v[3], v[2], pick);
+                a[b][j] = __builtin_bit_cast(s16x4_t, o);
+            }
+        const ByteTable<FMT> t(row);
+        static_for<0, 4>([&](auto q_) __attribute__((always_inline)) {
+            constexpr int q = decltype(q_)::value;
+            uint32_t v[16];          // of each eight k (0, 2), (4, 6), (1, 3), (5, 7)
+            decode(t, code[q], v);
+            static_for<0, 8>([&](auto i_) __attribute__((always_inline)) {
+                constexpr int i = decltype(i_)::value;
+                const u32x2_t w = {v[2 * i], v[2 * i + 1]};
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    acc[b] = mfma4<8 * (q & 1) + i>(a[b][q / 2], __builtin_bit_cast(s16x4_t, w), acc[b]);
+            });
+        });
+    }
+}
+
+// A lane has one row of W, so that its table and scales serve 128 weights at a
+// time, which the matrix cores multiply as they stand: the 16 blocks of a 4 x 4 x 4
+// product hold 64 rows of W, four k each, and four rows of x go to all of them.
+template <int FMT>
+__global__ __launch_bounds__(FEW_THREADS) void k_few(const FewArgs p)
+{
+    __shared__ int own[FEW_WAVES][FEW_T];
+    __shared__ float red[FEW_WAVES][FEW_T][WAVE];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Tile t = find_few(p.r, blockIdx.y, own[w]);
+    if (t.e < 0)
+        return;
+    const bool gate = p.q.gated();
+    const int half = gate ? lane >> 5 : 0;
+    const int col = gate ? blockIdx.x * 32 + (lane & 31) : blockIdx.x * 64 + lane;
+    const bool live = col < p.q.No;
+    const int wr = live ? col + half * p.q.No : 0;
+    if (t.e == p.r.E) {              // no expert: zeros
+        if (blockIdx.z == 0 && live)
+            for (int i = w; i < t.count; i += FEW_WAVES) {
+                if (half == 0)
+                    p.q.out[static_cast<size_t>(own[w][i]) * p.q.No + col] = 0;
+                if (p.q.z)
+                    p.q.z[static_cast<size_t>(own[w][i]) * p.q.N + wr] = 0;
+            }
+        return;
+    }
+    const int Kc = p.w.K / 128, parts = p.q.S * FEW_WAVES, at = blockIdx.z * FEW_WAVES + w;
+    const int s0 = static_cast<int>(static_cast<int64_t>(Kc) * at / parts);
+    const int s1 = static_cast<int>(static_cast<int64_t>(Kc) * (at + 1) / parts);
+    f32x4_t acc[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        acc[b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (t.count <= 4)
+        few_product<FMT, 1>(p, t.e, wr, own[w], t.count, s0, s1, acc);
+    else if (t.count <= 8)
+        few_product<FMT, 2>(p, t.e, wr, own[w], t.count, s0, s1, acc);
+    else
+        few_product<FMT, 4>(p, t.e, wr, own[w], t.count, s0, s1, acc);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        if (4 * b < t.count)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                red[w][4 * b + i][lane] = acc[b][i];
+    __syncthreads();
+    for (int i = w; i < t.count; i += FEW_WAVES) {
+        const int pair = own[w][i];
+        float v = 0.0f;
+#pragma unroll
+        for (int o = 0; o < FEW_WAVES; ++o)
+            v += red[o][i][lane];
+        if (p.q.part) {
+            if (live)
+                p.q.part[(static_cast<size_t>(blockIdx.z) * p.r.P + pair) * p.q.N + wr] = v;
+            continue;
+        }
+        if (p.q.bias && live)
+            v += bf16_to_f32(p.q.bias[static_cast<size_t>(t.e) * p.q.N + wr]);
+        if (p.q.z && live)
+            p.q.z[static_cast<size_t>(pair) * p.q.N + wr] = static_cast<uint16_t>(f32_to_bf16(v));
+        const float up = __shfl(v, lane | 32);
+        if (half || !live)
+            continue;
+        v = activate(v, p.q.act);
+        if (gate)
+            v *= up;
+        const size_t to = static_cast<size_t>(pair) * p.q.No + col;
+        if (p.q.residual)
+            v += bf16_to_f32(p.q.residual[to]);
+        p.q.out[to] = static_cast<uint16_t>(f32_to_bf16(v));
+    }
+}
+
+// The splits' sums in order, then the epilogue; 8 columns a thread.
+__global__ __launch_bounds__(256) void k_join(const Epilogue q, const int* __restrict__ ids, int P, int E, size_t pieces)
+{
+    const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;
+    if (i >= pieces)
+        return;
+    const int per = (q.No + 7) / 8, p = static_cast<int>(i / per), col = static_cast<int>(i % per) * 8;
+    const int e = ids ? expert_of(ids[p], E) : 0;
+    if (ids && e == E)
+        return;                      // zeros are there already
+    float v[8], u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        v[k] = u[k] = 0.0f;
+    const int valid = q.No - col;
+    for (int s = 0; s < q.S; ++s) {
+        const float* f = q.part + (static_cast<size_t>(s) * P + p) * q.N + col;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h && !q.gated())
+                break;
+            float (&to)[8] = h ? u : v;
+            const float* from = f + h * q.No;
+            if (valid >= 8) {
+                const f32x4_t a = *reinterpret_cast<const f32x4_a4_t*>(from), b = *reinterpret_cast<const f32x4_a4_t*>(from + 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    to[k] += a[k];
+                    to[4 + k] += b[k];
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < valid)
+                        to[k] += from[k];
+            }
+        }
+    }
+    finish8(q, e, p, col, v, u);
+}
+
+// ---------------------------------------------------------------------------
+// more rows: tiles for the matrix cores, weights decoded into LDS
+// ---------------------------------------------------------------------------
+struct TileArgs {
+    Rows r;
+    Layer w;
+    const uint16_t* x;       // [rows][D], D the summed dimension (padded to 8)
+    Epilogue q;
+    int rows, D, steps;
+    int tiles_m, tiles_n;
+};
+
+// The tile's expert, its pairs among the plan's rows and their number.  Every
+// wave sums the experts' tiles for itself.
+__device__ __forceinline__ Tile find_tile(const Rows& r, int t, int BM, int64_t& first)
+{
+    const int lane = threadIdx.x & 63;
+    if (!r.plan) {
+        const int left = r.P - t * BM;
+        return {left > 0 ? 0 : -1, left < BM ? left : BM};
+    }
+    if (r.plan[2] != r.P || r.plan[3] != r.E)
+        return {-1, 0};
+    const PlanLayout p(r.P, r.E);
+    for (int e0 = 0; e0 <= r.E; e0 += WAVE) {
+        const int e = e0 + lane;
+        const int n = e <= r.E ? r.plan[p.count + e] : 0, at = e <= r.E ? r.plan[p.first + e] : 0;
+        const int tiles = (n + BM - 1) / BM;
+        int sum = tiles;
+        for (int d = 1; d < WAVE; d <<= 1) {
+            const int o = __shfl_up(sum, d);
+            sum += lane >= d ? o : 0;
+        }
+        const uint64_t hit = __ballot(t < sum);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            const int before = __builtin_amdgcn_readlane(sum - tiles, l), rows = __builtin_amdgcn_readlane(n, l);
+            const int from = (t - before) * BM;
+            first = p.rows + static_cast<int64_t>(__builtin_amdgcn_readlane(at, l)) * TILE_T + from;
+            return {e0 + l, rows - from < BM ? rows - from : BM};
+        }
+        t -= __builtin_amdgcn_readlane(sum, WAVE - 1);
+    }
+    return {-1, 0};
+}
+
+// Columns of the products of a wave: place 16 t + rho of its 64 holds column
+// 16 (rho / 4) + 4 t + rho % 4, so that a lane's results are 16 adjacent columns.
+__device__ __forceinline__ int column_of(int place) { return 16 * (place >> 2 & 3) + 4 * (place >> 4 & 3) + (place & 3); }
+
+// Rows of 64 values in LDS, eight pieces of 16 bytes; piece q stands at q ^ key(row):
+// 16 rows of an operand read, and 16 rows that lanes write, touch all 64 banks once.
+__device__ __forceinline__ int key(int row) { return row >> 1 & 7; }
+// rows 2 and 3 of each four exchanged, so that rows r and r + 2 lie in other banks
+template <bool TURN>
+__device__ __forceinline__ int row_at(int row) { return TURN ? row ^ (row >> 1 & 1) : row; }
+
+// The weights of eight k in order from decode()'s (0, 2), (4, 6), (1, 3), (5, 7).
+__device__ __forceinline__ u32x4_t in_order(const uint32_t* v)
+{
+    return u32x4_t{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
+                   __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
+}
+
+__device__ __forceinline__ void put8(float* to, f32x4_t a, f32x4_t b, int valid)
+{
+    if (valid >= 8) {
+        *reinterpret_cast<f32x4_a4_t*>(to) = a;
+        *reinterpret_cast<f32x4_a4_t*>(to + 4) = b;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i < valid)
+            to[i] = a[i];
+        if (4 + i < valid)
+            to[4 + i] = b[i];
+    }
+}
+
+// 2 x WN waves of RM x 4 blocks of 16 x 16.  TURN: the sum runs over the rows of W
+// and the results are its columns (the input's gradient).
+template <int FMT, int WN, int RM, bool TURN>
+__global__ __launch_bounds__(128 * WN) void k_tile(const TileArgs p)
+{
+    constexpr int BM = 32 * RM, BN = WN * 64, WAVES = 2 * WN, LA = BM / 8 / WAVES;
+    static_assert(LA >= 1, "every wave loads rows of x");
+    __shared__ __attribute__((aligned(16))) uint16_t sa0[BM * STEP], sb0[BN * STEP], sa1[BM * STEP], sb1[BN * STEP];
+    __shared__ int pairs[BM];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
+    const int tiles = p.tiles_m * p.tiles_n;
+    // workgroups go to the eight XCDs in turn: each XCD gets a run of tiles, four
+    // rows of tiles high, whose operands its L2 then shares
+    int id = blockIdx.x;
+    if (tiles % 8 == 0)
+        id = id % 8 * (tiles / 8) + id / 8;
+    constexpr int HIGH = 4;
+    const int band = id / (HIGH * p.tiles_n), high = p.tiles_m - band * HIGH < HIGH ? p.tiles_m - band * HIGH : HIGH;
+    const int in_band = id - band * HIGH * p.tiles_n;
+    const int tm = band * HIGH + in_band % high, tn = in_band / high;
+    int64_t first = 0;
+    const Tile t = find_tile(p.r, tm, BM, first);
+    if (t.e < 0)
+        return;
+    for (int i = tid; i < BM; i += 128 * WN)
+        pairs[i] = i >= t.count ? -1 : p.r.plan ? p.r.plan[first + i] : tm * BM + i;
+    __syncthreads();
+    const bool gate = p.q.gated();
+    const int col0 = gate ? tn * (BN / 2) : tn * BN;       // of out
+    if (t.e == p.r.E) {              // no expert: zeros
+        if (blockIdx.y == 0)
+            for (int i = w; i < t.count; i += WAVES)
+                for (int o = lane; o < (gate ? BN / 2 : BN); o += WAVE)
+                    if (col0 + o < p.q.No) {
+                        p.q.out[static_cast<size_t>(pairs[i]) * p.q.No + col0 + o] = 0;
+                        if (p.q.z) {
+                            uint16_t* z = p.q.z + static_cast<size_t>(pairs[i]) * p.q.N + col0 + o;
+                            z[0] = 0;
+                            if (gate)
+                                z[p.q.No] = 0;
+                        }
+                    }
+        return;
+    }
+    const int s0 = static_cast<int>(static_cast<int64_t>(p.steps) * blockIdx.y / p.q.S);
+    const int s1 = static_cast<int>(static_cast<int64_t>(p.steps) * (blockIdx.y + 1) / p.q.S);
+
+    // x: a wave's load instruction fills 8 rows of a tile; lane: row lane / 8, place lane % 8
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(p.x), static_cast<short>(0), static_cast<int>(static_cast<size_t>(p.rows) * p.D * 2), 0x00020000);
+    uint32_t ga[LA];
+    int na[LA];                      // TURN: where the piece stands in the sum
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+        const int r = (w * LA + i) * 8 + lane / 8, pair = pairs[r], piece = (lane & 7) ^ key(r);
+        ga[i] = pair < 0 ? OOR : static_cast<uint32_t>(pair / p.r.div) * (static_cast<uint32_t>(p.D) * 2u) + piece * 16u;
+        na[i] = 8 * piece;
+    }
+    auto fetch = [&](int st, uint16_t* sa) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < LA; ++i)
+            load_lds(ra, sa + (w * LA + i) * 8 * STEP, static_cast<int>(TURN && st * STEP + na[i] >= p.D ? OOR : ga[i]), st * STEP * 2);
+    };
+    // W: a thread decodes 32 weights a step
+    const int Kc = p.w.K / 128;
+    const uint8_t* packed = p.w.codes(t.e);
+    const uint16_t* lut = FMT == FMT_INT4 ? nullptr : p.w.table(t.e);
+    const uint16_t *alpha = p.w.alpha + p.w.scales(t.e), *beta = p.w.beta + p.w.scales(t.e);
+    const int place = tid % BN, h = tid / BN;      // forward: half h of the step's k of the row at a place
+    int wr = 0;
+    bool live = true;
+    if constexpr (!TURN) {
+        const int b = column_of(place), half = gate ? b >> 3 & 1 : 0;
+        const int col = gate ? col0 + (place & ~63) / 2 + 8 * (b >> 4) + (b & 7) : col0 + (place & ~63) + b;
+        live = col < p.q.No;
+        wr = live ? col + half * p.q.No : 0;
+    }
+    // TURN: the 32 k of the wave (any where the tile reaches past the last)
+    const int slot = col0 + 32 * w < p.w.K ? (col0 >> 5) + w : 0;
+    uint32_t code[4];
+    RowTable row;
+    auto fetch_weights = [&](int st) __attribute__((always_inline)) {
+        if constexpr (TURN) {
+            const int n = st * STEP + lane < p.w.N ? st * STEP + lane : 0;
+            row = fetch_table<FMT>(lut, alpha, beta, n, Kc, slot >> 2, p.w.g);
+            fetch_codes<FMT>(packed, n, Kc, slot >> 2, slot & 3, code);
+        } else {
+            fetch_codes<FMT>(packed, wr, Kc, st >> 1, 2 * (st & 1) + h, code);
+            if (!(st & 1) || st == s0)
+                row = fetch_table<FMT>(lut, alpha, beta, wr, Kc, st >> 1, p.w.g);
+        }
+    };
+    auto unpack = [&](int st, uint16_t* sb) __attribute__((always_inline)) {
+        const ByteTable<FMT> table(row);
+        uint32_t v[16];
+        decode(table, code, v);
+        if constexpr (TURN) {
+            const bool in = st * STEP + lane < p.w.N;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int k = first_k(i) + 2 * (lane & 1);                   // of the wave's 32
+                const int b = 32 * (w & 1) + k;
+                const int at = 64 * (w >> 1) + 16 * (b >> 2 & 3) + 4 * (b >> 4) + (b & 3);
+                const uint32_t o = pair_rows(in ? v[i] : 0u, lane & 1);
+                reinterpret_cast<uint32_t*>(sb)[row_at<true>(at) * (STEP / 2) + ((lane >> 3) ^ key(at)) * 4 + (lane >> 1 & 3)] = o;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<u32x4_t*>(sb + place * STEP + ((4 * h + i) ^ key(place)) * 8) = in_order(v + 4 * i);
+        }
+    };
+    f32x4_t acc[RM][4];
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const int wm = (w / WN) * (RM * 16), wn = (w % WN) * 64;
+    auto multiply = [&](const uint16_t* sa, const uint16_t* sb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            bf16x8_t a[RM], b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = wn + 16 * j + c;
+                b[j] = *reinterpret_cast<const bf16x8_t*>(sb + row_at<TURN>(at) * STEP + ((4 * kk + g) ^ key(at)) * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+                a[i] = *reinterpret_cast<const bf16x8_t*>(sa + (wm + 16 * i + c) * STEP + ((4 * kk + g) ^ key(wm + 16 * i + c)) * 8);
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = mfma(b[j], a[i], acc[i][j]);
+        }
+    };
+    // this step's tiles are in, and every wave has read the other buffers
+    auto meet = [&]() __attribute__((always_inline)) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    };
+    if (s0 < s1) {
+        fetch(s0, sa0);
+        fetch_weights(s0);
+        unpack(s0, sb0);
+        if (s0 + 1 < s1)
+            fetch_weights(s0 + 1);
+    }
+    auto step = [&](int st, uint16_t* sa, uint16_t* sb, uint16_t* sa_next, uint16_t* sb_next) __attribute__((always_inline)) {
+        meet();
+        if (st + 1 < s1) {
+            fetch(st + 1, sa_next);
+            unpack(st + 1, sb_next);
+            if (st + 2 < s1)
+                fetch_weights(st + 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(sa, sb);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    int st = s0;
+    for (; st + 1 < s1; st += 2) {
+        step(st, sa0, sb0, sa1, sb1);
+        step(st + 1, sa1, sb1, sa0, sb0);
+    }
+    if (st < s1)
+        step(st, sa0, sb0, sa1, sb1);
+    // The sums leave through LDS of the wave's own, so that lanes next to one another
+    // write columns next to one another: 16 pieces of four floats a row, piece q at
+    // q ^ row.  With a gate its columns come first, those of the up rows behind.
+    meet();
+    constexpr int HALVES = RM == 8 ? 2 : 1, ROWS = 16 * RM / HALVES;
+    const int room = w * 4 / WAVES;       // a wave's, or two waves', of the four buffers
+    uint16_t* const in = room == 0 ? sa0 : room == 1 ? sb0 : room == 2 ? sa1 : sb1;
+    f32x4_t* stage = reinterpret_cast<f32x4_t*>(in) + w % (WAVES / 4) * (ROWS * 16);
+    const int pieces = gate ? 4 : 8;      // of eight columns of out a row
+#pragma unroll
+    for (int half = 0; half < HALVES; ++half) {
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < RM / HALVES; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                stage[(16 * i + c) * 16 + ((gate ? 8 * (j >> 1) + 2 * g + (j & 1) : 4 * g + j) ^ c)] = acc[half * (RM / HALVES) + i][j];
+        wave_sync();
+        for (int o = lane; o < ROWS * pieces; o += WAVE) {
+            const int row = o / pieces, q = o % pieces;
+            const int pair = pairs[wm + half * ROWS + row], col = col0 + (gate ? wn / 2 : wn) + 8 * q;
+            if (pair < 0 || col >= p.q.No)
+                continue;
+            f32x4_t f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                f[e] = stage[row * 16 + ((2 * q + (e & 1) + (gate ? 8 * (e >> 1) : 0)) ^ (row & 15))];
+            if (p.q.part) {
+                float* to = p.q.part + (static_cast<size_t>(blockIdx.y) * p.r.P + pair) * p.q.N + col;
+                put8(to, f[0], f[1], p.q.No - col);
+                if (gate)
+                    put8(to + p.q.No, f[2], f[3], p.q.No - col);
+                continue;
+            }
+            float v[8], u[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = f[0][e];
+                v[4 + e] = f[1][e];
+                u[e] = f[2][e];
+                u[4 + e] = f[3][e];
+            }
+            finish8(p.q, t.e, pair, col, v, u);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the activation's backward pass
+// ---------------------------------------------------------------------------
+struct BwdArgs {
+    const uint16_t *dy, *z;
+    uint16_t* dz;
+    float* part;             // [slabs][N] or null: no bias
+    int M, N, No, act, slab; // rows of a workgroup
+};
+
+constexpr int BWD_COLS = 8 * WAVE;           // columns of out of a workgroup
+
+// A wave takes 512 columns of every fourth row of a slab; the column sums of the
+// four waves meet in LDS.
+__global__ __launch_bounds__(256) void k_act_bwd(const BwdArgs p)
+{
+    __shared__ float red[4][2][8][WAVE];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col = blockIdx.x * BWD_COLS + 8 * lane, valid = p.No - col;
+    const int m0 = blockIdx.y * p.slab, m1 = m0 + p.slab < p.M ? m0 + p.slab : p.M;
+    const bool gate = p.No != p.N;
+    float sum[2][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        sum[0][i] = sum[1][i] = 0.0f;
+    for (int m = m0 + w; m < m1; m += 4) {
+        if (valid <= 0)
+            break;
+        const uint16_t* z = p.z + static_cast<size_t>(m) * p.N + col;
+        uint16_t* dz = p.dz + static_cast<size_t>(m) * p.N + col;
+        const u32x4_t dy = load8(p.dy + static_cast<size_t>(m) * p.No + col, valid), zg = load8(z, valid);
+        u32x4_t zu = {0u, 0u, 0u, 0u};
+        if (gate)
+            zu = load8(z + p.No, valid);
+        float a[8], b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float f, slope;
+            activate_both(half_of(zg, i), p.act, f, slope);
+            const float d = half_of(dy, i);
+            a[i] = gate ? d * half_of(zu, i) * slope : d * slope;
+            b[i] = d * f;
+            sum[0][i] += a[i];
+            sum[1][i] += b[i];
+        }
+        store8(dz, round8(a), valid);
+        if (gate)
+            store8(dz + p.No, round8(b), valid);
+    }
+    if (!p.part)
+        return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            red[w][h][i][lane] = sum[h][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * BWD_COLS; i += 256) {
+        const int h = i / BWD_COLS, o = i % BWD_COLS, c = blockIdx.x * BWD_COLS + o;
+        if (c >= p.No || (h && !gate))
+            continue;
+        p.part[static_cast<size_t>(blockIdx.y) * p.N + h * p.No + c] =
+            red[0][h][o & 7][o >> 3] + red[1][h][o & 7][o >> 3] + red[2][h][o & 7][o >> 3] + red[3][h][o & 7][o >> 3];
+    }
+}
+
+__global__ __launch_bounds__(256) void k_bias_sum(const float* __restrict__ part, float* __restrict__ dbias, int N, int slabs)
+{
+    const int n = blockIdx.x * 256 + threadIdx.x;
+    if (n >= N)
+        return;
+    float v = 0.0f;
+    for (int s = 0; s < slabs; ++s)
+        v += part[static_cast<size_t>(s) * N + n];
+    dbias[n] = v;
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+size_t layer_bytes(int fmt, int64_t N, int64_t K)
+{
+    return static_cast<size_t>((N + 15) / 16 * 16) * (K / 8) * (fmt == FMT_ANY2 ? 2 : fmt == FMT_ANY3 ? 3 : 4);
+}
+
+// How a product is run: the rows of a tile (0: k_few), its columns, tiles and splits.
+struct Shape {
+    int rm, wn, S;
+    int64_t tiles_m, tiles_n;
+};
+
+int64_t few_tiles(int64_t P, int64_t E, bool experts)
+{
+    if (!experts)
+        return (P + FEW_T - 1) / FEW_T;
+    if (P <= FEW_P)
+        return P / FEW_T + (P < E + 1 ? P : E + 1);
+    return PlanLayout(P, E).TB * (TILE_T / FEW_T);
+}
+
+// P rows through E experts (experts = false: one layer), D summed, C columns of the
+// product (both halves of a gate).
+Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool turn)
+{
+    Shape s{0, 2, 1, 0, 0};
+    const int64_t each = (P + E - 1) / E;        // rows of an expert, on average
+    const int64_t live = experts ? (P < E ? P : E) : 1;
+    if (!turn && (experts ? P <= FEW_P || each <= 12 : P <= 16)) {
+        s.tiles_m = few_tiles(P, E, experts);
+        s.tiles_n = (C + FEW_ROWS - 1) / FEW_ROWS;
+        const int64_t groups = s.tiles_n * live, chunks = D / 128;
+        while (s.S < 8 && groups * s.S < 256 && chunks >= 8 * 2 * s.S)
+            s.S *= 2;
+        return s;
+    }
+    if (each > 128 && C >= 1024) {
+        s.rm = 8;
+        s.wn = 4;
+    } else {
+        s.rm = each > 64 ? 4 : each > 32 ? 2 : 1;
+    }
+    const int64_t bm = 32 * s.rm, bn = 64 * s.wn;
+    s.tiles_m = experts ? P / bm + (P < E + 1 ? P : E + 1) : (P + bm - 1) / bm;
+    s.tiles_n = (C + bn - 1) / bn;
+    const int64_t groups = s.tiles_n * live * ((each + bm - 1) / bm), steps = (D + STEP - 1) / STEP;
+    while (s.S < 8 && groups * s.S <= 128 && steps >= 8 * s.S)
+        s.S *= 2;
+    return s;
+}
+
+size_t part_bytes(const Shape& s, int64_t P, int64_t C) { return s.S > 1 ? up256(static_cast<size_t>(s.S) * P * C * 4) : 0; }
+
+template <int FMT, bool TURN>
+void launch_tile(const Shape& s, const TileArgs& a, hipStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>(s.tiles_m * s.tiles_n), static_cast<unsigned>(s.S));
+#define TILE(WN_, RM_) hipLaunchKernelGGL((k_tile<FMT, WN_, RM_, TURN>), grid, dim3(128 * WN_), 0, stream, a)
+    if (s.rm == 8) TILE(4, 8);
+    else if (s.rm == 4) TILE(2, 4);
+    else if (s.rm == 2) TILE(2, 2);
+    else TILE(2, 1);
+#undef TILE
+}
+
+template <bool TURN>
+void launch_tile(int fmt, const Shape& s, const TileArgs& a, hipStream_t stream)
+{
+    if (fmt == FMT_ANY4) launch_tile<FMT_ANY4, TURN>(s, a, stream);
+    else if (fmt == FMT_INT4) launch_tile<FMT_INT4, TURN>(s, a, stream);
+    else if (fmt == FMT_ANY2) launch_tile<FMT_ANY2, TURN>(s, a, stream);
+    else launch_tile<FMT_ANY3, TURN>(s, a, stream);
+}
+
+void launch_few(int fmt, const Shape& s, const FewArgs& a, hipStream_t stream)
+{
+    const int per = a.q.gated() ? FEW_ROWS / 2 : FEW_ROWS;
+    const dim3 grid(static_cast<unsigned>((a.q.No + per - 1) / per), static_cast<unsigned>(s.tiles_m), static_cast<unsigned>(s.S));
+#define FEW(FMT_) hipLaunchKernelGGL(k_few<FMT_>, grid, dim3(FEW_THREADS), 0, stream, a)
+    if (fmt == FMT_ANY4) FEW(FMT_ANY4);
+    else if (fmt == FMT_INT4) FEW(FMT_INT4);
+    else if (fmt == FMT_ANY2) FEW(FMT_ANY2);
+    else FEW(FMT_ANY3);
+#undef FEW
+}
+
+constexpr int64_t GIB2 = static_cast<int64_t>(1) << 31;
+
+bool act_ok(int act) { return act >= 0 && act < ACTS; }
+bool fmt_ok(int fmt) { return fmt >= FMT_ANY4 && fmt <= FMT_ANY3; }
+
+// P rows of out [P][No], x [X][K], a layer [N][K] of each of E experts
+bool sizes_ok(int64_t P, int64_t X, int64_t E, int64_t N, int64_t K, int64_t g)
+{
+    return P >= 0 && P <= MAX_PAIRS && X >= 0 && E >= 1 && E <= MAX_EXPERTS && N >= 0 && N < GIB2 / 2 && K > 0 && K < GIB2 / 2 &&
+           g > 0 && g % 128 == 0 && K % g == 0 && N * K < 2 * GIB2 && (P == 0 || N < GIB2 / 2 / P) && (X == 0 || K < GIB2 / 2 / X);
+}
+
+any4_status product(int fmt, const Rows& rows, int64_t X, const uint16_t* x, const Layer& w, const Epilogue& q, const int32_t* ids,
+                    void* workspace, size_t workspace_bytes, bool experts, hipStream_t stream)
+{
+    const Shape s = shape_of(rows.P, rows.E, experts, w.K, w.N, false);
+    char* at = static_cast<char*>(workspace);
+    Rows r = rows;
+    Epilogue e = q;
+    e.S = s.S;
+    size_t need = part_bytes(s, r.P, w.N);
+    if (experts && r.P <= FEW_P) {
+        r.plan = nullptr;
+        r.ids = ids;
+    } else if (experts && !r.plan) {
+        const size_t bytes = any4_lora_plan_bytes(r.P, r.E);
+        if (workspace_bytes < need + bytes || !workspace)
+            return workspace ? ANY4_E_WORKSPACE : ANY4_E_NULL;
+        const any4_status st = any4_lora_plan(ids, at, bytes, r.P, r.E, stream);
+        if (st != ANY4_OK)
+            return st;
+        r.plan = reinterpret_cast<const int*>(at);
+        at += up256(bytes);
+        workspace_bytes -= bytes;
+    }
+    if (need && (workspace_bytes < need || !workspace))
+        return workspace ? ANY4_E_WORKSPACE : ANY4_E_NULL;
+    if (s.S > 1)
+        e.part = reinterpret_cast<float*>(at);
+    if (s.rm == 0) {
+        launch_few(fmt, s, FewArgs{r, w, x, e}, stream);
+    } else {
+        r.ids = nullptr;
+        launch_tile<false>(fmt, s, TileArgs{r, w, x, e, static_cast<int>(X), w.K, w.K / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
+                           stream);
+    }
+    if (s.S > 1) {
+        const size_t pieces = static_cast<size_t>(r.P) * ((e.No + 7) / 8);
+        hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, e, experts ? ids : nullptr, r.P, r.E,
+                           pieces);
+    }
+    return launch_status();
+}
+
+int64_t bwd_slab(int64_t M, int64_t No)
+{
+    // about eight workgroups a CU, at least four rows each
+    const int64_t across = (No + BWD_COLS - 1) / BWD_COLS, want = (2048 + across - 1) / across;
+    const int64_t slab = (M + want - 1) / want;
+    return (slab + 3) / 4 * 4;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t any4_gemm_act_workspace_size(int64_t M, int64_t N, int64_t K, int64_t g)
+{
+    if (M <= 0 || N <= 0 || !sizes_ok(M, M, 1, N, K, g))
+        return 0;
+    return part_bytes(shape_of(M, 1, false, K, N, false), M, N);
+}
+
+any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* packed, const uint16_t* lut, const uint16_t* alpha,
+                          const uint16_t* beta, const uint16_t* bias, const uint16_t* residual, uint16_t* z, uint16_t* out,
+                          any4_activation act, int gate, int64_t M, int64_t N, int64_t K, int64_t g, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream)
+{
+    const int fmt = static_cast<int>(format);
+    if (!fmt_ok(fmt) || !act_ok(act) || !sizes_ok(M, M, 1, N, K, g) || (gate && N % 2))
+        return ANY4_E_SHAPE;
+    if (M == 0 || N == 0)
+        return ANY4_OK;
+    if (!x || !packed || (fmt != FMT_INT4 && !lut) || !alpha || !beta || !out)
+        return ANY4_E_NULL;
+    if (!is_aligned(x, 16) || !is_aligned(packed, 16) || !is_aligned(lut, 2) || !is_aligned(alpha, 2) || !is_aligned(beta, 2) ||
+        !is_aligned(bias, 2) || !is_aligned(residual, 2) || !is_aligned(z, 2) || !is_aligned(out, 2) || !is_aligned(workspace, 16))
+        return ANY4_E_ALIGN;
+    (void)hipGetLastError();
+    const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
+    const Epilogue q{bias, residual, z, out, nullptr, static_cast<int>(N), static_cast<int>(gate ? N / 2 : N), static_cast<int>(act), 1};
+    return product(fmt, Rows{nullptr, nullptr, static_cast<int>(M), 1, 1}, M, x, w, q, nullptr, workspace, workspace_bytes, false, stream);
+}
+
+size_t any4_act_backward_workspace_size(int64_t M, int64_t N, int gate)
+{
+    if (M <= 0 || N <= 0 || M > MAX_PAIRS || N >= GIB2 / 2 / M || (gate && N % 2))
+        return 0;
+    const int64_t slab = bwd_slab(M, gate ? N / 2 : N), slabs = (M + slab - 1) / slab;
+    return up256(static_cast<size_t>(slabs) * N * 4);
+}
+
+any4_status any4_act_backward(const uint16_t* dy, const uint16_t* z, uint16_t* dz, float* dbias, any4_activation act, int gate,
+                              int64_t M, int64_t N, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!act_ok(act) || M < 0 || M > MAX_PAIRS || N < 0 || N >= GIB2 / 2 || (M > 0 && N >= GIB2 / 2 / M) || (gate && N % 2))
+        return ANY4_E_SHAPE;
+    if (N == 0 || (M == 0 && !dbias))
+        return ANY4_OK;
+    if (M > 0 && (!dy || !z || !dz || (dbias && !workspace)))
+        return ANY4_E_NULL;
+    if (!is_aligned(dbias, 4) || (M > 0 && (!is_aligned(dy, 2) || !is_aligned(z, 2) || !is_aligned(dz, 2) || !is_aligned(workspace, 16))))
+        return ANY4_E_ALIGN;
+    const int n = static_cast<int>(N), no = static_cast<int>(gate ? N / 2 : N);
+    const int slab = M > 0 ? static_cast<int>(bwd_slab(M, no)) : 1, slabs = static_cast<int>((M + slab - 1) / slab);
+    if (dbias && workspace_bytes < any4_act_backward_workspace_size(M, N, gate))
+        return ANY4_E_WORKSPACE;
+    (void)hipGetLastError();
+    float* part = dbias ? static_cast<float*>(workspace) : nullptr;
+    if (M > 0)
+        hipLaunchKernelGGL(k_act_bwd, dim3(static_cast<unsigned>((no + BWD_COLS - 1) / BWD_COLS), static_cast<unsigned>(slabs)), dim3(256), 0,
+                           stream, BwdArgs{dy, z, dz, part, static_cast<int>(M), n, no, static_cast<int>(act), slab});
+    if (dbias)
+        hipLaunchKernelGGL(k_bias_sum, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, part, dbias, n, slabs);
+    return launch_status();
+}
+
+size_t any4_experts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g)
+{
+    if (T <= 0 || k <= 0 || N <= 0 || T > MAX_PAIRS || k > MAX_PAIRS || !sizes_ok(T * k, T * k, E, N, K, g))
+        return 0;
+    const int64_t P = T * k;
+    return part_bytes(shape_of(P, E, true, K, N, false), P, N) + (P <= FEW_P ? 0 : any4_lora_plan_bytes(P, E));
+}
+
+any4_status any4_experts_gemm(any4_format format, const uint16_t* x, int per_pair, const uint8_t* packed, const uint16_t* lut,
+                              const uint16_t* alpha, const uint16_t* beta, const uint16_t* bias, const int32_t* ids, const void* plan,
+                              uint16_t* z, uint16_t* out, any4_activation act, int gate, int64_t T, int64_t k, int64_t E, int64_t N,
+                              int64_t K, int64_t g, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const int fmt = static_cast<int>(format);
+    if (!fmt_ok(fmt) || !act_ok(act) || T < 0 || k < 1 || T > MAX_PAIRS || k > MAX_PAIRS ||
+        !sizes_ok(T * k, per_pair ? T * k : T, E, N, K, g) || (gate && N % 2))
+        return ANY4_E_SHAPE;
+    if (T == 0 || N == 0)
+        return ANY4_OK;
+    if (!x || !packed || (fmt != FMT_INT4 && !lut) || !alpha || !beta || !ids || !out)
+        return ANY4_E_NULL;
+    if (!is_aligned(x, 16) || !is_aligned(packed, 16) || !is_aligned(lut, 2) || !is_aligned(alpha, 2) || !is_aligned(beta, 2) ||
+        !is_aligned(bias, 2) || !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(z, 2) || !is_aligned(out, 2) ||
+        !is_aligned(workspace, 16))
+        return ANY4_E_ALIGN;
+    (void)hipGetLastError();
+    const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
+    const Epilogue q{bias, nullptr, z, out, nullptr, static_cast<int>(N), static_cast<int>(gate ? N / 2 : N), static_cast<int>(act), 1};
+    const Rows r{nullptr, static_cast<const int*>(plan), static_cast<int>(T * k), static_cast<int>(E), per_pair ? 1 : static_cast<int>(k)};
+    return product(fmt, r, per_pair ? T * k : T, x, w, q, ids, workspace, workspace_bytes, true, stream);
+}
+
+size_t any4_experts_dx_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g)
+{
+    if (T <= 0 || k <= 0 || N <= 0 || T > MAX_PAIRS || k > MAX_PAIRS || !sizes_ok(T * k, T * k, E, (N + 7) / 8 * 8, K, g))
+        return 0;
+    const int64_t P = T * k;
+    return part_bytes(shape_of(P, E, true, N, K, true), P, K) + any4_lora_plan_bytes(P, E) +
+           up256(static_cast<size_t>(P) * ((N + 7) / 8 * 8) * 2);
+}
+
+any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const uint8_t* packed, const uint16_t* lut,
+                                 const uint16_t* alpha, const uint16_t* beta, const int32_t* ids, const void* plan, uint16_t* dx,
+                                 int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream)
+{
+    const int fmt = static_cast<int>(format);
+    if (!fmt_ok(fmt) || T < 0 || k < 1 || T > MAX_PAIRS || k > MAX_PAIRS || N < 1 ||
+        !sizes_ok(T * k, T * k, E, (N + 7) / 8 * 8, K, g))
+        return ANY4_E_SHAPE;
+    if (T == 0)
+        return ANY4_OK;
+    if (!dy || !packed || (fmt != FMT_INT4 && !lut) || !alpha || !beta || !ids || !dx || !workspace)
+        return ANY4_E_NULL;
+    if (!is_aligned(dy, 2) || !is_aligned(packed, 16) || !is_aligned(lut, 2) || !is_aligned(alpha, 2) || !is_aligned(beta, 2) ||
+        !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(dx, 2) || !is_aligned(workspace, 16))
+        return ANY4_E_ALIGN;
+    if (workspace_bytes < any4_experts_dx_workspace_size(T, k, E, N, K, g))
+        return ANY4_E_WORKSPACE;
+    (void)hipGetLastError();
+    const int P = static_cast<int>(T * k), Np = static_cast<int>((N + 7) / 8 * 8);
+    const Shape s = shape_of(P, E, true, N, K, true);
+    char* at = static_cast<char*>(workspace);
+    if (!plan) {
+        const any4_status st = any4_lora_plan(ids, at, any4_lora_plan_bytes(P, E), P, E, stream);
+        if (st != ANY4_OK)
+            return st;
+        plan = at;
+    }
+    at += any4_lora_plan_bytes(P, E);
+    if (N != Np || !is_aligned(dy, 16)) {
+        uint16_t* copy = reinterpret_cast<uint16_t*>(at);
+        const size_t pieces = static_cast<size_t>(P) * (Np / 8);
+        hipLaunchKernelGGL(k_pad_rows, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, dy, copy,
+                           static_cast<int>(N), Np, pieces);
+        dy = copy;
+    }
+    at += up256(static_cast<size_t>(P) * Np * 2);
+    const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
+    const Epilogue q{nullptr, nullptr, nullptr, dx, s.S > 1 ? reinterpret_cast<float*>(at) : nullptr, static_cast<int>(K),
+                     static_cast<int>(K), ACT_NONE, s.S};
+    const Rows r{nullptr, static_cast<const int*>(plan), P, static_cast<int>(E), 1};
+    launch_tile<true>(fmt, s, TileArgs{r, w, dy, q, P, Np, (Np + STEP - 1) / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
+                      stream);
+    if (s.S > 1) {
+        const size_t pieces = static_cast<size_t>(P) * (K / 8);
+        hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, q, ids, P, static_cast<int>(E), pieces);
+    }
+    return launch_status();
+}
+
+}  // extern "C"

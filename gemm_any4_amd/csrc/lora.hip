@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "frag.h"
+#include "plan.h"
 
 namespace {
 
@@ -29,45 +30,14 @@ constexpr int SMALL_M = 64;          // up to here tiles come from ballots over 
 constexpr int SMALL_M_FORWARD = 256; // and in the forward pass up to here with few adapters
 constexpr int SMALL_L_FORWARD = 8;
 constexpr int SMALL_T = 16;          // rows of a tile there
-constexpr int TILE_T = 32;           // rows of a tile of the plan
-constexpr int CHUNK = 512;           // rows of a chunk of the weight gradient
 constexpr int MAX_RANK = 128;
 constexpr int MAX_ADAPTERS = 4096;
 constexpr int64_t MAX_M = static_cast<int64_t>(1) << 20;   // tiles fit a grid's second dimension
 constexpr int64_t ACT8_MAX_M = 65535 * 64;
 
 // ---------------------------------------------------------------------------
-// the plan: rows sorted by adapter (stable), tiles and chunks of equal adapter
+// the plan (plan.h) and how it is made
 // ---------------------------------------------------------------------------
-// int32 words: [0] tiles, [1] chunks, [2] M, [3] L, then
-//   first [L+1]  first tile of each adapter (entry L: of the rows without one)
-//   count [L+1]  its rows
-//   slot  [L+1]  its first partial-sum slot (adapters of one chunk or none have
-//                no slot)
-//   chunk [CB][4]  adapter, first place, rows, slot (-1: the only chunk)
-//   tile  [TB][2]  adapter (-1: none), rows
-//   rows  [TB][TILE_T]  the rows of each tile; places behind the last repeat it
-// A place is TILE_T * tile + position: the rows of one adapter stand together, and
-// a kernel that knows its tile's number knows where they are.
-struct PlanLayout {
-    int64_t first, count, slot, chunk, tile, rows, words;
-    int64_t TB, CB;
-
-    __host__ __device__ PlanLayout(int64_t M, int64_t L)
-    {
-        const int64_t segs = M < L + 1 ? M : L + 1;
-        TB = M / TILE_T + segs;
-        CB = M / CHUNK + segs;
-        first = 4;
-        count = first + L + 1;
-        slot = count + L + 1;
-        chunk = (slot + L + 1 + 3) / 4 * 4;
-        tile = chunk + 4 * CB;
-        rows = tile + (2 * TB + 3) / 4 * 4;
-        words = rows + TILE_T * TB;
-    }
-};
-
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_WAVES = PLAN_THREADS / WAVE;
 constexpr int PLAN_ONE_M = 16384;    // up to here (and PLAN_ONE_L) one workgroup does it all

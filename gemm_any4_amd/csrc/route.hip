@@ -1,0 +1,511 @@
+// Routing to experts and the sum that the router weights, with their backward
+// passes.  The C ABI and the formulas are in include/any4.h.
+#include <type_traits>
+
+#include "frag.h"
+
+namespace {
+
+constexpr int MAX_EXPERTS = 1024;
+constexpr int MAX_K = 64;
+constexpr int MAX_GROUPS = 64;
+constexpr int64_t MAX_T = static_cast<int64_t>(1) << 20;
+
+enum { SCORE_SOFTMAX, SCORE_SIGMOID };
+
+constexpr int ROUTE_WAVES = 4;       // tokens of a workgroup, a wave each
+
+// A logit: -inf where the expert is out (-inf, NaN), +inf as the largest finite value.
+__device__ __forceinline__ float logit_at(const void* logits, int bf16, size_t i)
+{
+    const float l = bf16 ? bf16_to_f32(static_cast<const uint16_t*>(logits)[i]) : static_cast<const float*>(logits)[i];
+    return l != l ? -INFINITY : fminf(l, 3.4028234663852886e38f);
+}
+
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v)
+{
+#pragma unroll
+    for (int d = 1; d < WAVE; d <<= 1)
+        v += __shfl_xor(v, d);
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ T wave_max(T v)
+{
+#pragma unroll
+    for (int d = 1; d < WAVE; d <<= 1) {
+        const T o = __shfl_xor(v, d);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+struct RouteArgs {
+    const void* logits;
+    const float* bias;
+    float* w;
+    int* ids;
+    float scale;
+    int T, E, k, groups, top_groups, score, renorm, bf16;
+};
+
+// exp(l - top) in 64 bits; 0 for an expert that is out
+__device__ __forceinline__ double lift(float l, float top) { return l == -INFINITY ? 0.0 : exp(static_cast<double>(l) - top); }
+__device__ __forceinline__ double sigmoid64(float l) { return l == -INFINITY ? 0.0 : 1.0 / (1.0 + exp(-static_cast<double>(l))); }
+
+// A wave a token, lane l the experts l, l + 64, ...  Rank is what experts are chosen by:
+// the logit, or (SCORED) the choice value in 64 bits.
+template <int V, bool SCORED>
+__global__ __launch_bounds__(64 * ROUTE_WAVES) void k_route(const RouteArgs p)
+{
+    typedef std::conditional_t<SCORED, double, float> Rank;
+    __shared__ Rank shown[SCORED ? ROUTE_WAVES : 1][SCORED ? 64 * V : 1];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, t = blockIdx.x * ROUTE_WAVES + w;
+    if (t >= p.T)
+        return;
+    const size_t row = static_cast<size_t>(t) * p.E;
+    float l[V];
+    Rank rank[V];
+    float top = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = lane + 64 * v;
+        l[v] = e < p.E ? logit_at(p.logits, p.bf16, row + e) : -INFINITY;
+        top = fmaxf(top, l[v]);
+    }
+    top = wave_max(top);
+    double total = 0.0;              // of the softmax, where it is needed
+    if (p.score == SCORE_SOFTMAX && (SCORED || !p.renorm)) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            total += lift(l[v], top);
+        total = wave_sum(total);
+    }
+    if constexpr (SCORED) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = lane + 64 * v;
+            const double s = p.score == SCORE_SOFTMAX ? lift(l[v], top) / total : sigmoid64(l[v]);
+            const double c = p.bias && e < p.E ? s + p.bias[e] : s;
+            rank[v] = l[v] == -INFINITY || c != c ? -INFINITY : c;
+        }
+        if (p.top_groups < p.groups) {
+            const int size = p.E / p.groups;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                shown[w][lane + 64 * v] = rank[v];
+            wave_sync();
+            double score = -INFINITY;
+            if (lane < p.groups) {
+                double a = -INFINITY, b = -INFINITY;
+                for (int i = 0; i < size; ++i) {
+                    const double c = shown[w][lane * size + i];
+                    b = c > a ? a : c > b ? c : b;
+                    a = c > a ? c : a;
+                }
+                score = size > 1 ? a + b : a;
+                score = score != score ? -INFINITY : score;      // +inf beside an expert that is out
+            }
+            int before = 0;
+            for (int g = 0; g < p.groups; ++g) {
+                const double o = __shfl(score, g);
+                before += o > score || (o == score && g < lane);
+            }
+            const uint64_t kept = __ballot(lane < p.groups && before < p.top_groups);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = lane + 64 * v;
+                if (e < p.E && !(kept >> (e / size) & 1))
+                    rank[v] = -INFINITY;
+            }
+        }
+        if (!p.bias)                 // the scores' order without their rounding
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                rank[v] = rank[v] == -INFINITY ? -INFINITY : l[v];
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            rank[v] = l[v];
+    }
+    // the k of largest rank, one after another; lane j keeps the j-th
+    int mine = -1;
+    float logit = -INFINITY;
+    for (int j = 0; j < p.k; ++j) {
+        Rank best = -INFINITY;
+        float its = -INFINITY;
+        int at = MAX_EXPERTS;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (rank[v] > best) {
+                best = rank[v];
+                its = l[v];
+                at = lane + 64 * v;
+            }
+#pragma unroll
+        for (int d = 1; d < WAVE; d <<= 1) {
+            const Rank o = __shfl_xor(best, d);
+            const int o_at = __shfl_xor(at, d);
+            const float o_its = __shfl_xor(its, d);
+            const bool take = o > best || (o == best && o_at < at);
+            best = take ? o : best;
+            at = take ? o_at : at;
+            its = take ? o_its : its;
+        }
+        if (at == MAX_EXPERTS)
+            break;
+        if (lane == j) {
+            mine = at;
+            logit = its;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (lane + 64 * v == at)
+                rank[v] = -INFINITY;
+    }
+    double s;
+    if (p.score == SCORE_SIGMOID)
+        s = sigmoid64(logit);
+    else if (p.renorm)
+        s = lift(logit, wave_max(logit));     // the chosen ones' own largest: never all 0
+    else
+        s = total > 0.0 ? lift(logit, top) / total : 0.0;
+    if (p.renorm) {
+        const double sum = wave_sum(s);
+        s = sum > 0.0 ? s / sum : 0.0;
+    }
+    if (lane < p.k) {
+        p.w[static_cast<size_t>(t) * p.k + lane] = static_cast<float>(s * p.scale);
+        p.ids[static_cast<size_t>(t) * p.k + lane] = mine;
+    }
+}
+
+struct RouteBwdArgs {
+    const float* dw;
+    const void* logits;
+    const int* ids;
+    void* dlogits;
+    float scale;
+    int T, E, k, score, renorm, bf16;
+};
+
+// A wave a token.  Lane j has the j-th chosen expert and finds the derivative with
+// respect to its logit; the softmax's own sum over all experts follows where
+// the weights are not renormalised.
+template <int V>
+__global__ __launch_bounds__(64 * ROUTE_WAVES) void k_route_bwd(const RouteBwdArgs p)
+{
+    const int lane = threadIdx.x & 63, t = blockIdx.x * ROUTE_WAVES + (threadIdx.x >> 6);
+    if (t >= p.T)
+        return;
+    const size_t row = static_cast<size_t>(t) * p.E;
+    int id = -1;
+    double dw = 0.0;
+    float logit = -INFINITY;
+    if (lane < p.k) {
+        const int i = p.ids[static_cast<size_t>(t) * p.k + lane];
+        if (static_cast<uint32_t>(i) < static_cast<uint32_t>(p.E)) {
+            id = i;
+            logit = logit_at(p.logits, p.bf16, row + i);
+            dw = static_cast<double>(p.dw[static_cast<size_t>(t) * p.k + lane]) * p.scale;
+        }
+    }
+    // d l_e = f_e (own_e - c): own_e what the chosen one's weight gives
+    double own = 0.0, c = 0.0, total = 1.0;
+    float top = 0.0f;
+    const bool all = p.score == SCORE_SOFTMAX && !p.renorm;
+    float l[V];
+    if (all) {
+        top = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = lane + 64 * v;
+            l[v] = e < p.E ? logit_at(p.logits, p.bf16, row + e) : -INFINITY;
+            top = fmaxf(top, l[v]);
+        }
+        top = wave_max(top);
+        total = 0.0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            total += lift(l[v], top);
+        total = wave_sum(total);
+        const double s = total > 0.0 ? lift(logit, top) / total : 0.0;
+        own = s * dw;
+        c = wave_sum(own);
+    } else if (p.score == SCORE_SOFTMAX) {
+        const double e = lift(logit, wave_max(logit)), sum = wave_sum(e), s = sum > 0.0 ? e / sum : 0.0;
+        const double mean = wave_sum(s * dw);
+        own = s * (dw - mean);
+    } else {
+        const double s = sigmoid64(logit), rest = logit == -INFINITY ? 0.0 : 1.0 / (1.0 + exp(static_cast<double>(logit)));
+        if (p.renorm) {
+            const double sum = wave_sum(s), inv = sum > 0.0 ? 1.0 / sum : 0.0;
+            const double mean = wave_sum(s * inv * dw);
+            own = s * inv * rest * (dw - mean);
+        } else {
+            own = s * rest * dw;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = lane + 64 * v;
+        double d = 0.0;
+        for (int j = 0; j < p.k; ++j) {
+            const int at = __builtin_amdgcn_readlane(id, j);
+            const double o = __shfl(own, j);
+            d += at == e ? o : 0.0;
+        }
+        if (all)
+            d -= total > 0.0 ? lift(l[v], top) / total * c : 0.0;
+        if (e < p.E) {
+            const float f = static_cast<float>(d);
+            if (p.bf16)
+                static_cast<uint16_t*>(p.dlogits)[row + e] = static_cast<uint16_t>(f32_to_bf16(f));
+            else
+                static_cast<float*>(p.dlogits)[row + e] = f;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the weighted sum
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float half_of(const u32x4_t& v, int i) { return bf16_to_f32(v[i / 2] >> (16 * (i & 1)) & 0xffffu); }
+
+__device__ __forceinline__ u32x4_t round8(const float (&v)[8])
+{
+    u32x4_t o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = f32_to_bf16(v[2 * i]) | f32_to_bf16(v[2 * i + 1]) << 16;
+    return o;
+}
+
+struct CombineArgs {
+    const uint16_t* y;
+    const float* w;
+    const uint16_t* residual;
+    uint16_t* out;
+    int k, N, per;           // pieces of eight columns a row
+    size_t pieces;
+};
+
+// Eight columns of a token a thread, eight pairs' loads at a time; bound by its bytes.
+__global__ __launch_bounds__(256) void k_combine(const CombineArgs p)
+{
+    const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;
+    if (i >= p.pieces)
+        return;
+    const size_t t = i / p.per;
+    const int col = static_cast<int>(i % p.per) * 8, valid = p.N - col;
+    float s[8];
+    u32x4_t r = {0u, 0u, 0u, 0u};
+    if (p.residual)
+        r = load8(p.residual + t * p.N + col, valid);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        s[e] = half_of(r, e);
+    const uint16_t* y = p.y + t * p.k * p.N + col;
+    const float* w = p.w ? p.w + t * p.k : nullptr;
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+        u32x4_t v[8];
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j0 + j < p.k) {
+                v[j] = load8(y + static_cast<size_t>(j0 + j) * p.N, valid);
+                f[j] = w ? w[j0 + j] : 1.0f;
+            }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j0 + j < p.k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    s[e] = fmaf(f[j], half_of(v[j], e), s[e]);
+    }
+    store8(p.out + t * p.N + col, round8(s), valid);
+}
+
+struct CombineBwdArgs {
+    const uint16_t *dout, *y;
+    const float* w;
+    uint16_t* dy;
+    float* dw;
+    int k, N;
+};
+
+// A workgroup a token, 2048 columns a round; the sums of up to eight pairs at a time.
+__global__ __launch_bounds__(256) void k_combine_bwd(const CombineBwdArgs p)
+{
+    __shared__ float red[4][8];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const size_t t = blockIdx.x;
+    const uint16_t* dout = p.dout + t * p.N;
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+        float sum[8], f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sum[j] = 0.0f;
+            f[j] = j0 + j < p.k ? p.w[t * p.k + j0 + j] : 0.0f;
+        }
+        for (int col = threadIdx.x * 8; col < p.N; col += 2048) {
+            const int valid = p.N - col;
+            const u32x4_t d = load8(dout + col, valid);
+            u32x4_t v[8];
+            if (p.dw)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j0 + j < p.k)
+                        v[j] = load8(p.y + (t * p.k + j0 + j) * p.N + col, valid);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j0 + j >= p.k)
+                    break;
+                if (p.dw)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        sum[j] = fmaf(half_of(d, e), half_of(v[j], e), sum[j]);
+                if (p.dy) {
+                    float o[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        o[e] = f[j] * half_of(d, e);
+                    store8(p.dy + (t * p.k + j0 + j) * p.N + col, round8(o), valid);
+                }
+            }
+        }
+        if (!p.dw)
+            continue;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float s = wave_sum(sum[j]);
+            if (lane == 0)
+                red[wave][j] = s;
+        }
+        __syncthreads();
+        if (threadIdx.x < 8 && j0 + static_cast<int>(threadIdx.x) < p.k)
+            p.dw[t * p.k + j0 + threadIdx.x] = red[0][threadIdx.x] + red[1][threadIdx.x] + red[2][threadIdx.x] + red[3][threadIdx.x];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+constexpr int64_t GIB1 = static_cast<int64_t>(1) << 30;
+
+bool route_ok(int64_t T, int64_t E, int64_t k, int score)
+{
+    return T >= 0 && T <= MAX_T && E >= 1 && E <= MAX_EXPERTS && k >= 1 && k <= MAX_K && k <= E && T * k <= MAX_T &&
+           (score == SCORE_SOFTMAX || score == SCORE_SIGMOID);
+}
+
+bool combine_ok(int64_t T, int64_t k, int64_t N)
+{
+    return T >= 0 && T <= MAX_T && k >= 1 && k <= MAX_T && T * k <= MAX_T && N >= 0 && N < GIB1 && (T == 0 || N < GIB1 / (T * k));
+}
+
+template <bool SCORED>
+void launch_route(const RouteArgs& a, hipStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>((a.T + ROUTE_WAVES - 1) / ROUTE_WAVES)), block(64 * ROUTE_WAVES);
+#define ROUTE(V_) hipLaunchKernelGGL((k_route<V_, SCORED>), grid, block, 0, stream, a)
+    if (a.E <= 64) ROUTE(1);
+    else if (a.E <= 128) ROUTE(2);
+    else if (a.E <= 256) ROUTE(4);
+    else if (a.E <= 512) ROUTE(8);
+    else ROUTE(16);
+#undef ROUTE
+}
+
+}  // namespace
+
+extern "C" {
+
+any4_status any4_route(const void* logits, int logits_bf16, const float* bias, float* w, int32_t* ids, any4_score score, int renorm,
+                       float scale, int64_t T, int64_t E, int64_t k, int64_t groups, int64_t top_groups, hipStream_t stream)
+{
+    if (!route_ok(T, E, k, score) || groups < 1 || groups > MAX_GROUPS || E % groups || top_groups < 1 || top_groups > groups ||
+        k > top_groups * (E / groups))
+        return ANY4_E_SHAPE;
+    if (T == 0)
+        return ANY4_OK;
+    if (!logits || !w || !ids)
+        return ANY4_E_NULL;
+    if (!is_aligned(logits, logits_bf16 ? 2 : 4) || !is_aligned(bias, 4) || !is_aligned(w, 4) || !is_aligned(ids, 4))
+        return ANY4_E_ALIGN;
+    (void)hipGetLastError();
+    const RouteArgs a{logits, bias, w, ids, scale, static_cast<int>(T), static_cast<int>(E), static_cast<int>(k), static_cast<int>(groups),
+                      static_cast<int>(top_groups), static_cast<int>(score), renorm != 0, logits_bf16 != 0};
+    if (bias || top_groups < groups)
+        launch_route<true>(a, stream);
+    else
+        launch_route<false>(a, stream);
+    return launch_status();
+}
+
+any4_status any4_route_backward(const float* dw, const void* logits, int logits_bf16, const int32_t* ids, void* dlogits, any4_score score,
+                                int renorm, float scale, int64_t T, int64_t E, int64_t k, hipStream_t stream)
+{
+    if (!route_ok(T, E, k, score))
+        return ANY4_E_SHAPE;
+    if (T == 0)
+        return ANY4_OK;
+    if (!dw || !logits || !ids || !dlogits)
+        return ANY4_E_NULL;
+    const size_t size = logits_bf16 ? 2 : 4;
+    if (!is_aligned(dw, 4) || !is_aligned(logits, size) || !is_aligned(ids, 4) || !is_aligned(dlogits, size))
+        return ANY4_E_ALIGN;
+    (void)hipGetLastError();
+    const RouteBwdArgs a{dw, logits, ids, dlogits, scale, static_cast<int>(T), static_cast<int>(E), static_cast<int>(k),
+                         static_cast<int>(score), renorm != 0, logits_bf16 != 0};
+    const dim3 grid(static_cast<unsigned>((T + ROUTE_WAVES - 1) / ROUTE_WAVES)), block(64 * ROUTE_WAVES);
+#define ROUTE(V_) hipLaunchKernelGGL((k_route_bwd<V_>), grid, block, 0, stream, a)
+    if (E <= 64) ROUTE(1);
+    else if (E <= 128) ROUTE(2);
+    else if (E <= 256) ROUTE(4);
+    else if (E <= 512) ROUTE(8);
+    else ROUTE(16);
+#undef ROUTE
+    return launch_status();
+}
+
+any4_status any4_combine(const uint16_t* y, const float* w, const uint16_t* residual, uint16_t* out, int64_t T, int64_t k, int64_t N,
+                         hipStream_t stream)
+{
+    if (!combine_ok(T, k, N))
+        return ANY4_E_SHAPE;
+    if (T == 0 || N == 0)
+        return ANY4_OK;
+    if (!y || !out)
+        return ANY4_E_NULL;
+    if (!is_aligned(y, 2) || !is_aligned(w, 4) || !is_aligned(residual, 2) || !is_aligned(out, 2))
+        return ANY4_E_ALIGN;
+    (void)hipGetLastError();
+    const int per = static_cast<int>((N + 7) / 8);
+    const size_t pieces = static_cast<size_t>(T) * per;
+    hipLaunchKernelGGL(k_combine, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream,
+                       CombineArgs{y, w, residual, out, static_cast<int>(k), static_cast<int>(N), per, pieces});
+    return launch_status();
+}
+
+any4_status any4_combine_backward(const uint16_t* dout, const uint16_t* y, const float* w, uint16_t* dy, float* dw, int64_t T, int64_t k,
+                                  int64_t N, hipStream_t stream)
+{
+    if (!combine_ok(T, k, N))
+        return ANY4_E_SHAPE;
+    if (T == 0 || (!dy && !dw) || (N == 0 && !dw))
+        return ANY4_OK;
+    if (!w || (N > 0 && (!dout || (dw && !y))))
+        return ANY4_E_NULL;
+    if (!is_aligned(dout, 2) || !is_aligned(y, 2) || !is_aligned(w, 4) || !is_aligned(dy, 2) || !is_aligned(dw, 4))
+        return ANY4_E_ALIGN;
+    (void)hipGetLastError();
+    hipLaunchKernelGGL(k_combine_bwd, dim3(static_cast<unsigned>(T)), dim3(256), 0, stream,
+                       CombineBwdArgs{dout, y, w, dy, dw, static_cast<int>(k), static_cast<int>(N)});
+    return launch_status();
+}
+
+}  // extern "C"

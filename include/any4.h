@@ -503,6 +503,185 @@ any4_status any3_gemm_dx(const uint16_t* dy, const uint8_t* packed, const uint16
                          hipStream_t stream);
 
 /*
+ * The feed-forward block around a quantised layer, dense or of many experts:
+ * bias, activation, gate and residual in the product's epilogue, a router, the
+ * experts' products and the sum that the router weights.
+ */
+typedef enum any4_format {
+    ANY4_FORMAT_ANY4 = 0, /* any4_pack, lut of 16 entries              */
+    ANY4_FORMAT_INT4 = 1, /* any4_pack, plain codes 0..15, lut not read */
+    ANY4_FORMAT_ANY2 = 2, /* any2_pack, lut entries 0..3               */
+    ANY4_FORMAT_ANY3 = 3  /* any3_pack, lut entries 0..7               */
+} any4_format;
+
+typedef enum any4_activation {
+    ANY4_ACT_NONE = 0,     /* z                                              */
+    ANY4_ACT_RELU = 1,     /* max(z, 0)                                      */
+    ANY4_ACT_SILU = 2,     /* z / (1 + e^-z)                                 */
+    ANY4_ACT_GELU = 3,     /* z (1 + erf(z / sqrt 2)) / 2                    */
+    ANY4_ACT_GELU_TANH = 4 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+} any4_activation;
+
+/*
+ * any4_gemm_act -- a layer's product with what surrounds it:
+ *     zf[m][n] = sum_k x[m][k] w[n][k] + bias[n]          (fp32, w the any4_dequant values)
+ *     out[m][n] = bf16_rne( act(zf[m][n]) + residual[m][n] )
+ * or with gate != 0, the layer's N rows being [gate; up] of N/2 each:
+ *     out[m][n] = bf16_rne( act(zf[m][n]) * zf[m][N/2 + n] + residual[m][n] ),  n < N/2
+ * The weights are exactly the any4_dequant values, products are exact and sums
+ * fp32, nothing is rounded in between.  z, where asked for, is bf16_rne(zf): what
+ * any4_act_backward needs.  Non-finite z give what the formulas give (act(-inf)
+ * may be NaN).  Deterministic; a row's result depends on no other row's values.
+ *   x         device, [M][K] bf16      bias  device, [N] bf16, or NULL
+ *   residual  device, [M][No] bf16, or NULL; may be out itself (No = N, gated N/2)
+ *   z         device, [M][N] bf16, written; or NULL
+ *   out       device, [M][No] bf16, written
+ *   packed, lut, alpha, beta  as for the format's dequantisation.
+ *   0 <= M <= 2^20, N >= 0 (even with a gate), K a positive multiple of 128, g as for
+ *   any4_gemm (K/g is not limited); M*N and M*K below 2^30, N*K below 2^32.
+ *   M*N == 0 is a no-op.
+ *   workspace  device, 16-byte aligned, any4_gemm_act_workspace_size(M, N, K, g)
+ *          bytes, required where that is not 0; contents need not be
+ *          initialised; calls that share one must be ordered.
+ *   x, packed and workspace need 16-byte alignment, the others 2.
+ * Errors: ANY4_E_SHAPE (also an unknown format or activation), ANY4_E_NULL,
+ * ANY4_E_ALIGN, ANY4_E_WORKSPACE, ANY4_E_HIP.
+ */
+size_t any4_gemm_act_workspace_size(int64_t M, int64_t N, int64_t K, int64_t g);
+any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* packed, const uint16_t* lut,
+                          const uint16_t* alpha, const uint16_t* beta, const uint16_t* bias,
+                          const uint16_t* residual, uint16_t* z, uint16_t* out, any4_activation act,
+                          int gate, int64_t M, int64_t N, int64_t K, int64_t g, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * any4_act_backward -- the gradients of an epilogue for dy = d loss / d out,
+ * from z as any4_gemm_act or any4_experts_gemm kept it:
+ *     dz[m][n] = bf16_rne( dy[m][n] act'(z[m][n]) ), or with a gate
+ *     dz[m][n] = bf16_rne( dy[m][n] z[m][N/2 + n] act'(z[m][n]) ),
+ *     dz[m][N/2 + n] = bf16_rne( dy[m][n] act(z[m][n]) ),      n < N/2
+ *     dbias[n] = sum_m of the same values before their rounding     (fp32)
+ * act' of ANY4_ACT_RELU is 0 at 0.  The gradient of x is any4_gemm_dx of dz, that of the
+ * residual dy itself.
+ *   dy  device, [M][No] bf16    z, dz  device, [M][N] bf16 (dz may be z itself)
+ *   dbias  device, [N] fp32, or NULL (workspace is then not used)
+ *   0 <= M <= 2^20, N >= 0, M*N below 2^30.  M = 0 writes dbias = 0.
+ *   workspace  device, 16-byte aligned, any4_act_backward_workspace_size(M, N, gate)
+ *          bytes, with dbias.
+ *   dy, z and dz need 2-byte alignment, dbias 4.
+ * Errors: as any4_gemm_act.
+ */
+size_t any4_act_backward_workspace_size(int64_t M, int64_t N, int gate);
+any4_status any4_act_backward(const uint16_t* dy, const uint16_t* z, uint16_t* dz, float* dbias,
+                              any4_activation act, int gate, int64_t M, int64_t N, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * any4_route -- the experts of each token and their weights, from the router's
+ * logits:
+ *     s[t] = softmax(logits[t]) or sigmoid(logits[t])
+ *     c[t] = s[t] + bias                        (a bias for balance: it chooses, it does not weight)
+ *     of `groups` groups of E / groups experts, the top_groups stay whose two
+ *     largest c have the largest sum (one-expert groups: whose c is largest; an
+ *     expert that is out counts as -inf, a sum without a value too)
+ *     ids[t] = the k experts of largest c among those that stay, largest first
+ *     w[t][j] = scale * s[t][ids[t][j]], with renorm != 0 divided by the sum of the k
+ * Experts are compared by c in 64 bits, without a bias by the logits themselves (the same
+ * order); ties go to the lowest index.  An expert whose logit is -inf or NaN, or whose c is
+ * NaN or -inf, is never chosen and has a score of 0; where fewer than k are left, the
+ * remaining ids are -1 with weights of 0.  A logit of +inf counts as the largest
+ * finite fp32 value.  With renorm, weights whose scores are all 0 are 0.
+ *   logits  device, [T][E], fp32 or (logits_bf16 != 0) bf16
+ *   bias    device, [E] fp32, or NULL
+ *   w       device, [T][k] fp32, written       ids  device, [T][k] int32, written
+ *   0 <= T <= 2^20, 1 <= E <= 1024, 1 <= k <= 64, groups in 1..64 that divide E,
+ *   1 <= top_groups <= groups, k <= top_groups * E / groups, T*k <= 2^20.  T = 0 is a no-op.
+ *   Alignment: that of the elements.
+ * Errors: ANY4_E_SHAPE (also an unknown score), ANY4_E_NULL, ANY4_E_ALIGN, ANY4_E_HIP.
+ */
+typedef enum any4_score { ANY4_SCORE_SOFTMAX = 0, ANY4_SCORE_SIGMOID = 1 } any4_score;
+any4_status any4_route(const void* logits, int logits_bf16, const float* bias, float* w, int32_t* ids,
+                       any4_score score, int renorm, float scale, int64_t T, int64_t E, int64_t k,
+                       int64_t groups, int64_t top_groups, hipStream_t stream);
+
+/*
+ * any4_route_backward -- dlogits (of the logits' type) from dw = d loss / d w, the
+ * choice being constant: the derivative of w[t][j] above.  ids as any4_route
+ * wrote them (outside 0..E-1: no expert; dw there is not used).
+ *   dw  device, [T][k] fp32    dlogits  device, [T][E], written whole
+ * Sizes and errors as any4_route.
+ */
+any4_status any4_route_backward(const float* dw, const void* logits, int logits_bf16, const int32_t* ids,
+                                void* dlogits, any4_score score, int renorm, float scale, int64_t T,
+                                int64_t E, int64_t k, hipStream_t stream);
+
+/*
+ * any4_experts_gemm -- any4_gemm_act through stacked layers: pair p = t*k + j goes
+ * through expert e = ids[t][j],
+ *     zf[p] = W_e x[per_pair ? p : t] + bias[e],   out[p] = bf16_rne( act(zf[p]) ) or gated
+ * A pair whose id is not in 0..E-1 gives zeros (out and z).
+ *   x       device, [T][K] bf16, or with per_pair != 0 [T*k][K]
+ *   packed  device, the experts' packed layers one after another (each of
+ *           any4_packed_bytes(N, K), or the format's)
+ *   lut [E][N][16], alpha, beta [E][N][K/g], bias [E][N] bf16 (or NULL)
+ *   ids     device, [T][k] int32
+ *   plan    device, any4_lora_plan(ids, ..., T*k, E), which a program makes once for the
+ *           products of a block; or NULL (made in the workspace; up to 64 pairs
+ *           need none and ignore it).  A plan that any4_lora_plan made for other sizes
+ *           leaves the outputs unwritten.
+ *   z       device, [T*k][N] bf16, written; or NULL      out  device, [T*k][No] bf16, written
+ *   0 <= T*k <= 2^20, 1 <= E <= 1024, the other sizes as any4_gemm_act for M = T*k; the
+ *   stacked arrays may be of any size.  T = 0 and N = 0 are no-ops.
+ *   workspace  as for any4_gemm_act, any4_experts_workspace_size(T, k, E, N, K, g) bytes
+ *          (where the call makes its own plan or splits K).
+ *   x, packed, plan and workspace need 16-byte alignment, ids 4, the others 2.
+ * Errors: as any4_gemm_act.
+ */
+size_t any4_experts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g);
+any4_status any4_experts_gemm(any4_format format, const uint16_t* x, int per_pair, const uint8_t* packed,
+                              const uint16_t* lut, const uint16_t* alpha, const uint16_t* beta,
+                              const uint16_t* bias, const int32_t* ids, const void* plan, uint16_t* z,
+                              uint16_t* out, any4_activation act, int gate, int64_t T, int64_t k,
+                              int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * any4_experts_gemm_dx -- the gradient of the rows that went through the experts:
+ *     dx[p][k] = bf16_rne( sum_n dy[p][n] w_e[n][k] ),   e = ids[p]
+ * A pair whose id is not in 0..E-1 gives zeros.  (The gradient of an x that k
+ * pairs share is the sum of theirs: any4_combine without weights.)
+ *   dy  device, [T*k][N] bf16 (read in place if 16-byte aligned and N % 8 == 0, else
+ *       through a padded copy)      dx  device, [T*k][K] bf16, written
+ *   N >= 1; sizes, ids, plan and errors as any4_experts_gemm (here N is taken
+ *   rounded up to a multiple of 8).
+ *   workspace  device, any4_experts_dx_workspace_size(T, k, E, N, K, g) bytes, required.
+ */
+size_t any4_experts_dx_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g);
+any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const uint8_t* packed,
+                                 const uint16_t* lut, const uint16_t* alpha, const uint16_t* beta,
+                                 const int32_t* ids, const void* plan, uint16_t* dx, int64_t T, int64_t k,
+                                 int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * any4_combine, any4_combine_backward -- the experts' outputs as the router
+ * weights them, and the gradients:
+ *     out[t]   = bf16_rne( residual[t] + sum_j w[t][j] y[t][j] )
+ *     dy[t][j] = bf16_rne( w[t][j] dout[t] ),   dw[t][j] = sum_n dout[t][n] y[t][j][n]
+ * Sums are fp32, in the order of j.
+ *   y, dy  device, [T][k][N] bf16       w, dw  device, [T][k] fp32 (w NULL in any4_combine:
+ *   weights of 1)     residual  device, [T][N] bf16, or NULL; may be out itself
+ *   out, dout  device, [T][N] bf16.   dy or dw NULL: not wanted.  dy may be y itself.
+ *   0 <= T <= 2^20, k >= 1, T*k <= 2^20, N >= 0, T*k*N below 2^30.  T*N == 0 is a no-op
+ *   (with N = 0 dw gets zeros).  Alignment: that of the elements.
+ * Errors: ANY4_E_SHAPE, ANY4_E_NULL, ANY4_E_ALIGN, ANY4_E_HIP.
+ */
+any4_status any4_combine(const uint16_t* y, const float* w, const uint16_t* residual, uint16_t* out,
+                         int64_t T, int64_t k, int64_t N, hipStream_t stream);
+any4_status any4_combine_backward(const uint16_t* dout, const uint16_t* y, const float* w, uint16_t* dy,
+                                  float* dw, int64_t T, int64_t k, int64_t N, hipStream_t stream);
+
+/*
  * any4_read_probe -- a measurement aid, not part of the method: reads `bytes`
  * of device memory at `buf` once, with the GEMM kernels' loads (16 bytes per
  * lane, 1 KB per wave, non-temporal), one workgroup of 16 waves per CU, each
