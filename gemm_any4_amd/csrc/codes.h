@@ -58,6 +58,7 @@ struct ByteTable {
     static constexpr int ENTRIES = FMT == FMT_ANY2 ? 4 : FMT == FMT_ANY3 ? 8 : 16;
     uint32_t lo[ENTRIES / 4], hi[ENTRIES / 4];
 
+    ByteTable() = default;
     __device__ __forceinline__ explicit ByteTable(const RowTable& r)
     {
         const float a = bf16_to_f32(r.alpha), b = bf16_to_f32(r.beta);
@@ -122,6 +123,61 @@ __device__ __forceinline__ void decode(const ByteTable<FMT>& t, const uint32_t (
         }
         t.find(even, out[4 * i], out[4 * i + 1]);
         t.find(odd, out[4 * i + 2], out[4 * i + 3]);
+    }
+}
+
+// The same weights in order, eight at a time: out holds (8i, 8i + 1) .. (8i + 6, 8i + 7).
+// The codes' bytes are laid out in pairs before the lookup, and which half of a
+// 16-entry table a code is in comes from its top bit by v_perm's selectors 8 .. 11 (the
+// sign of every other byte as a whole byte): 26 instructions for eight weights (27
+// above, not in order).
+template <int FMT>
+__device__ __forceinline__ void decode8(const ByteTable<FMT>& t, const uint32_t (&code)[4], int i, uint32_t (&out)[4])
+{
+    if constexpr (FMT == FMT_ANY2) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {            // k % 4 below 2, and the others
+            const uint32_t w = code[i / 2] >> (4 * j), even = w & 0x03030303u, odd = w >> 2 & 0x03030303u;
+            const uint32_t s = __builtin_amdgcn_perm(odd, even, i % 2 ? 0x07030602u : 0x05010400u);
+            const uint32_t l = __builtin_amdgcn_perm(0u, t.lo[0], s), h = __builtin_amdgcn_perm(0u, t.hi[0], s);
+            out[j] = __builtin_amdgcn_perm(h, l, 0x05010400u);
+            out[2 + j] = __builtin_amdgcn_perm(h, l, 0x07030602u);
+        }
+    } else if constexpr (FMT == FMT_ANY3) {
+        const uint32_t w = i < 3 ? code[i < 3 ? i : 0]
+                                 : (code[0] >> 6 & 0x03030303u) | (code[1] >> 4 & 0x0c0c0c0cu) | (code[2] >> 2 & 0x30303030u);
+        const uint32_t even = w & 0x07070707u, odd = w >> 3 & 0x07070707u;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t s = __builtin_amdgcn_perm(odd, even, j ? 0x07030602u : 0x05010400u);
+            const uint32_t l = __builtin_amdgcn_perm(t.lo[1], t.lo[0], s), h = __builtin_amdgcn_perm(t.hi[1], t.hi[0], s);
+            out[2 * j] = __builtin_amdgcn_perm(h, l, 0x05010400u);
+            out[2 * j + 1] = __builtin_amdgcn_perm(h, l, 0x07030602u);
+        }
+    } else {
+        const uint32_t w = code[i], even = w & 0x07070707u, odd = w >> 4 & 0x07070707u;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {            // codes (0, 1, 4, 5), (2, 3, 6, 7)
+            const uint32_t s = __builtin_amdgcn_perm(odd, even, j ? 0x07030501u : 0x06020400u);
+            const uint32_t upper = j ? __builtin_amdgcn_perm(w, w << 4, 0x0b090a08u) : __builtin_amdgcn_perm(w << 8, w << 12, 0x0b090a08u);
+            const uint32_t l = (__builtin_amdgcn_perm(t.lo[1], t.lo[0], s) & ~upper) | (__builtin_amdgcn_perm(t.lo[3], t.lo[2], s) & upper);
+            const uint32_t h = (__builtin_amdgcn_perm(t.hi[1], t.hi[0], s) & ~upper) | (__builtin_amdgcn_perm(t.hi[3], t.hi[2], s) & upper);
+            out[j] = __builtin_amdgcn_perm(h, l, 0x05010400u);
+            out[2 + j] = __builtin_amdgcn_perm(h, l, 0x07030602u);
+        }
+    }
+}
+
+template <int FMT>
+__device__ __forceinline__ void decode_in_order(const ByteTable<FMT>& t, const uint32_t (&code)[4], uint32_t (&out)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t v[4];
+        decode8(t, code, i, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            out[4 * i + j] = v[j];
     }
 }
 

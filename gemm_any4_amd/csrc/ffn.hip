@@ -222,6 +222,10 @@ __device__ __forceinline__ void finish8(const Epilogue& q, int e, int p, int col
     store8(q.out + at, round8(o), valid);
 }
 
+// Where part i of n starts among `all` (below 2^24, n at most 64); the same for all
+// lanes, which the compiler does not see of a division.
+__device__ __forceinline__ int share(int all, int i, int n) { return __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(all) * i / n)); }
+
 // ---------------------------------------------------------------------------
 // few rows: packed weights read once, decoded in registers
 // ---------------------------------------------------------------------------
@@ -252,44 +256,59 @@ __device__ __forceinline__ f32x4_t mfma4(s16x4_t a, s16x4_t b, f32x4_t c)
     return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(a, b, c, 4, ABID, 0);
 }
 
+// A row's next 128 weights and their scales.
+template <int FMT>
+struct RowChunk {
+    uint32_t code[4][4], alpha, beta;
+
+    __device__ __forceinline__ void fetch(const uint8_t* packed, const uint16_t* a, const uint16_t* b, int row, int Kc, int chunk, int g)
+    {
+        const size_t grp = static_cast<size_t>(row) * (Kc * 128 / g) + chunk * 128 / g;
+        alpha = a[grp];
+        beta = b[grp];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            fetch_codes<FMT>(packed, row, Kc, chunk, q, code[q]);
+    }
+};
+
 // The product of 4 * NB rows of x with the lane's row of W over chunks s0 .. s1.
 template <int FMT, int NB>
 __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, const int* own, int count, int s0, int s1,
                                             f32x4_t (&acc)[4])
 {
+    if (s0 >= s1)
+        return;
     const int lane = threadIdx.x & 63, Kc = p.w.K / 128;
     const uint8_t* packed = p.w.codes(e);
-    const uint16_t* lut = FMT == FMT_INT4 ? nullptr : p.w.table(e);
     const uint16_t *alpha = p.w.alpha + p.w.scales(e), *beta = p.w.beta + p.w.scales(e);
-    const uint16_t* x[NB];           // 8 k of a row: the lane uses the even or the odd ones
+    const uint16_t* x[NB];           // the lane's four k of a row, of each 64
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const int i = 4 * b + (lane & 3);
-        x[b] = p.x + static_cast<size_t>(own[i < count ? i : count - 1] / p.r.div) * p.w.K + 8 * (lane >> 3);
+        x[b] = p.x + static_cast<size_t>(own[i < count ? i : count - 1] / p.r.div) * p.w.K + 4 * (lane >> 2);
     }
-    const uint32_t pick = lane & 4 ? 0x07060302u : 0x05040100u;
+    RowChunk<FMT> next;
+    next.fetch(packed, alpha, beta, wr, Kc, s0, p.w.g);
+    RowTable row = fetch_table<FMT>(FMT == FMT_INT4 ? nullptr : p.w.table(e), alpha, beta, wr, Kc, s0, p.w.g);
     for (int s = s0; s < s1; ++s) {
-        uint32_t code[4][4];
-        const RowTable row = fetch_table<FMT>(lut, alpha, beta, wr, Kc, s, p.w.g);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            fetch_codes<FMT>(packed, wr, Kc, s, q, code[q]);
         s16x4_t a[NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x[b] + s * 128 + 64 * j);
-                u32x2_t o;
-                o[0] = __builtin_amdgcn_perm(v[1], v[0], pick);
-                o[1] = __builtin_amdgcn_perm(v[3], v[2], pick);
-                a[b][j] = __builtin_bit_cast(s16x4_t, o);
-            }
+            for (int j = 0; j < 2; ++j)
+                a[b][j] = *reinterpret_cast<const s16x4_t*>(x[b] + s * 128 + 64 * j);
+        const RowChunk<FMT> now = next;
+        if (s + 1 < s1)
+            next.fetch(packed, alpha, beta, wr, Kc, s + 1, p.w.g);
+        __builtin_amdgcn_sched_barrier(0);      // asked for here, not where they are used
+        row.alpha = now.alpha;
+        row.beta = now.beta;
         const ByteTable<FMT> t(row);
         static_for<0, 4>([&](auto q_) __attribute__((always_inline)) {
             constexpr int q = decltype(q_)::value;
-            uint32_t v[16];          // of each eight k (0, 2), (4, 6), (1, 3), (5, 7)
-            decode(t, code[q], v);
+            uint32_t v[16];
+            decode_in_order(t, now.code[q], v);
             static_for<0, 8>([&](auto i_) __attribute__((always_inline)) {
                 constexpr int i = decltype(i_)::value;
                 const u32x2_t w = {v[2 * i], v[2 * i + 1]};
@@ -329,8 +348,7 @@ __global__ __launch_bounds__(FEW_THREADS) void k_few(const FewArgs p)
         return;
     }
     const int Kc = p.w.K / 128, parts = p.q.S * FEW_WAVES, at = blockIdx.z * FEW_WAVES + w;
-    const int s0 = static_cast<int>(static_cast<int64_t>(Kc) * at / parts);
-    const int s1 = static_cast<int>(static_cast<int64_t>(Kc) * (at + 1) / parts);
+    const int s0 = share(Kc, at, parts), s1 = share(Kc, at + 1, parts);
     f32x4_t acc[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b)
@@ -470,17 +488,6 @@ __device__ __forceinline__ int column_of(int place) { return 16 * (place >> 2 & 
 // Rows of 64 values in LDS, eight pieces of 16 bytes; piece q stands at q ^ key(row):
 // 16 rows of an operand read, and 16 rows that lanes write, touch all 64 banks once.
 __device__ __forceinline__ int key(int row) { return row >> 1 & 7; }
-// rows 2 and 3 of each four exchanged, so that rows r and r + 2 lie in other banks
-template <bool TURN>
-__device__ __forceinline__ int row_at(int row) { return TURN ? row ^ (row >> 1 & 1) : row; }
-
-// The weights of eight k in order from decode()'s (0, 2), (4, 6), (1, 3), (5, 7).
-__device__ __forceinline__ u32x4_t in_order(const uint32_t* v)
-{
-    return u32x4_t{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
-                   __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
-}
-
 __device__ __forceinline__ void put8(float* to, f32x4_t a, f32x4_t b, int valid)
 {
     if (valid >= 8) {
@@ -497,31 +504,95 @@ __device__ __forceinline__ void put8(float* to, f32x4_t a, f32x4_t b, int valid)
     }
 }
 
+constexpr int slot_bytes(int fmt) { return fmt == FMT_ANY2 ? 8 : fmt == FMT_ANY3 ? 12 : 16; }    // of 32 codes
+
+template <int FMT>
+__device__ __forceinline__ void load_slot(__amdgpu_buffer_rsrc_t codes, int at, int from, uint32_t (&c)[4])
+{
+    c[0] = c[1] = c[2] = c[3] = 0u;
+    if constexpr (FMT == FMT_ANY2) {
+        const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(codes, at, from, 0);
+        c[0] = v[0];
+        c[1] = v[1];
+    } else if constexpr (FMT == FMT_ANY3) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b96(codes, at, from, 0);
+        c[0] = v[0];
+        c[1] = v[1];
+        c[2] = v[2];
+    } else {
+        const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(codes, at, from, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c[i] = v[i];
+    }
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, size_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), static_cast<int>(bytes), 0x00020000);
+}
+
+// A chunk of 128 k of a row, of which a thread decodes a quarter a step, by buffer
+// loads: the row's place is the lane's offset, the chunk's the wave's.
+struct RowPart {
+    uint32_t code[2][4], alpha, beta;
+};
+
+template <int FMT>
+struct RowReader {
+    static constexpr int BYTES = slot_bytes(FMT), LOADS = 4;
+    __amdgpu_buffer_rsrc_t codes, alpha, beta;
+    int at, scale_at, g;
+
+    __device__ __forceinline__ RowReader(const Layer& w, int e, int row, int h) : g(w.g)
+    {
+        const size_t scales = static_cast<size_t>(w.N) * (w.K / w.g) * 2;
+        codes = buffer_of(w.codes(e), w.packed_bytes);
+        alpha = buffer_of(w.alpha + w.scales(e), scales);
+        beta = buffer_of(w.beta + w.scales(e), scales);
+        at = (row / 16 * (w.K / 128) * 64 + 16 * h + row % 16) * BYTES;
+        scale_at = row * (w.K / w.g) * 2;
+    }
+    // LOADS instructions
+    __device__ __forceinline__ void fetch(RowPart& c, int chunk) const
+    {
+        const int from = chunk * 64 * BYTES, scale = chunk * 128 / g * 2;
+        load_slot<FMT>(codes, at, from, c.code[0]);
+        load_slot<FMT>(codes, at + 32 * BYTES, from, c.code[1]);
+        c.alpha = __builtin_amdgcn_raw_buffer_load_b16(alpha, scale_at, scale, 0);
+        c.beta = __builtin_amdgcn_raw_buffer_load_b16(beta, scale_at, scale, 0);
+    }
+};
+
+constexpr int parts_of(int blocks) { return blocks >= 2 ? 4 : 2; }
+
 // 2 x WN waves of RM x 4 blocks of 16 x 16.  TURN: the sum runs over the rows of W
 // and the results are its columns (the input's gradient).
 template <int FMT, int WN, int RM, bool TURN>
 __global__ __launch_bounds__(128 * WN) void k_tile(const TileArgs p)
 {
-    constexpr int BM = 32 * RM, BN = WN * 64, WAVES = 2 * WN, LA = BM / 8 / WAVES;
+    constexpr int THREADS = 128 * WN, BM = 32 * RM, BN = WN * 64, WAVES = 2 * WN, LA = BM / 8 / WAVES;
     static_assert(LA >= 1, "every wave loads rows of x");
     __shared__ __attribute__((aligned(16))) uint16_t sa0[BM * STEP], sb0[BN * STEP], sa1[BM * STEP], sb1[BN * STEP];
     __shared__ int pairs[BM];
+    // forward: the tables of the rows at the places; TURN: byte tables of the next steps' rows
+    __shared__ u32x4_t tables[TURN || FMT == FMT_INT4 ? 1 : BN][FMT == FMT_ANY4 ? 2 : 1];
+    __shared__ uint32_t turned[TURN ? 2 : 1][TURN ? BN / 128 : 1][TURN ? 2 * ByteTable<FMT>::ENTRIES / 4 : 1][STEP];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
-    const int tiles = p.tiles_m * p.tiles_n;
-    // workgroups go to the eight XCDs in turn: each XCD gets a run of tiles, four
-    // rows of tiles high, whose operands its L2 then shares
-    int id = blockIdx.x;
-    if (tiles % 8 == 0)
-        id = id % 8 * (tiles / 8) + id / 8;
-    constexpr int HIGH = 4;
+    // Workgroups go to the eight XCDs in turn: each XCD gets a run of tiles whose
+    // operands its L2 then shares, four rows of tiles high, or with experts all rows (some
+    // of the last have no rows of x: every XCD gets its share of them).
+    const int id = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8, HIGH = p.r.plan ? p.tiles_m : 4;
+    if (id >= p.tiles_m * p.tiles_n)
+        return;
     const int band = id / (HIGH * p.tiles_n), high = p.tiles_m - band * HIGH < HIGH ? p.tiles_m - band * HIGH : HIGH;
     const int in_band = id - band * HIGH * p.tiles_n;
-    const int tm = band * HIGH + in_band % high, tn = in_band / high;
+    const int tm = __builtin_amdgcn_readfirstlane(band * HIGH + in_band % high), tn = __builtin_amdgcn_readfirstlane(in_band / high);
     int64_t first = 0;
     const Tile t = find_tile(p.r, tm, BM, first);
     if (t.e < 0)
         return;
-    for (int i = tid; i < BM; i += 128 * WN)
+    for (int i = tid; i < BM; i += THREADS)
         pairs[i] = i >= t.count ? -1 : p.r.plan ? p.r.plan[first + i] : tm * BM + i;
     __syncthreads();
     const bool gate = p.q.gated();
@@ -541,8 +612,6 @@ __global__ __launch_bounds__(128 * WN) void k_tile(const TileArgs p)
                     }
         return;
     }
-    const int s0 = static_cast<int>(static_cast<int64_t>(p.steps) * blockIdx.y / p.q.S);
-    const int s1 = static_cast<int>(static_cast<int64_t>(p.steps) * (blockIdx.y + 1) / p.q.S);
 
     // x: a wave's load instruction fills 8 rows of a tile; lane: row lane / 8, place lane % 8
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
@@ -560,133 +629,292 @@ __global__ __launch_bounds__(128 * WN) void k_tile(const TileArgs p)
         for (int i = 0; i < LA; ++i)
             load_lds(ra, sa + (w * LA + i) * 8 * STEP, static_cast<int>(TURN && st * STEP + na[i] >= p.D ? OOR : ga[i]), st * STEP * 2);
     };
-    // W: a thread decodes 32 weights a step
     const int Kc = p.w.K / 128;
-    const uint8_t* packed = p.w.codes(t.e);
-    const uint16_t* lut = FMT == FMT_INT4 ? nullptr : p.w.table(t.e);
-    const uint16_t *alpha = p.w.alpha + p.w.scales(t.e), *beta = p.w.beta + p.w.scales(t.e);
-    const int place = tid % BN, h = tid / BN;      // forward: half h of the step's k of the row at a place
-    int wr = 0;
-    bool live = true;
-    if constexpr (!TURN) {
-        const int b = column_of(place), half = gate ? b >> 3 & 1 : 0;
-        const int col = gate ? col0 + (place & ~63) / 2 + 8 * (b >> 4) + (b & 7) : col0 + (place & ~63) + b;
-        live = col < p.q.No;
-        wr = live ? col + half * p.q.No : 0;
-    }
-    // TURN: the 32 k of the wave (any where the tile reaches past the last)
-    const int slot = col0 + 32 * w < p.w.K ? (col0 >> 5) + w : 0;
-    uint32_t code[4];
-    RowTable row;
-    auto fetch_weights = [&](int st) __attribute__((always_inline)) {
-        if constexpr (TURN) {
-            const int n = st * STEP + lane < p.w.N ? st * STEP + lane : 0;
-            row = fetch_table<FMT>(lut, alpha, beta, n, Kc, slot >> 2, p.w.g);
-            fetch_codes<FMT>(packed, n, Kc, slot >> 2, slot & 3, code);
-        } else {
-            fetch_codes<FMT>(packed, wr, Kc, st >> 1, 2 * (st & 1) + h, code);
-            if (!(st & 1) || st == s0)
-                row = fetch_table<FMT>(lut, alpha, beta, wr, Kc, st >> 1, p.w.g);
-        }
-    };
-    auto unpack = [&](int st, uint16_t* sb) __attribute__((always_inline)) {
-        const ByteTable<FMT> table(row);
-        uint32_t v[16];
-        decode(table, code, v);
-        if constexpr (TURN) {
-            const bool in = st * STEP + lane < p.w.N;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int k = first_k(i) + 2 * (lane & 1);                   // of the wave's 32
-                const int b = 32 * (w & 1) + k;
-                const int at = 64 * (w >> 1) + 16 * (b >> 2 & 3) + 4 * (b >> 4) + (b & 3);
-                const uint32_t o = pair_rows(in ? v[i] : 0u, lane & 1);
-                reinterpret_cast<uint32_t*>(sb)[row_at<true>(at) * (STEP / 2) + ((lane >> 3) ^ key(at)) * 4 + (lane >> 1 & 3)] = o;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<u32x4_t*>(sb + place * STEP + ((4 * h + i) ^ key(place)) * 8) = in_order(v + 4 * i);
-        }
-    };
+
     f32x4_t acc[RM][4];
 #pragma unroll
     for (int i = 0; i < RM; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const int wm = (w / WN) * (RM * 16), wn = (w % WN) * 64;
-    auto multiply = [&](const uint16_t* sa, const uint16_t* sb) __attribute__((always_inline)) {
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            bf16x8_t a[RM], b[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int at = wn + 16 * j + c;
-                b[j] = *reinterpret_cast<const bf16x8_t*>(sb + row_at<TURN>(at) * STEP + ((4 * kk + g) ^ key(at)) * 8);
-            }
-#pragma unroll
-            for (int i = 0; i < RM; ++i)
-                a[i] = *reinterpret_cast<const bf16x8_t*>(sa + (wm + 16 * i + c) * STEP + ((4 * kk + g) ^ key(wm + 16 * i + c)) * 8);
-#pragma unroll
-            for (int i = 0; i < RM; ++i)
+    // of every 32 rows of the tile a wave takes the first or the second 16
+    const int wm = w / WN * 16, wn = (w % WN) * 64;
+    const int blocks = __builtin_amdgcn_readfirstlane(t.count > wm ? (t.count - wm + 31) / 32 : 0);
+    // operand reads: 16 or 32 rows on the key is the same, so one place each and
+    // constant distances; the second half of a step is four pieces on.  (Kept from the
+    // compiler, which would hold row and piece apart and add them every time.)
+    int oa = (wm + c) * STEP + (g ^ key(wm + c)) * 8, ob = (wn + c) * STEP + (g ^ key(wn + c)) * 8;
+    asm("" : "+v"(oa), "+v"(ob));
+    auto operand_a = [&](const uint16_t* sa, int i, int kk) __attribute__((always_inline)) {
+        return *reinterpret_cast<const bf16x8_t*>(sa + (oa ^ 32 * kk) + 32 * i * STEP);
+    };
+    auto operand_b = [&](const uint16_t* sb, int j, int kk) __attribute__((always_inline)) {
+        return *reinterpret_cast<const bf16x8_t*>(sb + (ob ^ 32 * kk) + 16 * j * STEP);
+    };
+    // A step's products in parts, each with a share of the decoding, aside(part),
+    // between them: a product leaves the vector ALU three issues in four, and what a
+    // part decodes is written before the next begins, or the compiler keeps all of it
+    // in registers.
+    // Blocks: of 16 rows of the tile that the wave works on.
+    auto multiply = [&](auto blocks_, const uint16_t* sa, const uint16_t* sb, auto aside) __attribute__((always_inline)) {
+        constexpr int BLOCKS = decltype(blocks_)::value, PARTS = parts_of(BLOCKS), PER = 2 * BLOCKS / PARTS;
+        bf16x8_t b[4];
+        static_for<0, PARTS>([&](auto part_) __attribute__((always_inline)) {
+            constexpr int part = decltype(part_)::value, kk = part * PER / BLOCKS;
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (part * PER % BLOCKS == 0)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    acc[i][j] = mfma(b[j], a[i], acc[i][j]);
-        }
+                    b[j] = operand_b(sb, j, kk);
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+                const int i = part * PER % BLOCKS + q;
+                const bf16x8_t a = operand_a(sa, i, kk);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = mfma(b[j], a, acc[i][j]);
+            }
+            aside(part_);
+        });
+        __builtin_amdgcn_sched_barrier(0);
     };
-    // this step's tiles are in, and every wave has read the other buffers
-    auto meet = [&]() __attribute__((always_inline)) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // this step's tiles are in, all but the wave's last n loads, and every wave has
+    // read the other buffers
+    auto meet = [&](auto n) __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(decltype(n)::value) : "memory");
         __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
     };
-    if (s0 < s1) {
-        fetch(s0, sa0);
-        fetch_weights(s0);
-        unpack(s0, sb0);
-        if (s0 + 1 < s1)
-            fetch_weights(s0 + 1);
-    }
-    auto step = [&](int st, uint16_t* sa, uint16_t* sb, uint16_t* sa_next, uint16_t* sb_next) __attribute__((always_inline)) {
-        meet();
-        if (st + 1 < s1) {
-            fetch(st + 1, sa_next);
-            unpack(st + 1, sb_next);
-            if (st + 2 < s1)
-                fetch_weights(st + 2);
+    typedef std::integral_constant<int, 0> All;
+    typedef std::integral_constant<int, RowReader<FMT>::LOADS> AllButChunk;
+    auto run = [&](auto blocks_) __attribute__((always_inline)) {
+        constexpr int PARTS = parts_of(decltype(blocks_)::value);
+        auto product = [&](const uint16_t* sa, const uint16_t* sb, auto aside) __attribute__((always_inline)) {
+            multiply(blocks_, sa, sb, aside);
+        };
+        if constexpr (TURN) {
+            // A wave decodes 32 k of 64 rows (any 32 where the tile reaches past the last).
+            // A row's byte table serves 128 k, four waves: four threads make a quarter each, two
+            // steps ahead, and it lies in LDS.
+            constexpr int QUARTERS = ByteTable<FMT>::ENTRIES / 4;
+            const int s0 = share(p.steps, blockIdx.y, p.q.S), s1 = share(p.steps, blockIdx.y + 1, p.q.S);
+            const int slot = col0 + 32 * w < p.w.K ? (col0 >> 5) + w : 0, chunk = slot >> 2, part = w & 3;
+            const size_t scales = static_cast<size_t>(p.w.N) * (p.w.K / p.w.g) * 2;
+            const __amdgpu_buffer_rsrc_t codes = buffer_of(p.w.codes(t.e), p.w.packed_bytes),
+                                         alpha = buffer_of(p.w.alpha + p.w.scales(t.e), scales),
+                                         beta = buffer_of(p.w.beta + p.w.scales(t.e), scales);
+            const uint16_t* lut = FMT == FMT_INT4 ? nullptr : p.w.table(t.e);
+            const int tile_pitch = Kc * 64 * slot_bytes(FMT);
+            const int at = (lane >> 4) * tile_pitch + ((slot & 3) * 16 + (lane & 15)) * slot_bytes(FMT);
+            uint32_t code[4];
+            struct {
+                u32x2_t entries;
+                uint32_t alpha, beta;
+            } row;
+            auto fetch_row = [&](int st) __attribute__((always_inline)) {     // for a quarter of a table
+                const int n = st * STEP + lane < p.w.N ? st * STEP + lane : 0, at_scale = n * (p.w.K / p.w.g) * 2;
+                row.alpha = __builtin_amdgcn_raw_buffer_load_b16(alpha, at_scale, chunk * 128 / p.w.g * 2, 0);
+                row.beta = __builtin_amdgcn_raw_buffer_load_b16(beta, at_scale, chunk * 128 / p.w.g * 2, 0);
+                typedef u32x2_t __attribute__((aligned(2))) entries_t;
+                if constexpr (FMT != FMT_INT4)
+                    row.entries = *reinterpret_cast<const entries_t*>(lut + static_cast<size_t>(n) * 16 + 4 * part);
+            };
+            auto make_table = [&](int st, int buffer) __attribute__((always_inline)) {
+                const float fa = bf16_to_f32(row.alpha), fb = bf16_to_f32(row.beta);
+                uint32_t v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float x = FMT == FMT_INT4 ? static_cast<float>(4 * part + 2 * i) : __uint_as_float(row.entries[i] << 16);
+                    const float y = FMT == FMT_INT4 ? static_cast<float>(4 * part + 2 * i + 1) : __uint_as_float(row.entries[i] & 0xffff0000u);
+                    v[i] = f32_to_bf16(fmaf(fa, x, fb)) | f32_to_bf16(fmaf(fa, y, fb)) << 16;
+                }
+                const bool in = st * STEP + lane < p.w.N;                  // rows behind the last: weights of 0
+                if (part < QUARTERS) {
+                    turned[buffer][w >> 2][part][lane] = in ? __builtin_amdgcn_perm(v[1], v[0], 0x06040200u) : 0u;
+                    turned[buffer][w >> 2][QUARTERS + part][lane] = in ? __builtin_amdgcn_perm(v[1], v[0], 0x07050301u) : 0u;
+                }
+            };
+            auto fetch_weights = [&](int st) __attribute__((always_inline)) {
+                load_slot<FMT>(codes, at, (st * (STEP / 16) * Kc + chunk) * 64 * slot_bytes(FMT), code);
+            };
+            ByteTable<FMT> table;
+            auto read_table = [&](int buffer) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < QUARTERS; ++i) {
+                    table.lo[i] = turned[buffer][w >> 2][i][lane];
+                    table.hi[i] = turned[buffer][w >> 2][QUARTERS + i][lane];
+                }
+            };
+            auto unpack = [&](int i, uint16_t* sb) __attribute__((always_inline)) {
+                uint32_t v[4];
+                decode8(table, code, i, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int b = 32 * (w & 1) + 8 * i + 2 * j + (lane & 1);         // of the 64 k of two waves
+                    const int to = 64 * (w >> 1) + 16 * (b >> 2 & 3) + 4 * (b >> 4) + (b & 3);
+                    reinterpret_cast<uint32_t*>(sb)[to * (STEP / 2) + ((lane >> 3) ^ key(to)) * 4 + (lane >> 1 & 3)] = pair_rows(v[j], lane & 1);
+                }
+            };
+            // what lies past the last step is fetched and decoded for nothing: there is no
+            // branch between the products
+            auto near = [&](int st) __attribute__((always_inline)) { return st < s1 ? st : s1 - 1; };
+            auto step = [&](int st, uint16_t* sa, uint16_t* sb, uint16_t* sa_next, uint16_t* sb_next) __attribute__((always_inline)) {
+                meet(All{});
+                fetch(near(st + 1), sa_next);
+                make_table(near(st + 2), st - s0 & 1);
+                fetch_row(near(st + 3));
+                read_table(st + 1 - s0 & 1);
+                product(sa, sb, [&](auto n) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int i = 0; i < 4 / PARTS; ++i)
+                        unpack(4 / PARTS * decltype(n)::value + i, sb_next);
+                });
+                fetch_weights(near(st + 2));
+            };
+            fetch_row(s0);
+            make_table(s0, 0);
+            fetch_row(near(s0 + 1));
+            make_table(near(s0 + 1), 1);
+            fetch(s0, sa0);
+            fetch_weights(s0);
+            fetch_row(near(s0 + 2));
+            __syncthreads();
+            read_table(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                unpack(i, sb0);
+            fetch_weights(near(s0 + 1));
+            int st = s0;
+            for (; st + 1 < s1; st += 2) {
+                step(st, sa0, sb0, sa1, sb1);
+                step(st + 1, sa1, sb1, sa0, sb0);
+            }
+            if (st < s1)
+                step(st, sa0, sb0, sa1, sb1);
+        } else {
+            // chunks of two steps; thread h of the row at a place has half h of each step's k
+            const int c0 = share(Kc, blockIdx.y, p.q.S), c1 = share(Kc, blockIdx.y + 1, p.q.S);
+            const int place = tid % BN, h = tid / BN;
+            const int b = column_of(place), half = gate ? b >> 3 & 1 : 0;
+            const int col = gate ? col0 + (place & ~63) / 2 + 8 * (b >> 4) + (b & 7) : col0 + (place & ~63) + b;
+            const int wr = col < p.q.No ? col + half * p.q.No : 0;
+            const RowReader<FMT> reader(p.w, t.e, wr, h);
+            int ow = place * STEP + (4 * h ^ key(place)) * 8;        // where the first goes; the i-th at ow ^ 8 i
+            asm("" : "+v"(ow));
+            if constexpr (FMT != FMT_INT4) {
+                if (h == 0) {
+                    const RowTable row = fetch_table<FMT>(p.w.table(t.e), p.w.alpha + p.w.scales(t.e), p.w.beta + p.w.scales(t.e), wr, Kc, c0, p.w.g);
+#pragma unroll
+                    for (int i = 0; i < (FMT == FMT_ANY4 ? 2 : 1); ++i)
+                        tables[place][i] = row.table[i];
+                }
+                __syncthreads();
+            }
+            RowPart A, B;
+            ByteTable<FMT> table;
+            // a chunk's table serves both its steps
+            auto tabulate = [&](const RowPart& from) __attribute__((always_inline)) {
+                RowTable row;
+                row.table[0] = row.table[1] = u32x4_t{0u, 0u, 0u, 0u};
+                if constexpr (FMT != FMT_INT4)
+#pragma unroll
+                    for (int i = 0; i < (FMT == FMT_ANY4 ? 2 : 1); ++i)
+                        row.table[i] = tables[place][i];
+                row.alpha = from.alpha;
+                row.beta = from.beta;
+                return ByteTable<FMT>(row);
+            };
+            auto unpack = [&](const RowPart& from, int which, int i, uint16_t* sb) __attribute__((always_inline)) {
+                uint32_t v[4];
+                decode8(table, from.code[which], i, v);
+                *reinterpret_cast<u32x4_t*>(sb + (ow ^ 8 * i)) = u32x4_t{v[0], v[1], v[2], v[3]};
+            };
+            // The first step of a chunk: its second half is decoded, and the chunk after
+            // the next asked for; the second step decodes the next chunk's first half.
+            // (Past the last chunk both do so for nothing: a branch would keep the decoding
+            // from standing between the products.)
+            auto first_step = [&](int ch, RowPart& mine) __attribute__((always_inline)) {
+                fetch(2 * ch + 1, sa1);
+                product(sa0, sb0, [&](auto part) __attribute__((always_inline)) {
+                    constexpr int n = decltype(part)::value, share = 4 / PARTS;
+#pragma unroll
+                    for (int i = 0; i < share; ++i)
+                        unpack(mine, 1, share * n + i, sb1);
+                });
+                reader.fetch(mine, ch + 2 < c1 ? ch + 2 : c0);
+            };
+            auto second_step = [&](int ch, const RowPart& other) __attribute__((always_inline)) {
+                fetch(ch + 1 < c1 ? 2 * ch + 2 : 2 * c0, sa0);
+                product(sa1, sb1, [&](auto part) __attribute__((always_inline)) {
+                    constexpr int n = decltype(part)::value;
+                    if constexpr (n == 0)
+                        table = tabulate(other);
+                    // four parts: the table, then one, one and two eighths of 32 weights
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (PARTS == 4 ? n == (i < 2 ? i + 1 : 3) : n == i / 2)
+                            unpack(other, 0, i, sb0);
+                });
+            };
+            reader.fetch(A, c0);
+            reader.fetch(B, c0 + 1 < c1 ? c0 + 1 : c0);
+            fetch(2 * c0, sa0);
+            table = tabulate(A);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                unpack(A, 0, i, sb0);
+            int ch = c0;
+            for (; ch + 1 < c1; ch += 2) {
+                meet(All{});
+                first_step(ch, A);
+                meet(AllButChunk{});
+                second_step(ch, B);
+                meet(All{});
+                first_step(ch + 1, B);
+                meet(AllButChunk{});
+                second_step(ch + 1, A);
+            }
+            if (ch < c1) {
+                meet(All{});
+                first_step(ch, A);
+                meet(AllButChunk{});
+                second_step(ch, B);
+            }
         }
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(sa, sb);
-        __builtin_amdgcn_sched_barrier(0);
     };
-    int st = s0;
-    for (; st + 1 < s1; st += 2) {
-        step(st, sa0, sb0, sa1, sb1);
-        step(st + 1, sa1, sb1, sa0, sb0);
-    }
-    if (st < s1)
-        step(st, sa0, sb0, sa1, sb1);
+    // rows behind the last are zeros; where they fill half of the wave's blocks, those
+    // are left out
+    if (RM > 1 && blocks <= RM / 2)
+        run(std::integral_constant<int, (RM > 1 ? RM / 2 : 1)>{});
+    else
+        run(std::integral_constant<int, RM>{});
     // The sums leave through LDS of the wave's own, so that lanes next to one another
     // write columns next to one another: 16 pieces of four floats a row, piece q at
     // q ^ row.  With a gate its columns come first, those of the up rows behind.
-    meet();
-    constexpr int HALVES = RM == 8 ? 2 : 1, ROWS = 16 * RM / HALVES;
+    meet(All{});
+    constexpr int HALVES = RM > 4 ? 2 : 1, ROWS = 16 * RM / HALVES;
+    static_assert(WAVES / 4 * ROWS * 256 <= (BM < BN ? BM : BN) * STEP * 2, "the waves' rooms lie in the four buffers");
     const int room = w * 4 / WAVES;       // a wave's, or two waves', of the four buffers
     uint16_t* const in = room == 0 ? sa0 : room == 1 ? sb0 : room == 2 ? sa1 : sb1;
     f32x4_t* stage = reinterpret_cast<f32x4_t*>(in) + w % (WAVES / 4) * (ROWS * 16);
-    const int pieces = gate ? 4 : 8;      // of eight columns of out a row
+    const int lane2 = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)), c2 = lane2 & 15, g2 = lane2 >> 4;   // no register for them until here
+    const int pieces = gate ? 4 : 8;       // of eight columns of out a row
 #pragma unroll
     for (int half = 0; half < HALVES; ++half) {
         wave_sync();
 #pragma unroll
         for (int i = 0; i < RM / HALVES; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                stage[(16 * i + c) * 16 + ((gate ? 8 * (j >> 1) + 2 * g + (j & 1) : 4 * g + j) ^ c)] = acc[half * (RM / HALVES) + i][j];
+            for (int j = 0; j < 4; ++j) {
+                const int to = gate ? 8 * (j >> 1) + 2 * g2 + (j & 1) : 4 * g2 + j;
+                stage[(16 * i + c2) * 16 + (to ^ c2)] = acc[half * (RM / HALVES) + i][j];
+            }
         wave_sync();
-        for (int o = lane; o < ROWS * pieces; o += WAVE) {
+        for (int o = lane2; o < ROWS * pieces; o += WAVE) {
             const int row = o / pieces, q = o % pieces;
-            const int pair = pairs[wm + half * ROWS + row], col = col0 + (gate ? wn / 2 : wn) + 8 * q;
+            const int pair = pairs[32 * (half * (RM / HALVES) + row / 16) + wm + row % 16];
+            const int col = col0 + (gate ? wn / 2 : wn) + 8 * q;
             if (pair < 0 || col >= p.q.No)
                 continue;
             f32x4_t f[4];
@@ -849,7 +1077,7 @@ size_t part_bytes(const Shape& s, int64_t P, int64_t C) { return s.S > 1 ? up256
 template <int FMT, bool TURN>
 void launch_tile(const Shape& s, const TileArgs& a, hipStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>(s.tiles_m * s.tiles_n), static_cast<unsigned>(s.S));
+    const dim3 grid(static_cast<unsigned>((s.tiles_m * s.tiles_n + 7) / 8 * 8), static_cast<unsigned>(s.S));
 #define TILE(WN_, RM_) hipLaunchKernelGGL((k_tile<FMT, WN_, RM_, TURN>), grid, dim3(128 * WN_), 0, stream, a)
     if (s.rm == 8) TILE(4, 8);
     else if (s.rm == 4) TILE(2, 4);
