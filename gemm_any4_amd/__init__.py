@@ -32,7 +32,9 @@ any2_gemm_act and any3_gemm_act (the product with bias, activation, gate and
 residual), act_backward; route and route_backward (the experts of each token),
 experts_plan, experts_gemm and experts_gemm_dx (and their int4, any2 and any3
 forms: stacked layers, each row through its expert), combine and
-combine_backward (the weighted sum of the experts' outputs).
+combine_backward (the weighted sum of the experts' outputs).  What one of these
+calls writes for another (z, an output for combine, an input's gradient for
+act_backward or combine) may be a bf16 tensor or an fp32 one, given as z or out.
 These and the calls for fine-tunes take tensors of any GPU, run on that GPU's current stream (or `stream`,
 on which their outputs and workspaces are then allocated too) and can be
 captured into a graph.
@@ -128,19 +130,19 @@ def lib() -> ctypes.CDLL:
                 ("any2_gemm_dx", ctypes.c_int, [P] * 6 + [I64] * 4 + [P, SZ, P]),
                 ("any3_gemm_dx", ctypes.c_int, [P] * 6 + [I64] * 4 + [P, SZ, P]),
                 ("any4_gemm_act_workspace_size", SZ, [I64] * 4),
-                ("any4_gemm_act", ctypes.c_int, [INT] + [P] * 9 + [INT] * 2 + [I64] * 4 + [P, SZ, P]),
+                ("any4_gemm_act", ctypes.c_int, [INT] + [P] * 8 + [INT, P] + [INT] * 3 + [I64] * 4 + [P, SZ, P]),
                 ("any4_act_backward_workspace_size", SZ, [I64] * 2 + [INT]),
-                ("any4_act_backward", ctypes.c_int, [P] * 4 + [INT] * 2 + [I64] * 2 + [P, SZ, P]),
+                ("any4_act_backward", ctypes.c_int, [P, INT, P, INT, P, P] + [INT] * 2 + [I64] * 2 + [P, SZ, P]),
                 ("any4_route", ctypes.c_int, [P, INT] + [P] * 3 + [INT] * 2 + [F32] + [I64] * 5 + [P]),
                 ("any4_route_backward", ctypes.c_int,
                  [P, P, INT, P, P] + [INT] * 2 + [F32] + [I64] * 3 + [P]),
                 ("any4_experts_workspace_size", SZ, [I64] * 6),
                 ("any4_experts_gemm", ctypes.c_int,
-                 [INT, P, INT] + [P] * 9 + [INT] * 2 + [I64] * 6 + [P, SZ, P]),
+                 [INT, P, INT] + [P] * 8 + [INT, P] + [INT] * 3 + [I64] * 6 + [P, SZ, P]),
                 ("any4_experts_dx_workspace_size", SZ, [I64] * 6),
-                ("any4_experts_gemm_dx", ctypes.c_int, [INT] + [P] * 8 + [I64] * 6 + [P, SZ, P]),
-                ("any4_combine", ctypes.c_int, [P] * 4 + [I64] * 3 + [P]),
-                ("any4_combine_backward", ctypes.c_int, [P] * 5 + [I64] * 3 + [P])):
+                ("any4_experts_gemm_dx", ctypes.c_int, [INT] + [P] * 8 + [INT] + [I64] * 6 + [P, SZ, P]),
+                ("any4_combine", ctypes.c_int, [P, INT] + [P] * 3 + [I64] * 3 + [P]),
+                ("any4_combine_backward", ctypes.c_int, [P, P, INT] + [P] * 3 + [I64] * 3 + [P])):
             getattr(L, name).restype = restype
             getattr(L, name).argtypes = argtypes
         L.any4_read_probe.restype = ctypes.c_int
@@ -953,14 +955,16 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 def gemm_act_raw(fmt, x_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, residual_ptr, z_ptr, out_ptr, act, gate,
-                 M, N, K, g, ws_ptr, ws_bytes, stream=None) -> int:
+                 M, N, K, g, ws_ptr, ws_bytes, stream=None, z_f32=0, out_f32=0) -> int:
     """fmt, act: the numbers of any4_format and any4_activation."""
     return lib().any4_gemm_act(fmt, x_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, residual_ptr, z_ptr,
-                               out_ptr, act, gate, M, N, K, g, ws_ptr, ws_bytes, _stream(stream))
+                               z_f32, out_ptr, out_f32, act, gate, M, N, K, g, ws_ptr, ws_bytes, _stream(stream))
 
 
-def act_backward_raw(dy_ptr, z_ptr, dz_ptr, dbias_ptr, act, gate, M, N, ws_ptr, ws_bytes, stream=None) -> int:
-    return lib().any4_act_backward(dy_ptr, z_ptr, dz_ptr, dbias_ptr, act, gate, M, N, ws_ptr, ws_bytes, _stream(stream))
+def act_backward_raw(dy_ptr, z_ptr, dz_ptr, dbias_ptr, act, gate, M, N, ws_ptr, ws_bytes, stream=None, dy_f32=0,
+                     z_f32=0) -> int:
+    return lib().any4_act_backward(dy_ptr, dy_f32, z_ptr, z_f32, dz_ptr, dbias_ptr, act, gate, M, N, ws_ptr, ws_bytes,
+                                   _stream(stream))
 
 
 def route_raw(logits_ptr, bf16, bias_ptr, w_ptr, ids_ptr, score, renorm, scale, T, E, k, groups, top_groups,
@@ -976,24 +980,24 @@ def route_backward_raw(dw_ptr, logits_ptr, bf16, ids_ptr, dlogits_ptr, score, re
 
 
 def experts_gemm_raw(fmt, x_ptr, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, ids_ptr, plan_ptr, z_ptr,
-                     out_ptr, act, gate, T, k, E, N, K, g, ws_ptr, ws_bytes, stream=None) -> int:
+                     out_ptr, act, gate, T, k, E, N, K, g, ws_ptr, ws_bytes, stream=None, z_f32=0, out_f32=0) -> int:
     return lib().any4_experts_gemm(fmt, x_ptr, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, ids_ptr,
-                                   plan_ptr, z_ptr, out_ptr, act, gate, T, k, E, N, K, g, ws_ptr, ws_bytes,
-                                   _stream(stream))
+                                   plan_ptr, z_ptr, z_f32, out_ptr, out_f32, act, gate, T, k, E, N, K, g, ws_ptr,
+                                   ws_bytes, _stream(stream))
 
 
 def experts_gemm_dx_raw(fmt, dy_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, ids_ptr, plan_ptr, dx_ptr, T, k, E, N, K, g,
-                        ws_ptr, ws_bytes, stream=None) -> int:
+                        ws_ptr, ws_bytes, stream=None, dx_f32=0) -> int:
     return lib().any4_experts_gemm_dx(fmt, dy_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, ids_ptr, plan_ptr, dx_ptr,
-                                      T, k, E, N, K, g, ws_ptr, ws_bytes, _stream(stream))
+                                      dx_f32, T, k, E, N, K, g, ws_ptr, ws_bytes, _stream(stream))
 
 
-def combine_raw(y_ptr, w_ptr, residual_ptr, out_ptr, T, k, N, stream=None) -> int:
-    return lib().any4_combine(y_ptr, w_ptr, residual_ptr, out_ptr, T, k, N, _stream(stream))
+def combine_raw(y_ptr, w_ptr, residual_ptr, out_ptr, T, k, N, stream=None, y_f32=0) -> int:
+    return lib().any4_combine(y_ptr, y_f32, w_ptr, residual_ptr, out_ptr, T, k, N, _stream(stream))
 
 
-def combine_backward_raw(dout_ptr, y_ptr, w_ptr, dy_ptr, dw_ptr, T, k, N, stream=None) -> int:
-    return lib().any4_combine_backward(dout_ptr, y_ptr, w_ptr, dy_ptr, dw_ptr, T, k, N, _stream(stream))
+def combine_backward_raw(dout_ptr, y_ptr, w_ptr, dy_ptr, dw_ptr, T, k, N, stream=None, y_f32=0) -> int:
+    return lib().any4_combine_backward(dout_ptr, y_ptr, y_f32, w_ptr, dy_ptr, dw_ptr, T, k, N, _stream(stream))
 
 
 @functools.lru_cache(maxsize=4096)      # constant for its sizes
@@ -1032,6 +1036,22 @@ def _maybe(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple, 
     return None if t is None else _tensor(t, name, dtype, shape, device)
 
 
+def _kept(t: torch.Tensor | None, name: str, shape: tuple, device) -> tuple:
+    """(address, whether fp32) of values that are kept in bf16 or in fp32."""
+    if t is None:
+        return None, 0
+    f32 = t.dtype is torch.float32
+    return _tensor(t, name, torch.float32 if f32 else torch.bfloat16, shape, device), 1 if f32 else 0
+
+
+def _result(out: torch.Tensor | None, name: str, shape: tuple, device) -> tuple:
+    """(tensor, address, whether fp32) of a result: the caller's, bf16 or fp32, or a new bf16 one."""
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        return out, out.data_ptr() or None, 0
+    return (out,) + _kept(out, name, shape, device)
+
+
 def _layer(fmt: int, packed, lut, alpha, beta, g: int, dev, experts: bool) -> tuple:
     """Checks a layer [N, K], or stacked ones [E, N, K]: (E, N, K, their addresses)."""
     if g <= 0 or alpha.dim() != 2 + experts:
@@ -1060,16 +1080,13 @@ def _gemm_act(fmt: int, x, packed, lut, alpha, beta, g, bias, act, gate, residua
         raise ValueError("a gated layer must have an even number of rows")
     p_x = _tensor(x, "x", bf16, (M, K), dev)
     p_bias, p_residual = _maybe(bias, "bias", bf16, (N,), dev), _maybe(residual, "residual", bf16, (M, No), dev)
-    p_z, number = _maybe(z, "z", bf16, (M, N), dev), _choice("act", act, ACTIVATIONS)
+    (p_z, z32), number = _kept(z, "z", (M, N), dev), _choice("act", act, ACTIVATIONS)
     with _on(dev, stream):
-        if out is None:
-            out = torch.empty((M, No), dtype=bf16, device=dev)
-            p_out = out.data_ptr() or None
-        else:
-            p_out = _tensor(out, "out", bf16, (M, No), dev)
+        out, p_out, out32 = _result(out, "out", (M, No), dev)
         ws, p_ws, nbytes = _scratch(workspace, gemm_act_workspace_size(M, N, K, g), dev)
-        check(lib().any4_gemm_act(fmt, p_x, p_packed, p_lut, p_alpha, p_beta, p_bias, p_residual, p_z, p_out, number,
-                                  1 if gate else 0, M, N, K, g, p_ws, nbytes, _current_handle(dev.index)))
+        check(lib().any4_gemm_act(fmt, p_x, p_packed, p_lut, p_alpha, p_beta, p_bias, p_residual, p_z, z32, p_out,
+                                  out32, number, 1 if gate else 0, M, N, K, g, p_ws, nbytes,
+                                  _current_handle(dev.index)))
     return out
 
 
@@ -1082,8 +1099,8 @@ def gemm_act(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: to
 
     act: one of ACTIVATIONS.  gate: the layer's rows are [gate; up], No = N / 2, and
     out = act(gate) * up + residual.  bias bf16 [N]; residual bf16 [M, No] (may
-    be out itself).  For the backward pass z bf16 [M, N] gets x W^T + bias:
-    act_backward, then gemm_dx."""
+    be out itself).  For the backward pass z [M, N] gets x W^T + bias:
+    act_backward, then gemm_dx.  z and out may be bf16 or fp32."""
     return _gemm_act(0, x, packed, lut, alpha, beta, g, bias, act, gate, residual, z, out, workspace, stream)
 
 
@@ -1114,9 +1131,8 @@ def any3_gemm_act(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alph
 def act_backward(dy: torch.Tensor, z: torch.Tensor, act: str, gate: bool = False, need_bias: bool = True,
                  dz: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
                  workspace: torch.Tensor | None = None, stream=None) -> tuple:
-    """(dz, dbias) of an epilogue for dy bf16 [..., No], from z bf16 [..., N] as
-    gemm_act or experts_gemm kept it: dz bf16 like z (may be z), dbias fp32 [N], the
-    sum over all rows (need_bias = False: None).  The gradient of the product's
+    """(dz, dbias) of an epilogue for dy [..., No], from z [..., N] as gemm_act or
+    experts_gemm kept it (bf16 or fp32): dz bf16 (may be z), dbias fp32 [N], the sum over all rows (need_bias = False: None).  The gradient of the product's
     input is gemm_dx (experts_gemm_dx) of dz, that of the residual dy itself."""
     if not z.is_cuda:
         raise ValueError("z must be a GPU tensor")
@@ -1127,8 +1143,8 @@ def act_backward(dy: torch.Tensor, z: torch.Tensor, act: str, gate: bool = False
     M = z.numel() // N if N else 0
     if gate and N % 2:
         raise ValueError("a gated layer must have an even number of rows")
-    p_z = _tensor(z, "z", bf16, shape, dev)
-    p_dy = _tensor(dy, "dy", bf16, shape[:-1] + (N // 2 if gate else N,), dev)
+    p_z, z32 = _kept(z, "z", shape, dev)
+    p_dy, dy32 = _kept(dy, "dy", shape[:-1] + (N // 2 if gate else N,), dev)
     number = _choice("act", act, ACTIVATIONS)
     with _on(dev, stream):
         if dz is None:
@@ -1145,8 +1161,8 @@ def act_backward(dy: torch.Tensor, z: torch.Tensor, act: str, gate: bool = False
             p_dbias = _tensor(dbias, "dbias", torch.float32, (N,), dev)
             need = act_backward_workspace_size(M, N, bool(gate))
         ws, p_ws, nbytes = _scratch(workspace, need, dev)
-        check(lib().any4_act_backward(p_dy, p_z, p_dz, p_dbias, number, 1 if gate else 0, M, N, p_ws, nbytes,
-                                      _current_handle(dev.index)))
+        check(lib().any4_act_backward(p_dy, dy32, p_z, z32, p_dz, p_dbias, number, 1 if gate else 0, M, N, p_ws,
+                                      nbytes, _current_handle(dev.index)))
     return dz, dbias
 
 
@@ -1229,18 +1245,14 @@ def _experts_gemm(fmt: int, x, packed, lut, alpha, beta, g, ids, bias, act, gate
     if gate and N % 2:
         raise ValueError("a gated layer must have an even number of rows")
     p_x = _tensor(x, "x", bf16, (T, k, K) if per_pair else (T, K), dev)
-    p_bias, p_z = _maybe(bias, "bias", bf16, (E, N), dev), _maybe(z, "z", bf16, (T, k, N), dev)
+    p_bias, (p_z, z32) = _maybe(bias, "bias", bf16, (E, N), dev), _kept(z, "z", (T, k, N), dev)
     number = _choice("act", act, ACTIVATIONS)
     with _on(dev, stream):
-        if out is None:
-            out = torch.empty((T, k, No), dtype=bf16, device=dev)
-            p_out = out.data_ptr() or None
-        else:
-            p_out = _tensor(out, "out", bf16, (T, k, No), dev)
+        out, p_out, out32 = _result(out, "out", (T, k, No), dev)
         ws, p_ws, nbytes = _scratch(workspace, experts_workspace_size(T, k, E, N, K, g), dev)
         check(lib().any4_experts_gemm(fmt, p_x, 1 if per_pair else 0, p_packed, p_lut, p_alpha, p_beta, p_bias, p_ids,
-                                      p_plan, p_z, p_out, number, 1 if gate else 0, T, k, E, N, K, g, p_ws, nbytes,
-                                      _current_handle(dev.index)))
+                                      p_plan, p_z, z32, p_out, out32, number, 1 if gate else 0, T, k, E, N, K, g,
+                                      p_ws, nbytes, _current_handle(dev.index)))
     return out
 
 
@@ -1254,7 +1266,8 @@ def experts_gemm(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha
 
     x bf16 [T, K], or [T, k, K]: a row for each pair (the block's second product).  act, gate
     and z ([T, k, N]) as in gemm_act.  A pair whose id is not in 0..E-1 gives zeros.
-    plan: of experts_plan(ids, E), kept over the products of a block."""
+    plan: of experts_plan(ids, E), kept over the products of a block.  z and out
+    may be bf16 or fp32."""
     return _experts_gemm(0, x, packed, lut, alpha, beta, g, ids, bias, act, gate, z, plan, out, workspace, stream)
 
 
@@ -1290,22 +1303,18 @@ def _experts_gemm_dx(fmt: int, dy, packed, lut, alpha, beta, g, ids, plan, out, 
     T, k, p_ids, p_plan = _pairs(ids, E, plan, dev)
     p_dy = _tensor(dy, "dy", bf16, (T, k, N), dev)
     with _on(dev, stream):
-        if out is None:
-            out = torch.empty((T, k, K), dtype=bf16, device=dev)
-            p_out = out.data_ptr() or None
-        else:
-            p_out = _tensor(out, "out", bf16, (T, k, K), dev)
+        out, p_out, out32 = _result(out, "out", (T, k, K), dev)
         ws, p_ws, nbytes = _scratch(workspace, experts_dx_workspace_size(T, k, E, N, K, g), dev)
-        check(lib().any4_experts_gemm_dx(fmt, p_dy, p_packed, p_lut, p_alpha, p_beta, p_ids, p_plan, p_out, T, k, E, N,
-                                         K, g, p_ws, nbytes, _current_handle(dev.index)))
+        check(lib().any4_experts_gemm_dx(fmt, p_dy, p_packed, p_lut, p_alpha, p_beta, p_ids, p_plan, p_out, out32, T, k,
+                                         E, N, K, g, p_ws, nbytes, _current_handle(dev.index)))
     return out
 
 
 def experts_gemm_dx(dy: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor,
                     g: int, ids: torch.Tensor, plan: LoraPlan | None = None, out: torch.Tensor | None = None,
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """dx bf16 [T, k, K] = dy [T, k, N] W_e, the gradient of the rows that went through
-    experts_gemm.  Where the k pairs of a token shared a row, its gradient is their
+    """dx [T, k, K] = dy bf16 [T, k, N] W_e, the gradient of the rows that went through
+    experts_gemm (bf16, or out's fp32).  Where the k pairs of a token shared a row, its gradient is their
     sum: combine(dx)."""
     return _experts_gemm_dx(0, dy, packed, lut, alpha, beta, g, ids, plan, out, workspace, stream)
 
@@ -1335,18 +1344,18 @@ def any3_experts_gemm_dx(dy: torch.Tensor, packed: torch.Tensor, lut: torch.Tens
 
 def combine(y: torch.Tensor, w: torch.Tensor | None = None, residual: torch.Tensor | None = None,
             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """out bf16 [T, N] = residual + sum_j w[:, j] y[:, j]: the experts' outputs y bf16
-    [T, k, N] as the router weights them (w fp32 [T, k]; None: weights of 1, the sum of
+    """out bf16 [T, N] = residual + sum_j w[:, j] y[:, j]: the experts' outputs y (bf16 or fp32
+    [T, k, N]) as the router weights them (w fp32 [T, k]; None: weights of 1, the sum of
     the pairs' gradients).  residual bf16 [T, N] may be out itself."""
     dev, bf16 = _gpu(y, "y", 3), torch.bfloat16
     T, k, N = y.shape
-    p_y, p_w = _tensor(y, "y", bf16, (T, k, N), dev), _maybe(w, "w", torch.float32, (T, k), dev)
+    (p_y, y32), p_w = _kept(y, "y", (T, k, N), dev), _maybe(w, "w", torch.float32, (T, k), dev)
     p_residual = _maybe(residual, "residual", bf16, (T, N), dev)
     with _on(dev, stream):
         if out is None:
             out = torch.empty((T, N), dtype=bf16, device=dev)
         p_out = _tensor(out, "out", bf16, (T, N), dev)
-        check(lib().any4_combine(p_y, p_w, p_residual, p_out, T, k, N, _current_handle(dev.index)))
+        check(lib().any4_combine(p_y, y32, p_w, p_residual, p_out, T, k, N, _current_handle(dev.index)))
     return out
 
 
@@ -1356,7 +1365,7 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, w: torch.Tensor, dy: t
     gradient of the residual is dout itself.  dy may be y itself."""
     dev, bf16, f32 = _gpu(y, "y", 3), torch.bfloat16, torch.float32
     T, k, N = y.shape
-    p_y, p_w = _tensor(y, "y", bf16, (T, k, N), dev), _tensor(w, "w", f32, (T, k), dev)
+    (p_y, y32), p_w = _kept(y, "y", (T, k, N), dev), _tensor(w, "w", f32, (T, k), dev)
     p_dout = _tensor(dout, "dout", bf16, (T, N), dev)
     with _on(dev, stream):
         if dy is None:
@@ -1364,7 +1373,7 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, w: torch.Tensor, dy: t
         if dw is None:
             dw = torch.empty((T, k), dtype=f32, device=dev)
         p_dy, p_dw = _tensor(dy, "dy", bf16, (T, k, N), dev), _tensor(dw, "dw", f32, (T, k), dev)
-        check(lib().any4_combine_backward(p_dout, p_y, p_w, p_dy, p_dw, T, k, N, _current_handle(dev.index)))
+        check(lib().any4_combine_backward(p_dout, p_y, y32, p_w, p_dy, p_dw, T, k, N, _current_handle(dev.index)))
     return dy, dw
 
 

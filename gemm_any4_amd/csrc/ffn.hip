@@ -20,6 +20,7 @@ namespace {
 
 constexpr int MAX_EXPERTS = 1024;
 constexpr int STEP = 64;                                  // of the summed dimension, k_tile
+constexpr int FMT_BF16 = FMT_ANY3 + 1;                    // of k_tile: a layer that k_rows has laid out as bf16 rows
 constexpr int64_t MAX_PAIRS = static_cast<int64_t>(1) << 20;
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -159,24 +160,14 @@ __device__ __forceinline__ void activate_both(float z, int act, float& f, float&
 struct Epilogue {
     const uint16_t* bias;        // [E][N] or null
     const uint16_t* residual;    // [P][No] or null
-    uint16_t* z;                 // [P][N] or null
-    uint16_t* out;               // [P][No]
+    void* z;                     // [P][N] or null
+    void* out;                   // [P][No]
     float* part;                 // [S][P][N] or null (S = 1)
     int N, No, act, S;           // No = N / 2: gated
+    int z32, out32;              // fp32 instead of bf16
 
     __host__ __device__ __forceinline__ bool gated() const { return No != N; }
 };
-
-__device__ __forceinline__ float half_of(const u32x4_t& v, int i) { return bf16_to_f32(v[i / 2] >> (16 * (i & 1)) & 0xffffu); }
-
-__device__ __forceinline__ u32x4_t round8(const float (&v)[8])
-{
-    u32x4_t o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        o[i] = f32_to_bf16(v[2 * i]) | f32_to_bf16(v[2 * i + 1]) << 16;
-    return o;
-}
 
 // Columns col .. col + 7 of pair p: v the (gate's) sums, u the up rows' where there
 // is a gate.
@@ -187,23 +178,24 @@ __device__ __forceinline__ void finish8(const Epilogue& q, int e, int p, int col
         return;
     const bool gate = q.gated();
     if (q.bias) {
-        const uint16_t* b = q.bias + static_cast<size_t>(e) * q.N + col;
-        const u32x4_t bv = load8(b, valid);
+        const size_t at = static_cast<size_t>(e) * q.N + col;
+        float b[8];
+        get_values(q.bias, 0, at, valid, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] += half_of(bv, i);
+            v[i] += b[i];
         if (gate) {
-            const u32x4_t bu = load8(b + q.No, valid);
+            get_values(q.bias, 0, at + q.No, valid, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                u[i] += half_of(bu, i);
+                u[i] += b[i];
         }
     }
     if (q.z) {
-        uint16_t* z = q.z + static_cast<size_t>(p) * q.N + col;
-        store8(z, round8(v), valid);
+        const size_t at = static_cast<size_t>(p) * q.N + col;
+        put_values(q.z, q.z32, at, valid, v);
         if (gate)
-            store8(z + q.No, round8(u), valid);
+            put_values(q.z, q.z32, at + q.No, valid, u);
     }
     float o[8];
 #pragma unroll
@@ -214,15 +206,16 @@ __device__ __forceinline__ void finish8(const Epilogue& q, int e, int p, int col
     }
     const size_t at = static_cast<size_t>(p) * q.No + col;
     if (q.residual) {
-        const u32x4_t r = load8(q.residual + at, valid);
+        float r[8];
+        get_values(q.residual, 0, at, valid, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            o[i] += half_of(r, i);
+            o[i] += r[i];
     }
-    store8(q.out + at, round8(o), valid);
+    put_values(q.out, q.out32, at, valid, o);
 }
 
-// Where part i of n starts among `all` (below 2^24, n at most 64); the same for all
+// Where part i of n starts among `all` (below 2^25, n at most 64); the same for all
 // lanes, which the compiler does not see of a division.
 __device__ __forceinline__ int share(int all, int i, int n) { return __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(all) * i / n)); }
 
@@ -334,16 +327,16 @@ __global__ __launch_bounds__(FEW_THREADS) void k_few(const FewArgs p)
         return;
     const bool gate = p.q.gated();
     const int half = gate ? lane >> 5 : 0;
-    const int col = gate ? blockIdx.x * 32 + (lane & 31) : blockIdx.x * 64 + lane;
+    const int col = gate ? blockIdx.x * (FEW_ROWS / 2) + (lane & 31) : blockIdx.x * FEW_ROWS + lane;
     const bool live = col < p.q.No;
     const int wr = live ? col + half * p.q.No : 0;
     if (t.e == p.r.E) {              // no expert: zeros
         if (blockIdx.z == 0 && live)
             for (int i = w; i < t.count; i += FEW_WAVES) {
                 if (half == 0)
-                    p.q.out[static_cast<size_t>(own[w][i]) * p.q.No + col] = 0;
+                    put_value(p.q.out, p.q.out32, static_cast<size_t>(own[w][i]) * p.q.No + col, 0.0f);
                 if (p.q.z)
-                    p.q.z[static_cast<size_t>(own[w][i]) * p.q.N + wr] = 0;
+                    put_value(p.q.z, p.q.z32, static_cast<size_t>(own[w][i]) * p.q.N + wr, 0.0f);
             }
         return;
     }
@@ -353,12 +346,11 @@ __global__ __launch_bounds__(FEW_THREADS) void k_few(const FewArgs p)
 #pragma unroll
     for (int b = 0; b < 4; ++b)
         acc[b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    if (t.count <= 4)
-        few_product<FMT, 1>(p, t.e, wr, own[w], t.count, s0, s1, acc);
-    else if (t.count <= 8)
-        few_product<FMT, 2>(p, t.e, wr, own[w], t.count, s0, s1, acc);
-    else
-        few_product<FMT, 4>(p, t.e, wr, own[w], t.count, s0, s1, acc);
+    static_for<0, 3>([&](auto n_) __attribute__((always_inline)) {
+        constexpr int NB = 1 << decltype(n_)::value;
+        if (t.count <= 4 * NB && (NB == 1 || t.count > 2 * NB))
+            few_product<FMT, NB>(p, t.e, wr, own[w], t.count, s0, s1, acc);
+    });
 #pragma unroll
     for (int b = 0; b < 4; ++b)
         if (4 * b < t.count)
@@ -380,7 +372,7 @@ __global__ __launch_bounds__(FEW_THREADS) void k_few(const FewArgs p)
         if (p.q.bias && live)
             v += bf16_to_f32(p.q.bias[static_cast<size_t>(t.e) * p.q.N + wr]);
         if (p.q.z && live)
-            p.q.z[static_cast<size_t>(pair) * p.q.N + wr] = static_cast<uint16_t>(f32_to_bf16(v));
+            put_value(p.q.z, p.q.z32, static_cast<size_t>(pair) * p.q.N + wr, v);
         const float up = __shfl(v, lane | 32);
         if (half || !live)
             continue;
@@ -390,7 +382,7 @@ __global__ __launch_bounds__(FEW_THREADS) void k_few(const FewArgs p)
         const size_t to = static_cast<size_t>(pair) * p.q.No + col;
         if (p.q.residual)
             v += bf16_to_f32(p.q.residual[to]);
-        p.q.out[to] = static_cast<uint16_t>(f32_to_bf16(v));
+        put_value(p.q.out, p.q.out32, to, v);
     }
 }
 
@@ -569,14 +561,14 @@ constexpr int parts_of(int blocks) { return blocks >= 2 ? 4 : 2; }
 // 2 x WN waves of RM x 4 blocks of 16 x 16.  TURN: the sum runs over the rows of W
 // and the results are its columns (the input's gradient).
 template <int FMT, int WN, int RM, bool TURN>
-__global__ __launch_bounds__(128 * WN) void k_tile(const TileArgs p)
+__global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileArgs p)
 {
     constexpr int THREADS = 128 * WN, BM = 32 * RM, BN = WN * 64, WAVES = 2 * WN, LA = BM / 8 / WAVES;
     static_assert(LA >= 1, "every wave loads rows of x");
     __shared__ __attribute__((aligned(16))) uint16_t sa0[BM * STEP], sb0[BN * STEP], sa1[BM * STEP], sb1[BN * STEP];
     __shared__ int pairs[BM];
     // forward: the tables of the rows at the places; TURN: byte tables of the next steps' rows
-    __shared__ u32x4_t tables[TURN || FMT == FMT_INT4 ? 1 : BN][FMT == FMT_ANY4 ? 2 : 1];
+    __shared__ u32x4_t tables[TURN || FMT == FMT_INT4 || FMT == FMT_BF16 ? 1 : BN][FMT == FMT_ANY4 ? 2 : 1];
     __shared__ uint32_t turned[TURN ? 2 : 1][TURN ? BN / 128 : 1][TURN ? 2 * ByteTable<FMT>::ENTRIES / 4 : 1][STEP];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
     // Workgroups go to the eight XCDs in turn: each XCD gets a run of tiles whose
@@ -602,12 +594,12 @@ __global__ __launch_bounds__(128 * WN) void k_tile(const TileArgs p)
             for (int i = w; i < t.count; i += WAVES)
                 for (int o = lane; o < (gate ? BN / 2 : BN); o += WAVE)
                     if (col0 + o < p.q.No) {
-                        p.q.out[static_cast<size_t>(pairs[i]) * p.q.No + col0 + o] = 0;
+                        put_value(p.q.out, p.q.out32, static_cast<size_t>(pairs[i]) * p.q.No + col0 + o, 0.0f);
                         if (p.q.z) {
-                            uint16_t* z = p.q.z + static_cast<size_t>(pairs[i]) * p.q.N + col0 + o;
-                            z[0] = 0;
+                            const size_t z = static_cast<size_t>(pairs[i]) * p.q.N + col0 + o;
+                            put_value(p.q.z, p.q.z32, z, 0.0f);
                             if (gate)
-                                z[p.q.No] = 0;
+                                put_value(p.q.z, p.q.z32, z + p.q.No, 0.0f);
                         }
                     }
         return;
@@ -688,6 +680,12 @@ __global__ __launch_bounds__(128 * WN) void k_tile(const TileArgs p)
     };
     typedef std::integral_constant<int, 0> All;
     typedef std::integral_constant<int, RowReader<FMT>::LOADS> AllButChunk;
+    // the column of out and the row of W at a place
+    auto row_of = [&](int place) __attribute__((always_inline)) {
+        const int b = column_of(place), half = gate ? b >> 3 & 1 : 0;
+        const int col = gate ? col0 + (place & ~63) / 2 + 8 * (b >> 4) + (b & 7) : col0 + (place & ~63) + b;
+        return col < p.q.No ? col + half * p.q.No : 0;
+    };
     auto run = [&](auto blocks_) __attribute__((always_inline)) {
         constexpr int PARTS = parts_of(decltype(blocks_)::value);
         auto product = [&](const uint16_t* sa, const uint16_t* sb, auto aside) __attribute__((always_inline)) {
@@ -792,13 +790,40 @@ __global__ __launch_bounds__(128 * WN) void k_tile(const TileArgs p)
             }
             if (st < s1)
                 step(st, sa0, sb0, sa1, sb1);
+        } else if constexpr (FMT == FMT_BF16) {
+            constexpr int LB = BN / 8 / WAVES;
+            const int s0 = share(p.steps, blockIdx.y, p.q.S), s1 = share(p.steps, blockIdx.y + 1, p.q.S);
+            const __amdgpu_buffer_rsrc_t rb = buffer_of(p.w.packed, static_cast<size_t>(p.w.N) * p.w.K * 2);
+            uint32_t gb[LB];
+#pragma unroll
+            for (int i = 0; i < LB; ++i) {
+                const int r = (w * LB + i) * 8 + lane / 8;
+                gb[i] = static_cast<uint32_t>(row_of(r)) * (static_cast<uint32_t>(p.w.K) * 2u) + ((lane & 7) ^ key(r)) * 16u;
+            }
+            auto fetch_both = [&](int st, uint16_t* sa, uint16_t* sb) __attribute__((always_inline)) {
+                fetch(st, sa);
+#pragma unroll
+                for (int i = 0; i < LB; ++i)
+                    load_lds(rb, sb + (w * LB + i) * 8 * STEP, static_cast<int>(gb[i]), st * STEP * 2);
+            };
+            fetch_both(s0, sa0, sb0);
+            int st = s0;
+            for (; st + 1 < s1; st += 2) {
+                meet(All{});
+                fetch_both(st + 1, sa1, sb1);
+                product(sa0, sb0, [](auto) {});
+                meet(All{});
+                fetch_both(st + 2 < s1 ? st + 2 : s0, sa0, sb0);
+                product(sa1, sb1, [](auto) {});
+            }
+            meet(All{});
+            if (st < s1)
+                product(sa0, sb0, [](auto) {});
         } else {
             // chunks of two steps; thread h of the row at a place has half h of each step's k
             const int c0 = share(Kc, blockIdx.y, p.q.S), c1 = share(Kc, blockIdx.y + 1, p.q.S);
             const int place = tid % BN, h = tid / BN;
-            const int b = column_of(place), half = gate ? b >> 3 & 1 : 0;
-            const int col = gate ? col0 + (place & ~63) / 2 + 8 * (b >> 4) + (b & 7) : col0 + (place & ~63) + b;
-            const int wr = col < p.q.No ? col + half * p.q.No : 0;
+            const int wr = row_of(place);
             const RowReader<FMT> reader(p.w, t.e, wr, h);
             int ow = place * STEP + (4 * h ^ key(place)) * 8;        // where the first goes; the i-th at ow ^ 8 i
             asm("" : "+v"(ow));
@@ -893,8 +918,9 @@ __global__ __launch_bounds__(128 * WN) void k_tile(const TileArgs p)
     // write columns next to one another: 16 pieces of four floats a row, piece q at
     // q ^ row.  With a gate its columns come first, those of the up rows behind.
     meet(All{});
-    constexpr int HALVES = RM > 4 ? 2 : 1, ROWS = 16 * RM / HALVES;
-    static_assert(WAVES / 4 * ROWS * 256 <= (BM < BN ? BM : BN) * STEP * 2, "the waves' rooms lie in the four buffers");
+    constexpr int ROOM = (BM < BN ? BM : BN) * STEP * 2 / (WAVES / 4);          // bytes of a wave
+    constexpr int HALVES = 16 * RM * 256 > ROOM ? 2 : 1, ROWS = 16 * RM / HALVES;
+    static_assert(ROWS * 256 <= ROOM, "the waves' rooms lie in the four buffers");
     const int room = w * 4 / WAVES;       // a wave's, or two waves', of the four buffers
     uint16_t* const in = room == 0 ? sa0 : room == 1 ? sb0 : room == 2 ? sa1 : sb1;
     f32x4_t* stage = reinterpret_cast<f32x4_t*>(in) + w % (WAVES / 4) * (ROWS * 16);
@@ -942,13 +968,46 @@ __global__ __launch_bounds__(128 * WN) void k_tile(const TileArgs p)
 }
 
 // ---------------------------------------------------------------------------
+// many rows: the layer laid out as bf16 once, for k_tile<FMT_BF16>
+// ---------------------------------------------------------------------------
+// A wave decodes a packed tile of 16 rows x 128 k and turns it in LDS of its own,
+// so that it leaves in whole pieces of rows.  Bound by its writes.
+constexpr int ROWS_WAVES = 4;
+
+template <int FMT>
+__global__ __launch_bounds__(64 * ROWS_WAVES) void k_rows(const Layer layer, uint16_t* __restrict__ to)
+{
+    __shared__ u32x4_t room[ROWS_WAVES][16 * 16];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+    const int Kc = layer.K / 128, per = (Kc + ROWS_WAVES - 1) / ROWS_WAVES;
+    const int chunk = blockIdx.x % per * ROWS_WAVES + w, block = blockIdx.x / per;
+    if (chunk >= Kc)
+        return;
+    const int n = block * 16 + c < layer.N ? block * 16 + c : layer.N - 1;
+    uint32_t code[4], v[16];
+    fetch_codes<FMT>(layer.packed, n, Kc, chunk, g, code);
+    decode_in_order(ByteTable<FMT>(fetch_table<FMT>(layer.lut, layer.alpha, layer.beta, n, Kc, chunk, layer.g)), code, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        room[w][c * 16 + ((4 * g + i) ^ c)] = u32x4_t{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * i + g;
+        if (block * 16 + r < layer.N)
+            *reinterpret_cast<u32x4_t*>(to + static_cast<size_t>(block * 16 + r) * layer.K + chunk * 128 + 8 * c) = room[w][r * 16 + (c ^ r)];
+    }
+}
+
+// ---------------------------------------------------------------------------
 // the activation's backward pass
 // ---------------------------------------------------------------------------
 struct BwdArgs {
-    const uint16_t *dy, *z;
+    const void *dy, *z;
     uint16_t* dz;
     float* part;             // [slabs][N] or null: no bias
     int M, N, No, act, slab; // rows of a workgroup
+    int dy32, z32;           // fp32 instead of bf16
 };
 
 constexpr int BWD_COLS = 8 * WAVE;           // columns of out of a workgroup
@@ -968,26 +1027,24 @@ __global__ __launch_bounds__(256) void k_act_bwd(const BwdArgs p)
     for (int m = m0 + w; m < m1; m += 4) {
         if (valid <= 0)
             break;
-        const uint16_t* z = p.z + static_cast<size_t>(m) * p.N + col;
-        uint16_t* dz = p.dz + static_cast<size_t>(m) * p.N + col;
-        const u32x4_t dy = load8(p.dy + static_cast<size_t>(m) * p.No + col, valid), zg = load8(z, valid);
-        u32x4_t zu = {0u, 0u, 0u, 0u};
+        const size_t at = static_cast<size_t>(m) * p.N + col;
+        float d[8], zg[8], zu[8], a[8], b[8];
+        get_values(p.dy, p.dy32, static_cast<size_t>(m) * p.No + col, valid, d);
+        get_values(p.z, p.z32, at, valid, zg);
         if (gate)
-            zu = load8(z + p.No, valid);
-        float a[8], b[8];
+            get_values(p.z, p.z32, at + p.No, valid, zu);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float f, slope;
-            activate_both(half_of(zg, i), p.act, f, slope);
-            const float d = half_of(dy, i);
-            a[i] = gate ? d * half_of(zu, i) * slope : d * slope;
-            b[i] = d * f;
+            activate_both(zg[i], p.act, f, slope);
+            a[i] = gate ? d[i] * zu[i] * slope : d[i] * slope;
+            b[i] = d[i] * f;
             sum[0][i] += a[i];
             sum[1][i] += b[i];
         }
-        store8(dz, round8(a), valid);
+        put_values(p.dz, 0, at, valid, a);
         if (gate)
-            store8(dz + p.No, round8(b), valid);
+            put_values(p.dz, 0, at + p.No, valid, b);
     }
     if (!p.part)
         return;
@@ -1006,20 +1063,34 @@ __global__ __launch_bounds__(256) void k_act_bwd(const BwdArgs p)
     }
 }
 
+// The slabs' sums: 64 columns a workgroup, every wave a quarter of the slabs, eight
+// loads at a time (one thread a column: 18.6 us for 74 slabs of 28672).
 __global__ __launch_bounds__(256) void k_bias_sum(const float* __restrict__ part, float* __restrict__ dbias, int N, int slabs)
 {
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= N)
-        return;
+    __shared__ float red[4][WAVE];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = blockIdx.x * WAVE + lane;
     float v = 0.0f;
-    for (int s = 0; s < slabs; ++s)
-        v += part[static_cast<size_t>(s) * N + n];
-    dbias[n] = v;
+    if (n < N)
+        for (int s0 = w; s0 < slabs; s0 += 32) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = s0 + 4 * i < slabs ? part[static_cast<size_t>(s0 + 4 * i) * N + n] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v += x[i];
+        }
+    red[w][lane] = v;
+    __syncthreads();
+    if (w == 0 && n < N)
+        dbias[n] = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
 }
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+constexpr int64_t GIB2 = static_cast<int64_t>(1) << 31;
+
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 size_t layer_bytes(int fmt, int64_t N, int64_t K)
@@ -1027,10 +1098,11 @@ size_t layer_bytes(int fmt, int64_t N, int64_t K)
     return static_cast<size_t>((N + 15) / 16 * 16) * (K / 8) * (fmt == FMT_ANY2 ? 2 : fmt == FMT_ANY3 ? 3 : 4);
 }
 
-// How a product is run: the rows of a tile (0: k_few), its columns, tiles and splits.
+// How a product is run: the tile of k_tile (rm 0: k_few), its number and the splits.
 struct Shape {
     int rm, wn, S;
     int64_t tiles_m, tiles_n;
+    bool rows;               // the layer is laid out first
 };
 
 int64_t few_tiles(int64_t P, int64_t E, bool experts)
@@ -1042,47 +1114,92 @@ int64_t few_tiles(int64_t P, int64_t E, bool experts)
     return PlanLayout(P, E).TB * (TILE_T / FEW_T);
 }
 
+// What a step of 64 was measured to take, in units of 10 ns, of one workgroup that
+// has its CU to itself and for each of several (28672 x 4096, 4096 x 14336 and
+// 2048 x 2048, one layer of 16 to 4096 rows and 8 to 64 experts; forward, and turned).
+struct Form {
+    int rm, wn, one[2], more[2];
+};
+constexpr Form FORMS[] = {{8, 4, {190, 0}, {200, 0}}, {4, 2, {120, 140}, {71, 100}}, {2, 2, {88, 110}, {48, 63}}, {1, 2, {75, 100}, {38, 52}}};
+constexpr Form ROWS_FORM = {8, 4, {168, 0}, {180, 0}};
+// the same for a chunk of 128 of a wave of k_few, by its rows of x (up to 4, 8, 16)
+constexpr int FEW_TIME[3] = {195, 215, 300};
+
 // P rows through E experts (experts = false: one layer), D summed, C columns of the
-// product (both halves of a gate).
+// product (both halves of a gate).  Of the forms and splits the one with the least
+// time for the CU with the most workgroups, splits with their partial sums' bytes
+// and a launch.  Rows fall on experts at random: the last tile of an expert is on
+// average a quarter of a tile's work more than its rows.
 Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool turn)
 {
-    Shape s{0, 2, 1, 0, 0};
+    Shape s{0, 2, 1, 0, 0, false};
     const int64_t each = (P + E - 1) / E;        // rows of an expert, on average
     const int64_t live = experts ? (P < E ? P : E) : 1;
-    if (!turn && (experts ? P <= FEW_P || each <= 12 : P <= 16)) {
+    int64_t least = INT64_MAX;
+    auto better = [&](int64_t time, int rm, int wn, int64_t n, bool rows) {
+        time += n > 1 ? 400 + n * P * C / 8000 : 0;
+        if (time >= least)
+            return;
+        least = time;
+        s.rm = rm;
+        s.wn = wn;
+        s.S = static_cast<int>(n);
+        s.rows = rows;
+    };
+    if (!turn && (!experts || P <= FEW_P || each <= 64)) {
+        const int64_t chunks = D / 128;
+        const int rows = each <= 4 ? 0 : each <= 8 ? 1 : 2;
+        const int64_t row_tiles = experts ? live * (each < 8 ? 4 : each / 4 + 2) / 4 : (P + FEW_T - 1) / FEW_T;
+        const int64_t tiles = (C + FEW_ROWS - 1) / FEW_ROWS * row_tiles;
+        for (int64_t n = 1; n <= 8 && (n == 1 || chunks / n >= 8); n *= 2)
+            better((tiles * n + 255) / 256 * FEW_TIME[rows] * ((chunks + 8 * n - 1) / (8 * n)) + (n > 1 ? 250 : 0), 0, 2, n, false);
+    }
+    const int64_t steps = (D + STEP - 1) / STEP;
+    auto weigh = [&](const Form& f, int64_t before, bool rows) {
+        const int64_t bm = 32 * f.rm, bn = 64 * f.wn, tiles_n = (C + bn - 1) / bn;
+        // in quarters
+        const int64_t tiles_m = experts ? live * (4 * each < 3 * bm ? 4 : 4 * each / bm + 1) : 4 * ((P + bm - 1) / bm);
+        for (int64_t n = 1; n <= 8 && (n == 1 || steps / n >= 8); ++n) {
+            const int64_t tiles = tiles_m * tiles_n * n, on_cu = (tiles + 1023) / 1024 * 1024;
+            const int64_t all = (on_cu < 3 * 1024 ? on_cu : tiles + 512) * f.more[turn] / 1024;
+            better(before + (all > f.one[turn] ? all : f.one[turn]) * ((steps + n - 1) / n), f.rm, f.wn, n, rows);
+        }
+    };
+    if (turn || !experts || P > FEW_P)           // fewer pairs have no plan forward
+        for (const Form& f : FORMS)
+            if (f.one[turn])
+                weigh(f, 0, false);
+    if (!experts && !turn && C * D < GIB2 / 2)
+        weigh(ROWS_FORM, 300 + C * D / 22000, true);       // 2.5 bytes a weight at 5.5 TB/s
+    if (s.rm == 0) {
         s.tiles_m = few_tiles(P, E, experts);
         s.tiles_n = (C + FEW_ROWS - 1) / FEW_ROWS;
-        const int64_t groups = s.tiles_n * live, chunks = D / 128;
-        while (s.S < 8 && groups * s.S < 256 && chunks >= 8 * 2 * s.S)
-            s.S *= 2;
         return s;
-    }
-    if (each > 128 && C >= 1024) {
-        s.rm = 8;
-        s.wn = 4;
-    } else {
-        s.rm = each > 64 ? 4 : each > 32 ? 2 : 1;
     }
     const int64_t bm = 32 * s.rm, bn = 64 * s.wn;
     s.tiles_m = experts ? P / bm + (P < E + 1 ? P : E + 1) : (P + bm - 1) / bm;
     s.tiles_n = (C + bn - 1) / bn;
-    const int64_t groups = s.tiles_n * live * ((each + bm - 1) / bm), steps = (D + STEP - 1) / STEP;
-    while (s.S < 8 && groups * s.S <= 128 && steps >= 8 * s.S)
-        s.S *= 2;
     return s;
 }
 
-size_t part_bytes(const Shape& s, int64_t P, int64_t C) { return s.S > 1 ? up256(static_cast<size_t>(s.S) * P * C * 4) : 0; }
+size_t part_bytes(const Shape& s, int64_t P, int64_t C, int64_t D)
+{
+    return (s.S > 1 ? up256(static_cast<size_t>(s.S) * P * C * 4) : 0) + (s.rows ? up256(static_cast<size_t>(C) * D * 2) : 0);
+}
 
 template <int FMT, bool TURN>
 void launch_tile(const Shape& s, const TileArgs& a, hipStream_t stream)
 {
     const dim3 grid(static_cast<unsigned>((s.tiles_m * s.tiles_n + 7) / 8 * 8), static_cast<unsigned>(s.S));
 #define TILE(WN_, RM_) hipLaunchKernelGGL((k_tile<FMT, WN_, RM_, TURN>), grid, dim3(128 * WN_), 0, stream, a)
-    if (s.rm == 8) TILE(4, 8);
-    else if (s.rm == 4) TILE(2, 4);
-    else if (s.rm == 2) TILE(2, 2);
-    else TILE(2, 1);
+    if constexpr (FMT == FMT_BF16) {
+        TILE(4, 8);
+    } else {
+        if (s.rm == 4) TILE(2, 4);
+        else if (s.rm == 2) TILE(2, 2);
+        else if (s.rm == 1) TILE(2, 1);
+        else if constexpr (!TURN) TILE(4, 8);
+    }
 #undef TILE
 }
 
@@ -1107,8 +1224,6 @@ void launch_few(int fmt, const Shape& s, const FewArgs& a, hipStream_t stream)
 #undef FEW
 }
 
-constexpr int64_t GIB2 = static_cast<int64_t>(1) << 31;
-
 bool act_ok(int act) { return act >= 0 && act < ACTS; }
 bool fmt_ok(int fmt) { return fmt >= FMT_ANY4 && fmt <= FMT_ANY3; }
 
@@ -1127,7 +1242,7 @@ any4_status product(int fmt, const Rows& rows, int64_t X, const uint16_t* x, con
     Rows r = rows;
     Epilogue e = q;
     e.S = s.S;
-    size_t need = part_bytes(s, r.P, w.N);
+    const size_t need = part_bytes(s, r.P, w.N, w.K);
     if (experts && r.P <= FEW_P) {
         r.plan = nullptr;
         r.ids = ids;
@@ -1148,6 +1263,20 @@ any4_status product(int fmt, const Rows& rows, int64_t X, const uint16_t* x, con
         e.part = reinterpret_cast<float*>(at);
     if (s.rm == 0) {
         launch_few(fmt, s, FewArgs{r, w, x, e}, stream);
+    } else if (s.rows) {
+        uint16_t* rows = reinterpret_cast<uint16_t*>(at + (s.S > 1 ? up256(static_cast<size_t>(s.S) * r.P * w.N * 4) : 0));
+        const int Kc = w.K / 128;
+        const dim3 grid(static_cast<unsigned>((w.N + 15) / 16) * ((Kc + ROWS_WAVES - 1) / ROWS_WAVES));
+#define LAY_OUT(FMT_) hipLaunchKernelGGL(k_rows<FMT_>, grid, dim3(64 * ROWS_WAVES), 0, stream, w, rows)
+        if (fmt == FMT_ANY4) LAY_OUT(FMT_ANY4);
+        else if (fmt == FMT_INT4) LAY_OUT(FMT_INT4);
+        else if (fmt == FMT_ANY2) LAY_OUT(FMT_ANY2);
+        else LAY_OUT(FMT_ANY3);
+#undef LAY_OUT
+        Layer laid = w;
+        laid.packed = reinterpret_cast<const uint8_t*>(rows);
+        launch_tile<FMT_BF16, false>(s, TileArgs{r, laid, x, e, static_cast<int>(X), w.K, w.K / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
+                                     stream);
     } else {
         r.ids = nullptr;
         launch_tile<false>(fmt, s, TileArgs{r, w, x, e, static_cast<int>(X), w.K, w.K / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
@@ -1177,11 +1306,11 @@ size_t any4_gemm_act_workspace_size(int64_t M, int64_t N, int64_t K, int64_t g)
 {
     if (M <= 0 || N <= 0 || !sizes_ok(M, M, 1, N, K, g))
         return 0;
-    return part_bytes(shape_of(M, 1, false, K, N, false), M, N);
+    return part_bytes(shape_of(M, 1, false, K, N, false), M, N, K);
 }
 
 any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* packed, const uint16_t* lut, const uint16_t* alpha,
-                          const uint16_t* beta, const uint16_t* bias, const uint16_t* residual, uint16_t* z, uint16_t* out,
+                          const uint16_t* beta, const uint16_t* bias, const uint16_t* residual, void* z, int z_f32, void* out, int out_f32,
                           any4_activation act, int gate, int64_t M, int64_t N, int64_t K, int64_t g, void* workspace,
                           size_t workspace_bytes, hipStream_t stream)
 {
@@ -1193,11 +1322,12 @@ any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* 
     if (!x || !packed || (fmt != FMT_INT4 && !lut) || !alpha || !beta || !out)
         return ANY4_E_NULL;
     if (!is_aligned(x, 16) || !is_aligned(packed, 16) || !is_aligned(lut, 2) || !is_aligned(alpha, 2) || !is_aligned(beta, 2) ||
-        !is_aligned(bias, 2) || !is_aligned(residual, 2) || !is_aligned(z, 2) || !is_aligned(out, 2) || !is_aligned(workspace, 16))
+        !is_aligned(bias, 2) || !is_aligned(residual, 2) || !is_aligned(z, z_f32 ? 4 : 2) || !is_aligned(out, out_f32 ? 4 : 2) || !is_aligned(workspace, 16))
         return ANY4_E_ALIGN;
     (void)hipGetLastError();
     const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
-    const Epilogue q{bias, residual, z, out, nullptr, static_cast<int>(N), static_cast<int>(gate ? N / 2 : N), static_cast<int>(act), 1};
+    const Epilogue q{bias, residual, z, out, nullptr, static_cast<int>(N), static_cast<int>(gate ? N / 2 : N), static_cast<int>(act), 1,
+                     z_f32 != 0, out_f32 != 0};
     return product(fmt, Rows{nullptr, nullptr, static_cast<int>(M), 1, 1}, M, x, w, q, nullptr, workspace, workspace_bytes, false, stream);
 }
 
@@ -1209,8 +1339,8 @@ size_t any4_act_backward_workspace_size(int64_t M, int64_t N, int gate)
     return up256(static_cast<size_t>(slabs) * N * 4);
 }
 
-any4_status any4_act_backward(const uint16_t* dy, const uint16_t* z, uint16_t* dz, float* dbias, any4_activation act, int gate,
-                              int64_t M, int64_t N, void* workspace, size_t workspace_bytes, hipStream_t stream)
+any4_status any4_act_backward(const void* dy, int dy_f32, const void* z, int z_f32, uint16_t* dz, float* dbias, any4_activation act,
+                              int gate, int64_t M, int64_t N, void* workspace, size_t workspace_bytes, hipStream_t stream)
 {
     if (!act_ok(act) || M < 0 || M > MAX_PAIRS || N < 0 || N >= GIB2 / 2 || (M > 0 && N >= GIB2 / 2 / M) || (gate && N % 2))
         return ANY4_E_SHAPE;
@@ -1218,7 +1348,7 @@ any4_status any4_act_backward(const uint16_t* dy, const uint16_t* z, uint16_t* d
         return ANY4_OK;
     if (M > 0 && (!dy || !z || !dz || (dbias && !workspace)))
         return ANY4_E_NULL;
-    if (!is_aligned(dbias, 4) || (M > 0 && (!is_aligned(dy, 2) || !is_aligned(z, 2) || !is_aligned(dz, 2) || !is_aligned(workspace, 16))))
+    if (!is_aligned(dbias, 4) || (M > 0 && (!is_aligned(dy, dy_f32 ? 4 : 2) || !is_aligned(z, z_f32 ? 4 : 2) || !is_aligned(dz, 2) || !is_aligned(workspace, 16))))
         return ANY4_E_ALIGN;
     const int n = static_cast<int>(N), no = static_cast<int>(gate ? N / 2 : N);
     const int slab = M > 0 ? static_cast<int>(bwd_slab(M, no)) : 1, slabs = static_cast<int>((M + slab - 1) / slab);
@@ -1228,9 +1358,10 @@ any4_status any4_act_backward(const uint16_t* dy, const uint16_t* z, uint16_t* d
     float* part = dbias ? static_cast<float*>(workspace) : nullptr;
     if (M > 0)
         hipLaunchKernelGGL(k_act_bwd, dim3(static_cast<unsigned>((no + BWD_COLS - 1) / BWD_COLS), static_cast<unsigned>(slabs)), dim3(256), 0,
-                           stream, BwdArgs{dy, z, dz, part, static_cast<int>(M), n, no, static_cast<int>(act), slab});
+                           stream, BwdArgs{dy, z, dz, part, static_cast<int>(M), n, no, static_cast<int>(act), slab,
+                                   dy_f32 != 0, z_f32 != 0});
     if (dbias)
-        hipLaunchKernelGGL(k_bias_sum, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, part, dbias, n, slabs);
+        hipLaunchKernelGGL(k_bias_sum, dim3(static_cast<unsigned>((n + WAVE - 1) / WAVE)), dim3(256), 0, stream, part, dbias, n, slabs);
     return launch_status();
 }
 
@@ -1239,12 +1370,12 @@ size_t any4_experts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, i
     if (T <= 0 || k <= 0 || N <= 0 || T > MAX_PAIRS || k > MAX_PAIRS || !sizes_ok(T * k, T * k, E, N, K, g))
         return 0;
     const int64_t P = T * k;
-    return part_bytes(shape_of(P, E, true, K, N, false), P, N) + (P <= FEW_P ? 0 : any4_lora_plan_bytes(P, E));
+    return part_bytes(shape_of(P, E, true, K, N, false), P, N, K) + (P <= FEW_P ? 0 : any4_lora_plan_bytes(P, E));
 }
 
 any4_status any4_experts_gemm(any4_format format, const uint16_t* x, int per_pair, const uint8_t* packed, const uint16_t* lut,
                               const uint16_t* alpha, const uint16_t* beta, const uint16_t* bias, const int32_t* ids, const void* plan,
-                              uint16_t* z, uint16_t* out, any4_activation act, int gate, int64_t T, int64_t k, int64_t E, int64_t N,
+                              void* z, int z_f32, void* out, int out_f32, any4_activation act, int gate, int64_t T, int64_t k, int64_t E, int64_t N,
                               int64_t K, int64_t g, void* workspace, size_t workspace_bytes, hipStream_t stream)
 {
     const int fmt = static_cast<int>(format);
@@ -1256,12 +1387,13 @@ any4_status any4_experts_gemm(any4_format format, const uint16_t* x, int per_pai
     if (!x || !packed || (fmt != FMT_INT4 && !lut) || !alpha || !beta || !ids || !out)
         return ANY4_E_NULL;
     if (!is_aligned(x, 16) || !is_aligned(packed, 16) || !is_aligned(lut, 2) || !is_aligned(alpha, 2) || !is_aligned(beta, 2) ||
-        !is_aligned(bias, 2) || !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(z, 2) || !is_aligned(out, 2) ||
+        !is_aligned(bias, 2) || !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(z, z_f32 ? 4 : 2) || !is_aligned(out, out_f32 ? 4 : 2) ||
         !is_aligned(workspace, 16))
         return ANY4_E_ALIGN;
     (void)hipGetLastError();
     const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
-    const Epilogue q{bias, nullptr, z, out, nullptr, static_cast<int>(N), static_cast<int>(gate ? N / 2 : N), static_cast<int>(act), 1};
+    const Epilogue q{bias, nullptr, z, out, nullptr, static_cast<int>(N), static_cast<int>(gate ? N / 2 : N), static_cast<int>(act), 1,
+                     z_f32 != 0, out_f32 != 0};
     const Rows r{nullptr, static_cast<const int*>(plan), static_cast<int>(T * k), static_cast<int>(E), per_pair ? 1 : static_cast<int>(k)};
     return product(fmt, r, per_pair ? T * k : T, x, w, q, ids, workspace, workspace_bytes, true, stream);
 }
@@ -1271,13 +1403,13 @@ size_t any4_experts_dx_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N
     if (T <= 0 || k <= 0 || N <= 0 || T > MAX_PAIRS || k > MAX_PAIRS || !sizes_ok(T * k, T * k, E, (N + 7) / 8 * 8, K, g))
         return 0;
     const int64_t P = T * k;
-    return part_bytes(shape_of(P, E, true, N, K, true), P, K) + any4_lora_plan_bytes(P, E) +
+    return part_bytes(shape_of(P, E, true, N, K, true), P, K, N) + any4_lora_plan_bytes(P, E) +
            up256(static_cast<size_t>(P) * ((N + 7) / 8 * 8) * 2);
 }
 
 any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const uint8_t* packed, const uint16_t* lut,
-                                 const uint16_t* alpha, const uint16_t* beta, const int32_t* ids, const void* plan, uint16_t* dx,
-                                 int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
+                                 const uint16_t* alpha, const uint16_t* beta, const int32_t* ids, const void* plan, void* dx,
+                                 int dx_f32, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream)
 {
     const int fmt = static_cast<int>(format);
@@ -1289,7 +1421,7 @@ any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const u
     if (!dy || !packed || (fmt != FMT_INT4 && !lut) || !alpha || !beta || !ids || !dx || !workspace)
         return ANY4_E_NULL;
     if (!is_aligned(dy, 2) || !is_aligned(packed, 16) || !is_aligned(lut, 2) || !is_aligned(alpha, 2) || !is_aligned(beta, 2) ||
-        !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(dx, 2) || !is_aligned(workspace, 16))
+        !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(dx, dx_f32 ? 4 : 2) || !is_aligned(workspace, 16))
         return ANY4_E_ALIGN;
     if (workspace_bytes < any4_experts_dx_workspace_size(T, k, E, N, K, g))
         return ANY4_E_WORKSPACE;
@@ -1314,7 +1446,7 @@ any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const u
     at += up256(static_cast<size_t>(P) * Np * 2);
     const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
     const Epilogue q{nullptr, nullptr, nullptr, dx, s.S > 1 ? reinterpret_cast<float*>(at) : nullptr, static_cast<int>(K),
-                     static_cast<int>(K), ACT_NONE, s.S};
+                     static_cast<int>(K), ACT_NONE, s.S, 0, dx_f32 != 0};
     const Rows r{nullptr, static_cast<const int*>(plan), P, static_cast<int>(E), 1};
     launch_tile<true>(fmt, s, TileArgs{r, w, dy, q, P, Np, (Np + STEP - 1) / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
                       stream);

@@ -219,6 +219,62 @@ __device__ __forceinline__ Split3 split3(const float (&f)[8])
              __builtin_bit_cast(bf16x8_t, lo)}};
 }
 
+// Values that are kept in bf16 or in fp32 (f32): eight of a row at `at` on, of which the
+// first `valid` (any integer) are in the row.
+__device__ __forceinline__ void get_values(const void* p, int f32, size_t at, int valid, float (&v)[8])
+{
+    if (f32) {
+        const float* q = static_cast<const float*>(p) + at;
+        if (valid >= 8) {
+            const f32x4_t a = *reinterpret_cast<const f32x4_a4_t*>(q), b = *reinterpret_cast<const f32x4_a4_t*>(q + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = a[i];
+                v[4 + i] = b[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = i < valid ? q[i] : 0.0f;
+        }
+        return;
+    }
+    const u32x4_t x = load8(static_cast<const uint16_t*>(p) + at, valid);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = bf16_to_f32(x[i / 2] >> (16 * (i & 1)) & 0xffffu);
+}
+
+__device__ __forceinline__ void put_values(void* p, int f32, size_t at, int valid, const float (&v)[8])
+{
+    if (f32) {
+        float* q = static_cast<float*>(p) + at;
+        if (valid >= 8) {
+            *reinterpret_cast<f32x4_a4_t*>(q) = f32x4_t{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<f32x4_a4_t*>(q + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < valid)
+                    q[i] = v[i];
+        }
+        return;
+    }
+    u32x4_t o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = f32_to_bf16(v[2 * i]) | f32_to_bf16(v[2 * i + 1]) << 16;
+    store8(static_cast<uint16_t*>(p) + at, o, valid);
+}
+
+__device__ __forceinline__ void put_value(void* p, int f32, size_t at, float v)
+{
+    if (f32)
+        static_cast<float*>(p)[at] = v;
+    else
+        static_cast<uint16_t*>(p)[at] = static_cast<uint16_t>(f32_to_bf16(v));
+}
+
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 inline any4_status launch_status() { return hipGetLastError() == hipSuccess ? ANY4_OK : ANY4_E_HIP; }

@@ -22,24 +22,59 @@ __device__ __forceinline__ float logit_at(const void* logits, int bf16, size_t i
     return l != l ? -INFINITY : fminf(l, 3.4028234663852886e38f);
 }
 
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v)
+// A value from another lane by DPP (0 where there is none): rows of 16 shifted, then
+// the last lane of a row to the next row and of 32 lanes to the rest.
+template <int CTRL, int ROW_MASK, typename T>
+__device__ __forceinline__ T moved(T v, T otherwise)
 {
-#pragma unroll
-    for (int d = 1; d < WAVE; d <<= 1)
-        v += __shfl_xor(v, d);
-    return v;
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, otherwise), __builtin_bit_cast(int, v), CTRL, ROW_MASK, 0xf, false));
+    } else {
+        const u32x2_t a = __builtin_bit_cast(u32x2_t, v), o = __builtin_bit_cast(u32x2_t, otherwise);
+        const u32x2_t r = {static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(o[0]), static_cast<int>(a[0]), CTRL, ROW_MASK, 0xf, false)),
+                           static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(o[1]), static_cast<int>(a[1]), CTRL, ROW_MASK, 0xf, false))};
+        return __builtin_bit_cast(T, r);
+    }
 }
 
 template <typename T>
-__device__ __forceinline__ T wave_max(T v)
+__device__ __forceinline__ T from_lane(T v, int lane)
 {
-#pragma unroll
-    for (int d = 1; d < WAVE; d <<= 1) {
-        const T o = __shfl_xor(v, d);
-        v = o > v ? o : v;
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+    } else {
+        const u32x2_t a = __builtin_bit_cast(u32x2_t, v);
+        const u32x2_t r = {static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(a[0]), lane)),
+                           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(a[1]), lane))};
+        return __builtin_bit_cast(T, r);
     }
-    return v;
+}
+
+// Over the wave's 64 lanes, the same for all: each lane joins with ever farther ones
+// before it, and lane 63 has them all (a shuffle through LDS takes several times a
+// DPP move's time, and routing is a chain of these).
+template <typename T, typename F>
+__device__ __forceinline__ T wave_reduce(T v, T none, F join)
+{
+    v = join(v, moved<0x111, 0xf>(v, none));     // row_shr 1, 2, 4, 8
+    v = join(v, moved<0x112, 0xf>(v, none));
+    v = join(v, moved<0x114, 0xf>(v, none));
+    v = join(v, moved<0x118, 0xf>(v, none));
+    v = join(v, moved<0x142, 0xa>(v, none));     // row_bcast 15 to rows 1 and 3
+    v = join(v, moved<0x143, 0xc>(v, none));     // row_bcast 31 to rows 2 and 3
+    return from_lane(v, 63);
+}
+
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v)
+{
+    return wave_reduce(v, static_cast<T>(0), [](T a, T b) { return a + b; });
+}
+
+template <typename T>
+__device__ __forceinline__ T wave_max(T v)       // no NaN
+{
+    return wave_reduce(v, static_cast<T>(-INFINITY), [](T a, T b) { return a > b ? a : b; });
 }
 
 struct RouteArgs {
@@ -110,7 +145,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void k_route(const RouteArgs p)
             }
             int before = 0;
             for (int g = 0; g < p.groups; ++g) {
-                const double o = __shfl(score, g);
+                const double o = from_lane(score, g);
                 before += o > score || (o == score && g < lane);
             }
             const uint64_t kept = __ballot(lane < p.groups && before < p.top_groups);
@@ -130,40 +165,34 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void k_route(const RouteArgs p)
         for (int v = 0; v < V; ++v)
             rank[v] = l[v];
     }
-    // the k of largest rank, one after another; lane j keeps the j-th
+    // the k of largest rank, one after another; lane j keeps the j-th.  Experts of one v
+    // come before those of the next, lanes in order: the lowest index first.
     int mine = -1;
     float logit = -INFINITY;
     for (int j = 0; j < p.k; ++j) {
-        Rank best = -INFINITY;
-        float its = -INFINITY;
-        int at = MAX_EXPERTS;
+        Rank best = rank[0];
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (rank[v] > best) {
-                best = rank[v];
-                its = l[v];
-                at = lane + 64 * v;
-            }
-#pragma unroll
-        for (int d = 1; d < WAVE; d <<= 1) {
-            const Rank o = __shfl_xor(best, d);
-            const int o_at = __shfl_xor(at, d);
-            const float o_its = __shfl_xor(its, d);
-            const bool take = o > best || (o == best && o_at < at);
-            best = take ? o : best;
-            at = take ? o_at : at;
-            its = take ? o_its : its;
-        }
-        if (at == MAX_EXPERTS)
+        for (int v = 1; v < V; ++v)
+            best = rank[v] > best ? rank[v] : best;
+        best = wave_max(best);
+        if (best == -INFINITY)
             break;
-        if (lane == j) {
-            mine = at;
-            logit = its;
-        }
+        bool found = false;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (lane + 64 * v == at)
-                rank[v] = -INFINITY;
+        for (int v = 0; v < V; ++v) {
+            const uint64_t hit = __ballot(rank[v] == best);
+            if (!found && hit) {
+                found = true;
+                const int at = __builtin_ctzll(hit);
+                const float its = from_lane(l[v], at);
+                if (lane == j) {
+                    mine = at + 64 * v;
+                    logit = its;
+                }
+                if (lane == at)
+                    rank[v] = -INFINITY;
+            }
+        }
     }
     double s;
     if (p.score == SCORE_SIGMOID)
@@ -253,8 +282,8 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void k_route_bwd(const RouteBwdAr
         const int e = lane + 64 * v;
         double d = 0.0;
         for (int j = 0; j < p.k; ++j) {
-            const int at = __builtin_amdgcn_readlane(id, j);
-            const double o = __shfl(own, j);
+            const int at = from_lane(id, j);
+            const double o = from_lane(own, j);
             d += at == e ? o : 0.0;
         }
         if (all)
@@ -272,24 +301,14 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void k_route_bwd(const RouteBwdAr
 // ---------------------------------------------------------------------------
 // the weighted sum
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float half_of(const u32x4_t& v, int i) { return bf16_to_f32(v[i / 2] >> (16 * (i & 1)) & 0xffffu); }
-
-__device__ __forceinline__ u32x4_t round8(const float (&v)[8])
-{
-    u32x4_t o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        o[i] = f32_to_bf16(v[2 * i]) | f32_to_bf16(v[2 * i + 1]) << 16;
-    return o;
-}
-
 struct CombineArgs {
-    const uint16_t* y;
+    const void* y;
     const float* w;
     const uint16_t* residual;
     uint16_t* out;
     int k, N, per;           // pieces of eight columns a row
     size_t pieces;
+    int y32;                 // y in fp32 instead of bf16
 };
 
 // Eight columns of a token a thread, eight pairs' loads at a time; bound by its bytes.
@@ -301,21 +320,19 @@ __global__ __launch_bounds__(256) void k_combine(const CombineArgs p)
     const size_t t = i / p.per;
     const int col = static_cast<int>(i % p.per) * 8, valid = p.N - col;
     float s[8];
-    u32x4_t r = {0u, 0u, 0u, 0u};
-    if (p.residual)
-        r = load8(p.residual + t * p.N + col, valid);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        s[e] = half_of(r, e);
-    const uint16_t* y = p.y + t * p.k * p.N + col;
+        s[e] = 0.0f;
+    if (p.residual)
+        get_values(p.residual, 0, t * p.N + col, valid, s);
+    const size_t y = t * p.k * p.N + col;
     const float* w = p.w ? p.w + t * p.k : nullptr;
     for (int j0 = 0; j0 < p.k; j0 += 8) {
-        u32x4_t v[8];
-        float f[8];
+        float v[8][8], f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (j0 + j < p.k) {
-                v[j] = load8(y + static_cast<size_t>(j0 + j) * p.N, valid);
+                get_values(p.y, p.y32, y + static_cast<size_t>(j0 + j) * p.N, valid, v[j]);
                 f[j] = w ? w[j0 + j] : 1.0f;
             }
 #pragma unroll
@@ -323,17 +340,19 @@ __global__ __launch_bounds__(256) void k_combine(const CombineArgs p)
             if (j0 + j < p.k)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    s[e] = fmaf(f[j], half_of(v[j], e), s[e]);
+                    s[e] = fmaf(f[j], v[j][e], s[e]);
     }
-    store8(p.out + t * p.N + col, round8(s), valid);
+    put_values(p.out, 0, t * p.N + col, valid, s);
 }
 
 struct CombineBwdArgs {
-    const uint16_t *dout, *y;
+    const uint16_t* dout;
+    const void* y;
     const float* w;
     uint16_t* dy;
     float* dw;
     int k, N;
+    int y32;                 // y in fp32 instead of bf16
 };
 
 // A workgroup a token, 2048 columns a round; the sums of up to eight pairs at a time.
@@ -352,13 +371,13 @@ __global__ __launch_bounds__(256) void k_combine_bwd(const CombineBwdArgs p)
         }
         for (int col = threadIdx.x * 8; col < p.N; col += 2048) {
             const int valid = p.N - col;
-            const u32x4_t d = load8(dout + col, valid);
-            u32x4_t v[8];
+            float d[8], v[8][8];
+            get_values(dout, 0, col, valid, d);
             if (p.dw)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (j0 + j < p.k)
-                        v[j] = load8(p.y + (t * p.k + j0 + j) * p.N + col, valid);
+                        get_values(p.y, p.y32, (t * p.k + j0 + j) * p.N + col, valid, v[j]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 if (j0 + j >= p.k)
@@ -366,13 +385,13 @@ __global__ __launch_bounds__(256) void k_combine_bwd(const CombineBwdArgs p)
                 if (p.dw)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        sum[j] = fmaf(half_of(d, e), half_of(v[j], e), sum[j]);
+                        sum[j] = fmaf(d[e], v[j][e], sum[j]);
                 if (p.dy) {
                     float o[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        o[e] = f[j] * half_of(d, e);
-                    store8(p.dy + (t * p.k + j0 + j) * p.N + col, round8(o), valid);
+                        o[e] = f[j] * d[e];
+                    put_values(p.dy, 0, (t * p.k + j0 + j) * p.N + col, valid, o);
                 }
             }
         }
@@ -472,7 +491,7 @@ any4_status any4_route_backward(const float* dw, const void* logits, int logits_
     return launch_status();
 }
 
-any4_status any4_combine(const uint16_t* y, const float* w, const uint16_t* residual, uint16_t* out, int64_t T, int64_t k, int64_t N,
+any4_status any4_combine(const void* y, int y_f32, const float* w, const uint16_t* residual, uint16_t* out, int64_t T, int64_t k, int64_t N,
                          hipStream_t stream)
 {
     if (!combine_ok(T, k, N))
@@ -481,17 +500,17 @@ any4_status any4_combine(const uint16_t* y, const float* w, const uint16_t* resi
         return ANY4_OK;
     if (!y || !out)
         return ANY4_E_NULL;
-    if (!is_aligned(y, 2) || !is_aligned(w, 4) || !is_aligned(residual, 2) || !is_aligned(out, 2))
+    if (!is_aligned(y, y_f32 ? 4 : 2) || !is_aligned(w, 4) || !is_aligned(residual, 2) || !is_aligned(out, 2))
         return ANY4_E_ALIGN;
     (void)hipGetLastError();
     const int per = static_cast<int>((N + 7) / 8);
     const size_t pieces = static_cast<size_t>(T) * per;
     hipLaunchKernelGGL(k_combine, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream,
-                       CombineArgs{y, w, residual, out, static_cast<int>(k), static_cast<int>(N), per, pieces});
+                       CombineArgs{y, w, residual, out, static_cast<int>(k), static_cast<int>(N), per, pieces, y_f32 != 0});
     return launch_status();
 }
 
-any4_status any4_combine_backward(const uint16_t* dout, const uint16_t* y, const float* w, uint16_t* dy, float* dw, int64_t T, int64_t k,
+any4_status any4_combine_backward(const uint16_t* dout, const void* y, int y_f32, const float* w, uint16_t* dy, float* dw, int64_t T, int64_t k,
                                   int64_t N, hipStream_t stream)
 {
     if (!combine_ok(T, k, N))
@@ -500,11 +519,11 @@ any4_status any4_combine_backward(const uint16_t* dout, const uint16_t* y, const
         return ANY4_OK;
     if (!w || (N > 0 && (!dout || (dw && !y))))
         return ANY4_E_NULL;
-    if (!is_aligned(dout, 2) || !is_aligned(y, 2) || !is_aligned(w, 4) || !is_aligned(dy, 2) || !is_aligned(dw, 4))
+    if (!is_aligned(dout, 2) || !is_aligned(y, y_f32 ? 4 : 2) || !is_aligned(w, 4) || !is_aligned(dy, 2) || !is_aligned(dw, 4))
         return ANY4_E_ALIGN;
     (void)hipGetLastError();
     hipLaunchKernelGGL(k_combine_bwd, dim3(static_cast<unsigned>(T)), dim3(256), 0, stream,
-                       CombineBwdArgs{dout, y, w, dy, dw, static_cast<int>(k), static_cast<int>(N)});
+                       CombineBwdArgs{dout, y, w, dy, dw, static_cast<int>(k), static_cast<int>(N), y_f32 != 0});
     return launch_status();
 }
 

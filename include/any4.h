@@ -505,7 +505,10 @@ any4_status any3_gemm_dx(const uint16_t* dy, const uint8_t* packed, const uint16
 /*
  * The feed-forward block around a quantised layer, dense or of many experts:
  * bias, activation, gate and residual in the product's epilogue, a router, the
- * experts' products and the sum that the router weights.
+ * experts' products and the sum that the router weights.  What lies between two of
+ * these calls (z, an output that any4_combine or any4_act_backward reads, an input's
+ * gradient) is bf16, or where the argument behind it (z_f32, out_f32, ..) is not 0 fp32, in
+ * the same shape and with an alignment of 4: then it is not rounded in between.
  */
 typedef enum any4_format {
     ANY4_FORMAT_ANY4 = 0, /* any4_pack, lut of 16 entries              */
@@ -529,13 +532,13 @@ typedef enum any4_activation {
  * or with gate != 0, the layer's N rows being [gate; up] of N/2 each:
  *     out[m][n] = bf16_rne( act(zf[m][n]) * zf[m][N/2 + n] + residual[m][n] ),  n < N/2
  * The weights are exactly the any4_dequant values, products are exact and sums
- * fp32, nothing is rounded in between.  z, where asked for, is bf16_rne(zf): what
- * any4_act_backward needs.  Non-finite z give what the formulas give (act(-inf)
+ * fp32, nothing is rounded in between.  z, where asked for, is bf16_rne(zf) (or zf itself):
+ * what any4_act_backward needs.  Non-finite z give what the formulas give (act(-inf)
  * may be NaN).  Deterministic; a row's result depends on no other row's values.
  *   x         device, [M][K] bf16      bias  device, [N] bf16, or NULL
- *   residual  device, [M][No] bf16, or NULL; may be out itself (No = N, gated N/2)
- *   z         device, [M][N] bf16, written; or NULL
- *   out       device, [M][No] bf16, written
+ *   residual  device, [M][No] bf16, or NULL; may be out itself where that is bf16 (No = N, gated N/2)
+ *   z         device, [M][N] bf16 or fp32, written; or NULL
+ *   out       device, [M][No] bf16 or fp32, written
  *   packed, lut, alpha, beta  as for the format's dequantisation.
  *   0 <= M <= 2^20, N >= 0 (even with a gate), K a positive multiple of 128, g as for
  *   any4_gemm (K/g is not limited); M*N and M*K below 2^30, N*K below 2^32.
@@ -550,8 +553,8 @@ typedef enum any4_activation {
 size_t any4_gemm_act_workspace_size(int64_t M, int64_t N, int64_t K, int64_t g);
 any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* packed, const uint16_t* lut,
                           const uint16_t* alpha, const uint16_t* beta, const uint16_t* bias,
-                          const uint16_t* residual, uint16_t* z, uint16_t* out, any4_activation act,
-                          int gate, int64_t M, int64_t N, int64_t K, int64_t g, void* workspace,
+                          const uint16_t* residual, void* z, int z_f32, void* out, int out_f32,
+                          any4_activation act, int gate, int64_t M, int64_t N, int64_t K, int64_t g, void* workspace,
                           size_t workspace_bytes, hipStream_t stream);
 
 /*
@@ -563,7 +566,8 @@ any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* 
  *     dbias[n] = sum_m of the same values before their rounding     (fp32)
  * act' of ANY4_ACT_RELU is 0 at 0.  The gradient of x is any4_gemm_dx of dz, that of the
  * residual dy itself.
- *   dy  device, [M][No] bf16    z, dz  device, [M][N] bf16 (dz may be z itself)
+ *   dy  device, [M][No] bf16 or fp32    z  device, [M][N] bf16 or fp32
+ *   dz  device, [M][N] bf16, written (may be z itself where that is bf16)
  *   dbias  device, [N] fp32, or NULL (workspace is then not used)
  *   0 <= M <= 2^20, N >= 0, M*N below 2^30.  M = 0 writes dbias = 0.
  *   workspace  device, 16-byte aligned, any4_act_backward_workspace_size(M, N, gate)
@@ -572,8 +576,8 @@ any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* 
  * Errors: as any4_gemm_act.
  */
 size_t any4_act_backward_workspace_size(int64_t M, int64_t N, int gate);
-any4_status any4_act_backward(const uint16_t* dy, const uint16_t* z, uint16_t* dz, float* dbias,
-                              any4_activation act, int gate, int64_t M, int64_t N, void* workspace,
+any4_status any4_act_backward(const void* dy, int dy_f32, const void* z, int z_f32, uint16_t* dz,
+                              float* dbias, any4_activation act, int gate, int64_t M, int64_t N, void* workspace,
                               size_t workspace_bytes, hipStream_t stream);
 
 /*
@@ -629,7 +633,8 @@ any4_status any4_route_backward(const float* dw, const void* logits, int logits_
  *           products of a block; or NULL (made in the workspace; up to 64 pairs
  *           need none and ignore it).  A plan that any4_lora_plan made for other sizes
  *           leaves the outputs unwritten.
- *   z       device, [T*k][N] bf16, written; or NULL      out  device, [T*k][No] bf16, written
+ *   z       device, [T*k][N] bf16 or fp32, written; or NULL
+ *   out     device, [T*k][No] bf16 or fp32, written
  *   0 <= T*k <= 2^20, 1 <= E <= 1024, the other sizes as any4_gemm_act for M = T*k; the
  *   stacked arrays may be of any size.  T = 0 and N = 0 are no-ops.
  *   workspace  as for any4_gemm_act, any4_experts_workspace_size(T, k, E, N, K, g) bytes
@@ -640,8 +645,8 @@ any4_status any4_route_backward(const float* dw, const void* logits, int logits_
 size_t any4_experts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g);
 any4_status any4_experts_gemm(any4_format format, const uint16_t* x, int per_pair, const uint8_t* packed,
                               const uint16_t* lut, const uint16_t* alpha, const uint16_t* beta,
-                              const uint16_t* bias, const int32_t* ids, const void* plan, uint16_t* z,
-                              uint16_t* out, any4_activation act, int gate, int64_t T, int64_t k,
+                              const uint16_t* bias, const int32_t* ids, const void* plan, void* z,
+                              int z_f32, void* out, int out_f32, any4_activation act, int gate, int64_t T, int64_t k,
                               int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
                               size_t workspace_bytes, hipStream_t stream);
 
@@ -651,7 +656,7 @@ any4_status any4_experts_gemm(any4_format format, const uint16_t* x, int per_pai
  * A pair whose id is not in 0..E-1 gives zeros.  (The gradient of an x that k
  * pairs share is the sum of theirs: any4_combine without weights.)
  *   dy  device, [T*k][N] bf16 (read in place if 16-byte aligned and N % 8 == 0, else
- *       through a padded copy)      dx  device, [T*k][K] bf16, written
+ *       through a padded copy)      dx  device, [T*k][K] bf16 or fp32, written
  *   N >= 1; sizes, ids, plan and errors as any4_experts_gemm (here N is taken
  *   rounded up to a multiple of 8).
  *   workspace  device, any4_experts_dx_workspace_size(T, k, E, N, K, g) bytes, required.
@@ -659,8 +664,8 @@ any4_status any4_experts_gemm(any4_format format, const uint16_t* x, int per_pai
 size_t any4_experts_dx_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g);
 any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const uint8_t* packed,
                                  const uint16_t* lut, const uint16_t* alpha, const uint16_t* beta,
-                                 const int32_t* ids, const void* plan, uint16_t* dx, int64_t T, int64_t k,
-                                 int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
+                                 const int32_t* ids, const void* plan, void* dx, int dx_f32, int64_t T,
+                                 int64_t k, int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream);
 
 /*
@@ -669,17 +674,18 @@ any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const u
  *     out[t]   = bf16_rne( residual[t] + sum_j w[t][j] y[t][j] )
  *     dy[t][j] = bf16_rne( w[t][j] dout[t] ),   dw[t][j] = sum_n dout[t][n] y[t][j][n]
  * Sums are fp32, in the order of j.
- *   y, dy  device, [T][k][N] bf16       w, dw  device, [T][k] fp32 (w NULL in any4_combine:
+ *   y   device, [T][k][N] bf16 or fp32       dy  device, [T][k][N] bf16
+ *   w, dw  device, [T][k] fp32 (w NULL in any4_combine:
  *   weights of 1)     residual  device, [T][N] bf16, or NULL; may be out itself
- *   out, dout  device, [T][N] bf16.   dy or dw NULL: not wanted.  dy may be y itself.
+ *   out, dout  device, [T][N] bf16.   dy or dw NULL: not wanted.  dy may be y itself where that is bf16.
  *   0 <= T <= 2^20, k >= 1, T*k <= 2^20, N >= 0, T*k*N below 2^30.  T*N == 0 is a no-op
  *   (with N = 0 dw gets zeros).  Alignment: that of the elements.
  * Errors: ANY4_E_SHAPE, ANY4_E_NULL, ANY4_E_ALIGN, ANY4_E_HIP.
  */
-any4_status any4_combine(const uint16_t* y, const float* w, const uint16_t* residual, uint16_t* out,
-                         int64_t T, int64_t k, int64_t N, hipStream_t stream);
-any4_status any4_combine_backward(const uint16_t* dout, const uint16_t* y, const float* w, uint16_t* dy,
-                                  float* dw, int64_t T, int64_t k, int64_t N, hipStream_t stream);
+any4_status any4_combine(const void* y, int y_f32, const float* w, const uint16_t* residual,
+                         uint16_t* out, int64_t T, int64_t k, int64_t N, hipStream_t stream);
+any4_status any4_combine_backward(const uint16_t* dout, const void* y, int y_f32, const float* w,
+                                  uint16_t* dy, float* dw, int64_t T, int64_t k, int64_t N, hipStream_t stream);
 
 /*
  * any4_read_probe -- a measurement aid, not part of the method: reads `bytes`
