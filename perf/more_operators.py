@@ -417,8 +417,8 @@ def _run_moe(s, case):
         w, ids = any4.route(s["logits"], case["k"])
         plan = any4.experts_plan(ids, E)
         h = call(s["x"], *_tables(fmt, s["up"]), g, ids, act="silu", gate=True, plan=plan)
-        y = call(h, *_tables(fmt, s["down"]), g, ids, plan=plan)
-        return any4.combine(y, w)
+        y = torch.empty((case["T"], case["k"], case["D"]), dtype=torch.float32, device=ids.device)
+        return any4.combine(call(h, *_tables(fmt, s["down"]), g, ids, plan=plan, out=y), w)
     w, ids, _ = _route(s, case)
     h = _activate(_through(s["x"].float()[:, None], _weights(s["up"], fmt, g), ids, E), "silu", True)
     y = _through(h, _weights(s["down"], fmt, g), ids, E)
@@ -435,12 +435,15 @@ def _run_experts(s, case):
         back = {"any4": any4.experts_gemm_dx, "int4": any4.experts_gemm_int4_dx, "any2": any4.any2_experts_gemm_dx,
                 "any3": any4.any3_experts_gemm_dx}[fmt]
         plan = any4.experts_plan(ids, E)
-        z = torch.empty((T, k, 2 * case["F"]), dtype=torch.bfloat16, device=ids.device)
+        # z and the rows' gradients are kept in fp32
+        z, dh, dx = (torch.empty((T, k, n), dtype=torch.float32, device=ids.device)
+                     for n in (2 * case["F"], case["F"], case["D"]))
         h = call(s["x"], *_tables(fmt, s["up"]), g, ids, act="silu", gate=True, z=z, plan=plan)
         y = call(h, *_tables(fmt, s["down"]), g, ids, plan=plan)
-        dh = back(s["dy"], *_tables(fmt, s["down"]), g, ids, plan=plan)
+        back(s["dy"], *_tables(fmt, s["down"]), g, ids, plan=plan, out=dh)
         dz, _ = any4.act_backward(dh, z, act="silu", gate=True, need_bias=False)
-        return {"y": y, "dx": any4.combine(back(dz, *_tables(fmt, s["up"]), g, ids, plan=plan))}
+        back(dz, *_tables(fmt, s["up"]), g, ids, plan=plan, out=dx)
+        return {"y": y, "dx": any4.combine(dx)}
     up, down = _weights(s["up"], fmt, g), _weights(s["down"], fmt, g)
     z = _through(s["x"].float()[:, None], up, ids, E)
     y = _through(_activate(z, "silu", True), down, ids, E)
