@@ -1007,44 +1007,60 @@ struct BwdArgs {
     uint16_t* dz;
     float* part;             // [slabs][N] or null: no bias
     int M, N, No, act, slab; // rows of a workgroup
-    int dy32, z32;           // fp32 instead of bf16
 };
 
 constexpr int BWD_COLS = 8 * WAVE;           // columns of out of a workgroup
 
-// A wave takes 512 columns of every fourth row of a slab; the column sums of the
-// four waves meet in LDS.
+// A wave takes 512 columns of every fourth row of a slab, two rows at a time; the
+// column sums of the four waves meet in LDS.  Bound by its bytes.  What the loads depend
+// on is known to the compiler, and a row past the last is the last again: a branch
+// between them would make each wait for the one before.
+template <bool DY32, bool Z32, bool GATE, bool WHOLE>
 __global__ __launch_bounds__(256) void k_act_bwd(const BwdArgs p)
 {
     __shared__ float red[4][2][8][WAVE];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col = blockIdx.x * BWD_COLS + 8 * lane, valid = p.No - col;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col = blockIdx.x * BWD_COLS + 8 * lane;
     const int m0 = blockIdx.y * p.slab, m1 = m0 + p.slab < p.M ? m0 + p.slab : p.M;
-    const bool gate = p.No != p.N;
+    const int left = p.No - col, valid = WHOLE ? 8 : left;
+    constexpr int ROWS = 2;
     float sum[2][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         sum[0][i] = sum[1][i] = 0.0f;
-    for (int m = m0 + w; m < m1; m += 4) {
-        if (valid <= 0)
+    for (int m = m0 + w; m < m1; m += 4 * ROWS) {
+        if (left <= 0)
             break;
-        const size_t at = static_cast<size_t>(m) * p.N + col;
-        float d[8], zg[8], zu[8], a[8], b[8];
-        get_values(p.dy, p.dy32, static_cast<size_t>(m) * p.No + col, valid, d);
-        get_values(p.z, p.z32, at, valid, zg);
-        if (gate)
-            get_values(p.z, p.z32, at + p.No, valid, zu);
+        float d[ROWS][8], zg[ROWS][8], zu[ROWS][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float f, slope;
-            activate_both(zg[i], p.act, f, slope);
-            a[i] = gate ? d[i] * zu[i] * slope : d[i] * slope;
-            b[i] = d[i] * f;
-            sum[0][i] += a[i];
-            sum[1][i] += b[i];
+        for (int r = 0; r < ROWS; ++r) {
+            const size_t row = m + 4 * r < m1 ? m + 4 * r : m;
+            get_values(p.dy, DY32, row * p.No + col, valid, d[r]);
+            get_values(p.z, Z32, row * p.N + col, valid, zg[r]);
+            if constexpr (GATE)
+                get_values(p.z, Z32, row * p.N + p.No + col, valid, zu[r]);
         }
-        put_values(p.dz, 0, at, valid, a);
-        if (gate)
-            put_values(p.dz, 0, at + p.No, valid, b);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            if (m + 4 * r >= m1)
+                break;
+            float a[8], b[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float f, slope;
+                activate_both(zg[r][i], p.act, f, slope);
+                a[i] = d[r][i] * slope;
+                if constexpr (GATE) {
+                    a[i] *= zu[r][i];
+                    b[i] = d[r][i] * f;
+                    sum[1][i] += b[i];
+                }
+                sum[0][i] += a[i];
+            }
+            const size_t at = static_cast<size_t>(m + 4 * r) * p.N + col;
+            put_values(p.dz, 0, at, valid, a);
+            if constexpr (GATE)
+                put_values(p.dz, 0, at + p.No, valid, b);
+        }
     }
     if (!p.part)
         return;
@@ -1056,7 +1072,7 @@ __global__ __launch_bounds__(256) void k_act_bwd(const BwdArgs p)
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * BWD_COLS; i += 256) {
         const int h = i / BWD_COLS, o = i % BWD_COLS, c = blockIdx.x * BWD_COLS + o;
-        if (c >= p.No || (h && !gate))
+        if (c >= p.No || (h && !GATE))
             continue;
         p.part[static_cast<size_t>(blockIdx.y) * p.N + h * p.No + c] =
             red[0][h][o & 7][o >> 3] + red[1][h][o & 7][o >> 3] + red[2][h][o & 7][o >> 3] + red[3][h][o & 7][o >> 3];
@@ -1356,10 +1372,22 @@ any4_status any4_act_backward(const void* dy, int dy_f32, const void* z, int z_f
         return ANY4_E_WORKSPACE;
     (void)hipGetLastError();
     float* part = dbias ? static_cast<float*>(workspace) : nullptr;
-    if (M > 0)
-        hipLaunchKernelGGL(k_act_bwd, dim3(static_cast<unsigned>((no + BWD_COLS - 1) / BWD_COLS), static_cast<unsigned>(slabs)), dim3(256), 0,
-                           stream, BwdArgs{dy, z, dz, part, static_cast<int>(M), n, no, static_cast<int>(act), slab,
-                                   dy_f32 != 0, z_f32 != 0});
+    if (M > 0) {
+        const BwdArgs a{dy, z, dz, part, static_cast<int>(M), n, no, static_cast<int>(act), slab};
+        const dim3 grid(static_cast<unsigned>((no + BWD_COLS - 1) / BWD_COLS), static_cast<unsigned>(slabs));
+        auto launch = [&](auto dy32, auto z32) {
+#define BWD(GATE_, WHOLE_) hipLaunchKernelGGL((k_act_bwd<decltype(dy32)::value, decltype(z32)::value, GATE_, WHOLE_>), grid, dim3(256), 0, stream, a)
+            if (gate && no % 8 == 0) BWD(true, true);
+            else if (gate) BWD(true, false);
+            else if (no % 8 == 0) BWD(false, true);
+            else BWD(false, false);
+#undef BWD
+        };
+        if (dy_f32 && z_f32) launch(std::true_type{}, std::true_type{});
+        else if (dy_f32) launch(std::true_type{}, std::false_type{});
+        else if (z_f32) launch(std::false_type{}, std::true_type{});
+        else launch(std::false_type{}, std::false_type{});
+    }
     if (dbias)
         hipLaunchKernelGGL(k_bias_sum, dim3(static_cast<unsigned>((n + WAVE - 1) / WAVE)), dim3(256), 0, stream, part, dbias, n, slabs);
     return launch_status();

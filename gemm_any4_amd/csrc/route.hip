@@ -308,17 +308,20 @@ struct CombineArgs {
     uint16_t* out;
     int k, N, per;           // pieces of eight columns a row
     size_t pieces;
-    int y32;                 // y in fp32 instead of bf16
 };
 
-// Eight columns of a token a thread, eight pairs' loads at a time; bound by its bytes.
+// Eight columns of a token a thread, the loads of up to JB pairs at a time; bound by
+// its bytes.  What the loads depend on (Y32, rows of whole pieces, JB) is known to the
+// compiler, and pairs past the last are read as the last again: a branch between the
+// loads would make each wait for the one before (8192 x 8 x 2048: 335 MB).
+template <bool Y32, bool WHOLE, int JB>
 __global__ __launch_bounds__(256) void k_combine(const CombineArgs p)
 {
     const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;
     if (i >= p.pieces)
         return;
     const size_t t = i / p.per;
-    const int col = static_cast<int>(i % p.per) * 8, valid = p.N - col;
+    const int col = static_cast<int>(i % p.per) * 8, valid = WHOLE ? 8 : p.N - col;
     float s[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -326,17 +329,16 @@ __global__ __launch_bounds__(256) void k_combine(const CombineArgs p)
     if (p.residual)
         get_values(p.residual, 0, t * p.N + col, valid, s);
     const size_t y = t * p.k * p.N + col;
-    const float* w = p.w ? p.w + t * p.k : nullptr;
-    for (int j0 = 0; j0 < p.k; j0 += 8) {
-        float v[8][8], f[8];
+    for (int j0 = 0; j0 < p.k; j0 += JB) {
+        float v[JB][8], f[JB];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j0 + j < p.k) {
-                get_values(p.y, p.y32, y + static_cast<size_t>(j0 + j) * p.N, valid, v[j]);
-                f[j] = w ? w[j0 + j] : 1.0f;
-            }
+        for (int j = 0; j < JB; ++j) {
+            const int at = j0 + j < p.k ? j0 + j : p.k - 1;
+            get_values(p.y, Y32, y + static_cast<size_t>(at) * p.N, valid, v[j]);
+            f[j] = p.w ? p.w[t * p.k + at] : 1.0f;
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < JB; ++j)
             if (j0 + j < p.k)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -352,60 +354,62 @@ struct CombineBwdArgs {
     uint16_t* dy;
     float* dw;
     int k, N;
-    int y32;                 // y in fp32 instead of bf16
 };
 
-// A workgroup a token, 2048 columns a round; the sums of up to eight pairs at a time.
+// A workgroup a token, 2048 columns a round; the sums of up to JB pairs at a time, loads
+// as above.
+template <bool Y32, bool WHOLE, int JB>
 __global__ __launch_bounds__(256) void k_combine_bwd(const CombineBwdArgs p)
 {
-    __shared__ float red[4][8];
+    __shared__ float red[4][JB];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const size_t t = blockIdx.x;
     const uint16_t* dout = p.dout + t * p.N;
-    for (int j0 = 0; j0 < p.k; j0 += 8) {
-        float sum[8], f[8];
+    for (int j0 = 0; j0 < p.k; j0 += JB) {
+        float sum[JB], f[JB];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < JB; ++j) {
             sum[j] = 0.0f;
-            f[j] = j0 + j < p.k ? p.w[t * p.k + j0 + j] : 0.0f;
+            f[j] = p.w[t * p.k + (j0 + j < p.k ? j0 + j : p.k - 1)];
         }
         for (int col = threadIdx.x * 8; col < p.N; col += 2048) {
-            const int valid = p.N - col;
-            float d[8], v[8][8];
+            const int valid = WHOLE ? 8 : p.N - col;
+            float d[8];
             get_values(dout, 0, col, valid, d);
-            if (p.dw)
+            if (p.dw) {
+                float v[JB][8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j0 + j < p.k)
-                        get_values(p.y, p.y32, (t * p.k + j0 + j) * p.N + col, valid, v[j]);
+                for (int j = 0; j < JB; ++j)
+                    get_values(p.y, Y32, (t * p.k + (j0 + j < p.k ? j0 + j : p.k - 1)) * p.N + col, valid, v[j]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (j0 + j >= p.k)
-                    break;
-                if (p.dw)
+                for (int j = 0; j < JB; ++j)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         sum[j] = fmaf(d[e], v[j][e], sum[j]);
-                if (p.dy) {
+            }
+            if (p.dy)
+#pragma unroll
+                for (int j = 0; j < JB; ++j) {
+                    if (j0 + j >= p.k)
+                        break;
                     float o[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         o[e] = f[j] * d[e];
                     put_values(p.dy, 0, (t * p.k + j0 + j) * p.N + col, valid, o);
                 }
-            }
         }
         if (!p.dw)
             continue;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < JB; ++j) {
             const float s = wave_sum(sum[j]);
             if (lane == 0)
                 red[wave][j] = s;
         }
         __syncthreads();
-        if (threadIdx.x < 8 && j0 + static_cast<int>(threadIdx.x) < p.k)
+        if (threadIdx.x < JB && j0 + static_cast<int>(threadIdx.x) < p.k)
             p.dw[t * p.k + j0 + threadIdx.x] = red[0][threadIdx.x] + red[1][threadIdx.x] + red[2][threadIdx.x] + red[3][threadIdx.x];
     }
 }
@@ -424,6 +428,25 @@ bool route_ok(int64_t T, int64_t E, int64_t k, int score)
 bool combine_ok(int64_t T, int64_t k, int64_t N)
 {
     return T >= 0 && T <= MAX_T && k >= 1 && k <= MAX_T && T * k <= MAX_T && N >= 0 && N < GIB1 && (T == 0 || N < GIB1 / (T * k));
+}
+
+// Calls f with the form of a weighted sum: fp32 or not, rows of whole pieces or not, how
+// many pairs at a time.
+template <typename F>
+void by_form(bool y32, int64_t N, int64_t k, F&& f)
+{
+    auto pairs = [&](auto a, auto b) {
+        if (k == 1) f(a, b, std::integral_constant<int, 1>{});
+        else if (k == 2) f(a, b, std::integral_constant<int, 2>{});
+        else if (k <= 4) f(a, b, std::integral_constant<int, 4>{});
+        else f(a, b, std::integral_constant<int, 8>{});
+    };
+    auto rows = [&](auto a) {
+        if (N % 8 == 0) pairs(a, std::true_type{});
+        else pairs(a, std::false_type{});
+    };
+    if (y32) rows(std::true_type{});
+    else rows(std::false_type{});
 }
 
 template <bool SCORED>
@@ -505,8 +528,11 @@ any4_status any4_combine(const void* y, int y_f32, const float* w, const uint16_
     (void)hipGetLastError();
     const int per = static_cast<int>((N + 7) / 8);
     const size_t pieces = static_cast<size_t>(T) * per;
-    hipLaunchKernelGGL(k_combine, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream,
-                       CombineArgs{y, w, residual, out, static_cast<int>(k), static_cast<int>(N), per, pieces, y_f32 != 0});
+    const CombineArgs a{y, w, residual, out, static_cast<int>(k), static_cast<int>(N), per, pieces};
+    const dim3 grid(static_cast<unsigned>((pieces + 255) / 256));
+    by_form(y_f32 != 0, N, k, [&](auto y32, auto whole, auto jb) {
+        hipLaunchKernelGGL((k_combine<decltype(y32)::value, decltype(whole)::value, decltype(jb)::value>), grid, dim3(256), 0, stream, a);
+    });
     return launch_status();
 }
 
@@ -522,8 +548,11 @@ any4_status any4_combine_backward(const uint16_t* dout, const void* y, int y_f32
     if (!is_aligned(dout, 2) || !is_aligned(y, y_f32 ? 4 : 2) || !is_aligned(w, 4) || !is_aligned(dy, 2) || !is_aligned(dw, 4))
         return ANY4_E_ALIGN;
     (void)hipGetLastError();
-    hipLaunchKernelGGL(k_combine_bwd, dim3(static_cast<unsigned>(T)), dim3(256), 0, stream,
-                       CombineBwdArgs{dout, y, w, dy, dw, static_cast<int>(k), static_cast<int>(N), y_f32 != 0});
+    const CombineBwdArgs a{dout, y, w, dy, dw, static_cast<int>(k), static_cast<int>(N)};
+    by_form(y_f32 != 0, N, k, [&](auto y32, auto whole, auto jb) {
+        hipLaunchKernelGGL((k_combine_bwd<decltype(y32)::value, decltype(whole)::value, decltype(jb)::value>), dim3(static_cast<unsigned>(T)),
+                           dim3(256), 0, stream, a);
+    });
     return launch_status();
 }
 
