@@ -222,8 +222,6 @@ __device__ __forceinline__ int share(int all, int i, int n) { return __builtin_a
 // ---------------------------------------------------------------------------
 // few rows: packed weights read once, decoded in registers
 // ---------------------------------------------------------------------------
-constexpr int FEW_THREADS = 512;
-constexpr int FEW_WAVES = FEW_THREADS / WAVE;
 constexpr int FEW_ROWS = 64;         // rows of W of a workgroup
 
 struct FewArgs {
@@ -316,11 +314,12 @@ __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, con
 // A lane has one row of W, so that its table and scales serve 128 weights at a
 // time, which the matrix cores multiply as they stand: the 16 blocks of a 4 x 4 x 4
 // product hold 64 rows of W, four k each, and four rows of x go to all of them.
-template <int FMT>
-__global__ __launch_bounds__(FEW_THREADS) void k_few(const FewArgs p)
+// WAVES share the chunks out.
+template <int FMT, int WAVES>
+__global__ __launch_bounds__(WAVE * WAVES) void k_few(const FewArgs p)
 {
-    __shared__ int own[FEW_WAVES][FEW_T];
-    __shared__ float red[FEW_WAVES][FEW_T][WAVE];
+    __shared__ int own[WAVES][FEW_T];
+    __shared__ float red[WAVES][FEW_T][WAVE];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Tile t = find_few(p.r, blockIdx.y, own[w]);
     if (t.e < 0)
@@ -332,7 +331,7 @@ __global__ __launch_bounds__(FEW_THREADS) void k_few(const FewArgs p)
     const int wr = live ? col + half * p.q.No : 0;
     if (t.e == p.r.E) {              // no expert: zeros
         if (blockIdx.z == 0 && live)
-            for (int i = w; i < t.count; i += FEW_WAVES) {
+            for (int i = w; i < t.count; i += WAVES) {
                 if (half == 0)
                     put_value(p.q.out, p.q.out32, static_cast<size_t>(own[w][i]) * p.q.No + col, 0.0f);
                 if (p.q.z)
@@ -340,7 +339,7 @@ __global__ __launch_bounds__(FEW_THREADS) void k_few(const FewArgs p)
             }
         return;
     }
-    const int Kc = p.w.K / 128, parts = p.q.S * FEW_WAVES, at = blockIdx.z * FEW_WAVES + w;
+    const int Kc = p.w.K / 128, parts = p.q.S * WAVES, at = blockIdx.z * WAVES + w;
     const int s0 = share(Kc, at, parts), s1 = share(Kc, at + 1, parts);
     f32x4_t acc[4];
 #pragma unroll
@@ -358,11 +357,11 @@ __global__ __launch_bounds__(FEW_THREADS) void k_few(const FewArgs p)
             for (int i = 0; i < 4; ++i)
                 red[w][4 * b + i][lane] = acc[b][i];
     __syncthreads();
-    for (int i = w; i < t.count; i += FEW_WAVES) {
+    for (int i = w; i < t.count; i += WAVES) {
         const int pair = own[w][i];
         float v = 0.0f;
 #pragma unroll
-        for (int o = 0; o < FEW_WAVES; ++o)
+        for (int o = 0; o < WAVES; ++o)
             v += red[o][i][lane];
         if (p.q.part) {
             if (live)
@@ -1114,7 +1113,8 @@ size_t layer_bytes(int fmt, int64_t N, int64_t K)
     return static_cast<size_t>((N + 15) / 16 * 16) * (K / 8) * (fmt == FMT_ANY2 ? 2 : fmt == FMT_ANY3 ? 3 : 4);
 }
 
-// How a product is run: the tile of k_tile (rm 0: k_few), its number and the splits.
+// How a product is run: the tile of k_tile (rm 0: k_few of 2 wn waves), its number and
+// the splits.
 struct Shape {
     int rm, wn, S;
     int64_t tiles_m, tiles_n;
@@ -1162,13 +1162,17 @@ Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool tu
         s.S = static_cast<int>(n);
         s.rows = rows;
     };
+    // Eight waves a workgroup where they are few (28672 x 4096 in 448: the same; 4096 x 4096
+    // in 64: 11.9 us for 13.6), four where there are many or a wave had less than four
+    // chunks (64 experts of 2048 x 2048, 1 token 8.2 us for 11.8, 8 tokens 28 for 40).
     if (!turn && (!experts || P <= FEW_P || each <= 64)) {
         const int64_t chunks = D / 128;
         const int rows = each <= 4 ? 0 : each <= 8 ? 1 : 2;
         const int64_t row_tiles = experts ? live * (each < 8 ? 4 : each / 4 + 2) / 4 : (P + FEW_T - 1) / FEW_T;
         const int64_t tiles = (C + FEW_ROWS - 1) / FEW_ROWS * row_tiles;
         for (int64_t n = 1; n <= 8 && (n == 1 || chunks / n >= 8); n *= 2)
-            better((tiles * n + 255) / 256 * FEW_TIME[rows] * ((chunks + 8 * n - 1) / (8 * n)) + (n > 1 ? 250 : 0), 0, 2, n, false);
+            better((tiles * n + 255) / 256 * FEW_TIME[rows] * ((chunks + 8 * n - 1) / (8 * n)) + (n > 1 ? 250 : 0), 0,
+                   tiles * n >= 512 || chunks < 32 ? 2 : 4, n, false);
     }
     const int64_t steps = (D + STEP - 1) / STEP;
     auto weigh = [&](const Form& f, int64_t before, bool rows) {
@@ -1232,7 +1236,13 @@ void launch_few(int fmt, const Shape& s, const FewArgs& a, hipStream_t stream)
 {
     const int per = a.q.gated() ? FEW_ROWS / 2 : FEW_ROWS;
     const dim3 grid(static_cast<unsigned>((a.q.No + per - 1) / per), static_cast<unsigned>(s.tiles_m), static_cast<unsigned>(s.S));
-#define FEW(FMT_) hipLaunchKernelGGL(k_few<FMT_>, grid, dim3(FEW_THREADS), 0, stream, a)
+#define FEW(FMT_)                                                                              \
+    do {                                                                                       \
+        if (s.wn == 2)                                                                         \
+            hipLaunchKernelGGL((k_few<FMT_, 4>), grid, dim3(4 * WAVE), 0, stream, a);          \
+        else                                                                                   \
+            hipLaunchKernelGGL((k_few<FMT_, 8>), grid, dim3(8 * WAVE), 0, stream, a);          \
+    } while (0)
     if (fmt == FMT_ANY4) FEW(FMT_ANY4);
     else if (fmt == FMT_INT4) FEW(FMT_INT4);
     else if (fmt == FMT_ANY2) FEW(FMT_ANY2);
