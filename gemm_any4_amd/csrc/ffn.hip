@@ -386,10 +386,11 @@ __global__ __launch_bounds__(WAVE * WAVES) void k_few(const FewArgs p)
 }
 
 // The splits' sums in order, then the epilogue; 8 columns a thread.
-__global__ __launch_bounds__(256) void k_join(const Epilogue q, const int* __restrict__ ids, int P, int E, size_t pieces)
+__global__ __launch_bounds__(256) void k_join(const Epilogue q, const int* __restrict__ ids, const int* __restrict__ plan, int P, int E,
+                                              size_t pieces)
 {
     const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;
-    if (i >= pieces)
+    if (i >= pieces || (plan && (plan[2] != P || plan[3] != E)))
         return;
     const int per = (q.No + 7) / 8, p = static_cast<int>(i / per), col = static_cast<int>(i % per) * 8;
     const int e = ids ? expert_of(ids[p], E) : 0;
@@ -1257,7 +1258,7 @@ bool fmt_ok(int fmt) { return fmt >= FMT_ANY4 && fmt <= FMT_ANY3; }
 bool sizes_ok(int64_t P, int64_t X, int64_t E, int64_t N, int64_t K, int64_t g)
 {
     return P >= 0 && P <= MAX_PAIRS && X >= 0 && E >= 1 && E <= MAX_EXPERTS && N >= 0 && N < GIB2 / 2 && K > 0 && K < GIB2 / 2 &&
-           g > 0 && g % 128 == 0 && K % g == 0 && N * K < 2 * GIB2 && (P == 0 || N < GIB2 / 2 / P) && (X == 0 || K < GIB2 / 2 / X);
+           g > 0 && g % 128 == 0 && K % g == 0 && (N + 15) / 16 * 16 * K < 2 * GIB2 && (P == 0 || N < GIB2 / 2 / P) && (X == 0 || K < GIB2 / 2 / X);
 }
 
 any4_status product(int fmt, const Rows& rows, int64_t X, const uint16_t* x, const Layer& w, const Epilogue& q, const int32_t* ids,
@@ -1310,7 +1311,7 @@ any4_status product(int fmt, const Rows& rows, int64_t X, const uint16_t* x, con
     }
     if (s.S > 1) {
         const size_t pieces = static_cast<size_t>(r.P) * ((e.No + 7) / 8);
-        hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, e, experts ? ids : nullptr, r.P, r.E,
+        hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, e, experts ? ids : nullptr, r.plan, r.P, r.E,
                            pieces);
     }
     return launch_status();
@@ -1359,7 +1360,7 @@ any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* 
 
 size_t any4_act_backward_workspace_size(int64_t M, int64_t N, int gate)
 {
-    if (M <= 0 || N <= 0 || M > MAX_PAIRS || N >= GIB2 / 2 / M || (gate && N % 2))
+    if (M <= 0 || N <= 0 || M > MAX_PAIRS || N > GIB2 / 4 || N >= GIB2 / 2 / M || (gate && N % 2))
         return 0;
     const int64_t slab = bwd_slab(M, gate ? N / 2 : N), slabs = (M + slab - 1) / slab;
     return up256(static_cast<size_t>(slabs) * N * 4);
@@ -1368,7 +1369,7 @@ size_t any4_act_backward_workspace_size(int64_t M, int64_t N, int gate)
 any4_status any4_act_backward(const void* dy, int dy_f32, const void* z, int z_f32, uint16_t* dz, float* dbias, any4_activation act,
                               int gate, int64_t M, int64_t N, void* workspace, size_t workspace_bytes, hipStream_t stream)
 {
-    if (!act_ok(act) || M < 0 || M > MAX_PAIRS || N < 0 || N >= GIB2 / 2 || (M > 0 && N >= GIB2 / 2 / M) || (gate && N % 2))
+    if (!act_ok(act) || M < 0 || M > MAX_PAIRS || N < 0 || N > GIB2 / 4 || (M > 0 && N >= GIB2 / 2 / M) || (gate && N % 2))
         return ANY4_E_SHAPE;
     if (N == 0 || (M == 0 && !dbias))
         return ANY4_OK;
@@ -1490,7 +1491,8 @@ any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const u
                       stream);
     if (s.S > 1) {
         const size_t pieces = static_cast<size_t>(P) * (K / 8);
-        hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, q, ids, P, static_cast<int>(E), pieces);
+        hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, q, ids, r.plan, P, static_cast<int>(E),
+                           pieces);
     }
     return launch_status();
 }

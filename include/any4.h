@@ -541,7 +541,8 @@ typedef enum any4_activation {
  *   out       device, [M][No] bf16 or fp32, written
  *   packed, lut, alpha, beta  as for the format's dequantisation.
  *   0 <= M <= 2^20, N >= 0 (even with a gate), K a positive multiple of 128, g as for
- *   any4_gemm (K/g is not limited); M*N and M*K below 2^30, N*K below 2^32.
+ *   any4_gemm (K/g is not limited); M*N and M*K below 2^30, N*K (N rounded up to a
+ *   multiple of 16) below 2^32.
  *   M*N == 0 is a no-op.
  *   workspace  device, 16-byte aligned, any4_gemm_act_workspace_size(M, N, K, g)
  *          bytes, required where that is not 0; contents need not be
@@ -569,7 +570,7 @@ any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* 
  *   dy  device, [M][No] bf16 or fp32    z  device, [M][N] bf16 or fp32
  *   dz  device, [M][N] bf16, written (may be z itself where that is bf16)
  *   dbias  device, [N] fp32, or NULL (workspace is then not used)
- *   0 <= M <= 2^20, N >= 0, M*N below 2^30.  M = 0 writes dbias = 0.
+ *   0 <= M <= 2^20, 0 <= N <= 2^29, M*N below 2^30.  M = 0 writes dbias = 0.
  *   workspace  device, 16-byte aligned, any4_act_backward_workspace_size(M, N, gate)
  *          bytes, with dbias.
  *   dy, z and dz need 2-byte alignment, dbias 4.

@@ -183,3 +183,24 @@ def test_the_binding_refuses():
         any4.combine(x[:, None])
     with pytest.raises(ValueError):
         any4.combine_backward(x, x[:, None], torch.ones(2, 1))
+
+
+def test_fp32_results_and_inputs_need_four_bytes():
+    for name, flag in (("z", "z_f32"), ("out", "out_f32")):
+        args = dict(fmt=0, x_ptr=A, packed_ptr=A, lut_ptr=A, alpha_ptr=A, beta_ptr=A, bias_ptr=None, z_ptr=A, out_ptr=A, act=2, gate=0,
+                    N=16, K=128, g=128, ws_ptr=A, ws_bytes=BIG, stream=0) | {name + "_ptr": A + 2, flag: 1}
+        assert any4.gemm_act_raw(**args, residual_ptr=None, M=4) == 3
+        assert any4.experts_gemm_raw(**args, per_pair=0, ids_ptr=A, plan_ptr=None, T=100, k=2, E=4) == 3
+    assert any4.experts_gemm_dx_raw(0, A, A, A, A, A, A, None, A + 2, 100, 2, 4, 16, 128, 128, A, BIG, stream=0, dx_f32=1) == 3
+    assert any4.act_backward_raw(A + 2, A, A, A, 2, 0, 4, 16, A, BIG, stream=0, dy_f32=1) == 3
+    assert any4.act_backward_raw(A, A + 2, A, A, 2, 0, 4, 16, A, BIG, stream=0, z_f32=1) == 3
+    assert any4.combine_raw(A + 2, A, None, A, 4, 2, 16, stream=0, y_f32=1) == 3
+    assert any4.combine_backward_raw(A, A + 2, A, A, A, 4, 2, 16, stream=0, y_f32=1) == 3
+
+
+def test_sizes_whose_packed_layers_or_grids_would_be_too_large():
+    """A layer is packed in groups of 16 rows, whatever its N."""
+    assert act(M=1, N=1, K=1 << 29, g=1 << 20) == 2 and any4.gemm_act_workspace_size(1, 1, 1 << 29, 1 << 20) == 0
+    assert experts(T=1, k=1, N=1, K=1 << 28, g=1 << 20) == 2 and dx(T=1, k=1, N=1, K=1 << 28, g=1 << 20) == 2
+    assert any4.act_backward_raw(A, A, A, A, 0, 0, 1, (1 << 29) + 2, A, BIG, stream=0) == 2
+    assert any4.act_backward_workspace_size(1, (1 << 29) + 2, 0) == 0

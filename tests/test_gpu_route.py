@@ -119,7 +119,9 @@ def test_experts_that_are_out():
     b = torch.zeros(20, device=gu.DEV)
     b[3], b[4], b[5] = nan, -inf, inf
     w, ids = any4.route(l, 4, bias=b, renorm=False)
-    assert not ((ids == 3) | (ids == 4)).any() and (ids[1:3, 0] == torch.tensor([0, 0], device=gu.DEV)).sum() <= 2
+    assert not ((ids == 3) | (ids == 4)).any()
+    assert (ids[[4, 5, 7], 0] == 5).all()         # a bias of +inf comes first, where its expert is not out
+    assert not (ids[[2, 6]] == 5).any() and (ids[[0, 3]] == -1).all() and (w[[0, 3]] == 0).all()
 
 
 def test_far_logits():
