@@ -138,7 +138,7 @@ def lib() -> ctypes.CDLL:
                  [P, P, INT, P, P] + [INT] * 2 + [F32] + [I64] * 3 + [P]),
                 ("any4_experts_workspace_size", SZ, [I64] * 6),
                 ("any4_experts_gemm", ctypes.c_int,
-                 [INT, P, INT] + [P] * 8 + [INT, P] + [INT] * 3 + [I64] * 6 + [P, SZ, P]),
+                 [INT, P, INT, INT] + [P] * 8 + [INT, P] + [INT] * 3 + [I64] * 6 + [P, SZ, P]),
                 ("any4_experts_dx_workspace_size", SZ, [I64] * 6),
                 ("any4_experts_gemm_dx", ctypes.c_int, [INT] + [P] * 8 + [INT] + [I64] * 6 + [P, SZ, P]),
                 ("any4_combine", ctypes.c_int, [P, INT] + [P] * 3 + [I64] * 3 + [P]),
@@ -980,8 +980,9 @@ def route_backward_raw(dw_ptr, logits_ptr, bf16, ids_ptr, dlogits_ptr, score, re
 
 
 def experts_gemm_raw(fmt, x_ptr, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, ids_ptr, plan_ptr, z_ptr,
-                     out_ptr, act, gate, T, k, E, N, K, g, ws_ptr, ws_bytes, stream=None, z_f32=0, out_f32=0) -> int:
-    return lib().any4_experts_gemm(fmt, x_ptr, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, ids_ptr,
+                     out_ptr, act, gate, T, k, E, N, K, g, ws_ptr, ws_bytes, stream=None, z_f32=0, out_f32=0,
+                     x_f32=0) -> int:
+    return lib().any4_experts_gemm(fmt, x_ptr, x_f32, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, ids_ptr,
                                    plan_ptr, z_ptr, z_f32, out_ptr, out_f32, act, gate, T, k, E, N, K, g, ws_ptr,
                                    ws_bytes, _stream(stream))
 
@@ -1244,13 +1245,15 @@ def _experts_gemm(fmt: int, x, packed, lut, alpha, beta, g, ids, bias, act, gate
     No, per_pair = N // 2 if gate else N, x.dim() == 3
     if gate and N % 2:
         raise ValueError("a gated layer must have an even number of rows")
-    p_x = _tensor(x, "x", bf16, (T, k, K) if per_pair else (T, K), dev)
+    p_x, x32 = _kept(x, "x", (T, k, K) if per_pair else (T, K), dev)
+    if x32 and T * k > 64:
+        raise ValueError("x may be fp32 for up to 64 pairs")
     p_bias, (p_z, z32) = _maybe(bias, "bias", bf16, (E, N), dev), _kept(z, "z", (T, k, N), dev)
     number = _choice("act", act, ACTIVATIONS)
     with _on(dev, stream):
         out, p_out, out32 = _result(out, "out", (T, k, No), dev)
         ws, p_ws, nbytes = _scratch(workspace, experts_workspace_size(T, k, E, N, K, g), dev)
-        check(lib().any4_experts_gemm(fmt, p_x, 1 if per_pair else 0, p_packed, p_lut, p_alpha, p_beta, p_bias, p_ids,
+        check(lib().any4_experts_gemm(fmt, p_x, x32, 1 if per_pair else 0, p_packed, p_lut, p_alpha, p_beta, p_bias, p_ids,
                                       p_plan, p_z, z32, p_out, out32, number, 1 if gate else 0, T, k, E, N, K, g,
                                       p_ws, nbytes, _current_handle(dev.index)))
     return out
@@ -1264,7 +1267,7 @@ def experts_gemm(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha
     any4 layers [N, K] stacked: packed the E layers' bytes one after another, lut
     [E, N, 16], alpha and beta [E, N, K/g], bias [E, N].
 
-    x bf16 [T, K], or [T, k, K]: a row for each pair (the block's second product).  act, gate
+    x bf16 (up to 64 pairs: or fp32) [T, K], or [T, k, K]: a row for each pair (the block's second product).  act, gate
     and z ([T, k, N]) as in gemm_act.  A pair whose id is not in 0..E-1 gives zeros.
     plan: of experts_plan(ids, E), kept over the products of a block.  z and out
     may be bf16 or fp32."""

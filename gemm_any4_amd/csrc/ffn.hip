@@ -227,7 +227,7 @@ constexpr int FEW_ROWS = 64;         // rows of W of a workgroup
 struct FewArgs {
     Rows r;
     Layer w;
-    const uint16_t* x;
+    const void* x;           // bf16, or (X32) fp32
     Epilogue q;
 };
 
@@ -263,8 +263,30 @@ struct RowChunk {
     }
 };
 
-// The product of 4 * NB rows of x with the lane's row of W over chunks s0 .. s1.
-template <int FMT, int NB>
+// fp32 values as the bf16 parts hi + lo: hi cut off, lo what is left, rounded (2^-16
+// of the value at most).  An infinity has no lo.
+__device__ __forceinline__ void split2(f32x4_t v, s16x4_t& hi, s16x4_t& lo)
+{
+    u32x2_t h, l;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t top[2], rest[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float x = v[2 * i + j];
+            top[j] = __builtin_bit_cast(uint32_t, x) & 0xffff0000u;
+            rest[j] = f32_to_bf16(__builtin_isinf(x) ? 0.0f : x - __builtin_bit_cast(float, top[j]));
+        }
+        h[i] = top[0] >> 16 | top[1];
+        l[i] = rest[0] | rest[1] << 16;
+    }
+    hi = __builtin_bit_cast(s16x4_t, h);
+    lo = __builtin_bit_cast(s16x4_t, l);
+}
+
+// The product of 4 * NB rows of x with the lane's row of W over chunks s0 .. s1.  Rows
+// of fp32 are two of bf16.
+template <int FMT, int NB, bool X32>
 __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, const int* own, int count, int s0, int s1,
                                             f32x4_t (&acc)[4])
 {
@@ -273,22 +295,24 @@ __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, con
     const int lane = threadIdx.x & 63, Kc = p.w.K / 128;
     const uint8_t* packed = p.w.codes(e);
     const uint16_t *alpha = p.w.alpha + p.w.scales(e), *beta = p.w.beta + p.w.scales(e);
-    const uint16_t* x[NB];           // the lane's four k of a row, of each 64
+    typedef std::conditional_t<X32, float, uint16_t> X;
+    typedef std::conditional_t<X32, f32x4_t, s16x4_t> Four;
+    const X* x[NB];                  // the lane's four k of a row, of each 64
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const int i = 4 * b + (lane & 3);
-        x[b] = p.x + static_cast<size_t>(own[i < count ? i : count - 1] / p.r.div) * p.w.K + 4 * (lane >> 2);
+        x[b] = static_cast<const X*>(p.x) + static_cast<size_t>(own[i < count ? i : count - 1] / p.r.div) * p.w.K + 4 * (lane >> 2);
     }
     RowChunk<FMT> next;
     next.fetch(packed, alpha, beta, wr, Kc, s0, p.w.g);
     RowTable row = fetch_table<FMT>(FMT == FMT_INT4 ? nullptr : p.w.table(e), alpha, beta, wr, Kc, s0, p.w.g);
     for (int s = s0; s < s1; ++s) {
-        s16x4_t a[NB][2];
+        Four in[NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                a[b][j] = *reinterpret_cast<const s16x4_t*>(x[b] + s * 128 + 64 * j);
+                in[b][j] = *reinterpret_cast<const Four*>(x[b] + s * 128 + 64 * j);
         const RowChunk<FMT> now = next;
         if (s + 1 < s1)
             next.fetch(packed, alpha, beta, wr, Kc, s + 1, p.w.g);
@@ -296,16 +320,27 @@ __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, con
         row.alpha = now.alpha;
         row.beta = now.beta;
         const ByteTable<FMT> t(row);
+        s16x4_t a[NB], lo[NB];
         static_for<0, 4>([&](auto q_) __attribute__((always_inline)) {
             constexpr int q = decltype(q_)::value;
+            if constexpr (q % 2 == 0)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    if constexpr (X32)
+                        split2(in[b][q / 2], a[b], lo[b]);
+                    else
+                        a[b] = in[b][q / 2];
             uint32_t v[16];
             decode_in_order(t, now.code[q], v);
             static_for<0, 8>([&](auto i_) __attribute__((always_inline)) {
                 constexpr int i = decltype(i_)::value;
                 const u32x2_t w = {v[2 * i], v[2 * i + 1]};
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    acc[b] = mfma4<8 * (q & 1) + i>(a[b][q / 2], __builtin_bit_cast(s16x4_t, w), acc[b]);
+                for (int b = 0; b < NB; ++b) {
+                    acc[b] = mfma4<8 * (q & 1) + i>(a[b], __builtin_bit_cast(s16x4_t, w), acc[b]);
+                    if constexpr (X32)
+                        acc[b] = mfma4<8 * (q & 1) + i>(lo[b], __builtin_bit_cast(s16x4_t, w), acc[b]);
+                }
             });
         });
     }
@@ -315,8 +350,8 @@ __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, con
 // time, which the matrix cores multiply as they stand: the 16 blocks of a 4 x 4 x 4
 // product hold 64 rows of W, four k each, and four rows of x go to all of them.
 // WAVES share the chunks out.
-template <int FMT, int WAVES>
-__global__ __launch_bounds__(WAVE * WAVES) void k_few(const FewArgs p)
+template <int FMT, int WAVES, bool X32>
+__global__ __launch_bounds__(WAVE * WAVES, 4) void k_few(const FewArgs p)
 {
     __shared__ int own[WAVES][FEW_T];
     __shared__ float red[WAVES][FEW_T][WAVE];
@@ -348,7 +383,7 @@ __global__ __launch_bounds__(WAVE * WAVES) void k_few(const FewArgs p)
     static_for<0, 3>([&](auto n_) __attribute__((always_inline)) {
         constexpr int NB = 1 << decltype(n_)::value;
         if (t.count <= 4 * NB && (NB == 1 || t.count > 2 * NB))
-            few_product<FMT, NB>(p, t.e, wr, own[w], t.count, s0, s1, acc);
+            few_product<FMT, NB, X32>(p, t.e, wr, own[w], t.count, s0, s1, acc);
     });
 #pragma unroll
     for (int b = 0; b < 4; ++b)
@@ -1233,16 +1268,20 @@ void launch_tile(int fmt, const Shape& s, const TileArgs& a, hipStream_t stream)
     else launch_tile<FMT_ANY3, TURN>(s, a, stream);
 }
 
-void launch_few(int fmt, const Shape& s, const FewArgs& a, hipStream_t stream)
+void launch_few(int fmt, const Shape& s, const FewArgs& a, bool x32, hipStream_t stream)
 {
     const int per = a.q.gated() ? FEW_ROWS / 2 : FEW_ROWS;
     const dim3 grid(static_cast<unsigned>((a.q.No + per - 1) / per), static_cast<unsigned>(s.tiles_m), static_cast<unsigned>(s.S));
 #define FEW(FMT_)                                                                              \
     do {                                                                                       \
-        if (s.wn == 2)                                                                         \
-            hipLaunchKernelGGL((k_few<FMT_, 4>), grid, dim3(4 * WAVE), 0, stream, a);          \
+        if (x32 && s.wn == 2)                                                                  \
+            hipLaunchKernelGGL((k_few<FMT_, 4, true>), grid, dim3(4 * WAVE), 0, stream, a);    \
+        else if (x32)                                                                          \
+            hipLaunchKernelGGL((k_few<FMT_, 8, true>), grid, dim3(8 * WAVE), 0, stream, a);    \
+        else if (s.wn == 2)                                                                    \
+            hipLaunchKernelGGL((k_few<FMT_, 4, false>), grid, dim3(4 * WAVE), 0, stream, a);   \
         else                                                                                   \
-            hipLaunchKernelGGL((k_few<FMT_, 8>), grid, dim3(8 * WAVE), 0, stream, a);          \
+            hipLaunchKernelGGL((k_few<FMT_, 8, false>), grid, dim3(8 * WAVE), 0, stream, a);   \
     } while (0)
     if (fmt == FMT_ANY4) FEW(FMT_ANY4);
     else if (fmt == FMT_INT4) FEW(FMT_INT4);
@@ -1261,7 +1300,7 @@ bool sizes_ok(int64_t P, int64_t X, int64_t E, int64_t N, int64_t K, int64_t g)
            g > 0 && g % 128 == 0 && K % g == 0 && (N + 15) / 16 * 16 * K < 2 * GIB2 && (P == 0 || N < GIB2 / 2 / P) && (X == 0 || K < GIB2 / 2 / X);
 }
 
-any4_status product(int fmt, const Rows& rows, int64_t X, const uint16_t* x, const Layer& w, const Epilogue& q, const int32_t* ids,
+any4_status product(int fmt, const Rows& rows, int64_t X, const void* x, bool x32, const Layer& w, const Epilogue& q, const int32_t* ids,
                     void* workspace, size_t workspace_bytes, bool experts, hipStream_t stream)
 {
     const Shape s = shape_of(rows.P, rows.E, experts, w.K, w.N, false);
@@ -1289,7 +1328,7 @@ any4_status product(int fmt, const Rows& rows, int64_t X, const uint16_t* x, con
     if (s.S > 1)
         e.part = reinterpret_cast<float*>(at);
     if (s.rm == 0) {
-        launch_few(fmt, s, FewArgs{r, w, x, e}, stream);
+        launch_few(fmt, s, FewArgs{r, w, x, e}, x32, stream);
     } else if (s.rows) {
         uint16_t* rows = reinterpret_cast<uint16_t*>(at + (s.S > 1 ? up256(static_cast<size_t>(s.S) * r.P * w.N * 4) : 0));
         const int Kc = w.K / 128;
@@ -1302,11 +1341,11 @@ any4_status product(int fmt, const Rows& rows, int64_t X, const uint16_t* x, con
 #undef LAY_OUT
         Layer laid = w;
         laid.packed = reinterpret_cast<const uint8_t*>(rows);
-        launch_tile<FMT_BF16, false>(s, TileArgs{r, laid, x, e, static_cast<int>(X), w.K, w.K / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
+        launch_tile<FMT_BF16, false>(s, TileArgs{r, laid, static_cast<const uint16_t*>(x), e, static_cast<int>(X), w.K, w.K / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
                                      stream);
     } else {
         r.ids = nullptr;
-        launch_tile<false>(fmt, s, TileArgs{r, w, x, e, static_cast<int>(X), w.K, w.K / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
+        launch_tile<false>(fmt, s, TileArgs{r, w, static_cast<const uint16_t*>(x), e, static_cast<int>(X), w.K, w.K / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
                            stream);
     }
     if (s.S > 1) {
@@ -1355,7 +1394,7 @@ any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* 
     const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
     const Epilogue q{bias, residual, z, out, nullptr, static_cast<int>(N), static_cast<int>(gate ? N / 2 : N), static_cast<int>(act), 1,
                      z_f32 != 0, out_f32 != 0};
-    return product(fmt, Rows{nullptr, nullptr, static_cast<int>(M), 1, 1}, M, x, w, q, nullptr, workspace, workspace_bytes, false, stream);
+    return product(fmt, Rows{nullptr, nullptr, static_cast<int>(M), 1, 1}, M, x, false, w, q, nullptr, workspace, workspace_bytes, false, stream);
 }
 
 size_t any4_act_backward_workspace_size(int64_t M, int64_t N, int gate)
@@ -1412,14 +1451,14 @@ size_t any4_experts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, i
     return part_bytes(shape_of(P, E, true, K, N, false), P, N, K) + (P <= FEW_P ? 0 : any4_lora_plan_bytes(P, E));
 }
 
-any4_status any4_experts_gemm(any4_format format, const uint16_t* x, int per_pair, const uint8_t* packed, const uint16_t* lut,
+any4_status any4_experts_gemm(any4_format format, const void* x, int x_f32, int per_pair, const uint8_t* packed, const uint16_t* lut,
                               const uint16_t* alpha, const uint16_t* beta, const uint16_t* bias, const int32_t* ids, const void* plan,
                               void* z, int z_f32, void* out, int out_f32, any4_activation act, int gate, int64_t T, int64_t k, int64_t E, int64_t N,
                               int64_t K, int64_t g, void* workspace, size_t workspace_bytes, hipStream_t stream)
 {
     const int fmt = static_cast<int>(format);
     if (!fmt_ok(fmt) || !act_ok(act) || T < 0 || k < 1 || T > MAX_PAIRS || k > MAX_PAIRS ||
-        !sizes_ok(T * k, per_pair ? T * k : T, E, N, K, g) || (gate && N % 2))
+        !sizes_ok(T * k, per_pair ? T * k : T, E, N, K, g) || (gate && N % 2) || (x_f32 && T * k > FEW_P))
         return ANY4_E_SHAPE;
     if (T == 0 || N == 0)
         return ANY4_OK;
@@ -1434,7 +1473,7 @@ any4_status any4_experts_gemm(any4_format format, const uint16_t* x, int per_pai
     const Epilogue q{bias, nullptr, z, out, nullptr, static_cast<int>(N), static_cast<int>(gate ? N / 2 : N), static_cast<int>(act), 1,
                      z_f32 != 0, out_f32 != 0};
     const Rows r{nullptr, static_cast<const int*>(plan), static_cast<int>(T * k), static_cast<int>(E), per_pair ? 1 : static_cast<int>(k)};
-    return product(fmt, r, per_pair ? T * k : T, x, w, q, ids, workspace, workspace_bytes, true, stream);
+    return product(fmt, r, per_pair ? T * k : T, x, x_f32 != 0, w, q, ids, workspace, workspace_bytes, true, stream);
 }
 
 size_t any4_experts_dx_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g)

@@ -625,7 +625,9 @@ any4_status any4_route_backward(const float* dw, const void* logits, int logits_
  * through expert e = ids[t][j],
  *     zf[p] = W_e x[per_pair ? p : t] + bias[e],   out[p] = bf16_rne( act(zf[p]) ) or gated
  * A pair whose id is not in 0..E-1 gives zeros (out and z).
- *   x       device, [T][K] bf16, or with per_pair != 0 [T*k][K]
+ *   x       device, [T][K] bf16, or with per_pair != 0 [T*k][K]; for up to 64 pairs with
+ *           x_f32 != 0 fp32, of which 16 bits or more enter the products (with one token a
+ *           rounding of the first product's results is not averaged over others)
  *   packed  device, the experts' packed layers one after another (each of
  *           any4_packed_bytes(N, K), or the format's)
  *   lut [E][N][16], alpha, beta [E][N][K/g], bias [E][N] bf16 (or NULL)
@@ -644,8 +646,8 @@ any4_status any4_route_backward(const float* dw, const void* logits, int logits_
  * Errors: as any4_gemm_act.
  */
 size_t any4_experts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g);
-any4_status any4_experts_gemm(any4_format format, const uint16_t* x, int per_pair, const uint8_t* packed,
-                              const uint16_t* lut, const uint16_t* alpha, const uint16_t* beta,
+any4_status any4_experts_gemm(any4_format format, const void* x, int x_f32, int per_pair,
+                              const uint8_t* packed, const uint16_t* lut, const uint16_t* alpha, const uint16_t* beta,
                               const uint16_t* bias, const int32_t* ids, const void* plan, void* z,
                               int z_f32, void* out, int out_f32, any4_activation act, int gate, int64_t T, int64_t k,
                               int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,

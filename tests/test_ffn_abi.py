@@ -204,3 +204,9 @@ def test_sizes_whose_packed_layers_or_grids_would_be_too_large():
     assert experts(T=1, k=1, N=1, K=1 << 28, g=1 << 20) == 2 and dx(T=1, k=1, N=1, K=1 << 28, g=1 << 20) == 2
     assert any4.act_backward_raw(A, A, A, A, 0, 0, 1, (1 << 29) + 2, A, BIG, stream=0) == 2
     assert any4.act_backward_workspace_size(1, (1 << 29) + 2, 0) == 0
+
+
+def test_fp32_rows_for_few_pairs():
+    args = (0, A, 0, A, A, A, A, None, A, None, None, A, 2, 0)
+    assert any4.experts_gemm_raw(*args, 65, 1, 4, 16, 128, 128, A, BIG, stream=0, x_f32=1) == 2
+    assert any4.experts_gemm_raw(0, A + 4, *args[2:], 8, 8, 4, 16, 128, 128, A, BIG, stream=0, x_f32=1) == 3

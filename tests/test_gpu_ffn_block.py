@@ -100,6 +100,43 @@ def test_forms_of_dx(fmt, T, k, E, N, K):
         near(out, want, e)
 
 
+@pytest.mark.parametrize("fmt", ["any4", "int4", "any2", "any3"])
+@pytest.mark.parametrize("T,k,E,N,K", [(1, 1, 1, 1, 128), (1, 2, 8, 96, 384), (6, 3, 5, 50, 256), (32, 2, 3, 130, 4096), (64, 1, 1, 33, 256),
+                                       (2, 2, 4, 66, 8192), (16, 4, 20, 2050, 512)])
+def test_fp32_rows(fmt, T, k, E, N, K):
+    """At least 16 bits of a value enter: 2^-16 of its magnitude is left out."""
+    packed, tables, w = layers(fmt, E, N, K, 128)
+    ids = choose(T, k, E)
+    gen = torch.Generator().manual_seed(T)
+    for shape in ((T, K), (T, k, K)):
+        x = torch.randn(*shape, generator=gen).to(gu.DEV)
+        out = empty(T, k, N)
+        call_of(fmt, "experts")(x, packed, *tables, 128, ids, out=out)
+        wide = x.double() if len(shape) == 3 else x.double()[:, None].expand(T, k, K)
+        want, e = each_expert(wide, w, ids)
+        # twice as many terms as the bound of a bf16 row's
+        near(out, want, 2 * e + 2.0 ** -16 * each_expert(wide.abs(), w.abs(), ids)[0])
+
+
+def test_fp32_rows_that_are_not_finite():
+    """The formulas' infinities and NaN, and values beyond bf16's largest."""
+    packed, tables, w = layers("any4", 2, 40, 256, 128)
+    ids, x = torch.tensor([[0, 1]] * 5, dtype=torch.int32, device=gu.DEV), torch.randn(5, 256, device=gu.DEV)
+    x[1, 7], x[2, 9], x[3, 200], x[4] = float("inf"), float("-inf"), float("nan"), 0.0
+    x[4, 3] = torch.finfo(F32).max
+    out = empty(5, 2, 40)
+    any4.experts_gemm(x, packed, *tables, 128, ids, out=out)
+    for j in range(2):
+        for t, k in ((1, 7), (2, 9)):
+            assert torch.equal(out[t, j], (x[t, k].double() * w[j, :, k]).float())
+    assert torch.isnan(out[3]).all() and torch.isfinite(out[0]).all()
+    want = x[4, 3].double() * torch.stack([w[j, :, 3] for j in range(2)])
+    small = want.abs() < 3e38
+    assert small.any() and ((out[4].double() - want).abs()[small] <= 2.0 ** -15 * want.abs()[small]).all()
+    with pytest.raises(ValueError):
+        any4.experts_gemm(x.repeat(7, 1), packed, *tables, 128, ids.repeat(7, 1))
+
+
 def test_fp32_results_at_odd_places():
     """fp32 rows that start 4 bytes off a piece of 16."""
     packed, tables, w = layers("any4", 1, 75, 256, 128)
