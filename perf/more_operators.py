@@ -408,6 +408,13 @@ def _experts_call(fmt):
             "any3": any4.any3_experts_gemm}[fmt]
 
 
+def _between(case, device):
+    """For what lies between the two products: in fp32 where the second takes it, for up to 64 pairs (a
+    few tokens' roundings to bf16 are not averaged over others)."""
+    kind = torch.float32 if case["T"] * case["k"] <= 64 else torch.bfloat16
+    return torch.empty((case["T"], case["k"], case["F"]), dtype=kind, device=device)
+
+
 def _run_moe(s, case):
     fmt, g, E = case["fmt"], case["g"], case["E"]
     if own:
@@ -416,7 +423,8 @@ def _run_moe(s, case):
         call = _experts_call(fmt)
         w, ids = any4.route(s["logits"], case["k"])
         plan = any4.experts_plan(ids, E)
-        h = call(s["x"], *_tables(fmt, s["up"]), g, ids, act="silu", gate=True, plan=plan)
+        h = _between(case, ids.device)
+        call(s["x"], *_tables(fmt, s["up"]), g, ids, act="silu", gate=True, plan=plan, out=h)
         y = torch.empty((case["T"], case["k"], case["D"]), dtype=torch.float32, device=ids.device)
         return any4.combine(call(h, *_tables(fmt, s["down"]), g, ids, plan=plan, out=y), w)
     w, ids, _ = _route(s, case)
@@ -438,7 +446,8 @@ def _run_experts(s, case):
         # z and the rows' gradients are kept in fp32
         z, dh, dx = (torch.empty((T, k, n), dtype=torch.float32, device=ids.device)
                      for n in (2 * case["F"], case["F"], case["D"]))
-        h = call(s["x"], *_tables(fmt, s["up"]), g, ids, act="silu", gate=True, z=z, plan=plan)
+        h = _between(case, ids.device)
+        call(s["x"], *_tables(fmt, s["up"]), g, ids, act="silu", gate=True, z=z, plan=plan, out=h)
         y = call(h, *_tables(fmt, s["down"]), g, ids, plan=plan)
         back(s["dy"], *_tables(fmt, s["down"]), g, ids, plan=plan, out=dh)
         dz, _ = any4.act_backward(dh, z, act="silu", gate=True, need_bias=False)
