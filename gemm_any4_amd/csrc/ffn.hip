@@ -11,6 +11,7 @@
 //
 // Rows of one expert are worked on in tiles, from the plan (plan.h) or, for few
 // pairs, from ballots over the ids.
+#include <cmath>
 #include <type_traits>
 
 #include "codes.h"
@@ -1200,15 +1201,18 @@ Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool tu
     };
     // Eight waves a workgroup where they are few (28672 x 4096 in 448: the same; 4096 x 4096
     // in 64: 11.9 us for 13.6), four where there are many or a wave had less than four
-    // chunks (64 experts of 2048 x 2048, 1 token 8.2 us for 11.8, 8 tokens 28 for 40).
+    // chunks (64 experts of 2048 x 2048, 1 token 8.2 us for 11.8, 8 tokens 28 for 40; two
+    // of eight 28672 x 4096, 896 workgroups: the same).
     if (!turn && (!experts || P <= FEW_P || each <= 64)) {
         const int64_t chunks = D / 128;
         const int rows = each <= 4 ? 0 : each <= 8 ? 1 : 2;
-        const int64_t row_tiles = experts ? live * (each < 8 ? 4 : each / 4 + 2) / 4 : (P + FEW_T - 1) / FEW_T;
-        const int64_t tiles = (C + FEW_ROWS - 1) / FEW_ROWS * row_tiles;
+        // experts that some pair names: 5.3 of 8 for 8 pairs (4096 x 14336: two splits, 49 us for 60)
+        const double named = E * (1.0 - std::pow(1.0 - 1.0 / E, static_cast<double>(P)));
+        const double row_tiles = experts ? named * (each < 8 ? 4 : each / 4 + 2) / 4 : static_cast<double>((P + FEW_T - 1) / FEW_T);
+        const int64_t tiles = static_cast<int64_t>((C + FEW_ROWS - 1) / FEW_ROWS * row_tiles + 0.5);
         for (int64_t n = 1; n <= 8 && (n == 1 || chunks / n >= 8); n *= 2)
             better((tiles * n + 255) / 256 * FEW_TIME[rows] * ((chunks + 8 * n - 1) / (8 * n)) + (n > 1 ? 250 : 0), 0,
-                   tiles * n >= 512 || chunks < 32 ? 2 : 4, n, false);
+                   tiles * n >= 1024 || chunks < 32 ? 2 : 4, n, false);
     }
     const int64_t steps = (D + STEP - 1) / STEP;
     auto weigh = [&](const Form& f, int64_t before, bool rows) {
