@@ -351,6 +351,14 @@ __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, con
 // time, which the matrix cores multiply as they stand: the 16 blocks of a 4 x 4 x 4
 // product hold 64 rows of W, four k each, and four rows of x go to all of them.
 // WAVES share the chunks out.
+//
+// Bound by the vector ALU: of some 550 instructions for a lane's 128 weights 416 look
+// them up.  One row with 28672 x 4096 takes 21 us (63 MB, 3.0 TB/s): 13.5 of these
+// instructions, where the bytes alone would take 12.5; half its layer takes 12.5 us, twice
+// as much 43.  448 workgroups are 1.75 to a CU and take the time of two: 16 rows of W a
+// wave, four quarters of k side by side, fill the CUs evenly and gained less than 10% (not
+// kept).  any2 and any3 have half the lookups: 14336 x 4096 in 10.4 us for any4's 12.5.
+// Rows of fp32 (X32): one token through two experts' 4096 x 14336 27.7 us for 24.7.
 template <int FMT, int WAVES, bool X32>
 __global__ __launch_bounds__(WAVE * WAVES, 4) void k_few(const FewArgs p)
 {
@@ -421,7 +429,8 @@ __global__ __launch_bounds__(WAVE * WAVES, 4) void k_few(const FewArgs p)
     }
 }
 
-// The splits' sums in order, then the epilogue; 8 columns a thread.
+// The splits' sums in order, then the epilogue; 8 columns a thread.  Bound by its bytes
+// (2062 rows of 4096 in three splits, 135 MB: 26 us), for few rows by its launch (4 us).
 __global__ __launch_bounds__(256) void k_join(const Epilogue q, const int* __restrict__ ids, const int* __restrict__ plan, int P, int E,
                                               size_t pieces)
 {
@@ -596,6 +605,20 @@ constexpr int parts_of(int blocks) { return blocks >= 2 ? 4 : 2; }
 
 // 2 x WN waves of RM x 4 blocks of 16 x 16.  TURN: the sum runs over the rows of W
 // and the results are its columns (the input's gradient).
+//
+// The matrix cores take a 16 x 16 x 32 product in 7.8 ns and let two vector instructions
+// in for nothing; every further one costs its 1.9 ns.  Decoding is 4.2 instructions a
+// product in tiles of 128 rows and 2.1 in tiles of 256, so those are the faster where
+// there are rows for them (a step of 64 of 256 x 256: 1.9 us; four tiles of 128 x 128:
+// 2.8): 1024 rows with 28672 x 4096 253 us, 950 TFLOP/s, for 300.  With one barrier a
+// step and one workgroup a CU of 256 x 256, and 192 KB a step through LDS, half the
+// time the matrix cores wait.  TURN pairs two rows' values before they are written: 1.0 us
+// a step of 128 x 128 for 0.7.
+//
+// Tried and not kept: the weights decoded into the operands' registers, every wave with
+// 32 columns and all rows of a tile, and x alone in LDS: 4096 rows with 28672 x 4096 in
+// tiles of 128 x 128 1168 us for 1203, and 64 rows 44 for 46, since the lookups bound both;
+// four waves of 128 x 128 each (accumulators moved between register files).
 template <int FMT, int WN, int RM, bool TURN>
 __global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileArgs p)
 {
@@ -1007,7 +1030,8 @@ __global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileAr
 // many rows: the layer laid out as bf16 once, for k_tile<FMT_BF16>
 // ---------------------------------------------------------------------------
 // A wave decodes a packed tile of 16 rows x 128 k and turns it in LDS of its own,
-// so that it leaves in whole pieces of rows.  Bound by its writes.
+// so that it leaves in whole pieces of rows.  Bound by its bytes (28672 x 4096, 298 MB:
+// 53 us, 5.6 TB/s).  Then 4096 rows' product takes 810 us, a library's alone 722.
 constexpr int ROWS_WAVES = 4;
 
 template <int FMT>
@@ -1050,7 +1074,8 @@ constexpr int BWD_COLS = 8 * WAVE;           // columns of out of a workgroup
 // A wave takes 512 columns of every fourth row of a slab, two rows at a time; the
 // column sums of the four waves meet in LDS.  Bound by its bytes.  What the loads depend
 // on is known to the compiler, and a row past the last is the last again: a branch
-// between them would make each wait for the one before.
+// between them would make each wait for the one before.  4096 x 28672, gated, 587 MB:
+// 117 us, 5.0 TB/s, a copy's rate.
 template <bool DY32, bool Z32, bool GATE, bool WHOLE>
 __global__ __launch_bounds__(256) void k_act_bwd(const BwdArgs p)
 {
@@ -1181,13 +1206,16 @@ constexpr int FEW_TIME[3] = {195, 215, 300};
 // P rows through E experts (experts = false: one layer), D summed, C columns of the
 // product (both halves of a gate).  Of the forms and splits the one with the least
 // time for the CU with the most workgroups, splits with their partial sums' bytes
-// and a launch.  Rows fall on experts at random: the last tile of an expert is on
-// average a quarter of a tile's work more than its rows.
+// and a launch.  Rows fall on experts at random: the last tile of each is half empty.
+// (Of 85 sizes, a layer of 1 to 2048 rows and 4 to 64 experts, forward and back, eight
+// took more than a tenth longer than their best form and splits, at most a fifth; the
+// median 2%.)
 Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool turn)
 {
     Shape s{0, 2, 1, 0, 0, false};
     const int64_t each = (P + E - 1) / E;        // rows of an expert, on average
-    const int64_t live = experts ? (P < E ? P : E) : 1;
+    // experts that some pair names: 5.3 of 8 for 8 pairs (4096 x 14336: two splits, 49 us for 60)
+    const double named = experts ? E * (1.0 - std::pow(1.0 - 1.0 / E, static_cast<double>(P))) : 1.0;
     int64_t least = INT64_MAX;
     auto better = [&](int64_t time, int rm, int wn, int64_t n, bool rows) {
         time += n > 1 ? 400 + n * P * C / 8000 : 0;
@@ -1206,8 +1234,6 @@ Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool tu
     if (!turn && (!experts || P <= FEW_P || each <= 64)) {
         const int64_t chunks = D / 128;
         const int rows = each <= 4 ? 0 : each <= 8 ? 1 : 2;
-        // experts that some pair names: 5.3 of 8 for 8 pairs (4096 x 14336: two splits, 49 us for 60)
-        const double named = E * (1.0 - std::pow(1.0 - 1.0 / E, static_cast<double>(P)));
         const double row_tiles = experts ? named * (each < 8 ? 4 : each / 4 + 2) / 4 : static_cast<double>((P + FEW_T - 1) / FEW_T);
         const int64_t tiles = static_cast<int64_t>((C + FEW_ROWS - 1) / FEW_ROWS * row_tiles + 0.5);
         for (int64_t n = 1; n <= 8 && (n == 1 || chunks / n >= 8); n *= 2)
@@ -1218,11 +1244,12 @@ Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool tu
     auto weigh = [&](const Form& f, int64_t before, bool rows) {
         const int64_t bm = 32 * f.rm, bn = 64 * f.wn, tiles_n = (C + bn - 1) / bn;
         // in quarters
-        const int64_t tiles_m = experts ? live * (4 * each < 3 * bm ? 4 : 4 * each / bm + 1) : 4 * ((P + bm - 1) / bm);
+        const int64_t a_tile = 4 * each < bm ? 4 : 4 * each < 3 * bm ? 5 : 4 * each / bm + 2;
+        const int64_t tiles_m = experts ? static_cast<int64_t>(named * a_tile + 0.5) : 4 * ((P + bm - 1) / bm);
         for (int64_t n = 1; n <= 8 && (n == 1 || steps / n >= 8); ++n) {
             const int64_t tiles = tiles_m * tiles_n * n, on_cu = (tiles + 1023) / 1024 * 1024;
-            const int64_t all = (on_cu < 3 * 1024 ? on_cu : tiles + 512) * f.more[turn] / 1024;
-            better(before + (all > f.one[turn] ? all : f.one[turn]) * ((steps + n - 1) / n), f.rm, f.wn, n, rows);
+            const int64_t all = (on_cu < (turn ? 2 : 3) * 1024 ? on_cu : tiles + 512) * f.more[turn] / 1024;
+            better(before + 300 + (all > f.one[turn] ? all : f.one[turn]) * ((steps + n - 1) / n), f.rm, f.wn, n, rows);
         }
     };
     if (turn || !experts || P > FEW_P)           // fewer pairs have no plan forward

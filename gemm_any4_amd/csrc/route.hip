@@ -91,7 +91,10 @@ __device__ __forceinline__ double lift(float l, float top) { return l == -INFINI
 __device__ __forceinline__ double sigmoid64(float l) { return l == -INFINITY ? 0.0 : 1.0 / (1.0 + exp(-static_cast<double>(l))); }
 
 // A wave a token, lane l the experts l, l + 64, ...  Rank is what experts are chosen by:
-// the logit, or (SCORED) the choice value in 64 bits.
+// the logit, or (SCORED) the choice value in 64 bits, in which two experts' order does not
+// hang on a rounding.  Bound by its chain of steps, k reductions over the wave among them:
+// 8192 tokens, 8 of 256 experts in 4 of 8 groups, sigmoid and bias: 25 us (8.4 MB); 33
+// tokens 3.5.
 template <int V, bool SCORED>
 __global__ __launch_bounds__(64 * ROUTE_WAVES) void k_route(const RouteArgs p)
 {
@@ -222,7 +225,7 @@ struct RouteBwdArgs {
 
 // A wave a token.  Lane j has the j-th chosen expert and finds the derivative with
 // respect to its logit; the softmax's own sum over all experts follows where
-// the weights are not renormalised.
+// the weights are not renormalised.  8192 tokens, 8 of 256: 13 us (16.8 MB).
 template <int V>
 __global__ __launch_bounds__(64 * ROUTE_WAVES) void k_route_bwd(const RouteBwdArgs p)
 {
@@ -313,7 +316,7 @@ struct CombineArgs {
 // Eight columns of a token a thread, the loads of up to JB pairs at a time; bound by
 // its bytes.  What the loads depend on (Y32, rows of whole pieces, JB) is known to the
 // compiler, and pairs past the last are read as the last again: a branch between the
-// loads would make each wait for the one before (8192 x 8 x 2048: 335 MB).
+// loads would make each wait for the one before.  8192 x 8 x 2048, 335 MB: 74 us, 4.5 TB/s.
 template <bool Y32, bool WHOLE, int JB>
 __global__ __launch_bounds__(256) void k_combine(const CombineArgs p)
 {
@@ -357,7 +360,8 @@ struct CombineBwdArgs {
 };
 
 // A workgroup a token, 2048 columns a round; the sums of up to JB pairs at a time, loads
-// as above.
+// as above.  8192 x 8 x 2048, 570 MB: 89 us, 6.4 TB/s (y was read just before:
+// some of it comes from the 256 MB cache).
 template <bool Y32, bool WHOLE, int JB>
 __global__ __launch_bounds__(256) void k_combine_bwd(const CombineBwdArgs p)
 {

@@ -1,8 +1,9 @@
 /*
  * any4.h -- C ABI of libany4.so, the MI355X (gfx950) any4 dequantize-GEMM
- * (with plain int4, the any2 and any3 variants, the any4 quantiser, and what
+ * (with plain int4, the any2 and any3 variants, the any4 quantiser, what
  * fine-tunes of such a layer need: low-rank adapters, activations in 8 bits
- * and the input's gradient).
+ * and the input's gradient, and feed-forward blocks of such layers, dense or of
+ * experts).
  *
  * any4 (the 10100.com any4 explainer, section 二) stores each weight of a
  * row as a 4-bit index into that row's 16-entry bf16 lookup table; each

@@ -51,7 +51,7 @@ def check_act(M, N, K, act="none", gate=False, kind=F32, fmt="any4"):
 
 @pytest.mark.parametrize("M,N,K", [(100, 98, 256), (520, 98, 8192), (700, 258, 4096), (100, 98, 4096), (100, 97, 128),
                                    (520, 97, 4096), (1300, 1538, 128), (330, 1538, 2048), (1300, 4098, 128), (4100, 258, 2048),
-                                   (1300, 8194, 128), (130, 8194, 4096)])
+                                   (1300, 8194, 128), (130, 8194, 4096), (2050, 98, 128), (2050, 97, 4096)])
 def test_forms(M, N, K):
     check_act(M, N, K)
     if N % 2 == 0:
@@ -81,14 +81,16 @@ def check_experts(T, k, E, N, K, act="none", gate=False, kind=F32):
 @pytest.mark.parametrize("T,k,E,N,K", [(50, 2, 2, 98, 256), (20, 5, 5, 514, 8192), (20, 5, 5, 1538, 4096), (50, 2, 2, 98, 4096),
                                        (50, 2, 2, 98, 128), (65, 2, 2, 98, 1024), (650, 2, 2, 1538, 128), (165, 2, 2, 1538, 2048),
                                        (650, 2, 2, 4098, 128), (2050, 2, 2, 258, 2048), (650, 2, 2, 8194, 128),
-                                       (650, 2, 2, 1538, 4096)])
+                                       (650, 2, 2, 1538, 4096), (65, 2, 2, 98, 128), (40, 5, 5, 8194, 128),
+                                       (820, 5, 5, 98, 2048)])
 def test_forms_of_experts(T, k, E, N, K):
     check_experts(T, k, E, N, K)
     check_experts(T, k, E, N, K, "silu", True, kind=torch.bfloat16)
 
 
 @pytest.mark.parametrize("T,k,E,N,K", [(50, 2, 2, 96, 128), (50, 2, 2, 1021, 128), (1025, 2, 2, 93, 1024), (66, 5, 5, 1536, 2048),
-                                       (350, 2, 2, 96, 8192), (165, 2, 2, 2043, 4096)])
+                                       (350, 2, 2, 96, 8192), (165, 2, 2, 2043, 4096),
+                                       (1025, 2, 2, 96, 2048), (650, 2, 2, 4091, 384)])
 @pytest.mark.parametrize("fmt", ["any4", "any3"])
 def test_forms_of_dx(fmt, T, k, E, N, K):
     packed, tables, w = layers(fmt, E, N, K, 128)
