@@ -146,7 +146,8 @@ __device__ __forceinline__ void activate_both(float z, int act, float& f, float&
     case ACT_GELU_TANH: {
         const float p = sigmoid(GELU_C * (z + GELU_D * z * z * z));
         f = z * p;
-        slope = p + z * p * (1.0f - p) * GELU_C * (1.0f + 3.0f * GELU_D * z * z);
+        const float turn = p * (1.0f - p);       // 0 before z * z is no longer finite
+        slope = turn > 0.0f ? p + z * turn * GELU_C * (1.0f + 3.0f * GELU_D * z * z) : p;
         break;
     }
     default:

@@ -261,6 +261,29 @@ def test_slopes_against_differences(act):
     close(dz, want, torch.full_like(want, h * h + 2.0 ** -17))
 
 
+@pytest.mark.parametrize("act", ACTS)
+def test_values_far_out(act):
+    """Up to the largest finite ones an activation and its slope are those of z or of 0.
+    At |z| = 30 silu and its slope are off by |z| e^-|z| < 30 * 9.4e-14 < 2^-38, the others
+    and values farther out by less; all factors here are at most 1."""
+    same = lambda got, want: bool(((got - want).abs() <= 2.0 ** -38).all())      # noqa: E731
+    z = torch.tensor([[s * v for v in (30.0, 1e4, 1e13, 1e19, 3e19, 1e30, 3e38) for s in (1, -1)]], dtype=torch.bfloat16, device=gu.DEV)
+    up = act == "none"
+    dz, dbias = any4.act_backward(torch.ones_like(z), z, act)
+    want = ((z > 0) | up).float()
+    assert same(dz.float(), want) and same(dbias, want[0])
+    gated = torch.cat([z, torch.full_like(z, 0.5)], dim=1)
+    dz = any4.act_backward(torch.full_like(z, 2.0 ** -8), gated, act, gate=True)[0].float()
+    assert same(dz[:, :14], want * 2.0 ** -9) and same(dz[:, 14:], want * z.float() * 2.0 ** -8)
+    # an identity layer: forward
+    one = lambda v: torch.full((16, 1), v, dtype=torch.bfloat16, device=gu.DEV)      # noqa: E731
+    packed = any4.pack(torch.zeros((16, 128), dtype=torch.uint8, device=gu.DEV))
+    lut = torch.ones((16, 16), dtype=torch.bfloat16, device=gu.DEV)
+    x = torch.zeros((14, 128), dtype=torch.bfloat16, device=gu.DEV)
+    x[:, 5] = z[0]
+    assert same(any4.gemm_act(x, packed, lut, one(1.0), one(0.0), 128, act=act)[:, 3].float(), (want * z.float())[0])
+
+
 # ---------------------------------------------------------------------------
 # experts
 # ---------------------------------------------------------------------------
