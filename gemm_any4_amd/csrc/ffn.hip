@@ -1072,30 +1072,33 @@ struct BwdArgs {
 
 constexpr int BWD_COLS = 8 * WAVE;           // columns of out of a workgroup
 
-// A wave takes 512 columns of every fourth row of a slab, two rows at a time; the
-// column sums of the four waves meet in LDS.  Bound by its bytes.  What the loads depend
+constexpr int BWD_FEW = 64;                  // rows of the one slab of few
+
+// LANES of a wave take eight columns each, its other lanes other rows: 512 columns of
+// every fourth row of a slab, two rows at a time (LANES 64, four waves), or 64 columns of
+// 64 rows (LANES 8, eight waves).  The column sums meet in LDS.  Bound by its bytes.  What the loads depend
 // on is known to the compiler, and a row past the last is the last again: a branch
 // between them would make each wait for the one before.  4096 x 28672, gated, 587 MB:
 // 117 us, 5.0 TB/s, a copy's rate.
-template <bool DY32, bool Z32, bool GATE, bool WHOLE>
-__global__ __launch_bounds__(256) void k_act_bwd(const BwdArgs p)
+template <bool DY32, bool Z32, bool GATE, bool WHOLE, int WAVES, int LANES>
+__global__ __launch_bounds__(WAVE * WAVES) void k_act_bwd(const BwdArgs p)
 {
-    __shared__ float red[4][2][8][WAVE];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col = blockIdx.x * BWD_COLS + 8 * lane;
+    constexpr int COLS = 8 * LANES, AT_ONCE = WAVES * (WAVE / LANES), ROWS = WAVES == 4 ? 2 : 1;
+    __shared__ float red[AT_ONCE][GATE ? 2 : 1][8][LANES];
+    const int lane = threadIdx.x % LANES, w = threadIdx.x / LANES, col = blockIdx.x * COLS + 8 * lane;
     const int m0 = blockIdx.y * p.slab, m1 = m0 + p.slab < p.M ? m0 + p.slab : p.M;
     const int left = p.No - col, valid = WHOLE ? 8 : left;
-    constexpr int ROWS = 2;
     float sum[2][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         sum[0][i] = sum[1][i] = 0.0f;
-    for (int m = m0 + w; m < m1; m += 4 * ROWS) {
+    for (int m = m0 + w; m < m1; m += AT_ONCE * ROWS) {
         if (left <= 0)
             break;
         float d[ROWS][8], zg[ROWS][8], zu[ROWS][8];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            const size_t row = m + 4 * r < m1 ? m + 4 * r : m;
+            const size_t row = m + AT_ONCE * r < m1 ? m + AT_ONCE * r : m;
             get_values(p.dy, DY32, row * p.No + col, valid, d[r]);
             get_values(p.z, Z32, row * p.N + col, valid, zg[r]);
             if constexpr (GATE)
@@ -1103,7 +1106,7 @@ __global__ __launch_bounds__(256) void k_act_bwd(const BwdArgs p)
         }
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            if (m + 4 * r >= m1)
+            if (m + AT_ONCE * r >= m1)
                 break;
             float a[8], b[8];
 #pragma unroll
@@ -1118,7 +1121,7 @@ __global__ __launch_bounds__(256) void k_act_bwd(const BwdArgs p)
                 }
                 sum[0][i] += a[i];
             }
-            const size_t at = static_cast<size_t>(m + 4 * r) * p.N + col;
+            const size_t at = static_cast<size_t>(m + AT_ONCE * r) * p.N + col;
             put_values(p.dz, 0, at, valid, a);
             if constexpr (GATE)
                 put_values(p.dz, 0, at + p.No, valid, b);
@@ -1127,17 +1130,20 @@ __global__ __launch_bounds__(256) void k_act_bwd(const BwdArgs p)
     if (!p.part)
         return;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < (GATE ? 2 : 1); ++h)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             red[w][h][i][lane] = sum[h][i];
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * BWD_COLS; i += 256) {
-        const int h = i / BWD_COLS, o = i % BWD_COLS, c = blockIdx.x * BWD_COLS + o;
-        if (c >= p.No || (h && !GATE))
+    for (int i = threadIdx.x; i < (GATE ? 2 : 1) * COLS; i += WAVE * WAVES) {
+        const int h = i / COLS, o = i % COLS, c = blockIdx.x * COLS + o;
+        if (c >= p.No)
             continue;
-        p.part[static_cast<size_t>(blockIdx.y) * p.N + h * p.No + c] =
-            red[0][h][o & 7][o >> 3] + red[1][h][o & 7][o >> 3] + red[2][h][o & 7][o >> 3] + red[3][h][o & 7][o >> 3];
+        float v = 0.0f;
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j)
+            v += red[j][h][o & 7][o >> 3];
+        p.part[static_cast<size_t>(blockIdx.y) * p.N + h * p.No + c] = v;
     }
 }
 
@@ -1388,8 +1394,13 @@ any4_status product(int fmt, const Rows& rows, int64_t X, const void* x, bool x3
     return launch_status();
 }
 
-int64_t bwd_slab(int64_t M, int64_t No)
+int64_t bwd_slab(int64_t M, int64_t No, bool bias)
 {
+    // Few rows are one slab, whose sums are dbias itself: no second launch, no workspace.
+    // 64 x 512: a call 9.7 us for 13.9, captured in a graph 3.2 for 5.1; 64 x 28672, gated,
+    // 4.1 for 6.9.
+    if (bias && M <= BWD_FEW)
+        return M;
     // about eight workgroups a CU, at least four rows each
     const int64_t across = (No + BWD_COLS - 1) / BWD_COLS, want = (2048 + across - 1) / across;
     const int64_t slab = (M + want - 1) / want;
@@ -1433,8 +1444,8 @@ size_t any4_act_backward_workspace_size(int64_t M, int64_t N, int gate)
 {
     if (M <= 0 || N <= 0 || M > MAX_PAIRS || N > GIB2 / 4 || N >= GIB2 / 2 / M || (gate && N % 2))
         return 0;
-    const int64_t slab = bwd_slab(M, gate ? N / 2 : N), slabs = (M + slab - 1) / slab;
-    return up256(static_cast<size_t>(slabs) * N * 4);
+    const int64_t slab = bwd_slab(M, gate ? N / 2 : N, true), slabs = (M + slab - 1) / slab;
+    return slabs == 1 ? 0 : up256(static_cast<size_t>(slabs) * N * 4);
 }
 
 any4_status any4_act_backward(const void* dy, int dy_f32, const void* z, int z_f32, uint16_t* dz, float* dbias, any4_activation act,
@@ -1444,21 +1455,31 @@ any4_status any4_act_backward(const void* dy, int dy_f32, const void* z, int z_f
         return ANY4_E_SHAPE;
     if (N == 0 || (M == 0 && !dbias))
         return ANY4_OK;
-    if (M > 0 && (!dy || !z || !dz || (dbias && !workspace)))
+    const size_t need = dbias ? any4_act_backward_workspace_size(M, N, gate) : 0;
+    if (M > 0 && (!dy || !z || !dz || (need && !workspace)))
         return ANY4_E_NULL;
     if (!is_aligned(dbias, 4) || (M > 0 && (!is_aligned(dy, dy_f32 ? 4 : 2) || !is_aligned(z, z_f32 ? 4 : 2) || !is_aligned(dz, 2) || !is_aligned(workspace, 16))))
         return ANY4_E_ALIGN;
     const int n = static_cast<int>(N), no = static_cast<int>(gate ? N / 2 : N);
-    const int slab = M > 0 ? static_cast<int>(bwd_slab(M, no)) : 1, slabs = static_cast<int>((M + slab - 1) / slab);
-    if (dbias && workspace_bytes < any4_act_backward_workspace_size(M, N, gate))
+    const int slab = M > 0 ? static_cast<int>(bwd_slab(M, no, dbias != nullptr)) : 1, slabs = static_cast<int>((M + slab - 1) / slab);
+    if (need && workspace_bytes < need)
         return ANY4_E_WORKSPACE;
     (void)hipGetLastError();
-    float* part = dbias ? static_cast<float*>(workspace) : nullptr;
+    float* part = need ? static_cast<float*>(workspace) : dbias;
     if (M > 0) {
         const BwdArgs a{dy, z, dz, part, static_cast<int>(M), n, no, static_cast<int>(act), slab};
-        const dim3 grid(static_cast<unsigned>((no + BWD_COLS - 1) / BWD_COLS), static_cast<unsigned>(slabs));
+        const bool few = slabs == 1 && dbias;
+        const int cols = few ? 64 : BWD_COLS;
+        const dim3 grid(static_cast<unsigned>((no + cols - 1) / cols), static_cast<unsigned>(slabs));
         auto launch = [&](auto dy32, auto z32) {
-#define BWD(GATE_, WHOLE_) hipLaunchKernelGGL((k_act_bwd<decltype(dy32)::value, decltype(z32)::value, GATE_, WHOLE_>), grid, dim3(256), 0, stream, a)
+#define BWD(GATE_, WHOLE_)                                                                                                     \
+    do {                                                                                                                       \
+        constexpr bool D = decltype(dy32)::value, Z = decltype(z32)::value;                                                    \
+        if (few)                                                                                                               \
+            hipLaunchKernelGGL((k_act_bwd<D, Z, GATE_, WHOLE_, 8, 8>), grid, dim3(8 * WAVE), 0, stream, a);                    \
+        else                                                                                                                   \
+            hipLaunchKernelGGL((k_act_bwd<D, Z, GATE_, WHOLE_, 4, WAVE>), grid, dim3(4 * WAVE), 0, stream, a);                 \
+    } while (0)
             if (gate && no % 8 == 0) BWD(true, true);
             else if (gate) BWD(true, false);
             else if (no % 8 == 0) BWD(false, true);
@@ -1470,7 +1491,7 @@ any4_status any4_act_backward(const void* dy, int dy_f32, const void* z, int z_f
         else if (z_f32) launch(std::false_type{}, std::true_type{});
         else launch(std::false_type{}, std::false_type{});
     }
-    if (dbias)
+    if (dbias && slabs != 1)         // none: zeros
         hipLaunchKernelGGL(k_bias_sum, dim3(static_cast<unsigned>((n + WAVE - 1) / WAVE)), dim3(256), 0, stream, part, dbias, n, slabs);
     return launch_status();
 }

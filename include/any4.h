@@ -573,7 +573,7 @@ any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* 
  *   dbias  device, [N] fp32, or NULL (workspace is then not used)
  *   0 <= M <= 2^20, 0 <= N <= 2^29, M*N below 2^30.  M = 0 writes dbias = 0.
  *   workspace  device, 16-byte aligned, any4_act_backward_workspace_size(M, N, gate)
- *          bytes, with dbias.
+ *          bytes, required with dbias where that is not 0.
  *   dy, z and dz need 2-byte alignment, dbias 4.
  * Errors: as any4_gemm_act.
  */
