@@ -35,9 +35,9 @@ forms: stacked layers, each row through its expert), combine and
 combine_backward (the weighted sum of the experts' outputs).  What one of these
 calls writes for another (z, an output for combine, an input's gradient for
 act_backward or combine) may be a bf16 tensor or an fp32 one, given as z or out.
-These and the calls for fine-tunes take tensors of any GPU, run on that GPU's current stream (or `stream`,
-on which their outputs and workspaces are then allocated too) and can be
-captured into a graph.
+These and the calls for fine-tunes take tensors of any GPU, run on that GPU's
+current stream (or `stream`, on which their outputs and workspaces are then
+allocated too) and can be captured into a graph.
 """
 from __future__ import annotations
 
@@ -954,8 +954,8 @@ ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-def gemm_act_raw(fmt, x_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, residual_ptr, z_ptr, out_ptr, act, gate,
-                 M, N, K, g, ws_ptr, ws_bytes, stream=None, z_f32=0, out_f32=0) -> int:
+def gemm_act_raw(fmt, x_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, residual_ptr, z_ptr, out_ptr, act,
+                 gate, M, N, K, g, ws_ptr, ws_bytes, stream=None, z_f32=0, out_f32=0) -> int:
     """fmt, act: the numbers of any4_format and any4_activation."""
     return lib().any4_gemm_act(fmt, x_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, residual_ptr, z_ptr,
                                z_f32, out_ptr, out_f32, act, gate, M, N, K, g, ws_ptr, ws_bytes, _stream(stream))
@@ -982,13 +982,13 @@ def route_backward_raw(dw_ptr, logits_ptr, bf16, ids_ptr, dlogits_ptr, score, re
 def experts_gemm_raw(fmt, x_ptr, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, ids_ptr, plan_ptr, z_ptr,
                      out_ptr, act, gate, T, k, E, N, K, g, ws_ptr, ws_bytes, stream=None, z_f32=0, out_f32=0,
                      x_f32=0) -> int:
-    return lib().any4_experts_gemm(fmt, x_ptr, x_f32, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr, ids_ptr,
-                                   plan_ptr, z_ptr, z_f32, out_ptr, out_f32, act, gate, T, k, E, N, K, g, ws_ptr,
-                                   ws_bytes, _stream(stream))
+    return lib().any4_experts_gemm(fmt, x_ptr, x_f32, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr,
+                                   ids_ptr, plan_ptr, z_ptr, z_f32, out_ptr, out_f32, act, gate, T, k, E, N, K, g,
+                                   ws_ptr, ws_bytes, _stream(stream))
 
 
-def experts_gemm_dx_raw(fmt, dy_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, ids_ptr, plan_ptr, dx_ptr, T, k, E, N, K, g,
-                        ws_ptr, ws_bytes, stream=None, dx_f32=0) -> int:
+def experts_gemm_dx_raw(fmt, dy_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, ids_ptr, plan_ptr, dx_ptr, T, k, E, N, K,
+                        g, ws_ptr, ws_bytes, stream=None, dx_f32=0) -> int:
     return lib().any4_experts_gemm_dx(fmt, dy_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, ids_ptr, plan_ptr, dx_ptr,
                                       dx_f32, T, k, E, N, K, g, ws_ptr, ws_bytes, _stream(stream))
 
@@ -1133,8 +1133,9 @@ def act_backward(dy: torch.Tensor, z: torch.Tensor, act: str, gate: bool = False
                  dz: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
                  workspace: torch.Tensor | None = None, stream=None) -> tuple:
     """(dz, dbias) of an epilogue for dy [..., No], from z [..., N] as gemm_act or
-    experts_gemm kept it (bf16 or fp32): dz bf16 (may be z), dbias fp32 [N], the sum over all rows (need_bias = False: None).  The gradient of the product's
-    input is gemm_dx (experts_gemm_dx) of dz, that of the residual dy itself."""
+    experts_gemm kept it (either may be bf16 or fp32): dz bf16 (may be a bf16 z itself),
+    dbias fp32 [N], the sum over all rows (need_bias = False: None).  The gradient of the
+    product's input is gemm_dx (experts_gemm_dx) of dz, that of the residual dy itself."""
     if not z.is_cuda:
         raise ValueError("z must be a GPU tensor")
     if z.dim() < 2:
@@ -1253,8 +1254,8 @@ def _experts_gemm(fmt: int, x, packed, lut, alpha, beta, g, ids, bias, act, gate
     with _on(dev, stream):
         out, p_out, out32 = _result(out, "out", (T, k, No), dev)
         ws, p_ws, nbytes = _scratch(workspace, experts_workspace_size(T, k, E, N, K, g), dev)
-        check(lib().any4_experts_gemm(fmt, p_x, x32, 1 if per_pair else 0, p_packed, p_lut, p_alpha, p_beta, p_bias, p_ids,
-                                      p_plan, p_z, z32, p_out, out32, number, 1 if gate else 0, T, k, E, N, K, g,
+        check(lib().any4_experts_gemm(fmt, p_x, x32, 1 if per_pair else 0, p_packed, p_lut, p_alpha, p_beta, p_bias,
+                                      p_ids, p_plan, p_z, z32, p_out, out32, number, 1 if gate else 0, T, k, E, N, K, g,
                                       p_ws, nbytes, _current_handle(dev.index)))
     return out
 
@@ -1267,10 +1268,10 @@ def experts_gemm(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha
     any4 layers [N, K] stacked: packed the E layers' bytes one after another, lut
     [E, N, 16], alpha and beta [E, N, K/g], bias [E, N].
 
-    x bf16 (up to 64 pairs: or fp32) [T, K], or [T, k, K]: a row for each pair (the block's second product).  act, gate
-    and z ([T, k, N]) as in gemm_act.  A pair whose id is not in 0..E-1 gives zeros.
-    plan: of experts_plan(ids, E), kept over the products of a block.  z and out
-    may be bf16 or fp32."""
+    x bf16 [T, K], or [T, k, K]: a row for each pair (the block's second product); for up
+    to 64 pairs fp32 too.  act, gate and z ([T, k, N]) as in gemm_act.  A pair whose id
+    is not in 0..E-1 gives zeros.  plan: of experts_plan(ids, E), kept over the products of a
+    block.  z and out may be bf16 or fp32."""
     return _experts_gemm(0, x, packed, lut, alpha, beta, g, ids, bias, act, gate, z, plan, out, workspace, stream)
 
 

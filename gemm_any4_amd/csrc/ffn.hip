@@ -1072,11 +1072,11 @@ struct BwdArgs {
 
 constexpr int BWD_COLS = 8 * WAVE;           // columns of out of a workgroup
 
-constexpr int BWD_FEW = 64;                  // rows of the one slab of few
+constexpr int BWD_FEW = 128;                 // rows of the one slab of few
 
 // LANES of a wave take eight columns each, its other lanes other rows: 512 columns of
 // every fourth row of a slab, two rows at a time (LANES 64, four waves), or 64 columns of
-// 64 rows (LANES 8, eight waves).  The column sums meet in LDS.  Bound by its bytes.  What the loads depend
+// 64 rows at a time (LANES 8, eight waves).  The column sums meet in LDS.  Bound by its bytes.  What the loads depend
 // on is known to the compiler, and a row past the last is the last again: a branch
 // between them would make each wait for the one before.  4096 x 28672, gated, 587 MB:
 // 117 us, 5.0 TB/s, a copy's rate.
@@ -1397,8 +1397,8 @@ any4_status product(int fmt, const Rows& rows, int64_t X, const void* x, bool x3
 int64_t bwd_slab(int64_t M, int64_t No, bool bias)
 {
     // Few rows are one slab, whose sums are dbias itself: no second launch, no workspace.
-    // 64 x 512: a call 9.7 us for 13.9, captured in a graph 3.2 for 5.1; 64 x 28672, gated,
-    // 4.1 for 6.9.
+    // 64 x 512: a call 9.7 us for 13.9, captured in a graph 3.2 for 5.1; 128 x 28672, gated,
+    // 9.6 for 13.7, and 6.0 for 9.3.  (256 x 2048 in a graph: 7.6 for 6.4.)
     if (bias && M <= BWD_FEW)
         return M;
     // about eight workgroups a CU, at least four rows each

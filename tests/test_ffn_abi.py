@@ -103,7 +103,7 @@ def test_empty_calls_are_no_ops():
 
 
 def test_act_backward_errors():
-    def call(dy=A, z=A, dz=A, dbias=A, act=2, gate=0, M=65, N=16, ws=A, ws_bytes=BIG):
+    def call(dy=A, z=A, dz=A, dbias=A, act=2, gate=0, M=129, N=16, ws=A, ws_bytes=BIG):
         return any4.act_backward_raw(dy, z, dz, dbias, act, gate, M, N, ws, ws_bytes, stream=0)
     for bad in (dict(M=-1), dict(N=-1), dict(M=(1 << 20) + 1), dict(M=1 << 20, N=1024), dict(N=1 << 31), dict(act=5),
                 dict(act=-1), dict(gate=1, N=15)):
@@ -112,8 +112,8 @@ def test_act_backward_errors():
         assert call(**{name: None}) == 1
     for name, off in (("dy", 1), ("z", 1), ("dz", 1), ("dbias", 2), ("ws", 8)):
         assert call(**{name: A + off}) == 3
-    need = any4.act_backward_workspace_size(65, 16, 0)
-    assert need > 0 and call(ws_bytes=need - 1) == 4 and any4.act_backward_workspace_size(64, 16, 0) == 0
+    need = any4.act_backward_workspace_size(129, 16, 0)
+    assert need > 0 and call(ws_bytes=need - 1) == 4 and any4.act_backward_workspace_size(128, 16, 0) == 0
     assert call(None, None, None, None, N=0, ws=None) == 0 and call(None, None, None, None, M=0, ws=None) == 0
 
 

@@ -231,7 +231,7 @@ def check_backward(M, N, act, gate):
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("gate", [False, True])
-@pytest.mark.parametrize("M,N", [(1, 2), (5, 34), (64, 512), (33, 1030), (257, 2050), (1000, 130)])
+@pytest.mark.parametrize("M,N", [(1, 2), (5, 34), (64, 512), (33, 1030), (128, 98), (129, 98), (257, 2050), (1000, 130)])
 def test_act_backward(act, gate, M, N):
     check_backward(M, N, act, gate)
 

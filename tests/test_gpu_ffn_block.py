@@ -367,16 +367,16 @@ def test_a_plan_of_other_sizes_leaves_the_results(T, k, N, K):
 def test_workspaces_of_the_callers():
     """Exactly as large as asked for, with others' bytes behind; and too small."""
     packed, tables, _ = layers("any4", 2, 98, 4096, 128)
-    ids, x, dy, z = choose(50, 2, 2), normal(7, 50, 4096), normal(9, 50, 2, 98), normal(5, 100, 98)
+    ids, x, dy, z = choose(50, 2, 2), normal(7, 50, 4096), normal(9, 50, 2, 98), normal(5, 150, 98)
     calls = [(any4.gemm_act_workspace_size(50, 98, 4096, 128),
               lambda ws: any4.gemm_act(x, packed[:packed.numel() // 2], *[t[0] for t in tables], 128, workspace=ws)),
              (any4.experts_workspace_size(50, 2, 2, 98, 4096, 128),
               lambda ws: any4.experts_gemm(x, packed, *tables, 128, ids, workspace=ws)),
              (any4.experts_dx_workspace_size(50, 2, 2, 98, 4096, 128),
               lambda ws: any4.experts_gemm_dx(dy, packed, *tables, 128, ids, workspace=ws)),
-             (any4.act_backward_workspace_size(100, 98, True),
-              lambda ws: torch.cat([t.flatten().float() for t in any4.act_backward(dy.view(100, 98)[:, :49].contiguous(), z, "silu",
-                                                                                   gate=True, workspace=ws)]))]
+             (any4.act_backward_workspace_size(150, 98, True),
+              lambda ws: torch.cat([t.flatten().float() for t in any4.act_backward(normal(10, 150, 49), z, "silu", gate=True,
+                                                                                   workspace=ws)]))]
     for need, call in calls:
         assert need > 0
         room = torch.full((need + 256,), 77, dtype=torch.uint8, device=gu.DEV)
