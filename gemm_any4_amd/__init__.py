@@ -34,7 +34,9 @@ experts_plan, experts_gemm and experts_gemm_dx (and their int4, any2 and any3
 forms: stacked layers, each row through its expert), combine and
 combine_backward (the weighted sum of the experts' outputs).  What one of these
 calls writes for another (z, an output for combine, an input's gradient for
-act_backward or combine) may be a bf16 tensor or an fp32 one, given as z or out.
+act_backward or combine) may be a bf16 tensor or an fp32 one, given as z or out;
+what enters another product (experts_gemm's out) may be in two bf16 parts, a bf16 tensor
+with one more dimension of 2 in front: hi, the values cut to bf16, and lo, the rest.
 These and the calls for fine-tunes take tensors of any GPU, run on that GPU's
 current stream (or `stream`, on which their outputs and workspaces are then
 allocated too) and can be captured into a graph.
@@ -53,6 +55,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libany4.so")
 
 ANY4_OK = 0
+ANY4_PARTS = -1         # in the place of a flag that says fp32: values in two bf16 parts
 _STATUS_NAMES = {0: "ANY4_OK", 1: "ANY4_E_NULL", 2: "ANY4_E_SHAPE", 3: "ANY4_E_ALIGN",
                  4: "ANY4_E_WORKSPACE", 5: "ANY4_E_HIP"}
 
@@ -66,7 +69,7 @@ EXPORTS = ("any4_packed_bytes", "any4_pack", "any4_dequant", "any4_gemm_workspac
            "any4_act8_load", "any4_gemm_dx_workspace_size", "any4_gemm_dx", "any4_gemm_int4_dx",
            "any2_gemm_dx", "any3_gemm_dx", "any4_gemm_act_workspace_size", "any4_gemm_act",
            "any4_act_backward_workspace_size", "any4_act_backward", "any4_route", "any4_route_backward",
-           "any4_experts_workspace_size", "any4_experts_gemm", "any4_experts_dx_workspace_size",
+           "any4_experts_workspace_size", "any4_experts_parts_workspace_size", "any4_experts_gemm", "any4_experts_dx_workspace_size",
            "any4_experts_gemm_dx", "any4_combine", "any4_combine_backward")
 
 _lib = None
@@ -137,6 +140,7 @@ def lib() -> ctypes.CDLL:
                 ("any4_route_backward", ctypes.c_int,
                  [P, P, INT, P, P] + [INT] * 2 + [F32] + [I64] * 3 + [P]),
                 ("any4_experts_workspace_size", SZ, [I64] * 6),
+                ("any4_experts_parts_workspace_size", SZ, [I64] * 6),
                 ("any4_experts_gemm", ctypes.c_int,
                  [INT, P, INT, INT] + [P] * 8 + [INT, P] + [INT] * 3 + [I64] * 6 + [P, SZ, P]),
                 ("any4_experts_dx_workspace_size", SZ, [I64] * 6),
@@ -1017,6 +1021,11 @@ def experts_workspace_size(T: int, k: int, E: int, N: int, K: int, g: int) -> in
 
 
 @functools.lru_cache(maxsize=4096)      # constant for its sizes
+def experts_parts_workspace_size(T: int, k: int, E: int, N: int, K: int, g: int) -> int:
+    return int(lib().any4_experts_parts_workspace_size(T, k, E, N, K, g))
+
+
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
 def experts_dx_workspace_size(T: int, k: int, E: int, N: int, K: int, g: int) -> int:
     return int(lib().any4_experts_dx_workspace_size(T, k, E, N, K, g))
 
@@ -1051,6 +1060,11 @@ def _result(out: torch.Tensor | None, name: str, shape: tuple, device) -> tuple:
         out = torch.empty(shape, dtype=torch.bfloat16, device=device)
         return out, out.data_ptr() or None, 0
     return (out,) + _kept(out, name, shape, device)
+
+
+def _parts(t: torch.Tensor | None, shape: tuple) -> bool:
+    """Whether t is meant as values of this shape in two bf16 parts."""
+    return t is not None and t.dim() == len(shape) + 1
 
 
 def _layer(fmt: int, packed, lut, alpha, beta, g: int, dev, experts: bool) -> tuple:
@@ -1243,17 +1257,24 @@ def _experts_gemm(fmt: int, x, packed, lut, alpha, beta, g, ids, bias, act, gate
     dev, bf16 = x.device, torch.bfloat16
     E, N, K, p_packed, p_lut, p_alpha, p_beta = _layer(fmt, packed, lut, alpha, beta, g, dev, True)
     T, k, p_ids, p_plan = _pairs(ids, E, plan, dev)
-    No, per_pair = N // 2 if gate else N, x.dim() == 3
+    No, per_pair, parts = N // 2 if gate else N, x.dim() >= 3, _parts(x, (T, k, K))
     if gate and N % 2:
         raise ValueError("a gated layer must have an even number of rows")
-    p_x, x32 = _kept(x, "x", (T, k, K) if per_pair else (T, K), dev)
-    if x32 and T * k > 64:
-        raise ValueError("x may be fp32 for up to 64 pairs")
+    if parts:
+        p_x, x32 = _tensor(x, "x", bf16, (2, T, k, K), dev), ANY4_PARTS
+    else:
+        p_x, x32 = _kept(x, "x", (T, k, K) if per_pair else (T, K), dev)
+        if x32 and T * k > 64:
+            raise ValueError("x may be fp32 for up to 64 pairs (for more in two bf16 parts, [2, T, k, K])")
     p_bias, (p_z, z32) = _maybe(bias, "bias", bf16, (E, N), dev), _kept(z, "z", (T, k, N), dev)
     number = _choice("act", act, ACTIVATIONS)
     with _on(dev, stream):
-        out, p_out, out32 = _result(out, "out", (T, k, No), dev)
-        ws, p_ws, nbytes = _scratch(workspace, experts_workspace_size(T, k, E, N, K, g), dev)
+        if _parts(out, (T, k, No)):
+            p_out, out32 = _tensor(out, "out", bf16, (2, T, k, No), dev), ANY4_PARTS
+        else:
+            out, p_out, out32 = _result(out, "out", (T, k, No), dev)
+        size = experts_parts_workspace_size if parts else experts_workspace_size
+        ws, p_ws, nbytes = _scratch(workspace, size(T, k, E, N, K, g), dev)
         check(lib().any4_experts_gemm(fmt, p_x, x32, 1 if per_pair else 0, p_packed, p_lut, p_alpha, p_beta, p_bias,
                                       p_ids, p_plan, p_z, z32, p_out, out32, number, 1 if gate else 0, T, k, E, N, K, g,
                                       p_ws, nbytes, _current_handle(dev.index)))
@@ -1271,7 +1292,12 @@ def experts_gemm(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, alpha
     x bf16 [T, K], or [T, k, K]: a row for each pair (the block's second product); for up
     to 64 pairs fp32 too.  act, gate and z ([T, k, N]) as in gemm_act.  A pair whose id
     is not in 0..E-1 gives zeros.  plan: of experts_plan(ids, E), kept over the products of a
-    block.  z and out may be bf16 or fp32."""
+    block.  z and out may be bf16 or fp32.
+
+    Between a block's two products out and x may also be bf16 [2, T, k, .], the values in
+    two parts: the second product then takes 16 bits or more of each (a bf16 row has 8:
+    the block's error is 1.4 times that of a result that is only rounded at its end),
+    for twice its matrix work."""
     return _experts_gemm(0, x, packed, lut, alpha, beta, g, ids, bias, act, gate, z, plan, out, workspace, stream)
 
 

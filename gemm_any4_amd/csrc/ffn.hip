@@ -23,6 +23,7 @@ constexpr int MAX_EXPERTS = 1024;
 constexpr int STEP = 64;                                  // of the summed dimension, k_tile
 constexpr int FMT_BF16 = FMT_ANY3 + 1;                    // of k_tile: a layer that k_rows has laid out as bf16 rows
 constexpr int64_t MAX_PAIRS = static_cast<int64_t>(1) << 20;
+enum { X_BF16, X_F32, X_PARTS };     // how the rows of x are kept
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
@@ -163,13 +164,56 @@ struct Epilogue {
     const uint16_t* bias;        // [E][N] or null
     const uint16_t* residual;    // [P][No] or null
     void* z;                     // [P][N] or null
-    void* out;                   // [P][No]
+    void* out;                   // [P][No], in parts [2][P][No]
     float* part;                 // [S][P][N] or null (S = 1)
     int N, No, act, S;           // No = N / 2: gated
-    int z32, out32;              // fp32 instead of bf16
+    int z32, out32;              // fp32 instead of bf16; out32 ANY4_PARTS: two bf16 parts
+    size_t plane;                // in parts: from hi to lo
 
     __host__ __device__ __forceinline__ bool gated() const { return No != N; }
 };
+
+// fp32 as the bf16 parts hi + lo: hi cut off, lo what is left, rounded (2^-16 of the
+// value at most).  An infinity has no lo.
+__device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo)
+{
+    const uint32_t top = __builtin_bit_cast(uint32_t, v) & 0xffff0000u;
+    hi = top >> 16;
+    lo = f32_to_bf16(__builtin_isinf(v) ? 0.0f : v - __builtin_bit_cast(float, top));
+}
+
+__device__ __forceinline__ void put_outs(const Epilogue& q, size_t at, int valid, const float (&v)[8])
+{
+    if (q.out32 != ANY4_PARTS) {
+        put_values(q.out, q.out32, at, valid, v);
+        return;
+    }
+    u32x4_t hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h[2], l[2];
+        split(v[2 * i], h[0], l[0]);
+        split(v[2 * i + 1], h[1], l[1]);
+        hi[i] = h[0] | h[1] << 16;
+        lo[i] = l[0] | l[1] << 16;
+    }
+    uint16_t* out = static_cast<uint16_t*>(q.out) + at;
+    store8(out, hi, valid);
+    store8(out + q.plane, lo, valid);
+}
+
+__device__ __forceinline__ void put_out(const Epilogue& q, size_t at, float v)
+{
+    if (q.out32 != ANY4_PARTS) {
+        put_value(q.out, q.out32, at, v);
+        return;
+    }
+    uint32_t hi, lo;
+    split(v, hi, lo);
+    uint16_t* out = static_cast<uint16_t*>(q.out) + at;
+    out[0] = static_cast<uint16_t>(hi);
+    out[q.plane] = static_cast<uint16_t>(lo);
+}
 
 // Columns col .. col + 7 of pair p: v the (gate's) sums, u the up rows' where there
 // is a gate.
@@ -214,7 +258,7 @@ __device__ __forceinline__ void finish8(const Epilogue& q, int e, int p, int col
         for (int i = 0; i < 8; ++i)
             o[i] += r[i];
     }
-    put_values(q.out, q.out32, at, valid, o);
+    put_outs(q, at, valid, o);
 }
 
 // Where part i of n starts among `all` (below 2^25, n at most 64); the same for all
@@ -229,8 +273,9 @@ constexpr int FEW_ROWS = 64;         // rows of W of a workgroup
 struct FewArgs {
     Rows r;
     Layer w;
-    const void* x;           // bf16, or (X32) fp32
+    const void* x;
     Epilogue q;
+    size_t plane;            // X_PARTS: from hi to lo
 };
 
 template <int I, int N, typename F>
@@ -265,21 +310,16 @@ struct RowChunk {
     }
 };
 
-// fp32 values as the bf16 parts hi + lo: hi cut off, lo what is left, rounded (2^-16
-// of the value at most).  An infinity has no lo.
-__device__ __forceinline__ void split2(f32x4_t v, s16x4_t& hi, s16x4_t& lo)
+__device__ __forceinline__ void split4(f32x4_t v, s16x4_t& hi, s16x4_t& lo)
 {
     u32x2_t h, l;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         uint32_t top[2], rest[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float x = v[2 * i + j];
-            top[j] = __builtin_bit_cast(uint32_t, x) & 0xffff0000u;
-            rest[j] = f32_to_bf16(__builtin_isinf(x) ? 0.0f : x - __builtin_bit_cast(float, top[j]));
-        }
-        h[i] = top[0] >> 16 | top[1];
+        for (int j = 0; j < 2; ++j)
+            split(v[2 * i + j], top[j], rest[j]);
+        h[i] = top[0] | top[1] << 16;
         l[i] = rest[0] | rest[1] << 16;
     }
     hi = __builtin_bit_cast(s16x4_t, h);
@@ -287,8 +327,8 @@ __device__ __forceinline__ void split2(f32x4_t v, s16x4_t& hi, s16x4_t& lo)
 }
 
 // The product of 4 * NB rows of x with the lane's row of W over chunks s0 .. s1.  Rows
-// of fp32 are two of bf16.
-template <int FMT, int NB, bool X32>
+// of fp32 or in parts are two of bf16.
+template <int FMT, int NB, int X>
 __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, const int* own, int count, int s0, int s1,
                                             f32x4_t (&acc)[4])
 {
@@ -297,24 +337,30 @@ __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, con
     const int lane = threadIdx.x & 63, Kc = p.w.K / 128;
     const uint8_t* packed = p.w.codes(e);
     const uint16_t *alpha = p.w.alpha + p.w.scales(e), *beta = p.w.beta + p.w.scales(e);
-    typedef std::conditional_t<X32, float, uint16_t> X;
-    typedef std::conditional_t<X32, f32x4_t, s16x4_t> Four;
-    const X* x[NB];                  // the lane's four k of a row, of each 64
+    typedef std::conditional_t<X == X_F32, float, uint16_t> Element;
+    typedef std::conditional_t<X == X_F32, f32x4_t, s16x4_t> Four;
+    uint32_t at[NB];                 // bytes to the lane's four k of a row, of each 64 (below 2^32)
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const int i = 4 * b + (lane & 3);
-        x[b] = static_cast<const X*>(p.x) + static_cast<size_t>(own[i < count ? i : count - 1] / p.r.div) * p.w.K + 4 * (lane >> 2);
+        at[b] = static_cast<uint32_t>(sizeof(Element)) *
+                (static_cast<uint32_t>(own[i < count ? i : count - 1] / p.r.div) * static_cast<uint32_t>(p.w.K) + 4u * (lane >> 2));
     }
     RowChunk<FMT> next;
     next.fetch(packed, alpha, beta, wr, Kc, s0, p.w.g);
     RowTable row = fetch_table<FMT>(FMT == FMT_INT4 ? nullptr : p.w.table(e), alpha, beta, wr, Kc, s0, p.w.g);
     for (int s = s0; s < s1; ++s) {
-        Four in[NB][2];
+        Four in[NB][2], rest[NB][2];
+        const char *hi = reinterpret_cast<const char*>(static_cast<const Element*>(p.x) + s * 128),
+                   *lo_part = reinterpret_cast<const char*>(static_cast<const Element*>(p.x) + p.plane + s * 128);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                in[b][j] = *reinterpret_cast<const Four*>(x[b] + s * 128 + 64 * j);
+            for (int j = 0; j < 2; ++j) {
+                in[b][j] = *reinterpret_cast<const Four*>(hi + at[b] + 64 * j * sizeof(Element));
+                if constexpr (X == X_PARTS)
+                    rest[b][j] = *reinterpret_cast<const Four*>(lo_part + at[b] + 64 * j * sizeof(Element));
+            }
         const RowChunk<FMT> now = next;
         if (s + 1 < s1)
             next.fetch(packed, alpha, beta, wr, Kc, s + 1, p.w.g);
@@ -327,11 +373,14 @@ __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, con
             constexpr int q = decltype(q_)::value;
             if constexpr (q % 2 == 0)
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    if constexpr (X32)
-                        split2(in[b][q / 2], a[b], lo[b]);
+                for (int b = 0; b < NB; ++b) {
+                    if constexpr (X == X_F32)
+                        split4(in[b][q / 2], a[b], lo[b]);
                     else
                         a[b] = in[b][q / 2];
+                    if constexpr (X == X_PARTS)
+                        lo[b] = rest[b][q / 2];
+                }
             uint32_t v[16];
             decode_in_order(t, now.code[q], v);
             static_for<0, 8>([&](auto i_) __attribute__((always_inline)) {
@@ -340,7 +389,7 @@ __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, con
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     acc[b] = mfma4<8 * (q & 1) + i>(a[b], __builtin_bit_cast(s16x4_t, w), acc[b]);
-                    if constexpr (X32)
+                    if constexpr (X != X_BF16)
                         acc[b] = mfma4<8 * (q & 1) + i>(lo[b], __builtin_bit_cast(s16x4_t, w), acc[b]);
                 }
             });
@@ -359,8 +408,9 @@ __device__ __forceinline__ void few_product(const FewArgs& p, int e, int wr, con
 // as much 43.  448 workgroups are 1.75 to a CU and take the time of two: 16 rows of W a
 // wave, four quarters of k side by side, fill the CUs evenly and gained less than 10% (not
 // kept).  any2 and any3 have half the lookups: 14336 x 4096 in 10.4 us for any4's 12.5.
-// Rows of fp32 (X32): one token through two experts' 4096 x 14336 27.7 us for 24.7.
-template <int FMT, int WAVES, bool X32>
+// Rows of fp32: one token through two experts' 4096 x 14336 27.7 us for 24.7, rows in parts
+// 25.4 (they need no splitting).
+template <int FMT, int WAVES, int X>
 __global__ __launch_bounds__(WAVE * WAVES, 4) void k_few(const FewArgs p)
 {
     __shared__ int own[WAVES][FEW_T];
@@ -378,7 +428,7 @@ __global__ __launch_bounds__(WAVE * WAVES, 4) void k_few(const FewArgs p)
         if (blockIdx.z == 0 && live)
             for (int i = w; i < t.count; i += WAVES) {
                 if (half == 0)
-                    put_value(p.q.out, p.q.out32, static_cast<size_t>(own[w][i]) * p.q.No + col, 0.0f);
+                    put_out(p.q, static_cast<size_t>(own[w][i]) * p.q.No + col, 0.0f);
                 if (p.q.z)
                     put_value(p.q.z, p.q.z32, static_cast<size_t>(own[w][i]) * p.q.N + wr, 0.0f);
             }
@@ -393,7 +443,7 @@ __global__ __launch_bounds__(WAVE * WAVES, 4) void k_few(const FewArgs p)
     static_for<0, 3>([&](auto n_) __attribute__((always_inline)) {
         constexpr int NB = 1 << decltype(n_)::value;
         if (t.count <= 4 * NB && (NB == 1 || t.count > 2 * NB))
-            few_product<FMT, NB, X32>(p, t.e, wr, own[w], t.count, s0, s1, acc);
+            few_product<FMT, NB, X>(p, t.e, wr, own[w], t.count, s0, s1, acc);
     });
 #pragma unroll
     for (int b = 0; b < 4; ++b)
@@ -426,7 +476,7 @@ __global__ __launch_bounds__(WAVE * WAVES, 4) void k_few(const FewArgs p)
         const size_t to = static_cast<size_t>(pair) * p.q.No + col;
         if (p.q.residual)
             v += bf16_to_f32(p.q.residual[to]);
-        put_value(p.q.out, p.q.out32, to, v);
+        put_out(p.q, to, v);
     }
 }
 
@@ -479,7 +529,7 @@ __global__ __launch_bounds__(256) void k_join(const Epilogue q, const int* __res
 struct TileArgs {
     Rows r;
     Layer w;
-    const uint16_t* x;       // [rows][D], D the summed dimension (padded to 8)
+    const uint16_t* x;       // [rows][D], D the summed dimension (padded to 8); in parts [2][rows][D]
     Epilogue q;
     int rows, D, steps;
     int tiles_m, tiles_n;
@@ -605,7 +655,11 @@ struct RowReader {
 constexpr int parts_of(int blocks) { return blocks >= 2 ? 4 : 2; }
 
 // 2 x WN waves of RM x 4 blocks of 16 x 16.  TURN: the sum runs over the rows of W
-// and the results are its columns (the input's gradient).
+// and the results are its columns (the input's gradient).  SPLIT: of every 64 rows of the
+// tile the first 32 are the hi parts of 32 pairs, the others their lo parts; a wave has both,
+// and adds their sums at the end.  (2062 pairs through 8 experts of 4096 x 14336 686 us for
+// 444 in bf16, 8192 through 16 of 2048 x 1024 115 for 89: what is decoded serves as many
+// products, of half as many pairs.)
 //
 // The matrix cores take a 16 x 16 x 32 product in 7.8 ns and let two vector instructions
 // in for nothing; every further one costs its 1.9 ns.  Decoding is 4.2 instructions a
@@ -620,13 +674,15 @@ constexpr int parts_of(int blocks) { return blocks >= 2 ? 4 : 2; }
 // 32 columns and all rows of a tile, and x alone in LDS: 4096 rows with 28672 x 4096 in
 // tiles of 128 x 128 1168 us for 1203, and 64 rows 44 for 46, since the lookups bound both;
 // four waves of 128 x 128 each (accumulators moved between register files).
-template <int FMT, int WN, int RM, bool TURN>
+template <int FMT, int WN, int RM, bool TURN, bool SPLIT>
 __global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileArgs p)
 {
     constexpr int THREADS = 128 * WN, BM = 32 * RM, BN = WN * 64, WAVES = 2 * WN, LA = BM / 8 / WAVES;
+    constexpr int BP = SPLIT ? BM / 2 : BM, RP = SPLIT ? RM / 2 : RM;       // pairs of a tile, their blocks of a wave
     static_assert(LA >= 1, "every wave loads rows of x");
+    static_assert(!SPLIT || (RM >= 2 && 4 % LA == 0), "what a wave loads are hi parts or lo parts");
     __shared__ __attribute__((aligned(16))) uint16_t sa0[BM * STEP], sb0[BN * STEP], sa1[BM * STEP], sb1[BN * STEP];
-    __shared__ int pairs[BM];
+    __shared__ int pairs[BP];
     // forward: the tables of the rows at the places; TURN: byte tables of the next steps' rows
     __shared__ u32x4_t tables[TURN || FMT == FMT_INT4 || FMT == FMT_BF16 ? 1 : BN][FMT == FMT_ANY4 ? 2 : 1];
     __shared__ uint32_t turned[TURN ? 2 : 1][TURN ? BN / 128 : 1][TURN ? 2 * ByteTable<FMT>::ENTRIES / 4 : 1][STEP];
@@ -641,11 +697,11 @@ __global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileAr
     const int in_band = id - band * HIGH * p.tiles_n;
     const int tm = __builtin_amdgcn_readfirstlane(band * HIGH + in_band % high), tn = __builtin_amdgcn_readfirstlane(in_band / high);
     int64_t first = 0;
-    const Tile t = find_tile(p.r, tm, BM, first);
+    const Tile t = find_tile(p.r, tm, BP, first);
     if (t.e < 0)
         return;
-    for (int i = tid; i < BM; i += THREADS)
-        pairs[i] = i >= t.count ? -1 : p.r.plan ? p.r.plan[first + i] : tm * BM + i;
+    for (int i = tid; i < BP; i += THREADS)
+        pairs[i] = i >= t.count ? -1 : p.r.plan ? p.r.plan[first + i] : tm * BP + i;
     __syncthreads();
     const bool gate = p.q.gated();
     const int col0 = gate ? tn * (BN / 2) : tn * BN;       // of out
@@ -654,7 +710,7 @@ __global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileAr
             for (int i = w; i < t.count; i += WAVES)
                 for (int o = lane; o < (gate ? BN / 2 : BN); o += WAVE)
                     if (col0 + o < p.q.No) {
-                        put_value(p.q.out, p.q.out32, static_cast<size_t>(pairs[i]) * p.q.No + col0 + o, 0.0f);
+                        put_out(p.q, static_cast<size_t>(pairs[i]) * p.q.No + col0 + o, 0.0f);
                         if (p.q.z) {
                             const size_t z = static_cast<size_t>(pairs[i]) * p.q.N + col0 + o;
                             put_value(p.q.z, p.q.z32, z, 0.0f);
@@ -666,13 +722,14 @@ __global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileAr
     }
 
     // x: a wave's load instruction fills 8 rows of a tile; lane: row lane / 8, place lane % 8
-    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(p.x), static_cast<short>(0), static_cast<int>(static_cast<size_t>(p.rows) * p.D * 2), 0x00020000);
+    const size_t plane = static_cast<size_t>(p.rows) * p.D;
+    const __amdgpu_buffer_rsrc_t ra = buffer_of(p.x + (SPLIT && w * LA / 4 % 2 ? plane : 0), plane * 2);
     uint32_t ga[LA];
     int na[LA];                      // TURN: where the piece stands in the sum
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-        const int r = (w * LA + i) * 8 + lane / 8, pair = pairs[r], piece = (lane & 7) ^ key(r);
+        const int r = (w * LA + i) * 8 + lane / 8, piece = (lane & 7) ^ key(r);
+        const int pair = pairs[SPLIT ? r / 64 * 32 + r % 32 : r];
         ga[i] = pair < 0 ? OOR : static_cast<uint32_t>(pair / p.r.div) * (static_cast<uint32_t>(p.D) * 2u) + piece * 16u;
         na[i] = 8 * piece;
     }
@@ -691,7 +748,7 @@ __global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileAr
             acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     // of every 32 rows of the tile a wave takes the first or the second 16
     const int wm = w / WN * 16, wn = (w % WN) * 64;
-    const int blocks = __builtin_amdgcn_readfirstlane(t.count > wm ? (t.count - wm + 31) / 32 : 0);
+    const int blocks = __builtin_amdgcn_readfirstlane(t.count > wm ? (t.count - wm + 31) / 32 * (SPLIT ? 2 : 1) : 0);
     // operand reads: 16 or 32 rows on the key is the same, so one place each and
     // constant distances; the second half of a step is four pieces on.  (Kept from the
     // compiler, which would hold row and piece apart and add them every time.)
@@ -974,12 +1031,18 @@ __global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileAr
         run(std::integral_constant<int, (RM > 1 ? RM / 2 : 1)>{});
     else
         run(std::integral_constant<int, RM>{});
+    if constexpr (SPLIT)
+#pragma unroll
+        for (int i = 0; i < RP; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = acc[2 * i][j] + acc[2 * i + 1][j];
     // The sums leave through LDS of the wave's own, so that lanes next to one another
     // write columns next to one another: 16 pieces of four floats a row, piece q at
     // q ^ row.  With a gate its columns come first, those of the up rows behind.
     meet(All{});
     constexpr int ROOM = (BM < BN ? BM : BN) * STEP * 2 / (WAVES / 4);          // bytes of a wave
-    constexpr int HALVES = 16 * RM * 256 > ROOM ? 2 : 1, ROWS = 16 * RM / HALVES;
+    constexpr int HALVES = 16 * RP * 256 > ROOM ? 2 : 1, ROWS = 16 * RP / HALVES;
     static_assert(ROWS * 256 <= ROOM, "the waves' rooms lie in the four buffers");
     const int room = w * 4 / WAVES;       // a wave's, or two waves', of the four buffers
     uint16_t* const in = room == 0 ? sa0 : room == 1 ? sb0 : room == 2 ? sa1 : sb1;
@@ -990,16 +1053,16 @@ __global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileAr
     for (int half = 0; half < HALVES; ++half) {
         wave_sync();
 #pragma unroll
-        for (int i = 0; i < RM / HALVES; ++i)
+        for (int i = 0; i < RP / HALVES; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int to = gate ? 8 * (j >> 1) + 2 * g2 + (j & 1) : 4 * g2 + j;
-                stage[(16 * i + c2) * 16 + (to ^ c2)] = acc[half * (RM / HALVES) + i][j];
+                stage[(16 * i + c2) * 16 + (to ^ c2)] = acc[half * (RP / HALVES) + i][j];
             }
         wave_sync();
         for (int o = lane2; o < ROWS * pieces; o += WAVE) {
             const int row = o / pieces, q = o % pieces;
-            const int pair = pairs[32 * (half * (RM / HALVES) + row / 16) + wm + row % 16];
+            const int pair = pairs[32 * (half * (RP / HALVES) + row / 16) + wm + row % 16];
             const int col = col0 + (gate ? wn / 2 : wn) + 8 * q;
             if (pair < 0 || col >= p.q.No)
                 continue;
@@ -1207,8 +1270,12 @@ struct Form {
 };
 constexpr Form FORMS[] = {{8, 4, {190, 0}, {200, 0}}, {4, 2, {120, 140}, {71, 100}}, {2, 2, {88, 110}, {48, 63}}, {1, 2, {75, 100}, {38, 52}}};
 constexpr Form ROWS_FORM = {8, 4, {168, 0}, {180, 0}};
-// the same for a chunk of 128 of a wave of k_few, by its rows of x (up to 4, 8, 16)
-constexpr int FEW_TIME[3] = {195, 215, 300};
+// the same for a chunk of 128 of a wave of k_few, by its rows of x (up to 4, 8, 16), in bf16 and
+// in parts (through 8 experts of 4096 x 14336 8 pairs 54 and 56 us, 64 pairs 76 and 107)
+constexpr int FEW_TIME[2][3] = {{195, 215, 300}, {205, 290, 430}};
+
+// pairs of a tile of rm blocks
+int64_t tile_pairs(int rm, bool parts) { return parts ? 16 * rm : 32 * rm; }
 
 // P rows through E experts (experts = false: one layer), D summed, C columns of the
 // product (both halves of a gate).  Of the forms and splits the one with the least
@@ -1217,7 +1284,7 @@ constexpr int FEW_TIME[3] = {195, 215, 300};
 // (Of 85 sizes, a layer of 1 to 2048 rows and 4 to 64 experts, forward and back, eight
 // took more than a tenth longer than their best form and splits, at most a fifth; the
 // median 2%.)
-Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool turn)
+Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool turn, bool parts = false)
 {
     Shape s{0, 2, 1, 0, 0, false};
     const int64_t each = (P + E - 1) / E;        // rows of an expert, on average
@@ -1244,12 +1311,12 @@ Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool tu
         const double row_tiles = experts ? named * (each < 8 ? 4 : each / 4 + 2) / 4 : static_cast<double>((P + FEW_T - 1) / FEW_T);
         const int64_t tiles = static_cast<int64_t>((C + FEW_ROWS - 1) / FEW_ROWS * row_tiles + 0.5);
         for (int64_t n = 1; n <= 8 && (n == 1 || chunks / n >= 8); n *= 2)
-            better((tiles * n + 255) / 256 * FEW_TIME[rows] * ((chunks + 8 * n - 1) / (8 * n)) + (n > 1 ? 250 : 0), 0,
+            better((tiles * n + 255) / 256 * FEW_TIME[parts][rows] * ((chunks + 8 * n - 1) / (8 * n)) + (n > 1 ? 250 : 0), 0,
                    tiles * n >= 1024 || chunks < 32 ? 2 : 4, n, false);
     }
     const int64_t steps = (D + STEP - 1) / STEP;
     auto weigh = [&](const Form& f, int64_t before, bool rows) {
-        const int64_t bm = 32 * f.rm, bn = 64 * f.wn, tiles_n = (C + bn - 1) / bn;
+        const int64_t bm = tile_pairs(f.rm, parts), bn = 64 * f.wn, tiles_n = (C + bn - 1) / bn;
         // in quarters
         const int64_t a_tile = 4 * each < bm ? 4 : 4 * each < 3 * bm ? 5 : 4 * each / bm + 2;
         const int64_t tiles_m = experts ? static_cast<int64_t>(named * a_tile + 0.5) : 4 * ((P + bm - 1) / bm);
@@ -1261,7 +1328,7 @@ Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool tu
     };
     if (turn || !experts || P > FEW_P)           // fewer pairs have no plan forward
         for (const Form& f : FORMS)
-            if (f.one[turn])
+            if (f.one[turn] && !(parts && f.rm == 1))
                 weigh(f, 0, false);
     if (!experts && !turn && C * D < GIB2 / 2)
         weigh(ROWS_FORM, 300 + C * D / 22000, true);       // 2.5 bytes a weight at 5.5 TB/s
@@ -1270,7 +1337,7 @@ Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool tu
         s.tiles_n = (C + FEW_ROWS - 1) / FEW_ROWS;
         return s;
     }
-    const int64_t bm = 32 * s.rm, bn = 64 * s.wn;
+    const int64_t bm = tile_pairs(s.rm, parts), bn = 64 * s.wn;
     s.tiles_m = experts ? P / bm + (P < E + 1 ? P : E + 1) : (P + bm - 1) / bm;
     s.tiles_n = (C + bn - 1) / bn;
     return s;
@@ -1281,51 +1348,52 @@ size_t part_bytes(const Shape& s, int64_t P, int64_t C, int64_t D)
     return (s.S > 1 ? up256(static_cast<size_t>(s.S) * P * C * 4) : 0) + (s.rows ? up256(static_cast<size_t>(C) * D * 2) : 0);
 }
 
-template <int FMT, bool TURN>
+template <int FMT, bool TURN, bool SPLIT>
 void launch_tile(const Shape& s, const TileArgs& a, hipStream_t stream)
 {
     const dim3 grid(static_cast<unsigned>((s.tiles_m * s.tiles_n + 7) / 8 * 8), static_cast<unsigned>(s.S));
-#define TILE(WN_, RM_) hipLaunchKernelGGL((k_tile<FMT, WN_, RM_, TURN>), grid, dim3(128 * WN_), 0, stream, a)
+#define TILE(WN_, RM_) hipLaunchKernelGGL((k_tile<FMT, WN_, RM_, TURN, SPLIT>), grid, dim3(128 * WN_), 0, stream, a)
     if constexpr (FMT == FMT_BF16) {
         TILE(4, 8);
     } else {
         if (s.rm == 4) TILE(2, 4);
         else if (s.rm == 2) TILE(2, 2);
-        else if (s.rm == 1) TILE(2, 1);
-        else if constexpr (!TURN) TILE(4, 8);
+        else if (s.rm == 8) {
+            if constexpr (!TURN) TILE(4, 8);
+        } else {
+            if constexpr (!SPLIT) TILE(2, 1);
+        }
     }
 #undef TILE
 }
 
-template <bool TURN>
+template <bool TURN, bool SPLIT>
 void launch_tile(int fmt, const Shape& s, const TileArgs& a, hipStream_t stream)
 {
-    if (fmt == FMT_ANY4) launch_tile<FMT_ANY4, TURN>(s, a, stream);
-    else if (fmt == FMT_INT4) launch_tile<FMT_INT4, TURN>(s, a, stream);
-    else if (fmt == FMT_ANY2) launch_tile<FMT_ANY2, TURN>(s, a, stream);
-    else launch_tile<FMT_ANY3, TURN>(s, a, stream);
+    if (fmt == FMT_ANY4) launch_tile<FMT_ANY4, TURN, SPLIT>(s, a, stream);
+    else if (fmt == FMT_INT4) launch_tile<FMT_INT4, TURN, SPLIT>(s, a, stream);
+    else if (fmt == FMT_ANY2) launch_tile<FMT_ANY2, TURN, SPLIT>(s, a, stream);
+    else launch_tile<FMT_ANY3, TURN, SPLIT>(s, a, stream);
 }
 
-void launch_few(int fmt, const Shape& s, const FewArgs& a, bool x32, hipStream_t stream)
+template <int FMT, int X>
+void launch_few(const Shape& s, const FewArgs& a, hipStream_t stream)
 {
     const int per = a.q.gated() ? FEW_ROWS / 2 : FEW_ROWS;
     const dim3 grid(static_cast<unsigned>((a.q.No + per - 1) / per), static_cast<unsigned>(s.tiles_m), static_cast<unsigned>(s.S));
-#define FEW(FMT_)                                                                              \
-    do {                                                                                       \
-        if (x32 && s.wn == 2)                                                                  \
-            hipLaunchKernelGGL((k_few<FMT_, 4, true>), grid, dim3(4 * WAVE), 0, stream, a);    \
-        else if (x32)                                                                          \
-            hipLaunchKernelGGL((k_few<FMT_, 8, true>), grid, dim3(8 * WAVE), 0, stream, a);    \
-        else if (s.wn == 2)                                                                    \
-            hipLaunchKernelGGL((k_few<FMT_, 4, false>), grid, dim3(4 * WAVE), 0, stream, a);   \
-        else                                                                                   \
-            hipLaunchKernelGGL((k_few<FMT_, 8, false>), grid, dim3(8 * WAVE), 0, stream, a);   \
-    } while (0)
-    if (fmt == FMT_ANY4) FEW(FMT_ANY4);
-    else if (fmt == FMT_INT4) FEW(FMT_INT4);
-    else if (fmt == FMT_ANY2) FEW(FMT_ANY2);
-    else FEW(FMT_ANY3);
-#undef FEW
+    if (s.wn == 2)
+        hipLaunchKernelGGL((k_few<FMT, 4, X>), grid, dim3(4 * WAVE), 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_few<FMT, 8, X>), grid, dim3(8 * WAVE), 0, stream, a);
+}
+
+template <int X>
+void launch_few(int fmt, const Shape& s, const FewArgs& a, hipStream_t stream)
+{
+    if (fmt == FMT_ANY4) launch_few<FMT_ANY4, X>(s, a, stream);
+    else if (fmt == FMT_INT4) launch_few<FMT_INT4, X>(s, a, stream);
+    else if (fmt == FMT_ANY2) launch_few<FMT_ANY2, X>(s, a, stream);
+    else launch_few<FMT_ANY3, X>(s, a, stream);
 }
 
 bool act_ok(int act) { return act >= 0 && act < ACTS; }
@@ -1338,10 +1406,11 @@ bool sizes_ok(int64_t P, int64_t X, int64_t E, int64_t N, int64_t K, int64_t g)
            g > 0 && g % 128 == 0 && K % g == 0 && (N + 15) / 16 * 16 * K < 2 * GIB2 && (P == 0 || N < GIB2 / 2 / P) && (X == 0 || K < GIB2 / 2 / X);
 }
 
-any4_status product(int fmt, const Rows& rows, int64_t X, const void* x, bool x32, const Layer& w, const Epilogue& q, const int32_t* ids,
+// kind: of x's rows
+any4_status product(int fmt, const Rows& rows, int64_t X, const void* x, int kind, const Layer& w, const Epilogue& q, const int32_t* ids,
                     void* workspace, size_t workspace_bytes, bool experts, hipStream_t stream)
 {
-    const Shape s = shape_of(rows.P, rows.E, experts, w.K, w.N, false);
+    const Shape s = shape_of(rows.P, rows.E, experts, w.K, w.N, false, kind == X_PARTS);
     char* at = static_cast<char*>(workspace);
     Rows r = rows;
     Epilogue e = q;
@@ -1366,7 +1435,10 @@ any4_status product(int fmt, const Rows& rows, int64_t X, const void* x, bool x3
     if (s.S > 1)
         e.part = reinterpret_cast<float*>(at);
     if (s.rm == 0) {
-        launch_few(fmt, s, FewArgs{r, w, x, e}, x32, stream);
+        const FewArgs a{r, w, x, e, static_cast<size_t>(X) * w.K};
+        if (kind == X_F32) launch_few<X_F32>(fmt, s, a, stream);
+        else if (kind == X_PARTS) launch_few<X_PARTS>(fmt, s, a, stream);
+        else launch_few<X_BF16>(fmt, s, a, stream);
     } else if (s.rows) {
         uint16_t* rows = reinterpret_cast<uint16_t*>(at + (s.S > 1 ? up256(static_cast<size_t>(s.S) * r.P * w.N * 4) : 0));
         const int Kc = w.K / 128;
@@ -1379,12 +1451,13 @@ any4_status product(int fmt, const Rows& rows, int64_t X, const void* x, bool x3
 #undef LAY_OUT
         Layer laid = w;
         laid.packed = reinterpret_cast<const uint8_t*>(rows);
-        launch_tile<FMT_BF16, false>(s, TileArgs{r, laid, static_cast<const uint16_t*>(x), e, static_cast<int>(X), w.K, w.K / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
+        launch_tile<FMT_BF16, false, false>(s, TileArgs{r, laid, static_cast<const uint16_t*>(x), e, static_cast<int>(X), w.K, w.K / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
                                      stream);
     } else {
         r.ids = nullptr;
-        launch_tile<false>(fmt, s, TileArgs{r, w, static_cast<const uint16_t*>(x), e, static_cast<int>(X), w.K, w.K / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
-                           stream);
+        const TileArgs a{r, w, static_cast<const uint16_t*>(x), e, static_cast<int>(X), w.K, w.K / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)};
+        if (kind == X_PARTS) launch_tile<false, true>(fmt, s, a, stream);
+        else launch_tile<false, false>(fmt, s, a, stream);
     }
     if (s.S > 1) {
         const size_t pieces = static_cast<size_t>(r.P) * ((e.No + 7) / 8);
@@ -1436,8 +1509,8 @@ any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* 
     (void)hipGetLastError();
     const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
     const Epilogue q{bias, residual, z, out, nullptr, static_cast<int>(N), static_cast<int>(gate ? N / 2 : N), static_cast<int>(act), 1,
-                     z_f32 != 0, out_f32 != 0};
-    return product(fmt, Rows{nullptr, nullptr, static_cast<int>(M), 1, 1}, M, x, false, w, q, nullptr, workspace, workspace_bytes, false, stream);
+                     z_f32 != 0, out_f32 != 0, 0};
+    return product(fmt, Rows{nullptr, nullptr, static_cast<int>(M), 1, 1}, M, x, X_BF16, w, q, nullptr, workspace, workspace_bytes, false, stream);
 }
 
 size_t any4_act_backward_workspace_size(int64_t M, int64_t N, int gate)
@@ -1504,6 +1577,14 @@ size_t any4_experts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, i
     return part_bytes(shape_of(P, E, true, K, N, false), P, N, K) + (P <= FEW_P ? 0 : any4_lora_plan_bytes(P, E));
 }
 
+size_t any4_experts_parts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g)
+{
+    if (T <= 0 || k <= 0 || N <= 0 || T > MAX_PAIRS || k > MAX_PAIRS || !sizes_ok(T * k, T * k, E, N, K, g))
+        return 0;
+    const int64_t P = T * k;
+    return part_bytes(shape_of(P, E, true, K, N, false, true), P, N, K) + (P <= FEW_P ? 0 : any4_lora_plan_bytes(P, E));
+}
+
 any4_status any4_experts_gemm(any4_format format, const void* x, int x_f32, int per_pair, const uint8_t* packed, const uint16_t* lut,
                               const uint16_t* alpha, const uint16_t* beta, const uint16_t* bias, const int32_t* ids, const void* plan,
                               void* z, int z_f32, void* out, int out_f32, any4_activation act, int gate, int64_t T, int64_t k, int64_t E, int64_t N,
@@ -1511,22 +1592,26 @@ any4_status any4_experts_gemm(any4_format format, const void* x, int x_f32, int 
 {
     const int fmt = static_cast<int>(format);
     if (!fmt_ok(fmt) || !act_ok(act) || T < 0 || k < 1 || T > MAX_PAIRS || k > MAX_PAIRS ||
-        !sizes_ok(T * k, per_pair ? T * k : T, E, N, K, g) || (gate && N % 2) || (x_f32 && T * k > FEW_P))
+        !sizes_ok(T * k, per_pair ? T * k : T, E, N, K, g) || (gate && N % 2))
+        return ANY4_E_SHAPE;
+    const int kind = !x_f32 ? X_BF16 : x_f32 == ANY4_PARTS ? X_PARTS : X_F32;
+    if ((kind == X_F32 && T * k > FEW_P) || (kind == X_PARTS && !per_pair))
         return ANY4_E_SHAPE;
     if (T == 0 || N == 0)
         return ANY4_OK;
     if (!x || !packed || (fmt != FMT_INT4 && !lut) || !alpha || !beta || !ids || !out)
         return ANY4_E_NULL;
     if (!is_aligned(x, 16) || !is_aligned(packed, 16) || !is_aligned(lut, 2) || !is_aligned(alpha, 2) || !is_aligned(beta, 2) ||
-        !is_aligned(bias, 2) || !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(z, z_f32 ? 4 : 2) || !is_aligned(out, out_f32 ? 4 : 2) ||
-        !is_aligned(workspace, 16))
+        !is_aligned(bias, 2) || !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(z, z_f32 ? 4 : 2) ||
+        !is_aligned(out, out_f32 && out_f32 != ANY4_PARTS ? 4 : 2) || !is_aligned(workspace, 16))
         return ANY4_E_ALIGN;
     (void)hipGetLastError();
     const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
-    const Epilogue q{bias, nullptr, z, out, nullptr, static_cast<int>(N), static_cast<int>(gate ? N / 2 : N), static_cast<int>(act), 1,
-                     z_f32 != 0, out_f32 != 0};
+    const int64_t No = gate ? N / 2 : N;
+    const Epilogue q{bias, nullptr, z, out, nullptr, static_cast<int>(N), static_cast<int>(No), static_cast<int>(act), 1,
+                     z_f32 != 0, out_f32 == ANY4_PARTS ? ANY4_PARTS : out_f32 != 0, static_cast<size_t>(T * k * No)};
     const Rows r{nullptr, static_cast<const int*>(plan), static_cast<int>(T * k), static_cast<int>(E), per_pair ? 1 : static_cast<int>(k)};
-    return product(fmt, r, per_pair ? T * k : T, x, x_f32 != 0, w, q, ids, workspace, workspace_bytes, true, stream);
+    return product(fmt, r, per_pair ? T * k : T, x, kind, w, q, ids, workspace, workspace_bytes, true, stream);
 }
 
 size_t any4_experts_dx_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g)
@@ -1577,9 +1662,9 @@ any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const u
     at += up256(static_cast<size_t>(P) * Np * 2);
     const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
     const Epilogue q{nullptr, nullptr, nullptr, dx, s.S > 1 ? reinterpret_cast<float*>(at) : nullptr, static_cast<int>(K),
-                     static_cast<int>(K), ACT_NONE, s.S, 0, dx_f32 != 0};
+                     static_cast<int>(K), ACT_NONE, s.S, 0, dx_f32 != 0, 0};
     const Rows r{nullptr, static_cast<const int*>(plan), P, static_cast<int>(E), 1};
-    launch_tile<true>(fmt, s, TileArgs{r, w, dy, q, P, Np, (Np + STEP - 1) / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
+    launch_tile<true, false>(fmt, s, TileArgs{r, w, dy, q, P, Np, (Np + STEP - 1) / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
                       stream);
     if (s.S > 1) {
         const size_t pieces = static_cast<size_t>(P) * (K / 8);

@@ -510,7 +510,14 @@ any4_status any3_gemm_dx(const uint16_t* dy, const uint8_t* packed, const uint16
  * these calls (z, an output that any4_combine or any4_act_backward reads, an input's
  * gradient) is bf16, or where the argument behind it (z_f32, out_f32, ..) is not 0 fp32, in
  * the same shape and with an alignment of 4: then it is not rounded in between.
+ * Rows that enter a matrix product are bf16.  So that they need not be rounded to
+ * 8 bits either, the outputs and inputs that say so may be in two bf16 parts (the
+ * argument behind them ANY4_PARTS, which no truth value is): a tensor [2][..] of the hi
+ * parts, each value cut to bf16, and the lo parts, bf16_rne(value - hi); hi + lo is
+ * the value but for 2^-16 of it at most.  An infinity has a lo of 0.  A product takes both
+ * parts of a row, for twice the matrix work.
  */
+enum { ANY4_PARTS = -1 };
 typedef enum any4_format {
     ANY4_FORMAT_ANY4 = 0, /* any4_pack, lut of 16 entries              */
     ANY4_FORMAT_INT4 = 1, /* any4_pack, plain codes 0..15, lut not read */
@@ -626,9 +633,9 @@ any4_status any4_route_backward(const float* dw, const void* logits, int logits_
  * through expert e = ids[t][j],
  *     zf[p] = W_e x[per_pair ? p : t] + bias[e],   out[p] = bf16_rne( act(zf[p]) ) or gated
  * A pair whose id is not in 0..E-1 gives zeros (out and z).
- *   x       device, [T][K] bf16, or with per_pair != 0 [T*k][K]; for up to 64 pairs with
- *           x_f32 != 0 fp32, of which 16 bits or more enter the products (with one token a
- *           rounding of the first product's results is not averaged over others)
+ *   x       device, [T][K] bf16, or with per_pair != 0 [T*k][K]; then also, x_f32 being
+ *           ANY4_PARTS, [2][T*k][K], the results of another such product in two parts; for
+ *           up to 64 pairs, with any other x_f32 but 0, fp32, split into such parts here
  *   packed  device, the experts' packed layers one after another (each of
  *           any4_packed_bytes(N, K), or the format's)
  *   lut [E][N][16], alpha, beta [E][N][K/g], bias [E][N] bf16 (or NULL)
@@ -638,15 +645,17 @@ any4_status any4_route_backward(const float* dw, const void* logits, int logits_
  *           need none and ignore it).  A plan that any4_lora_plan made for other sizes
  *           leaves the outputs unwritten.
  *   z       device, [T*k][N] bf16 or fp32, written; or NULL
- *   out     device, [T*k][No] bf16 or fp32, written
+ *   out     device, [T*k][No] bf16 or fp32, or (out_f32 ANY4_PARTS) [2][T*k][No], written
  *   0 <= T*k <= 2^20, 1 <= E <= 1024, the other sizes as any4_gemm_act for M = T*k; the
  *   stacked arrays may be of any size.  T = 0 and N = 0 are no-ops.
  *   workspace  as for any4_gemm_act, any4_experts_workspace_size(T, k, E, N, K, g) bytes
- *          (where the call makes its own plan or splits K).
+ *          (where the call makes its own plan or splits K), for an x in parts
+ *          any4_experts_parts_workspace_size.
  *   x, packed, plan and workspace need 16-byte alignment, ids 4, the others 2.
  * Errors: as any4_gemm_act.
  */
 size_t any4_experts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g);
+size_t any4_experts_parts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g);
 any4_status any4_experts_gemm(any4_format format, const void* x, int x_f32, int per_pair,
                               const uint8_t* packed, const uint16_t* lut, const uint16_t* alpha, const uint16_t* beta,
                               const uint16_t* bias, const int32_t* ids, const void* plan, void* z,
