@@ -35,8 +35,9 @@ forms: stacked layers, each row through its expert), combine and
 combine_backward (the weighted sum of the experts' outputs).  What one of these
 calls writes for another (z, an output for combine, an input's gradient for
 act_backward or combine) may be a bf16 tensor or an fp32 one, given as z or out;
-what enters another product (experts_gemm's out) may be in two bf16 parts, a bf16 tensor
-with one more dimension of 2 in front: hi, the values cut to bf16, and lo, the rest.
+what enters another product (experts_gemm's out, act_backward's dz) may be in two bf16
+parts, a bf16 tensor with one more dimension of 2 in front: hi, the values cut to bf16, and
+lo, the rest.
 These and the calls for fine-tunes take tensors of any GPU, run on that GPU's
 current stream (or `stream`, on which their outputs and workspaces are then
 allocated too) and can be captured into a graph.
@@ -68,9 +69,9 @@ EXPORTS = ("any4_packed_bytes", "any4_pack", "any4_dequant", "any4_gemm_workspac
            "any4_lora_backward_workspace_size", "any4_lora_backward", "any4_act8_save",
            "any4_act8_load", "any4_gemm_dx_workspace_size", "any4_gemm_dx", "any4_gemm_int4_dx",
            "any2_gemm_dx", "any3_gemm_dx", "any4_gemm_act_workspace_size", "any4_gemm_act",
-           "any4_act_backward_workspace_size", "any4_act_backward", "any4_route", "any4_route_backward",
+           "any4_act_backward_workspace_size", "any4_act_backward", "any4_act_backward_parts", "any4_route", "any4_route_backward",
            "any4_experts_workspace_size", "any4_experts_parts_workspace_size", "any4_experts_gemm", "any4_experts_dx_workspace_size",
-           "any4_experts_gemm_dx", "any4_combine", "any4_combine_backward")
+           "any4_experts_gemm_dx", "any4_experts_dx_parts_workspace_size", "any4_experts_gemm_dx_parts", "any4_combine", "any4_combine_backward")
 
 _lib = None
 
@@ -136,6 +137,7 @@ def lib() -> ctypes.CDLL:
                 ("any4_gemm_act", ctypes.c_int, [INT] + [P] * 8 + [INT, P] + [INT] * 3 + [I64] * 4 + [P, SZ, P]),
                 ("any4_act_backward_workspace_size", SZ, [I64] * 2 + [INT]),
                 ("any4_act_backward", ctypes.c_int, [P, INT, P, INT, P, P] + [INT] * 2 + [I64] * 2 + [P, SZ, P]),
+                ("any4_act_backward_parts", ctypes.c_int, [P, INT, P, INT, P, P] + [INT] * 2 + [I64] * 2 + [P, SZ, P]),
                 ("any4_route", ctypes.c_int, [P, INT] + [P] * 3 + [INT] * 2 + [F32] + [I64] * 5 + [P]),
                 ("any4_route_backward", ctypes.c_int,
                  [P, P, INT, P, P] + [INT] * 2 + [F32] + [I64] * 3 + [P]),
@@ -145,6 +147,8 @@ def lib() -> ctypes.CDLL:
                  [INT, P, INT, INT] + [P] * 8 + [INT, P] + [INT] * 3 + [I64] * 6 + [P, SZ, P]),
                 ("any4_experts_dx_workspace_size", SZ, [I64] * 6),
                 ("any4_experts_gemm_dx", ctypes.c_int, [INT] + [P] * 8 + [INT] + [I64] * 6 + [P, SZ, P]),
+                ("any4_experts_dx_parts_workspace_size", SZ, [I64] * 6),
+                ("any4_experts_gemm_dx_parts", ctypes.c_int, [INT] + [P] * 8 + [INT] + [I64] * 6 + [P, SZ, P]),
                 ("any4_combine", ctypes.c_int, [P, INT] + [P] * 3 + [I64] * 3 + [P]),
                 ("any4_combine_backward", ctypes.c_int, [P, P, INT] + [P] * 3 + [I64] * 3 + [P])):
             getattr(L, name).restype = restype
@@ -966,9 +970,10 @@ def gemm_act_raw(fmt, x_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, bias_ptr,
 
 
 def act_backward_raw(dy_ptr, z_ptr, dz_ptr, dbias_ptr, act, gate, M, N, ws_ptr, ws_bytes, stream=None, dy_f32=0,
-                     z_f32=0) -> int:
-    return lib().any4_act_backward(dy_ptr, dy_f32, z_ptr, z_f32, dz_ptr, dbias_ptr, act, gate, M, N, ws_ptr, ws_bytes,
-                                   _stream(stream))
+                     z_f32=0, call="any4_act_backward") -> int:
+    """call: "any4_act_backward" or "any4_act_backward_parts"."""
+    return getattr(lib(), call)(dy_ptr, dy_f32, z_ptr, z_f32, dz_ptr, dbias_ptr, act, gate, M, N, ws_ptr, ws_bytes,
+                                _stream(stream))
 
 
 def route_raw(logits_ptr, bf16, bias_ptr, w_ptr, ids_ptr, score, renorm, scale, T, E, k, groups, top_groups,
@@ -992,9 +997,10 @@ def experts_gemm_raw(fmt, x_ptr, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_
 
 
 def experts_gemm_dx_raw(fmt, dy_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, ids_ptr, plan_ptr, dx_ptr, T, k, E, N, K,
-                        g, ws_ptr, ws_bytes, stream=None, dx_f32=0) -> int:
-    return lib().any4_experts_gemm_dx(fmt, dy_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, ids_ptr, plan_ptr, dx_ptr,
-                                      dx_f32, T, k, E, N, K, g, ws_ptr, ws_bytes, _stream(stream))
+                        g, ws_ptr, ws_bytes, stream=None, dx_f32=0, call="any4_experts_gemm_dx") -> int:
+    """call: "any4_experts_gemm_dx" or "any4_experts_gemm_dx_parts"."""
+    return getattr(lib(), call)(fmt, dy_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, ids_ptr, plan_ptr, dx_ptr,
+                                dx_f32, T, k, E, N, K, g, ws_ptr, ws_bytes, _stream(stream))
 
 
 def combine_raw(y_ptr, w_ptr, residual_ptr, out_ptr, T, k, N, stream=None, y_f32=0) -> int:
@@ -1028,6 +1034,11 @@ def experts_parts_workspace_size(T: int, k: int, E: int, N: int, K: int, g: int)
 @functools.lru_cache(maxsize=4096)      # constant for its sizes
 def experts_dx_workspace_size(T: int, k: int, E: int, N: int, K: int, g: int) -> int:
     return int(lib().any4_experts_dx_workspace_size(T, k, E, N, K, g))
+
+
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
+def experts_dx_parts_workspace_size(T: int, k: int, E: int, N: int, K: int, g: int) -> int:
+    return int(lib().any4_experts_dx_parts_workspace_size(T, k, E, N, K, g))
 
 
 @functools.lru_cache(maxsize=4096)      # constant for its sizes
@@ -1147,7 +1158,8 @@ def act_backward(dy: torch.Tensor, z: torch.Tensor, act: str, gate: bool = False
                  dz: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
                  workspace: torch.Tensor | None = None, stream=None) -> tuple:
     """(dz, dbias) of an epilogue for dy [..., No], from z [..., N] as gemm_act or
-    experts_gemm kept it (either may be bf16 or fp32): dz bf16 (may be a bf16 z itself),
+    experts_gemm kept it (either may be bf16 or fp32): dz bf16 (may be a bf16 z itself), or
+    given as [2, ..., N] the values in two parts, for experts_gemm_dx;
     dbias fp32 [N], the sum over all rows (need_bias = False: None).  The gradient of the
     product's input is gemm_dx (experts_gemm_dx) of dz, that of the residual dy itself."""
     if not z.is_cuda:
@@ -1161,13 +1173,14 @@ def act_backward(dy: torch.Tensor, z: torch.Tensor, act: str, gate: bool = False
         raise ValueError("a gated layer must have an even number of rows")
     p_z, z32 = _kept(z, "z", shape, dev)
     p_dy, dy32 = _kept(dy, "dy", shape[:-1] + (N // 2 if gate else N,), dev)
-    number = _choice("act", act, ACTIVATIONS)
+    number, parts = _choice("act", act, ACTIVATIONS), _parts(dz, shape)
+    call = lib().any4_act_backward_parts if parts else lib().any4_act_backward
     with _on(dev, stream):
         if dz is None:
             dz = torch.empty(shape, dtype=bf16, device=dev)
             p_dz = dz.data_ptr() or None
         else:
-            p_dz = _tensor(dz, "dz", bf16, shape, dev)
+            p_dz = _tensor(dz, "dz", bf16, (2,) + shape if parts else shape, dev)
         p_dbias, need = None, 0
         if not need_bias:
             dbias = None
@@ -1177,8 +1190,8 @@ def act_backward(dy: torch.Tensor, z: torch.Tensor, act: str, gate: bool = False
             p_dbias = _tensor(dbias, "dbias", torch.float32, (N,), dev)
             need = act_backward_workspace_size(M, N, bool(gate))
         ws, p_ws, nbytes = _scratch(workspace, need, dev)
-        check(lib().any4_act_backward(p_dy, dy32, p_z, z32, p_dz, p_dbias, number, 1 if gate else 0, M, N, p_ws,
-                                      nbytes, _current_handle(dev.index)))
+        check(call(p_dy, dy32, p_z, z32, p_dz, p_dbias, number, 1 if gate else 0, M, N, p_ws, nbytes,
+                   _current_handle(dev.index)))
     return dz, dbias
 
 
@@ -1328,15 +1341,18 @@ def any3_experts_gemm(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, 
 
 
 def _experts_gemm_dx(fmt: int, dy, packed, lut, alpha, beta, g, ids, plan, out, workspace, stream) -> torch.Tensor:
-    dev, bf16 = _gpu(dy, "dy", 3), torch.bfloat16
+    parts = dy.dim() == 4
+    dev, bf16 = _gpu(dy, "dy", 4 if parts else 3), torch.bfloat16
     E, N, K, p_packed, p_lut, p_alpha, p_beta = _layer(fmt, packed, lut, alpha, beta, g, dev, True)
     T, k, p_ids, p_plan = _pairs(ids, E, plan, dev)
-    p_dy = _tensor(dy, "dy", bf16, (T, k, N), dev)
+    p_dy = _tensor(dy, "dy", bf16, (2, T, k, N) if parts else (T, k, N), dev)
+    call = lib().any4_experts_gemm_dx_parts if parts else lib().any4_experts_gemm_dx
+    size = experts_dx_parts_workspace_size if parts else experts_dx_workspace_size
     with _on(dev, stream):
         out, p_out, out32 = _result(out, "out", (T, k, K), dev)
-        ws, p_ws, nbytes = _scratch(workspace, experts_dx_workspace_size(T, k, E, N, K, g), dev)
-        check(lib().any4_experts_gemm_dx(fmt, p_dy, p_packed, p_lut, p_alpha, p_beta, p_ids, p_plan, p_out, out32, T, k,
-                                         E, N, K, g, p_ws, nbytes, _current_handle(dev.index)))
+        ws, p_ws, nbytes = _scratch(workspace, size(T, k, E, N, K, g), dev)
+        check(call(fmt, p_dy, p_packed, p_lut, p_alpha, p_beta, p_ids, p_plan, p_out, out32, T, k, E, N, K, g, p_ws, nbytes,
+                   _current_handle(dev.index)))
     return out
 
 
@@ -1344,8 +1360,9 @@ def experts_gemm_dx(dy: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, a
                     g: int, ids: torch.Tensor, plan: LoraPlan | None = None, out: torch.Tensor | None = None,
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dx [T, k, K] = dy bf16 [T, k, N] W_e, the gradient of the rows that went through
-    experts_gemm (bf16, or out's fp32).  Where the k pairs of a token shared a row, its gradient is their
-    sum: combine(dx)."""
+    experts_gemm (bf16, or out's fp32).  dy may be [2, T, k, N], in two parts (act_backward's
+    dz), for twice the matrix work: then it is not rounded to bf16 in between.  Where the k
+    pairs of a token shared a row, its gradient is their sum: combine(dx)."""
     return _experts_gemm_dx(0, dy, packed, lut, alpha, beta, g, ids, plan, out, workspace, stream)
 
 

@@ -174,20 +174,18 @@ struct Epilogue {
 };
 
 // fp32 as the bf16 parts hi + lo: hi cut off, lo what is left, rounded (2^-16 of the
-// value at most).  An infinity has no lo.
+// value at most).  An infinity has no lo.  (Not contracted: lo is what is left of the
+// rounded value that hi was cut from, not of a product behind it.)
 __device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo)
 {
+#pragma clang fp contract(off)
     const uint32_t top = __builtin_bit_cast(uint32_t, v) & 0xffff0000u;
     hi = top >> 16;
     lo = f32_to_bf16(__builtin_isinf(v) ? 0.0f : v - __builtin_bit_cast(float, top));
 }
 
-__device__ __forceinline__ void put_outs(const Epilogue& q, size_t at, int valid, const float (&v)[8])
+__device__ __forceinline__ void put_parts(uint16_t* to, size_t plane, int valid, const float (&v)[8])
 {
-    if (q.out32 != ANY4_PARTS) {
-        put_values(q.out, q.out32, at, valid, v);
-        return;
-    }
     u32x4_t hi, lo;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -197,9 +195,17 @@ __device__ __forceinline__ void put_outs(const Epilogue& q, size_t at, int valid
         hi[i] = h[0] | h[1] << 16;
         lo[i] = l[0] | l[1] << 16;
     }
-    uint16_t* out = static_cast<uint16_t*>(q.out) + at;
-    store8(out, hi, valid);
-    store8(out + q.plane, lo, valid);
+    store8(to, hi, valid);
+    store8(to + plane, lo, valid);
+}
+
+__device__ __forceinline__ void put_outs(const Epilogue& q, size_t at, int valid, const float (&v)[8])
+{
+    if (q.out32 != ANY4_PARTS) {
+        put_values(q.out, q.out32, at, valid, v);
+        return;
+    }
+    put_parts(static_cast<uint16_t*>(q.out) + at, q.plane, valid, v);
 }
 
 __device__ __forceinline__ void put_out(const Epilogue& q, size_t at, float v)
@@ -1128,7 +1134,7 @@ __global__ __launch_bounds__(64 * ROWS_WAVES) void k_rows(const Layer layer, uin
 // ---------------------------------------------------------------------------
 struct BwdArgs {
     const void *dy, *z;
-    uint16_t* dz;
+    uint16_t* dz;            // [M][N], in parts [2][M][N]
     float* part;             // [slabs][N] or null: no bias
     int M, N, No, act, slab; // rows of a workgroup
 };
@@ -1143,7 +1149,7 @@ constexpr int BWD_FEW = 128;                 // rows of the one slab of few
 // on is known to the compiler, and a row past the last is the last again: a branch
 // between them would make each wait for the one before.  4096 x 28672, gated, 587 MB:
 // 117 us, 5.0 TB/s, a copy's rate.
-template <bool DY32, bool Z32, bool GATE, bool WHOLE, int WAVES, int LANES>
+template <bool DY32, bool Z32, bool GATE, bool WHOLE, bool SPLIT, int WAVES, int LANES>
 __global__ __launch_bounds__(WAVE * WAVES) void k_act_bwd(const BwdArgs p)
 {
     constexpr int COLS = 8 * LANES, AT_ONCE = WAVES * (WAVE / LANES), ROWS = WAVES == 4 ? 2 : 1;
@@ -1185,9 +1191,15 @@ __global__ __launch_bounds__(WAVE * WAVES) void k_act_bwd(const BwdArgs p)
                 sum[0][i] += a[i];
             }
             const size_t at = static_cast<size_t>(m + AT_ONCE * r) * p.N + col;
-            put_values(p.dz, 0, at, valid, a);
+            auto put = [&](size_t to, const float (&v)[8]) __attribute__((always_inline)) {
+                if constexpr (SPLIT)
+                    put_parts(p.dz + to, static_cast<size_t>(p.M) * p.N, valid, v);
+                else
+                    put_values(p.dz, 0, to, valid, v);
+            };
+            put(at, a);
             if constexpr (GATE)
-                put_values(p.dz, 0, at + p.No, valid, b);
+                put(at + p.No, b);
         }
     }
     if (!p.part)
@@ -1480,6 +1492,117 @@ int64_t bwd_slab(int64_t M, int64_t No, bool bias)
     return (slab + 3) / 4 * 4;
 }
 
+template <bool SPLIT>
+any4_status act_backward(const void* dy, int dy_f32, const void* z, int z_f32, uint16_t* dz, float* dbias, any4_activation act,
+                         int gate, int64_t M, int64_t N, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!act_ok(act) || M < 0 || M > MAX_PAIRS || N < 0 || N > GIB2 / 4 || (M > 0 && N >= GIB2 / 2 / M) || (gate && N % 2))
+        return ANY4_E_SHAPE;
+    if (N == 0 || (M == 0 && !dbias))
+        return ANY4_OK;
+    const size_t need = dbias ? any4_act_backward_workspace_size(M, N, gate) : 0;
+    if (M > 0 && (!dy || !z || !dz || (need && !workspace)))
+        return ANY4_E_NULL;
+    if (!is_aligned(dbias, 4) || (M > 0 && (!is_aligned(dy, dy_f32 ? 4 : 2) || !is_aligned(z, z_f32 ? 4 : 2) || !is_aligned(dz, 2) || !is_aligned(workspace, 16))))
+        return ANY4_E_ALIGN;
+    const int n = static_cast<int>(N), no = static_cast<int>(gate ? N / 2 : N);
+    const int slab = M > 0 ? static_cast<int>(bwd_slab(M, no, dbias != nullptr)) : 1, slabs = static_cast<int>((M + slab - 1) / slab);
+    if (need && workspace_bytes < need)
+        return ANY4_E_WORKSPACE;
+    (void)hipGetLastError();
+    float* part = need ? static_cast<float*>(workspace) : dbias;
+    if (M > 0) {
+        const BwdArgs a{dy, z, dz, part, static_cast<int>(M), n, no, static_cast<int>(act), slab};
+        const bool few = slabs == 1 && dbias;
+        const int cols = few ? 64 : BWD_COLS;
+        const dim3 grid(static_cast<unsigned>((no + cols - 1) / cols), static_cast<unsigned>(slabs));
+        auto launch = [&](auto dy32, auto z32) {
+#define BWD(GATE_, WHOLE_)                                                                                                     \
+    do {                                                                                                                       \
+        constexpr bool D = decltype(dy32)::value, Z = decltype(z32)::value;                                                    \
+        if (few)                                                                                                               \
+            hipLaunchKernelGGL((k_act_bwd<D, Z, GATE_, WHOLE_, SPLIT, 8, 8>), grid, dim3(8 * WAVE), 0, stream, a);                    \
+        else                                                                                                                   \
+            hipLaunchKernelGGL((k_act_bwd<D, Z, GATE_, WHOLE_, SPLIT, 4, WAVE>), grid, dim3(4 * WAVE), 0, stream, a);                 \
+    } while (0)
+            if (gate && no % 8 == 0) BWD(true, true);
+            else if (gate) BWD(true, false);
+            else if (no % 8 == 0) BWD(false, true);
+            else BWD(false, false);
+#undef BWD
+        };
+        if (dy_f32 && z_f32) launch(std::true_type{}, std::true_type{});
+        else if (dy_f32) launch(std::true_type{}, std::false_type{});
+        else if (z_f32) launch(std::false_type{}, std::true_type{});
+        else launch(std::false_type{}, std::false_type{});
+    }
+    if (dbias && slabs != 1)         // none: zeros
+        hipLaunchKernelGGL(k_bias_sum, dim3(static_cast<unsigned>((n + WAVE - 1) / WAVE)), dim3(256), 0, stream, part, dbias, n, slabs);
+    return launch_status();
+}
+
+size_t experts_dx_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g, bool parts)
+{
+    if (T <= 0 || k <= 0 || N <= 0 || T > MAX_PAIRS || k > MAX_PAIRS || !sizes_ok(T * k, T * k, E, (N + 7) / 8 * 8, K, g))
+        return 0;
+    const int64_t P = T * k;
+    return part_bytes(shape_of(P, E, true, N, K, true, parts), P, K, N) + any4_lora_plan_bytes(P, E) +
+           up256(static_cast<size_t>(P) * ((N + 7) / 8 * 8) * (parts ? 4 : 2));
+}
+
+// parts: dy in two parts
+any4_status experts_dx(any4_format format, const uint16_t* dy, bool parts, const uint8_t* packed, const uint16_t* lut,
+                       const uint16_t* alpha, const uint16_t* beta, const int32_t* ids, const void* plan, void* dx,
+                       int dx_f32, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream)
+{
+    const int fmt = static_cast<int>(format);
+    if (!fmt_ok(fmt) || T < 0 || k < 1 || T > MAX_PAIRS || k > MAX_PAIRS || N < 1 ||
+        !sizes_ok(T * k, T * k, E, (N + 7) / 8 * 8, K, g))
+        return ANY4_E_SHAPE;
+    if (T == 0)
+        return ANY4_OK;
+    if (!dy || !packed || (fmt != FMT_INT4 && !lut) || !alpha || !beta || !ids || !dx || !workspace)
+        return ANY4_E_NULL;
+    if (!is_aligned(dy, 2) || !is_aligned(packed, 16) || !is_aligned(lut, 2) || !is_aligned(alpha, 2) || !is_aligned(beta, 2) ||
+        !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(dx, dx_f32 ? 4 : 2) || !is_aligned(workspace, 16))
+        return ANY4_E_ALIGN;
+    if (workspace_bytes < experts_dx_bytes(T, k, E, N, K, g, parts))
+        return ANY4_E_WORKSPACE;
+    (void)hipGetLastError();
+    const int P = static_cast<int>(T * k), Np = static_cast<int>((N + 7) / 8 * 8);
+    const Shape s = shape_of(P, E, true, N, K, true, parts);
+    char* at = static_cast<char*>(workspace);
+    if (!plan) {
+        const any4_status st = any4_lora_plan(ids, at, any4_lora_plan_bytes(P, E), P, E, stream);
+        if (st != ANY4_OK)
+            return st;
+        plan = at;
+    }
+    at += any4_lora_plan_bytes(P, E);
+    if (N != Np || !is_aligned(dy, 16)) {
+        uint16_t* copy = reinterpret_cast<uint16_t*>(at);
+        const size_t pieces = static_cast<size_t>(P) * (Np / 8) * (parts ? 2 : 1);
+        hipLaunchKernelGGL(k_pad_rows, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, dy, copy,
+                           static_cast<int>(N), Np, pieces);
+        dy = copy;
+    }
+    at += up256(static_cast<size_t>(P) * Np * (parts ? 4 : 2));
+    const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
+    const Epilogue q{nullptr, nullptr, nullptr, dx, s.S > 1 ? reinterpret_cast<float*>(at) : nullptr, static_cast<int>(K),
+                     static_cast<int>(K), ACT_NONE, s.S, 0, dx_f32 != 0, 0};
+    const Rows r{nullptr, static_cast<const int*>(plan), P, static_cast<int>(E), 1};
+    const TileArgs a{r, w, dy, q, P, Np, (Np + STEP - 1) / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)};
+    if (parts) launch_tile<true, true>(fmt, s, a, stream);
+    else launch_tile<true, false>(fmt, s, a, stream);
+    if (s.S > 1) {
+        const size_t pieces = static_cast<size_t>(P) * (K / 8);
+        hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, q, ids, r.plan, P, static_cast<int>(E),
+                           pieces);
+    }
+    return launch_status();
+}
+
 }  // namespace
 
 extern "C" {
@@ -1524,49 +1647,13 @@ size_t any4_act_backward_workspace_size(int64_t M, int64_t N, int gate)
 any4_status any4_act_backward(const void* dy, int dy_f32, const void* z, int z_f32, uint16_t* dz, float* dbias, any4_activation act,
                               int gate, int64_t M, int64_t N, void* workspace, size_t workspace_bytes, hipStream_t stream)
 {
-    if (!act_ok(act) || M < 0 || M > MAX_PAIRS || N < 0 || N > GIB2 / 4 || (M > 0 && N >= GIB2 / 2 / M) || (gate && N % 2))
-        return ANY4_E_SHAPE;
-    if (N == 0 || (M == 0 && !dbias))
-        return ANY4_OK;
-    const size_t need = dbias ? any4_act_backward_workspace_size(M, N, gate) : 0;
-    if (M > 0 && (!dy || !z || !dz || (need && !workspace)))
-        return ANY4_E_NULL;
-    if (!is_aligned(dbias, 4) || (M > 0 && (!is_aligned(dy, dy_f32 ? 4 : 2) || !is_aligned(z, z_f32 ? 4 : 2) || !is_aligned(dz, 2) || !is_aligned(workspace, 16))))
-        return ANY4_E_ALIGN;
-    const int n = static_cast<int>(N), no = static_cast<int>(gate ? N / 2 : N);
-    const int slab = M > 0 ? static_cast<int>(bwd_slab(M, no, dbias != nullptr)) : 1, slabs = static_cast<int>((M + slab - 1) / slab);
-    if (need && workspace_bytes < need)
-        return ANY4_E_WORKSPACE;
-    (void)hipGetLastError();
-    float* part = need ? static_cast<float*>(workspace) : dbias;
-    if (M > 0) {
-        const BwdArgs a{dy, z, dz, part, static_cast<int>(M), n, no, static_cast<int>(act), slab};
-        const bool few = slabs == 1 && dbias;
-        const int cols = few ? 64 : BWD_COLS;
-        const dim3 grid(static_cast<unsigned>((no + cols - 1) / cols), static_cast<unsigned>(slabs));
-        auto launch = [&](auto dy32, auto z32) {
-#define BWD(GATE_, WHOLE_)                                                                                                     \
-    do {                                                                                                                       \
-        constexpr bool D = decltype(dy32)::value, Z = decltype(z32)::value;                                                    \
-        if (few)                                                                                                               \
-            hipLaunchKernelGGL((k_act_bwd<D, Z, GATE_, WHOLE_, 8, 8>), grid, dim3(8 * WAVE), 0, stream, a);                    \
-        else                                                                                                                   \
-            hipLaunchKernelGGL((k_act_bwd<D, Z, GATE_, WHOLE_, 4, WAVE>), grid, dim3(4 * WAVE), 0, stream, a);                 \
-    } while (0)
-            if (gate && no % 8 == 0) BWD(true, true);
-            else if (gate) BWD(true, false);
-            else if (no % 8 == 0) BWD(false, true);
-            else BWD(false, false);
-#undef BWD
-        };
-        if (dy_f32 && z_f32) launch(std::true_type{}, std::true_type{});
-        else if (dy_f32) launch(std::true_type{}, std::false_type{});
-        else if (z_f32) launch(std::false_type{}, std::true_type{});
-        else launch(std::false_type{}, std::false_type{});
-    }
-    if (dbias && slabs != 1)         // none: zeros
-        hipLaunchKernelGGL(k_bias_sum, dim3(static_cast<unsigned>((n + WAVE - 1) / WAVE)), dim3(256), 0, stream, part, dbias, n, slabs);
-    return launch_status();
+    return act_backward<false>(dy, dy_f32, z, z_f32, dz, dbias, act, gate, M, N, workspace, workspace_bytes, stream);
+}
+
+any4_status any4_act_backward_parts(const void* dy, int dy_f32, const void* z, int z_f32, uint16_t* dz, float* dbias, any4_activation act,
+                                    int gate, int64_t M, int64_t N, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    return act_backward<true>(dy, dy_f32, z, z_f32, dz, dbias, act, gate, M, N, workspace, workspace_bytes, stream);
 }
 
 size_t any4_experts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g)
@@ -1616,11 +1703,12 @@ any4_status any4_experts_gemm(any4_format format, const void* x, int x_f32, int 
 
 size_t any4_experts_dx_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g)
 {
-    if (T <= 0 || k <= 0 || N <= 0 || T > MAX_PAIRS || k > MAX_PAIRS || !sizes_ok(T * k, T * k, E, (N + 7) / 8 * 8, K, g))
-        return 0;
-    const int64_t P = T * k;
-    return part_bytes(shape_of(P, E, true, N, K, true), P, K, N) + any4_lora_plan_bytes(P, E) +
-           up256(static_cast<size_t>(P) * ((N + 7) / 8 * 8) * 2);
+    return experts_dx_bytes(T, k, E, N, K, g, false);
+}
+
+size_t any4_experts_dx_parts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g)
+{
+    return experts_dx_bytes(T, k, E, N, K, g, true);
 }
 
 any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const uint8_t* packed, const uint16_t* lut,
@@ -1628,50 +1716,15 @@ any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const u
                                  int dx_f32, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream)
 {
-    const int fmt = static_cast<int>(format);
-    if (!fmt_ok(fmt) || T < 0 || k < 1 || T > MAX_PAIRS || k > MAX_PAIRS || N < 1 ||
-        !sizes_ok(T * k, T * k, E, (N + 7) / 8 * 8, K, g))
-        return ANY4_E_SHAPE;
-    if (T == 0)
-        return ANY4_OK;
-    if (!dy || !packed || (fmt != FMT_INT4 && !lut) || !alpha || !beta || !ids || !dx || !workspace)
-        return ANY4_E_NULL;
-    if (!is_aligned(dy, 2) || !is_aligned(packed, 16) || !is_aligned(lut, 2) || !is_aligned(alpha, 2) || !is_aligned(beta, 2) ||
-        !is_aligned(ids, 4) || !is_aligned(plan, 16) || !is_aligned(dx, dx_f32 ? 4 : 2) || !is_aligned(workspace, 16))
-        return ANY4_E_ALIGN;
-    if (workspace_bytes < any4_experts_dx_workspace_size(T, k, E, N, K, g))
-        return ANY4_E_WORKSPACE;
-    (void)hipGetLastError();
-    const int P = static_cast<int>(T * k), Np = static_cast<int>((N + 7) / 8 * 8);
-    const Shape s = shape_of(P, E, true, N, K, true);
-    char* at = static_cast<char*>(workspace);
-    if (!plan) {
-        const any4_status st = any4_lora_plan(ids, at, any4_lora_plan_bytes(P, E), P, E, stream);
-        if (st != ANY4_OK)
-            return st;
-        plan = at;
-    }
-    at += any4_lora_plan_bytes(P, E);
-    if (N != Np || !is_aligned(dy, 16)) {
-        uint16_t* copy = reinterpret_cast<uint16_t*>(at);
-        const size_t pieces = static_cast<size_t>(P) * (Np / 8);
-        hipLaunchKernelGGL(k_pad_rows, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, dy, copy,
-                           static_cast<int>(N), Np, pieces);
-        dy = copy;
-    }
-    at += up256(static_cast<size_t>(P) * Np * 2);
-    const Layer w{packed, lut, alpha, beta, static_cast<int>(N), static_cast<int>(K), static_cast<int>(g), layer_bytes(fmt, N, K)};
-    const Epilogue q{nullptr, nullptr, nullptr, dx, s.S > 1 ? reinterpret_cast<float*>(at) : nullptr, static_cast<int>(K),
-                     static_cast<int>(K), ACT_NONE, s.S, 0, dx_f32 != 0, 0};
-    const Rows r{nullptr, static_cast<const int*>(plan), P, static_cast<int>(E), 1};
-    launch_tile<true, false>(fmt, s, TileArgs{r, w, dy, q, P, Np, (Np + STEP - 1) / STEP, static_cast<int>(s.tiles_m), static_cast<int>(s.tiles_n)},
-                      stream);
-    if (s.S > 1) {
-        const size_t pieces = static_cast<size_t>(P) * (K / 8);
-        hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, stream, q, ids, r.plan, P, static_cast<int>(E),
-                           pieces);
-    }
-    return launch_status();
+    return experts_dx(format, dy, false, packed, lut, alpha, beta, ids, plan, dx, dx_f32, T, k, E, N, K, g, workspace, workspace_bytes, stream);
+}
+
+any4_status any4_experts_gemm_dx_parts(any4_format format, const uint16_t* dy, const uint8_t* packed, const uint16_t* lut,
+                                       const uint16_t* alpha, const uint16_t* beta, const int32_t* ids, const void* plan, void* dx,
+                                       int dx_f32, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream)
+{
+    return experts_dx(format, dy, true, packed, lut, alpha, beta, ids, plan, dx, dx_f32, T, k, E, N, K, g, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -582,12 +582,17 @@ any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* 
  *   workspace  device, 16-byte aligned, any4_act_backward_workspace_size(M, N, gate)
  *          bytes, required with dbias where that is not 0.
  *   dy, z and dz need 2-byte alignment, dbias 4.
+ * any4_act_backward_parts writes dz in two bf16 parts, [2][M][N] (not z itself), as
+ * any4_experts_gemm_dx_parts takes it; all else is the same.
  * Errors: as any4_gemm_act.
  */
 size_t any4_act_backward_workspace_size(int64_t M, int64_t N, int gate);
 any4_status any4_act_backward(const void* dy, int dy_f32, const void* z, int z_f32, uint16_t* dz,
                               float* dbias, any4_activation act, int gate, int64_t M, int64_t N, void* workspace,
                               size_t workspace_bytes, hipStream_t stream);
+any4_status any4_act_backward_parts(const void* dy, int dy_f32, const void* z, int z_f32, uint16_t* dz,
+                                    float* dbias, any4_activation act, int gate, int64_t M, int64_t N, void* workspace,
+                                    size_t workspace_bytes, hipStream_t stream);
 
 /*
  * any4_route -- the experts of each token and their weights, from the router's
@@ -673,6 +678,8 @@ any4_status any4_experts_gemm(any4_format format, const void* x, int x_f32, int 
  *   N >= 1; sizes, ids, plan and errors as any4_experts_gemm (here N is taken
  *   rounded up to a multiple of 8).
  *   workspace  device, any4_experts_dx_workspace_size(T, k, E, N, K, g) bytes, required.
+ * any4_experts_gemm_dx_parts takes dy in two bf16 parts, [2][T*k][N], for twice the matrix work,
+ * and any4_experts_dx_parts_workspace_size bytes; all else is the same.
  */
 size_t any4_experts_dx_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g);
 any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const uint8_t* packed,
@@ -680,6 +687,12 @@ any4_status any4_experts_gemm_dx(any4_format format, const uint16_t* dy, const u
                                  const int32_t* ids, const void* plan, void* dx, int dx_f32, int64_t T,
                                  int64_t k, int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream);
+size_t any4_experts_dx_parts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g);
+any4_status any4_experts_gemm_dx_parts(any4_format format, const uint16_t* dy, const uint8_t* packed,
+                                       const uint16_t* lut, const uint16_t* alpha, const uint16_t* beta,
+                                       const int32_t* ids, const void* plan, void* dx, int dx_f32, int64_t T,
+                                       int64_t k, int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream);
 
 /*
  * any4_combine, any4_combine_backward -- the experts' outputs as the router
