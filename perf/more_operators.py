@@ -408,11 +408,10 @@ def _experts_call(fmt):
             "any3": any4.any3_experts_gemm}[fmt]
 
 
-def _between(case, device):
-    """For what lies between the two products: in fp32 where the second takes it, for up to 64 pairs (a
-    few tokens' roundings to bf16 are not averaged over others)."""
-    kind = torch.float32 if case["T"] * case["k"] <= 64 else torch.bfloat16
-    return torch.empty((case["T"], case["k"], case["F"]), dtype=kind, device=device)
+def _between(case, n, device):
+    """For n columns of what lies between two products, in two bf16 parts: rows of a product need not
+    be rounded to bf16, whatever the number of pairs."""
+    return torch.empty((2, case["T"], case["k"], n), dtype=torch.bfloat16, device=device)
 
 
 def _run_moe(s, case):
@@ -423,7 +422,7 @@ def _run_moe(s, case):
         call = _experts_call(fmt)
         w, ids = any4.route(s["logits"], case["k"])
         plan = any4.experts_plan(ids, E)
-        h = _between(case, ids.device)
+        h = _between(case, case["F"], ids.device)
         call(s["x"], *_tables(fmt, s["up"]), g, ids, act="silu", gate=True, plan=plan, out=h)
         y = torch.empty((case["T"], case["k"], case["D"]), dtype=torch.float32, device=ids.device)
         return any4.combine(call(h, *_tables(fmt, s["down"]), g, ids, plan=plan, out=y), w)
@@ -443,14 +442,14 @@ def _run_experts(s, case):
         back = {"any4": any4.experts_gemm_dx, "int4": any4.experts_gemm_int4_dx, "any2": any4.any2_experts_gemm_dx,
                 "any3": any4.any3_experts_gemm_dx}[fmt]
         plan = any4.experts_plan(ids, E)
-        # z and the rows' gradients are kept in fp32
+        # z and the rows' gradients are kept in fp32, what enters a product in parts
         z, dh, dx = (torch.empty((T, k, n), dtype=torch.float32, device=ids.device)
                      for n in (2 * case["F"], case["F"], case["D"]))
-        h = _between(case, ids.device)
+        h, dz = (_between(case, n, ids.device) for n in (case["F"], 2 * case["F"]))
         call(s["x"], *_tables(fmt, s["up"]), g, ids, act="silu", gate=True, z=z, plan=plan, out=h)
         y = call(h, *_tables(fmt, s["down"]), g, ids, plan=plan)
         back(s["dy"], *_tables(fmt, s["down"]), g, ids, plan=plan, out=dh)
-        dz, _ = any4.act_backward(dh, z, act="silu", gate=True, need_bias=False)
+        any4.act_backward(dh, z, act="silu", gate=True, need_bias=False, dz=dz)
         back(dz, *_tables(fmt, s["up"]), g, ids, plan=plan, out=dx)
         return {"y": y, "dx": any4.combine(dx)}
     up, down = _weights(s["up"], fmt, g), _weights(s["down"], fmt, g)
