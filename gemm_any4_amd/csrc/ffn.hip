@@ -1026,7 +1026,7 @@ __global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileAr
             if (ch < c1) {
                 meet(All{});
                 first_step(ch, A);
-                meet(AllButChunk{});
+                meet(All{});         // no chunk is asked for here: the last loads are the tile's own
                 second_step(ch, B);
             }
         }
