@@ -113,12 +113,15 @@ __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf
 constexpr float GELU_C = 1.5957691216057308f;       // 2 sqrt(2 / pi)
 constexpr float GELU_D = 0.044715f;
 
+// The normal distribution's integral up to z; 1 + erf would cancel left of 0 (4% off at -5).
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }
+
 __device__ __forceinline__ float activate(float z, int act)
 {
     switch (act) {
     case ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
     case ACT_SILU: return z * sigmoid(z);
-    case ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case ACT_GELU: return z * normal_cdf(z);
     case ACT_GELU_TANH: return z * sigmoid(GELU_C * (z + GELU_D * z * z * z));
     default: return z;
     }
@@ -139,7 +142,7 @@ __device__ __forceinline__ void activate_both(float z, int act, float& f, float&
         break;
     }
     case ACT_GELU: {
-        const float p = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+        const float p = normal_cdf(z);
         f = z * p;
         slope = p + z * 0.39894228040143268f * expf(-0.5f * z * z);
         break;
