@@ -1516,7 +1516,8 @@ any4_status act_backward(const void* dy, int dy_f32, const void* z, int z_f32, u
     float* part = need ? static_cast<float*>(workspace) : dbias;
     if (M > 0) {
         const BwdArgs a{dy, z, dz, part, static_cast<int>(M), n, no, static_cast<int>(act), slab};
-        const bool few = slabs == 1 && dbias;
+        // a grid has less than 2^32 threads, eight of these for each column
+        const bool few = slabs == 1 && dbias && no <= GIB2 / 8;
         const int cols = few ? 64 : BWD_COLS;
         const dim3 grid(static_cast<unsigned>((no + cols - 1) / cols), static_cast<unsigned>(slabs));
         auto launch = [&](auto dy32, auto z32) {
