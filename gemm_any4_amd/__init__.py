@@ -31,7 +31,7 @@ For a feed-forward block, dense or of experts: gemm_act, gemm_int4_act,
 any2_gemm_act and any3_gemm_act (the product with bias, activation, gate and
 residual), act_backward; route and route_backward (the experts of each token),
 experts_plan, experts_gemm and experts_gemm_dx (and their int4, any2 and any3
-forms: stacked layers, each row through its expert), combine and
+forms: stacked layers, each row through its expert), experts_bias_backward, combine and
 combine_backward (the weighted sum of the experts' outputs).  What one of these
 calls writes for another (z, an output for combine, an input's gradient for
 act_backward or combine) may be a bf16 tensor or an fp32 one, given as z or out;
@@ -70,7 +70,8 @@ EXPORTS = ("any4_packed_bytes", "any4_pack", "any4_dequant", "any4_gemm_workspac
            "any4_act8_load", "any4_gemm_dx_workspace_size", "any4_gemm_dx", "any4_gemm_int4_dx",
            "any2_gemm_dx", "any3_gemm_dx", "any4_gemm_act_workspace_size", "any4_gemm_act",
            "any4_act_backward_workspace_size", "any4_act_backward", "any4_act_backward_parts", "any4_route", "any4_route_backward",
-           "any4_experts_workspace_size", "any4_experts_parts_workspace_size", "any4_experts_gemm", "any4_experts_dx_workspace_size",
+           "any4_experts_workspace_size", "any4_experts_parts_workspace_size", "any4_experts_gemm", "any4_experts_bias_workspace_size", "any4_experts_bias_backward",
+           "any4_experts_dx_workspace_size",
            "any4_experts_gemm_dx", "any4_experts_dx_parts_workspace_size", "any4_experts_gemm_dx_parts", "any4_combine", "any4_combine_backward")
 
 _lib = None
@@ -145,6 +146,9 @@ def lib() -> ctypes.CDLL:
                 ("any4_experts_parts_workspace_size", SZ, [I64] * 6),
                 ("any4_experts_gemm", ctypes.c_int,
                  [INT, P, INT, INT] + [P] * 8 + [INT, P] + [INT] * 3 + [I64] * 6 + [P, SZ, P]),
+                ("any4_experts_bias_workspace_size", SZ, [I64] * 4),
+                ("any4_experts_bias_backward", ctypes.c_int,
+                 [P, INT, P, INT] + [P] * 3 + [INT] * 2 + [I64] * 4 + [P, SZ, P]),
                 ("any4_experts_dx_workspace_size", SZ, [I64] * 6),
                 ("any4_experts_gemm_dx", ctypes.c_int, [INT] + [P] * 8 + [INT] + [I64] * 6 + [P, SZ, P]),
                 ("any4_experts_dx_parts_workspace_size", SZ, [I64] * 6),
@@ -996,6 +1000,12 @@ def experts_gemm_raw(fmt, x_ptr, per_pair, packed_ptr, lut_ptr, alpha_ptr, beta_
                                    ws_ptr, ws_bytes, _stream(stream))
 
 
+def experts_bias_backward_raw(dy_ptr, z_ptr, ids_ptr, plan_ptr, dbias_ptr, act, gate, T, k, E, N, ws_ptr, ws_bytes,
+                              stream=None, dy_f32=0, z_f32=0) -> int:
+    return lib().any4_experts_bias_backward(dy_ptr, dy_f32, z_ptr, z_f32, ids_ptr, plan_ptr, dbias_ptr, act, gate, T, k,
+                                            E, N, ws_ptr, ws_bytes, _stream(stream))
+
+
 def experts_gemm_dx_raw(fmt, dy_ptr, packed_ptr, lut_ptr, alpha_ptr, beta_ptr, ids_ptr, plan_ptr, dx_ptr, T, k, E, N, K,
                         g, ws_ptr, ws_bytes, stream=None, dx_f32=0, call="any4_experts_gemm_dx") -> int:
     """call: "any4_experts_gemm_dx" or "any4_experts_gemm_dx_parts"."""
@@ -1029,6 +1039,11 @@ def experts_workspace_size(T: int, k: int, E: int, N: int, K: int, g: int) -> in
 @functools.lru_cache(maxsize=4096)      # constant for its sizes
 def experts_parts_workspace_size(T: int, k: int, E: int, N: int, K: int, g: int) -> int:
     return int(lib().any4_experts_parts_workspace_size(T, k, E, N, K, g))
+
+
+@functools.lru_cache(maxsize=4096)      # constant for its sizes
+def experts_bias_workspace_size(T: int, k: int, E: int, N: int) -> int:
+    return int(lib().any4_experts_bias_workspace_size(T, k, E, N))
 
 
 @functools.lru_cache(maxsize=4096)      # constant for its sizes
@@ -1160,8 +1175,9 @@ def act_backward(dy: torch.Tensor, z: torch.Tensor, act: str, gate: bool = False
     """(dz, dbias) of an epilogue for dy [..., No], from z [..., N] as gemm_act or
     experts_gemm kept it (either may be bf16 or fp32): dz bf16 (may be a bf16 z itself), or
     given as [2, ..., N] the values in two parts, for experts_gemm_dx;
-    dbias fp32 [N], the sum over all rows (need_bias = False: None).  The gradient of the
-    product's input is gemm_dx (experts_gemm_dx) of dz, that of the residual dy itself."""
+    dbias fp32 [N], the sum over all rows (need_bias = False: None; the bias [E, N] of many
+    experts has its gradient from experts_bias_backward).  The gradient of the product's
+    input is gemm_dx (experts_gemm_dx) of dz, that of the residual dy itself."""
     if not z.is_cuda:
         raise ValueError("z must be a GPU tensor")
     if z.dim() < 2:
@@ -1338,6 +1354,31 @@ def any3_experts_gemm(x: torch.Tensor, packed: torch.Tensor, lut: torch.Tensor, 
                       stream=None) -> torch.Tensor:
     """experts_gemm of any3 layers."""
     return _experts_gemm(3, x, packed, lut, alpha, beta, g, ids, bias, act, gate, z, plan, out, workspace, stream)
+
+
+def experts_bias_backward(dy: torch.Tensor, z: torch.Tensor, ids: torch.Tensor, E: int, act: str, gate: bool = False,
+                          plan: LoraPlan | None = None, out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dbias fp32 [E, N], the gradient of experts_gemm's bias, for dy [T, k, No] and the
+    z [T, k, N] that it kept (either bf16 or fp32): the sum over each expert's pairs of what
+    act_backward gives as dz, before its rounding.  Zeros for experts without a pair; pairs
+    whose id is not in 0..E-1 are left out."""
+    dev = _gpu(z, "z", 3)
+    T, k, p_ids, p_plan = _pairs(ids, E, plan, dev)
+    N = z.shape[2]
+    if gate and N % 2:
+        raise ValueError("a gated layer must have an even number of rows")
+    p_z, z32 = _kept(z, "z", (T, k, N), dev)
+    p_dy, dy32 = _kept(dy, "dy", (T, k, N // 2 if gate else N), dev)
+    number = _choice("act", act, ACTIVATIONS)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((E, N), dtype=torch.float32, device=dev)
+        p_out = _tensor(out, "out", torch.float32, (E, N), dev)
+        ws, p_ws, nbytes = _scratch(workspace, experts_bias_workspace_size(T, k, E, N), dev)
+        check(lib().any4_experts_bias_backward(p_dy, dy32, p_z, z32, p_ids, p_plan, p_out, number, 1 if gate else 0, T, k, E,
+                                               N, p_ws, nbytes, _current_handle(dev.index)))
+    return out
 
 
 def _experts_gemm_dx(fmt: int, dy, packed, lut, alpha, beta, g, ids, plan, out, workspace, stream) -> torch.Tensor:

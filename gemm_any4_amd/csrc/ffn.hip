@@ -668,7 +668,8 @@ constexpr int parts_of(int blocks) { return blocks >= 2 ? 4 : 2; }
 // tile the first 32 are the hi parts of 32 pairs, the others their lo parts; a wave has both,
 // and adds their sums at the end.  (2062 pairs through 8 experts of 4096 x 14336 686 us for
 // 444 in bf16, 8192 through 16 of 2048 x 1024 115 for 89: what is decoded serves as many
-// products, of half as many pairs.)
+// products, of half as many pairs.  TURN: 2062 pairs back through 28672 x 4096 1800 for 1029, 8192
+// through 2048 x 2048 271 for 179.)
 //
 // The matrix cores take a 16 x 16 x 32 product in 7.8 ns and let two vector instructions
 // in for nothing; every further one costs its 1.9 ns.  Decoding is 4.2 instructions a
@@ -1142,6 +1143,22 @@ struct BwdArgs {
     int M, N, No, act, slab; // rows of a workgroup
 };
 
+// Of eight columns: a what dz is, or with a gate its half of the gate's rows, b the up rows'.
+template <bool GATE>
+__device__ __forceinline__ void gradients(const float (&d)[8], const float (&zg)[8], const float (&zu)[8], int act, float (&a)[8], float (&b)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float f, slope;
+        activate_both(zg[i], act, f, slope);
+        a[i] = d[i] * slope;
+        if constexpr (GATE) {
+            a[i] *= zu[i];
+            b[i] = d[i] * f;
+        }
+    }
+}
+
 constexpr int BWD_COLS = 8 * WAVE;           // columns of out of a workgroup
 
 constexpr int BWD_FEW = 128;                 // rows of the one slab of few
@@ -1181,17 +1198,12 @@ __global__ __launch_bounds__(WAVE * WAVES) void k_act_bwd(const BwdArgs p)
             if (m + AT_ONCE * r >= m1)
                 break;
             float a[8], b[8];
+            gradients<GATE>(d[r], zg[r], zu[r], p.act, a, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                float f, slope;
-                activate_both(zg[r][i], p.act, f, slope);
-                a[i] = d[r][i] * slope;
-                if constexpr (GATE) {
-                    a[i] *= zu[r][i];
-                    b[i] = d[r][i] * f;
-                    sum[1][i] += b[i];
-                }
                 sum[0][i] += a[i];
+                if constexpr (GATE)
+                    sum[1][i] += b[i];
             }
             const size_t at = static_cast<size_t>(m + AT_ONCE * r) * p.N + col;
             auto put = [&](size_t to, const float (&v)[8]) __attribute__((always_inline)) {
@@ -1246,6 +1258,97 @@ __global__ __launch_bounds__(256) void k_bias_sum(const float* __restrict__ part
     __syncthreads();
     if (w == 0 && n < N)
         dbias[n] = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
+}
+
+// ---------------------------------------------------------------------------
+// the gradient of the experts' bias
+// ---------------------------------------------------------------------------
+struct ExpertBiasArgs {
+    const void *dy, *z;
+    const int* plan;         // null: no pairs
+    float *dbias, *part;     // [E][N], [slots][N]
+    int P, E, N, No, act;
+
+    __device__ __forceinline__ bool fits() const { return !plan || (plan[2] == P && plan[3] == E); }
+};
+
+// The sums over one expert's pairs, 64 columns and a chunk of the plan (up to 512 pairs) a
+// workgroup: eight lanes have a pair's columns, 64 pairs at a time, whose sums meet in LDS.  In
+// the plan's order, so that they are the same each time.  Bound by its bytes: 2062 pairs of 28672
+// columns in fp32, gated, 355 MB: 69 us, 5.1 TB/s; 8192 of 2048 through 16 experts 24 us.
+template <bool DY32, bool Z32, bool GATE, bool WHOLE>
+__global__ __launch_bounds__(8 * WAVE) void k_expert_bias(const ExpertBiasArgs p)
+{
+    constexpr int LANES = 8, COLS = 8 * LANES, AT_ONCE = 8 * WAVE / LANES;
+    __shared__ float red[AT_ONCE][GATE ? 2 : 1][8][LANES];
+    if (!p.fits() || static_cast<int>(blockIdx.y) >= p.plan[1])
+        return;
+    const PlanLayout l(p.P, p.E);
+    const int* chunk = p.plan + l.chunk + 4 * static_cast<int64_t>(blockIdx.y);
+    const int* pairs = p.plan + l.rows + chunk[1];
+    const int count = chunk[2], slot = chunk[3];
+    const int lane = threadIdx.x % LANES, w = threadIdx.x / LANES, col = blockIdx.x * COLS + 8 * lane;
+    const int left = p.No - col, valid = WHOLE ? 8 : left;
+    float sum[2][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        sum[0][i] = sum[1][i] = 0.0f;
+    for (int m = w; m < count && left > 0; m += AT_ONCE) {
+        const size_t row = pairs[m];
+        float d[8], zg[8], zu[8], a[8], b[8];
+        get_values(p.dy, DY32, row * p.No + col, valid, d);
+        get_values(p.z, Z32, row * p.N + col, valid, zg);
+        if constexpr (GATE)
+            get_values(p.z, Z32, row * p.N + p.No + col, valid, zu);
+        gradients<GATE>(d, zg, zu, p.act, a, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            sum[0][i] += a[i];
+            if constexpr (GATE)
+                sum[1][i] += b[i];
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < (GATE ? 2 : 1); ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            red[w][h][i][lane] = sum[h][i];
+    __syncthreads();
+    float* to = slot < 0 ? p.dbias + static_cast<size_t>(chunk[0]) * p.N : p.part + static_cast<size_t>(slot) * p.N;
+    for (int i = threadIdx.x; i < (GATE ? 2 : 1) * COLS; i += 8 * WAVE) {
+        const int h = i / COLS, o = i % COLS, c = blockIdx.x * COLS + o;
+        if (c >= p.No)
+            continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j)
+            v += red[j][h][o & 7][o >> 3];
+        to[h * p.No + c] = v;
+    }
+}
+
+// Experts of several chunks: their sums in order; those without a pair: zeros.
+__global__ __launch_bounds__(256) void k_expert_bias_sum(const ExpertBiasArgs p)
+{
+    const int e = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+    if (n >= p.N || !p.fits())
+        return;
+    const PlanLayout l(p.P, p.E);
+    const int chunks = p.plan ? (p.plan[l.count + e] + CHUNK - 1) / CHUNK : 0;
+    if (chunks == 1)                 // there already
+        return;
+    const float* part = chunks ? p.part + static_cast<size_t>(p.plan[l.slot + e]) * p.N + n : nullptr;
+    float v = 0.0f;
+    for (int i0 = 0; i0 < chunks; i0 += 8) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = i0 + i < chunks ? part[static_cast<size_t>(i0 + i) * p.N] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v += x[i];
+    }
+    p.dbias[static_cast<size_t>(e) * p.N + n] = v;
 }
 
 // ---------------------------------------------------------------------------
@@ -1545,6 +1648,15 @@ any4_status act_backward(const void* dy, int dy_f32, const void* z, int z_f32, u
     return launch_status();
 }
 
+bool bias_ok(int64_t T, int64_t k, int64_t E, int64_t N)
+{
+    return T >= 0 && T <= MAX_PAIRS && k >= 1 && k <= MAX_PAIRS && T * k <= MAX_PAIRS && E >= 1 && E <= MAX_EXPERTS && N >= 0 &&
+           N <= GIB2 / 8 && (T == 0 || N < GIB2 / 2 / (T * k));
+}
+
+// partial sums: of the chunks of experts with more than one
+size_t bias_part_bytes(int64_t P, int64_t N) { return P > CHUNK ? up256(static_cast<size_t>(2 * (P / CHUNK)) * N * 4) : 0; }
+
 size_t experts_dx_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g, bool parts)
 {
     if (T <= 0 || k <= 0 || N <= 0 || T > MAX_PAIRS || k > MAX_PAIRS || !sizes_ok(T * k, T * k, E, (N + 7) / 8 * 8, K, g))
@@ -1658,6 +1770,60 @@ any4_status any4_act_backward_parts(const void* dy, int dy_f32, const void* z, i
                                     int gate, int64_t M, int64_t N, void* workspace, size_t workspace_bytes, hipStream_t stream)
 {
     return act_backward<true>(dy, dy_f32, z, z_f32, dz, dbias, act, gate, M, N, workspace, workspace_bytes, stream);
+}
+
+size_t any4_experts_bias_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N)
+{
+    if (T <= 0 || N <= 0 || !bias_ok(T, k, E, N))
+        return 0;
+    return bias_part_bytes(T * k, N) + any4_lora_plan_bytes(T * k, E);
+}
+
+any4_status any4_experts_bias_backward(const void* dy, int dy_f32, const void* z, int z_f32, const int32_t* ids, const void* plan,
+                                       float* dbias, any4_activation act, int gate, int64_t T, int64_t k, int64_t E, int64_t N,
+                                       void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!act_ok(act) || !bias_ok(T, k, E, N) || (gate && N % 2))
+        return ANY4_E_SHAPE;
+    if (N == 0)
+        return ANY4_OK;
+    const int64_t P = T * k;
+    const size_t parts = bias_part_bytes(P, N), need = P == 0 ? 0 : parts + (plan ? 0 : any4_lora_plan_bytes(P, E));
+    if (!dbias || (P > 0 && (!dy || !z || !ids || (need && !workspace))))
+        return ANY4_E_NULL;
+    if (!is_aligned(dbias, 4) || (P > 0 && (!is_aligned(dy, dy_f32 ? 4 : 2) || !is_aligned(z, z_f32 ? 4 : 2) || !is_aligned(ids, 4) ||
+                                            !is_aligned(plan, 16) || !is_aligned(workspace, 16))))
+        return ANY4_E_ALIGN;
+    if (need && workspace_bytes < need)
+        return ANY4_E_WORKSPACE;
+    (void)hipGetLastError();
+    char* at = static_cast<char*>(workspace);
+    if (P > 0 && !plan) {
+        const any4_status st = any4_lora_plan(ids, at + parts, any4_lora_plan_bytes(P, E), P, E, stream);
+        if (st != ANY4_OK)
+            return st;
+        plan = at + parts;
+    }
+    const ExpertBiasArgs a{dy, z, P > 0 ? static_cast<const int*>(plan) : nullptr, dbias, reinterpret_cast<float*>(at), static_cast<int>(P),
+                           static_cast<int>(E), static_cast<int>(N), static_cast<int>(gate ? N / 2 : N), static_cast<int>(act)};
+    if (P > 0) {
+        const dim3 grid(static_cast<unsigned>((a.No + 63) / 64), static_cast<unsigned>(PlanLayout(P, E).CB));
+        auto launch = [&](auto dy32, auto z32) {
+            constexpr bool D = decltype(dy32)::value, Z = decltype(z32)::value;
+#define EXPERT_BIAS(GATE_, WHOLE_) hipLaunchKernelGGL((k_expert_bias<D, Z, GATE_, WHOLE_>), grid, dim3(8 * WAVE), 0, stream, a)
+            if (gate && a.No % 8 == 0) EXPERT_BIAS(true, true);
+            else if (gate) EXPERT_BIAS(true, false);
+            else if (a.No % 8 == 0) EXPERT_BIAS(false, true);
+            else EXPERT_BIAS(false, false);
+#undef EXPERT_BIAS
+        };
+        if (dy_f32 && z_f32) launch(std::true_type{}, std::true_type{});
+        else if (dy_f32) launch(std::true_type{}, std::false_type{});
+        else if (z_f32) launch(std::false_type{}, std::true_type{});
+        else launch(std::false_type{}, std::false_type{});
+    }
+    hipLaunchKernelGGL(k_expert_bias_sum, dim3(static_cast<unsigned>((N + 255) / 256), static_cast<unsigned>(E)), dim3(256), 0, stream, a);
+    return launch_status();
 }
 
 size_t any4_experts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g)

@@ -573,7 +573,8 @@ any4_status any4_gemm_act(any4_format format, const uint16_t* x, const uint8_t* 
  *     dz[m][n] = bf16_rne( dy[m][n] z[m][N/2 + n] act'(z[m][n]) ),
  *     dz[m][N/2 + n] = bf16_rne( dy[m][n] act(z[m][n]) ),      n < N/2
  *     dbias[n] = sum_m of the same values before their rounding     (fp32)
- * act' of ANY4_ACT_RELU is 0 at 0.  The gradient of x is any4_gemm_dx of dz, that of the
+ * (all rows' sum: the bias that many experts have of their own has its gradient from
+ * any4_experts_bias_backward).  act' of ANY4_ACT_RELU is 0 at 0.  The gradient of x is any4_gemm_dx of dz, that of the
  * residual dy itself.
  *   dy  device, [M][No] bf16 or fp32    z  device, [M][N] bf16 or fp32
  *   dz  device, [M][N] bf16, written (may be z itself where that is bf16)
@@ -667,6 +668,26 @@ any4_status any4_experts_gemm(any4_format format, const void* x, int x_f32, int 
                               int z_f32, void* out, int out_f32, any4_activation act, int gate, int64_t T, int64_t k,
                               int64_t E, int64_t N, int64_t K, int64_t g, void* workspace,
                               size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * any4_experts_bias_backward -- the gradient of any4_experts_gemm's bias:
+ *     dbias[e][n] = sum of dz[p][n] over the pairs p with ids[p] = e     (fp32)
+ * dz being any4_act_backward's values before their rounding, of the same dy, z, act and
+ * gate.  Experts without a pair get zeros, pairs without an expert are left out.
+ * Sums are fp32, in an order that the ids alone decide.
+ *   dy  device, [T*k][No] bf16 or fp32    z  device, [T*k][N] bf16 or fp32, as kept
+ *   dbias  device, [E][N] fp32, written whole      ids, plan  as any4_experts_gemm
+ *   0 <= T*k <= 2^20, k >= 1, 1 <= E <= 1024, 0 <= N <= 2^28, T*k*N below 2^30.  T = 0 writes zeros.
+ *   workspace  device, 16-byte aligned, any4_experts_bias_workspace_size(T, k, E, N) bytes,
+ *          with a plan less by any4_lora_plan_bytes(T*k, E): none for up to 512 pairs.
+ *   dy and z need 2-byte (fp32: 4-byte) alignment, ids and dbias 4, plan 16.
+ * Errors: as any4_gemm_act.
+ */
+size_t any4_experts_bias_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N);
+any4_status any4_experts_bias_backward(const void* dy, int dy_f32, const void* z, int z_f32, const int32_t* ids,
+                                       const void* plan, float* dbias, any4_activation act, int gate, int64_t T,
+                                       int64_t k, int64_t E, int64_t N, void* workspace, size_t workspace_bytes,
+                                       hipStream_t stream);
 
 /*
  * any4_experts_gemm_dx -- the gradient of the rows that went through the experts:
