@@ -1828,7 +1828,7 @@ any4_status any4_experts_bias_backward(const void* dy, int dy_f32, const void* z
 
 size_t any4_experts_workspace_size(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, int64_t g)
 {
-    if (T <= 0 || k <= 0 || N <= 0 || T > MAX_PAIRS || k > MAX_PAIRS || !sizes_ok(T * k, T * k, E, N, K, g))
+    if (T <= 0 || k <= 0 || N <= 0 || T > MAX_PAIRS || k > MAX_PAIRS || !sizes_ok(T * k, T, E, N, K, g))
         return 0;
     const int64_t P = T * k;
     return part_bytes(shape_of(P, E, true, K, N, false), P, N, K) + (P <= FEW_P ? 0 : any4_lora_plan_bytes(P, E));

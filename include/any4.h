@@ -652,8 +652,9 @@ any4_status any4_route_backward(const float* dw, const void* logits, int logits_
  *           leaves the outputs unwritten.
  *   z       device, [T*k][N] bf16 or fp32, written; or NULL
  *   out     device, [T*k][No] bf16 or fp32, or (out_f32 ANY4_PARTS) [2][T*k][No], written
- *   0 <= T*k <= 2^20, 1 <= E <= 1024, the other sizes as any4_gemm_act for M = T*k; the
- *   stacked arrays may be of any size.  T = 0 and N = 0 are no-ops.
+ *   0 <= T*k <= 2^20, 1 <= E <= 1024, the other sizes as any4_gemm_act for M = T*k, or in M*K
+ *   for the rows that x has (T without per_pair); the stacked arrays may be of any size.
+ *   T = 0 and N = 0 are no-ops.
  *   workspace  as for any4_gemm_act, any4_experts_workspace_size(T, k, E, N, K, g) bytes
  *          (where the call makes its own plan or splits K), for an x in parts
  *          any4_experts_parts_workspace_size.
