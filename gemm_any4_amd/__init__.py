@@ -72,7 +72,8 @@ EXPORTS = ("any4_packed_bytes", "any4_pack", "any4_dequant", "any4_gemm_workspac
            "any4_act_backward_workspace_size", "any4_act_backward", "any4_act_backward_parts", "any4_route", "any4_route_backward",
            "any4_experts_workspace_size", "any4_experts_parts_workspace_size", "any4_experts_gemm", "any4_experts_bias_workspace_size", "any4_experts_bias_backward",
            "any4_experts_dx_workspace_size",
-           "any4_experts_gemm_dx", "any4_experts_dx_parts_workspace_size", "any4_experts_gemm_dx_parts", "any4_combine", "any4_combine_backward")
+           "any4_experts_gemm_dx", "any4_experts_dx_parts_workspace_size", "any4_experts_gemm_dx_parts", "any4_combine", "any4_combine_backward",
+           "any4_ffn_form")
 
 _lib = None
 
@@ -142,6 +143,7 @@ def lib() -> ctypes.CDLL:
                 ("any4_route", ctypes.c_int, [P, INT] + [P] * 3 + [INT] * 2 + [F32] + [I64] * 5 + [P]),
                 ("any4_route_backward", ctypes.c_int,
                  [P, P, INT, P, P] + [INT] * 2 + [F32] + [I64] * 3 + [P]),
+                ("any4_ffn_form", ctypes.c_int, [I64] * 4 + [INT] * 2 + [P]),
                 ("any4_experts_workspace_size", SZ, [I64] * 6),
                 ("any4_experts_parts_workspace_size", SZ, [I64] * 6),
                 ("any4_experts_gemm", ctypes.c_int,
@@ -1019,6 +1021,23 @@ def combine_raw(y_ptr, w_ptr, residual_ptr, out_ptr, T, k, N, stream=None, y_f32
 
 def combine_backward_raw(dout_ptr, y_ptr, w_ptr, dy_ptr, dw_ptr, T, k, N, stream=None, y_f32=0) -> int:
     return lib().any4_combine_backward(dout_ptr, y_ptr, y_f32, w_ptr, dy_ptr, dw_ptr, T, k, N, _stream(stream))
+
+
+class FfnForm(NamedTuple):
+    """Which kernel runs a product: rows of a tile (0: the few-row kernel), waves of a
+    workgroup, splits of the sum, whether the layer is laid out as bf16 first."""
+    tile: int
+    waves: int
+    splits: int
+    laid_out: bool
+
+
+def ffn_form(P: int, E: int, N: int, K: int, back: bool = False, parts: bool = False) -> FfnForm:
+    """The form of gemm_act's product (E = 0) of P rows, or of experts_gemm's and
+    experts_gemm_dx's (back) of P pairs, their rows in two parts or not."""
+    form = (ctypes.c_int32 * 4)()
+    check(lib().any4_ffn_form(P, E, N, K, 1 if back else 0, 1 if parts else 0, form))
+    return FfnForm(form[0], form[1], form[2], bool(form[3]))
 
 
 @functools.lru_cache(maxsize=4096)      # constant for its sizes

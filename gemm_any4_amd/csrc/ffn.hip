@@ -1723,6 +1723,20 @@ any4_status experts_dx(any4_format format, const uint16_t* dy, bool parts, const
 
 extern "C" {
 
+any4_status any4_ffn_form(int64_t P, int64_t E, int64_t N, int64_t K, int back, int parts, int32_t* form)
+{
+    if (!sizes_ok(P, P, E > 0 ? E : 1, N, K, K) || P == 0 || N == 0 || E < 0 || (E == 0 && (back || parts)))
+        return ANY4_E_SHAPE;
+    if (!form)
+        return ANY4_E_NULL;
+    const Shape s = shape_of(P, E > 0 ? E : 1, E > 0, back ? N : K, back ? K : N, back != 0, parts != 0);
+    form[0] = 32 * s.rm;
+    form[1] = 2 * s.wn;
+    form[2] = s.S;
+    form[3] = s.rows;
+    return ANY4_OK;
+}
+
 size_t any4_gemm_act_workspace_size(int64_t M, int64_t N, int64_t K, int64_t g)
 {
     if (M <= 0 || N <= 0 || !sizes_ok(M, M, 1, N, K, g))

@@ -736,6 +736,17 @@ any4_status any4_combine_backward(const uint16_t* dout, const void* y, int y_f32
                                   uint16_t* dy, float* dw, int64_t T, int64_t k, int64_t N, hipStream_t stream);
 
 /*
+ * any4_ffn_form -- a measurement aid, not part of the method: which kernel the products of
+ * these sizes run, for tests that mean to reach one.  E = 0: any4_gemm_act of P rows; else
+ * the experts' products of P pairs, back != 0 the input's gradient, parts != 0 of rows in two
+ * parts.  Touches no GPU.
+ *   form  host, 4 words: rows of a tile (0: the few-row kernel), waves of a workgroup, splits of
+ *         the sum, 1 where the layer is laid out as bf16 first
+ * Errors: ANY4_E_SHAPE, ANY4_E_NULL.
+ */
+any4_status any4_ffn_form(int64_t P, int64_t E, int64_t N, int64_t K, int back, int parts, int32_t* form);
+
+/*
  * any4_read_probe -- a measurement aid, not part of the method: reads `bytes`
  * of device memory at `buf` once, with the GEMM kernels' loads (16 bytes per
  * lane, 1 KB per wave, non-temporal), one workgroup of 16 waves per CU, each
