@@ -490,7 +490,7 @@ __global__ __launch_bounds__(WAVE * WAVES, 4) void k_few(const FewArgs p)
 }
 
 // The splits' sums in order, then the epilogue; 8 columns a thread.  Bound by its bytes
-// (2062 rows of 4096 in three splits, 135 MB: 26 us), for few rows by its launch (4 us).
+// (2062 rows of 4096 in four splits to fp32, 169 MB: 33 us), for few rows by its launch (4 us).
 __global__ __launch_bounds__(256) void k_join(const Epilogue q, const int* __restrict__ ids, const int* __restrict__ plan, int P, int E,
                                               size_t pieces)
 {
@@ -1105,7 +1105,7 @@ __global__ __launch_bounds__(128 * WN, WN == 2 ? 2 : 1) void k_tile(const TileAr
 // ---------------------------------------------------------------------------
 // A wave decodes a packed tile of 16 rows x 128 k and turns it in LDS of its own,
 // so that it leaves in whole pieces of rows.  Bound by its bytes (28672 x 4096, 298 MB:
-// 53 us, 5.6 TB/s).  Then 4096 rows' product takes 810 us, a library's alone 722.
+// 53 us, 5.6 TB/s).  A call of 4096 rows takes 864 to 885 us with it, a library's product alone 722.
 constexpr int ROWS_WAVES = 4;
 
 template <int FMT>
@@ -1399,9 +1399,6 @@ int64_t tile_pairs(int rm, bool parts) { return parts ? 16 * rm : 32 * rm; }
 // product (both halves of a gate).  Of the forms and splits the one with the least
 // time for the CU with the most workgroups, splits with their partial sums' bytes
 // and a launch.  Rows fall on experts at random: the last tile of each is half empty.
-// (Of 85 sizes, a layer of 1 to 2048 rows and 4 to 64 experts, forward and back, eight
-// took more than a tenth longer than their best form and splits, at most a fifth; the
-// median 2%.)
 Shape shape_of(int64_t P, int64_t E, bool experts, int64_t D, int64_t C, bool turn, bool parts = false)
 {
     Shape s{0, 2, 1, 0, 0, false};

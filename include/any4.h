@@ -606,9 +606,9 @@ any4_status any4_act_backward_parts(const void* dy, int dy_f32, const void* z, i
  *     ids[t] = the k experts of largest c among those that stay, largest first
  *     w[t][j] = scale * s[t][ids[t][j]], with renorm != 0 divided by the sum of the k
  * Experts are compared by c in 64 bits, without a bias by the logits themselves (the same
- * order); ties go to the lowest index.  An expert whose logit is -inf or NaN, or whose c is
- * NaN or -inf, is never chosen and has a score of 0; where fewer than k are left, the
- * remaining ids are -1 with weights of 0.  A logit of +inf counts as the largest
+ * order); ties go to the lowest index.  An expert whose logit is -inf or NaN has a score of 0
+ * and is never chosen, nor is one whose c is NaN or -inf (its score counts in the softmax's
+ * sum all the same); where fewer than k are left, the remaining ids are -1 with weights of 0.  A logit of +inf counts as the largest
  * finite fp32 value.  With renorm, weights whose scores are all 0 are 0.
  *   logits  device, [T][E], fp32 or (logits_bf16 != 0) bf16
  *   bias    device, [E] fp32, or NULL
